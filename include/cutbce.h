@@ -186,6 +186,108 @@ cutbce_status cutbce_topk(const cutbce_problem *p, const void *H, const void *E,
 cutbce_status cutbce_targets_to_csr(int64_t rows, int32_t slots, const int32_t *targets, int32_t pad_id,
                                     int32_t *row_offsets, int32_t *item_ids, void *stream);
 
+/* ---------------------------------------------------------------------------------------------------------
+ * The sequence encoder's operators: what stands between item ids and the hidden states H of the loss. The
+ * conventions above hold for them (device pointers, caller-owned memory, asynchronous on `stream`, checks before
+ * anything is enqueued, bitwise deterministic, launches only, so they can be captured into a HIP graph). dtype is
+ * a cutbce_dtype: the element type of every dense array unless a call says otherwise. All sums, norms and softmax
+ * statistics are float32; every output is rounded once.
+ * --------------------------------------------------------------------------------------------------------- */
+
+/* Embedding lookup: out[i] = scale * table[ids[i]] for i < n; a row of zeros where ids[i] is outside [0, vocab)
+ * (padding). scale is finite.
+ *   ids      (device) [n], int32 (id_bytes = 4) or int64 (id_bytes = 8), aligned to id_bytes.
+ *   table    (device) [vocab][dim]; out (device) [n][dim]: dense, 16-byte aligned.
+ * 0 <= n <= 2^31 - 1, 1 <= vocab <= 2^31 - 1025, 1 <= dim <= 65536. Errors: SHAPE, DTYPE, NULL, ALIGN. */
+cutbce_status cutbce_embedding_forward(int64_t n, int64_t vocab, int32_t dim, int32_t dtype, int32_t id_bytes,
+                                       const void *ids, const void *table, float scale, void *out, void *stream);
+
+/* Bytes of workspace of cutbce_embedding_backward: the sorted (id, position) pairs and the partial sums of items
+ * that many positions share; grows with n and n * dim, not with vocab * dim. */
+cutbce_status cutbce_embedding_backward_workspace_size(int64_t n, int64_t vocab, int32_t dim, int32_t dtype,
+                                                       size_t *bytes);
+
+/* Gradient of the lookup: dtable[v] = scale * sum over i with ids[i] == v of dout[i], added in float32 in an
+ * order fixed by the positions (sorted by id), rounded once.
+ *   accumulate  0: dtable [vocab][dim] is overwritten (rows without a position become 0). Otherwise only the rows
+ *               that have a position are read and written: dtable[v] = round(dtable[v] + the sum), for a table
+ *               shared with the loss whose dE is there already.
+ * Arguments otherwise as for cutbce_embedding_forward; the workspace is 256-byte aligned. */
+cutbce_status cutbce_embedding_backward(int64_t n, int64_t vocab, int32_t dim, int32_t dtype, int32_t id_bytes,
+                                        const void *ids, const void *dout, float scale, int32_t accumulate,
+                                        void *dtable, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Layer norm of each row: y = (x - mean) * rstd * weight + bias, mean = sum x / dim,
+ * rstd = 1 / sqrt(sum (x - mean)^2 / dim + eps).
+ *   x      (device) [rows][dim] with rows x_stride elements apart (x_stride >= dim), aligned to an element;
+ *   weight, bias (device) [dim] in param_dtype, or NULL (1 and 0);
+ *   y      (device) [rows][dim] dense; mean, rstd (device) float [rows], or both NULL (no backward).
+ * 0 <= rows <= 2^31 - 1, 1 <= dim <= 65536, eps >= 0. Errors: SHAPE, DTYPE, NULL, ALIGN. */
+cutbce_status cutbce_layer_norm_forward(int64_t rows, int32_t dim, int32_t dtype, int32_t param_dtype, const void *x,
+                                        int64_t x_stride, const void *weight, const void *bias, float eps, void *y,
+                                        float *mean, float *rstd, void *stream);
+
+/* Bytes of workspace of cutbce_layer_norm_backward (partial sums of the weight's and bias' gradients). */
+cutbce_status cutbce_layer_norm_backward_workspace_size(int64_t rows, int32_t dim, size_t *bytes);
+
+/* Gradients of the layer norm from the cotangent dy [rows][dim] (rows dy_stride elements apart) and the forward's
+ * mean and rstd: with xhat = (x - mean) * rstd and g = dy * weight,
+ *   dx = rstd * (g - sum g / dim - xhat * sum(g * xhat) / dim),  dweight = sum_rows dy * xhat,
+ *   dbias = sum_rows dy.
+ * dx (dense), dweight, dbias (param_dtype): each may be NULL to skip it. */
+cutbce_status cutbce_layer_norm_backward(int64_t rows, int32_t dim, int32_t dtype, int32_t param_dtype,
+                                         const void *dy, int64_t dy_stride, const void *x, int64_t x_stride,
+                                         const void *weight, const float *mean, const float *rstd, void *dx,
+                                         void *dweight, void *dbias, void *workspace, size_t workspace_bytes,
+                                         void *stream);
+
+/* Attention over packed sequences or over a key/value cache (host struct). Row t of a sequence of n query rows and
+ * m keys attends, in each head, to the keys j <= t + m - n of the sequence when causal (the last row sees all
+ * keys), else to all m; a row that sees no key gives out = 0, lse = -inf and zero gradients.
+ *   out = softmax(scale * q . k) v,  lse = log sum exp(scale * q . k).
+ * Query head h reads key/value head h / (q_heads / kv_heads).
+ * Strides are in elements: row r, head h of q starts at q + r * q_row_stride + h * q_head_stride (k and v alike);
+ * the head_dim elements of one row and head are contiguous. Arrays may be parts of a wider one (a fused
+ * projection). q, k, v and their strides in bytes are multiples of 16 (strides may be 0). Outputs (out, dq, dk, dv) are dense
+ * [rows][heads][head_dim].
+ * Sequences, query side: sequence b has the rows cu_q[b] .. cu_q[b+1] - 1 (int32 [seqs + 1] on the device,
+ * cu_q[0] = 0, non-decreasing, cu_q[seqs] <= q_rows), or, with cu_q NULL, the q_rows / seqs rows from
+ * b * (q_rows / seqs) on. Key side: cu_k in the same way; with cu_k NULL, k_rows / seqs rows each when cu_q is NULL
+ * too or k_lens is given (a cache: sequence b's row j, head h of k starts at k + b * k_seq_stride + j * k_row_stride
+ * + h * k_head_stride), else the same ranges as cu_q. k_lens (int32 [seqs] on the device or NULL): only the first
+ * k_lens[b] rows of the range are keys (the filled part of a cache). Rows outside every sequence give out = 0,
+ * lse = -inf and zero gradients; keys past k_lens get zero gradients, and their contents are never used.
+ * Malformed ranges are clamped: every access stays inside the arrays. */
+typedef struct {
+    int64_t q_rows, k_rows;
+    int64_t q_row_stride, q_head_stride;
+    int64_t k_row_stride, k_head_stride;
+    int64_t v_row_stride, v_head_stride;
+    int64_t k_seq_stride, v_seq_stride; /* used only where every sequence has k_rows / seqs rows */
+    int32_t seqs;
+    int32_t q_heads, kv_heads; /* q_heads a multiple of kv_heads */
+    int32_t head_dim;          /* a multiple of 8, at most 128 */
+    int32_t dtype;
+    int32_t causal;
+    float scale;
+} cutbce_attention;
+
+/* Bytes of workspace of cutbce_attention_forward (backward = 0) or cutbce_attention_backward (backward = 1). */
+cutbce_status cutbce_attention_workspace_size(const cutbce_attention *a, int32_t backward, size_t *bytes);
+
+/* out [q_rows][q_heads][head_dim]; lse (device) float [q_rows][q_heads] or NULL (no backward). */
+cutbce_status cutbce_attention_forward(const cutbce_attention *a, const void *q, const void *k, const void *v,
+                                       const int32_t *cu_q, const int32_t *cu_k, const int32_t *k_lens, void *out,
+                                       float *lse, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Gradients from the cotangent dout (dense, like out) and the forward's out and lse. dq [q_rows][q_heads][head_dim],
+ * dk, dv [k_rows][kv_heads][head_dim] (summed over the query heads that share a key/value head), all overwritten.
+ * The probabilities are recomputed from q, k and lse. */
+cutbce_status cutbce_attention_backward(const cutbce_attention *a, const void *dout, const void *q, const void *k,
+                                        const void *v, const void *out, const float *lse, const int32_t *cu_q,
+                                        const int32_t *cu_k, const int32_t *k_lens, void *dq, void *dk, void *dv,
+                                        void *workspace, size_t workspace_bytes, void *stream);
+
 /* Opt-in kernel timing for benchmarks (host calls). While enabled, every launch of the logit-tile sweeps
  * (kind 0: forward rows sweep, kind 1: backward dE sweep, kind 2: the scoring sweep of cutbce_topk) is
  * bracketed by HIP events recorded on the launch stream. cutbce_profile_read waits for those events and

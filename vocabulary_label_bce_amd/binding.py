@@ -7,6 +7,7 @@ library has not been built, the first call raises (there is no fallback path).
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -30,9 +31,20 @@ class Problem(ctypes.Structure):
                 ("dim", ctypes.c_int32), ("dtype", ctypes.c_int32)]
 
 
+class Attention(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("q_rows", "k_rows", "q_row_stride", "q_head_stride", "k_row_stride",
+                                              "k_head_stride", "v_row_stride", "v_head_stride", "k_seq_stride",
+                                              "v_seq_stride")] + \
+               [(n, ctypes.c_int32) for n in ("seqs", "q_heads", "kv_heads", "head_dim", "dtype", "causal")] + \
+               [("scale", ctypes.c_float)]
+
+
 EXPORTS = ["cutbce_workspace_size", "cutbce_forward", "cutbce_forward_noalloc", "cutbce_backward",
            "cutbce_backward_reuse", "cutbce_validate_targets",
            "cutbce_targets_to_csr", "cutbce_topk",
+           "cutbce_embedding_forward", "cutbce_embedding_backward_workspace_size", "cutbce_embedding_backward",
+           "cutbce_layer_norm_forward", "cutbce_layer_norm_backward_workspace_size", "cutbce_layer_norm_backward",
+           "cutbce_attention_workspace_size", "cutbce_attention_forward", "cutbce_attention_backward",
            "cutbce_profile_enable", "cutbce_profile_read", "cutbce_mfma_ceiling",
            "cutbce_mfma_ceiling_random", "cutbce_status_string",
            "cutbce_version"]
@@ -57,6 +69,17 @@ def lib():
         L.cutbce_validate_targets.argtypes = [P, vp, vp, vp, vp]
         L.cutbce_targets_to_csr.argtypes = [ctypes.c_int64, ctypes.c_int32, vp, ctypes.c_int32, vp, vp, vp]
         L.cutbce_topk.argtypes = [P, vp, vp, vp, vp, vp, ctypes.c_int32, vp, vp, vp, vp, sz, vp]
+        i64, f32, AP = ctypes.c_int64, ctypes.c_float, ctypes.POINTER(Attention)
+        L.cutbce_embedding_forward.argtypes = [i64, i64, i32, i32, i32, vp, vp, f32, vp, vp]
+        L.cutbce_embedding_backward_workspace_size.argtypes = [i64, i64, i32, i32, ctypes.POINTER(sz)]
+        L.cutbce_embedding_backward.argtypes = [i64, i64, i32, i32, i32, vp, vp, f32, i32, vp, vp, sz, vp]
+        L.cutbce_layer_norm_forward.argtypes = [i64, i32, i32, i32, vp, i64, vp, vp, f32, vp, vp, vp, vp]
+        L.cutbce_layer_norm_backward_workspace_size.argtypes = [i64, i32, ctypes.POINTER(sz)]
+        L.cutbce_layer_norm_backward.argtypes = [i64, i32, i32, i32, vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp, sz,
+                                                 vp]
+        L.cutbce_attention_workspace_size.argtypes = [AP, i32, ctypes.POINTER(sz)]
+        L.cutbce_attention_forward.argtypes = [AP, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.cutbce_attention_backward.argtypes = [AP, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
         L.cutbce_profile_enable.argtypes = [i32]
         L.cutbce_profile_read.argtypes = [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_int64), i32]
         L.cutbce_profile_enable.restype = i32
@@ -70,7 +93,11 @@ def lib():
         L.cutbce_version.restype = i32
         for f in ("cutbce_workspace_size", "cutbce_forward", "cutbce_forward_noalloc", "cutbce_backward",
                   "cutbce_backward_reuse", "cutbce_validate_targets",
-                  "cutbce_targets_to_csr", "cutbce_topk"):
+                  "cutbce_targets_to_csr", "cutbce_topk", "cutbce_embedding_forward",
+                  "cutbce_embedding_backward_workspace_size", "cutbce_embedding_backward",
+                  "cutbce_layer_norm_forward", "cutbce_layer_norm_backward_workspace_size",
+                  "cutbce_layer_norm_backward", "cutbce_attention_workspace_size", "cutbce_attention_forward",
+                  "cutbce_attention_backward"):
             getattr(L, f).restype = i32
         _lib = L
         return L
@@ -159,6 +186,99 @@ def targets_to_csr(targets, pad_id: int, row_offsets, item_ids, stream=None):
 def validate_targets(p: Problem, row_offsets, item_ids, bad, stream=None):
     _check(lib().cutbce_validate_targets(ctypes.byref(p), _ptr(row_offsets), _ptr(item_ids), _ptr(bad),
                                          _stream(stream)))
+
+
+# ---- the sequence encoder's operators ---------------------------------------------------------------------------
+# These are called once per layer and step on small arrays as well, where the host's time counts: plain integers go
+# to ctypes for the pointers, and what depends on the sizes alone (workspace bytes, the attention description) is
+# kept per set of sizes.
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(stream):
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+
+
+def _dtype(dtype) -> int:
+    dt = _DTYPES.get(dtype)
+    if dt is None:
+        raise CutBCEError(f"unsupported dtype {dtype}")
+    return dt
+
+
+def embedding_forward(ids, table, scale: float, out, stream=None):
+    """cutbce_embedding_forward: ids int32 or int64 [n], table [V, D], out [n, D]."""
+    _check(lib().cutbce_embedding_forward(ids.numel(), table.shape[0], table.shape[1], _dtype(table.dtype),
+                                          ids.element_size(), _at(ids), _at(table), scale, _at(out),
+                                          _raw_stream(stream)))
+
+
+@functools.lru_cache(maxsize=256)
+def embedding_backward_workspace_size(n: int, vocab: int, dim: int, dtype) -> int:
+    b = ctypes.c_size_t(0)
+    _check(lib().cutbce_embedding_backward_workspace_size(n, vocab, dim, _dtype(dtype), ctypes.byref(b)))
+    return int(b.value)
+
+
+def embedding_backward(ids, dout, scale: float, accumulate: bool, dtable, ws, stream=None):
+    """cutbce_embedding_backward: dout [n, D], dtable [V, D] overwritten, or added to where accumulate."""
+    _check(lib().cutbce_embedding_backward(ids.numel(), dtable.shape[0], dtable.shape[1], _dtype(dtable.dtype),
+                                           ids.element_size(), _at(ids), _at(dout), scale, 1 if accumulate else 0,
+                                           _at(dtable), _at(ws), ws.numel(), _raw_stream(stream)))
+
+
+def layer_norm_forward(x, weight, bias, eps: float, y, mean, rstd, stream=None):
+    """cutbce_layer_norm_forward: x [rows, D] (unit column stride); weight, bias [D] or None; mean, rstd float32
+    [rows] or None."""
+    p = weight if weight is not None else (bias if bias is not None else x)
+    _check(lib().cutbce_layer_norm_forward(x.shape[0], x.shape[1], _dtype(x.dtype), _dtype(p.dtype), _at(x),
+                                           x.stride(0), _at(weight), _at(bias), eps, _at(y), _at(mean), _at(rstd),
+                                           _raw_stream(stream)))
+
+
+@functools.lru_cache(maxsize=256)
+def layer_norm_backward_workspace_size(rows: int, dim: int) -> int:
+    b = ctypes.c_size_t(0)
+    _check(lib().cutbce_layer_norm_backward_workspace_size(rows, dim, ctypes.byref(b)))
+    return int(b.value)
+
+
+def layer_norm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, ws, stream=None):
+    """cutbce_layer_norm_backward: dx, dweight, dbias may be None."""
+    p = next((t for t in (weight, dweight, dbias) if t is not None), x)
+    _check(lib().cutbce_layer_norm_backward(x.shape[0], x.shape[1], _dtype(x.dtype), _dtype(p.dtype), _at(dy),
+                                            dy.stride(0), _at(x), x.stride(0), _at(weight), _at(mean), _at(rstd),
+                                            _at(dx), _at(dweight), _at(dbias), _at(ws),
+                                            ws.numel() if ws is not None else 0, _raw_stream(stream)))
+
+
+@functools.lru_cache(maxsize=256)
+def attention_problem(*fields):
+    """(Attention, bytes of the forward's workspace, bytes of the backward's): fields as in Attention, in order."""
+    a = Attention(*fields)
+    sizes = []
+    for backward in (0, 1):
+        b = ctypes.c_size_t(0)
+        _check(lib().cutbce_attention_workspace_size(ctypes.byref(a), backward, ctypes.byref(b)))
+        sizes.append(int(b.value))
+    return a, sizes[0], sizes[1]
+
+
+def attention_forward(a: Attention, q, k, v, cu_q, cu_k, k_lens, out, lse, ws, stream=None):
+    """cutbce_attention_forward: lse float32 [q_rows, q_heads] or None."""
+    _check(lib().cutbce_attention_forward(a, _at(q), _at(k), _at(v), _at(cu_q), _at(cu_k), _at(k_lens), _at(out),
+                                          _at(lse), _at(ws), ws.numel() if ws is not None else 0,
+                                          _raw_stream(stream)))
+
+
+def attention_backward(a: Attention, dout, q, k, v, out, lse, cu_q, cu_k, k_lens, dq, dk, dv, ws, stream=None):
+    """cutbce_attention_backward: dq, dk, dv overwritten."""
+    _check(lib().cutbce_attention_backward(a, _at(dout), _at(q), _at(k), _at(v), _at(out), _at(lse), _at(cu_q),
+                                           _at(cu_k), _at(k_lens), _at(dq), _at(dk), _at(dv), _at(ws),
+                                           ws.numel() if ws is not None else 0, _raw_stream(stream)))
 
 
 SWEEP_KINDS = ("rows_sweep", "items_sweep", "topk_sweep")

@@ -2,13 +2,17 @@
 libcutbce.so ("Cut Binary Cross Entropy", Listing 1 and the custom VJP of Section III-B).
 
 PyTorch only allocates memory (inputs, outputs, the scratch workspace and the saved dH) and supplies the
-stream; the library does all the arithmetic. Inputs must live on the GPU; there is no CPU path.
+stream; the library does all the arithmetic. Inputs must live on the GPU; there is no CPU path. The operators that
+make the hidden states (embedding lookup, layer norm, attention) are in ``encoder`` and are reached from here too.
 """
 from __future__ import annotations
 
 import torch
 
 from . import binding as B
+from .encoder import (cached_attention, embedding, embedding_backward, embedding_forward,  # noqa: F401
+                      layer_norm, layer_norm_backward, layer_norm_forward, packed_attention,
+                      packed_attention_backward, packed_attention_forward)
 
 
 def _weights(row_weight, H):
