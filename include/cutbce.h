@@ -248,7 +248,8 @@ cutbce_status cutbce_layer_norm_backward(int64_t rows, int32_t dim, int32_t dtyp
  * Query head h reads key/value head h / (q_heads / kv_heads).
  * Strides are in elements: row r, head h of q starts at q + r * q_row_stride + h * q_head_stride (k and v alike);
  * the head_dim elements of one row and head are contiguous. Arrays may be parts of a wider one (a fused
- * projection). q, k, v and their strides in bytes are multiples of 16 (strides may be 0). Outputs (out, dq, dk, dv) are dense
+ * projection). q, k, v and their strides in bytes are multiples of 16 (strides may be 0; row strides and q_heads *
+ * head_dim are at most 2^22). Outputs (out, dq, dk, dv) are dense
  * [rows][heads][head_dim].
  * Sequences, query side: sequence b has the rows cu_q[b] .. cu_q[b+1] - 1 (int32 [seqs + 1] on the device,
  * cu_q[0] = 0, non-decreasing, cu_q[seqs] <= q_rows), or, with cu_q NULL, the q_rows / seqs rows from

@@ -3,191 +3,790 @@
 //   out = softmax(s q k^T) v, row t of a sequence of n rows and m keys seeing the keys j <= t + m - n
 //   P = exp(s q k^T - lse), dP = dO v^T, delta = rowsum(dO * out), dS = P * (dP - delta)
 //   dv = P^T dO, dk = s dS^T q, dq = s dS k, dk and dv summed over the query heads that share them
+//
+// All products run on 32x32 matrix instructions with one side's rows as the columns of the result, so that a lane
+// holds values of one row (or key) only: lane l has column l % 32, and of the rows acc_row(i, l / 32), i < 16. The
+// forward and dq form S^T = K Q^T: a row's maximum and sum are the lane's own, joined with lane l ^ 32, and P^T (or
+// dS^T) is the second product's B operand as it stands, with the keys in the order acc_row. dk and dv form S = Q K^T
+// likewise with the keys as columns. The second product's A operand is the transpose of a tile that is in LDS
+// row by row: for 16-bit elements the LDS transpose read delivers it, for float32 a plain read does.
+//
+// Tiles go from memory to LDS by direct buffer loads. A tile's rows past the sequence's end and columns past
+// head_dim lie outside the buffer's range and arrive as zeros. The 16-byte chunks of a row are permuted by the
+// row (swz) so that both the row-wise and the transposed reads spread over the LDS banks.
 #include "encoder.h"
 
 namespace cutbce {
 
 namespace {
 
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+#define CUTBCE_LDS __attribute__((address_space(3)))
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr int kRows = 128;  // rows (or keys) of a workgroup: four waves of 32
+constexpr float kLazy = 8.f;
+
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-__device__ inline float wave_sum(float x) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) x += __shfl_xor(x, o, 64);
-  return x;
-}
-__device__ inline float wave_max(float x) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) x = fmaxf(x, __shfl_xor(x, o, 64));
-  return x;
-}
+__host__ __device__ constexpr inline int acc_row(int i, int h) { return (i / 4) * 8 + h * 4 + (i % 4); }
 
-template <typename T> __device__ inline float dot(const T* x, const T* y, int d) {
-  float s = 0.f;
-  for (int i = 0; i < d; ++i) s += to_f32(x[i]) * to_f32(y[i]);
+__device__ inline int uni(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ inline int64_t uni64(int64_t x) {
+  return (int64_t)(((uint64_t)(uint32_t)uni((int)(x >> 32)) << 32) | (uint32_t)uni((int)x));
+}
+__device__ inline float other_half(float x) {  // the value of lane l ^ 32
+  const u32x2 r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float((threadIdx.x & 32) ? r[0] : r[1]);
+}
+__device__ inline float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// A tile of rows in LDS: DH features padded to a power of two, CPR 16-byte chunks a row, chunk c of row r at
+// c ^ swz(r).
+template <typename T, int DH> struct Tile {
+  static constexpr int kEsz = sizeof(T);
+  static constexpr int kRowB = (DH <= 32 ? 32 : (DH <= 64 ? 64 : 128)) * kEsz;
+  static constexpr int kCPR = kRowB / 16;
+  static constexpr int kNT = DH * kEsz / 32;  // pairs of chunks: k-steps of a product over the features
+  static constexpr int kNDB = DH / 32;        // 32-wide blocks of features
+  __device__ static inline int swz(int r) {
+    if constexpr (kEsz == 4) return r & 7;
+    else if constexpr (kCPR == 4) return (((r >> 1) & 1) << 1) | ((r >> 2) & 1);
+    else if constexpr (kCPR == 8) return ((r & 3) << 1) | ((r >> 2) & 1);
+    else return ((r & 3) << 1) | ((r >> 2) & 1) | (r & 8);
+  }
+};
+
+// One workgroup's (or wave's) loads of NR rows into LDS: NL lanes, 16 bytes each per instruction.
+template <typename T, int DH, int NR, int NL> struct Dma {
+  using Ti = Tile<T, DH>;
+  static constexpr int kRounds = NR * Ti::kCPR / NL, kStep = NL / Ti::kCPR;  // rows per round
+  static constexpr int kBytes = NR * Ti::kRowB;
+  static_assert(kRounds >= 1 && kRounds * kStep == NR, "");
+  int row, chunk, step;  // this lane's row offset in bytes and chunk in the first round; bytes from round to round
+  __device__ inline void init(int lane, int64_t stride) {
+    const int r = lane / Ti::kCPR;
+    row = (int)(r * stride * Ti::kEsz);
+    chunk = (lane % Ti::kCPR) ^ Ti::swz(r);
+    step = (int)(stride * Ti::kEsz) * kStep;
+  }
+  // round q's rows are kStep q further on: swz is linear in the row's bits, and r < kStep
+  __device__ inline int offset(int q, int dh) const {
+    const int c = (chunk ^ Ti::swz(q * kStep)) * 16;
+    return c < dh * Ti::kEsz ? row + c + q * step : (int)0x80000000u;
+  }
+  // rows [0, rem) of `base` (uniform; rem may be <= 0 or > NR) to LDS byte `dst` (uniform: the wave's first kilobyte)
+  __device__ inline void load(const T* base, int64_t rem, int64_t stride, int dh, uint32_t dst) const {
+#if defined(__HIP_DEVICE_COMPILE__)  // (the host pass silently drops kernels that reach these builtins this way)
+    const int rows = (int)clamp64(rem, 0, NR);
+    const int bytes = rows > 0 ? (int)((rows - 1) * stride + dh) * Ti::kEsz : 0;
+    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)base, (short)0, bytes, 0x00020000);
+#pragma unroll
+    for (int q = 0; q < kRounds; ++q)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (CUTBCE_LDS void*)(size_t)(dst + q * NL * 16), 16, offset(q, dh), 0, 0,
+                                               0);
+#endif
+  }
+};
+
+__device__ inline u32x4 lds16(uint32_t at) { return *(CUTBCE_LDS const u32x4*)(size_t)at; }
+
+template <typename T> struct Mma;
+
+template <> struct Mma<__bf16> {
+  struct P { bf16x8 g[2]; };  // a 32x32 result as the second product's B operand
+  __device__ static inline f32x16 mma(u32x4 a, u32x4 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
+                                                   0, 0);
+  }
+  __device__ static inline u32x4 negate(u32x4 x) { return x ^ 0x80008000u; }
+  __device__ static inline P pack(const f32x16& x) {  // rounds to nearest even
+    P p;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) p.g[i / 8][i % 8] = (__bf16)x[i];
+    return p;
+  }
+  // acc += X^T P: X the 32 rows from LDS row r0 (a multiple of 32) of the tile at `at`
+  template <int DH>
+  __device__ static inline void mma_t(f32x16* acc, const P& p, uint32_t at, int r0, int lane) {
+    using Ti = Tile<__bf16, DH>;
+    const int h = lane / 32, s = lane % 16;
+#pragma unroll
+    for (int g = 0; g < 2; ++g)
+#pragma unroll
+      for (int db = 0; db < Ti::kNDB; ++db) {
+        s16x4 x[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int row = 16 * g + 8 * e + 4 * h + s / 4;
+          const int c = (db * 4 + 2 * ((lane / 16) & 1) + ((s & 3) >> 1)) ^ Ti::swz(row);
+          x[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+              (CUTBCE_LDS s16x4*)(size_t)(at + (r0 + row) * Ti::kRowB + c * 16 + (s & 1) * 8));
+        }
+        const s16x8 a = __builtin_shufflevector(x[0], x[1], 0, 1, 2, 3, 4, 5, 6, 7);
+        acc[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), p.g[g], acc[db], 0, 0, 0);
+      }
+  }
+};
+
+template <> struct Mma<float> {
+  typedef f32x16 P;
+  __device__ static inline f32x16 mma(u32x4 a, u32x4 b, f32x16 c) {
+    const f32x4 x = __builtin_bit_cast(f32x4, a), y = __builtin_bit_cast(f32x4, b);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_32x32x2f32(x[j], y[j], c, 0, 0, 0);
+    return c;
+  }
+  __device__ static inline u32x4 negate(u32x4 x) { return x ^ 0x80000000u; }
+  __device__ static inline P pack(const f32x16& x) { return x; }
+  template <int DH>
+  __device__ static inline void mma_t(f32x16* acc, const P& p, uint32_t at, int r0, int lane) {
+    using Ti = Tile<float, DH>;
+    const int h = lane / 32, n = lane % 32;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int row = acc_row(i, h);
+#pragma unroll
+      for (int db = 0; db < Ti::kNDB; ++db) {
+        const int c = (db * 8 + n / 4) ^ Ti::swz(row);
+        const float x = *(CUTBCE_LDS const float*)(size_t)(at + (r0 + row) * Ti::kRowB + c * 16 + (n % 4) * 4);
+        acc[db] = __builtin_amdgcn_mfma_f32_32x32x2f32(x, p[i], acc[db], 0, 0, 0);
+      }
+    }
+  }
+};
+
+// 32 rows of a tile times the own operand: the result's rows are the tile's, its columns the own rows.
+template <typename T, int DH>
+__device__ inline f32x16 product(uint32_t at, int r0, const u32x4* own, int lane) {
+  using Ti = Tile<T, DH>;
+  const int r = lane % 32, h = lane / 32;
+  f32x16 s = {};
+#pragma unroll
+  for (int t = 0; t < Ti::kNT; ++t)
+    s = Mma<T>::mma(lds16(at + (r0 + r) * Ti::kRowB + (((2 * t + h) ^ Ti::swz(r)) * 16)), own[t], s);
   return s;
 }
 
-// One wave per (row, head): the lanes take 64 keys at a time for the scores and the features for the output.
-template <typename T> __global__ __launch_bounds__(256) void k_attn_fwd(Attn a, T* __restrict__ out,
-                                                                        float* __restrict__ lse) {
-  const int lane = threadIdx.x % 64;
-  const int64_t id = (int64_t)blockIdx.x * 4 + threadIdx.x / 64;
-  const int64_t r = id / a.hq;
-  const int h = (int)(id % a.hq), hk = h / a.group, dh = a.dh;
-  if (r >= a.q_rows) return;
-  const SeqRange s = seq_range(a, seq_of_row(a.cu_q, a.q_pitch, a.seqs, r));
-  const int64_t t = r - s.q0;
-  int64_t seen = t < 0 || t >= s.n ? 0 : (a.causal ? t + s.m - s.n + 1 : s.m);
-  const T* q = (const T*)a.q + r * a.q_rs + h * a.q_hs;
-  const T* k = (const T*)a.k + s.kb + hk * a.k_hs;
-  const T* v = (const T*)a.v + s.vb + hk * a.v_hs;
-  float m = -INFINITY, l = 0.f, o0 = 0.f, o1 = 0.f;
-  for (int64_t j0 = 0; j0 < seen; j0 += 64) {
-    const bool live = j0 + lane < seen;
-    const float z = live ? a.scale * dot(q, k + (j0 + lane) * a.k_rs, dh) : -INFINITY;
-    const float mn = fmaxf(m, wave_max(z));
-    const float c = m == -INFINITY ? 0.f : expf(m - mn);
-    const float p = live && mn != -INFINITY ? expf(z - mn) : 0.f;
-    m = mn;
-    l = l * c + wave_sum(p);
-    o0 *= c;
-    o1 *= c;
-    const int cnt = (int)(seen - j0 < 64 ? seen - j0 : 64);
-    for (int j = 0; j < cnt; ++j) {
-      const float pj = __shfl(p, j, 64);
-      const T* vj = v + (j0 + j) * a.v_rs;
-      if (lane < dh) o0 += pj * to_f32(vj[lane]);
-      if (lane + 64 < dh) o1 += pj * to_f32(vj[lane + 64]);
-    }
+// The own operand: lane l has the chunks 2t + l / 32 of one row (zeros past head_dim, or where !live).
+template <typename T, int DH> __device__ inline void load_own(u32x4* own, const T* row, bool live, int dh, int lane) {
+  using Ti = Tile<T, DH>;
+  const int h = lane / 32;
+#pragma unroll
+  for (int t = 0; t < Ti::kNT; ++t) {
+    const int c = 2 * t + h;
+    u32x4 x = {0, 0, 0, 0};
+    if (live && c * 16 < dh * Ti::kEsz) x = *(const u32x4*)((const char*)row + c * 16);
+    own[t] = x;
   }
-  const float inv = l > 0.f ? 1.f / l : (seen > 0 ? l / l : 0.f);
-  T* o = out + (r * a.hq + h) * dh;
-  if (lane < dh) o[lane] = from_f32<T>(o0 * inv);
-  if (lane + 64 < dh) o[lane + 64] = from_f32<T>(o1 * inv);
-  if (lse && lane == 0) lse[r * a.hq + h] = seen > 0 ? m + logf(l) : -INFINITY;
 }
 
-// delta[row][head] = dO . out
-template <typename T>
-__global__ __launch_bounds__(256) void k_attn_delta(int64_t n, int dh, const T* __restrict__ dout,
-                                                    const T* __restrict__ out, float* __restrict__ delta) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i < n) delta[i] = dot(dout + i * dh, out + i * dh, dh);
-}
-
-template <typename T>
-__global__ __launch_bounds__(256) void k_attn_dq(Attn a, const T* __restrict__ dout, const float* __restrict__ lse,
-                                                 const float* __restrict__ delta, T* __restrict__ dq) {
-  const int lane = threadIdx.x % 64;
-  const int64_t id = (int64_t)blockIdx.x * 4 + threadIdx.x / 64;
-  const int64_t r = id / a.hq;
-  const int h = (int)(id % a.hq), hk = h / a.group, dh = a.dh;
-  if (r >= a.q_rows) return;
-  const SeqRange s = seq_range(a, seq_of_row(a.cu_q, a.q_pitch, a.seqs, r));
-  const int64_t t = r - s.q0;
-  const int64_t seen = t < 0 || t >= s.n ? 0 : (a.causal ? t + s.m - s.n + 1 : s.m);
-  const T* q = (const T*)a.q + r * a.q_rs + h * a.q_hs;
-  const T* g = dout + (r * a.hq + h) * dh;
-  const T* k = (const T*)a.k + s.kb + hk * a.k_hs;
-  const T* v = (const T*)a.v + s.vb + hk * a.v_hs;
-  const float L = lse[r * a.hq + h], dl = delta[r * a.hq + h];
-  float x0 = 0.f, x1 = 0.f;
-  for (int64_t j0 = 0; j0 < seen; j0 += 64) {
-    const bool live = j0 + lane < seen;
-    float ds = 0.f;
-    if (live) {
-      const float p = expf(a.scale * dot(q, k + (j0 + lane) * a.k_rs, dh) - L);
-      ds = p * (dot(g, v + (j0 + lane) * a.v_rs, dh) - dl);
-    }
-    const int cnt = (int)(seen - j0 < 64 ? seen - j0 : 64);
-    for (int j = 0; j < cnt; ++j) {
-      const float d = __shfl(ds, j, 64);
-      const T* kj = k + (j0 + j) * a.k_rs;
-      if (lane < dh) x0 += d * to_f32(kj[lane]);
-      if (lane + 64 < dh) x1 += d * to_f32(kj[lane + 64]);
-    }
-  }
-  T* o = dq + (r * a.hq + h) * dh;
-  if (lane < dh) o[lane] = from_f32<T>(x0 * a.scale);
-  if (lane + 64 < dh) o[lane + 64] = from_f32<T>(x1 * a.scale);
-}
-
-// One wave per (key, key/value head): the lanes take 64 rows at a time, the group's heads in turn.
-template <typename T>
-__global__ __launch_bounds__(256) void k_attn_dkv(Attn a, const T* __restrict__ dout, const float* __restrict__ lse,
-                                                  const float* __restrict__ delta, T* __restrict__ dk,
-                                                  T* __restrict__ dv) {
-  const int lane = threadIdx.x % 64;
-  const int64_t id = (int64_t)blockIdx.x * 4 + threadIdx.x / 64;
-  const int64_t r = id / a.hk;
-  const int hk = (int)(id % a.hk), dh = a.dh;
-  if (r >= a.k_rows) return;
-  const SeqRange s = seq_range(a, seq_of_row(a.cu_k, a.k_pitch, a.seqs, r));
-  const int64_t j = r - s.k0;
-  const bool key = j >= 0 && j < s.m;
-  int64_t t0 = a.causal ? j - (s.m - s.n) : 0;  // the first row that sees the key
-  if (t0 < 0) t0 = 0;
-  const T* k = (const T*)a.k + s.kb + j * a.k_rs + hk * a.k_hs;
-  const T* v = (const T*)a.v + s.vb + j * a.v_rs + hk * a.v_hs;
-  float k0 = 0.f, k1 = 0.f, v0 = 0.f, v1 = 0.f;
-  if (key)
-    for (int h = hk * a.group; h < (hk + 1) * a.group; ++h) {
-      const T* q = (const T*)a.q + s.q0 * a.q_rs + h * a.q_hs;
-      for (int64_t i0 = t0; i0 < s.n; i0 += 64) {
-        float p = 0.f, ds = 0.f;
-        if (i0 + lane < s.n) {
-          const int64_t at = (s.q0 + i0 + lane) * a.hq + h;
-          p = expf(a.scale * dot(q + (i0 + lane) * a.q_rs, k, dh) - lse[at]);
-          ds = p * (dot(dout + at * dh, v, dh) - delta[at]);
-        }
-        const int cnt = (int)(s.n - i0 < 64 ? s.n - i0 : 64);
-        for (int i = 0; i < cnt; ++i) {
-          const float pi = __shfl(p, i, 64), di = __shfl(ds, i, 64);
-          const T* qi = q + (i0 + i) * a.q_rs;
-          const T* gi = dout + ((s.q0 + i0 + i) * a.hq + h) * dh;
-          if (lane < dh) k0 += di * to_f32(qi[lane]), v0 += pi * to_f32(gi[lane]);
-          if (lane + 64 < dh) k1 += di * to_f32(qi[lane + 64]), v1 += pi * to_f32(gi[lane + 64]);
-        }
+// A transposed result (lane: one row, the features 32 db + acc_row) times f, to a row of dh elements.
+template <typename T, int NDB> __device__ inline void store_row(T* row, const f32x16* acc, float f, int dh, int lane) {
+  const int h = lane / 32;
+#pragma unroll
+  for (int db = 0; db < NDB; ++db)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int d = db * 32 + 8 * k + 4 * h;
+      if (d < dh) {
+        typedef T V4 __attribute__((ext_vector_type(4)));
+        V4 v;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = (T)(acc[db][4 * k + j] * f);
+        *(V4*)(row + d) = v;
       }
     }
-  const int64_t o = (r * a.hk + hk) * dh;
-  if (lane < dh) dk[o + lane] = from_f32<T>(k0 * a.scale), dv[o + lane] = from_f32<T>(v0);
-  if (lane + 64 < dh) dk[o + lane + 64] = from_f32<T>(k1 * a.scale), dv[o + lane + 64] = from_f32<T>(v1);
 }
 
-template <typename T> hipError_t forward_t(const Attn& a, void* out, float* lse, hipStream_t st) {
-  k_attn_fwd<T><<<dim3((unsigned)cdiv(a.q_rows * a.hq, 4)), dim3(256), 0, st>>>(a, (T*)out, lse);
+// Work units: tiles of kRows rows. Sequence b's tiles start at unit start(b) / kRows + b, which leaves room for each
+// of them (a range of n rows spans at most n / kRows + 1 units' worth of starts), so the units can be found without a
+// running total. The lanes of a wave look at 64 sequences at a time.
+struct Unit {
+  SeqRange s;
+  int tile;  // tile of the sequence; may lie behind its end
+};
+__device__ inline int64_t start_of(const int32_t* cu, int64_t pitch, int64_t rows, int b) {
+  return cu ? clamp64(cu[b], 0, rows) : b * pitch;
+}
+__device__ inline Unit find_unit(const Attn& a, const int32_t* cu, int64_t pitch, int64_t rows, int64_t unit) {
+  const int lane = threadIdx.x % 64;
+  int lo = 0, cnt = a.seqs + 1;
+  while (cnt > 1) {
+    const int step = (cnt + 63) / 64, at = lane * step;
+    const bool ok = at < cnt && start_of(cu, pitch, rows, lo + at) / kRows + lo + at <= unit;
+    const uint64_t m = __ballot(ok);
+    const int n = m ? 63 - __builtin_clzll(m) : 0;
+    lo += n * step;
+    cnt = cnt - n * step < step ? cnt - n * step : step;
+  }
+  lo = uni(lo);
+  Unit u;
+  const int64_t first = start_of(cu, pitch, rows, lo) / kRows + lo;
+  u.tile = uni((int)clamp64(unit - first, 0, 1 << 30));
+  const SeqRange s = seq_range(a, lo);
+  u.s.q0 = uni64(s.q0), u.s.k0 = uni64(s.k0), u.s.kb = uni64(s.kb), u.s.vb = uni64(s.vb);
+  u.s.n = uni(s.n), u.s.m = uni(s.m), u.s.cap = uni(s.cap);
+  return u;
+}
+int64_t units_of(int64_t rows, int seqs) { return rows / kRows + seqs + 1; }
+
+// Keys that row t of the sequence sees.
+__device__ inline int seen_by(const Attn& a, const SeqRange& s, int64_t t) {
+  return a.causal ? (int)clamp64(t + s.m - s.n + 1, 0, s.m) : s.m;
+}
+
+__device__ inline void wait_and_sync() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+template <typename T, int DH> constexpr int key_tile() { return sizeof(T) == 4 && DH > 64 ? 32 : 64; }
+
+// Running softmax of one row per lane: `used` is the maximum that the exponents are taken against.
+struct Online {
+  float used = -INFINITY, sum = 0.f;
+};
+
+// P from scores of NS 32-key blocks (row-wise, c = scale * log2 e > 0); rescales the output when a row's maximum has
+// grown by more than a factor of 2^kLazy since it was last used (the exponentials stay below 2^kLazy until then).
+template <int NS, int NDB> __device__ inline void softmax_step(f32x16* s, float c, Online& st, f32x16* o) {
+  float mx = s[0][0];
+#pragma unroll
+  for (int b = 0; b < NS; ++b)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[b][i]);
+  mx = fmaxf(mx, other_half(mx));
+  if (__any(mx * c > st.used + kLazy)) {
+    const float nw = fmaxf(st.used, mx * c);
+    const float f = st.used == -INFINITY ? 0.f : exp2_of(st.used - nw);
+    st.used = nw;
+    st.sum *= f;
+#pragma unroll
+    for (int d = 0; d < NDB; ++d) o[d] *= f;
+  }
+  const float base = st.used == -INFINITY ? 0.f : st.used;
+#pragma unroll
+  for (int b = 0; b < NS; ++b)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      s[b][i] = exp2_of(__builtin_fmaf(s[b][i], c, -base));
+      st.sum += s[b][i];
+    }
+}
+
+__device__ inline float finish_lse(float used, float sum, bool any) {
+  return any ? (used + __builtin_amdgcn_logf(sum)) * kLn2 : -INFINITY;
+}
+
+// Forward: a workgroup has 128 rows of one sequence and head, a wave 32 of them; the keys stream through two LDS
+// stages of KT keys.
+template <typename T, int DH>
+__global__ __launch_bounds__(256, 2) void k_attn_fwd(Attn a, int64_t units, T* __restrict__ out,
+                                                     float* __restrict__ lse) {
+  using Ti = Tile<T, DH>;
+  constexpr int KT = key_tile<T, DH>(), NS = KT / 32;
+  using Ld = Dma<T, DH, KT, 256>;
+  extern __shared__ __align__(1024) char lds[];
+  const uint32_t lds0 = uni((uint32_t)(size_t)(CUTBCE_LDS char*)lds);
+  const int tid = threadIdx.x, wave = uni(tid / 64), lane = tid % 64;
+  const int h = blockIdx.x % a.hq;
+  const Unit u = find_unit(a, a.cu_q, a.q_pitch, a.q_rows, units - 1 - blockIdx.x / a.hq);
+  const SeqRange& s = u.s;
+  const int64_t r0 = (int64_t)u.tile * kRows;  // first row of the workgroup in its sequence
+  if (r0 >= s.n) return;
+  const int64_t t = r0 + wave * 32 + lane % 32;
+  const bool live = t < s.n;
+  const T* q = (const T*)a.q + (s.q0 + t) * a.q_rs + h * a.q_hs;
+  u32x4 qo[Ti::kNT];
+  load_own<T, DH>(qo, q, live, a.dh, lane);
+  // c > 0: a negative scale negates q, and a scale of 0 becomes one so small that every finite score is 0
+  const float c = fmaxf(fabsf(a.scale) * kLog2e, 1e-38f);
+  if (a.scale < 0.f) {
+#pragma unroll
+    for (int i = 0; i < Ti::kNT; ++i) qo[i] = Mma<T>::negate(qo[i]);
+  }
+  const T* k = (const T*)a.k + s.kb + (h / a.group) * a.k_hs;
+  const T* v = (const T*)a.v + s.vb + (h / a.group) * a.v_hs;
+  const int mine = seen_by(a, s, t);                                     // keys of the lane's row
+  const int wave_lo = seen_by(a, s, r0 + wave * 32);                     // fewest and most of the wave's rows
+  const int wave_hi = r0 + wave * 32 < s.n ? seen_by(a, s, clamp64(r0 + wave * 32 + 31, 0, s.n - 1)) : 0;
+  const int steps = (seen_by(a, s, clamp64(r0 + kRows - 1, 0, s.n - 1)) + KT - 1) / KT;
+  Ld lk, lv;
+  lk.init(tid, a.k_rs);
+  lv.init(tid, a.v_rs);
+  const uint32_t dst = lds0 + wave * 1024;
+  auto fetch = [&](int i) {
+    const int64_t j = (int64_t)i * KT;
+    const uint32_t at = dst + (i & 1) * 2 * Ld::kBytes;
+    lk.load(k + j * a.k_rs, s.m - j, a.k_rs, a.dh, at);
+    lv.load(v + j * a.v_rs, s.m - j, a.v_rs, a.dh, at + Ld::kBytes);
+  };
+  f32x16 o[Ti::kNDB] = {};
+  Online st;
+  if (steps > 0) fetch(0);
+  for (int i = 0; i < steps; ++i) {
+    wait_and_sync();
+    if (i + 1 < steps) fetch(i + 1);
+    const int j0 = i * KT;
+    if (j0 < wave_hi) {
+      const uint32_t kt = lds0 + (i & 1) * 2 * Ld::kBytes, vt = kt + Ld::kBytes;
+      f32x16 x[NS];
+#pragma unroll
+      for (int b = 0; b < NS; ++b) x[b] = product<T, DH>(kt, b * 32, qo, lane);
+      if (j0 + KT > wave_lo) {
+#pragma unroll
+        for (int b = 0; b < NS; ++b)
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (j0 + b * 32 + acc_row(e, lane / 32) >= mine) x[b][e] = -INFINITY;
+      }
+      softmax_step<NS, Ti::kNDB>(x, c, st, o);
+#pragma unroll
+      for (int b = 0; b < NS; ++b) Mma<T>::template mma_t<DH>(o, Mma<T>::pack(x[b]), vt, b * 32, lane);
+    }
+  }
+  const float sum = st.sum + other_half(st.sum);
+  if (live) {
+    const int64_t at = (s.q0 + t) * a.hq + h;
+    store_row<T, Ti::kNDB>(out + at * a.dh, o, mine > 0 ? 1.f / sum : 0.f, a.dh, lane);
+    if (lse && lane < 32) lse[at] = finish_lse(st.used, sum, mine > 0);
+  }
+}
+
+// dq, and the rows' (lse in base 2, delta) for dk and dv: the forward's layout and loop.
+template <typename T, int DH>
+__global__ __launch_bounds__(256, sizeof(T) == 4 && DH > 64 ? 1 : 2) void k_attn_dq(
+    Attn a, int64_t units, const T* __restrict__ dout, const T* __restrict__ out, const float* __restrict__ lse,
+    T* __restrict__ dq, float2* __restrict__ stat) {
+  using Ti = Tile<T, DH>;
+  constexpr int KT = key_tile<T, DH>(), NS = KT / 32;
+  using Ld = Dma<T, DH, KT, 256>;
+  extern __shared__ __align__(1024) char lds[];
+  const uint32_t lds0 = uni((uint32_t)(size_t)(CUTBCE_LDS char*)lds);
+  const int tid = threadIdx.x, wave = uni(tid / 64), lane = tid % 64;
+  const int h = blockIdx.x % a.hq;
+  const Unit u = find_unit(a, a.cu_q, a.q_pitch, a.q_rows, units - 1 - blockIdx.x / a.hq);
+  const SeqRange& s = u.s;
+  const int64_t r0 = (int64_t)u.tile * kRows;
+  if (r0 >= s.n) return;
+  const int64_t t = r0 + wave * 32 + lane % 32;
+  const bool live = t < s.n;
+  const int64_t at = (s.q0 + t) * a.hq + h;
+  u32x4 qo[Ti::kNT], go[Ti::kNT];
+  load_own<T, DH>(qo, (const T*)a.q + (s.q0 + t) * a.q_rs + h * a.q_hs, live, a.dh, lane);
+  load_own<T, DH>(go, dout + at * a.dh, live, a.dh, lane);
+  const int mine = live ? seen_by(a, s, t) : 0;
+  float delta = 0.f;
+  {
+    u32x4 oo[Ti::kNT];
+    load_own<T, DH>(oo, out + at * a.dh, live, a.dh, lane);
+    constexpr int N = 16 / sizeof(T);
+    typedef T V __attribute__((ext_vector_type(N)));
+#pragma unroll
+    for (int i = 0; i < Ti::kNT; ++i) {
+      const V x = __builtin_bit_cast(V, go[i]), y = __builtin_bit_cast(V, oo[i]);
+#pragma unroll
+      for (int j = 0; j < N; ++j) delta += to_f32(x[j]) * to_f32(y[j]);
+    }
+    delta += other_half(delta);
+  }
+  // a row that sees no key has lse = -inf; +inf makes its probabilities 0
+  const float L = mine > 0 ? lse[at] * kLog2e : INFINITY;
+  if (live && lane < 32) stat[(int64_t)h * a.q_rows + s.q0 + t] = make_float2(L, delta);
+  const float c = a.scale * kLog2e;
+  const T* k = (const T*)a.k + s.kb + (h / a.group) * a.k_hs;
+  const T* v = (const T*)a.v + s.vb + (h / a.group) * a.v_hs;
+  const int wave_lo = seen_by(a, s, r0 + wave * 32);
+  const int wave_hi = r0 + wave * 32 < s.n ? seen_by(a, s, clamp64(r0 + wave * 32 + 31, 0, s.n - 1)) : 0;
+  const int steps = (seen_by(a, s, clamp64(r0 + kRows - 1, 0, s.n - 1)) + KT - 1) / KT;
+  Ld lk, lv;
+  lk.init(tid, a.k_rs);
+  lv.init(tid, a.v_rs);
+  const uint32_t dst = lds0 + wave * 1024;
+  auto fetch = [&](int i) {
+    const int64_t j = (int64_t)i * KT;
+    const uint32_t to = dst + (i & 1) * 2 * Ld::kBytes;
+    lk.load(k + j * a.k_rs, s.m - j, a.k_rs, a.dh, to);
+    lv.load(v + j * a.v_rs, s.m - j, a.v_rs, a.dh, to + Ld::kBytes);
+  };
+  f32x16 acc[Ti::kNDB] = {};
+  if (steps > 0) fetch(0);
+  for (int i = 0; i < steps; ++i) {
+    wait_and_sync();
+    if (i + 1 < steps) fetch(i + 1);
+    const int j0 = i * KT;
+    if (j0 < wave_hi) {
+      const uint32_t kt = lds0 + (i & 1) * 2 * Ld::kBytes, vt = kt + Ld::kBytes;
+      const bool edge = j0 + KT > wave_lo;
+#pragma unroll
+      for (int b = 0; b < NS; ++b) {
+        f32x16 x = product<T, DH>(kt, b * 32, qo, lane);
+        const f32x16 g = product<T, DH>(vt, b * 32, go, lane);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[e] = exp2_of(__builtin_fmaf(x[e], c, -L)) * (g[e] - delta);
+        if (edge) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (j0 + b * 32 + acc_row(e, lane / 32) >= mine) x[e] = 0.f;
+        }
+        Mma<T>::template mma_t<DH>(acc, Mma<T>::pack(x), kt, b * 32, lane);
+      }
+    }
+  }
+  if (live) store_row<T, Ti::kNDB>(dq + at * a.dh, acc, a.scale, a.dh, lane);
+}
+
+// dk and dv: a workgroup has 128 keys of one sequence and key/value head, a wave 32 of them; the rows of the group's
+// heads stream through two LDS stages of 32 rows.
+template <typename T, int DH>
+__global__ __launch_bounds__(256, DH > 64 || sizeof(T) == 4 ? 1 : 2) void k_attn_dkv(
+    Attn a, const T* __restrict__ dout, const float2* __restrict__ stat, T* __restrict__ dk, T* __restrict__ dv) {
+  using Ti = Tile<T, DH>;
+  constexpr int QT = sizeof(T) == 2 && DH <= 32 ? 64 : 32, NS = QT / 32;
+  using Ld = Dma<T, DH, QT, 256>;
+  constexpr int kStage = 2 * Ld::kBytes + QT * 8;
+  extern __shared__ __align__(1024) char lds[];
+  const uint32_t lds0 = uni((uint32_t)(size_t)(CUTBCE_LDS char*)lds);
+  const int tid = threadIdx.x, wave = uni(tid / 64), lane = tid % 64, half = lane / 32;
+  const int hk = blockIdx.x % a.hk;
+  const Unit u = find_unit(a, a.cu_k, a.k_pitch, a.k_rows, blockIdx.x / a.hk);
+  const SeqRange& s = u.s;
+  const int64_t j0 = (int64_t)u.tile * kRows;
+  if (j0 >= s.cap) return;
+  const int64_t j = j0 + wave * 32 + lane % 32;
+  const bool key = j < s.m;
+  u32x4 ko[Ti::kNT], vo[Ti::kNT];
+  load_own<T, DH>(ko, (const T*)a.k + s.kb + j * a.k_rs + hk * a.k_hs, key, a.dh, lane);
+  load_own<T, DH>(vo, (const T*)a.v + s.vb + j * a.v_rs + hk * a.v_hs, key, a.dh, lane);
+  const float c = a.scale * kLog2e;
+  // the first row that sees key x: row t sees it if t >= x - (m - n)
+  auto first_row = [&](int64_t x) { return a.causal ? (int)clamp64(x - ((int64_t)s.m - s.n), 0, s.n) : 0; };
+  const int mine = first_row(j);
+  const int wave_lo = first_row(j0 + wave * 32), wave_hi = first_row(j0 + wave * 32 + 31);
+  const bool wave_live = j0 + wave * 32 < s.m;
+  const int begin = j0 < s.m ? first_row(j0) / QT : 0, end = j0 < s.m ? (s.n + QT - 1) / QT : 0;
+  const int steps = end > begin ? (end - begin) * a.group : 0;
+  Ld lq, lg;
+  lq.init(tid, a.q_rs);
+  lg.init(tid, (int64_t)a.hq * a.dh);
+  const uint32_t dst = lds0 + wave * 1024;
+  int fh = hk * a.group, ft = begin;  // head and tile of the next fetch
+  auto fetch = [&](int i) {
+    const int64_t t = (int64_t)ft * QT;
+    const uint32_t to = dst + (i & 1) * kStage;
+    lq.load((const T*)a.q + (s.q0 + t) * a.q_rs + fh * a.q_hs, s.n - t, a.q_rs, a.dh, to);
+    lg.load(dout + ((s.q0 + t) * a.hq + fh) * a.dh, s.n - t, (int64_t)a.hq * a.dh, a.dh, to + Ld::kBytes);
+    if (wave < NS) {  // (lse, delta) of 32 rows: 64 lanes, 4 bytes each
+      const int64_t rem = clamp64(s.n - t - wave * 32, 0, 32);
+      const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+          (void*)(stat + (int64_t)fh * a.q_rows + s.q0 + t + wave * 32), (short)0, (int)rem * 8, 0x00020000);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          r, (CUTBCE_LDS void*)(size_t)(lds0 + (i & 1) * kStage + 2 * Ld::kBytes + wave * 256), 4, lane * 4, 0, 0, 0);
+    }
+    if (++ft == end) ft = begin, ++fh;
+  };
+  f32x16 ak[Ti::kNDB] = {}, av[Ti::kNDB] = {};
+  if (steps > 0) fetch(0);
+  int ct = begin;
+  for (int i = 0; i < steps; ++i) {
+    wait_and_sync();
+    if (i + 1 < steps) fetch(i + 1);
+    const int t0 = ct * QT;
+    if (++ct == end) ct = begin;
+    const uint32_t qt = lds0 + (i & 1) * kStage, gt = qt + Ld::kBytes, sl = gt + Ld::kBytes;
+#pragma unroll
+    for (int b = 0; b < NS; ++b) {
+      const int t1 = t0 + b * 32;
+      if (wave_live && t1 + 31 >= wave_lo && t1 < s.n) {
+        f32x16 x = product<T, DH>(qt, b * 32, ko, lane);
+        f32x16 g = product<T, DH>(gt, b * 32, vo, lane);
+        const bool edge = t1 < wave_hi || t1 + 32 > s.n;
+#pragma unroll
+        for (int e = 0; e < 16; e += 2) {
+          const f32x4 ld = __builtin_bit_cast(f32x4, lds16(sl + (b * 32 + acc_row(e, half)) * 8));
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            float p = exp2_of(__builtin_fmaf(x[e + w], c, -ld[2 * w]));
+            float d = p * (g[e + w] - ld[2 * w + 1]);
+            const int t = t1 + acc_row(e + w, half);
+            if (edge && (t < mine || t >= s.n)) p = 0.f, d = 0.f;
+            x[e + w] = p;
+            g[e + w] = d;
+          }
+        }
+        Mma<T>::template mma_t<DH>(av, Mma<T>::pack(x), gt, b * 32, lane);
+        Mma<T>::template mma_t<DH>(ak, Mma<T>::pack(g), qt, b * 32, lane);
+      }
+    }
+  }
+  if (j < s.cap) {
+    const int64_t at = ((s.k0 + j) * a.hk + hk) * a.dh;
+    if (!key) {  // a place behind the keys: its own values are not used
+#pragma unroll
+      for (int d = 0; d < Ti::kNDB; ++d) ak[d] = f32x16{}, av[d] = f32x16{};
+    }
+    store_row<T, Ti::kNDB>(dk + at, ak, a.scale, a.dh, lane);
+    store_row<T, Ti::kNDB>(dv + at, av, 1.f, a.dh, lane);
+  }
+}
+
+// ---- few query rows against long key ranges ---------------------------------------------------------------------
+// The query heads that share a key/value head, and a sequence's few tokens, are the 32 columns of one tile, so the
+// keys are read once for all of them. A workgroup has one part of the keys of one (sequence, key/value head); its
+// waves take 32-key blocks in turn, each through an LDS ring of its own (no barriers), and join their results in
+// LDS. With more than one part, the parts leave (out, max, sum) in the workspace and k_attn_join joins them in order.
+
+constexpr int kCols = 32;
+
+template <typename T, int DH> constexpr int few_waves() { return Tile<T, DH>::kRowB > 256 ? 2 : 4; }
+
+// Parts of each key range: enough workgroups for every CU, at least 256 keys in each part (shorter parts are mostly
+// start-up: the first tile's latency and the join).
+int few_parts(const Attn& a) {
+  const int64_t wgs = (int64_t)a.seqs * a.hk;
+  int64_t p = cdiv(1024, wgs);
+  const int64_t most = cdiv(a.k_pitch, 256);
+  if (p > most) p = most;
+  return (int)(p < 1 ? 1 : (p > 256 ? 256 : p));
+}
+
+template <typename T, int DH>
+__global__ __launch_bounds__((few_waves<T, DH>() * 64), 1) void k_attn_few(Attn a, int parts, T* __restrict__ out,
+                                                                        float* __restrict__ lse,
+                                                                        float* __restrict__ part) {
+  using Ti = Tile<T, DH>;
+  constexpr int NW = few_waves<T, DH>(), NDB = Ti::kNDB;
+  using Ld = Dma<T, DH, 32, 64>;
+  extern __shared__ __align__(1024) char lds[];
+  const int tid = threadIdx.x, wave = uni(tid / 64), lane = tid % 64;
+  const uint32_t ring = uni((uint32_t)(size_t)(CUTBCE_LDS char*)lds) + wave * 4 * Ld::kBytes;
+  const int pi = blockIdx.x % parts;
+  const int64_t bh = blockIdx.x / parts;
+  const int hk = (int)(bh % a.hk), seq = (int)(bh / a.hk);
+  const SeqRange s0 = seq_range(a, seq);
+  SeqRange s = s0;
+  s.m = uni(s0.m);
+  const int col = lane % 32, cols = s.n * a.group;
+  const int t = col / a.group, head = hk * a.group + col % a.group;
+  const bool live = col < cols;
+  u32x4 qo[Ti::kNT];
+  load_own<T, DH>(qo, (const T*)a.q + (s.q0 + t) * a.q_rs + head * a.q_hs, live, a.dh, lane);
+  const float c = fmaxf(fabsf(a.scale) * kLog2e, 1e-38f);
+  if (a.scale < 0.f) {
+#pragma unroll
+    for (int i = 0; i < Ti::kNT; ++i) qo[i] = Mma<T>::negate(qo[i]);
+  }
+  const int mine = live ? seen_by(a, s, t) : 0, least = seen_by(a, s, 0);
+  // this part's 32-key blocks, and the wave's
+  const int blocks = (s.m + 31) / 32;
+  const int b0 = (int)((int64_t)blocks * pi / parts), b1 = (int)((int64_t)blocks * (pi + 1) / parts);
+  const T* k = (const T*)a.k + uni64(s.kb) + hk * a.k_hs;
+  const T* v = (const T*)a.v + uni64(s.vb) + hk * a.v_hs;
+  Ld lk, lv;
+  lk.init(lane, a.k_rs);
+  lv.init(lane, a.v_rs);
+  auto fetch = [&](int b, int stage) {
+    const int64_t j = (int64_t)b * 32;
+    lk.load(k + j * a.k_rs, s.m - j, a.k_rs, a.dh, ring + stage * 2 * Ld::kBytes);
+    lv.load(v + j * a.v_rs, s.m - j, a.v_rs, a.dh, ring + stage * 2 * Ld::kBytes + Ld::kBytes);
+  };
+  f32x16 o[NDB] = {};
+  Online st;
+  int stage = 0;
+  if (b0 + wave < b1) fetch(b0 + wave, 0);
+  for (int b = b0 + wave; b < b1; b += NW, stage ^= 1) {
+    // the other stage's reads were waited for by the products that used them
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    if (b + NW < b1) {
+      fetch(b + NW, stage ^ 1);
+      asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * Ld::kRounds) : "memory");
+    } else {
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    }
+    const uint32_t kt = ring + stage * 2 * Ld::kBytes;
+    f32x16 x = product<T, DH>(kt, 0, qo, lane);
+    if (b * 32 + 32 > least) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        if (b * 32 + acc_row(e, lane / 32) >= mine) x[e] = -INFINITY;
+    }
+    softmax_step<1, NDB>(&x, c, st, o);
+    Mma<T>::template mma_t<DH>(o, Mma<T>::pack(x), kt + Ld::kBytes, 0, lane);
+  }
+  st.sum += other_half(st.sum);
+  // join the waves: each leaves (max, sum) and its scaled output in LDS, which the rings no longer use
+  __syncthreads();
+  float* ms = (float*)lds;                  // [NW][2][32]
+  float* ot = (float*)(lds + NW * 256);     // [NW][DH][32], one column per row's lane
+  if (lane < 32) {
+    ms[wave * 64 + lane] = st.used;
+    ms[wave * 64 + 32 + lane] = st.sum;
+  }
+  __syncthreads();
+  float mx = -INFINITY, sum = 0.f;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) mx = fmaxf(mx, ms[w * 64 + col]);
+#pragma unroll
+  for (int w = 0; w < NW; ++w)
+    sum += ms[w * 64 + col] == -INFINITY ? 0.f * ms[w * 64 + 32 + col] : exp2_of(ms[w * 64 + col] - mx) * ms[w * 64 + 32 + col];
+  const float f = st.used == -INFINITY ? 0.f : exp2_of(st.used - mx);
+#pragma unroll
+  for (int db = 0; db < NDB; ++db)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) ot[(wave * DH + db * 32 + acc_row(e, lane / 32)) * 32 + col] = o[db][e] * f;
+  __syncthreads();
+  // column cc, feature d
+  const float inv = mine > 0 ? 1.f / sum : 0.f;
+  __shared__ float scale_of[kCols];
+  if (wave == 0 && lane < 32) scale_of[lane] = parts == 1 ? inv : 1.f;
+  __syncthreads();
+  for (int x = tid; x < cols * DH; x += NW * 64) {
+    const int cc = x / DH, d = x % DH;
+    float y = 0.f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) y += ot[(w * DH + d) * 32 + cc];
+    y *= scale_of[cc];
+    const int64_t row = s.q0 + cc / a.group;
+    const int hd = hk * a.group + cc % a.group;
+    if (parts == 1) {
+      if (d < a.dh) out[(row * a.hq + hd) * a.dh + d] = (T)y;
+    } else {
+      part[((bh * parts + pi) * cols + cc) * (DH + 2) + d] = y;
+    }
+  }
+  if (wave == 0 && lane < 32 && live) {
+    if (parts > 1) {
+      float* p = part + ((bh * parts + pi) * cols + col) * (DH + 2) + DH;
+      p[0] = mx;
+      p[1] = sum;
+    } else if (lse) {
+      lse[(s.q0 + t) * a.hq + head] = finish_lse(mx, sum, mine > 0);
+    }
+  }
+}
+
+// One wave per (sequence, key/value head, column): the parts' results in order.
+template <typename T, int DH>
+__global__ __launch_bounds__(256) void k_attn_join(Attn a, int parts, int cols, T* __restrict__ out,
+                                                   float* __restrict__ lse, const float* __restrict__ part) {
+  const int64_t id = (int64_t)blockIdx.x * 4 + threadIdx.x / 64;
+  const int lane = threadIdx.x % 64;
+  const int64_t bh = id / cols;
+  const int col = (int)(id % cols);
+  if (bh >= (int64_t)a.seqs * a.hk) return;
+  const SeqRange s = seq_range(a, (int)(bh / a.hk));
+  const int t = col / a.group, head = (int)(bh % a.hk) * a.group + col % a.group;
+  const bool any = seen_by(a, s, t) > 0;
+  const float* p = part + (bh * parts * cols + col) * (DH + 2);
+  const int64_t step = (int64_t)cols * (DH + 2);
+  float mx = -INFINITY;
+  for (int i = 0; i < parts; ++i) mx = fmaxf(mx, p[i * step + DH]);
+  float sum = 0.f, y0 = 0.f, y1 = 0.f;
+  for (int i = 0; i < parts; ++i) {
+    const float m = p[i * step + DH];
+    const float f = m == -INFINITY ? 0.f : exp2_of(m - mx);
+    sum += f * p[i * step + DH + 1];
+    if (lane < DH) y0 += f * p[i * step + lane];
+    if (lane + 64 < DH) y1 += f * p[i * step + lane + 64];
+  }
+  const float inv = any ? 1.f / sum : 0.f;
+  const int64_t at = (s.q0 + t) * a.hq + head;
+  if (lane < a.dh) out[at * a.dh + lane] = (T)(y0 * inv);
+  if (lane + 64 < a.dh) out[at * a.dh + lane + 64] = (T)(y1 * inv);
+  if (lse && lane == 0) lse[at] = finish_lse(mx, sum, any);
+}
+
+// Few query rows: fixed rows per sequence that fill at most one tile's columns with their group's heads.
+bool few_rows(const Attn& a) { return !a.cu_q && !a.cu_k && a.q_rows % a.seqs == 0 && a.q_pitch * a.group <= kCols; }
+
+size_t few_bytes(const Attn& a) {
+  const int parts = few_parts(a);
+  return parts > 1 ? (size_t)a.seqs * a.hk * parts * a.q_pitch * a.group * (128 + 2) * 4 : 0;
+}
+
+hipError_t allow_lds(const void* f, int bytes) {
+  return bytes > 65536 ? hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, bytes) : hipSuccess;
+}
+
+template <typename T, int DH> hipError_t forward_t(const Attn& a, void* out, float* lse, char* ws, hipStream_t st) {
+  using Ti = Tile<T, DH>;
+  if (few_rows(a)) {
+    constexpr int NW = few_waves<T, DH>();
+    const int ring = NW * 4 * 32 * Ti::kRowB, join = NW * 256 + NW * DH * 32 * 4;
+    const int bytes = ring > join ? ring : join;
+    const int parts = few_parts(a), cols = (int)a.q_pitch * a.group;
+    const hipError_t e = allow_lds((const void*)k_attn_few<T, DH>, bytes);
+    if (e != hipSuccess) return e;
+    const int64_t bh = (int64_t)a.seqs * a.hk;
+    k_attn_few<T, DH><<<dim3((unsigned)(bh * parts)), dim3(NW * 64), bytes, st>>>(a, parts, (T*)out, lse, (float*)ws);
+    if (parts > 1)
+      k_attn_join<T, DH><<<dim3((unsigned)cdiv(bh * cols, 4)), dim3(256), 0, st>>>(a, parts, cols, (T*)out, lse,
+                                                                                   (const float*)ws);
+    return hipGetLastError();
+  }
+  const int64_t units = units_of(a.q_rows, a.seqs);
+  const int bytes = 4 * key_tile<T, DH>() * Ti::kRowB;
+  const hipError_t e = allow_lds((const void*)k_attn_fwd<T, DH>, bytes);
+  if (e != hipSuccess) return e;
+  k_attn_fwd<T, DH><<<dim3((unsigned)(units * a.hq)), dim3(256), bytes, st>>>(a, units, (T*)out, lse);
   return hipGetLastError();
 }
 
-template <typename T>
+template <typename T, int DH>
 hipError_t backward_t(const Attn& a, const void* dout, const void* out, const float* lse, void* dq, void* dk, void* dv,
                       char* ws, hipStream_t st) {
-  float* delta = (float*)ws;
-  const int64_t n = a.q_rows * a.hq;
-  if (n) {
-    k_attn_delta<T><<<dim3((unsigned)cdiv(n, 256)), dim3(256), 0, st>>>(n, a.dh, (const T*)dout, (const T*)out, delta);
-    k_attn_dq<T><<<dim3((unsigned)cdiv(n, 4)), dim3(256), 0, st>>>(a, (const T*)dout, lse, delta, (T*)dq);
+  using Ti = Tile<T, DH>;
+  float2* stat = (float2*)ws;
+  if (a.q_rows) {
+    const int64_t units = units_of(a.q_rows, a.seqs);
+    const int bytes = 4 * key_tile<T, DH>() * Ti::kRowB;
+    const hipError_t e = allow_lds((const void*)k_attn_dq<T, DH>, bytes);
+    if (e != hipSuccess) return e;
+    k_attn_dq<T, DH><<<dim3((unsigned)(units * a.hq)), dim3(256), bytes, st>>>(a, units, (const T*)dout, (const T*)out,
+                                                                               lse, (T*)dq, stat);
   }
-  if (a.k_rows)
-    k_attn_dkv<T><<<dim3((unsigned)cdiv(a.k_rows * a.hk, 4)), dim3(256), 0, st>>>(a, (const T*)dout, lse, delta,
-                                                                                  (T*)dk, (T*)dv);
+  if (a.k_rows) {
+    constexpr int QT = sizeof(T) == 2 && DH <= 32 ? 64 : 32;
+    const int bytes = 2 * (2 * QT * Ti::kRowB + QT * 8);
+    const hipError_t e = allow_lds((const void*)k_attn_dkv<T, DH>, bytes);
+    if (e != hipSuccess) return e;
+    k_attn_dkv<T, DH><<<dim3((unsigned)(units_of(a.k_rows, a.seqs) * a.hk)), dim3(256), bytes, st>>>(
+        a, (const T*)dout, stat, (T*)dk, (T*)dv);
+  }
   return hipGetLastError();
 }
+
+// The kernels are compiled for head_dim rounded up to a multiple of 32.
+#define CUTBCE_BY_DIM(F, ...)                                                               \
+  (a.dtype == 1 ? (a.dh <= 32   ? F<__bf16, 32>(__VA_ARGS__)                                \
+                   : a.dh <= 64 ? F<__bf16, 64>(__VA_ARGS__)                                \
+                   : a.dh <= 96 ? F<__bf16, 96>(__VA_ARGS__)                                \
+                                : F<__bf16, 128>(__VA_ARGS__))                              \
+                : (a.dh <= 32   ? F<float, 32>(__VA_ARGS__)                                 \
+                   : a.dh <= 64 ? F<float, 64>(__VA_ARGS__)                                 \
+                   : a.dh <= 96 ? F<float, 96>(__VA_ARGS__)                                 \
+                                : F<float, 128>(__VA_ARGS__)))
 
 }  // namespace
 
-size_t attention_bytes(const Attn& a, bool backward) { return backward ? (size_t)a.q_rows * a.hq * 4 : 0; }
+size_t attention_bytes(const Attn& a, bool backward) {
+  if (backward) return (size_t)a.q_rows * a.hq * sizeof(float2);
+  // (whether the call is one of few rows depends on its arrays too: the size covers both)
+  return a.q_rows % a.seqs == 0 && a.q_pitch * a.group <= kCols ? few_bytes(a) : 0;
+}
 
-hipError_t launch_attention_forward(const Attn& a, void* out, float* lse, char*, hipStream_t st) {
-  return a.dtype == 1 ? forward_t<__bf16>(a, out, lse, st) : forward_t<float>(a, out, lse, st);
+hipError_t launch_attention_forward(const Attn& a, void* out, float* lse, char* ws, hipStream_t st) {
+  return CUTBCE_BY_DIM(forward_t, a, out, lse, ws, st);
 }
 
 hipError_t launch_attention_backward(const Attn& a, const void* dout, const void* out, const float* lse, void* dq,
                                      void* dk, void* dv, char* ws, hipStream_t st) {
-  return a.dtype == 1 ? backward_t<__bf16>(a, dout, out, lse, dq, dk, dv, ws, st)
-                      : backward_t<float>(a, dout, out, lse, dq, dk, dv, ws, st);
+  return CUTBCE_BY_DIM(backward_t, a, dout, out, lse, dq, dk, dv, ws, st);
 }
 
 }  // namespace cutbce

@@ -23,9 +23,13 @@ def _need(ok, what):
 
 
 def _on_gpu(what, *tensors):
-    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    dev = None
     for t in tensors:
-        if t is not None and (not t.is_cuda or t.get_device() != dev):
+        if t is None:
+            continue
+        if t.is_cuda and dev is None:
+            dev = torch.cuda.current_device()
+        if not t.is_cuda or t.get_device() != dev:
             raise ValueError(f"{what} runs on the GPU only: its tensors must be on the current device")
 
 
@@ -195,7 +199,7 @@ def _strided(x, dims):
     step = 16 // x.element_size()
     for _ in range(2):
         st = [x.stride(d) if x.shape[d] > 1 else 0 for d in dims]
-        if x.stride(-1) == 1 and x.data_ptr() % 16 == 0 and all(s % step == 0 for s in st):
+        if x.stride(-1) == 1 and x.data_ptr() % 16 == 0 and all(s % step == 0 for s in st) and st[-2] <= 1 << 22:
             return x, st
         x = x.contiguous()
         if x.data_ptr() % 16:
