@@ -199,7 +199,8 @@ def _at(t):
 
 
 def _raw_stream(stream):
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+    # (the handle without the Stream object around it: 0.2 us instead of 2.8)
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) if stream is None else stream.cuda_stream
 
 
 def _dtype(dtype) -> int:

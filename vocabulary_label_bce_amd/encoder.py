@@ -27,9 +27,9 @@ def _on_gpu(what, *tensors):
     for t in tensors:
         if t is None:
             continue
-        if t.is_cuda and dev is None:
+        if dev is None and t.is_cuda:
             dev = torch.cuda.current_device()
-        if not t.is_cuda or t.get_device() != dev:
+        if t.get_device() != dev:
             raise ValueError(f"{what} runs on the GPU only: its tensors must be on the current device")
 
 
@@ -137,7 +137,8 @@ def layer_norm_forward(x, weight=None, bias=None, eps: float = 1e-5, stats: bool
     y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
     mean = rstd = None
     if stats:
-        mean, rstd = torch.empty(2, rows.shape[0], dtype=torch.float32, device=x.device)
+        mean = torch.empty(rows.shape[0], dtype=torch.float32, device=x.device)
+        rstd = torch.empty_like(mean)
     B.layer_norm_forward(rows, weight, bias, eps, y, mean, rstd)
     return y, mean, rstd
 
