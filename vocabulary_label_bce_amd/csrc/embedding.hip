@@ -16,7 +16,8 @@ namespace {
 constexpr int kSortThreads = 256;
 constexpr int kSortItems = 1024;  // pairs of one sorting workgroup
 constexpr int kMaxBits = 10;      // most bits of one sorting pass
-constexpr int kChunk = 32;        // sorted pairs that one lane group sums
+constexpr int kChunk = 8;         // sorted pairs that one lane group sums
+constexpr int kFillBytes = 65536; // what one workgroup clears
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
@@ -86,39 +87,75 @@ __global__ __launch_bounds__(256) void k_embed(int64_t n, int V, int D, int lpr,
   }
 }
 
+// The gradient's table is cleared by the sorting kernels, whose own work fills few CUs and is all latency: the
+// workgroups behind the sorting ones clear a share of it each. Clearing it before the sort instead took 28 us more at
+// 876,000 x 128 bf16 (224 MB).
+struct Fill {
+  char* p;          // of this launch's share
+  int64_t bytes;    // 0: nothing to clear
+  int first;        // workgroups from this one on clear
+};
+__device__ inline bool fill(const Fill& f) {
+  if ((int)blockIdx.x < f.first) return false;
+  const int64_t at = (int64_t)(blockIdx.x - f.first) * kFillBytes;
+#pragma unroll
+  for (int i = 0; i < kFillBytes / 16 / kSortThreads; ++i) {
+    const int64_t o = at + ((int64_t)i * kSortThreads + threadIdx.x) * 16;
+    if (o + 16 <= f.bytes) {
+      *(uint4*)(f.p + o) = make_uint4(0, 0, 0, 0);
+    } else {
+      for (int64_t b = o; b < f.bytes && b < o + 16; ++b) f.p[b] = 0;
+    }
+  }
+  return true;
+}
+__global__ __launch_bounds__(kSortThreads) void k_fill(Fill f) { fill(f); }
+
 // Counts of each digit in a workgroup's pairs: counts[digit][block].
 template <typename I>
-__global__ __launch_bounds__(kSortThreads) void k_sort_count(int64_t n, int V, int shift, int bits, int blocks,
+__global__ __launch_bounds__(kSortThreads) void k_sort_count(Fill f, int64_t n, int V, int shift, int bits, int blocks,
                                                              const I* __restrict__ ids, const int* __restrict__ keys,
                                                              int* __restrict__ counts) {
+  if (fill(f)) return;
+  constexpr int kPer = kSortItems / kSortThreads;
   __shared__ int h[1 << kMaxBits];
   const int R = 1 << bits;
+  const int64_t base = (int64_t)blockIdx.x * kSortItems + threadIdx.x;
+  int key[kPer];
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const int64_t i = base + j * kSortThreads;
+    key[j] = i < n ? (ids ? key_of(ids, i, V) : keys[i]) : -1;
+  }
   for (int d = threadIdx.x; d < R; d += kSortThreads) h[d] = 0;
   __syncthreads();
-  const int64_t base = (int64_t)blockIdx.x * kSortItems;
-  for (int j = threadIdx.x; j < kSortItems && base + j < n; j += kSortThreads) {
-    const int key = ids ? key_of(ids, base + j, V) : keys[base + j];
-    atomicAdd(&h[(key >> shift) & (R - 1)], 1);
-  }
+#pragma unroll
+  for (int j = 0; j < kPer; ++j)
+    if (key[j] >= 0) atomicAdd(&h[(key[j] >> shift) & (R - 1)], 1);
   __syncthreads();
   for (int d = threadIdx.x; d < R; d += kSortThreads) counts[(int64_t)d * blocks + blockIdx.x] = h[d];
 }
 
+__device__ inline int wave_scan(int x, int lane) {  // inclusive
+#pragma unroll
+  for (int o = 1; o < 64; o *= 2) {
+    const int y = __shfl_up(x, o, 64);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
+
 // Running totals of one digit's counts over the blocks (one wave per digit).
-__global__ __launch_bounds__(256) void k_sort_scan(int digits, int blocks, int* __restrict__ counts,
-                                                   int* __restrict__ totals) {
-  const int d = blockIdx.x * 4 + threadIdx.x / 64, lane = threadIdx.x % 64;
+__global__ __launch_bounds__(kSortThreads) void k_sort_scan(Fill f, int digits, int blocks, int* __restrict__ counts,
+                                                            int* __restrict__ totals) {
+  if (fill(f)) return;
+  const int d = blockIdx.x * (kSortThreads / 64) + threadIdx.x / 64, lane = threadIdx.x % 64;
   if (d >= digits) return;
   int* c = counts + (int64_t)d * blocks;
   int run = 0;
   for (int b0 = 0; b0 < blocks; b0 += 64) {
     const int x = b0 + lane < blocks ? c[b0 + lane] : 0;
-    int s = x;
-#pragma unroll
-    for (int o = 1; o < 64; o *= 2) {
-      const int y = __shfl_up(s, o, 64);
-      if (lane >= o) s += y;
-    }
+    const int s = wave_scan(x, lane);
     if (b0 + lane < blocks) c[b0 + lane] = run + s - x;
     run += __shfl(s, 63, 64);
   }
@@ -126,50 +163,41 @@ __global__ __launch_bounds__(256) void k_sort_scan(int digits, int blocks, int* 
 }
 
 // Moves each pair to its place: digit base + the counts of earlier blocks + its rank among the block's equal digits.
-// A wave takes the block's pairs in runs of 64 in order; lanes with equal digits find each other by ballots.
+// A wave takes the block's pairs in runs of 64 in order; lanes with equal digits find each other by ballots. Every
+// load from memory is issued at the start: the kernel's time is mostly their latency.
 template <typename I>
-__global__ __launch_bounds__(kSortThreads) void k_sort_move(int64_t n, int V, int shift, int bits, int blocks,
+__global__ __launch_bounds__(kSortThreads) void k_sort_move(Fill f, int64_t n, int V, int shift, int bits, int blocks,
                                                             const I* __restrict__ ids, const int* __restrict__ keys,
                                                             const int* __restrict__ pos,
                                                             const int* __restrict__ counts,
                                                             const int* __restrict__ totals, int* __restrict__ keys_out,
                                                             int* __restrict__ pos_out) {
-  constexpr int kWaves = kSortThreads / 64, kRuns = kSortItems / kSortThreads;
-  __shared__ int base[1 << kMaxBits];
-  __shared__ int wc[kWaves][1 << kMaxBits];
+  if (fill(f)) return;
+  constexpr int kWaves = kSortThreads / 64, kRuns = kSortItems / kSortThreads, kMost = 1 << kMaxBits;
+  constexpr int kPer = kMost / kSortThreads;  // digits of a thread: kPer consecutive ones
+  __shared__ int wc[kWaves][kMost];
   __shared__ int wsum[kWaves];
   const int R = 1 << bits, tid = threadIdx.x, wave = tid / 64, lane = tid % 64;
-  // digit bases: exclusive totals over the digits
-  int carry = 0;
-  for (int d0 = 0; d0 < R; d0 += kSortThreads) {
-    const int d = d0 + tid, x = d < R ? totals[d] : 0;
-    int s = x;
-#pragma unroll
-    for (int o = 1; o < 64; o *= 2) {
-      const int y = __shfl_up(s, o, 64);
-      if (lane >= o) s += y;
-    }
-    if (lane == 63) wsum[wave] = s;
-    __syncthreads();
-    int before = carry;
-    for (int w = 0; w < kWaves; ++w) {
-      if (w < wave) before += wsum[w];
-      carry += wsum[w];
-    }
-    if (d < R) base[d] = before + s - x + counts[(int64_t)d * blocks + blockIdx.x];
-    __syncthreads();
-  }
-  for (int d = tid; d < kWaves * R; d += kSortThreads) wc[d / R][d % R] = 0;
-  __syncthreads();
-  // each wave: 64 * kRuns consecutive pairs
   const int64_t first = (int64_t)blockIdx.x * kSortItems + (int64_t)wave * 64 * kRuns;
-  int key[kRuns], ps[kRuns], rank[kRuns];
+  int key[kRuns], ps[kRuns], rank[kRuns], tot[kPer], cnt[kPer];
 #pragma unroll
   for (int r = 0; r < kRuns; ++r) {
     const int64_t i = first + r * 64 + lane;
     const bool live = i < n;
     key[r] = live ? (ids ? key_of(ids, i, V) : keys[i]) : 0;
     ps[r] = live ? (ids ? (int)i : pos[i]) : 0;
+  }
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const int d = tid * kPer + j;
+    tot[j] = d < R ? totals[d] : 0;
+    cnt[j] = d < R ? counts[(int64_t)d * blocks + blockIdx.x] : 0;
+  }
+  for (int d = tid; d < kWaves * kMost; d += kSortThreads) ((int*)wc)[d] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < kRuns; ++r) {
+    const bool live = first + r * 64 + lane < n;
     const int d = (key[r] >> shift) & (R - 1);
     uint64_t same = __ballot(live);
     for (int b = 0; b < bits; ++b) {
@@ -177,19 +205,30 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_move(int64_t n, int V, in
       same &= ((d >> b) & 1) ? m : ~m;
     }
     const int before = __popcll(same & ((1ull << lane) - 1));
-    int old = 0;
-    if (live) old = wc[wave][d];
+    const int old = live ? wc[wave][d] : 0;
     rank[r] = old + before;
     if (live && before == 0) wc[wave][d] = old + __popcll(same);
   }
+  // digit bases: exclusive totals over the digits, kPer consecutive ones a thread
+  int sum = 0;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) sum += tot[j];
+  const int incl = wave_scan(sum, lane);
+  if (lane == 63) wsum[wave] = incl;
   __syncthreads();
-  for (int d = tid; d < R; d += kSortThreads) {
-    int s = base[d];
+  int base = incl - sum;
+  for (int w = 0; w < wave; ++w) base += wsum[w];
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const int d = tid * kPer + j;
+    int s = base + cnt[j];
+#pragma unroll
     for (int w = 0; w < kWaves; ++w) {
       const int c = wc[w][d];
       wc[w][d] = s;
       s += c;
     }
+    base += tot[j];
   }
   __syncthreads();
 #pragma unroll
@@ -200,12 +239,6 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_move(int64_t n, int V, in
       pos_out[to] = ps[r];
     }
   }
-}
-
-__global__ __launch_bounds__(256) void k_zero16(uint4* __restrict__ p, int64_t n16, char* __restrict__ tail, int rest) {
-  const int64_t step = (int64_t)gridDim.x * 256;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n16; i += step) p[i] = make_uint4(0, 0, 0, 0);
-  if (blockIdx.x == 0 && (int)threadIdx.x < rest) tail[threadIdx.x] = 0;
 }
 
 template <typename T>
@@ -224,9 +257,15 @@ __device__ inline void write_row(T* dtable, int v, int c, int D, const float* ac
   store_cols(row, c, D, y);
 }
 
+template <int N> __device__ inline void store_sums(float* row, int c, int D, const float* x) {
+#pragma unroll
+  for (int j = 0; j < N; j += Vec<float>::N) store_cols(row, c + j, D, x + j);
+}
+
 // One lane group per chunk of kChunk sorted pairs (and per lpr * N columns: blockIdx.y). An item whose pairs are all
 // in the chunk is written; the sum of the first item, where it began earlier, goes to part[chunk][0], that of the
-// last, where it began here and goes on, to part[chunk][1].
+// last, where it began here and goes on, to part[chunk][1]. The chunk's rows are loaded together before they are
+// added: with one row after another the kernel took 39 us at 25,600 x 128 bf16.
 template <typename T>
 __global__ __launch_bounds__(256) void k_embed_grad(int64_t n, int V, int D, int lpr, const int* __restrict__ keys,
                                                     const int* __restrict__ pos, const T* __restrict__ dout,
@@ -237,58 +276,114 @@ __global__ __launch_bounds__(256) void k_embed_grad(int64_t n, int V, int D, int
   const int c = (blockIdx.y * lpr + threadIdx.x % lpr) * N;
   const int64_t e0 = chunk * kChunk;
   if (e0 >= n || c >= D) return;
-  const int64_t e1 = e0 + kChunk < n ? e0 + kChunk : n;
-  int cur = keys[e0];
-  bool began_here = e0 == 0 || keys[e0 - 1] != cur;
-  float acc[N] = {};
-  for (int64_t e = e0; e < e1; ++e) {
-    const int v = keys[e];
-    if (v >= V) break;  // the pairs without an item come last
-    if (v != cur) {
-      if (began_here) write_row(dtable, cur, c, D, acc, scale, accumulate);
-      else {
-        for (int j = 0; j < N && c + j < D; ++j) part[(chunk * 2 + 0) * D + c + j] = acc[j];
-      }
-      cur = v;
-      began_here = true;
+  int key[kChunk], at[kChunk];
+  const int before = e0 > 0 ? keys[e0 - 1] : -1, after = e0 + kChunk < n ? keys[e0 + kChunk] : V;
 #pragma unroll
-      for (int j = 0; j < N; ++j) acc[j] = 0.f;
-    }
-    float x[N];
-    load_cols(dout + (int64_t)pos[e] * D, c, D, x);
-#pragma unroll
-    for (int j = 0; j < N; ++j) acc[j] += x[j];
+  for (int i = 0; i < kChunk; ++i) {
+    key[i] = e0 + i < n ? keys[e0 + i] : V;
+    at[i] = e0 + i < n ? pos[e0 + i] : 0;
   }
-  if (cur >= V) return;
-  const bool goes_on = e1 < n && keys[e1] == cur;
-  if (began_here && !goes_on) {
-    write_row(dtable, cur, c, D, acc, scale, accumulate);
-  } else {
-    float* p = part + (chunk * 2 + (began_here ? 1 : 0)) * D;
-    for (int j = 0; j < N && c + j < D; ++j) p[c + j] = acc[j];
+  float x[kChunk][N];
+#pragma unroll
+  for (int i = 0; i < kChunk; ++i) {
+    if (key[i] < V) {
+      load_cols(dout + (int64_t)at[i] * D, c, D, x[i]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < N; ++j) x[i][j] = 0.f;
+    }
+  }
+  bool began_here = before != key[0];
+  float acc[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) acc[j] = x[0][j];
+#pragma unroll
+  for (int i = 0; i < kChunk; ++i) {
+    if (key[i] >= V) return;  // the pairs without an item come last
+    const int next = i + 1 < kChunk ? key[i + 1] : after;
+    if (next != key[i]) {
+      if (began_here) {
+        write_row(dtable, key[i], c, D, acc, scale, accumulate);
+      } else {
+        store_sums<N>(part + chunk * 2 * D, c, D, acc);
+      }
+      began_here = true;
+    } else if (i + 1 == kChunk) {
+      store_sums<N>(part + (chunk * 2 + (began_here ? 1 : 0)) * D, c, D, acc);
+    }
+    if (i + 1 < kChunk) {
+#pragma unroll
+      for (int j = 0; j < N; ++j) acc[j] = (next != key[i] ? 0.f : acc[j]) + x[i + 1][j];
+    }
   }
 }
 
-// Joins the partial sums of the items that span chunks: the chunk where such an item begins adds its own and those
-// of the chunks behind it, in order.
+// Joins the partial sums of the items that span chunks. A wave looks at one chunk: if an item begins there and goes
+// on, it counts the chunks that the item reaches into (64 probes at a time: the keys are sorted). Then the workgroup
+// adds the partials of each such item: group g those of the chunks g, g + groups, ... in order, and the groups' sums
+// in order of g.
 template <typename T>
 __global__ __launch_bounds__(256) void k_embed_join(int64_t n, int64_t chunks, int V, int D, int lpr,
                                                     const int* __restrict__ keys, float scale, bool accumulate,
                                                     T* __restrict__ dtable, const float* __restrict__ part) {
   constexpr int N = Vec<T>::N;
-  const int64_t chunk = (int64_t)blockIdx.x * (256 / lpr) + threadIdx.x / lpr;
+  __shared__ int item[4];
+  __shared__ int64_t more[4];
+  __shared__ float sums[256][N];
+  const int wave = threadIdx.x / 64, lane = threadIdx.x % 64;
+  {
+    const int64_t chunk = (int64_t)blockIdx.x * 4 + wave, e0 = chunk * kChunk, e1 = e0 + kChunk;
+    int v = V;
+    int64_t count = 0;
+    if (e1 < n) {
+      const int last = keys[e1 - 1], next = keys[e1], head = keys[e0], before = e0 > 0 ? keys[e0 - 1] : -1;
+      if (last < V && next == last && !(head == last && before == last)) {
+        v = last;
+        int64_t lo = chunk + 1, cnt = chunks - lo;  // chunk lo begins with v; the answer is in [lo, lo + cnt)
+        while (cnt > 1) {
+          const int64_t step = (cnt + 63) / 64, p = lane * step;
+          const uint64_t m = __ballot(p < cnt && keys[(lo + p) * kChunk] == v);
+          const int64_t k = m ? 63 - __builtin_clzll(m) : 0;
+          lo += k * step;
+          cnt = cnt - k * step < step ? cnt - k * step : step;
+        }
+        count = lo - chunk;
+      }
+    }
+    if (lane == 0) item[wave] = v, more[wave] = count;
+  }
+  __syncthreads();
+  const int g = threadIdx.x / lpr, groups = 256 / lpr;
   const int c = (blockIdx.y * lpr + threadIdx.x % lpr) * N;
-  const int64_t e1 = (chunk + 1) * kChunk;
-  if (e1 >= n || c >= D) return;
-  const int v = keys[e1 - 1];
-  if (v >= V || keys[e1] != v) return;                              // nothing goes on
-  const int64_t e0 = chunk * kChunk;
-  if (keys[e0] == v && e0 > 0 && keys[e0 - 1] == v) return;         // it began earlier
-  float acc[N] = {};
-  for (int j = 0; j < N && c + j < D; ++j) acc[j] = part[(chunk * 2 + 1) * D + c + j];
-  for (int64_t k = chunk + 1; k < chunks && keys[k * kChunk] == v; ++k)
-    for (int j = 0; j < N && c + j < D; ++j) acc[j] += part[(k * 2) * D + c + j];
-  write_row(dtable, v, c, D, acc, scale, accumulate);
+  for (int w = 0; w < 4; ++w) {
+    const int64_t count = more[w];
+    if (count == 0) continue;  // the same for the whole workgroup
+    const float* p = part + ((int64_t)blockIdx.x * 4 + w) * 2 * D;
+    float acc[N] = {};
+    if (c < D) {
+      // partial 0 is the first chunk's last item, partial k > 0 the first item of the k-th chunk behind it
+#pragma unroll 4
+      for (int64_t k = g; k <= count; k += groups) {
+        float x[N];
+        constexpr int M = Vec<float>::N;
+        const float* q = p + (k * 2 + (k == 0 ? 1 : 0)) * D;
+#pragma unroll
+        for (int j = 0; j < N; j += M) load_cols(q, c + j, D, x + j);
+#pragma unroll
+        for (int j = 0; j < N; ++j) acc[j] += x[j];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < N; ++j) sums[threadIdx.x][j] = acc[j];
+    __syncthreads();
+    if (g == 0 && c < D) {
+      for (int k = 1; k < groups && k <= count; ++k)
+#pragma unroll
+        for (int j = 0; j < N; ++j) acc[j] += sums[k * lpr + threadIdx.x][j];
+      write_row(dtable, item[w], c, D, acc, scale, accumulate);
+    }
+    __syncthreads();
+  }
 }
 
 template <typename T, typename I>
@@ -303,38 +398,53 @@ hipError_t forward_t(int64_t n, int V, int D, const void* ids, const void* table
 template <typename T, typename I>
 hipError_t backward_t(int64_t n, int V, int D, const void* ids, const void* dout, float scale, bool accumulate,
                       void* dtable, char* ws, hipStream_t st) {
-  if (!accumulate) {
-    const size_t bytes = (size_t)V * D * sizeof(T);
-    const int64_t n16 = (int64_t)(bytes / 16);
-    const int64_t blocks = cdiv(n16, 256 * 8);
-    k_zero16<<<dim3((unsigned)(blocks < 1 ? 1 : (blocks > 8192 ? 8192 : blocks))), dim3(256), 0, st>>>(
-        (uint4*)dtable, n16, (char*)dtable + n16 * 16, (int)(bytes % 16));
+  const int64_t bytes = accumulate ? 0 : (int64_t)V * D * (int64_t)sizeof(T);
+  if (n == 0) {
+    if (bytes) k_fill<<<dim3((unsigned)cdiv(bytes, kFillBytes)), dim3(kSortThreads), 0, st>>>({(char*)dtable, bytes, 0});
+    return hipGetLastError();
   }
-  if (n == 0) return hipGetLastError();
   const BwdLayout L = bwd_layout(n, V, D);
   const SortPlan p = sort_plan(n, V);
   int* counts = (int*)(ws + L.counts);
   int* totals = (int*)(ws + L.totals);
   const int blocks = (int)p.blocks, digits = 1 << p.bits;
+  // the table's share of each of the sort's launches
+  const int64_t share = cdiv(cdiv(bytes, 3 * p.passes), kFillBytes) * kFillBytes;
+  int64_t done = 0;
+  int more = 0;  // workgroups that clear
+  auto next = [&](int first) {
+    const int64_t b = bytes - done < share ? bytes - done : share;
+    const Fill f = {(char*)dtable + done, b, first};
+    done += b;
+    more = (int)cdiv(b, kFillBytes);
+    return f;
+  };
   for (int s = 0; s < p.passes; ++s) {
     const I* id0 = s == 0 ? (const I*)ids : nullptr;
     const int* kin = (const int*)(ws + L.keys[(s + 1) & 1]);
     const int* pin = (const int*)(ws + L.pos[(s + 1) & 1]);
     int* kout = (int*)(ws + L.keys[s & 1]);
     int* pout = (int*)(ws + L.pos[s & 1]);
-    k_sort_count<I><<<dim3(blocks), dim3(kSortThreads), 0, st>>>(n, V, s * p.bits, p.bits, blocks, id0, kin, counts);
-    k_sort_scan<<<dim3((digits + 3) / 4), dim3(256), 0, st>>>(digits, blocks, counts, totals);
-    k_sort_move<I><<<dim3(blocks), dim3(kSortThreads), 0, st>>>(n, V, s * p.bits, p.bits, blocks, id0, kin, pin, counts,
-                                                               totals, kout, pout);
+    const int scans = (int)cdiv(digits, kSortThreads / 64);
+    Fill f = next(blocks);
+    k_sort_count<I><<<dim3(blocks + more), dim3(kSortThreads), 0, st>>>(f, n, V, s * p.bits, p.bits, blocks, id0, kin,
+                                                                       counts);
+    f = next(scans);
+    k_sort_scan<<<dim3(scans + more), dim3(kSortThreads), 0, st>>>(f, digits, blocks, counts, totals);
+    f = next(blocks);
+    k_sort_move<I><<<dim3(blocks + more), dim3(kSortThreads), 0, st>>>(f, n, V, s * p.bits, p.bits, blocks, id0, kin,
+                                                                      pin, counts, totals, kout, pout);
   }
   const int* keys = (const int*)(ws + L.keys[(p.passes - 1) & 1]);
   const int* pos = (const int*)(ws + L.pos[(p.passes - 1) & 1]);
   const int lpr = lanes_of(D, Vec<T>::N);
-  const dim3 grid((unsigned)cdiv(L.chunks, 256 / lpr), (unsigned)cdiv(D, lpr * Vec<T>::N));
+  const unsigned cols = (unsigned)cdiv(D, lpr * Vec<T>::N);
   float* part = (float*)(ws + L.part);
-  k_embed_grad<T><<<grid, dim3(256), 0, st>>>(n, V, D, lpr, keys, pos, (const T*)dout, scale, accumulate, (T*)dtable,
-                                              part);
-  k_embed_join<T><<<grid, dim3(256), 0, st>>>(n, L.chunks, V, D, lpr, keys, scale, accumulate, (T*)dtable, part);
+  k_embed_grad<T><<<dim3((unsigned)cdiv(L.chunks, 256 / lpr), cols), dim3(256), 0, st>>>(
+      n, V, D, lpr, keys, pos, (const T*)dout, scale, accumulate, (T*)dtable, part);
+  if (L.chunks > 1)
+    k_embed_join<T><<<dim3((unsigned)cdiv(L.chunks, 4), cols), dim3(256), 0, st>>>(n, L.chunks, V, D, lpr, keys, scale,
+                                                                                   accumulate, (T*)dtable, part);
   return hipGetLastError();
 }
 

@@ -301,13 +301,13 @@ __global__ __launch_bounds__(1024) void k_norm_join(int parts, int D, const floa
 struct Hold {
   int G, C;
 };
-template <typename T> Hold hold_of(int D) {
-  constexpr int N = Vec<T>::N, kMost = 32 / N;
+template <typename T> Hold hold_of(int D, int most) {
+  constexpr int N = Vec<T>::N;
   const int chunks = (int)cdiv(D, N);
   Hold h;
   h.G = 1;
   while (h.G < 64 && h.G < chunks) h.G *= 2;
-  if (cdiv(chunks, h.G) > kMost) h.G = kThreads;
+  if (cdiv(chunks, h.G) * N > most) h.G = kThreads;
   h.C = 1;
   while (h.C * h.G < chunks) h.C *= 2;
   return h;
@@ -316,7 +316,7 @@ template <typename T> Hold hold_of(int D) {
 // Workgroups of the backward, each with a partial: at least four rows for each of its groups, so that the partials are
 // a small part of what is moved.
 int parts_of(int64_t rows, int D) {
-  const int per = D > kWide ? 4 : 16;
+  const int per = D > kWide ? 4 : (D > 512 ? 8 : 32);
   const int64_t p = cdiv(rows, per);
   return (int)(p < kMaxParts ? p : kMaxParts);
 }
@@ -329,7 +329,7 @@ hipError_t forward_t(int64_t rows, int D, const void* x, int64_t xs, const void*
                                                                        eps, (T*)y, mean, rstd);
     return hipGetLastError();
   }
-  const Hold h = hold_of<T>(D);
+  const Hold h = hold_of<T>(D, 32);
   const dim3 grid((unsigned)cdiv(rows, kThreads / h.G));
 #define CUTBCE_NORM(C)                                                                                           \
   k_norm<T, P, C><<<grid, dim3(kThreads), 0, st>>>(rows, D, h.G, (const T*)x, xs, (const P*)w, (const P*)b, eps, \
@@ -358,7 +358,7 @@ hipError_t backward_t(int64_t rows, int D, const void* dy, int64_t dys, const vo
       k_norm_wide_part<T><<<dim3(parts, (unsigned)cdiv(D, kThreads)), dim3(kThreads), 0, st>>>(
           rows, D, (const T*)dy, dys, (const T*)x, xs, mean, rstd, (float*)ws);
   } else if (parts) {
-    const Hold h = hold_of<T>(D);
+    const Hold h = hold_of<T>(D, 16);
     const int lds = params && h.G <= 64 ? 2 * D * (int)sizeof(float) : 0;  // at most 16 KB
 #define CUTBCE_GRAD(C)                                                                                               \
   (params ? k_norm_grad<T, P, C, true><<<dim3(parts), dim3(kThreads), lds, st>>>(                                    \
