@@ -67,11 +67,14 @@ template <typename T, int DH> struct Tile {
 // One workgroup's (or wave's) loads of NR rows into LDS: NL lanes, 16 bytes each per instruction.
 template <typename T, int DH, int NR, int NL> struct Dma {
   using Ti = Tile<T, DH>;
-  static constexpr int kRounds = NR * Ti::kCPR / NL, kStep = NL / Ti::kCPR;  // rows per round
+  static constexpr int kChunks = NR * Ti::kCPR, kLanes = kChunks < NL ? kChunks : NL;  // whole waves load
+  static constexpr int kRounds = kChunks / kLanes, kStep = kLanes / Ti::kCPR;            // rows per round
   static constexpr int kBytes = NR * Ti::kRowB;
-  static_assert(kRounds >= 1 && kRounds * kStep == NR, "");
+  static_assert(kRounds * kStep == NR && kLanes % 64 == 0, "");
+  bool on;
   int row, chunk, step;  // this lane's row offset in bytes and chunk in the first round; bytes from round to round
   __device__ inline void init(int lane, int64_t stride) {
+    on = lane < kLanes;
     const int r = lane / Ti::kCPR;
     row = (int)(r * stride * Ti::kEsz);
     chunk = (lane % Ti::kCPR) ^ Ti::swz(r);
@@ -85,16 +88,25 @@ template <typename T, int DH, int NR, int NL> struct Dma {
   // rows [0, rem) of `base` (uniform; rem may be <= 0 or > NR) to LDS byte `dst` (uniform: the wave's first kilobyte)
   __device__ inline void load(const T* base, int64_t rem, int64_t stride, int dh, uint32_t dst) const {
 #if defined(__HIP_DEVICE_COMPILE__)  // (the host pass silently drops kernels that reach these builtins this way)
+    if (kLanes < NL && !on) return;
     const int rows = (int)clamp64(rem, 0, NR);
     const int bytes = rows > 0 ? (int)((rows - 1) * stride + dh) * Ti::kEsz : 0;
     const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)base, (short)0, bytes, 0x00020000);
 #pragma unroll
     for (int q = 0; q < kRounds; ++q)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (CUTBCE_LDS void*)(size_t)(dst + q * NL * 16), 16, offset(q, dh), 0, 0,
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (CUTBCE_LDS void*)(size_t)(dst + q * kLanes * 16), 16, offset(q, dh), 0, 0,
                                                0);
 #endif
   }
 };
+
+// 64 words of 4 bytes to LDS byte `dst` (uniform), zeros behind `bytes`.
+__device__ inline void load_words(const void* base, int bytes, uint32_t dst, int lane) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)base, (short)0, bytes, 0x00020000);
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (CUTBCE_LDS void*)(size_t)dst, 4, lane * 4, 0, 0, 0);
+#endif
+}
 
 __device__ inline u32x4 lds16(uint32_t at) { return *(CUTBCE_LDS const u32x4*)(size_t)at; }
 
@@ -113,26 +125,25 @@ template <> struct Mma<__bf16> {
     for (int i = 0; i < 16; ++i) p.g[i / 8][i % 8] = (__bf16)x[i];
     return p;
   }
-  // acc += X^T P: X the 32 rows from LDS row r0 (a multiple of 32) of the tile at `at`
-  template <int DH>
-  __device__ static inline void mma_t(f32x16* acc, const P& p, uint32_t at, int r0, int lane) {
+  // acc += X^T P, X the 32 rows from LDS row r0 (a multiple of 32) of the tile at `at`: in kSlots matrix instructions,
+  // the blocks of features in turn, each with an operand of its own.
+  typedef bf16x8 A;
+  static constexpr int kSlotsPerBlock = 2;
+  template <int DH> __device__ static inline A load_t(int slot, uint32_t at, int r0, int lane) {
     using Ti = Tile<__bf16, DH>;
-    const int h = lane / 32, s = lane % 16;
+    const int h = lane / 32, s = lane % 16, g = slot / Ti::kNDB, db = slot % Ti::kNDB;
+    s16x4 x[2];
 #pragma unroll
-    for (int g = 0; g < 2; ++g)
-#pragma unroll
-      for (int db = 0; db < Ti::kNDB; ++db) {
-        s16x4 x[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int row = 16 * g + 8 * e + 4 * h + s / 4;
-          const int c = (db * 4 + 2 * ((lane / 16) & 1) + ((s & 3) >> 1)) ^ Ti::swz(row);
-          x[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (CUTBCE_LDS s16x4*)(size_t)(at + (r0 + row) * Ti::kRowB + c * 16 + (s & 1) * 8));
-        }
-        const s16x8 a = __builtin_shufflevector(x[0], x[1], 0, 1, 2, 3, 4, 5, 6, 7);
-        acc[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), p.g[g], acc[db], 0, 0, 0);
-      }
+    for (int e = 0; e < 2; ++e) {
+      const int row = 16 * g + 8 * e + 4 * h + s / 4;
+      const int c = (db * 4 + 2 * ((lane / 16) & 1) + ((s & 3) >> 1)) ^ Ti::swz(row);
+      x[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+          (CUTBCE_LDS s16x4*)(size_t)(at + (r0 + row) * Ti::kRowB + c * 16 + (s & 1) * 8));
+    }
+    return __builtin_bit_cast(A, (s16x8)__builtin_shufflevector(x[0], x[1], 0, 1, 2, 3, 4, 5, 6, 7));
+  }
+  template <int NDB> __device__ static inline void slot_t(f32x16* acc, int slot, A a, const P& p) {
+    acc[slot % NDB] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, p.g[slot / NDB], acc[slot % NDB], 0, 0, 0);
   }
 };
 
@@ -146,32 +157,42 @@ template <> struct Mma<float> {
   }
   __device__ static inline u32x4 negate(u32x4 x) { return x ^ 0x80000000u; }
   __device__ static inline P pack(const f32x16& x) { return x; }
-  template <int DH>
-  __device__ static inline void mma_t(f32x16* acc, const P& p, uint32_t at, int r0, int lane) {
+  typedef float A;
+  static constexpr int kSlotsPerBlock = 16;
+  template <int DH> __device__ static inline A load_t(int slot, uint32_t at, int r0, int lane) {
     using Ti = Tile<float, DH>;
-    const int h = lane / 32, n = lane % 32;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int row = acc_row(i, h);
-#pragma unroll
-      for (int db = 0; db < Ti::kNDB; ++db) {
-        const int c = (db * 8 + n / 4) ^ Ti::swz(row);
-        const float x = *(CUTBCE_LDS const float*)(size_t)(at + (r0 + row) * Ti::kRowB + c * 16 + (n % 4) * 4);
-        acc[db] = __builtin_amdgcn_mfma_f32_32x32x2f32(x, p[i], acc[db], 0, 0, 0);
-      }
-    }
+    const int n = lane % 32, row = acc_row(slot / Ti::kNDB, lane / 32);
+    const int c = ((slot % Ti::kNDB) * 8 + n / 4) ^ Ti::swz(row);
+    return *(CUTBCE_LDS const float*)(size_t)(at + (r0 + row) * Ti::kRowB + c * 16 + (n % 4) * 4);
+  }
+  template <int NDB> __device__ static inline void slot_t(f32x16* acc, int slot, A a, const P& p) {
+    acc[slot % NDB] = __builtin_amdgcn_mfma_f32_32x32x2f32(a, p[slot / NDB], acc[slot % NDB], 0, 0, 0);
   }
 };
+
+// acc += X^T P, scheduled by the compiler.
+template <typename T, int DH>
+__device__ inline void product_t(f32x16* acc, const typename Mma<T>::P& p, uint32_t at, int r0, int lane) {
+  constexpr int NDB = Tile<T, DH>::kNDB;
+#pragma unroll
+  for (int k = 0; k < Mma<T>::kSlotsPerBlock * NDB; ++k)
+    Mma<T>::template slot_t<NDB>(acc, k, Mma<T>::template load_t<DH>(k, at, r0, lane), p);
+}
+
+// The tile's operand of k-step t: rows 0 .. 31 from `at`.
+template <typename T, int DH> __device__ inline u32x4 tile_chunk(uint32_t at, int t, int lane) {
+  using Ti = Tile<T, DH>;
+  const int r = lane % 32;
+  return lds16(at + r * Ti::kRowB + (((2 * t + lane / 32) ^ Ti::swz(r)) * 16));
+}
 
 // 32 rows of a tile times the own operand: the result's rows are the tile's, its columns the own rows.
 template <typename T, int DH>
 __device__ inline f32x16 product(uint32_t at, int r0, const u32x4* own, int lane) {
   using Ti = Tile<T, DH>;
-  const int r = lane % 32, h = lane / 32;
   f32x16 s = {};
 #pragma unroll
-  for (int t = 0; t < Ti::kNT; ++t)
-    s = Mma<T>::mma(lds16(at + (r0 + r) * Ti::kRowB + (((2 * t + h) ^ Ti::swz(r)) * 16)), own[t], s);
+  for (int t = 0; t < Ti::kNT; ++t) s = Mma<T>::mma(tile_chunk<T, DH>(at + r0 * Ti::kRowB, t, lane), own[t], s);
   return s;
 }
 
@@ -206,8 +227,8 @@ template <typename T, int NDB> __device__ inline void store_row(T* row, const f3
     }
 }
 
-// Work units: tiles of kRows rows. Sequence b's tiles start at unit start(b) / kRows + b, which leaves room for each
-// of them (a range of n rows spans at most n / kRows + 1 units' worth of starts), so the units can be found without a
+// Work units: tiles of M rows. Sequence b's tiles start at unit start(b) / M + b, which leaves room for each
+// of them (a range of n rows spans at least ceil(n / M) of these numbers), so the units can be found without a
 // running total. The lanes of a wave look at 64 sequences at a time.
 struct Unit {
   SeqRange s;
@@ -216,12 +237,12 @@ struct Unit {
 __device__ inline int64_t start_of(const int32_t* cu, int64_t pitch, int64_t rows, int b) {
   return cu ? clamp64(cu[b], 0, rows) : b * pitch;
 }
-__device__ inline Unit find_unit(const Attn& a, const int32_t* cu, int64_t pitch, int64_t rows, int64_t unit) {
+template <int M> __device__ inline Unit find_unit(const Attn& a, const int32_t* cu, int64_t pitch, int64_t rows, int64_t unit) {
   const int lane = threadIdx.x % 64;
   int lo = 0, cnt = a.seqs + 1;
   while (cnt > 1) {
     const int step = (cnt + 63) / 64, at = lane * step;
-    const bool ok = at < cnt && start_of(cu, pitch, rows, lo + at) / kRows + lo + at <= unit;
+    const bool ok = at < cnt && start_of(cu, pitch, rows, lo + at) / M + lo + at <= unit;
     const uint64_t m = __ballot(ok);
     const int n = m ? 63 - __builtin_clzll(m) : 0;
     lo += n * step;
@@ -229,21 +250,24 @@ __device__ inline Unit find_unit(const Attn& a, const int32_t* cu, int64_t pitch
   }
   lo = uni(lo);
   Unit u;
-  const int64_t first = start_of(cu, pitch, rows, lo) / kRows + lo;
+  const int64_t first = start_of(cu, pitch, rows, lo) / M + lo;
   u.tile = uni((int)clamp64(unit - first, 0, 1 << 30));
   const SeqRange s = seq_range(a, lo);
   u.s.q0 = uni64(s.q0), u.s.k0 = uni64(s.k0), u.s.kb = uni64(s.kb), u.s.vb = uni64(s.vb);
   u.s.n = uni(s.n), u.s.m = uni(s.m), u.s.cap = uni(s.cap);
   return u;
 }
-int64_t units_of(int64_t rows, int seqs) { return rows / kRows + seqs + 1; }
+int64_t units_of(int64_t rows, int seqs, int m = kRows) { return rows / m + seqs + 1; }
 
 // Keys that row t of the sequence sees.
 __device__ inline int seen_by(const Attn& a, const SeqRange& s, int64_t t) {
   return a.causal ? (int)clamp64(t + s.m - s.n + 1, 0, s.m) : s.m;
 }
 
-__device__ inline void wait_and_sync() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+// Waits until at most N of the wave's loads are in flight and its LDS accesses are done, then for the workgroup.
+template <int N = 0> __device__ inline void wait_and_sync() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
 
 template <typename T, int DH> constexpr int key_tile() { return sizeof(T) == 4 && DH > 64 ? 32 : 64; }
 
@@ -295,7 +319,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(Attn a, int64_t units, T* _
   const uint32_t lds0 = uni((uint32_t)(size_t)(CUTBCE_LDS char*)lds);
   const int tid = threadIdx.x, wave = uni(tid / 64), lane = tid % 64;
   const int h = blockIdx.x % a.hq;
-  const Unit u = find_unit(a, a.cu_q, a.q_pitch, a.q_rows, units - 1 - blockIdx.x / a.hq);
+  const Unit u = find_unit<kRows>(a, a.cu_q, a.q_pitch, a.q_rows, units - 1 - blockIdx.x / a.hq);
   const SeqRange& s = u.s;
   const int64_t r0 = (int64_t)u.tile * kRows;  // first row of the workgroup in its sequence
   if (r0 >= s.n) return;
@@ -330,7 +354,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(Attn a, int64_t units, T* _
   Online st;
   if (steps > 0) fetch(0);
   for (int i = 0; i < steps; ++i) {
-    wait_and_sync();
+    wait_and_sync<>();
     if (i + 1 < steps) fetch(i + 1);
     const int j0 = i * KT;
     if (j0 < wave_hi) {
@@ -347,7 +371,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(Attn a, int64_t units, T* _
       }
       softmax_step<NS, Ti::kNDB>(x, c, st, o);
 #pragma unroll
-      for (int b = 0; b < NS; ++b) Mma<T>::template mma_t<DH>(o, Mma<T>::pack(x[b]), vt, b * 32, lane);
+      for (int b = 0; b < NS; ++b) product_t<T, DH>(o, Mma<T>::pack(x[b]), vt, b * 32, lane);
     }
   }
   const float sum = st.sum + other_half(st.sum);
@@ -370,7 +394,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 4 && DH > 64 ? 1 : 2) void k_attn
   const uint32_t lds0 = uni((uint32_t)(size_t)(CUTBCE_LDS char*)lds);
   const int tid = threadIdx.x, wave = uni(tid / 64), lane = tid % 64;
   const int h = blockIdx.x % a.hq;
-  const Unit u = find_unit(a, a.cu_q, a.q_pitch, a.q_rows, units - 1 - blockIdx.x / a.hq);
+  const Unit u = find_unit<kRows>(a, a.cu_q, a.q_pitch, a.q_rows, units - 1 - blockIdx.x / a.hq);
   const SeqRange& s = u.s;
   const int64_t r0 = (int64_t)u.tile * kRows;
   if (r0 >= s.n) return;
@@ -417,7 +441,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 4 && DH > 64 ? 1 : 2) void k_attn
   f32x16 acc[Ti::kNDB] = {};
   if (steps > 0) fetch(0);
   for (int i = 0; i < steps; ++i) {
-    wait_and_sync();
+    wait_and_sync<>();
     if (i + 1 < steps) fetch(i + 1);
     const int j0 = i * KT;
     if (j0 < wave_hi) {
@@ -434,104 +458,153 @@ __global__ __launch_bounds__(256, sizeof(T) == 4 && DH > 64 ? 1 : 2) void k_attn
           for (int e = 0; e < 16; ++e)
             if (j0 + b * 32 + acc_row(e, lane / 32) >= mine) x[e] = 0.f;
         }
-        Mma<T>::template mma_t<DH>(acc, Mma<T>::pack(x), kt, b * 32, lane);
+        product_t<T, DH>(acc, Mma<T>::pack(x), kt, b * 32, lane);
       }
     }
   }
   if (live) store_row<T, Ti::kNDB>(dq + at * a.dh, acc, a.scale, a.dh, lane);
 }
 
-// dk and dv: a workgroup has 128 keys of one sequence and key/value head, a wave 32 of them; the rows of the group's
-// heads stream through two LDS stages of 32 rows.
+// How the dk/dv kernel lays out a workgroup: 64 keys, two waves for each 32 of them and each of the RS row blocks of
+// a stage (32 RS rows of q and dO with their (lse, delta), three stages), and P in float32 from the first wave of a
+// pair to the second, twice.
+template <typename T, int DH> struct Dkv {
+  static constexpr int kRS = sizeof(T) == 2 && DH > 64 ? 2 : 1;
+  static constexpr int kKeys = 64, kQT = 32 * kRS, kStages = 3, kPairs = 2 * kRS, kThreads = kPairs * 128;
+  using Ld = Dma<T, DH, kQT, kThreads>;
+  static constexpr int kStage = 2 * Ld::kBytes + kQT * 8;
+  static constexpr int kP = (kStages * kStage + 1023) / 1024 * 1024, kBytes = kP + kPairs * 2 * 4096;
+  static_assert(kBytes <= 160 * 1024 && kPairs * Tile<T, DH>::kNDB * 4096 <= kBytes, "");
+};
+
+// dk and dv: a workgroup has 64 keys of one sequence and key/value head; the rows of the group's heads stream through
+// LDS. One wave would need the sums of dk and dv, k and v of its keys and two score tiles (over 256 registers at
+// head_dim 128, one wave per SIMD, and half of them in accumulation registers that vector instructions cannot reach:
+// 1.33 ms at 4 x 8192). So a pair of waves shares 32 keys: the first has k and dv (scores, P, P^T dO), the second v
+// and dk (dP, dS, dS^T Q) one tile behind, with P handed over in LDS. Two waves per SIMD, one of each kind, hide each
+// other's latencies.
 template <typename T, int DH>
-__global__ __launch_bounds__(256, DH > 64 || sizeof(T) == 4 ? 1 : 2) void k_attn_dkv(
-    Attn a, const T* __restrict__ dout, const float2* __restrict__ stat, T* __restrict__ dk, T* __restrict__ dv) {
+__global__ __launch_bounds__((Dkv<T, DH>::kThreads), 2) void k_attn_dkv(Attn a, const T* __restrict__ dout,
+                                                                        const float2* __restrict__ stat,
+                                                                        T* __restrict__ dk, T* __restrict__ dv) {
   using Ti = Tile<T, DH>;
-  constexpr int QT = sizeof(T) == 2 && DH <= 32 ? 64 : 32, NS = QT / 32;
-  using Ld = Dma<T, DH, QT, 256>;
-  constexpr int kStage = 2 * Ld::kBytes + QT * 8;
+  using K = Dkv<T, DH>;
+  using Ld = typename K::Ld;
+  constexpr int QT = K::kQT;
   extern __shared__ __align__(1024) char lds[];
   const uint32_t lds0 = uni((uint32_t)(size_t)(CUTBCE_LDS char*)lds);
   const int tid = threadIdx.x, wave = uni(tid / 64), lane = tid % 64, half = lane / 32;
+  const int pair = wave % K::kPairs, kw = pair % 2, rw = pair / 2;  // which 32 keys, which rows of a stage
+  const bool first = wave < K::kPairs;
   const int hk = blockIdx.x % a.hk;
-  const Unit u = find_unit(a, a.cu_k, a.k_pitch, a.k_rows, blockIdx.x / a.hk);
+  const Unit u = find_unit<K::kKeys>(a, a.cu_k, a.k_pitch, a.k_rows, blockIdx.x / a.hk);
   const SeqRange& s = u.s;
-  const int64_t j0 = (int64_t)u.tile * kRows;
+  const int64_t j0 = (int64_t)u.tile * K::kKeys;
   if (j0 >= s.cap) return;
-  const int64_t j = j0 + wave * 32 + lane % 32;
+  const int64_t j = j0 + kw * 32 + lane % 32;
   const bool key = j < s.m;
-  u32x4 ko[Ti::kNT], vo[Ti::kNT];
-  load_own<T, DH>(ko, (const T*)a.k + s.kb + j * a.k_rs + hk * a.k_hs, key, a.dh, lane);
-  load_own<T, DH>(vo, (const T*)a.v + s.vb + j * a.v_rs + hk * a.v_hs, key, a.dh, lane);
+  u32x4 own[Ti::kNT];
+  load_own<T, DH>(own, first ? (const T*)a.k + s.kb + j * a.k_rs + hk * a.k_hs
+                             : (const T*)a.v + s.vb + j * a.v_rs + hk * a.v_hs, key, a.dh, lane);
   const float c = a.scale * kLog2e;
   // the first row that sees key x: row t sees it if t >= x - (m - n)
   auto first_row = [&](int64_t x) { return a.causal ? (int)clamp64(x - ((int64_t)s.m - s.n), 0, s.n) : 0; };
-  const int mine = first_row(j);
-  const int wave_lo = first_row(j0 + wave * 32), wave_hi = first_row(j0 + wave * 32 + 31);
-  const bool wave_live = j0 + wave * 32 < s.m;
+  const int mine = first_row(j), wave_hi = first_row(j0 + kw * 32 + 31);
   const int begin = j0 < s.m ? first_row(j0) / QT : 0, end = j0 < s.m ? (s.n + QT - 1) / QT : 0;
   const int steps = end > begin ? (end - begin) * a.group : 0;
   Ld lq, lg;
   lq.init(tid, a.q_rs);
   lg.init(tid, (int64_t)a.hq * a.dh);
-  const uint32_t dst = lds0 + wave * 1024;
-  int fh = hk * a.group, ft = begin;  // head and tile of the next fetch
-  auto fetch = [&](int i) {
-    const int64_t t = (int64_t)ft * QT;
-    const uint32_t to = dst + (i & 1) * kStage;
-    lq.load((const T*)a.q + (s.q0 + t) * a.q_rs + fh * a.q_hs, s.n - t, a.q_rs, a.dh, to);
-    lg.load(dout + ((s.q0 + t) * a.hq + fh) * a.dh, s.n - t, (int64_t)a.hq * a.dh, a.dh, to + Ld::kBytes);
-    if (wave < NS) {  // (lse, delta) of 32 rows: 64 lanes, 4 bytes each
-      const int64_t rem = clamp64(s.n - t - wave * 32, 0, 32);
-      const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
-          (void*)(stat + (int64_t)fh * a.q_rows + s.q0 + t + wave * 32), (short)0, (int)rem * 8, 0x00020000);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          r, (CUTBCE_LDS void*)(size_t)(lds0 + (i & 1) * kStage + 2 * Ld::kBytes + wave * 256), 4, lane * 4, 0, 0, 0);
-    }
+  int fh = hk * a.group, ft = begin, fs = 0;  // head, tile and stage of the next fetch
+  auto fetch = [&]() {
+    const int64_t t = (int64_t)ft * QT, rem = s.n - t;
+    const uint32_t stage = lds0 + (uint32_t)fs * K::kStage;
+    lq.load((const T*)a.q + (s.q0 + t) * a.q_rs + fh * a.q_hs, rem, a.q_rs, a.dh, stage + wave * 1024);
+    lg.load(dout + ((s.q0 + t) * a.hq + fh) * a.dh, rem, (int64_t)a.hq * a.dh, a.dh,
+            stage + Ld::kBytes + wave * 1024);
+    if (wave < K::kRS)
+      load_words(stat + (int64_t)fh * a.q_rows + s.q0 + t + wave * 32, (int)clamp64(rem - wave * 32, 0, 32) * 8,
+                 stage + 2 * Ld::kBytes + wave * 256, lane);
     if (++ft == end) ft = begin, ++fh;
+    if (++fs == K::kStages) fs = 0;
   };
-  f32x16 ak[Ti::kNDB] = {}, av[Ti::kNDB] = {};
-  if (steps > 0) fetch(0);
-  int ct = begin;
-  for (int i = 0; i < steps; ++i) {
-    wait_and_sync();
-    if (i + 1 < steps) fetch(i + 1);
-    const int t0 = ct * QT;
-    if (++ct == end) ct = begin;
-    const uint32_t qt = lds0 + (i & 1) * kStage, gt = qt + Ld::kBytes, sl = gt + Ld::kBytes;
-#pragma unroll
-    for (int b = 0; b < NS; ++b) {
-      const int t1 = t0 + b * 32;
-      if (wave_live && t1 + 31 >= wave_lo && t1 < s.n) {
-        f32x16 x = product<T, DH>(qt, b * 32, ko, lane);
-        f32x16 g = product<T, DH>(gt, b * 32, vo, lane);
-        const bool edge = t1 < wave_hi || t1 + 32 > s.n;
+  f32x16 acc[Ti::kNDB] = {};
+  int ct = begin, cs = 0, before = 0;  // the first wave's tile and stage, the second's stage
+  const uint32_t px = lds0 + K::kP + pair * 8192 + lane * 16;
+  if (steps > 0) fetch();
+  for (int i = 0; i <= steps && steps > 0; ++i) {
+    wait_and_sync<>();
+    if (i + 1 < steps) fetch();
+    const uint32_t at = lds0 + (uint32_t)(first ? cs : before) * K::kStage + rw * 32 * Ti::kRowB;
+    const uint32_t sl = lds0 + (uint32_t)(first ? cs : before) * K::kStage + 2 * Ld::kBytes + rw * 256;
+    if (first) {
+      if (i < steps) {
+        const int t1 = ct * QT + rw * 32;
+        f32x16 x = product<T, DH>(at, 0, own, lane);
 #pragma unroll
         for (int e = 0; e < 16; e += 2) {
-          const f32x4 ld = __builtin_bit_cast(f32x4, lds16(sl + (b * 32 + acc_row(e, half)) * 8));
+          const f32x4 ld = __builtin_bit_cast(f32x4, lds16(sl + acc_row(e, half) * 8));
+          x[e] = exp2_of(__builtin_fmaf(x[e], c, -ld[0]));
+          x[e + 1] = exp2_of(__builtin_fmaf(x[e + 1], c, -ld[2]));
+        }
+        if (t1 < wave_hi || t1 + 32 > s.n) {
 #pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            float p = exp2_of(__builtin_fmaf(x[e + w], c, -ld[2 * w]));
-            float d = p * (g[e + w] - ld[2 * w + 1]);
-            const int t = t1 + acc_row(e + w, half);
-            if (edge && (t < mine || t >= s.n)) p = 0.f, d = 0.f;
-            x[e + w] = p;
-            g[e + w] = d;
+          for (int e = 0; e < 16; ++e) {
+            const int t = t1 + acc_row(e, half);
+            if (t < mine || t >= s.n) x[e] = 0.f;
           }
         }
-        Mma<T>::template mma_t<DH>(av, Mma<T>::pack(x), gt, b * 32, lane);
-        Mma<T>::template mma_t<DH>(ak, Mma<T>::pack(g), qt, b * 32, lane);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          *(CUTBCE_LDS f32x4*)(size_t)(px + (i & 1) * 4096 + e * 1024) =
+              f32x4{x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]};
+        product_t<T, DH>(acc, Mma<T>::pack(x), at + Ld::kBytes, 0, lane);
       }
+    } else if (i > 0) {
+      f32x16 g = product<T, DH>(at + Ld::kBytes, 0, own, lane);
+#pragma unroll
+      for (int e = 0; e < 16; e += 4) {
+        const f32x4 p = __builtin_bit_cast(f32x4, lds16(px + ((i - 1) & 1) * 4096 + e * 256));
+        const f32x4 l0 = __builtin_bit_cast(f32x4, lds16(sl + acc_row(e, half) * 8));
+        const f32x4 l1 = __builtin_bit_cast(f32x4, lds16(sl + acc_row(e + 2, half) * 8));
+        g[e] = p[0] * (g[e] - l0[1]);
+        g[e + 1] = p[1] * (g[e + 1] - l0[3]);
+        g[e + 2] = p[2] * (g[e + 2] - l1[1]);
+        g[e + 3] = p[3] * (g[e + 3] - l1[3]);
+      }
+      product_t<T, DH>(acc, Mma<T>::pack(g), at, 0, lane);
     }
+    if (++ct == end) ct = begin;
+    before = cs;
+    if (++cs == K::kStages) cs = 0;
+  }
+  if constexpr (K::kRS > 1) {  // the second rows' sums to the first rows' waves, through LDS
+    wait_and_sync<>();
+    const uint32_t at = lds0 + ((first ? 0 : 2) + kw) * (Ti::kNDB * 4096) + lane * 16;
+#pragma unroll
+    for (int d = 0; d < Ti::kNDB; ++d)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (rw == 1)
+          *(CUTBCE_LDS f32x4*)(size_t)(at + (d * 4 + e) * 1024) =
+              f32x4{acc[d][4 * e], acc[d][4 * e + 1], acc[d][4 * e + 2], acc[d][4 * e + 3]};
+    wait_and_sync<>();
+    if (rw == 1) return;
+#pragma unroll
+    for (int d = 0; d < Ti::kNDB; ++d)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const f32x4 x = __builtin_bit_cast(f32x4, lds16(at + (d * 4 + e) * 1024));
+#pragma unroll
+        for (int w = 0; w < 4; ++w) acc[d][4 * e + w] += x[w];
+      }
   }
   if (j < s.cap) {
-    const int64_t at = ((s.k0 + j) * a.hk + hk) * a.dh;
     if (!key) {  // a place behind the keys: its own values are not used
 #pragma unroll
-      for (int d = 0; d < Ti::kNDB; ++d) ak[d] = f32x16{}, av[d] = f32x16{};
+      for (int d = 0; d < Ti::kNDB; ++d) acc[d] = f32x16{};
     }
-    store_row<T, Ti::kNDB>(dk + at, ak, a.scale, a.dh, lane);
-    store_row<T, Ti::kNDB>(dv + at, av, 1.f, a.dh, lane);
+    store_row<T, Ti::kNDB>((first ? dv : dk) + ((s.k0 + j) * a.hk + hk) * a.dh, acc, first ? 1.f : a.scale, a.dh, lane);
   }
 }
 
@@ -616,7 +689,7 @@ __global__ __launch_bounds__((few_waves<T, DH>() * 64), 1) void k_attn_few(Attn 
         if (b * 32 + acc_row(e, lane / 32) >= mine) x[e] = -INFINITY;
     }
     softmax_step<1, NDB>(&x, c, st, o);
-    Mma<T>::template mma_t<DH>(o, Mma<T>::pack(x), kt + Ld::kBytes, 0, lane);
+    product_t<T, DH>(o, Mma<T>::pack(x), kt + Ld::kBytes, 0, lane);
   }
   st.sum += other_half(st.sum);
   // join the waves: each leaves (max, sum) and its scaled output in LDS, which the rings no longer use
@@ -751,11 +824,11 @@ hipError_t backward_t(const Attn& a, const void* dout, const void* out, const fl
                                                                                lse, (T*)dq, stat);
   }
   if (a.k_rows) {
-    constexpr int QT = sizeof(T) == 2 && DH <= 32 ? 64 : 32;
-    const int bytes = 2 * (2 * QT * Ti::kRowB + QT * 8);
+    using K = Dkv<T, DH>;
+    const int bytes = K::kBytes;
     const hipError_t e = allow_lds((const void*)k_attn_dkv<T, DH>, bytes);
     if (e != hipSuccess) return e;
-    k_attn_dkv<T, DH><<<dim3((unsigned)(units_of(a.k_rows, a.seqs) * a.hk)), dim3(256), bytes, st>>>(
+    k_attn_dkv<T, DH><<<dim3((unsigned)(units_of(a.k_rows, a.seqs, K::kKeys) * a.hk)), dim3(K::kThreads), bytes, st>>>(
         a, (const T*)dout, stat, (T*)dk, (T*)dv);
   }
   return hipGetLastError();

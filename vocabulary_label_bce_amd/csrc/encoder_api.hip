@@ -48,9 +48,9 @@ cutbce_status make_attn(const cutbce_attention* p, const int32_t* cu_q, const in
   const int64_t row_max = (int64_t)1 << 22;
   if (st[0] > row_max || st[2] > row_max || st[4] > row_max || (int64_t)p->q_heads * p->head_dim > row_max)
     return CUTBCE_ERR_SHAPE;
-  // one workgroup per tile of 128 rows and head
+  // one workgroup per tile of 64 rows or more and head
   const int64_t rows = p->q_rows > p->k_rows ? p->q_rows : p->k_rows;
-  if ((rows / 128 + p->seqs + 1) * p->q_heads > kMaxRows) return CUTBCE_ERR_SHAPE;
+  if ((rows / 64 + p->seqs + 1) * p->q_heads > kMaxRows) return CUTBCE_ERR_SHAPE;
   a->q_rs = st[0], a->q_hs = st[1], a->k_rs = st[2], a->k_hs = st[3], a->v_rs = st[4], a->v_hs = st[5];
   a->k_ss = st[6], a->v_ss = st[7];
   a->q_rows = p->q_rows, a->k_rows = p->k_rows;
