@@ -64,8 +64,28 @@ template <typename T, int DH> struct Tile {
   }
 };
 
+// Direct loads from memory to LDS, 16 or 4 bytes a lane from byte `voff` of the buffer to LDS byte `dst` (uniform) +
+// lane * 16 (4); zeros where the buffer ends. As instructions of their own, not as the builtin (which the forward and
+// dq use): before a transpose read the compiler waits for every load to LDS that it knows to be in flight, those of
+// the next stages as well. Nothing is returned in registers; the kernels wait for these loads themselves
+// (wait_and_sync, before the stage is read and before the workgroup ends: no stage is written and read between the same
+// two of those, so the compiler may move LDS reads past these loads). The s_nop covers the wait states between a
+// scalar register's write by a vector instruction (v_readfirstlane) or m0's and its use here.
+__device__ inline u32x4 buffer_of(const void* base, int bytes) {  // uniform
+  const uint64_t at = (uint64_t)base;
+  return u32x4{(uint32_t)uni((int)at), (uint32_t)uni((int)(at >> 32)) & 0xffffu, (uint32_t)uni(bytes), 0x00020000u};
+}
+__device__ inline void load_lds16(u32x4 buffer, int voff, uint32_t dst) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+               :: "s"(dst), "v"(voff), "s"(buffer) : "m0");
+}
+__device__ inline void load_lds4(u32x4 buffer, int voff, uint32_t dst) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dword %1, %2, 0 offen lds"
+               :: "s"(dst), "v"(voff), "s"(buffer) : "m0");
+}
+
 // One workgroup's (or wave's) loads of NR rows into LDS: NL lanes, 16 bytes each per instruction.
-template <typename T, int DH, int NR, int NL> struct Dma {
+template <typename T, int DH, int NR, int NL, bool RAW = false> struct Dma {
   using Ti = Tile<T, DH>;
   static constexpr int kChunks = NR * Ti::kCPR, kLanes = kChunks < NL ? kChunks : NL;  // whole waves load
   static constexpr int kRounds = kChunks / kLanes, kStep = kLanes / Ti::kCPR;            // rows per round
@@ -87,25 +107,28 @@ template <typename T, int DH, int NR, int NL> struct Dma {
   }
   // rows [0, rem) of `base` (uniform; rem may be <= 0 or > NR) to LDS byte `dst` (uniform: the wave's first kilobyte)
   __device__ inline void load(const T* base, int64_t rem, int64_t stride, int dh, uint32_t dst) const {
-#if defined(__HIP_DEVICE_COMPILE__)  // (the host pass silently drops kernels that reach these builtins this way)
     if (kLanes < NL && !on) return;
     const int rows = (int)clamp64(rem, 0, NR);
     const int bytes = rows > 0 ? (int)((rows - 1) * stride + dh) * Ti::kEsz : 0;
-    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)base, (short)0, bytes, 0x00020000);
+    if constexpr (RAW) {
+      const u32x4 r = buffer_of(base, bytes);
 #pragma unroll
-    for (int q = 0; q < kRounds; ++q)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (CUTBCE_LDS void*)(size_t)(dst + q * kLanes * 16), 16, offset(q, dh), 0, 0,
-                                               0);
+      for (int q = 0; q < kRounds; ++q) load_lds16(r, offset(q, dh), dst + q * kLanes * 16);
+    } else {
+#if defined(__HIP_DEVICE_COMPILE__)  // (the host pass silently drops kernels that reach these builtins this way)
+      const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)base, (short)0, bytes, 0x00020000);
+#pragma unroll
+      for (int q = 0; q < kRounds; ++q)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (CUTBCE_LDS void*)(size_t)(dst + q * kLanes * 16), 16,
+                                                 offset(q, dh), 0, 0, 0);
 #endif
+    }
   }
 };
 
-// 64 words of 4 bytes to LDS byte `dst` (uniform), zeros behind `bytes`.
-__device__ inline void load_words(const void* base, int bytes, uint32_t dst, int lane) {
-#if defined(__HIP_DEVICE_COMPILE__)
-  const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)base, (short)0, bytes, 0x00020000);
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (CUTBCE_LDS void*)(size_t)dst, 4, lane * 4, 0, 0, 0);
-#endif
+// (x, y) of 32 rows as 32 x's and 32 y's to LDS byte `dst` (uniform); zeros behind `rows`.
+__device__ inline void load_pairs(const float2* base, int64_t rows, uint32_t dst, int lane) {
+  load_lds4(buffer_of(base, (int)clamp64(rows, 0, 32) * 8), (lane % 32) * 8 + (lane / 32) * 4, dst);
 }
 
 __device__ inline u32x4 lds16(uint32_t at) { return *(CUTBCE_LDS const u32x4*)(size_t)at; }
@@ -196,6 +219,34 @@ __device__ inline f32x16 product(uint32_t at, int r0, const u32x4* own, int lane
   return s;
 }
 
+// The same, and the operands of a transposed product of the tile at `at2` (product_of). In 16-bit elements the order is
+// pinned: all of the first product's operands are read before its first matrix instruction, the second's between
+// them. (Left alone, the compiler reads each operand right before its use and waits for it.)
+template <typename T, int DH>
+__device__ inline f32x16 product_ahead(uint32_t at, const u32x4* own, uint32_t at2, typename Mma<T>::A* a2, int lane) {
+  using Ti = Tile<T, DH>;
+  constexpr int S = Mma<T>::kSlotsPerBlock * Ti::kNDB, NT = Ti::kNT;
+  u32x4 x[NT];
+  f32x16 s = {};
+#pragma unroll
+  for (int t = 0; t < NT; ++t) x[t] = tile_chunk<T, DH>(at, t, lane);
+  if constexpr (sizeof(T) == 2) __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    s = Mma<T>::mma(x[t], own[t], s);
+#pragma unroll
+    for (int k = S * t / NT; k < S * (t + 1) / NT; ++k) a2[k] = Mma<T>::template load_t<DH>(k, at2, 0, lane);
+    if constexpr (sizeof(T) == 2) __builtin_amdgcn_sched_barrier(0);
+  }
+  return s;
+}
+template <typename T, int DH>
+__device__ inline void product_of(f32x16* acc, const typename Mma<T>::P& p, const typename Mma<T>::A* a) {
+  constexpr int NDB = Tile<T, DH>::kNDB;
+#pragma unroll
+  for (int k = 0; k < Mma<T>::kSlotsPerBlock * NDB; ++k) Mma<T>::template slot_t<NDB>(acc, k, a[k], p);
+}
+
 // The own operand: lane l has the chunks 2t + l / 32 of one row (zeros past head_dim, or where !live).
 template <typename T, int DH> __device__ inline void load_own(u32x4* own, const T* row, bool live, int dh, int lane) {
   using Ti = Tile<T, DH>;
@@ -227,9 +278,18 @@ template <typename T, int NDB> __device__ inline void store_row(T* row, const f3
     }
 }
 
-// Work units: tiles of M rows. Sequence b's tiles start at unit start(b) / M + b, which leaves room for each
-// of them (a range of n rows spans at least ceil(n / M) of these numbers), so the units can be found without a
-// running total. The lanes of a wave look at 64 sequences at a time.
+// Work units: tiles of M rows, units_of(rows, seqs, M) numbers for them.
+//
+// Up to 63 sequences: the units are numbered by the tiles left from them to one end of their sequence, most first
+// (ENDS: a tile counts those before it, for kernels whose later tiles see more; else those behind it), so that the
+// workgroups that take longest start first whatever the sequences' order. A lane has a sequence's number of tiles T;
+// the level of unit u is the l with sum max(0, T - l - 1) <= u < sum max(0, T - l). At 4 x 8192 the forward, whose
+// longest workgroup has as many steps as each of the 512 places gets in all, took 313 us with the sequences one after
+// another.
+//
+// More sequences: sequence b's tiles start at unit start(b) / M + b, which leaves room for each of them (a range of n
+// rows spans at least ceil(n / M) of these numbers), so that no running total is needed; the lanes look at 64
+// sequences at a time.
 struct Unit {
   SeqRange s;
   int tile;  // tile of the sequence; may lie behind its end
@@ -237,22 +297,55 @@ struct Unit {
 __device__ inline int64_t start_of(const int32_t* cu, int64_t pitch, int64_t rows, int b) {
   return cu ? clamp64(cu[b], 0, rows) : b * pitch;
 }
-template <int M> __device__ inline Unit find_unit(const Attn& a, const int32_t* cu, int64_t pitch, int64_t rows, int64_t unit) {
+template <int M, bool ENDS>
+__device__ inline Unit find_unit(const Attn& a, const int32_t* cu, int64_t pitch, int64_t rows, int64_t unit) {
   const int lane = threadIdx.x % 64;
-  int lo = 0, cnt = a.seqs + 1;
-  while (cnt > 1) {
-    const int step = (cnt + 63) / 64, at = lane * step;
-    const bool ok = at < cnt && start_of(cu, pitch, rows, lo + at) / M + lo + at <= unit;
-    const uint64_t m = __ballot(ok);
-    const int n = m ? 63 - __builtin_clzll(m) : 0;
-    lo += n * step;
-    cnt = cnt - n * step < step ? cnt - n * step : step;
-  }
-  lo = uni(lo);
   Unit u;
-  const int64_t first = start_of(cu, pitch, rows, lo) / M + lo;
-  u.tile = uni((int)clamp64(unit - first, 0, 1 << 30));
-  const SeqRange s = seq_range(a, lo);
+  int seq;
+  if (a.seqs < 64) {
+    int64_t from = 0, to = 0;
+    if (lane <= a.seqs) {
+      from = start_of(cu, pitch, rows, lane);
+      to = lane == a.seqs ? rows : start_of(cu, pitch, rows, lane + 1);
+    }
+    const int T = to > from ? (int)((to - from + M - 1) / M) : 0;
+    auto at_level = [&](int l) {  // tiles that have at least l others on the counted side
+      int x = T > l ? T - l : 0;
+#pragma unroll
+      for (int o = 32; o >= 1; o >>= 1) x += __shfl_xor(x, o, 64);
+      return x;
+    };
+    int lo = 0, hi = T;  // the level is in [lo, hi)
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) {
+      const int x = __shfl_xor(hi, o, 64);
+      hi = hi > x ? hi : x;
+    }
+    while (hi - lo > 1) {
+      const int mid = lo + (hi - lo) / 2;
+      if (at_level(mid) > unit) lo = mid; else hi = mid;
+    }
+    int r = (int)clamp64(unit - at_level(lo + 1), 0, 1 << 30);
+    uint64_t m = __ballot(T > lo);
+    while (r > 0 && m) m &= m - 1, --r;
+    seq = m ? __builtin_ctzll(m) : a.seqs;
+    const int n = __shfl(T, seq, 64);
+    u.tile = m ? (ENDS ? lo : n - 1 - lo) : 1 << 30;  // (no m: a number beyond the last unit)
+  } else {
+    int lo = 0, cnt = a.seqs + 1;
+    while (cnt > 1) {
+      const int step = (cnt + 63) / 64, at = lane * step;
+      const bool ok = at < cnt && start_of(cu, pitch, rows, lo + at) / M + lo + at <= unit;
+      const uint64_t m = __ballot(ok);
+      const int n = m ? 63 - __builtin_clzll(m) : 0;
+      lo += n * step;
+      cnt = cnt - n * step < step ? cnt - n * step : step;
+    }
+    seq = lo;
+    u.tile = (int)clamp64(unit - (start_of(cu, pitch, rows, lo) / M + lo), 0, 1 << 30);
+  }
+  u.tile = uni(u.tile);
+  const SeqRange s = seq_range(a, uni(seq));
   u.s.q0 = uni64(s.q0), u.s.k0 = uni64(s.k0), u.s.kb = uni64(s.kb), u.s.vb = uni64(s.vb);
   u.s.n = uni(s.n), u.s.m = uni(s.m), u.s.cap = uni(s.cap);
   return u;
@@ -268,6 +361,8 @@ __device__ inline int seen_by(const Attn& a, const SeqRange& s, int64_t t) {
 template <int N = 0> __device__ inline void wait_and_sync() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
+
+__device__ inline void sync_lds() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
 template <typename T, int DH> constexpr int key_tile() { return sizeof(T) == 4 && DH > 64 ? 32 : 64; }
 
@@ -310,7 +405,7 @@ __device__ inline float finish_lse(float used, float sum, bool any) {
 // Forward: a workgroup has 128 rows of one sequence and head, a wave 32 of them; the keys stream through two LDS
 // stages of KT keys.
 template <typename T, int DH>
-__global__ __launch_bounds__(256, 2) void k_attn_fwd(Attn a, int64_t units, T* __restrict__ out,
+__global__ __launch_bounds__(256, 2) void k_attn_fwd(Attn a, T* __restrict__ out,
                                                      float* __restrict__ lse) {
   using Ti = Tile<T, DH>;
   constexpr int KT = key_tile<T, DH>(), NS = KT / 32;
@@ -319,7 +414,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(Attn a, int64_t units, T* _
   const uint32_t lds0 = uni((uint32_t)(size_t)(CUTBCE_LDS char*)lds);
   const int tid = threadIdx.x, wave = uni(tid / 64), lane = tid % 64;
   const int h = blockIdx.x % a.hq;
-  const Unit u = find_unit<kRows>(a, a.cu_q, a.q_pitch, a.q_rows, units - 1 - blockIdx.x / a.hq);
+  const Unit u = find_unit<kRows, true>(a, a.cu_q, a.q_pitch, a.q_rows, blockIdx.x / a.hq);
   const SeqRange& s = u.s;
   const int64_t r0 = (int64_t)u.tile * kRows;  // first row of the workgroup in its sequence
   if (r0 >= s.n) return;
@@ -385,7 +480,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(Attn a, int64_t units, T* _
 // dq, and the rows' (lse in base 2, delta) for dk and dv: the forward's layout and loop.
 template <typename T, int DH>
 __global__ __launch_bounds__(256, sizeof(T) == 4 && DH > 64 ? 1 : 2) void k_attn_dq(
-    Attn a, int64_t units, const T* __restrict__ dout, const T* __restrict__ out, const float* __restrict__ lse,
+    Attn a, const T* __restrict__ dout, const T* __restrict__ out, const float* __restrict__ lse,
     T* __restrict__ dq, float2* __restrict__ stat) {
   using Ti = Tile<T, DH>;
   constexpr int KT = key_tile<T, DH>(), NS = KT / 32;
@@ -394,7 +489,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 4 && DH > 64 ? 1 : 2) void k_attn
   const uint32_t lds0 = uni((uint32_t)(size_t)(CUTBCE_LDS char*)lds);
   const int tid = threadIdx.x, wave = uni(tid / 64), lane = tid % 64;
   const int h = blockIdx.x % a.hq;
-  const Unit u = find_unit<kRows>(a, a.cu_q, a.q_pitch, a.q_rows, units - 1 - blockIdx.x / a.hq);
+  const Unit u = find_unit<kRows, true>(a, a.cu_q, a.q_pitch, a.q_rows, blockIdx.x / a.hq);
   const SeqRange& s = u.s;
   const int64_t r0 = (int64_t)u.tile * kRows;
   if (r0 >= s.n) return;
@@ -466,14 +561,14 @@ __global__ __launch_bounds__(256, sizeof(T) == 4 && DH > 64 ? 1 : 2) void k_attn
 }
 
 // How the dk/dv kernel lays out a workgroup: 64 keys, two waves for each 32 of them and each of the RS row blocks of
-// a stage (32 RS rows of q and dO with their (lse, delta), three stages), and P in float32 from the first wave of a
-// pair to the second, twice.
+// a stage (32 RS rows of q and dO, and for each wave 32 rows' lse and delta; four stages), and P in float32 from the
+// first wave of a pair to the second.
 template <typename T, int DH> struct Dkv {
   static constexpr int kRS = sizeof(T) == 2 && DH > 64 ? 2 : 1;
-  static constexpr int kKeys = 64, kQT = 32 * kRS, kStages = 3, kPairs = 2 * kRS, kThreads = kPairs * 128;
-  using Ld = Dma<T, DH, kQT, kThreads>;
-  static constexpr int kStage = 2 * Ld::kBytes + kQT * 8;
-  static constexpr int kP = (kStages * kStage + 1023) / 1024 * 1024, kBytes = kP + kPairs * 2 * 4096;
+  static constexpr int kKeys = 64, kQT = 32 * kRS, kStages = 4, kPairs = 2 * kRS, kThreads = kPairs * 128;
+  using Ld = Dma<T, DH, kQT, kThreads, true>;
+  static constexpr int kStage = 2 * Ld::kBytes + kPairs * 512;
+  static constexpr int kP = kStages * kStage, kBytes = kP + kPairs * 4096;
   static_assert(kBytes <= 160 * 1024 && kPairs * Tile<T, DH>::kNDB * 4096 <= kBytes, "");
 };
 
@@ -482,7 +577,9 @@ template <typename T, int DH> struct Dkv {
 // head_dim 128, one wave per SIMD, and half of them in accumulation registers that vector instructions cannot reach:
 // 1.33 ms at 4 x 8192). So a pair of waves shares 32 keys: the first has k and dv (scores, P, P^T dO), the second v
 // and dk (dP, dS, dS^T Q) one tile behind, with P handed over in LDS. Two waves per SIMD, one of each kind, hide each
-// other's latencies.
+// other's latencies. There is room for one P of each pair beside four stages, so a turn has a second barrier, between
+// the products that both kinds of wave begin with and the writing of the next P. (P in float16 would fit twice, but
+// loses what is under 2^-38 of a row's sum.)
 template <typename T, int DH>
 __global__ __launch_bounds__((Dkv<T, DH>::kThreads), 2) void k_attn_dkv(Attn a, const T* __restrict__ dout,
                                                                         const float2* __restrict__ stat,
@@ -497,7 +594,7 @@ __global__ __launch_bounds__((Dkv<T, DH>::kThreads), 2) void k_attn_dkv(Attn a, 
   const int pair = wave % K::kPairs, kw = pair % 2, rw = pair / 2;  // which 32 keys, which rows of a stage
   const bool first = wave < K::kPairs;
   const int hk = blockIdx.x % a.hk;
-  const Unit u = find_unit<K::kKeys>(a, a.cu_k, a.k_pitch, a.k_rows, blockIdx.x / a.hk);
+  const Unit u = find_unit<K::kKeys, false>(a, a.cu_k, a.k_pitch, a.k_rows, blockIdx.x / a.hk);
   const SeqRange& s = u.s;
   const int64_t j0 = (int64_t)u.tile * K::kKeys;
   if (j0 >= s.cap) return;
@@ -515,38 +612,51 @@ __global__ __launch_bounds__((Dkv<T, DH>::kThreads), 2) void k_attn_dkv(Attn a, 
   Ld lq, lg;
   lq.init(tid, a.q_rs);
   lg.init(tid, (int64_t)a.hq * a.dh);
-  int fh = hk * a.group, ft = begin, fs = 0;  // head, tile and stage of the next fetch
+  constexpr int kLoads = 2 * Ld::kRounds + 1;  // of a wave and stage, where all waves load
+  // The last rows come first, the group's heads in turn for each tile: every key of a sequence sees the last rows, so
+  // the workgroups of a sequence read the same tiles at about the same time, through the L2 cache.
+  int fh = 0, ft = end - 1, fi = 0;  // head of the group, tile and index of the next fetch
+  // Beyond the last tile the fetches' ranges are empty: they load nothing, but count like the others.
   auto fetch = [&]() {
-    const int64_t t = (int64_t)ft * QT, rem = s.n - t;
-    const uint32_t stage = lds0 + (uint32_t)fs * K::kStage;
-    lq.load((const T*)a.q + (s.q0 + t) * a.q_rs + fh * a.q_hs, rem, a.q_rs, a.dh, stage + wave * 1024);
-    lg.load(dout + ((s.q0 + t) * a.hq + fh) * a.dh, rem, (int64_t)a.hq * a.dh, a.dh,
+    const bool in = fi < steps;
+    const int64_t t = (int64_t)ft * QT, rem = in ? s.n - t : 0;
+    const int head = in ? hk * a.group + fh : 0;
+    const uint32_t stage = lds0 + (uint32_t)(fi % K::kStages) * K::kStage;
+    lq.load((const T*)a.q + (s.q0 + t) * a.q_rs + head * a.q_hs, rem, a.q_rs, a.dh, stage + wave * 1024);
+    lg.load(dout + ((s.q0 + t) * a.hq + head) * a.dh, rem, (int64_t)a.hq * a.dh, a.dh,
             stage + Ld::kBytes + wave * 1024);
-    if (wave < K::kRS)
-      load_words(stat + (int64_t)fh * a.q_rows + s.q0 + t + wave * 32, (int)clamp64(rem - wave * 32, 0, 32) * 8,
-                 stage + 2 * Ld::kBytes + wave * 256, lane);
-    if (++ft == end) ft = begin, ++fh;
-    if (++fs == K::kStages) fs = 0;
+    load_pairs(stat + (int64_t)head * a.q_rows + s.q0 + t + rw * 32, rem - rw * 32,
+               stage + 2 * Ld::kBytes + wave * 256, lane);
+    ++fi;
+    if (++fh == a.group) fh = 0, --ft;
+  };
+  // At turn i the first waves are at tile i, the second at tile i - 1; tile i + 2 is fetched over tile i - 2.
+  auto sync_turn = [&]() {
+    wait_and_sync<Ld::kLanes == K::kThreads ? kLoads : 1>();  // (waves that load no rows wait for their pairs alone)
+    fetch();
   };
   f32x16 acc[Ti::kNDB] = {};
-  int ct = begin, cs = 0, before = 0;  // the first wave's tile and stage, the second's stage
-  const uint32_t px = lds0 + K::kP + pair * 8192 + lane * 16;
-  if (steps > 0) fetch();
-  for (int i = 0; i <= steps && steps > 0; ++i) {
-    wait_and_sync<>();
-    if (i + 1 < steps) fetch();
-    const uint32_t at = lds0 + (uint32_t)(first ? cs : before) * K::kStage + rw * 32 * Ti::kRowB;
-    const uint32_t sl = lds0 + (uint32_t)(first ? cs : before) * K::kStage + 2 * Ld::kBytes + rw * 256;
+  const uint32_t px = lds0 + K::kP + pair * 4096 + lane * 16;
+  const uint32_t rows = lds0 + rw * 32 * Ti::kRowB;
+  const uint32_t words = lds0 + 2 * Ld::kBytes + wave * 256 + half * 16;
+  if (steps > 0) {
+    fetch();
+    fetch();
     if (first) {
-      if (i < steps) {
+      int ch = 0, ct = end - 1;
+      for (int i = 0; i < steps; ++i) {
+        sync_turn();
+        const uint32_t stage = (uint32_t)(i % K::kStages) * K::kStage;
         const int t1 = ct * QT + rw * 32;
-        f32x16 x = product<T, DH>(at, 0, own, lane);
+        if (++ch == a.group) ch = 0, --ct;
+        f32x4 ld[4];
 #pragma unroll
-        for (int e = 0; e < 16; e += 2) {
-          const f32x4 ld = __builtin_bit_cast(f32x4, lds16(sl + acc_row(e, half) * 8));
-          x[e] = exp2_of(__builtin_fmaf(x[e], c, -ld[0]));
-          x[e + 1] = exp2_of(__builtin_fmaf(x[e + 1], c, -ld[2]));
-        }
+        for (int e = 0; e < 4; ++e) ld[e] = __builtin_bit_cast(f32x4, lds16(words + stage + e * 32));
+        typename Mma<T>::A ta[Mma<T>::kSlotsPerBlock * Ti::kNDB];
+        f32x16 x = product_ahead<T, DH>(rows + stage, own, rows + stage + Ld::kBytes, ta, lane);
+        sync_lds();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[e] = exp2_of(__builtin_fmaf(x[e], c, -ld[e / 4][e % 4]));
         if (t1 < wave_hi || t1 + 32 > s.n) {
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
@@ -556,30 +666,34 @@ __global__ __launch_bounds__((Dkv<T, DH>::kThreads), 2) void k_attn_dkv(Attn a, 
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          *(CUTBCE_LDS f32x4*)(size_t)(px + (i & 1) * 4096 + e * 1024) =
-              f32x4{x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]};
-        product_t<T, DH>(acc, Mma<T>::pack(x), at + Ld::kBytes, 0, lane);
+          *(CUTBCE_LDS f32x4*)(size_t)(px + e * 1024) = f32x4{x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]};
+        product_of<T, DH>(acc, Mma<T>::pack(x), ta);
       }
-    } else if (i > 0) {
-      f32x16 g = product<T, DH>(at + Ld::kBytes, 0, own, lane);
+      sync_turn();
+      sync_lds();
+    } else {
+      sync_turn();
+      sync_lds();
+      for (int i = 0; i < steps; ++i) {
+        sync_turn();
+        const uint32_t stage = (uint32_t)(i % K::kStages) * K::kStage;
+        f32x4 ld[4];
 #pragma unroll
-      for (int e = 0; e < 16; e += 4) {
-        const f32x4 p = __builtin_bit_cast(f32x4, lds16(px + ((i - 1) & 1) * 4096 + e * 256));
-        const f32x4 l0 = __builtin_bit_cast(f32x4, lds16(sl + acc_row(e, half) * 8));
-        const f32x4 l1 = __builtin_bit_cast(f32x4, lds16(sl + acc_row(e + 2, half) * 8));
-        g[e] = p[0] * (g[e] - l0[1]);
-        g[e + 1] = p[1] * (g[e + 1] - l0[3]);
-        g[e + 2] = p[2] * (g[e + 2] - l1[1]);
-        g[e + 3] = p[3] * (g[e + 3] - l1[3]);
+        for (int e = 0; e < 4; ++e) ld[e] = __builtin_bit_cast(f32x4, lds16(words + stage + 128 + e * 32));
+        f32x4 p[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) p[e] = __builtin_bit_cast(f32x4, lds16(px + e * 1024));
+        typename Mma<T>::A ta[Mma<T>::kSlotsPerBlock * Ti::kNDB];
+        f32x16 g = product_ahead<T, DH>(rows + stage + Ld::kBytes, own, rows + stage, ta, lane);
+        sync_lds();  // p has been read
+#pragma unroll
+        for (int e = 0; e < 16; ++e) g[e] = p[e / 4][e % 4] * (g[e] - ld[e / 4][e % 4]);
+        product_of<T, DH>(acc, Mma<T>::pack(g), ta);
       }
-      product_t<T, DH>(acc, Mma<T>::pack(g), at, 0, lane);
     }
-    if (++ct == end) ct = begin;
-    before = cs;
-    if (++cs == K::kStages) cs = 0;
+    wait_and_sync<>();  // no load may reach LDS after this
   }
   if constexpr (K::kRS > 1) {  // the second rows' sums to the first rows' waves, through LDS
-    wait_and_sync<>();
     const uint32_t at = lds0 + ((first ? 0 : 2) + kw) * (Ti::kNDB * 4096) + lane * 16;
 #pragma unroll
     for (int d = 0; d < Ti::kNDB; ++d)
@@ -806,7 +920,7 @@ template <typename T, int DH> hipError_t forward_t(const Attn& a, void* out, flo
   const int bytes = 4 * key_tile<T, DH>() * Ti::kRowB;
   const hipError_t e = allow_lds((const void*)k_attn_fwd<T, DH>, bytes);
   if (e != hipSuccess) return e;
-  k_attn_fwd<T, DH><<<dim3((unsigned)(units * a.hq)), dim3(256), bytes, st>>>(a, units, (T*)out, lse);
+  k_attn_fwd<T, DH><<<dim3((unsigned)(units * a.hq)), dim3(256), bytes, st>>>(a, (T*)out, lse);
   return hipGetLastError();
 }
 
@@ -820,8 +934,8 @@ hipError_t backward_t(const Attn& a, const void* dout, const void* out, const fl
     const int bytes = 4 * key_tile<T, DH>() * Ti::kRowB;
     const hipError_t e = allow_lds((const void*)k_attn_dq<T, DH>, bytes);
     if (e != hipSuccess) return e;
-    k_attn_dq<T, DH><<<dim3((unsigned)(units * a.hq)), dim3(256), bytes, st>>>(a, units, (const T*)dout, (const T*)out,
-                                                                               lse, (T*)dq, stat);
+    k_attn_dq<T, DH><<<dim3((unsigned)(units * a.hq)), dim3(256), bytes, st>>>(a, (const T*)dout, (const T*)out, lse,
+                                                                              (T*)dq, stat);
   }
   if (a.k_rows) {
     using K = Dkv<T, DH>;
