@@ -220,10 +220,11 @@ __device__ inline f32x16 product(uint32_t at, int r0, const u32x4* own, int lane
 }
 
 // The same, and the operands of a transposed product of the tile at `at2` (product_of). In 16-bit elements the order is
-// pinned: all of the first product's operands are read before its first matrix instruction, the second's between
-// them. (Left alone, the compiler reads each operand right before its use and waits for it.)
-template <typename T, int DH>
-__device__ inline f32x16 product_ahead(uint32_t at, const u32x4* own, uint32_t at2, typename Mma<T>::A* a2, int lane) {
+// pinned: all of the first product's operands are read before its first matrix instruction (and meanwhile() runs while
+// they come), the second's between them. (Left alone, the compiler reads each operand right before its use and waits for it.)
+template <typename T, int DH, typename F>
+__device__ inline f32x16 product_ahead(uint32_t at, const u32x4* own, uint32_t at2, typename Mma<T>::A* a2, int lane,
+                                       F meanwhile) {
   using Ti = Tile<T, DH>;
   constexpr int S = Mma<T>::kSlotsPerBlock * Ti::kNDB, NT = Ti::kNT;
   u32x4 x[NT];
@@ -231,6 +232,7 @@ __device__ inline f32x16 product_ahead(uint32_t at, const u32x4* own, uint32_t a
 #pragma unroll
   for (int t = 0; t < NT; ++t) x[t] = tile_chunk<T, DH>(at, t, lane);
   if constexpr (sizeof(T) == 2) __builtin_amdgcn_sched_barrier(0);
+  meanwhile();
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     s = Mma<T>::mma(x[t], own[t], s);
@@ -361,8 +363,6 @@ __device__ inline int seen_by(const Attn& a, const SeqRange& s, int64_t t) {
 template <int N = 0> __device__ inline void wait_and_sync() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
-
-__device__ inline void sync_lds() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
 template <typename T, int DH> constexpr int key_tile() { return sizeof(T) == 4 && DH > 64 ? 32 : 64; }
 
@@ -561,25 +561,63 @@ __global__ __launch_bounds__(256, sizeof(T) == 4 && DH > 64 ? 1 : 2) void k_attn
 }
 
 // How the dk/dv kernel lays out a workgroup: 64 keys, two waves for each 32 of them and each of the RS row blocks of
-// a stage (32 RS rows of q and dO, and for each wave 32 rows' lse and delta; four stages), and P in float32 from the
-// first wave of a pair to the second.
+// a stage (32 RS rows of q and dO with their lse and delta; four stages), and P from the first wave of a pair to the
+// second, twice.
 template <typename T, int DH> struct Dkv {
   static constexpr int kRS = sizeof(T) == 2 && DH > 64 ? 2 : 1;
   static constexpr int kKeys = 64, kQT = 32 * kRS, kStages = 4, kPairs = 2 * kRS, kThreads = kPairs * 128;
   using Ld = Dma<T, DH, kQT, kThreads, true>;
-  static constexpr int kStage = 2 * Ld::kBytes + kPairs * 512;
-  static constexpr int kP = kStages * kStage, kBytes = kP + kPairs * 4096;
+  static constexpr int kStage = 2 * Ld::kBytes + kRS * 256;
+  static constexpr bool kPack = kRS > 1;  // P as the upper 24 bits of its float32
+  static constexpr int kPB = kPack ? 3072 : 4096;
+  static constexpr int kP = kStages * kStage, kBytes = kP + kPairs * 2 * kPB;
   static_assert(kBytes <= 160 * 1024 && kPairs * Tile<T, DH>::kNDB * 4096 <= kBytes, "");
 };
+
+// P of a wave's tile to LDS and back: 16 values a lane, whole or (PACK) the upper 24 bits of each, four in three words.
+template <bool PACK> __device__ inline void put_p(uint32_t at, const f32x16& x) {
+  if constexpr (PACK) {
+    uint32_t w[12];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t a = __float_as_uint(x[4 * e]), b = __float_as_uint(x[4 * e + 1]);
+      const uint32_t c = __float_as_uint(x[4 * e + 2]), d = __float_as_uint(x[4 * e + 3]);
+      w[3 * e] = __builtin_amdgcn_perm(b, a, 0x05030201);      // a1 a2 a3 b1
+      w[3 * e + 1] = __builtin_amdgcn_perm(c, b, 0x06050302);  // b2 b3 c1 c2
+      w[3 * e + 2] = __builtin_amdgcn_perm(d, c, 0x07060503);  // c3 d1 d2 d3
+    }
+#pragma unroll
+    for (int e = 0; e < 3; ++e)
+      *(CUTBCE_LDS u32x4*)(size_t)(at + e * 1024) = u32x4{w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]};
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      *(CUTBCE_LDS f32x4*)(size_t)(at + e * 1024) = f32x4{x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]};
+  }
+}
+template <bool PACK> __device__ inline float get_p(const u32x4* p, int e) {
+  if constexpr (PACK) {
+    const int k = e / 4 * 3;
+    const uint32_t a = p[k / 4][k % 4], b = p[(k + 1) / 4][(k + 1) % 4], c = p[(k + 2) / 4][(k + 2) % 4];
+    switch (e % 4) {
+      case 0: return __uint_as_float(a << 8);
+      case 1: return __uint_as_float(__builtin_amdgcn_perm(b, a, 0x0504030c));  // 0 a3 b0 b1
+      case 2: return __uint_as_float(__builtin_amdgcn_perm(c, b, 0x0403020c));  // 0 b2 b3 c0
+      default: return __uint_as_float(c & 0xffffff00u);
+    }
+  } else {
+    return __uint_as_float(p[e / 4][e % 4]);
+  }
+}
 
 // dk and dv: a workgroup has 64 keys of one sequence and key/value head; the rows of the group's heads stream through
 // LDS. One wave would need the sums of dk and dv, k and v of its keys and two score tiles (over 256 registers at
 // head_dim 128, one wave per SIMD, and half of them in accumulation registers that vector instructions cannot reach:
 // 1.33 ms at 4 x 8192). So a pair of waves shares 32 keys: the first has k and dv (scores, P, P^T dO), the second v
 // and dk (dP, dS, dS^T Q) one tile behind, with P handed over in LDS. Two waves per SIMD, one of each kind, hide each
-// other's latencies. There is room for one P of each pair beside four stages, so a turn has a second barrier, between
-// the products that both kinds of wave begin with and the writing of the next P. (P in float16 would fit twice, but
-// loses what is under 2^-38 of a row's sum.)
+// other's latencies. Where four stages leave too little room for two P's of each pair in float32, its upper 24 bits
+// are handed over: an error of 2^-16, under a hundredth of dS's rounding to bf16. (One P, with a second barrier before
+// it is overwritten, was slower; float16 loses what is under 2^-38 of a row's sum.)
 template <typename T, int DH>
 __global__ __launch_bounds__((Dkv<T, DH>::kThreads), 2) void k_attn_dkv(Attn a, const T* __restrict__ dout,
                                                                         const float2* __restrict__ stat,
@@ -612,7 +650,6 @@ __global__ __launch_bounds__((Dkv<T, DH>::kThreads), 2) void k_attn_dkv(Attn a, 
   Ld lq, lg;
   lq.init(tid, a.q_rs);
   lg.init(tid, (int64_t)a.hq * a.dh);
-  constexpr int kLoads = 2 * Ld::kRounds + 1;  // of a wave and stage, where all waves load
   // The last rows come first, the group's heads in turn for each tile: every key of a sequence sees the last rows, so
   // the workgroups of a sequence read the same tiles at about the same time, through the L2 cache.
   int fh = 0, ft = end - 1, fi = 0;  // head of the group, tile and index of the next fetch
@@ -625,20 +662,25 @@ __global__ __launch_bounds__((Dkv<T, DH>::kThreads), 2) void k_attn_dkv(Attn a, 
     lq.load((const T*)a.q + (s.q0 + t) * a.q_rs + head * a.q_hs, rem, a.q_rs, a.dh, stage + wave * 1024);
     lg.load(dout + ((s.q0 + t) * a.hq + head) * a.dh, rem, (int64_t)a.hq * a.dh, a.dh,
             stage + Ld::kBytes + wave * 1024);
-    load_pairs(stat + (int64_t)head * a.q_rows + s.q0 + t + rw * 32, rem - rw * 32,
-               stage + 2 * Ld::kBytes + wave * 256, lane);
+    if (wave < K::kRS)
+      load_pairs(stat + (int64_t)head * a.q_rows + s.q0 + t + wave * 32, rem - wave * 32,
+                 stage + 2 * Ld::kBytes + wave * 256, lane);
     ++fi;
     if (++fh == a.group) fh = 0, --ft;
   };
   // At turn i the first waves are at tile i, the second at tile i - 1; tile i + 2 is fetched over tile i - 2.
   auto sync_turn = [&]() {
-    wait_and_sync<Ld::kLanes == K::kThreads ? kLoads : 1>();  // (waves that load no rows wait for their pairs alone)
-    fetch();
+    if (Ld::kLanes == K::kThreads) {
+      if (wave < K::kRS) wait_and_sync<2 * Ld::kRounds + 1>();  // these load the pairs too
+      else wait_and_sync<2 * Ld::kRounds>();
+    } else {
+      wait_and_sync<0>();
+    }
   };
   f32x16 acc[Ti::kNDB] = {};
-  const uint32_t px = lds0 + K::kP + pair * 4096 + lane * 16;
+  const uint32_t px = lds0 + K::kP + pair * 2 * K::kPB + lane * 16;
   const uint32_t rows = lds0 + rw * 32 * Ti::kRowB;
-  const uint32_t words = lds0 + 2 * Ld::kBytes + wave * 256 + half * 16;
+  const uint32_t words = lds0 + 2 * Ld::kBytes + rw * 256 + half * 16;
   if (steps > 0) {
     fetch();
     fetch();
@@ -653,8 +695,7 @@ __global__ __launch_bounds__((Dkv<T, DH>::kThreads), 2) void k_attn_dkv(Attn a, 
 #pragma unroll
         for (int e = 0; e < 4; ++e) ld[e] = __builtin_bit_cast(f32x4, lds16(words + stage + e * 32));
         typename Mma<T>::A ta[Mma<T>::kSlotsPerBlock * Ti::kNDB];
-        f32x16 x = product_ahead<T, DH>(rows + stage, own, rows + stage + Ld::kBytes, ta, lane);
-        sync_lds();
+        f32x16 x = product_ahead<T, DH>(rows + stage, own, rows + stage + Ld::kBytes, ta, lane, fetch);
 #pragma unroll
         for (int e = 0; e < 16; ++e) x[e] = exp2_of(__builtin_fmaf(x[e], c, -ld[e / 4][e % 4]));
         if (t1 < wave_hi || t1 + 32 > s.n) {
@@ -664,30 +705,26 @@ __global__ __launch_bounds__((Dkv<T, DH>::kThreads), 2) void k_attn_dkv(Attn a, 
             if (t < mine || t >= s.n) x[e] = 0.f;
           }
         }
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          *(CUTBCE_LDS f32x4*)(size_t)(px + e * 1024) = f32x4{x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]};
+        put_p<K::kPack>(px + (i & 1) * K::kPB, x);
         product_of<T, DH>(acc, Mma<T>::pack(x), ta);
       }
       sync_turn();
-      sync_lds();
     } else {
       sync_turn();
-      sync_lds();
+      fetch();
       for (int i = 0; i < steps; ++i) {
         sync_turn();
         const uint32_t stage = (uint32_t)(i % K::kStages) * K::kStage;
         f32x4 ld[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) ld[e] = __builtin_bit_cast(f32x4, lds16(words + stage + 128 + e * 32));
-        f32x4 p[4];
+        u32x4 p[K::kPB / 1024];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) p[e] = __builtin_bit_cast(f32x4, lds16(px + e * 1024));
+        for (int e = 0; e < K::kPB / 1024; ++e) p[e] = lds16(px + (i & 1) * K::kPB + e * 1024);
         typename Mma<T>::A ta[Mma<T>::kSlotsPerBlock * Ti::kNDB];
-        f32x16 g = product_ahead<T, DH>(rows + stage + Ld::kBytes, own, rows + stage, ta, lane);
-        sync_lds();  // p has been read
+        f32x16 g = product_ahead<T, DH>(rows + stage + Ld::kBytes, own, rows + stage, ta, lane, fetch);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) g[e] = p[e / 4][e % 4] * (g[e] - ld[e / 4][e % 4]);
+        for (int e = 0; e < 16; ++e) g[e] = get_p<K::kPack>(p, e) * (g[e] - ld[e / 4][e % 4]);
         product_of<T, DH>(acc, Mma<T>::pack(g), ta);
       }
     }
