@@ -85,7 +85,7 @@ __device__ inline void load_lds4(u32x4 buffer, int voff, uint32_t dst) {
 }
 
 // One workgroup's (or wave's) loads of NR rows into LDS: NL lanes, 16 bytes each per instruction.
-template <typename T, int DH, int NR, int NL, bool RAW = false> struct Dma {
+template <typename T, int DH, int NR, int NL> struct Dma {
   using Ti = Tile<T, DH>;
   static constexpr int kChunks = NR * Ti::kCPR, kLanes = kChunks < NL ? kChunks : NL;  // whole waves load
   static constexpr int kRounds = kChunks / kLanes, kStep = kLanes / Ti::kCPR;            // rows per round
@@ -105,24 +105,27 @@ template <typename T, int DH, int NR, int NL, bool RAW = false> struct Dma {
     const int c = (chunk ^ Ti::swz(q * kStep)) * 16;
     return c < dh * Ti::kEsz ? row + c + q * step : (int)0x80000000u;
   }
+  // the range of rows [0, rem) of `base`, and one round of its loads (for kernels that spread them)
+  __device__ inline u32x4 range(const T* base, int64_t rem, int64_t stride, int dh) const {
+    const int rows = (int)clamp64(rem, 0, NR);
+    return buffer_of(base, rows > 0 ? (int)((rows - 1) * stride + dh) * Ti::kEsz : 0);
+  }
+  __device__ inline void round(int q, u32x4 range, int dh, uint32_t dst) const {
+    if (kLanes < NL && !on) return;
+    load_lds16(range, offset(q, dh), dst + q * kLanes * 16);
+  }
   // rows [0, rem) of `base` (uniform; rem may be <= 0 or > NR) to LDS byte `dst` (uniform: the wave's first kilobyte)
   __device__ inline void load(const T* base, int64_t rem, int64_t stride, int dh, uint32_t dst) const {
     if (kLanes < NL && !on) return;
     const int rows = (int)clamp64(rem, 0, NR);
     const int bytes = rows > 0 ? (int)((rows - 1) * stride + dh) * Ti::kEsz : 0;
-    if constexpr (RAW) {
-      const u32x4 r = buffer_of(base, bytes);
-#pragma unroll
-      for (int q = 0; q < kRounds; ++q) load_lds16(r, offset(q, dh), dst + q * kLanes * 16);
-    } else {
 #if defined(__HIP_DEVICE_COMPILE__)  // (the host pass silently drops kernels that reach these builtins this way)
-      const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)base, (short)0, bytes, 0x00020000);
+    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)base, (short)0, bytes, 0x00020000);
 #pragma unroll
-      for (int q = 0; q < kRounds; ++q)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (CUTBCE_LDS void*)(size_t)(dst + q * kLanes * 16), 16,
-                                                 offset(q, dh), 0, 0, 0);
+    for (int q = 0; q < kRounds; ++q)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (CUTBCE_LDS void*)(size_t)(dst + q * kLanes * 16), 16, offset(q, dh),
+                                               0, 0, 0);
 #endif
-    }
   }
 };
 
@@ -219,35 +222,46 @@ __device__ inline f32x16 product(uint32_t at, int r0, const u32x4* own, int lane
   return s;
 }
 
-// The same, and the operands of a transposed product of the tile at `at2` (product_of). In 16-bit elements the order is
-// pinned: all of the first product's operands are read before its first matrix instruction (and meanwhile() runs while
-// they come), the second's between them. (Left alone, the compiler reads each operand right before its use and waits for it.)
-template <typename T, int DH, typename F>
-__device__ inline f32x16 product_ahead(uint32_t at, const u32x4* own, uint32_t at2, typename Mma<T>::A* a2, int lane,
-                                       F meanwhile) {
-  using Ti = Tile<T, DH>;
-  constexpr int S = Mma<T>::kSlotsPerBlock * Ti::kNDB, NT = Ti::kNT;
-  u32x4 x[NT];
-  f32x16 s = {};
-#pragma unroll
-  for (int t = 0; t < NT; ++t) x[t] = tile_chunk<T, DH>(at, t, lane);
+// Products with their order pinned in 16-bit elements, for kernels whose waves run in step: a product's matrix
+// instructions are interleaved with the LDS reads of the operands that come after it. (Left alone, the compiler reads
+// each operand right before its use and waits for it.)
+template <typename T> __device__ inline void pin() {
   if constexpr (sizeof(T) == 2) __builtin_amdgcn_sched_barrier(0);
-  meanwhile();
+}
+template <typename T, int DH> struct Ahead {
+  static constexpr int NT = Tile<T, DH>::kNT, NDB = Tile<T, DH>::kNDB, S = Mma<T>::kSlotsPerBlock * NDB;
+  u32x4 x[NT];                // the tile's rows
+  typename Mma<T>::A t[S];    // the other tile's transpose
+  __device__ inline void read(uint32_t at, int lane) {
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    s = Mma<T>::mma(x[t], own[t], s);
-#pragma unroll
-    for (int k = S * t / NT; k < S * (t + 1) / NT; ++k) a2[k] = Mma<T>::template load_t<DH>(k, at2, 0, lane);
-    if constexpr (sizeof(T) == 2) __builtin_amdgcn_sched_barrier(0);
+    for (int k = 0; k < NT; ++k) x[k] = tile_chunk<T, DH>(at, k, lane);
   }
-  return s;
-}
-template <typename T, int DH>
-__device__ inline void product_of(f32x16* acc, const typename Mma<T>::P& p, const typename Mma<T>::A* a) {
-  constexpr int NDB = Tile<T, DH>::kNDB;
+  // x times the own operand, while the transposed operands are read from `at` and piece(0 .. pieces - 1) runs
+  template <typename F>
+  __device__ inline f32x16 product(const u32x4* own, uint32_t at, int lane, F piece, int pieces) {
+    f32x16 s = {};
 #pragma unroll
-  for (int k = 0; k < Mma<T>::kSlotsPerBlock * NDB; ++k) Mma<T>::template slot_t<NDB>(acc, k, a[k], p);
-}
+    for (int k = 0; k < NT; ++k) {
+      s = Mma<T>::mma(x[k], own[k], s);
+#pragma unroll
+      for (int e = S * k / NT; e < S * (k + 1) / NT; ++e) t[e] = Mma<T>::template load_t<DH>(e, at, 0, lane);
+#pragma unroll
+      for (int e = pieces * k / NT; e < pieces * (k + 1) / NT; ++e) piece(e);
+      pin<T>();
+    }
+    return s;
+  }
+  // acc += t p, while the next tile's rows are read from `at`
+  __device__ inline void product_t(f32x16* acc, const typename Mma<T>::P& p, uint32_t at, int lane) {
+#pragma unroll
+    for (int e = 0; e < S; ++e) {
+      Mma<T>::template slot_t<NDB>(acc, e, t[e], p);
+#pragma unroll
+      for (int k = NT * e / S; k < NT * (e + 1) / S; ++k) x[k] = tile_chunk<T, DH>(at, k, lane);
+      pin<T>();
+    }
+  }
+};
 
 // The own operand: lane l has the chunks 2t + l / 32 of one row (zeros past head_dim, or where !live).
 template <typename T, int DH> __device__ inline void load_own(u32x4* own, const T* row, bool live, int dh, int lane) {
@@ -566,7 +580,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 4 && DH > 64 ? 1 : 2) void k_attn
 template <typename T, int DH> struct Dkv {
   static constexpr int kRS = sizeof(T) == 2 && DH > 64 ? 2 : 1;
   static constexpr int kKeys = 64, kQT = 32 * kRS, kStages = 4, kPairs = 2 * kRS, kThreads = kPairs * 128;
-  using Ld = Dma<T, DH, kQT, kThreads, true>;
+  using Ld = Dma<T, DH, kQT, kThreads>;
   static constexpr int kStage = 2 * Ld::kBytes + kRS * 256;
   static constexpr bool kPack = kRS > 1;  // P as the upper 24 bits of its float32
   static constexpr int kPB = kPack ? 3072 : 4096;
@@ -652,50 +666,64 @@ __global__ __launch_bounds__((Dkv<T, DH>::kThreads), 2) void k_attn_dkv(Attn a, 
   lg.init(tid, (int64_t)a.hq * a.dh);
   // The last rows come first, the group's heads in turn for each tile: every key of a sequence sees the last rows, so
   // the workgroups of a sequence read the same tiles at about the same time, through the L2 cache.
-  int fh = 0, ft = end - 1, fi = 0;  // head of the group, tile and index of the next fetch
-  // Beyond the last tile the fetches' ranges are empty: they load nothing, but count like the others.
-  auto fetch = [&]() {
+  // Workgroups begin with different heads: the rows of one head lie a power of two apart as often as not, and would
+  // all come from a few channels of the cache.
+  const int turn = (int)(blockIdx.x / a.hk / 4 % a.group);
+  int fh = 0, ft = end - 1, fi = 0;  // head (from `turn` on), tile and index of the next fetch
+  // A fetch in pieces: one load each, to be spread over a turn (together at its beginning they held up the products
+  // behind them). Beyond the last tile the range is empty: zeros are loaded.
+  constexpr int kPieces = 2 * Ld::kRounds + 1;
+  u32x4 rq = {}, rg = {};
+  int64_t st_row = 0, st_rem = 0;
+  uint32_t st_at = 0;
+  auto prepare = [&]() {
     const bool in = fi < steps;
     const int64_t t = (int64_t)ft * QT, rem = in ? s.n - t : 0;
-    const int head = in ? hk * a.group + fh : 0;
-    const uint32_t stage = lds0 + (uint32_t)(fi % K::kStages) * K::kStage;
-    lq.load((const T*)a.q + (s.q0 + t) * a.q_rs + head * a.q_hs, rem, a.q_rs, a.dh, stage + wave * 1024);
-    lg.load(dout + ((s.q0 + t) * a.hq + head) * a.dh, rem, (int64_t)a.hq * a.dh, a.dh,
-            stage + Ld::kBytes + wave * 1024);
-    if (wave < K::kRS)
-      load_pairs(stat + (int64_t)head * a.q_rows + s.q0 + t + wave * 32, rem - wave * 32,
-                 stage + 2 * Ld::kBytes + wave * 256, lane);
+    const int head = in ? hk * a.group + (fh + turn < a.group ? fh + turn : fh + turn - a.group) : 0;
+    rq = lq.range((const T*)a.q + (s.q0 + t) * a.q_rs + head * a.q_hs, rem, a.q_rs, a.dh);
+    rg = lg.range(dout + ((s.q0 + t) * a.hq + head) * a.dh, rem, (int64_t)a.hq * a.dh, a.dh);
+    st_row = (int64_t)head * a.q_rows + s.q0 + t + wave * 32;
+    st_rem = rem - wave * 32;
+    st_at = lds0 + (uint32_t)(fi % K::kStages) * K::kStage;
     ++fi;
     if (++fh == a.group) fh = 0, --ft;
   };
-  // At turn i the first waves are at tile i, the second at tile i - 1; tile i + 2 is fetched over tile i - 2.
-  auto sync_turn = [&]() {
-    if (Ld::kLanes == K::kThreads) {
-      if (wave < K::kRS) wait_and_sync<2 * Ld::kRounds + 1>();  // these load the pairs too
-      else wait_and_sync<2 * Ld::kRounds>();
-    } else {
-      wait_and_sync<0>();
-    }
+  auto piece = [&](int k) {
+    if (k < Ld::kRounds) lq.round(k, rq, a.dh, st_at + wave * 1024);
+    else if (k < 2 * Ld::kRounds) lg.round(k - Ld::kRounds, rg, a.dh, st_at + Ld::kBytes + wave * 1024);
+    else if (k == 2 * Ld::kRounds && wave < K::kRS)
+      load_pairs(stat + st_row, st_rem, st_at + 2 * Ld::kBytes + wave * 256, lane);
   };
+  auto fetch = [&]() {
+    prepare();
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) piece(k);
+  };
+  // At turn i the first waves are at tile i and read the rows of tile i + 1 ahead, the second are one tile behind;
+  // tile i + 2 is fetched over tile i - 2.
   f32x16 acc[Ti::kNDB] = {};
   const uint32_t px = lds0 + K::kP + pair * 2 * K::kPB + lane * 16;
   const uint32_t rows = lds0 + rw * 32 * Ti::kRowB;
   const uint32_t words = lds0 + 2 * Ld::kBytes + rw * 256 + half * 16;
+  auto stage = [](int i) { return (uint32_t)(i % K::kStages) * K::kStage; };
   if (steps > 0) {
+    Ahead<T, DH> op;
     fetch();
     fetch();
+    wait_and_sync<>();
     if (first) {
+      op.read(rows, lane);
       int ch = 0, ct = end - 1;
       for (int i = 0; i < steps; ++i) {
-        sync_turn();
-        const uint32_t stage = (uint32_t)(i % K::kStages) * K::kStage;
+        wait_and_sync<>();
+        prepare();
+        const uint32_t at = stage(i);
         const int t1 = ct * QT + rw * 32;
         if (++ch == a.group) ch = 0, --ct;
         f32x4 ld[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) ld[e] = __builtin_bit_cast(f32x4, lds16(words + stage + e * 32));
-        typename Mma<T>::A ta[Mma<T>::kSlotsPerBlock * Ti::kNDB];
-        f32x16 x = product_ahead<T, DH>(rows + stage, own, rows + stage + Ld::kBytes, ta, lane, fetch);
+        for (int e = 0; e < 4; ++e) ld[e] = __builtin_bit_cast(f32x4, lds16(words + at + e * 32));
+        f32x16 x = op.product(own, rows + at + Ld::kBytes, lane, piece, kPieces);
 #pragma unroll
         for (int e = 0; e < 16; ++e) x[e] = exp2_of(__builtin_fmaf(x[e], c, -ld[e / 4][e % 4]));
         if (t1 < wave_hi || t1 + 32 > s.n) {
@@ -706,26 +734,27 @@ __global__ __launch_bounds__((Dkv<T, DH>::kThreads), 2) void k_attn_dkv(Attn a, 
           }
         }
         put_p<K::kPack>(px + (i & 1) * K::kPB, x);
-        product_of<T, DH>(acc, Mma<T>::pack(x), ta);
+        op.product_t(acc, Mma<T>::pack(x), rows + stage(i + 1), lane);
       }
-      sync_turn();
+      wait_and_sync<>();
     } else {
-      sync_turn();
+      wait_and_sync<>();
       fetch();
+      op.read(rows + Ld::kBytes, lane);
       for (int i = 0; i < steps; ++i) {
-        sync_turn();
-        const uint32_t stage = (uint32_t)(i % K::kStages) * K::kStage;
+        wait_and_sync<>();
+        prepare();
+        const uint32_t at = stage(i);
         f32x4 ld[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) ld[e] = __builtin_bit_cast(f32x4, lds16(words + stage + 128 + e * 32));
+        for (int e = 0; e < 4; ++e) ld[e] = __builtin_bit_cast(f32x4, lds16(words + at + 128 + e * 32));
         u32x4 p[K::kPB / 1024];
 #pragma unroll
         for (int e = 0; e < K::kPB / 1024; ++e) p[e] = lds16(px + (i & 1) * K::kPB + e * 1024);
-        typename Mma<T>::A ta[Mma<T>::kSlotsPerBlock * Ti::kNDB];
-        f32x16 g = product_ahead<T, DH>(rows + stage + Ld::kBytes, own, rows + stage, ta, lane, fetch);
+        f32x16 g = op.product(own, rows + at, lane, piece, kPieces);
 #pragma unroll
         for (int e = 0; e < 16; ++e) g[e] = get_p<K::kPack>(p, e) * (g[e] - ld[e / 4][e % 4]);
-        product_of<T, DH>(acc, Mma<T>::pack(g), ta);
+        op.product_t(acc, Mma<T>::pack(g), rows + stage(i + 1) + Ld::kBytes, lane);
       }
     }
     wait_and_sync<>();  // no load may reach LDS after this
