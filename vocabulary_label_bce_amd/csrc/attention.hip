@@ -228,36 +228,38 @@ __device__ inline f32x16 product(uint32_t at, int r0, const u32x4* own, int lane
 template <typename T> __device__ inline void pin() {
   if constexpr (sizeof(T) == 2) __builtin_amdgcn_sched_barrier(0);
 }
+// f(e) for slot k's share of n things in `slots` slots
+template <typename F> __device__ inline void spread(int k, int slots, int n, F f) {
+#pragma unroll
+  for (int e = n * k / slots; e < n * (k + 1) / slots; ++e) f(e);
+}
 template <typename T, int DH> struct Ahead {
   static constexpr int NT = Tile<T, DH>::kNT, NDB = Tile<T, DH>::kNDB, S = Mma<T>::kSlotsPerBlock * NDB;
-  u32x4 x[NT];                // the tile's rows
-  typename Mma<T>::A t[S];    // the other tile's transpose
-  __device__ inline void read(uint32_t at, int lane) {
+  u32x4 x[NT];              // 32 rows of a tile
+  typename Mma<T>::A t[S];  // 32 rows of a tile, transposed
+  __device__ inline void row(int k, uint32_t at, int lane) { x[k] = tile_chunk<T, DH>(at, k, lane); }
+  __device__ inline void col(int e, uint32_t at, int lane) { t[e] = Mma<T>::template load_t<DH>(e, at, 0, lane); }
+  __device__ inline void rows(uint32_t at, int lane) {
 #pragma unroll
-    for (int k = 0; k < NT; ++k) x[k] = tile_chunk<T, DH>(at, k, lane);
+    for (int k = 0; k < NT; ++k) row(k, at, lane);
   }
-  // x times the own operand, while the transposed operands are read from `at` and piece(0 .. pieces - 1) runs
-  template <typename F>
-  __device__ inline f32x16 product(const u32x4* own, uint32_t at, int lane, F piece, int pieces) {
+  // x times the own operand; work(k) after the k-th of NT steps, when x[k] is free
+  template <typename F> __device__ inline f32x16 product(const u32x4* own, F work) {
     f32x16 s = {};
 #pragma unroll
     for (int k = 0; k < NT; ++k) {
       s = Mma<T>::mma(x[k], own[k], s);
-#pragma unroll
-      for (int e = S * k / NT; e < S * (k + 1) / NT; ++e) t[e] = Mma<T>::template load_t<DH>(e, at, 0, lane);
-#pragma unroll
-      for (int e = pieces * k / NT; e < pieces * (k + 1) / NT; ++e) piece(e);
+      work(k);
       pin<T>();
     }
     return s;
   }
-  // acc += t p, while the next tile's rows are read from `at`
-  __device__ inline void product_t(f32x16* acc, const typename Mma<T>::P& p, uint32_t at, int lane) {
+  // acc += t p; work(e) after the e-th of S steps, when t[e] is free
+  template <typename F> __device__ inline void product_t(f32x16* acc, const typename Mma<T>::P& p, F work) {
 #pragma unroll
     for (int e = 0; e < S; ++e) {
       Mma<T>::template slot_t<NDB>(acc, e, t[e], p);
-#pragma unroll
-      for (int k = NT * e / S; k < NT * (e + 1) / S; ++k) x[k] = tile_chunk<T, DH>(at, k, lane);
+      work(e);
       pin<T>();
     }
   }
@@ -453,36 +455,63 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(Attn a, T* __restrict__ out
   lk.init(tid, a.k_rs);
   lv.init(tid, a.v_rs);
   const uint32_t dst = lds0 + wave * 1024;
-  auto fetch = [&](int i) {
+  u32x4 rk = {}, rv = {};
+  uint32_t to = 0;
+  auto prepare = [&](int i) {  // (beyond the last key the range is empty: zeros are loaded)
     const int64_t j = (int64_t)i * KT;
-    const uint32_t at = dst + (i & 1) * 2 * Ld::kBytes;
-    lk.load(k + j * a.k_rs, s.m - j, a.k_rs, a.dh, at);
-    lv.load(v + j * a.v_rs, s.m - j, a.v_rs, a.dh, at + Ld::kBytes);
+    rk = lk.range(k + j * a.k_rs, s.m - j, a.k_rs, a.dh);
+    rv = lv.range(v + j * a.v_rs, s.m - j, a.v_rs, a.dh);
+    to = dst + (i & 1) * 2 * Ld::kBytes;
   };
+  auto piece = [&](int q) {
+    if (q < Ld::kRounds) lk.round(q, rk, a.dh, to);
+    else lv.round(q - Ld::kRounds, rv, a.dh, to + Ld::kBytes);
+  };
+  constexpr int kPieces = 2 * Ld::kRounds;
+  auto fetch = [&](int i) {
+    prepare(i);
+#pragma unroll
+    for (int q = 0; q < kPieces; ++q) piece(q);
+  };
+  using Op = Ahead<T, DH>;
   f32x16 o[Ti::kNDB] = {};
   Online st;
   if (steps > 0) fetch(0);
   for (int i = 0; i < steps; ++i) {
     wait_and_sync<>();
-    if (i + 1 < steps) fetch(i + 1);
     const int j0 = i * KT;
-    if (j0 < wave_hi) {
-      const uint32_t kt = lds0 + (i & 1) * 2 * Ld::kBytes, vt = kt + Ld::kBytes;
-      f32x16 x[NS];
-#pragma unroll
-      for (int b = 0; b < NS; ++b) x[b] = product<T, DH>(kt, b * 32, qo, lane);
-      if (j0 + KT > wave_lo) {
-#pragma unroll
-        for (int b = 0; b < NS; ++b)
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            if (j0 + b * 32 + acc_row(e, lane / 32) >= mine) x[b][e] = -INFINITY;
-      }
-      softmax_step<NS, Ti::kNDB>(x, c, st, o);
-#pragma unroll
-      for (int b = 0; b < NS; ++b) product_t<T, DH>(o, Mma<T>::pack(x[b]), vt, b * 32, lane);
+    if (j0 >= wave_hi) {
+      fetch(i + 1);
+      continue;
     }
+    prepare(i + 1);
+    const uint32_t kt = lds0 + (i & 1) * 2 * Ld::kBytes, vt = kt + Ld::kBytes;
+    Op op;
+    op.rows(kt, lane);
+    pin<T>();
+    f32x16 x[NS];
+#pragma unroll
+    for (int b = 0; b < NS; ++b)
+      x[b] = op.product(qo, [&](int n) {
+        if (b + 1 < NS) op.row(n, kt + (b + 1) * 32 * Ti::kRowB, lane);
+        else spread(n, Op::NT, Op::S, [&](int e) { op.col(e, vt, lane); });
+        spread(b * Op::NT + n, NS * Op::NT, kPieces, piece);
+      });
+    if (j0 + KT > wave_lo) {
+#pragma unroll
+      for (int b = 0; b < NS; ++b)
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (j0 + b * 32 + acc_row(e, lane / 32) >= mine) x[b][e] = -INFINITY;
+    }
+    softmax_step<NS, Ti::kNDB>(x, c, st, o);
+#pragma unroll
+    for (int b = 0; b < NS; ++b)
+      op.product_t(o, Mma<T>::pack(x[b]), [&](int e) {
+        if (b + 1 < NS) op.col(e, vt + (b + 1) * 32 * Ti::kRowB, lane);
+      });
   }
+  wait_and_sync<>();  // no load may reach LDS after the workgroup's end
   const float sum = st.sum + other_half(st.sum);
   if (live) {
     const int64_t at = (s.q0 + t) * a.hq + h;
@@ -541,36 +570,63 @@ __global__ __launch_bounds__(256, sizeof(T) == 4 && DH > 64 ? 1 : 2) void k_attn
   lk.init(tid, a.k_rs);
   lv.init(tid, a.v_rs);
   const uint32_t dst = lds0 + wave * 1024;
-  auto fetch = [&](int i) {
+  u32x4 rk = {}, rv = {};
+  uint32_t to = 0;
+  auto prepare = [&](int i) {
     const int64_t j = (int64_t)i * KT;
-    const uint32_t to = dst + (i & 1) * 2 * Ld::kBytes;
-    lk.load(k + j * a.k_rs, s.m - j, a.k_rs, a.dh, to);
-    lv.load(v + j * a.v_rs, s.m - j, a.v_rs, a.dh, to + Ld::kBytes);
+    rk = lk.range(k + j * a.k_rs, s.m - j, a.k_rs, a.dh);
+    rv = lv.range(v + j * a.v_rs, s.m - j, a.v_rs, a.dh);
+    to = dst + (i & 1) * 2 * Ld::kBytes;
   };
+  auto piece = [&](int q) {
+    if (q < Ld::kRounds) lk.round(q, rk, a.dh, to);
+    else lv.round(q - Ld::kRounds, rv, a.dh, to + Ld::kBytes);
+  };
+  constexpr int kPieces = 2 * Ld::kRounds;
+  auto fetch = [&](int i) {
+    prepare(i);
+#pragma unroll
+    for (int q = 0; q < kPieces; ++q) piece(q);
+  };
+  using Op = Ahead<T, DH>;
   f32x16 acc[Ti::kNDB] = {};
   if (steps > 0) fetch(0);
   for (int i = 0; i < steps; ++i) {
     wait_and_sync<>();
-    if (i + 1 < steps) fetch(i + 1);
     const int j0 = i * KT;
-    if (j0 < wave_hi) {
-      const uint32_t kt = lds0 + (i & 1) * 2 * Ld::kBytes, vt = kt + Ld::kBytes;
-      const bool edge = j0 + KT > wave_lo;
+    if (j0 >= wave_hi) {
+      fetch(i + 1);
+      continue;
+    }
+    prepare(i + 1);
+    const uint32_t kt = lds0 + (i & 1) * 2 * Ld::kBytes, vt = kt + Ld::kBytes;
+    const bool edge = j0 + KT > wave_lo;
+    Op op;
+    op.rows(kt, lane);
+    pin<T>();
 #pragma unroll
-      for (int b = 0; b < NS; ++b) {
-        f32x16 x = product<T, DH>(kt, b * 32, qo, lane);
-        const f32x16 g = product<T, DH>(vt, b * 32, go, lane);
+    for (int b = 0; b < NS; ++b) {
+      const int off = b * 32 * Ti::kRowB;
+      f32x16 x = op.product(qo, [&](int n) {
+        op.row(n, vt + off, lane);
+        spread(b * Op::NT + n, NS * Op::NT, kPieces, piece);
+      });
+      const f32x16 g = op.product(go, [&](int n) {
+        spread(n, Op::NT, Op::S, [&](int e) { op.col(e, kt + off, lane); });
+      });
 #pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] = exp2_of(__builtin_fmaf(x[e], c, -L)) * (g[e] - delta);
-        if (edge) {
+      for (int e = 0; e < 16; ++e) x[e] = exp2_of(__builtin_fmaf(x[e], c, -L)) * (g[e] - delta);
+      if (edge) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            if (j0 + b * 32 + acc_row(e, lane / 32) >= mine) x[e] = 0.f;
-        }
-        product_t<T, DH>(acc, Mma<T>::pack(x), kt, b * 32, lane);
+        for (int e = 0; e < 16; ++e)
+          if (j0 + b * 32 + acc_row(e, lane / 32) >= mine) x[e] = 0.f;
       }
+      op.product_t(acc, Mma<T>::pack(x), [&](int e) {
+        if (b + 1 < NS) spread(e, Op::S, Op::NT, [&](int n) { op.row(n, kt + off + 32 * Ti::kRowB, lane); });
+      });
     }
   }
+  wait_and_sync<>();  // no load may reach LDS after the workgroup's end
   if (live) store_row<T, Ti::kNDB>(dq + at * a.dh, acc, a.scale, a.dh, lane);
 }
 
@@ -707,12 +763,19 @@ __global__ __launch_bounds__((Dkv<T, DH>::kThreads), 2) void k_attn_dkv(Attn a, 
   const uint32_t words = lds0 + 2 * Ld::kBytes + rw * 256 + half * 16;
   auto stage = [](int i) { return (uint32_t)(i % K::kStages) * K::kStage; };
   if (steps > 0) {
-    Ahead<T, DH> op;
+    using Op = Ahead<T, DH>;
+    Op op;
+    // beside the first product: the second one's operands, and the loads of tile i + 2; beside the second: the next rows
+    auto beside = [&](int k, uint32_t at) {
+      spread(k, Op::NT, Op::S, [&](int e) { op.col(e, at, lane); });
+      spread(k, Op::NT, kPieces, piece);
+    };
+    auto next = [&](int e, uint32_t at) { spread(e, Op::S, Op::NT, [&](int k) { op.row(k, at, lane); }); };
     fetch();
     fetch();
     wait_and_sync<>();
     if (first) {
-      op.read(rows, lane);
+      op.rows(rows, lane);
       int ch = 0, ct = end - 1;
       for (int i = 0; i < steps; ++i) {
         wait_and_sync<>();
@@ -723,7 +786,7 @@ __global__ __launch_bounds__((Dkv<T, DH>::kThreads), 2) void k_attn_dkv(Attn a, 
         f32x4 ld[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) ld[e] = __builtin_bit_cast(f32x4, lds16(words + at + e * 32));
-        f32x16 x = op.product(own, rows + at + Ld::kBytes, lane, piece, kPieces);
+        f32x16 x = op.product(own, [&](int k) { beside(k, rows + at + Ld::kBytes); });
 #pragma unroll
         for (int e = 0; e < 16; ++e) x[e] = exp2_of(__builtin_fmaf(x[e], c, -ld[e / 4][e % 4]));
         if (t1 < wave_hi || t1 + 32 > s.n) {
@@ -734,13 +797,13 @@ __global__ __launch_bounds__((Dkv<T, DH>::kThreads), 2) void k_attn_dkv(Attn a, 
           }
         }
         put_p<K::kPack>(px + (i & 1) * K::kPB, x);
-        op.product_t(acc, Mma<T>::pack(x), rows + stage(i + 1), lane);
+        op.product_t(acc, Mma<T>::pack(x), [&](int e) { next(e, rows + stage(i + 1)); });
       }
       wait_and_sync<>();
     } else {
       wait_and_sync<>();
       fetch();
-      op.read(rows + Ld::kBytes, lane);
+      op.rows(rows + Ld::kBytes, lane);
       for (int i = 0; i < steps; ++i) {
         wait_and_sync<>();
         prepare();
@@ -751,10 +814,10 @@ __global__ __launch_bounds__((Dkv<T, DH>::kThreads), 2) void k_attn_dkv(Attn a, 
         u32x4 p[K::kPB / 1024];
 #pragma unroll
         for (int e = 0; e < K::kPB / 1024; ++e) p[e] = lds16(px + (i & 1) * K::kPB + e * 1024);
-        f32x16 g = op.product(own, rows + at, lane, piece, kPieces);
+        f32x16 g = op.product(own, [&](int k) { beside(k, rows + at); });
 #pragma unroll
         for (int e = 0; e < 16; ++e) g[e] = get_p<K::kPack>(p, e) * (g[e] - ld[e / 4][e % 4]);
-        op.product_t(acc, Mma<T>::pack(g), rows + stage(i + 1) + Ld::kBytes, lane);
+        op.product_t(acc, Mma<T>::pack(g), [&](int e) { next(e, rows + stage(i + 1) + Ld::kBytes); });
       }
     }
     wait_and_sync<>();  // no load may reach LDS after this
