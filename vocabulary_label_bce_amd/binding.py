@@ -53,6 +53,8 @@ EXPORTS = ["cutbce_workspace_size", "cutbce_forward", "cutbce_forward_noalloc", 
 def lib():
     """Load libcutbce.so once; raise if it is missing."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -198,9 +200,15 @@ def _at(t):
     return None if t is None else t.data_ptr()
 
 
+def raw_stream(device: int) -> int:
+    """The current stream of the device, as its handle (without the Stream object around it: 0.1 us, not 2.8)."""
+    return torch._C._cuda_getCurrentRawStream(device)
+
+
 def _raw_stream(stream):
-    # (the handle without the Stream object around it: 0.2 us instead of 2.8)
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) if stream is None else stream.cuda_stream
+    if stream is None:
+        return raw_stream(torch.cuda.current_device())
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def _dtype(dtype) -> int:

@@ -16,21 +16,25 @@ from . import binding as B
 
 _FLOATS = (torch.float32, torch.bfloat16)
 
+# These calls are made once per layer and step, on small arrays as well, where the host's time is what they take: the
+# checks below are written for few Python operations.
+
 
 def _need(ok, what):
     if not ok:
         raise ValueError(what)
 
 
-def _on_gpu(what, *tensors):
-    dev = None
-    for t in tensors:
-        if t is None:
-            continue
-        if dev is None and t.is_cuda:
-            dev = torch.cuda.current_device()
-        if t.get_device() != dev:
-            raise ValueError(f"{what} runs on the GPU only: its tensors must be on the current device")
+def _on_gpu(what, first, *others):
+    """The device that every tensor given is on: the current one."""
+    dev = first.get_device()
+    if dev >= 0 and dev == torch._C._cuda_getDevice():
+        for t in others:
+            if t is not None and t.get_device() != dev:
+                break
+        else:
+            return dev
+    raise ValueError(f"{what} runs on the GPU only: its tensors must be on the current device")
 
 
 # ---- embedding lookup -----------------------------------------------------------------------------------------
@@ -43,17 +47,17 @@ def _ids(ids):
 
 def _aligned(t):
     """t itself where its data start at a multiple of 16 bytes, else a copy that does."""
-    return t if t.data_ptr() % 16 == 0 else t.clone()
+    return t.clone() if t.data_ptr() & 15 else t
 
 
 def embedding_forward(ids, table, scale: float = 1.0):
     """out[..., :] = scale * table[ids[...]], zeros where an id is outside [0, V) (padding, e.g. -1)."""
-    _on_gpu("embedding", ids, table)
+    dev = _on_gpu("embedding", ids, table)
     _need(table.dtype in _FLOATS and table.dim() == 2, "table must be float32 or bfloat16 [V, D]")
     _need(math.isfinite(scale), "scale must be finite")
     ids, table = _ids(ids), _aligned(table.contiguous())
-    out = torch.empty(ids.shape + table.shape[1:], dtype=table.dtype, device=table.device)
-    B.embedding_forward(ids, table, scale, out)
+    out = table.new_empty(ids.shape + table.shape[1:])
+    B.embedding_forward(ids, table, scale, out, B.raw_stream(dev))
     return out
 
 
@@ -64,7 +68,7 @@ def embedding_backward(dout, ids, vocab: int, scale: float = 1.0, dtable=None):
     With `dtable` (contiguous [vocab, D] of dout's dtype) the sums are added to it in place and only the rows of the
     looked-up items are touched: for a table shared with the loss, pass the dE that the loss returned. Returns the
     gradient."""
-    _on_gpu("embedding_backward", dout, ids, dtable)
+    dev = _on_gpu("embedding_backward", dout, ids, dtable)
     _need(dout.dtype in _FLOATS and dout.shape[:-1] == ids.shape, "dout must be float32 or bfloat16 [*ids.shape, D]")
     _need(math.isfinite(scale), "scale must be finite")
     ids, dout = _ids(ids), _aligned(dout.contiguous())
@@ -74,10 +78,9 @@ def embedding_backward(dout, ids, vocab: int, scale: float = 1.0, dtable=None):
         _need(dtable.shape == (vocab, D) and dtable.dtype == dout.dtype and dtable.is_contiguous(),
               "dtable must be a contiguous [vocab, D] of dout's dtype")
     else:
-        dtable = torch.empty(vocab, D, dtype=dout.dtype, device=dout.device)
-    ws = torch.empty(B.embedding_backward_workspace_size(ids.numel(), vocab, D, dout.dtype), dtype=torch.uint8,
-                     device=dout.device)
-    B.embedding_backward(ids, dout, scale, accumulate, dtable, ws)
+        dtable = dout.new_empty((vocab, D))
+    ws = dout.new_empty(B.embedding_backward_workspace_size(ids.numel(), vocab, D, dout.dtype), dtype=torch.uint8)
+    B.embedding_backward(ids, dout, scale, accumulate, dtable, ws, B.raw_stream(dev))
     return dtable
 
 
@@ -110,6 +113,8 @@ def _rows(x):
     D = x.shape[-1]
     if x.dim() != 2:
         x = x.reshape(-1, D)
+    if x.is_contiguous() and x.stride(0) == D:
+        return x
     if (D > 1 and x.stride(1) != 1) or (x.shape[0] > 1 and x.stride(0) < D):
         return x.contiguous()
     if x.stride(0) < D:  # a single row
@@ -117,29 +122,33 @@ def _rows(x):
     return x
 
 
-def _norm_params(x, weight, bias):
-    D = x.shape[-1]
-    for p in (weight, bias):
-        _need(p is None or (p.dtype in _FLOATS and p.shape == (D,)), "weight and bias must be float32 or bfloat16 [D]")
-    _need(weight is None or bias is None or weight.dtype == bias.dtype, "weight and bias must have one dtype")
+def _norm_param(p, D):
+    if p is None:
+        return None
+    if p.dtype not in _FLOATS or p.shape != (D,):
+        raise ValueError("weight and bias must be float32 or bfloat16 [D]")
+    return p.contiguous()
 
 
 def layer_norm_forward(x, weight=None, bias=None, eps: float = 1e-5, stats: bool = True):
     """(y, mean, rstd) of layer norm over the last dimension of x [..., D]; mean and rstd float32 [rows], or None
     with stats=False."""
-    _on_gpu("layer_norm", x, weight, bias)
-    _need(x.dtype in _FLOATS and x.dim() >= 1 and x.shape[-1] >= 1, "x must be float32 or bfloat16 [..., D]")
-    _need(0 <= eps < math.inf, "eps must be finite and >= 0")
-    _norm_params(x, weight, bias)
+    dev = _on_gpu("layer_norm", x, weight, bias)
+    if x.dtype not in _FLOATS or x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError("x must be float32 or bfloat16 [..., D]")
+    if not 0 <= eps < math.inf:
+        raise ValueError("eps must be finite and >= 0")
+    D = x.shape[-1]
+    weight, bias = _norm_param(weight, D), _norm_param(bias, D)
+    if weight is not None and bias is not None and weight.dtype != bias.dtype:
+        raise ValueError("weight and bias must have one dtype")
     rows = _rows(x)
-    weight = None if weight is None else weight.contiguous()
-    bias = None if bias is None else bias.contiguous()
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    y = x.new_empty(x.shape)
     mean = rstd = None
     if stats:
-        mean = torch.empty(rows.shape[0], dtype=torch.float32, device=x.device)
+        mean = x.new_empty(rows.shape[0], dtype=torch.float32)
         rstd = torch.empty_like(mean)
-    B.layer_norm_forward(rows, weight, bias, eps, y, mean, rstd)
+    B.layer_norm_forward(rows, weight, bias, eps, y, mean, rstd, B.raw_stream(dev))
     return y, mean, rstd
 
 
@@ -147,23 +156,24 @@ def layer_norm_backward(dy, x, weight, mean, rstd, want_dx: bool = True, want_dw
                         want_dbias: bool = True):
     """(dx, dweight, dbias) from the cotangent dy, the forward's x, weight (or None) and its mean and rstd; dweight
     and dbias in weight's dtype (x's without a weight). What is not wanted is None."""
-    _on_gpu("layer_norm_backward", dy, x, weight, mean, rstd)
-    _need(dy.shape == x.shape and dy.dtype == x.dtype and x.dtype in _FLOATS, "dy must have x's shape and dtype")
-    _norm_params(x, weight, None)
+    dev = _on_gpu("layer_norm_backward", dy, x, weight, mean, rstd)
+    if dy.shape != x.shape or dy.dtype != x.dtype or x.dtype not in _FLOATS:
+        raise ValueError("dy must have x's shape and dtype")
     D = x.shape[-1]
+    weight = _norm_param(weight, D)
     rx, rdy = _rows(x), _rows(dy)
-    for t in (mean, rstd):
-        _need(t.dtype == torch.float32 and t.is_contiguous() and t.numel() == rx.shape[0],
-              "mean and rstd must be the forward's float32 [rows]")
-    weight = None if weight is None else weight.contiguous()
+    n = rx.shape[:1]
+    if not (mean.shape == n and rstd.shape == n and mean.dtype == rstd.dtype == torch.float32 and
+            mean.is_contiguous() and rstd.is_contiguous()):
+        raise ValueError("mean and rstd must be the forward's float32 [rows]")
     pd = x.dtype if weight is None else weight.dtype
-    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if want_dx else None
-    dw = torch.empty(D, dtype=pd, device=x.device) if want_dweight else None
-    db = torch.empty(D, dtype=pd, device=x.device) if want_dbias else None
+    dx = x.new_empty(x.shape) if want_dx else None
+    dw = x.new_empty(D, dtype=pd) if want_dweight else None
+    db = x.new_empty(D, dtype=pd) if want_dbias else None
     ws = None
     if want_dweight or want_dbias:
-        ws = torch.empty(B.layer_norm_backward_workspace_size(rx.shape[0], D), dtype=torch.uint8, device=x.device)
-    B.layer_norm_backward(rdy, rx, weight, mean, rstd, dx, dw, db, ws)
+        ws = x.new_empty(B.layer_norm_backward_workspace_size(n[0], D), dtype=torch.uint8)
+    B.layer_norm_backward(rdy, rx, weight, mean, rstd, dx, dw, db, ws, B.raw_stream(dev))
     return dx, dw, db
 
 
@@ -194,93 +204,100 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5):
 # ---- attention ------------------------------------------------------------------------------------------------
 
 
-def _strided(x, dims):
-    """x, and the strides of `dims`, as the kernels take them: unit stride of the last dimension, 16-byte steps; a
-    contiguous copy where x is not laid out so. A dimension of size 1 steps by 0."""
-    step = 16 // x.element_size()
+def _strided(x):
+    """x [.., rows, heads, head_dim], and the strides of its rows and heads as the kernels take them: unit stride of the
+    last dimension, 16-byte steps; a contiguous copy where x is not laid out so. A dimension of size 1 steps by 0."""
+    mask = 16 // x.element_size() - 1
     for _ in range(2):
-        st = [x.stride(d) if x.shape[d] > 1 else 0 for d in dims]
-        if x.stride(-1) == 1 and x.data_ptr() % 16 == 0 and all(s % step == 0 for s in st) and st[-2] <= 1 << 22:
-            return x, st
+        st, size = x.stride(), x.shape
+        rs = st[-3] if size[-3] > 1 else 0
+        hs = st[-2] if size[-2] > 1 else 0
+        ss = st[0] if len(st) == 4 and size[0] > 1 else 0
+        if st[-1] == 1 and not (rs | hs | ss) & mask and not x.data_ptr() & 15 and rs <= 1 << 22:
+            return x, rs, hs, ss
         x = x.contiguous()
-        if x.data_ptr() % 16:
+        if x.data_ptr() & 15:
             x = x.clone()
-    raise ValueError("head_dim must be a multiple of 8")
+    raise ValueError("head_dim must be a multiple of 8, and heads * head_dim at most 2**22")
 
 
-def _offsets(cu, n, name, dev):
+def _offsets(cu, n, name):
     if cu is None:
         return None
-    _need(cu.dim() == 1 and cu.numel() == n and cu.device == dev, f"{name} must have {n} entries on the device")
-    return cu.to(torch.int32).contiguous()
+    if cu.shape != (n,):
+        raise ValueError(f"{name} must have {n} entries on the device")
+    return cu if cu.dtype == torch.int32 and cu.is_contiguous() else cu.to(torch.int32).contiguous()
 
 
-def _attention(q, k, v, cu_q, cu_k, k_lens, causal, scale, cached):
-    """Checked arguments, the problem with its workspace sizes, and the tensors as the kernels take them."""
-    _need(q.dtype in _FLOATS and q.dtype == k.dtype == v.dtype, "q, k and v must all be float32 or all bfloat16")
-    dh, hq, hk = q.shape[-1], q.shape[-2], k.shape[-2]
-    _need(k.shape == v.shape and k.shape[-1] == dh, "k and v must have one shape, and q's head_dim")
-    _need(hk > 0 and hq > 0 and hq % hk == 0, "the query heads must be a multiple of the key/value heads")
-    _need(dh % 8 == 0 and 8 <= dh <= 128, "head_dim must be a multiple of 8, at most 128")
-    scale = 1.0 / math.sqrt(dh) if scale is None else float(scale)
+def _attention(q, k, v, seqs, causal, scale):
+    """Checked q [rows, heads, head_dim] and k, v [(sequences,) rows, kv heads, head_dim] as the kernels take them, and
+    the problem with its workspace sizes."""
+    dt = q.dtype
+    if dt not in _FLOATS or k.dtype != dt or v.dtype != dt:
+        raise ValueError("q, k and v must all be float32 or all bfloat16")
+    q_rows, hq, dh = q.shape
+    hk = k.shape[-2]
+    if k.shape != v.shape or k.shape[-1] != dh:
+        raise ValueError("k and v must have one shape, and q's head_dim")
+    if hk < 1 or hq < 1 or hq % hk:
+        raise ValueError("the query heads must be a multiple of the key/value heads")
+    if dh & 7 or not 8 <= dh <= 128:
+        raise ValueError("head_dim must be a multiple of 8, at most 128")
+    scale = dh ** -0.5 if scale is None else float(scale)
     _need(math.isfinite(scale), "scale must be finite")
-    q, (q_rs, q_hs) = _strided(q, (0, 1))
-    q_rows = q.shape[0]
-    if cached:
-        seqs, k_rows = k.shape[0], k.shape[0] * k.shape[1]
-        k, (k_ss, k_rs, k_hs) = _strided(k, (0, 1, 2))
-        v, (v_ss, v_rs, v_hs) = _strided(v, (0, 1, 2))
-    else:
-        seqs, k_rows, k_ss, v_ss = cu_q.numel() - 1, k.shape[0], 0, 0
-        k, (k_rs, k_hs) = _strided(k, (0, 1))
-        v, (v_rs, v_hs) = _strided(v, (0, 1))
-    p = B.attention_problem(q_rows, k_rows, q_rs, q_hs, k_rs, k_hs, v_rs, v_hs, k_ss, v_ss, seqs, hq, hk, dh,
-                            B._dtype(q.dtype), 1 if causal else 0, scale)
-    return q, k, v, p
+    q, q_rs, q_hs, _ = _strided(q)
+    k, k_rs, k_hs, k_ss = _strided(k)
+    v, v_rs, v_hs, v_ss = _strided(v)
+    k_rows = k.shape[0] if k.dim() == 3 else k.shape[0] * k.shape[1]
+    return q, k, v, B.attention_problem(q_rows, k_rows, q_rs, q_hs, k_rs, k_hs, v_rs, v_hs, k_ss, v_ss, seqs, hq, hk,
+                                        dh, B._DTYPES[dt], 1 if causal else 0, scale)
 
 
 def _packed(q, k, v, cu_q, cu_k, k_lens, causal, scale):
-    _on_gpu("packed_attention", q, k, v, cu_q, cu_k, k_lens)
+    dev = _on_gpu("packed_attention", q, k, v, cu_q, cu_k, k_lens)
     _need(q.dim() == 3 and k.dim() == 3, "q must be [rows, heads, head_dim] and k, v [rows, kv heads, head_dim]")
     _need(cu_q.dim() == 1 and cu_q.numel() >= 2, "cu_q must be [sequences + 1]")
     n = cu_q.numel()
-    cu_q = _offsets(cu_q, n, "cu_q", q.device)
-    cu_k = _offsets(cu_k, n, "cu_k", q.device)
-    k_lens = _offsets(k_lens, n - 1, "k_lens", q.device)
+    cu_q = _offsets(cu_q, n, "cu_q")
+    cu_k = _offsets(cu_k, n, "cu_k")
+    k_lens = _offsets(k_lens, n - 1, "k_lens")
     if cu_k is None:
         _need(k.shape[0] == q.shape[0], "k must have q's rows where there is no cu_k")
         if k_lens is not None:
             cu_k = cu_q
-    return (cu_q, cu_k, k_lens) + _attention(q, k, v, cu_q, cu_k, k_lens, causal, scale, False)
+    return (dev, cu_q, cu_k, k_lens) + _attention(q, k, v, n - 1, causal, scale)
 
 
-def _scratch(size, dev):
-    return torch.empty(size, dtype=torch.uint8, device=dev) if size else None
+def _scratch(size, like):
+    return like.new_empty(size, dtype=torch.uint8) if size else None
 
 
 def packed_attention_forward(q, k, v, cu_q, cu_k=None, k_lens=None, causal: bool = True, scale=None,
                              want_lse: bool = True):
     """(out, lse) of packed_attention: out [rows, heads, head_dim]; lse float32 [rows, heads], the log of each row's
     sum of exponentials (-inf where a row sees no key), or None."""
-    cu_q, cu_k, k_lens, q, k, v, (a, size, _) = _packed(q, k, v, cu_q, cu_k, k_lens, causal, scale)
-    out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device) if want_lse else None
-    B.attention_forward(a, q, k, v, cu_q, cu_k, k_lens, out, lse, _scratch(size, q.device))
+    dev, cu_q, cu_k, k_lens, q, k, v, (a, size, _) = _packed(q, k, v, cu_q, cu_k, k_lens, causal, scale)
+    out = q.new_empty(q.shape)
+    lse = q.new_empty(q.shape[:2], dtype=torch.float32) if want_lse else None
+    B.attention_forward(a, q, k, v, cu_q, cu_k, k_lens, out, lse, _scratch(size, q), B.raw_stream(dev))
     return out, lse
 
 
 def packed_attention_backward(dout, q, k, v, out, lse, cu_q, cu_k=None, k_lens=None, causal: bool = True, scale=None):
     """(dq, dk, dv) from the cotangent dout, the forward's inputs, and its out and lse."""
-    cu_q, cu_k, k_lens, q, k, v, (a, _, size) = _packed(q, k, v, cu_q, cu_k, k_lens, causal, scale)
+    dev, cu_q, cu_k, k_lens, q, k, v, (a, _, size) = _packed(q, k, v, cu_q, cu_k, k_lens, causal, scale)
     _on_gpu("packed_attention_backward", dout, out, lse)
-    _need(dout.shape == q.shape and dout.dtype == q.dtype, "dout must have q's shape and dtype")
-    _need(out.shape == q.shape and out.dtype == q.dtype and out.is_contiguous() and lse.shape == q.shape[:2] and
-          lse.dtype == torch.float32 and lse.is_contiguous(), "out and lse must be the forward's")
+    if dout.shape != q.shape or dout.dtype != q.dtype:
+        raise ValueError("dout must have q's shape and dtype")
+    if (out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous() or lse.shape != q.shape[:2] or
+            lse.dtype != torch.float32 or not lse.is_contiguous()):
+        raise ValueError("out and lse must be the forward's")
     dout = _aligned(dout.contiguous())
-    dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    dk = torch.empty(k.shape, dtype=q.dtype, device=q.device)
-    dv = torch.empty(k.shape, dtype=q.dtype, device=q.device)
-    B.attention_backward(a, dout, q, k, v, out, lse, cu_q, cu_k, k_lens, dq, dk, dv, _scratch(size, q.device))
+    dq = torch.empty_like(dout)
+    dk = q.new_empty(k.shape)
+    dv = torch.empty_like(dk)
+    B.attention_backward(a, dout, q, k, v, out, lse, cu_q, cu_k, k_lens, dq, dk, dv, _scratch(size, q),
+                         B.raw_stream(dev))
     return dq, dk, dv
 
 
@@ -320,19 +337,18 @@ def cached_attention(q, k_cache, v_cache, lens, causal: bool = True, scale=None)
     [sequences, capacity, kv heads, head_dim] in any strides whose last is 1 (a view of [sequences, kv heads,
     capacity, head_dim] as well); lens [sequences] on the device: the first lens[b] rows are filled, the newest tokens'
     own keys included, and the rest is never used. Returns q's shape."""
-    if torch.is_grad_enabled() and any(t.requires_grad for t in (q, k_cache, v_cache)):
+    dev = _on_gpu("cached_attention", q, k_cache, v_cache, lens)
+    if torch.is_grad_enabled() and (q.requires_grad or k_cache.requires_grad or v_cache.requires_grad):
         raise ValueError("cached_attention has no gradient: use packed_attention, or torch.no_grad()")
-    _on_gpu("cached_attention", q, k_cache, v_cache, lens)
-    shape = q.shape
-    if q.dim() == 3:
-        q = q.unsqueeze(1)
-    _need(q.dim() == 4 and k_cache.dim() == 4 and k_cache.shape[0] == q.shape[0],
+    q = q.contiguous()
+    seqs = k_cache.shape[0]
+    _need(q.dim() in (3, 4) and k_cache.dim() == 4 and seqs == q.shape[0],
           "q must be [sequences, (tokens,) heads, head_dim] and the caches [sequences, capacity, kv heads, head_dim]")
-    lens = _offsets(lens, k_cache.shape[0], "lens", q.device)
-    q = q.contiguous().view(-1, *q.shape[2:])
-    out = torch.empty(shape, dtype=q.dtype, device=q.device)
-    if k_cache.shape[0] == 0:
+    lens = _offsets(lens, seqs, "lens")
+    out = torch.empty_like(q)
+    if seqs == 0:
         return out
-    q, k, v, (a, size, _) = _attention(q, k_cache, v_cache, None, None, lens, causal, scale, True)
-    B.attention_forward(a, q, k, v, None, None, lens, out, None, _scratch(size, q.device))
+    rows = q if q.dim() == 3 else q.view(-1, *q.shape[2:])
+    rows, k, v, (a, size, _) = _attention(rows, k_cache, v_cache, seqs, causal, scale)
+    B.attention_forward(a, rows, k, v, None, None, lens, out, None, _scratch(size, q), B.raw_stream(dev))
     return out
