@@ -381,6 +381,9 @@ template <int N = 0> __device__ inline void wait_and_sync() {
 }
 
 template <typename T, int DH> constexpr int key_tile() { return sizeof(T) == 4 && DH > 64 ? 32 : 64; }
+// LDS stages of the forward and dq: two of 32 KB, or four smaller ones, so that a short sequence's keys are all on
+// their way at once.
+template <typename T, int DH> constexpr int key_stages() { return key_tile<T, DH>() * Tile<T, DH>::kRowB > 8192 ? 2 : 4; }
 
 // Running softmax of one row per lane: `used` is the maximum that the exponents are taken against.
 struct Online {
@@ -418,13 +421,13 @@ __device__ inline float finish_lse(float used, float sum, bool any) {
   return any ? (used + __builtin_amdgcn_logf(sum)) * kLn2 : -INFINITY;
 }
 
-// Forward: a workgroup has 128 rows of one sequence and head, a wave 32 of them; the keys stream through two LDS
-// stages of KT keys.
+// Forward: a workgroup has 128 rows of one sequence and head, a wave 32 of them; the keys stream through LDS stages of
+// KT keys.
 template <typename T, int DH>
 __global__ __launch_bounds__(256, 2) void k_attn_fwd(Attn a, T* __restrict__ out,
                                                      float* __restrict__ lse) {
   using Ti = Tile<T, DH>;
-  constexpr int KT = key_tile<T, DH>(), NS = KT / 32;
+  constexpr int KT = key_tile<T, DH>(), NS = KT / 32, ST = key_stages<T, DH>();
   using Ld = Dma<T, DH, KT, 256>;
   extern __shared__ __align__(1024) char lds[];
   const uint32_t lds0 = uni((uint32_t)(size_t)(CUTBCE_LDS char*)lds);
@@ -461,7 +464,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(Attn a, T* __restrict__ out
     const int64_t j = (int64_t)i * KT;
     rk = lk.range(k + j * a.k_rs, s.m - j, a.k_rs, a.dh);
     rv = lv.range(v + j * a.v_rs, s.m - j, a.v_rs, a.dh);
-    to = dst + (i & 1) * 2 * Ld::kBytes;
+    to = dst + (i & (ST - 1)) * 2 * Ld::kBytes;
   };
   auto piece = [&](int q) {
     if (q < Ld::kRounds) lk.round(q, rk, a.dh, to);
@@ -476,16 +479,19 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(Attn a, T* __restrict__ out
   using Op = Ahead<T, DH>;
   f32x16 o[Ti::kNDB] = {};
   Online st;
-  if (steps > 0) fetch(0);
+  if (steps > 0) {
+#pragma unroll
+    for (int i = 0; i < ST - 1; ++i) fetch(i);
+  }
   for (int i = 0; i < steps; ++i) {
-    wait_and_sync<>();
+    wait_and_sync<(ST - 2) * kPieces>();  // tile i is there, tile i - 1 is done with
     const int j0 = i * KT;
     if (j0 >= wave_hi) {
-      fetch(i + 1);
+      fetch(i + ST - 1);
       continue;
     }
-    prepare(i + 1);
-    const uint32_t kt = lds0 + (i & 1) * 2 * Ld::kBytes, vt = kt + Ld::kBytes;
+    prepare(i + ST - 1);
+    const uint32_t kt = lds0 + (i & (ST - 1)) * 2 * Ld::kBytes, vt = kt + Ld::kBytes;
     Op op;
     op.rows(kt, lane);
     pin<T>();
@@ -526,7 +532,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 4 && DH > 64 ? 1 : 2) void k_attn
     Attn a, const T* __restrict__ dout, const T* __restrict__ out, const float* __restrict__ lse,
     T* __restrict__ dq, float2* __restrict__ stat) {
   using Ti = Tile<T, DH>;
-  constexpr int KT = key_tile<T, DH>(), NS = KT / 32;
+  constexpr int KT = key_tile<T, DH>(), NS = KT / 32, ST = key_stages<T, DH>();
   using Ld = Dma<T, DH, KT, 256>;
   extern __shared__ __align__(1024) char lds[];
   const uint32_t lds0 = uni((uint32_t)(size_t)(CUTBCE_LDS char*)lds);
@@ -576,7 +582,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 4 && DH > 64 ? 1 : 2) void k_attn
     const int64_t j = (int64_t)i * KT;
     rk = lk.range(k + j * a.k_rs, s.m - j, a.k_rs, a.dh);
     rv = lv.range(v + j * a.v_rs, s.m - j, a.v_rs, a.dh);
-    to = dst + (i & 1) * 2 * Ld::kBytes;
+    to = dst + (i & (ST - 1)) * 2 * Ld::kBytes;
   };
   auto piece = [&](int q) {
     if (q < Ld::kRounds) lk.round(q, rk, a.dh, to);
@@ -590,16 +596,19 @@ __global__ __launch_bounds__(256, sizeof(T) == 4 && DH > 64 ? 1 : 2) void k_attn
   };
   using Op = Ahead<T, DH>;
   f32x16 acc[Ti::kNDB] = {};
-  if (steps > 0) fetch(0);
+  if (steps > 0) {
+#pragma unroll
+    for (int i = 0; i < ST - 1; ++i) fetch(i);
+  }
   for (int i = 0; i < steps; ++i) {
-    wait_and_sync<>();
+    wait_and_sync<(ST - 2) * kPieces>();  // tile i is there, tile i - 1 is done with
     const int j0 = i * KT;
     if (j0 >= wave_hi) {
-      fetch(i + 1);
+      fetch(i + ST - 1);
       continue;
     }
-    prepare(i + 1);
-    const uint32_t kt = lds0 + (i & 1) * 2 * Ld::kBytes, vt = kt + Ld::kBytes;
+    prepare(i + ST - 1);
+    const uint32_t kt = lds0 + (i & (ST - 1)) * 2 * Ld::kBytes, vt = kt + Ld::kBytes;
     const bool edge = j0 + KT > wave_lo;
     Op op;
     op.rows(kt, lane);
@@ -859,7 +868,7 @@ __global__ __launch_bounds__((Dkv<T, DH>::kThreads), 2) void k_attn_dkv(Attn a, 
 
 constexpr int kCols = 32;
 
-template <typename T, int DH> constexpr int few_waves() { return Tile<T, DH>::kRowB > 256 ? 2 : 4; }
+template <typename T, int DH> constexpr int few_waves() { return Tile<T, DH>::kRowB > 256 ? 1 : (Tile<T, DH>::kRowB > 128 ? 2 : 4); }
 
 // Parts of each key range: enough workgroups for every CU, at least 256 keys in each part (shorter parts are mostly
 // start-up: the first tile's latency and the join).
@@ -986,35 +995,56 @@ __global__ __launch_bounds__((few_waves<T, DH>() * 64), 1) void k_attn_few(Attn 
   }
 }
 
-// One wave per (sequence, key/value head, column): the parts' results in order.
+// One workgroup per (sequence, key/value head, column): the parts' results. Thread i has part i's maximum and sum (at
+// most 256 parts), then the threads add the outputs, 32 lanes of four features and eight lots of parts, each in order.
 template <typename T, int DH>
 __global__ __launch_bounds__(256) void k_attn_join(Attn a, int parts, int cols, T* __restrict__ out,
                                                    float* __restrict__ lse, const float* __restrict__ part) {
-  const int64_t id = (int64_t)blockIdx.x * 4 + threadIdx.x / 64;
-  const int lane = threadIdx.x % 64;
-  const int64_t bh = id / cols;
-  const int col = (int)(id % cols);
-  if (bh >= (int64_t)a.seqs * a.hk) return;
+  __shared__ float f_of[256], red[4][2], acc[8][DH];
+  const int tid = threadIdx.x, wave = tid / 64;
+  const int64_t bh = blockIdx.x / cols;
+  const int col = (int)(blockIdx.x % cols);
   const SeqRange s = seq_range(a, (int)(bh / a.hk));
   const int t = col / a.group, head = (int)(bh % a.hk) * a.group + col % a.group;
   const bool any = seen_by(a, s, t) > 0;
   const float* p = part + (bh * parts * cols + col) * (DH + 2);
   const int64_t step = (int64_t)cols * (DH + 2);
-  float mx = -INFINITY;
-  for (int i = 0; i < parts; ++i) mx = fmaxf(mx, p[i * step + DH]);
-  float sum = 0.f, y0 = 0.f, y1 = 0.f;
-  for (int i = 0; i < parts; ++i) {
-    const float m = p[i * step + DH];
-    const float f = m == -INFINITY ? 0.f : exp2_of(m - mx);
-    sum += f * p[i * step + DH + 1];
-    if (lane < DH) y0 += f * p[i * step + lane];
-    if (lane + 64 < DH) y1 += f * p[i * step + lane + 64];
+  const float m = tid < parts ? p[tid * step + DH] : -INFINITY;
+  const float l = tid < parts ? p[tid * step + DH + 1] : 0.f;
+  float mx = m;
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor(mx, o, 64));
+  if (tid % 64 == 0) red[wave][0] = mx;
+  __syncthreads();
+  mx = fmaxf(fmaxf(red[0][0], red[1][0]), fmaxf(red[2][0], red[3][0]));
+  const float f = m == -INFINITY ? 0.f : exp2_of(m - mx);
+  f_of[tid] = f;
+  float sum = f * l;
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) sum += __shfl_xor(sum, o, 64);
+  if (tid % 64 == 0) red[wave][1] = sum;
+  __syncthreads();
+  sum = (red[0][1] + red[1][1]) + (red[2][1] + red[3][1]);
+  const int lot = tid / 32, d = tid % 32 * 4;
+  float y[4] = {};
+  if (d < DH) {
+#pragma unroll 4
+    for (int i = lot; i < parts; i += 8) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) y[j] += f_of[i] * p[i * step + d + j];
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[lot][d + j] = y[j];
   }
-  const float inv = any ? 1.f / sum : 0.f;
+  __syncthreads();
   const int64_t at = (s.q0 + t) * a.hq + head;
-  if (lane < a.dh) out[at * a.dh + lane] = (T)(y0 * inv);
-  if (lane + 64 < a.dh) out[at * a.dh + lane + 64] = (T)(y1 * inv);
-  if (lse && lane == 0) lse[at] = finish_lse(mx, sum, any);
+  if (tid < a.dh) {
+    float z = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z += acc[i][tid];
+    out[at * a.dh + tid] = (T)(z * (any ? 1.f / sum : 0.f));
+  }
+  if (lse && tid == 0) lse[at] = finish_lse(mx, sum, any);
 }
 
 // Few query rows: fixed rows per sequence that fill at most one tile's columns with their group's heads.
@@ -1041,12 +1071,12 @@ template <typename T, int DH> hipError_t forward_t(const Attn& a, void* out, flo
     const int64_t bh = (int64_t)a.seqs * a.hk;
     k_attn_few<T, DH><<<dim3((unsigned)(bh * parts)), dim3(NW * 64), bytes, st>>>(a, parts, (T*)out, lse, (float*)ws);
     if (parts > 1)
-      k_attn_join<T, DH><<<dim3((unsigned)cdiv(bh * cols, 4)), dim3(256), 0, st>>>(a, parts, cols, (T*)out, lse,
+      k_attn_join<T, DH><<<dim3((unsigned)(bh * cols)), dim3(256), 0, st>>>(a, parts, cols, (T*)out, lse,
                                                                                    (const float*)ws);
     return hipGetLastError();
   }
   const int64_t units = units_of(a.q_rows, a.seqs);
-  const int bytes = 4 * key_tile<T, DH>() * Ti::kRowB;
+  const int bytes = 2 * key_stages<T, DH>() * key_tile<T, DH>() * Ti::kRowB;
   const hipError_t e = allow_lds((const void*)k_attn_fwd<T, DH>, bytes);
   if (e != hipSuccess) return e;
   k_attn_fwd<T, DH><<<dim3((unsigned)(units * a.hq)), dim3(256), bytes, st>>>(a, (T*)out, lse);
@@ -1060,7 +1090,7 @@ hipError_t backward_t(const Attn& a, const void* dout, const void* out, const fl
   float2* stat = (float2*)ws;
   if (a.q_rows) {
     const int64_t units = units_of(a.q_rows, a.seqs);
-    const int bytes = 4 * key_tile<T, DH>() * Ti::kRowB;
+    const int bytes = 2 * key_stages<T, DH>() * key_tile<T, DH>() * Ti::kRowB;
     const hipError_t e = allow_lds((const void*)k_attn_dq<T, DH>, bytes);
     if (e != hipSuccess) return e;
     k_attn_dq<T, DH><<<dim3((unsigned)(units * a.hq)), dim3(256), bytes, st>>>(a, (const T*)dout, (const T*)out, lse,
