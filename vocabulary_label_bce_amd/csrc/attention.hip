@@ -77,11 +77,11 @@ __device__ inline u32x4 buffer_of(const void* base, int bytes) {  // uniform
 }
 __device__ inline void load_lds16(u32x4 buffer, int voff, uint32_t dst) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-               :: "s"(dst), "v"(voff), "s"(buffer) : "m0");
+               :: "s"(uni(dst)), "v"(voff), "s"(buffer) : "m0");
 }
 __device__ inline void load_lds4(u32x4 buffer, int voff, uint32_t dst) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dword %1, %2, 0 offen lds"
-               :: "s"(dst), "v"(voff), "s"(buffer) : "m0");
+               :: "s"(uni(dst)), "v"(voff), "s"(buffer) : "m0");
 }
 
 // One workgroup's (or wave's) loads of NR rows into LDS: NL lanes, 16 bytes each per instruction.
@@ -526,7 +526,9 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(Attn a, T* __restrict__ out
   }
 }
 
-// dq, and the rows' (lse in base 2, delta) for dk and dv: the forward's layout and loop.
+// dq, and the rows' (lse in base 2, delta) for dk and dv: the forward's layout and loop. dq's own delta is dO . out with
+// the rounded out, since it is needed from the first key on. The sum of a row's dS in float32, sum P dP - delta, is what
+// that delta is off by: for dk it is added (bf16, 200 rows: 0.16% of dk, beside 0.18% for the rounding of dS).
 template <typename T, int DH>
 __global__ __launch_bounds__(256, sizeof(T) == 4 && DH > 64 ? 1 : 2) void k_attn_dq(
     Attn a, const T* __restrict__ dout, const T* __restrict__ out, const float* __restrict__ lse,
@@ -565,7 +567,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 4 && DH > 64 ? 1 : 2) void k_attn
   }
   // a row that sees no key has lse = -inf; +inf makes its probabilities 0
   const float L = mine > 0 ? lse[at] * kLog2e : INFINITY;
-  if (live && lane < 32) stat[(int64_t)h * a.q_rows + s.q0 + t] = make_float2(L, delta);
+  float off_by = 0.f;  // sum dS
   const float c = a.scale * kLog2e;
   const T* k = (const T*)a.k + s.kb + (h / a.group) * a.k_hs;
   const T* v = (const T*)a.v + s.vb + (h / a.group) * a.v_hs;
@@ -611,17 +613,17 @@ __global__ __launch_bounds__(256, sizeof(T) == 4 && DH > 64 ? 1 : 2) void k_attn
     const uint32_t kt = lds0 + (i & (ST - 1)) * 2 * Ld::kBytes, vt = kt + Ld::kBytes;
     const bool edge = j0 + KT > wave_lo;
     Op op;
-    op.rows(kt, lane);
-    pin<T>();
 #pragma unroll
     for (int b = 0; b < NS; ++b) {
       const int off = b * 32 * Ti::kRowB;
+      op.rows(kt + off, lane);
+      pin<T>();
       f32x16 x = op.product(qo, [&](int n) {
         op.row(n, vt + off, lane);
         spread(b * Op::NT + n, NS * Op::NT, kPieces, piece);
       });
       const f32x16 g = op.product(go, [&](int n) {
-        spread(n, Op::NT, Op::S, [&](int e) { op.col(e, kt + off, lane); });
+        spread(n, Op::NT, Op::S / 2, [&](int e) { op.col(e, kt + off, lane); });
       });
 #pragma unroll
       for (int e = 0; e < 16; ++e) x[e] = exp2_of(__builtin_fmaf(x[e], c, -L)) * (g[e] - delta);
@@ -630,13 +632,21 @@ __global__ __launch_bounds__(256, sizeof(T) == 4 && DH > 64 ? 1 : 2) void k_attn
         for (int e = 0; e < 16; ++e)
           if (j0 + b * 32 + acc_row(e, lane / 32) >= mine) x[e] = 0.f;
       }
-      op.product_t(acc, Mma<T>::pack(x), [&](int e) {
-        if (b + 1 < NS) spread(e, Op::S, Op::NT, [&](int n) { op.row(n, kt + off + 32 * Ti::kRowB, lane); });
+#pragma unroll
+      for (int e = 0; e < 16; ++e) off_by += x[e];
+      const typename Mma<T>::P ds = Mma<T>::pack(x);
+      pin<T>();  // x ends here
+      op.product_t(acc, ds, [&](int e) {  // (half of its operands are read beside it: registers)
+        if (e + Op::S / 2 < Op::S) op.col(e + Op::S / 2, kt + off, lane);
       });
     }
   }
   wait_and_sync<>();  // no load may reach LDS after the workgroup's end
-  if (live) store_row<T, Ti::kNDB>(dq + at * a.dh, acc, a.scale, a.dh, lane);
+  off_by += other_half(off_by);
+  if (live) {
+    store_row<T, Ti::kNDB>(dq + at * a.dh, acc, a.scale, a.dh, lane);
+    if (lane < 32) stat[(int64_t)h * a.q_rows + s.q0 + t] = make_float2(L, delta + off_by);
+  }
 }
 
 // How the dk/dv kernel lays out a workgroup: 64 keys, two waves for each 32 of them and each of the RS row blocks of

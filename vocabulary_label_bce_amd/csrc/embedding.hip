@@ -13,6 +13,8 @@ namespace cutbce {
 
 namespace {
 
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+
 constexpr int kSortThreads = 256;
 constexpr int kSortItems = 1024;  // pairs of one sorting workgroup
 constexpr int kMaxBits = 10;      // most bits of one sorting pass
@@ -72,7 +74,8 @@ template <typename I> __device__ inline int key_of(const I* ids, int64_t i, int 
 
 template <typename T, typename I>
 __global__ __launch_bounds__(256) void k_embed(int64_t n, int V, int D, int lpr, const I* __restrict__ ids,
-                                               const T* __restrict__ table, float scale, T* __restrict__ out) {
+                                               const T* __restrict__ table, float scale, T* __restrict__ out,
+                                               bool past) {
   constexpr int N = Vec<T>::N;
   const int rpb = 256 / lpr, sub = threadIdx.x % lpr;
   const int64_t i = (int64_t)blockIdx.x * rpb + threadIdx.x / lpr;
@@ -83,13 +86,14 @@ __global__ __launch_bounds__(256) void k_embed(int64_t n, int V, int D, int lpr,
     if (v < V) load_cols(table + (int64_t)v * D, c, D, x);
 #pragma unroll
     for (int j = 0; j < N; ++j) x[j] *= scale;
-    store_cols(out + i * D, c, D, x);
+    store_cols(out + i * D, c, D, x, past);
   }
 }
 
 // The gradient's table is cleared by the sorting kernels, whose own work fills few CUs and is all latency: the
 // workgroups behind the sorting ones clear a share of it each. Clearing it before the sort instead took 28 us more at
-// 876,000 x 128 bf16 (224 MB).
+// 876,000 x 128 bf16 (224 MB). The stores go past the caches: at 262,144 x 512 float32 (537 MB) the lookup and the row
+// sums around them then still find their rows there (13 -> 8 us each).
 struct Fill {
   char* p;          // of this launch's share
   int64_t bytes;    // 0: nothing to clear
@@ -102,7 +106,7 @@ __device__ inline bool fill(const Fill& f) {
   for (int i = 0; i < kFillBytes / 16 / kSortThreads; ++i) {
     const int64_t o = at + ((int64_t)i * kSortThreads + threadIdx.x) * 16;
     if (o + 16 <= f.bytes) {
-      *(uint4*)(f.p + o) = make_uint4(0, 0, 0, 0);
+      __builtin_nontemporal_store(u32x4{0, 0, 0, 0}, (u32x4*)(f.p + o));
     } else {
       for (int64_t b = o; b < f.bytes && b < o + 16; ++b) f.p[b] = 0;
     }
@@ -391,7 +395,8 @@ hipError_t forward_t(int64_t n, int V, int D, const void* ids, const void* table
                      hipStream_t st) {
   const int lpr = lanes_of(D, Vec<T>::N);
   k_embed<T, I><<<dim3((unsigned)cdiv(n, 256 / lpr)), dim3(256), 0, st>>>(n, V, D, lpr, (const I*)ids,
-                                                                         (const T*)table, scale, (T*)out);
+                                                                         (const T*)table, scale, (T*)out,
+                                                                         goes_past(n * D * (int64_t)sizeof(T)));
   return hipGetLastError();
 }
 

@@ -118,7 +118,7 @@ __global__ __launch_bounds__(kThreads) void k_norm_grad(int64_t rows, int D, int
                                                         int64_t dys, const T* __restrict__ x, int64_t xs,
                                                         const P* __restrict__ w, const float* __restrict__ mean,
                                                         const float* __restrict__ rstd, T* __restrict__ dx,
-                                                        float* __restrict__ part) {
+                                                        float* __restrict__ part, bool past) {
   constexpr int N = Vec<T>::N;
   extern __shared__ float acc[];  // [2][D] where PARAMS and a wave holds a row
   __shared__ float sh[kWaves][2];
@@ -158,7 +158,7 @@ __global__ __launch_bounds__(kThreads) void k_norm_grad(int64_t rows, int D, int
       for (int k = 0; k < C; ++k) {
 #pragma unroll
         for (int i = 0; i < N; ++i) g[k][i] = inv * (g[k][i] - a - h[k][i] * t);
-        if ((k * G + s) * N < D) store_cols(dx + r * D, (k * G + s) * N, D, g[k]);
+        if ((k * G + s) * N < D) store_cols(dx + r * D, (k * G + s) * N, D, g[k], past);
       }
     }
   }
@@ -295,9 +295,10 @@ __global__ __launch_bounds__(1024) void k_norm_join(int parts, int D, const floa
   }
 }
 
-// How a row is held: G lanes of C chunks (C in {1, 2, 4} for 16-bit elements and {1, 2, 4, 8} for float32, 32
-// elements a lane at most; more would spill in the backward). Within a wave the fewest lanes that give each at most
-// 8 elements, where the wave's 64 do; measured at 65,536 x 2048 and 25,600 x 128 (see k_norm_grad's figures).
+// How a row is held: G lanes of C chunks, the fewest lanes of a wave that give each one chunk, else the wave's 64 with
+// up to `most` elements each, else the workgroup's 256. most = 32 in the forward. In the backward, where each element
+// brings two sums along, 16: at 65,536 x 2048 bf16 64 lanes of 32 elements took 260 us (251 registers, two waves per
+// SIMD), 256 lanes of 8 191 us.
 struct Hold {
   int G, C;
 };
@@ -359,12 +360,13 @@ hipError_t backward_t(int64_t rows, int D, const void* dy, int64_t dys, const vo
           rows, D, (const T*)dy, dys, (const T*)x, xs, mean, rstd, (float*)ws);
   } else if (parts) {
     const Hold h = hold_of<T>(D, 16);
+    const bool past = goes_past(rows * D * (int64_t)sizeof(T));
     const int lds = params && h.G <= 64 ? 2 * D * (int)sizeof(float) : 0;  // at most 16 KB
 #define CUTBCE_GRAD(C)                                                                                               \
   (params ? k_norm_grad<T, P, C, true><<<dim3(parts), dim3(kThreads), lds, st>>>(                                    \
-                rows, D, h.G, (const T*)dy, dys, (const T*)x, xs, (const P*)w, mean, rstd, (T*)dx, (float*)ws)       \
+                rows, D, h.G, (const T*)dy, dys, (const T*)x, xs, (const P*)w, mean, rstd, (T*)dx, (float*)ws, past) \
           : k_norm_grad<T, P, C, false><<<dim3(parts), dim3(kThreads), lds, st>>>(                                   \
-                rows, D, h.G, (const T*)dy, dys, (const T*)x, xs, (const P*)w, mean, rstd, (T*)dx, (float*)ws))
+                rows, D, h.G, (const T*)dy, dys, (const T*)x, xs, (const P*)w, mean, rstd, (T*)dx, (float*)ws, past))
     switch (h.C) {
       case 1: CUTBCE_GRAD(1); break;
       case 2: CUTBCE_GRAD(2); break;
