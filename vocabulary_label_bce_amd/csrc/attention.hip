@@ -56,11 +56,14 @@ template <typename T, int DH> struct Tile {
   static constexpr int kCPR = kRowB / 16;
   static constexpr int kNT = DH * kEsz / 32;  // pairs of chunks: k-steps of a product over the features
   static constexpr int kNDB = DH / 32;        // 32-wide blocks of features
+  // LDS has 64 banks, 256 bytes: a row-wise read takes one chunk of 16 rows at a time, a transpose read four chunks of
+  // four rows (from a multiple of 4), a float32 transposed read 128 bytes of rows r and r + 4. The row's bits are dealt to
+  // the chunk's so that each of these covers the banks once. (Dealt for 32 banks the transpose reads took twice as long.)
   __device__ static inline int swz(int r) {
-    if constexpr (kEsz == 4) return r & 7;
-    else if constexpr (kCPR == 4) return (((r >> 1) & 1) << 1) | ((r >> 2) & 1);
-    else if constexpr (kCPR == 8) return ((r & 3) << 1) | ((r >> 2) & 1);
-    else return ((r & 3) << 1) | ((r >> 2) & 1) | (r & 8);
+    if constexpr (kCPR == 4) return (r >> 2) & 3;
+    else if constexpr (kCPR == 8) return ((r >> 1) & 1) << 2 | ((r >> 2) & 3);
+    else if constexpr (kEsz == 2) return (r & 3) << 2 | ((r >> 2) & 3);
+    else return ((r >> 2) & 1) << 3 | ((r >> 3) & 1) << 2 | (r & 3);
   }
 };
 
@@ -151,21 +154,25 @@ template <> struct Mma<__bf16> {
     for (int i = 0; i < 16; ++i) p.g[i / 8][i % 8] = (__bf16)x[i];
     return p;
   }
-  // acc += X^T P, X the 32 rows from LDS row r0 (a multiple of 32) of the tile at `at`: in kSlots matrix instructions,
-  // the blocks of features in turn, each with an operand of its own.
+  // acc += X^T P, X 32 rows of a tile: kSlotsPerBlock matrix instructions for each block of features, the blocks in
+  // turn, each with an operand of its own. An operand's address is the lane's base for the tile with the slot's chunk
+  // bits flipped and its rows added, both constants: the bases are formed for each tile, so that no register holds an
+  // address from one tile to the next (tiles start at a multiple of their row's size).
   typedef bf16x8 A;
   static constexpr int kSlotsPerBlock = 2;
-  template <int DH> __device__ static inline A load_t(int slot, uint32_t at, int r0, int lane) {
+  template <int DH> __device__ static inline uint32_t base_t(uint32_t at, int lane) {
     using Ti = Tile<__bf16, DH>;
-    const int h = lane / 32, s = lane % 16, g = slot / Ti::kNDB, db = slot % Ti::kNDB;
+    const int s = lane % 16, row = 4 * (lane / 32) + s / 4;
+    return at + row * Ti::kRowB + ((2 * ((lane / 16) & 1) + ((s & 3) >> 1)) ^ Ti::swz(row)) * 16 + (s & 1) * 8;
+  }
+  template <int DH> __device__ static inline A load_t(int slot, uint32_t base) {
+    using Ti = Tile<__bf16, DH>;
+    const int g = slot / Ti::kNDB, db = slot % Ti::kNDB;
     s16x4 x[2];
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int row = 16 * g + 8 * e + 4 * h + s / 4;
-      const int c = (db * 4 + 2 * ((lane / 16) & 1) + ((s & 3) >> 1)) ^ Ti::swz(row);
-      x[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-          (CUTBCE_LDS s16x4*)(size_t)(at + (r0 + row) * Ti::kRowB + c * 16 + (s & 1) * 8));
-    }
+    for (int e = 0; e < 2; ++e)
+      x[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((CUTBCE_LDS s16x4*)(size_t)(
+          (base ^ ((db * 4) ^ Ti::swz(16 * g + 8 * e)) * 16) + (16 * g + 8 * e) * Ti::kRowB));
     return __builtin_bit_cast(A, (s16x8)__builtin_shufflevector(x[0], x[1], 0, 1, 2, 3, 4, 5, 6, 7));
   }
   template <int NDB> __device__ static inline void slot_t(f32x16* acc, int slot, A a, const P& p) {
@@ -185,40 +192,47 @@ template <> struct Mma<float> {
   __device__ static inline P pack(const f32x16& x) { return x; }
   typedef float A;
   static constexpr int kSlotsPerBlock = 16;
-  template <int DH> __device__ static inline A load_t(int slot, uint32_t at, int r0, int lane) {
+  template <int DH> __device__ static inline uint32_t base_t(uint32_t at, int lane) {
     using Ti = Tile<float, DH>;
-    const int n = lane % 32, row = acc_row(slot / Ti::kNDB, lane / 32);
-    const int c = ((slot % Ti::kNDB) * 8 + n / 4) ^ Ti::swz(row);
-    return *(CUTBCE_LDS const float*)(size_t)(at + (r0 + row) * Ti::kRowB + c * 16 + (n % 4) * 4);
+    const int n = lane % 32, row = 4 * (lane / 32);
+    return at + row * Ti::kRowB + ((n / 4) ^ Ti::swz(row)) * 16 + (n % 4) * 4;
+  }
+  template <int DH> __device__ static inline A load_t(int slot, uint32_t base) {
+    using Ti = Tile<float, DH>;
+    const int row = acc_row(slot / Ti::kNDB, 0);
+    return *(CUTBCE_LDS const float*)(size_t)((base ^ (((slot % Ti::kNDB) * 8) ^ Ti::swz(row)) * 16) + row * Ti::kRowB);
   }
   template <int NDB> __device__ static inline void slot_t(f32x16* acc, int slot, A a, const P& p) {
     acc[slot % NDB] = __builtin_amdgcn_mfma_f32_32x32x2f32(a, p[slot / NDB], acc[slot % NDB], 0, 0, 0);
   }
 };
 
-// acc += X^T P, scheduled by the compiler.
+// acc += X^T P, scheduled by the compiler: X the 32 rows at `at`.
 template <typename T, int DH>
-__device__ inline void product_t(f32x16* acc, const typename Mma<T>::P& p, uint32_t at, int r0, int lane) {
+__device__ inline void product_t(f32x16* acc, const typename Mma<T>::P& p, uint32_t at, int lane) {
   constexpr int NDB = Tile<T, DH>::kNDB;
+  const uint32_t base = Mma<T>::template base_t<DH>(at, lane);
 #pragma unroll
   for (int k = 0; k < Mma<T>::kSlotsPerBlock * NDB; ++k)
-    Mma<T>::template slot_t<NDB>(acc, k, Mma<T>::template load_t<DH>(k, at, r0, lane), p);
+    Mma<T>::template slot_t<NDB>(acc, k, Mma<T>::template load_t<DH>(k, base), p);
 }
 
-// The tile's operand of k-step t: rows 0 .. 31 from `at`.
-template <typename T, int DH> __device__ inline u32x4 tile_chunk(uint32_t at, int t, int lane) {
+// The tile's operand of k-step t: the 32 rows from `at`, through the lane's base as above.
+template <typename T, int DH> __device__ inline uint32_t base_row(uint32_t at, int lane) {
   using Ti = Tile<T, DH>;
   const int r = lane % 32;
-  return lds16(at + r * Ti::kRowB + (((2 * t + lane / 32) ^ Ti::swz(r)) * 16));
+  return at + r * Ti::kRowB + ((lane / 32) ^ Ti::swz(r)) * 16;
 }
+__device__ inline u32x4 load_row(uint32_t base, int t) { return lds16(base ^ (2 * t * 16)); }
 
 // 32 rows of a tile times the own operand: the result's rows are the tile's, its columns the own rows.
 template <typename T, int DH>
-__device__ inline f32x16 product(uint32_t at, int r0, const u32x4* own, int lane) {
+__device__ inline f32x16 product(uint32_t at, const u32x4* own, int lane) {
   using Ti = Tile<T, DH>;
+  const uint32_t base = base_row<T, DH>(at, lane);
   f32x16 s = {};
 #pragma unroll
-  for (int t = 0; t < Ti::kNT; ++t) s = Mma<T>::mma(tile_chunk<T, DH>(at + r0 * Ti::kRowB, t, lane), own[t], s);
+  for (int t = 0; t < Ti::kNT; ++t) s = Mma<T>::mma(load_row(base, t), own[t], s);
   return s;
 }
 
@@ -237,11 +251,14 @@ template <typename T, int DH> struct Ahead {
   static constexpr int NT = Tile<T, DH>::kNT, NDB = Tile<T, DH>::kNDB, S = Mma<T>::kSlotsPerBlock * NDB;
   u32x4 x[NT];              // 32 rows of a tile
   typename Mma<T>::A t[S];  // 32 rows of a tile, transposed
-  __device__ inline void row(int k, uint32_t at, int lane) { x[k] = tile_chunk<T, DH>(at, k, lane); }
-  __device__ inline void col(int e, uint32_t at, int lane) { t[e] = Mma<T>::template load_t<DH>(e, at, 0, lane); }
-  __device__ inline void rows(uint32_t at, int lane) {
+  // (bases of the lane: rows_at and cols_at of a tile)
+  __device__ static inline uint32_t rows_at(uint32_t at, int lane) { return base_row<T, DH>(at, lane); }
+  __device__ static inline uint32_t cols_at(uint32_t at, int lane) { return Mma<T>::template base_t<DH>(at, lane); }
+  __device__ inline void row(int k, uint32_t base) { x[k] = load_row(base, k); }
+  __device__ inline void col(int e, uint32_t base) { t[e] = Mma<T>::template load_t<DH>(e, base); }
+  __device__ inline void rows(uint32_t base) {
 #pragma unroll
-    for (int k = 0; k < NT; ++k) row(k, at, lane);
+    for (int k = 0; k < NT; ++k) row(k, base);
   }
   // x times the own operand; work(k) after the k-th of NT steps, when x[k] is free
   template <typename F> __device__ inline f32x16 product(const u32x4* own, F work) {
@@ -493,14 +510,15 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(Attn a, T* __restrict__ out
     prepare(i + ST - 1);
     const uint32_t kt = lds0 + (i & (ST - 1)) * 2 * Ld::kBytes, vt = kt + Ld::kBytes;
     Op op;
-    op.rows(kt, lane);
+    const uint32_t kr = Op::rows_at(kt, lane), vc = Op::cols_at(vt, lane);
+    op.rows(kr);
     pin<T>();
     f32x16 x[NS];
 #pragma unroll
     for (int b = 0; b < NS; ++b)
       x[b] = op.product(qo, [&](int n) {
-        if (b + 1 < NS) op.row(n, kt + (b + 1) * 32 * Ti::kRowB, lane);
-        else spread(n, Op::NT, Op::S, [&](int e) { op.col(e, vt, lane); });
+        if (b + 1 < NS) op.row(n, kr + (b + 1) * 32 * Ti::kRowB);
+        else spread(n, Op::NT, Op::S, [&](int e) { op.col(e, vc); });
         spread(b * Op::NT + n, NS * Op::NT, kPieces, piece);
       });
     if (j0 + KT > wave_lo) {
@@ -514,7 +532,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(Attn a, T* __restrict__ out
 #pragma unroll
     for (int b = 0; b < NS; ++b)
       op.product_t(o, Mma<T>::pack(x[b]), [&](int e) {
-        if (b + 1 < NS) op.col(e, vt + (b + 1) * 32 * Ti::kRowB, lane);
+        if (b + 1 < NS) op.col(e, vc + (b + 1) * 32 * Ti::kRowB);
       });
   }
   wait_and_sync<>();  // no load may reach LDS after the workgroup's end
@@ -616,14 +634,15 @@ __global__ __launch_bounds__(256, sizeof(T) == 4 && DH > 64 ? 1 : 2) void k_attn
 #pragma unroll
     for (int b = 0; b < NS; ++b) {
       const int off = b * 32 * Ti::kRowB;
-      op.rows(kt + off, lane);
+      const uint32_t kc = Op::cols_at(kt + off, lane), vr = Op::rows_at(vt + off, lane);
+      op.rows(Op::rows_at(kt + off, lane));
       pin<T>();
       f32x16 x = op.product(qo, [&](int n) {
-        op.row(n, vt + off, lane);
+        op.row(n, vr);
         spread(b * Op::NT + n, NS * Op::NT, kPieces, piece);
       });
       const f32x16 g = op.product(go, [&](int n) {
-        spread(n, Op::NT, Op::S / 2, [&](int e) { op.col(e, kt + off, lane); });
+        spread(n, Op::NT, Op::S / 2, [&](int e) { op.col(e, kc); });
       });
 #pragma unroll
       for (int e = 0; e < 16; ++e) x[e] = exp2_of(__builtin_fmaf(x[e], c, -L)) * (g[e] - delta);
@@ -637,7 +656,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 4 && DH > 64 ? 1 : 2) void k_attn
       const typename Mma<T>::P ds = Mma<T>::pack(x);
       pin<T>();  // x ends here
       op.product_t(acc, ds, [&](int e) {  // (half of its operands are read beside it: registers)
-        if (e + Op::S / 2 < Op::S) op.col(e + Op::S / 2, kt + off, lane);
+        if (e + Op::S / 2 < Op::S) op.col(e + Op::S / 2, kc);
       });
     }
   }
@@ -656,7 +675,7 @@ template <typename T, int DH> struct Dkv {
   static constexpr int kRS = sizeof(T) == 2 && DH > 64 ? 2 : 1;
   static constexpr int kKeys = 64, kQT = 32 * kRS, kStages = 4, kPairs = 2 * kRS, kThreads = kPairs * 128;
   using Ld = Dma<T, DH, kQT, kThreads>;
-  static constexpr int kStage = 2 * Ld::kBytes + kRS * 256;
+  static constexpr int kStage = 2 * Ld::kBytes + 512;  // (a multiple of the rows' size)
   static constexpr bool kPack = kRS > 1;  // P as the upper 24 bits of its float32
   static constexpr int kPB = kPack ? 3072 : 4096;
   static constexpr int kP = kStages * kStage, kBytes = kP + kPairs * 2 * kPB;
@@ -786,15 +805,15 @@ __global__ __launch_bounds__((Dkv<T, DH>::kThreads), 2) void k_attn_dkv(Attn a, 
     Op op;
     // beside the first product: the second one's operands, and the loads of tile i + 2; beside the second: the next rows
     auto beside = [&](int k, uint32_t at) {
-      spread(k, Op::NT, Op::S, [&](int e) { op.col(e, at, lane); });
+      spread(k, Op::NT, Op::S, [&](int e) { op.col(e, at); });
       spread(k, Op::NT, kPieces, piece);
     };
-    auto next = [&](int e, uint32_t at) { spread(e, Op::S, Op::NT, [&](int k) { op.row(k, at, lane); }); };
+    auto next = [&](int e, uint32_t at) { spread(e, Op::S, Op::NT, [&](int k) { op.row(k, at); }); };
     fetch();
     fetch();
     wait_and_sync<>();
     if (first) {
-      op.rows(rows, lane);
+      op.rows(Op::rows_at(rows, lane));
       int ch = 0, ct = end - 1;
       for (int i = 0; i < steps; ++i) {
         wait_and_sync<>();
@@ -805,7 +824,8 @@ __global__ __launch_bounds__((Dkv<T, DH>::kThreads), 2) void k_attn_dkv(Attn a, 
         f32x4 ld[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) ld[e] = __builtin_bit_cast(f32x4, lds16(words + at + e * 32));
-        f32x16 x = op.product(own, [&](int k) { beside(k, rows + at + Ld::kBytes); });
+        const uint32_t gc = Op::cols_at(rows + at + Ld::kBytes, lane), nr = Op::rows_at(rows + stage(i + 1), lane);
+        f32x16 x = op.product(own, [&](int k) { beside(k, gc); });
 #pragma unroll
         for (int e = 0; e < 16; ++e) x[e] = exp2_of(__builtin_fmaf(x[e], c, -ld[e / 4][e % 4]));
         if (t1 < wave_hi || t1 + 32 > s.n) {
@@ -816,13 +836,13 @@ __global__ __launch_bounds__((Dkv<T, DH>::kThreads), 2) void k_attn_dkv(Attn a, 
           }
         }
         put_p<K::kPack>(px + (i & 1) * K::kPB, x);
-        op.product_t(acc, Mma<T>::pack(x), [&](int e) { next(e, rows + stage(i + 1)); });
+        op.product_t(acc, Mma<T>::pack(x), [&](int e) { next(e, nr); });
       }
       wait_and_sync<>();
     } else {
       wait_and_sync<>();
       fetch();
-      op.rows(rows + Ld::kBytes, lane);
+      op.rows(Op::rows_at(rows + Ld::kBytes, lane));
       for (int i = 0; i < steps; ++i) {
         wait_and_sync<>();
         prepare();
@@ -833,10 +853,11 @@ __global__ __launch_bounds__((Dkv<T, DH>::kThreads), 2) void k_attn_dkv(Attn a, 
         u32x4 p[K::kPB / 1024];
 #pragma unroll
         for (int e = 0; e < K::kPB / 1024; ++e) p[e] = lds16(px + (i & 1) * K::kPB + e * 1024);
-        f32x16 g = op.product(own, [&](int k) { beside(k, rows + at); });
+        const uint32_t qc = Op::cols_at(rows + at, lane), nr = Op::rows_at(rows + stage(i + 1) + Ld::kBytes, lane);
+        f32x16 g = op.product(own, [&](int k) { beside(k, qc); });
 #pragma unroll
         for (int e = 0; e < 16; ++e) g[e] = get_p<K::kPack>(p, e) * (g[e] - ld[e / 4][e % 4]);
-        op.product_t(acc, Mma<T>::pack(g), [&](int e) { next(e, rows + stage(i + 1) + Ld::kBytes); });
+        op.product_t(acc, Mma<T>::pack(g), [&](int e) { next(e, nr); });
       }
     }
     wait_and_sync<>();  // no load may reach LDS after this
@@ -944,14 +965,14 @@ __global__ __launch_bounds__((few_waves<T, DH>() * 64), 1) void k_attn_few(Attn 
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     }
     const uint32_t kt = ring + stage * 2 * Ld::kBytes;
-    f32x16 x = product<T, DH>(kt, 0, qo, lane);
+    f32x16 x = product<T, DH>(kt, qo, lane);
     if (b * 32 + 32 > least) {
 #pragma unroll
       for (int e = 0; e < 16; ++e)
         if (b * 32 + acc_row(e, lane / 32) >= mine) x[e] = -INFINITY;
     }
     softmax_step<1, NDB>(&x, c, st, o);
-    product_t<T, DH>(o, Mma<T>::pack(x), kt + Ld::kBytes, 0, lane);
+    product_t<T, DH>(o, Mma<T>::pack(x), kt + Ld::kBytes, lane);
   }
   st.sum += other_half(st.sum);
   // join the waves: each leaves (max, sum) and its scaled output in LDS, which the rings no longer use

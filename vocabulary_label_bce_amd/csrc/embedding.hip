@@ -19,7 +19,7 @@ constexpr int kSortThreads = 256;
 constexpr int kSortItems = 1024;  // pairs of one sorting workgroup
 constexpr int kMaxBits = 10;      // most bits of one sorting pass
 constexpr int kChunk = 8;         // sorted pairs that one lane group sums
-constexpr int kFillBytes = 65536; // what one workgroup clears
+constexpr int kFillBytes = 32768; // what one workgroup clears
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
