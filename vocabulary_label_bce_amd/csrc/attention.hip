@@ -14,6 +14,8 @@
 // Tiles go from memory to LDS by direct buffer loads. A tile's rows past the sequence's end and columns past
 // head_dim lie outside the buffer's range and arrive as zeros. The 16-byte chunks of a row are permuted by the
 // row (swz) so that both the row-wise and the transposed reads spread over the LDS banks.
+#include <atomic>
+
 #include "encoder.h"
 
 namespace cutbce {
@@ -1086,8 +1088,18 @@ size_t few_bytes(const Attn& a) {
   return parts > 1 ? (size_t)a.seqs * a.hk * parts * a.q_pitch * a.group * (128 + 2) * 4 : 0;
 }
 
-hipError_t allow_lds(const void* f, int bytes) {
-  return bytes > 65536 ? hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, bytes) : hipSuccess;
+// Lets kernel F use `bytes` of LDS (the same for every launch of F): set once per device.
+template <auto F> hipError_t allow_lds(int bytes) {
+  static std::atomic<uint64_t> done{0};
+  if (bytes <= 65536) return hipSuccess;
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return hipSuccess;
+  e = hipFuncSetAttribute((const void*)F, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == hipSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 template <typename T, int DH> hipError_t forward_t(const Attn& a, void* out, float* lse, char* ws, hipStream_t st) {
@@ -1097,7 +1109,7 @@ template <typename T, int DH> hipError_t forward_t(const Attn& a, void* out, flo
     const int ring = NW * 4 * 32 * Ti::kRowB, join = NW * 256 + NW * DH * 32 * 4;
     const int bytes = ring > join ? ring : join;
     const int parts = few_parts(a), cols = (int)a.q_pitch * a.group;
-    const hipError_t e = allow_lds((const void*)k_attn_few<T, DH>, bytes);
+    const hipError_t e = allow_lds<k_attn_few<T, DH>>(bytes);
     if (e != hipSuccess) return e;
     const int64_t bh = (int64_t)a.seqs * a.hk;
     k_attn_few<T, DH><<<dim3((unsigned)(bh * parts)), dim3(NW * 64), bytes, st>>>(a, parts, (T*)out, lse, (float*)ws);
@@ -1108,7 +1120,7 @@ template <typename T, int DH> hipError_t forward_t(const Attn& a, void* out, flo
   }
   const int64_t units = units_of(a.q_rows, a.seqs);
   const int bytes = 2 * key_stages<T, DH>() * key_tile<T, DH>() * Ti::kRowB;
-  const hipError_t e = allow_lds((const void*)k_attn_fwd<T, DH>, bytes);
+  const hipError_t e = allow_lds<k_attn_fwd<T, DH>>(bytes);
   if (e != hipSuccess) return e;
   k_attn_fwd<T, DH><<<dim3((unsigned)(units * a.hq)), dim3(256), bytes, st>>>(a, (T*)out, lse);
   return hipGetLastError();
@@ -1122,7 +1134,7 @@ hipError_t backward_t(const Attn& a, const void* dout, const void* out, const fl
   if (a.q_rows) {
     const int64_t units = units_of(a.q_rows, a.seqs);
     const int bytes = 2 * key_stages<T, DH>() * key_tile<T, DH>() * Ti::kRowB;
-    const hipError_t e = allow_lds((const void*)k_attn_dq<T, DH>, bytes);
+    const hipError_t e = allow_lds<k_attn_dq<T, DH>>(bytes);
     if (e != hipSuccess) return e;
     k_attn_dq<T, DH><<<dim3((unsigned)(units * a.hq)), dim3(256), bytes, st>>>(a, (const T*)dout, (const T*)out, lse,
                                                                               (T*)dq, stat);
@@ -1130,7 +1142,7 @@ hipError_t backward_t(const Attn& a, const void* dout, const void* out, const fl
   if (a.k_rows) {
     using K = Dkv<T, DH>;
     const int bytes = K::kBytes;
-    const hipError_t e = allow_lds((const void*)k_attn_dkv<T, DH>, bytes);
+    const hipError_t e = allow_lds<k_attn_dkv<T, DH>>(bytes);
     if (e != hipSuccess) return e;
     k_attn_dkv<T, DH><<<dim3((unsigned)(units_of(a.k_rows, a.seqs, K::kKeys) * a.hk)), dim3(K::kThreads), bytes, st>>>(
         a, (const T*)dout, stat, (T*)dk, (T*)dv);

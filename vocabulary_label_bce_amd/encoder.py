@@ -143,7 +143,7 @@ def layer_norm_forward(x, weight=None, bias=None, eps: float = 1e-5, stats: bool
     if weight is not None and bias is not None and weight.dtype != bias.dtype:
         raise ValueError("weight and bias must have one dtype")
     rows = _rows(x)
-    y = x.new_empty(x.shape)
+    y = torch.empty_like(rows) if rows is x else x.new_empty(x.shape)
     mean = rstd = None
     if stats:
         mean = x.new_empty(rows.shape[0], dtype=torch.float32)
@@ -169,7 +169,9 @@ def layer_norm_backward(dy, x, weight, mean, rstd, want_dx: bool = True, want_dw
     pd = x.dtype if weight is None else weight.dtype
     dx = x.new_empty(x.shape) if want_dx else None
     dw = x.new_empty(D, dtype=pd) if want_dweight else None
-    db = x.new_empty(D, dtype=pd) if want_dbias else None
+    db = None
+    if want_dbias:
+        db = torch.empty_like(dw) if want_dweight else x.new_empty(D, dtype=pd)
     ws = None
     if want_dweight or want_dbias:
         ws = x.new_empty(B.layer_norm_backward_workspace_size(n[0], D), dtype=torch.uint8)
