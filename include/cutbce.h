@@ -212,7 +212,7 @@ cutbce_status cutbce_embedding_backward_workspace_size(int64_t n, int64_t vocab,
  *   accumulate  0: dtable [vocab][dim] is overwritten (rows without a position become 0). Otherwise only the rows
  *               that have a position are read and written: dtable[v] = round(dtable[v] + the sum), for a table
  *               shared with the loss whose dE is there already.
- * Arguments otherwise as for cutbce_embedding_forward; the workspace is 256-byte aligned. */
+ * Arguments otherwise as for cutbce_embedding_forward, with n <= 2^28; the workspace is 256-byte aligned. */
 cutbce_status cutbce_embedding_backward(int64_t n, int64_t vocab, int32_t dim, int32_t dtype, int32_t id_bytes,
                                         const void *ids, const void *dout, float scale, int32_t accumulate,
                                         void *dtable, void *workspace, size_t workspace_bytes, void *stream);
@@ -249,7 +249,7 @@ cutbce_status cutbce_layer_norm_backward(int64_t rows, int32_t dim, int32_t dtyp
  * Strides are in elements: row r, head h of q starts at q + r * q_row_stride + h * q_head_stride (k and v alike);
  * the head_dim elements of one row and head are contiguous. Arrays may be parts of a wider one (a fused
  * projection). q, k, v and their strides in bytes are multiples of 16 (strides may be 0; row strides and q_heads *
- * head_dim are at most 2^22). Outputs (out, dq, dk, dv) are dense
+ * head_dim are at most 2^22), and (max(q_rows, k_rows) / 64 + seqs + 1) * q_heads is under 2^23. Outputs (out, dq, dk, dv) are dense
  * [rows][heads][head_dim].
  * Sequences, query side: sequence b has the rows cu_q[b] .. cu_q[b+1] - 1 (int32 [seqs + 1] on the device,
  * cu_q[0] = 0, non-decreasing, cu_q[seqs] <= q_rows), or, with cu_q NULL, the q_rows / seqs rows from
@@ -320,7 +320,7 @@ cutbce_status cutbce_mfma_ceiling_random(int blocks, int waves_per_block, int it
 const char *cutbce_status_string(cutbce_status s);
 
 /* Library version as major*10000 + minor*100 + patch (host). 0.2.0 added row_weight to cutbce_forward and
- * cutbce_backward. */
+ * cutbce_backward; 0.3.0 added the sequence encoder's operators. */
 int cutbce_version(void);
 
 #ifdef __cplusplus

@@ -128,3 +128,16 @@ def test_layer_norm_more():
     need = B.layer_norm_backward_workspace_size(25600, 128)
     assert 0 < need < 25600 * 128 * 4
     assert _norm_grad(rows=25600, D=128, xs=128, dys=128, size=need - 1) == WORKSPACE
+
+
+def test_sizes_that_one_launch_does_not_take_are_refused():
+    most = 1 << 28
+    assert _embed_grad(n=most + 1) == SHAPE and _embed_grad(n=most, V=10, D=8, size=0) == WORKSPACE
+    n = ctypes.c_size_t(0)
+    size = B.lib().cutbce_embedding_backward_workspace_size
+    assert size(most + 1, 10, 8, B.BF16, ctypes.byref(n)) == SHAPE and size(most, 10, 8, B.BF16, ctypes.byref(n)) == OK
+    heads = dict(q_heads=128, kv_heads=1, seqs=1, q_row_stride=128 * 64, k_row_stride=64, v_row_stride=64)
+    rows = ((1 << 16) - 3) * 64   # rows / 64 + seqs + 1 tiles
+    assert B.lib().cutbce_attention_workspace_size(_attention(q_rows=rows, k_rows=rows, **heads), 1, ctypes.byref(n)) == OK
+    rows += 64
+    assert B.lib().cutbce_attention_workspace_size(_attention(q_rows=rows, k_rows=rows, **heads), 1, ctypes.byref(n)) == SHAPE

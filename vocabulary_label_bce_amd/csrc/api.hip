@@ -195,7 +195,7 @@ cutbce_status scratch_of_current_device(void** out) {
 
 extern "C" {
 
-int cutbce_version(void) { return 200; }
+int cutbce_version(void) { return 300; }
 
 const char* cutbce_status_string(cutbce_status s) {
   switch (s) {

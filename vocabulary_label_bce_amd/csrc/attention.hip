@@ -322,11 +322,11 @@ template <typename T, int NDB> __device__ inline void store_row(T* row, const f3
 // workgroups that take longest start first whatever the sequences' order. A lane has a sequence's number of tiles T;
 // the level of unit u is the l with sum max(0, T - l - 1) <= u < sum max(0, T - l). At 4 x 8192 the forward, whose
 // longest workgroup has as many steps as each of the 512 places gets in all, took 313 us with the sequences one after
-// another.
+// another and 275 so.
 //
-// More sequences: sequence b's tiles start at unit start(b) / M + b, which leaves room for each of them (a range of n
-// rows spans at least ceil(n / M) of these numbers), so that no running total is needed; the lanes look at 64
-// sequences at a time.
+// More sequences than a wave has lanes for: sequence b's tiles start at unit start(b) / M + b, which leaves room for each
+// of them (a range of n rows spans at least ceil(n / M) of these numbers), so that no running total is needed; the lanes
+// look at 64 sequences at a time.
 struct Unit {
   SeqRange s;
   int tile;  // tile of the sequence; may lie behind its end
@@ -441,7 +441,11 @@ __device__ inline float finish_lse(float used, float sum, bool any) {
 }
 
 // Forward: a workgroup has 128 rows of one sequence and head, a wave 32 of them; the keys stream through LDS stages of
-// KT keys.
+// KT keys, shared by the four waves. Two workgroups a CU (registers), so that a SIMD has a wave of each: one's softmax
+// beside the other's products. 4 sequences of up to 8,192 rows, 8 heads over 2 of 128, bf16: 260 us, about 990 TFLOP/s of the
+// seen pairs; the matrix unit is busy 48% of the cycles and vector instructions issue in 41%, so a wave's chain of
+// scores, softmax and product bounds it, and the tail of the longest sequences. 128 sequences of up to 200 rows, 2
+// heads of 64: 11 us, latency (search, first tiles, up to four steps).
 template <typename T, int DH>
 __global__ __launch_bounds__(256, 2) void k_attn_fwd(Attn a, T* __restrict__ out,
                                                      float* __restrict__ lse) {
@@ -546,7 +550,8 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(Attn a, T* __restrict__ out
   }
 }
 
-// dq, and the rows' (lse in base 2, delta) for dk and dv: the forward's layout and loop. dq's own delta is dO . out with
+// dq, and the rows' (lse in base 2, delta) for dk and dv: the forward's layout and loop. At the forward's sizes 365 us
+// (matrix unit busy 53%, vector issue 41%) and 14 us. dq's own delta is dO . out with
 // the rounded out, since it is needed from the first key on. The sum of a row's dS in float32, sum P dP - delta, is what
 // that delta is off by: for dk it is added (bf16, 200 rows: 0.16% of dk, beside 0.18% for the rounding of dS).
 template <typename T, int DH>
@@ -725,7 +730,8 @@ template <bool PACK> __device__ inline float get_p(const u32x4* p, int e) {
 // head_dim 128, one wave per SIMD, and half of them in accumulation registers that vector instructions cannot reach:
 // 1.33 ms at 4 x 8192). So a pair of waves shares 32 keys: the first has k and dv (scores, P, P^T dO), the second v
 // and dk (dP, dS, dS^T Q) one tile behind, with P handed over in LDS. Two waves per SIMD, one of each kind, hide each
-// other's latencies. Where four stages leave too little room for two P's of each pair in float32, its upper 24 bits
+// other's latencies: 600 us (matrix unit busy 38%; the chain of a turn, scores to P to product, is covered only in part by
+// the other wave), 16 us at 128 sequences of up to 200. Where four stages leave too little room for two P's of each pair in float32, its upper 24 bits
 // are handed over: an error of 2^-16, under a hundredth of dS's rounding to bf16. (One P, with a second barrier before
 // it is overwritten, was slower; float16 loses what is under 2^-38 of a row's sum.)
 template <typename T, int DH>
@@ -898,6 +904,11 @@ __global__ __launch_bounds__((Dkv<T, DH>::kThreads), 2) void k_attn_dkv(Attn a, 
 // keys are read once for all of them. A workgroup has one part of the keys of one (sequence, key/value head); its
 // waves take 32-key blocks in turn, each through an LDS ring of its own (no barriers), and join their results in
 // LDS. With more than one part, the parts leave (out, max, sum) in the workspace and k_attn_join joins them in order.
+//
+// Bound by the cache's bytes: 16 ranges of up to 32,768 keys, 16 heads over 2 of 128, bf16 (403 MB): 78 us, 5.1 TB/s, and
+// 4.7 for the join. A ring has two stages of 32 keys, K and V (4 x 32 rows), and a workgroup as many waves as let two
+// workgroups share a CU's LDS where a row is 256 bytes or less: two of two waves there took 81 us, one of four 86.
+// 128 ranges of up to 200 keys, 2 heads of 64: 7.1 us (lengths, first tiles, two blocks a wave, the waves' join).
 
 constexpr int kCols = 32;
 

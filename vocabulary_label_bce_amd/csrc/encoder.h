@@ -14,10 +14,9 @@ __device__ inline float to_f32(float x) { return x; }
 __device__ inline float to_f32(__bf16 x) { return (float)x; }
 template <typename T> __device__ inline T from_f32(float x) { return (T)x; }
 
-// 16 bytes of consecutive elements. U: a run that is aligned to one element only (rows of an odd width).
+// 16 bytes of consecutive elements, aligned to one element only (rows of an odd width).
 template <typename T> struct Vec {
   static constexpr int N = 16 / sizeof(T);
-  typedef T A __attribute__((ext_vector_type(N)));
   typedef T U __attribute__((ext_vector_type(N), aligned(sizeof(T))));
 };
 
@@ -62,9 +61,12 @@ __device__ inline void store_cols(T* row, int c, int D, const float* x, bool pas
 }
 
 // Outputs of more than a quarter of the 256 MB memory-side cache go past the caches (measured: a lookup of 262,144 x
-// 256 bf16, 134 MB, 44 -> 39 us, layer norm's dx of 65,536 x 2048 195 -> 187 us; at 25,600 x 128, 6.5 MB, no
+// 256 bf16, 134 MB, 44 -> 38 us, layer norm's backward at 65,536 x 2048 195 -> 187 us; at 25,600 x 128, 6.5 MB, no
 // difference, and a smaller output is likely still there when the next operator reads it).
 inline bool goes_past(int64_t bytes) { return bytes > (int64_t)64 << 20; }
+
+// Workgroups of one launch: a grid has fewer than 2^32 threads in a dimension. What needs more is launched in turns.
+constexpr int64_t kMaxGrid = (int64_t)1 << 23;
 
 // ---------------------------------------------------------------------------------------------------------
 // Attention: the call's arrays and the ranges of its sequences.
@@ -116,20 +118,6 @@ __device__ inline SeqRange seq_range(const Attn& a, int b) {
   s.cap = (int)(k1 - s.k0);
   s.m = tail ? 0 : (a.k_lens ? (int)clamp64(a.k_lens[b], 0, s.cap) : s.cap);
   return s;
-}
-
-// The sequence whose start is the last one <= row (rows of empty sequences go to the one behind them).
-__device__ inline int seq_of_row(const int32_t* cu, int64_t pitch, int seqs, int64_t row) {
-  if (!cu) {
-    const int64_t b = pitch > 0 ? row / pitch : seqs;
-    return b < seqs ? (int)b : seqs;
-  }
-  int lo = 0, hi = seqs;  // the answer is in [lo, hi]
-  while (lo < hi) {
-    const int mid = lo + (hi - lo + 1) / 2;
-    if (cu[mid] <= row) lo = mid; else hi = mid - 1;
-  }
-  return lo;
 }
 
 // ---------------------------------------------------------------------------------------------------------

@@ -9,6 +9,7 @@ namespace {
 constexpr int64_t kMaxRows = 0x7fffffff;
 constexpr int64_t kMaxVocab = (int64_t)0x7fffffff - 1024;
 constexpr int kMaxDim = 65536;
+constexpr int64_t kMaxSorted = (int64_t)1 << 28;  // a workgroup for 32 sorted positions or more, in one launch
 
 bool bad_align(const void* p, size_t a) { return p && ((uintptr_t)p % a) != 0; }
 bool known(int dtype) { return dtype == CUTBCE_F32 || dtype == CUTBCE_BF16; }
@@ -48,9 +49,9 @@ cutbce_status make_attn(const cutbce_attention* p, const int32_t* cu_q, const in
   const int64_t row_max = (int64_t)1 << 22;
   if (st[0] > row_max || st[2] > row_max || st[4] > row_max || (int64_t)p->q_heads * p->head_dim > row_max)
     return CUTBCE_ERR_SHAPE;
-  // one workgroup per tile of 64 rows or more and head
+  // one workgroup, of at most 512 threads, per tile of 64 rows or more and head, in one launch
   const int64_t rows = p->q_rows > p->k_rows ? p->q_rows : p->k_rows;
-  if ((rows / 64 + p->seqs + 1) * p->q_heads > kMaxRows) return CUTBCE_ERR_SHAPE;
+  if ((rows / 64 + p->seqs + 1) * p->q_heads >= kMaxGrid) return CUTBCE_ERR_SHAPE;
   a->q_rs = st[0], a->q_hs = st[1], a->k_rs = st[2], a->k_hs = st[3], a->v_rs = st[4], a->v_hs = st[5];
   a->k_ss = st[6], a->v_ss = st[7];
   a->q_rows = p->q_rows, a->k_rows = p->k_rows;
@@ -84,6 +85,7 @@ cutbce_status cutbce_embedding_backward_workspace_size(int64_t n, int64_t vocab,
                                                        size_t* bytes) {
   cutbce_status s = check_embedding(n, vocab, dim, dtype);
   if (s != CUTBCE_OK) return s;
+  if (n > kMaxSorted) return CUTBCE_ERR_SHAPE;
   if (!bytes) return CUTBCE_ERR_NULL;
   *bytes = embedding_backward_bytes(n, vocab, dim, dtype);
   return CUTBCE_OK;
@@ -94,6 +96,7 @@ cutbce_status cutbce_embedding_backward(int64_t n, int64_t vocab, int32_t dim, i
                                         void* dtable, void* workspace, size_t workspace_bytes, void* stream) {
   cutbce_status s = check_embedding(n, vocab, dim, dtype);
   if (s != CUTBCE_OK) return s;
+  if (n > kMaxSorted) return CUTBCE_ERR_SHAPE;
   if (id_bytes != 4 && id_bytes != 8) return CUTBCE_ERR_DTYPE;
   if (!dtable || (n > 0 && (!ids || !dout || !workspace))) return CUTBCE_ERR_NULL;
   if (bad_align(ids, id_bytes) || bad_align(dout, 16) || bad_align(dtable, 16) || bad_align(workspace, 256))
