@@ -95,8 +95,8 @@ __global__ __launch_bounds__(256) void k_embed(int64_t n, int V, int D, int lpr,
 
 // The gradient's table is cleared by the sorting kernels, whose own work fills few CUs and is all latency: the
 // workgroups behind the sorting ones clear a share of it each. At 876,000 x 128 bf16 (224 MB) and 25,600 ids the
-// six launches take 52 us; with the table cleared before them it was 28 us more. At 262,144 x 512 float32 (537 MB) and
-// 12,289 ids they take 95 us, 5.6 TB/s. The stores go past the caches: at 262,144 x 512 float32 (537 MB) the lookup and the row
+// six launches take 49 us; with the table cleared before them it was 28 us more. At 262,144 x 512 float32 (537 MB) and
+// 12,289 ids they take 94 us, 5.7 TB/s. The stores go past the caches: at 262,144 x 512 float32 (537 MB) the lookup and the row
 // sums around them then still find their rows there (13 -> 8 us each).
 struct Fill {
   char* p;          // of this launch's share
@@ -423,11 +423,12 @@ hipError_t backward_t(int64_t n, int V, int D, const void* ids, const void* dout
   int* counts = (int*)(ws + L.counts);
   int* totals = (int*)(ws + L.totals);
   const int blocks = (int)p.blocks, digits = 1 << p.bits;
-  // the table's share of each of the sort's launches
-  const int64_t share = cdiv(cdiv(bytes, 3 * p.passes), kFillBytes) * kFillBytes;
+  // A launch's share of the table: a quarter of the pass's to the counting and the scanning each, half to the moving,
+  // whose own work takes longest (the sort at 876,000 x 128 bf16 52 -> 49 us against equal shares; 1 : 1 : 3 49).
+  const int64_t quarter = cdiv(cdiv(bytes, 4 * p.passes), kFillBytes) * kFillBytes;
   int64_t done = 0;
   int more = 0;  // workgroups that clear
-  auto next = [&](int first) {
+  auto next = [&](int first, int64_t share) {
     const int64_t b = bytes - done < share ? bytes - done : share;
     const Fill f = {(char*)dtable + done, b, first};
     done += b;
@@ -441,12 +442,12 @@ hipError_t backward_t(int64_t n, int V, int D, const void* ids, const void* dout
     int* kout = (int*)(ws + L.keys[s & 1]);
     int* pout = (int*)(ws + L.pos[s & 1]);
     const int scans = (int)cdiv(digits, kSortThreads / 64);
-    Fill f = next(blocks);
+    Fill f = next(blocks, quarter);
     k_sort_count<I><<<dim3(blocks + more), dim3(kSortThreads), 0, st>>>(f, n, V, s * p.bits, p.bits, blocks, id0, kin,
                                                                        counts);
-    f = next(scans);
+    f = next(scans, quarter);
     k_sort_scan<<<dim3(scans + more), dim3(kSortThreads), 0, st>>>(f, digits, blocks, counts, totals);
-    f = next(blocks);
+    f = next(blocks, 2 * quarter);
     k_sort_move<I><<<dim3(blocks + more), dim3(kSortThreads), 0, st>>>(f, n, V, s * p.bits, p.bits, blocks, id0, kin,
                                                                       pin, counts, totals, kout, pout);
   }

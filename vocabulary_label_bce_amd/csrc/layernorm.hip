@@ -115,9 +115,10 @@ __global__ __launch_bounds__(kThreads) void k_norm(int64_t rows, int D, int G, c
 }
 
 // One pass over a workgroup's rows: dx, and its share of dw and db. PARAMS: part is wanted. 65,536 x 2048 bf16: 177 us,
-// 4.6 TB/s; 25,600 x 128: 11.6 us and 4,097 x 1000 float32: 18.7 us (2.6 TB/s), where a group's four rows or more come
-// one after another, a latency each (workgroups of fewer rows leave more partials to join: k_norm_join reads 2 D floats
-// of each, 10 us at 1,536 x 2 x 2048, 4 us at the smaller sizes).
+// 4.6 TB/s; 25,600 x 128: 11.6 us and 4,097 x 1000 float32: 18.5 us (2.7 TB/s), where a group's two rows come one
+// after another, a latency each, with the sums over the groups behind them (workgroups of fewer rows leave more partials
+// to join: k_norm_join reads 2 D floats of each, 10 us at 1,536 x 2 x 2048, 4 us at the smaller sizes). Loading a row
+// ahead of its turn: 18.9 us and, for the registers, 258 instead of 174 at 65,536 x 2048.
 template <typename T, typename P, int C, bool PARAMS>
 __global__ __launch_bounds__(kThreads) void k_norm_grad(int64_t rows, int D, int G, const T* __restrict__ dy,
                                                         int64_t dys, const T* __restrict__ x, int64_t xs,
