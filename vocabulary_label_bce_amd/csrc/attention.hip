@@ -15,6 +15,7 @@
 // head_dim lie outside the buffer's range and arrive as zeros. The 16-byte chunks of a row are permuted by the
 // row (swz) so that both the row-wise and the transposed reads spread over the LDS banks.
 #include <atomic>
+#include <type_traits>
 
 #include "encoder.h"
 
@@ -70,12 +71,12 @@ template <typename T, int DH> struct Tile {
 };
 
 // Direct loads from memory to LDS, 16 or 4 bytes a lane from byte `voff` of the buffer to LDS byte `dst` (uniform) +
-// lane * 16 (4); zeros where the buffer ends. As instructions of their own, not as the builtin (which the forward and
-// dq use): before a transpose read the compiler waits for every load to LDS that it knows to be in flight, those of
-// the next stages as well. Nothing is returned in registers; the kernels wait for these loads themselves
-// (wait_and_sync, before the stage is read and before the workgroup ends: no stage is written and read between the same
-// two of those, so the compiler may move LDS reads past these loads). The s_nop covers the wait states between a
-// scalar register's write by a vector instruction (v_readfirstlane) or m0's and its use here.
+// lane * 16 (4); zeros where the buffer ends. As instructions of their own, not as the builtin (which k_attn_few uses
+// for bf16, where it took 80 us and these 84): before a transpose read the compiler waits for every load to LDS that it
+// knows to be in flight, those of the next stages as well. Nothing is returned in registers; the kernels wait for these
+// loads themselves, before the stage is read and before the workgroup ends, and for the reads of a stage before it is
+// loaded over: the compiler may move LDS reads past these loads, but not past those waits. The s_nop covers the wait
+// states between a scalar register's write by a vector instruction (v_readfirstlane) or m0's and its use here.
 __device__ inline u32x4 buffer_of(const void* base, int bytes) {  // uniform
   const uint64_t at = (uint64_t)base;
   return u32x4{(uint32_t)uni((int)at), (uint32_t)uni((int)(at >> 32)) & 0xffffu, (uint32_t)uni(bytes), 0x00020000u};
@@ -905,14 +906,21 @@ __global__ __launch_bounds__((Dkv<T, DH>::kThreads), 2) void k_attn_dkv(Attn a, 
 // waves take 32-key blocks in turn, each through an LDS ring of its own (no barriers), and join their results in
 // LDS. With more than one part, the parts leave (out, max, sum) in the workspace and k_attn_join joins them in order.
 //
-// Bound by the cache's bytes: 16 ranges of up to 32,768 keys, 16 heads over 2 of 128, bf16 (403 MB): 78 us, 5.1 TB/s, and
-// 4.7 for the join. A ring has two stages of 32 keys, K and V (4 x 32 rows), and a workgroup as many waves as let two
-// workgroups share a CU's LDS where a row is 256 bytes or less: two of two waves there took 81 us, one of four 86.
-// 128 ranges of up to 200 keys, 2 heads of 64: 7.1 us (lengths, first tiles, two blocks a wave, the waves' join).
+// Bound by the cache's bytes: 16 ranges of up to 32,768 keys, 16 heads over 2 of 128, bf16 (403 MB): 80 us, 5.0 TB/s, and
+// 4.7 for the join. A workgroup has as many waves as let two of them share a CU's LDS: two of two waves took 81 us there,
+// one of four 86. 128 ranges of up to 200 keys, 2 heads of 64: 7.2 us (lengths, first tiles, two blocks a wave, the
+// waves' join).
+//
+// bf16 rings have two stages of 32 keys, K and V each. A float32 block keeps the matrix unit busy for about as long as
+// its bytes take (32 columns, however few are used), so more waves matter more than more loads in flight: one stage,
+// where K of the next block is loaded from the end of the scores on and V from the end of the second product on. 16
+// ranges of up to 16,384 keys, 16 heads over 2 of 128 (403 MB): 157 us with two stages and one wave, 105 with one and two
+// (3.8 TB/s); 4 heads over 2 of 64: 76 and 53; 100 ranges of up to 200, 2 heads of 128: 37 and 25.
 
 constexpr int kCols = 32;
 
-template <typename T, int DH> constexpr int few_waves() { return Tile<T, DH>::kRowB > 256 ? 1 : (Tile<T, DH>::kRowB > 128 ? 2 : 4); }
+template <typename T> constexpr int few_stages() { return sizeof(T) == 4 ? 1 : 2; }
+template <typename T, int DH> constexpr int few_waves() { return few_stages<T>() * Tile<T, DH>::kRowB > 256 ? 2 : 4; }
 
 // Parts of each key range: enough workgroups for every CU, at least 256 keys in each part (shorter parts are mostly
 // start-up: the first tile's latency and the join).
@@ -929,11 +937,11 @@ __global__ __launch_bounds__((few_waves<T, DH>() * 64), 1) void k_attn_few(Attn 
                                                                         float* __restrict__ lse,
                                                                         float* __restrict__ part) {
   using Ti = Tile<T, DH>;
-  constexpr int NW = few_waves<T, DH>(), NDB = Ti::kNDB;
+  constexpr int NW = few_waves<T, DH>(), NDB = Ti::kNDB, ST = few_stages<T>();
   using Ld = Dma<T, DH, 32, 64>;
   extern __shared__ __align__(1024) char lds[];
   const int tid = threadIdx.x, wave = uni(tid / 64), lane = tid % 64;
-  const uint32_t ring = uni((uint32_t)(size_t)(CUTBCE_LDS char*)lds) + wave * 4 * Ld::kBytes;
+  const uint32_t ring = uni((uint32_t)(size_t)(CUTBCE_LDS char*)lds) + wave * 2 * ST * Ld::kBytes;
   const int pi = blockIdx.x % parts;
   const int64_t bh = blockIdx.x / parts;
   const int hk = (int)(bh % a.hk), seq = (int)(bh / a.hk);
@@ -959,33 +967,65 @@ __global__ __launch_bounds__((few_waves<T, DH>() * 64), 1) void k_attn_few(Attn 
   Ld lk, lv;
   lk.init(lane, a.k_rs);
   lv.init(lane, a.v_rs);
-  auto fetch = [&](int b, int stage) {
+  auto fetch = [&](const Ld& ld, const T* x, int64_t stride, int b, uint32_t to) {
     const int64_t j = (int64_t)b * 32;
-    lk.load(k + j * a.k_rs, s.m - j, a.k_rs, a.dh, ring + stage * 2 * Ld::kBytes);
-    lv.load(v + j * a.v_rs, s.m - j, a.v_rs, a.dh, ring + stage * 2 * Ld::kBytes + Ld::kBytes);
+    if constexpr (ST == 2) {
+      ld.load(x + j * stride, s.m - j, stride, a.dh, to);
+    } else {
+      const u32x4 r = ld.range(x + j * stride, s.m - j, stride, a.dh);
+#pragma unroll
+      for (int q = 0; q < Ld::kRounds; ++q) ld.round(q, r, a.dh, to);
+    }
   };
+  auto fetch_k = [&](int b, int stage) { fetch(lk, k, a.k_rs, b, ring + stage * 2 * Ld::kBytes); };
+  auto fetch_v = [&](int b, int stage) { fetch(lv, v, a.v_rs, b, ring + stage * 2 * Ld::kBytes + Ld::kBytes); };
+  // what was read from LDS has arrived, so it may be loaded over
+  auto read = []() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); };
+  // all but the last `n` tiles' loads have arrived
+  auto arrived = [](auto n) { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(decltype(n)::value * Ld::kRounds) : "memory"); };
+  using std::integral_constant;
   f32x16 o[NDB] = {};
   Online st;
   int stage = 0;
-  if (b0 + wave < b1) fetch(b0 + wave, 0);
-  for (int b = b0 + wave; b < b1; b += NW, stage ^= 1) {
-    // the other stage's reads were waited for by the products that used them
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    if (b + NW < b1) {
-      fetch(b + NW, stage ^ 1);
-      asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * Ld::kRounds) : "memory");
+  if (b0 + wave < b1) {
+    fetch_k(b0 + wave, 0);
+    fetch_v(b0 + wave, 0);
+  }
+  for (int b = b0 + wave; b < b1; b += NW, stage ^= ST - 1) {
+    const bool more = b + NW < b1;
+    if (ST == 2) {
+      read();
+      if (more) {
+        fetch_k(b + NW, stage ^ 1);
+        fetch_v(b + NW, stage ^ 1);
+        arrived(integral_constant<int, 2>());
+      } else {
+        arrived(integral_constant<int, 0>());
+      }
     } else {
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      arrived(integral_constant<int, 1>());
     }
     const uint32_t kt = ring + stage * 2 * Ld::kBytes;
     f32x16 x = product<T, DH>(kt, qo, lane);
+    if (ST == 1 && more) {
+      read();
+      fetch_k(b + NW, 0);
+    }
     if (b * 32 + 32 > least) {
 #pragma unroll
       for (int e = 0; e < 16; ++e)
         if (b * 32 + acc_row(e, lane / 32) >= mine) x[e] = -INFINITY;
     }
     softmax_step<1, NDB>(&x, c, st, o);
+    if (ST == 1) {
+      if (more) arrived(integral_constant<int, 1>());
+      else arrived(integral_constant<int, 0>());
+    }
     product_t<T, DH>(o, Mma<T>::pack(x), kt + Ld::kBytes, lane);
+    if (ST == 1 && more) {
+      read();
+      fetch_v(b + NW, 0);
+    }
   }
   st.sum += other_half(st.sum);
   // join the waves: each leaves (max, sum) and its scaled output in LDS, which the rings no longer use
@@ -1117,7 +1157,7 @@ template <typename T, int DH> hipError_t forward_t(const Attn& a, void* out, flo
   using Ti = Tile<T, DH>;
   if (few_rows(a)) {
     constexpr int NW = few_waves<T, DH>();
-    const int ring = NW * 4 * 32 * Ti::kRowB, join = NW * 256 + NW * DH * 32 * 4;
+    const int ring = NW * 2 * few_stages<T>() * 32 * Ti::kRowB, join = NW * 256 + NW * DH * 32 * 4;
     const int bytes = ring > join ? ring : join;
     const int parts = few_parts(a), cols = (int)a.q_pitch * a.group;
     const hipError_t e = allow_lds<k_attn_few<T, DH>>(bytes);
