@@ -1,7 +1,7 @@
 """Attention over more sequences than a wave has lanes, and lookups and norms of more rows than one launch takes.
 
-Tolerances of the attention as in test_gpu_attention; the large row counts are compared bit for bit with calls on parts
-of the same rows, which the other tests hold to float64."""
+Tolerances of the attention as in test_gpu_attention where none are stated; the large row counts are compared bit for
+bit with calls on parts of the same rows, which the other tests hold to float64."""
 import math
 import random
 
@@ -133,3 +133,26 @@ def test_norm_of_more_rows_than_one_launch_takes():
         for a, b in zip((y, mean, rstd), first):
             part = a[i:i + (1 << 20)]
             assert torch.equal(part, b[:part.shape[0]])
+
+
+@pytest.mark.parametrize("dh", [32, 64, 96, 128])
+def test_dq_of_few_keys_is_not_off_by_the_rounding_of_out(dh):
+    """Up to 128 keys, bf16: dS is off by its own rounding, by the scores' error (e = (head_dim + 16) 2^-24 max|s q.k| +
+    (keys + 16) 2^-24, on P and through delta = sum P dP) and by dP's, but not by the rounding of out."""
+    lens, u, s = [1, 2, 3, 4, 5, 8, 16, 33, 64, 100, 128], 2.0 ** -8, 1 / math.sqrt(dh)
+    q, k, v, g = _make(lens, lens, 1, 1, dh, torch.bfloat16, dh)
+    cu = torch.tensor([0] + lens).cumsum(0).to(torch.int32).cuda()
+    out, lse = ops.packed_attention_forward(q, k, v, cu)
+    dq, _, _ = ops.packed_attention_backward(g, q, k, v, out, lse, cu)
+    at = 0
+    for n in lens:
+        Q, K, V, G = (x[at:at + n, 0].double() for x in (q, k, v, g))
+        S = s * Q @ K.T
+        e = (dh + 16) * 2.0 ** -24 * float(S.abs().max()) + (n + 16) * 2.0 ** -24
+        P = torch.softmax(S.masked_fill(torch.ones_like(S).triu(1).bool(), -math.inf), 1)
+        dP, A = G @ V.T, G.abs() @ V.abs().T
+        dS = P * (dP - (P * dP).sum(1, True))
+        b = (u + e) * dS.abs() + e * P * (A + 2 * (P * A).sum(1, True))
+        want = s * dS @ K
+        _close("dq", dq[at:at + n, 0], want, 2 * s * b @ K.abs() + u * want.abs())
+        at += n

@@ -552,9 +552,12 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(Attn a, T* __restrict__ out
 }
 
 // dq, and the rows' (lse in base 2, delta) for dk and dv: the forward's layout and loop. At the forward's sizes 365 us
-// (matrix unit busy 53%, vector issue 41%) and 14 us. dq's own delta is dO . out with
-// the rounded out, since it is needed from the first key on. The sum of a row's dS in float32, sum P dP - delta, is what
-// that delta is off by: for dk it is added (bf16, 200 rows: 0.16% of dk, beside 0.18% for the rounding of dS).
+// (matrix unit busy 53%, vector issue 41%) and 16 us. delta is needed from the first key on. dO . out with the rounded
+// out is off by out's rounding, which few keys leave as large as dS itself (bf16: dq off by 0.33% of its norm at 4 keys,
+// 0.28% at 16, 0.25% from 256 on; 0.23% is the rounding of dS and dq). So where a workgroup's keys fit into the LDS stages
+// all at once (256 keys, 128 at head_dim over 64), a first pass over them there sums P dP in float32 instead: dq off by
+// 0.23%, 14 -> 16 us at 128 sequences of up to 200. The workgroups with more keys take dO . out (their rows then add
+// little: 0.24% at any length); what it is off by is the sum of a row's dS in float32, and dk gets it added.
 template <typename T, int DH>
 __global__ __launch_bounds__(256, sizeof(T) == 4 && DH > 64 ? 1 : 2) void k_attn_dq(
     Attn a, const T* __restrict__ dout, const T* __restrict__ out, const float* __restrict__ lse,
@@ -577,20 +580,6 @@ __global__ __launch_bounds__(256, sizeof(T) == 4 && DH > 64 ? 1 : 2) void k_attn
   load_own<T, DH>(qo, (const T*)a.q + (s.q0 + t) * a.q_rs + h * a.q_hs, live, a.dh, lane);
   load_own<T, DH>(go, dout + at * a.dh, live, a.dh, lane);
   const int mine = live ? seen_by(a, s, t) : 0;
-  float delta = 0.f;
-  {
-    u32x4 oo[Ti::kNT];
-    load_own<T, DH>(oo, out + at * a.dh, live, a.dh, lane);
-    constexpr int N = 16 / sizeof(T);
-    typedef T V __attribute__((ext_vector_type(N)));
-#pragma unroll
-    for (int i = 0; i < Ti::kNT; ++i) {
-      const V x = __builtin_bit_cast(V, go[i]), y = __builtin_bit_cast(V, oo[i]);
-#pragma unroll
-      for (int j = 0; j < N; ++j) delta += to_f32(x[j]) * to_f32(y[j]);
-    }
-    delta += other_half(delta);
-  }
   // a row that sees no key has lse = -inf; +inf makes its probabilities 0
   const float L = mine > 0 ? lse[at] * kLog2e : INFINITY;
   float off_by = 0.f;  // sum dS
@@ -628,6 +617,41 @@ __global__ __launch_bounds__(256, sizeof(T) == 4 && DH > 64 ? 1 : 2) void k_attn
 #pragma unroll
     for (int i = 0; i < ST - 1; ++i) fetch(i);
   }
+  float delta = 0.f;
+  bool all = false;  // delta from all of the keys
+  if constexpr (sizeof(T) == 2) {
+    all = steps <= ST;
+    if (all && steps > 0) {
+      fetch(ST - 1);
+      wait_and_sync<>();
+      for (int i = 0; i * KT < wave_hi; ++i) {
+        const uint32_t kt = lds0 + i * 2 * Ld::kBytes;
+#pragma unroll
+        for (int b = 0; b < NS; ++b) {
+          f32x16 x = product<T, DH>(kt + b * 32 * Ti::kRowB, qo, lane);
+          const f32x16 g = product<T, DH>(kt + Ld::kBytes + b * 32 * Ti::kRowB, go, lane);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            x[e] = exp2_of(__builtin_fmaf(x[e], c, -L)) * g[e];
+            delta += i * KT + b * 32 + acc_row(e, lane / 32) < mine ? x[e] : 0.f;
+          }
+        }
+      }
+    }
+  }
+  if (!all) {
+    u32x4 oo[Ti::kNT];
+    load_own<T, DH>(oo, out + at * a.dh, live, a.dh, lane);
+    constexpr int N = 16 / sizeof(T);
+    typedef T V __attribute__((ext_vector_type(N)));
+#pragma unroll
+    for (int i = 0; i < Ti::kNT; ++i) {
+      const V x = __builtin_bit_cast(V, go[i]), y = __builtin_bit_cast(V, oo[i]);
+#pragma unroll
+      for (int j = 0; j < N; ++j) delta += to_f32(x[j]) * to_f32(y[j]);
+    }
+  }
+  delta += other_half(delta);
   for (int i = 0; i < steps; ++i) {
     wait_and_sync<(ST - 2) * kPieces>();  // tile i is there, tile i - 1 is done with
     const int j0 = i * KT;
