@@ -759,10 +759,14 @@ template <bool PACK> __device__ inline float get_p(const u32x4* p, int e) {
 // the other wave), 16 us at 128 sequences of up to 200. Where four stages leave too little room for two P's of each pair in float32, its upper 24 bits
 // are handed over: an error of 2^-16, under a hundredth of dS's rounding to bf16. (One P, with a second barrier before
 // it is overwritten, was slower; float16 loses what is under 2^-38 of a row's sum.)
-template <typename T, int DH>
-__global__ __launch_bounds__((Dkv<T, DH>::kThreads), 2) void k_attn_dkv(Attn a, const T* __restrict__ dout,
+//
+// SPLIT: `parts` workgroups for each key tile and head, with a share of its steps each (dkv_parts).
+template <typename T, int DH, bool SPLIT>
+__global__ __launch_bounds__((Dkv<T, DH>::kThreads), 2) void k_attn_dkv(Attn a, int parts,
+                                                                        const T* __restrict__ dout,
                                                                         const float2* __restrict__ stat,
-                                                                        T* __restrict__ dk, T* __restrict__ dv) {
+                                                                        T* __restrict__ dk, T* __restrict__ dv,
+                                                                        float* __restrict__ sums) {
   using Ti = Tile<T, DH>;
   using K = Dkv<T, DH>;
   using Ld = typename K::Ld;
@@ -772,8 +776,9 @@ __global__ __launch_bounds__((Dkv<T, DH>::kThreads), 2) void k_attn_dkv(Attn a, 
   const int tid = threadIdx.x, wave = uni(tid / 64), lane = tid % 64, half = lane / 32;
   const int pair = wave % K::kPairs, kw = pair % 2, rw = pair / 2;  // which 32 keys, which rows of a stage
   const bool first = wave < K::kPairs;
-  const int hk = blockIdx.x % a.hk;
-  const Unit u = find_unit<K::kKeys, false>(a, a.cu_k, a.k_pitch, a.k_rows, blockIdx.x / a.hk);
+  const unsigned part = SPLIT ? blockIdx.x % parts : 0, tile = SPLIT ? blockIdx.x / parts : blockIdx.x;
+  const int hk = tile % a.hk;
+  const Unit u = find_unit<K::kKeys, false>(a, a.cu_k, a.k_pitch, a.k_rows, tile / a.hk);
   const SeqRange& s = u.s;
   const int64_t j0 = (int64_t)u.tile * K::kKeys;
   if (j0 >= s.cap) return;
@@ -787,7 +792,9 @@ __global__ __launch_bounds__((Dkv<T, DH>::kThreads), 2) void k_attn_dkv(Attn a, 
   auto first_row = [&](int64_t x) { return a.causal ? (int)clamp64(x - ((int64_t)s.m - s.n), 0, s.n) : 0; };
   const int mine = first_row(j), wave_hi = first_row(j0 + kw * 32 + 31);
   const int begin = j0 < s.m ? first_row(j0) / QT : 0, end = j0 < s.m ? (s.n + QT - 1) / QT : 0;
-  const int steps = end > begin ? (end - begin) * a.group : 0;
+  const int total = end > begin ? (end - begin) * a.group : 0;
+  const int from = SPLIT ? (int)((int64_t)total * part / parts) : 0;  // the first of this part's steps
+  const int steps = SPLIT ? (int)((int64_t)total * (part + 1) / parts) - from : total;
   Ld lq, lg;
   lq.init(tid, a.q_rs);
   lg.init(tid, (int64_t)a.hq * a.dh);
@@ -795,8 +802,9 @@ __global__ __launch_bounds__((Dkv<T, DH>::kThreads), 2) void k_attn_dkv(Attn a, 
   // the workgroups of a sequence read the same tiles at about the same time, through the L2 cache.
   // Workgroups begin with different heads: the rows of one head lie a power of two apart as often as not, and would
   // all come from a few channels of the cache.
-  const int turn = (int)(blockIdx.x / a.hk / 4 % a.group);
-  int fh = 0, ft = end - 1, fi = 0;  // head (from `turn` on), tile and index of the next fetch
+  const int turn = (int)(tile / a.hk / 4 % a.group);
+  const int h0 = SPLIT ? from % a.group : 0, t0 = end - 1 - (SPLIT ? from / a.group : 0);
+  int fh = h0, ft = t0, fi = 0;  // head (from `turn` on), tile and index of the next fetch
   // A fetch in pieces: one load each, to be spread over a turn (together at its beginning they held up the products
   // behind them). Beyond the last tile the range is empty: zeros are loaded.
   constexpr int kPieces = 2 * Ld::kRounds + 1;
@@ -847,7 +855,7 @@ __global__ __launch_bounds__((Dkv<T, DH>::kThreads), 2) void k_attn_dkv(Attn a, 
     wait_and_sync<>();
     if (first) {
       op.rows(Op::rows_at(rows, lane));
-      int ch = 0, ct = end - 1;
+      int ch = h0, ct = t0;
       for (int i = 0; i < steps; ++i) {
         wait_and_sync<>();
         prepare();
@@ -920,8 +928,41 @@ __global__ __launch_bounds__((Dkv<T, DH>::kThreads), 2) void k_attn_dkv(Attn a, 
 #pragma unroll
       for (int d = 0; d < Ti::kNDB; ++d) acc[d] = f32x16{};
     }
-    store_row<T, Ti::kNDB>((first ? dv : dk) + ((s.k0 + j) * a.hk + hk) * a.dh, acc, first ? 1.f : a.scale, a.dh, lane);
+    const int64_t row = (s.k0 + j) * a.hk + hk;
+    if constexpr (!SPLIT) {
+      store_row<T, Ti::kNDB>((first ? dv : dk) + row * a.dh, acc, first ? 1.f : a.scale, a.dh, lane);
+    } else {
+      store_row<float, Ti::kNDB>(sums + ((2 * part + (first ? 0 : 1)) * a.k_rows * a.hk + row) * a.dh, acc,
+                                 first ? 1.f : a.scale, a.dh, lane);
+    }
   }
+}
+
+// Few key tiles leave CUs idle: the rows (and heads) that a tile meets are then dealt to several workgroups, which leave
+// their sums in the workspace for k_attn_dkv_join. At least 256 rows each (fewer are mostly start-up), and no more
+// workgroups than two a CU in all. One sequence of 4,096 rows, 8 heads over 1 of 128, bf16: 491 us whole, 111
+// in 7 parts with the join; of 2,048, 1 head of 128, float32: 293 and 59; of 600, 2 heads over 1 of 64, bf16: 31 and 18.
+int dkv_parts(const Attn& a) {
+  const int64_t wgs = (a.k_rows / 64 + a.seqs + 1) * a.hk, most = a.q_pitch * a.group / 256;
+  int64_t p = 512 / wgs;
+  if (p > most) p = most;
+  return (int)(p < 1 ? 1 : p);
+}
+
+// The parts' sums in their order: dv (blockIdx.y == 0) and dk of n elements each, four a thread.
+template <typename T>
+__global__ __launch_bounds__(256) void k_attn_dkv_join(int parts, int64_t n, const float* __restrict__ sums,
+                                                       T* __restrict__ dk, T* __restrict__ dv) {
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i >= n) return;
+  f32x4 x = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int p = 0; p < parts; ++p) x += *(const f32x4*)(sums + (2 * p + blockIdx.y) * n + i);
+  typedef T V4 __attribute__((ext_vector_type(4)));
+  V4 y;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) y[j] = (T)x[j];
+  *(V4*)((blockIdx.y ? dk : dv) + i) = y;
 }
 
 // ---- few query rows against long key ranges ---------------------------------------------------------------------
@@ -1201,6 +1242,8 @@ template <typename T, int DH> hipError_t forward_t(const Attn& a, void* out, flo
   return hipGetLastError();
 }
 
+size_t stat_bytes(const Attn& a) { return cdiv(a.q_rows * a.hq * (int64_t)sizeof(float2), 256) * 256; }
+
 template <typename T, int DH>
 hipError_t backward_t(const Attn& a, const void* dout, const void* out, const float* lse, void* dq, void* dk, void* dv,
                       char* ws, hipStream_t st) {
@@ -1217,10 +1260,22 @@ hipError_t backward_t(const Attn& a, const void* dout, const void* out, const fl
   if (a.k_rows) {
     using K = Dkv<T, DH>;
     const int bytes = K::kBytes;
-    const hipError_t e = allow_lds<k_attn_dkv<T, DH>>(bytes);
-    if (e != hipSuccess) return e;
-    k_attn_dkv<T, DH><<<dim3((unsigned)(units_of(a.k_rows, a.seqs, K::kKeys) * a.hk)), dim3(K::kThreads), bytes, st>>>(
-        a, (const T*)dout, stat, (T*)dk, (T*)dv);
+    const unsigned units = (unsigned)(units_of(a.k_rows, a.seqs, K::kKeys) * a.hk);
+    const int parts = dkv_parts(a);
+    if (parts == 1) {
+      const hipError_t e = allow_lds<k_attn_dkv<T, DH, false>>(bytes);
+      if (e != hipSuccess) return e;
+      k_attn_dkv<T, DH, false><<<dim3(units), dim3(K::kThreads), bytes, st>>>(a, 1, (const T*)dout, stat, (T*)dk, (T*)dv,
+                                                                             nullptr);
+    } else {
+      const hipError_t e = allow_lds<k_attn_dkv<T, DH, true>>(bytes);
+      if (e != hipSuccess) return e;
+      const int64_t n = a.k_rows * a.hk * a.dh;
+      float* sums = (float*)(ws + stat_bytes(a));
+      k_attn_dkv<T, DH, true><<<dim3(units * parts), dim3(K::kThreads), bytes, st>>>(a, parts, (const T*)dout, stat,
+                                                                                    (T*)dk, (T*)dv, sums);
+      k_attn_dkv_join<T><<<dim3((unsigned)cdiv(n, 1024), 2), dim3(256), 0, st>>>(parts, n, sums, (T*)dk, (T*)dv);
+    }
   }
   return hipGetLastError();
 }
@@ -1239,7 +1294,10 @@ hipError_t backward_t(const Attn& a, const void* dout, const void* out, const fl
 }  // namespace
 
 size_t attention_bytes(const Attn& a, bool backward) {
-  if (backward) return (size_t)a.q_rows * a.hq * sizeof(float2);
+  if (backward) {
+    const int parts = dkv_parts(a);
+    return stat_bytes(a) + (parts > 1 ? (size_t)parts * 2 * a.k_rows * a.hk * a.dh * sizeof(float) : 0);
+  }
   // (whether the call is one of few rows depends on its arrays too: the size covers both)
   return a.q_rows % a.seqs == 0 && a.q_pitch * a.group <= kCols ? few_bytes(a) : 0;
 }
