@@ -1,4 +1,5 @@
-"""Attention over more sequences than a wave has lanes, and lookups and norms of more rows than one launch takes.
+"""Attention over more sequences than a wave has lanes and over single long ones, and lookups and norms of more rows
+than one launch takes.
 
 Tolerances of the attention as in test_gpu_attention where none are stated; the large row counts are compared bit for
 bit with calls on parts of the same rows, which the other tests hold to float64."""
@@ -8,7 +9,7 @@ import random
 import pytest
 import torch
 
-from test_gpu_attention import _close, _make, _ref, _run
+from test_gpu_attention import _check_lse, _close, _make, _ref, _run
 from vocabulary_label_bce_amd import ops
 
 pytestmark = pytest.mark.gpu
@@ -156,3 +157,69 @@ def test_dq_of_few_keys_is_not_off_by_the_rounding_of_out(dh):
         want = s * dS @ K
         _close("dq", dq[at:at + n, 0], want, 2 * s * b @ K.abs() + u * want.abs())
         at += n
+
+
+@pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("n,m,fill,hq,hk,dh", [
+    (1900, 1900, 1900, 1, 1, 128), (700, 2500, 2321, 2, 1, 64), (2500, 1700, 1653, 2, 2, 40), (1, 3000, 3000, 2, 1, 32),
+    (130, 2000, 0, 2, 1, 96), (2050, 2050, 1, 4, 1, 64)])
+def test_one_sequence_with_few_heads(dt, causal, n, m, fill, hq, hk, dh):
+    """A tile's keys (forward, dq) or rows (dk, dv) are dealt to several workgroups: also where most parts have none, or
+    rows see no key."""
+    q, k, v, g = _make([n], [m], hq, hk, dh, dt, n)
+    k[fill:] = math.nan
+    v[fill:] = math.inf
+    cu_q, cu_k, kl = (torch.tensor(x, dtype=torch.int32).cuda() for x in ([0, n], [0, m], [fill]))
+    out, lse = ops.packed_attention_forward(q, k, v, cu_q, cu_k, kl, causal)
+    grads = ops.packed_attention_backward(g, q, k, v, out, lse, cu_q, cu_k, kl, causal)
+    kk, vv = (torch.nan_to_num(x.double(), 0, 0, 0) for x in (k, v))
+    (o, L, *want), (bo, bl, *bounds) = _ref(q, kk, vv, g, [(0, n, 0, fill)], causal, 1 / math.sqrt(dh), dt)
+    _close("out", out, o, bo)
+    _check_lse(lse, L, bl)
+    for name, got, w, b in zip(("dq", "dk", "dv"), grads, want, bounds):
+        _close(name, got, w, b)
+    again = ops.packed_attention_forward(q, k, v, cu_q, cu_k, kl, causal)
+    assert torch.equal(again[0], out) and torch.equal(again[1], lse)
+    for x, y in zip(ops.packed_attention_backward(g, q, k, v, out, lse, cu_q, cu_k, kl, causal), grads):
+        assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("dt", DTS)
+def test_a_prompt_against_a_long_cache(dt):
+    tokens, hq, hk, dh, lens, S = 50, 4, 2, 64, [5000, 33], 5100
+    gen = torch.Generator(device="cuda").manual_seed(31)
+    q = torch.randn(2, tokens, hq, dh, generator=gen, device="cuda").to(dt)
+    k = torch.randn(2, S, hk, dh, generator=gen, device="cuda").to(dt)
+    v = torch.randn(2, S, hk, dh, generator=gen, device="cuda").to(dt)
+    out = ops.cached_attention(q, k, v, torch.tensor(lens, dtype=torch.int32).cuda())
+    (o, *_), (bo, *_) = _ref(q.view(-1, hq, dh), k.view(-1, hk, dh), v.view(-1, hk, dh), q.view(-1, hq, dh),
+                             [(b * tokens, tokens, b * S, m) for b, m in enumerate(lens)], True, 1 / math.sqrt(dh), dt)
+    _close("out", out.view(-1, hq, dh), o, bo)
+
+
+def test_one_sequence_with_few_heads_in_a_graph():
+    q, k, v, g = _make([2100], [2100], 2, 1, 64, torch.bfloat16, 41)
+    cu = torch.tensor([0, 2100], dtype=torch.int32).cuda()
+
+    def run():
+        out, lse = ops.packed_attention_forward(q, k, v, cu)
+        return (out, lse) + ops.packed_attention_backward(g, q, k, v, out, lse, cu)
+
+    want = [x.clone() for x in run()]
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        run()
+    torch.cuda.current_stream().wait_stream(stream)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run()
+    for _ in range(3):
+        for x in got:
+            x.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+        run()
+        torch.cuda.synchronize()

@@ -447,17 +447,21 @@ __device__ inline float finish_lse(float used, float sum, bool any) {
 // seen pairs; the matrix unit is busy 48% of the cycles and vector instructions issue in 41%, so a wave's chain of
 // scores, softmax and product bounds it, and the tail of the longest sequences. 128 sequences of up to 200 rows, 2
 // heads of 64: 11 us, latency (search, first tiles, up to four steps).
-template <typename T, int DH>
-__global__ __launch_bounds__(256, 2) void k_attn_fwd(Attn a, T* __restrict__ out,
-                                                     float* __restrict__ lse) {
+//
+// SPLIT: `parts` workgroups for each tile of rows and head, with a share of its steps each (row_parts); they leave their
+// sums and, for each row, the maximum and sum of its exponentials (-1 for a row that sees no key) for k_attn_fwd_join.
+template <typename T, int DH, bool SPLIT>
+__global__ __launch_bounds__(256, 2) void k_attn_fwd(Attn a, int parts, T* __restrict__ out, float* __restrict__ lse,
+                                                     float* __restrict__ sums, float2* __restrict__ stats) {
   using Ti = Tile<T, DH>;
   constexpr int KT = key_tile<T, DH>(), NS = KT / 32, ST = key_stages<T, DH>();
   using Ld = Dma<T, DH, KT, 256>;
   extern __shared__ __align__(1024) char lds[];
   const uint32_t lds0 = uni((uint32_t)(size_t)(CUTBCE_LDS char*)lds);
   const int tid = threadIdx.x, wave = uni(tid / 64), lane = tid % 64;
-  const int h = blockIdx.x % a.hq;
-  const Unit u = find_unit<kRows, true>(a, a.cu_q, a.q_pitch, a.q_rows, blockIdx.x / a.hq);
+  const unsigned part = SPLIT ? blockIdx.x % parts : 0, tile = SPLIT ? blockIdx.x / parts : blockIdx.x;
+  const int h = tile % a.hq;
+  const Unit u = find_unit<kRows, true>(a, a.cu_q, a.q_pitch, a.q_rows, tile / a.hq);
   const SeqRange& s = u.s;
   const int64_t r0 = (int64_t)u.tile * kRows;  // first row of the workgroup in its sequence
   if (r0 >= s.n) return;
@@ -477,7 +481,9 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(Attn a, T* __restrict__ out
   const int mine = seen_by(a, s, t);                                     // keys of the lane's row
   const int wave_lo = seen_by(a, s, r0 + wave * 32);                     // fewest and most of the wave's rows
   const int wave_hi = r0 + wave * 32 < s.n ? seen_by(a, s, clamp64(r0 + wave * 32 + 31, 0, s.n - 1)) : 0;
-  const int steps = (seen_by(a, s, clamp64(r0 + kRows - 1, 0, s.n - 1)) + KT - 1) / KT;
+  const int total = (seen_by(a, s, clamp64(r0 + kRows - 1, 0, s.n - 1)) + KT - 1) / KT;
+  const int from = SPLIT ? (int)((int64_t)total * part / parts) : 0;
+  const int steps = SPLIT ? (int)((int64_t)total * (part + 1) / parts) : total;  // this part's: from .. steps - 1
   Ld lk, lv;
   lk.init(tid, a.k_rs);
   lv.init(tid, a.v_rs);
@@ -503,11 +509,11 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(Attn a, T* __restrict__ out
   using Op = Ahead<T, DH>;
   f32x16 o[Ti::kNDB] = {};
   Online st;
-  if (steps > 0) {
+  if (steps > from) {
 #pragma unroll
-    for (int i = 0; i < ST - 1; ++i) fetch(i);
+    for (int i = 0; i < ST - 1; ++i) fetch(from + i);
   }
-  for (int i = 0; i < steps; ++i) {
+  for (int i = from; i < steps; ++i) {
     wait_and_sync<(ST - 2) * kPieces>();  // tile i is there, tile i - 1 is done with
     const int j0 = i * KT;
     if (j0 >= wave_hi) {
@@ -546,10 +552,56 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(Attn a, T* __restrict__ out
   const float sum = st.sum + other_half(st.sum);
   if (live) {
     const int64_t at = (s.q0 + t) * a.hq + h;
-    store_row<T, Ti::kNDB>(out + at * a.dh, o, mine > 0 ? 1.f / sum : 0.f, a.dh, lane);
-    if (lse && lane < 32) lse[at] = finish_lse(st.used, sum, mine > 0);
+    if constexpr (SPLIT) {
+      const int64_t to = part * (a.q_rows * a.hq) + at;
+      store_row<float, Ti::kNDB>(sums + to * a.dh, o, 1.f, a.dh, lane);
+      if (lane < 32) stats[to] = make_float2(st.used, mine > 0 ? sum : -1.f);
+    } else {
+      store_row<T, Ti::kNDB>(out + at * a.dh, o, mine > 0 ? 1.f / sum : 0.f, a.dh, lane);
+      if (lse && lane < 32) lse[at] = finish_lse(st.used, sum, mine > 0);
+    }
   }
 }
+
+// Few tiles of rows leave CUs idle: the keys that a tile sees are then dealt to several workgroups, no more than two a CU
+// in all, where a part gets 512 keys or more (256 in float32, whose products take longer). One sequence of 4,096 rows, 1
+// head of 128, bf16, in 8 parts with the join: forward 74 -> 25 us, dq 98 -> 33; of 2,048, float32: 270 -> 80 and 406 ->
+// 118. Two parts of 512 bf16 keys gain nothing over one workgroup (1,024 rows, 2 heads of 64: 18 us): the join takes 4.
+int row_parts(const Attn& a) {
+  const int64_t wgs = (a.q_rows / kRows + a.seqs + 1) * a.hq, most = a.k_pitch / (a.dtype == 1 ? 512 : 256);
+  int64_t p = 512 / wgs;
+  if (p > most) p = most;
+  return (int)(most < 3 || p < 1 ? 1 : p);
+}
+
+// The parts' results of `rows` rows and heads joined in their order: 32 lanes a row, four features each.
+template <typename T>
+__global__ __launch_bounds__(256) void k_attn_fwd_join(int parts, int64_t rows, int dh, const float* __restrict__ sums,
+                                                       const float2* __restrict__ stats, T* __restrict__ out,
+                                                       float* __restrict__ lse) {
+  const int64_t r = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
+  const int d = threadIdx.x % 32 * 4;
+  if (r >= rows || d >= dh) return;
+  const bool any = stats[r].y >= 0.f || stats[r].y != stats[r].y;
+  float mx = -INFINITY, sum = 0.f;
+#pragma unroll 4
+  for (int p = 0; p < parts; ++p) mx = fmaxf(mx, stats[p * rows + r].x);
+  f32x4 x = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int p = 0; p < parts; ++p) {
+    const float2 t = stats[p * rows + r];
+    const float f = t.x == -INFINITY ? 0.f : exp2_of(t.x - mx);
+    sum += f * t.y;
+    x += f * *(const f32x4*)(sums + (p * rows + r) * dh + d);
+  }
+  typedef T V4 __attribute__((ext_vector_type(4)));
+  V4 y;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) y[j] = (T)(x[j] * (any ? 1.f / sum : 0.f));
+  *(V4*)(out + r * dh + d) = y;
+  if (lse && d == 0) lse[r] = finish_lse(mx, sum, any);
+}
+
 
 // dq, and the rows' (lse in base 2, delta) for dk and dv: the forward's layout and loop. At the forward's sizes 365 us
 // (matrix unit busy 53%, vector issue 41%) and 16 us. delta is needed from the first key on. dO . out with the rounded
@@ -558,18 +610,22 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(Attn a, T* __restrict__ out
 // all at once (256 keys, 128 at head_dim over 64), a first pass over them there sums P dP in float32 instead: dq off by
 // 0.23%, 14 -> 16 us at 128 sequences of up to 200. The workgroups with more keys take dO . out (their rows then add
 // little: 0.24% at any length); what it is off by is the sum of a row's dS in float32, and dk gets it added.
-template <typename T, int DH>
+//
+// SPLIT: `parts` workgroups for each tile of rows and head, as in the forward; they leave their sums (of dS in off) for
+// k_attn_dq_join. The first one takes all of the keys where they fit into LDS.
+template <typename T, int DH, bool SPLIT>
 __global__ __launch_bounds__(256, sizeof(T) == 4 && DH > 64 ? 1 : 2) void k_attn_dq(
-    Attn a, const T* __restrict__ dout, const T* __restrict__ out, const float* __restrict__ lse,
-    T* __restrict__ dq, float2* __restrict__ stat) {
+    Attn a, int parts, const T* __restrict__ dout, const T* __restrict__ out, const float* __restrict__ lse,
+    T* __restrict__ dq, float2* __restrict__ stat, float* __restrict__ sums, float* __restrict__ off) {
   using Ti = Tile<T, DH>;
   constexpr int KT = key_tile<T, DH>(), NS = KT / 32, ST = key_stages<T, DH>();
   using Ld = Dma<T, DH, KT, 256>;
   extern __shared__ __align__(1024) char lds[];
   const uint32_t lds0 = uni((uint32_t)(size_t)(CUTBCE_LDS char*)lds);
   const int tid = threadIdx.x, wave = uni(tid / 64), lane = tid % 64;
-  const int h = blockIdx.x % a.hq;
-  const Unit u = find_unit<kRows, true>(a, a.cu_q, a.q_pitch, a.q_rows, blockIdx.x / a.hq);
+  const unsigned part = SPLIT ? blockIdx.x % parts : 0, tile = SPLIT ? blockIdx.x / parts : blockIdx.x;
+  const int h = tile % a.hq;
+  const Unit u = find_unit<kRows, true>(a, a.cu_q, a.q_pitch, a.q_rows, tile / a.hq);
   const SeqRange& s = u.s;
   const int64_t r0 = (int64_t)u.tile * kRows;
   if (r0 >= s.n) return;
@@ -588,7 +644,13 @@ __global__ __launch_bounds__(256, sizeof(T) == 4 && DH > 64 ? 1 : 2) void k_attn
   const T* v = (const T*)a.v + s.vb + (h / a.group) * a.v_hs;
   const int wave_lo = seen_by(a, s, r0 + wave * 32);
   const int wave_hi = r0 + wave * 32 < s.n ? seen_by(a, s, clamp64(r0 + wave * 32 + 31, 0, s.n - 1)) : 0;
-  const int steps = (seen_by(a, s, clamp64(r0 + kRows - 1, 0, s.n - 1)) + KT - 1) / KT;
+  const int total = (seen_by(a, s, clamp64(r0 + kRows - 1, 0, s.n - 1)) + KT - 1) / KT;
+  const bool all = sizeof(T) == 2 && total <= ST;  // delta from all of the keys
+  int from = 0, steps = total;                     // this part's: from .. steps - 1
+  if constexpr (SPLIT) {
+    from = all ? 0 : (int)((int64_t)total * part / parts);
+    steps = all ? (part == 0 ? total : 0) : (int)((int64_t)total * (part + 1) / parts);
+  }
   Ld lk, lv;
   lk.init(tid, a.k_rs);
   lv.init(tid, a.v_rs);
@@ -613,14 +675,12 @@ __global__ __launch_bounds__(256, sizeof(T) == 4 && DH > 64 ? 1 : 2) void k_attn
   };
   using Op = Ahead<T, DH>;
   f32x16 acc[Ti::kNDB] = {};
-  if (steps > 0) {
+  if (steps > from) {
 #pragma unroll
-    for (int i = 0; i < ST - 1; ++i) fetch(i);
+    for (int i = 0; i < ST - 1; ++i) fetch(from + i);
   }
   float delta = 0.f;
-  bool all = false;  // delta from all of the keys
   if constexpr (sizeof(T) == 2) {
-    all = steps <= ST;
     if (all && steps > 0) {
       fetch(ST - 1);
       wait_and_sync<>();
@@ -652,7 +712,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 4 && DH > 64 ? 1 : 2) void k_attn
     }
   }
   delta += other_half(delta);
-  for (int i = 0; i < steps; ++i) {
+  for (int i = from; i < steps; ++i) {
     wait_and_sync<(ST - 2) * kPieces>();  // tile i is there, tile i - 1 is done with
     const int j0 = i * KT;
     if (j0 >= wave_hi) {
@@ -695,10 +755,44 @@ __global__ __launch_bounds__(256, sizeof(T) == 4 && DH > 64 ? 1 : 2) void k_attn
   wait_and_sync<>();  // no load may reach LDS after the workgroup's end
   off_by += other_half(off_by);
   if (live) {
-    store_row<T, Ti::kNDB>(dq + at * a.dh, acc, a.scale, a.dh, lane);
-    if (lane < 32) stat[(int64_t)h * a.q_rows + s.q0 + t] = make_float2(L, delta + off_by);
+    const int64_t st = (int64_t)h * a.q_rows + s.q0 + t;
+    if constexpr (SPLIT) {
+      const int64_t n = a.q_rows * a.hq;
+      store_row<float, Ti::kNDB>(sums + (part * n + at) * a.dh, acc, a.scale, a.dh, lane);
+      if (lane < 32) {
+        off[part * n + st] = off_by;
+        if (part == 0) stat[st] = make_float2(L, delta);
+      }
+    } else {
+      store_row<T, Ti::kNDB>(dq + at * a.dh, acc, a.scale, a.dh, lane);
+      if (lane < 32) stat[st] = make_float2(L, delta + off_by);
+    }
   }
 }
+
+// The parts' sums in their order, for n elements of dq, four a thread (blockIdx.y == 0), and the delta of n / dh rows.
+template <typename T>
+__global__ __launch_bounds__(256) void k_attn_dq_join(int parts, int64_t n, int dh, const float* __restrict__ sums,
+                                                      const float* __restrict__ off, T* __restrict__ dq,
+                                                      float2* __restrict__ stat) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, rows = n / dh;
+  if (blockIdx.y == 0) {
+    if (i * 4 >= n) return;
+    f32x4 x = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int p = 0; p < parts; ++p) x += *(const f32x4*)(sums + p * n + i * 4);
+    typedef T V4 __attribute__((ext_vector_type(4)));
+    V4 y;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) y[j] = (T)x[j];
+    *(V4*)(dq + i * 4) = y;
+  } else if (i < rows) {
+    float x = 0.f;
+    for (int p = 0; p < parts; ++p) x += off[p * rows + i];
+    stat[i].y += x;
+  }
+}
+
 
 // How the dk/dv kernel lays out a workgroup: 64 keys, two waves for each 32 of them and each of the RS row blocks of
 // a stage (32 RS rows of q and dO with their lse and delta; four stages), and P from the first wave of a pair to the
@@ -1234,11 +1328,22 @@ template <typename T, int DH> hipError_t forward_t(const Attn& a, void* out, flo
                                                                                    (const float*)ws);
     return hipGetLastError();
   }
-  const int64_t units = units_of(a.q_rows, a.seqs);
+  const unsigned units = (unsigned)(units_of(a.q_rows, a.seqs) * a.hq);
   const int bytes = 2 * key_stages<T, DH>() * key_tile<T, DH>() * Ti::kRowB;
-  const hipError_t e = allow_lds<k_attn_fwd<T, DH>>(bytes);
-  if (e != hipSuccess) return e;
-  k_attn_fwd<T, DH><<<dim3((unsigned)(units * a.hq)), dim3(256), bytes, st>>>(a, (T*)out, lse);
+  const int parts = row_parts(a);
+  if (parts == 1) {
+    const hipError_t e = allow_lds<k_attn_fwd<T, DH, false>>(bytes);
+    if (e != hipSuccess) return e;
+    k_attn_fwd<T, DH, false><<<dim3(units), dim3(256), bytes, st>>>(a, 1, (T*)out, lse, nullptr, nullptr);
+  } else {
+    const hipError_t e = allow_lds<k_attn_fwd<T, DH, true>>(bytes);
+    if (e != hipSuccess) return e;
+    const int64_t rows = a.q_rows * a.hq;
+    float* sums = (float*)ws;
+    float2* stats = (float2*)(sums + parts * rows * a.dh);
+    k_attn_fwd<T, DH, true><<<dim3(units * parts), dim3(256), bytes, st>>>(a, parts, (T*)out, lse, sums, stats);
+    k_attn_fwd_join<T><<<dim3((unsigned)cdiv(rows, 8)), dim3(256), 0, st>>>(parts, rows, a.dh, sums, stats, (T*)out, lse);
+  }
   return hipGetLastError();
 }
 
@@ -1250,12 +1355,23 @@ hipError_t backward_t(const Attn& a, const void* dout, const void* out, const fl
   using Ti = Tile<T, DH>;
   float2* stat = (float2*)ws;
   if (a.q_rows) {
-    const int64_t units = units_of(a.q_rows, a.seqs);
+    const unsigned units = (unsigned)(units_of(a.q_rows, a.seqs) * a.hq);
     const int bytes = 2 * key_stages<T, DH>() * key_tile<T, DH>() * Ti::kRowB;
-    const hipError_t e = allow_lds<k_attn_dq<T, DH>>(bytes);
-    if (e != hipSuccess) return e;
-    k_attn_dq<T, DH><<<dim3((unsigned)(units * a.hq)), dim3(256), bytes, st>>>(a, (const T*)dout, (const T*)out, lse,
-                                                                              (T*)dq, stat);
+    const int parts = row_parts(a);
+    if (parts == 1) {
+      const hipError_t e = allow_lds<k_attn_dq<T, DH, false>>(bytes);
+      if (e != hipSuccess) return e;
+      k_attn_dq<T, DH, false><<<dim3(units), dim3(256), bytes, st>>>(a, 1, (const T*)dout, (const T*)out, lse, (T*)dq,
+                                                                    stat, nullptr, nullptr);
+    } else {
+      const hipError_t e = allow_lds<k_attn_dq<T, DH, true>>(bytes);
+      if (e != hipSuccess) return e;
+      const int64_t n = a.q_rows * a.hq * a.dh;
+      float *sums = (float*)(ws + stat_bytes(a)), *off = sums + parts * n;
+      k_attn_dq<T, DH, true><<<dim3(units * parts), dim3(256), bytes, st>>>(a, parts, (const T*)dout, (const T*)out, lse,
+                                                                           (T*)dq, stat, sums, off);
+      k_attn_dq_join<T><<<dim3((unsigned)cdiv(n, 1024), 2), dim3(256), 0, st>>>(parts, n, a.dh, sums, off, (T*)dq, stat);
+    }
   }
   if (a.k_rows) {
     using K = Dkv<T, DH>;
@@ -1293,13 +1409,18 @@ hipError_t backward_t(const Attn& a, const void* dout, const void* out, const fl
 
 }  // namespace
 
+// (whether a forward is one of few rows depends on its arrays too: the size covers both)
 size_t attention_bytes(const Attn& a, bool backward) {
-  if (backward) {
-    const int parts = dkv_parts(a);
-    return stat_bytes(a) + (parts > 1 ? (size_t)parts * 2 * a.k_rows * a.hk * a.dh * sizeof(float) : 0);
+  const size_t rows = (size_t)a.q_rows * a.hq, keys = (size_t)a.k_rows * a.hk;
+  const int parts = row_parts(a), kparts = dkv_parts(a);
+  // each part's sums, and two floats a row (the forward) or one (dq)
+  const size_t by_rows = parts > 1 ? parts * rows * (a.dh + 2) * sizeof(float) : 0;
+  if (backward) {  // dq's are read before those of dk and dv are written
+    const size_t by_keys = kparts > 1 ? kparts * 2 * keys * a.dh * sizeof(float) : 0;
+    return stat_bytes(a) + (by_rows > by_keys ? by_rows : by_keys);
   }
-  // (whether the call is one of few rows depends on its arrays too: the size covers both)
-  return a.q_rows % a.seqs == 0 && a.q_pitch * a.group <= kCols ? few_bytes(a) : 0;
+  const size_t few = a.q_rows % a.seqs == 0 && a.q_pitch * a.group <= kCols ? few_bytes(a) : 0;
+  return few > by_rows ? few : by_rows;
 }
 
 hipError_t launch_attention_forward(const Attn& a, void* out, float* lse, char* ws, hipStream_t st) {
