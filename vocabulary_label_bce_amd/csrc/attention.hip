@@ -565,8 +565,8 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(Attn a, int parts, T* __res
 
 // Few tiles of rows leave CUs idle: the keys that a tile sees are then dealt to several workgroups, no more than two a CU
 // in all, where a part gets 512 keys or more (256 in float32, whose products take longer). One sequence of 4,096 rows, 1
-// head of 128, bf16, in 8 parts with the join: forward 74 -> 25 us, dq 98 -> 33; of 2,048, float32: 270 -> 80 and 406 ->
-// 118. Two parts of 512 bf16 keys gain nothing over one workgroup (1,024 rows, 2 heads of 64: 18 us): the join takes 4.
+// head of 128, bf16, in 8 parts with the join: forward 74 -> 25 us, dq 98 -> 33; of 2,048, float32: 270 -> 49 and 406 ->
+// 71. Two parts of 512 bf16 keys gain nothing over one workgroup (1,024 rows, 2 heads of 64: 18 us): the join takes 4.
 int row_parts(const Attn& a) {
   const int64_t wgs = (a.q_rows / kRows + a.seqs + 1) * a.hq, most = a.k_pitch / (a.dtype == 1 ? 512 : 256);
   int64_t p = 512 / wgs;
