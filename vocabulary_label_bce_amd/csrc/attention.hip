@@ -60,8 +60,9 @@ template <typename T, int DH> struct Tile {
   static constexpr int kNT = DH * kEsz / 32;  // pairs of chunks: k-steps of a product over the features
   static constexpr int kNDB = DH / 32;        // 32-wide blocks of features
   // LDS has 64 banks, 256 bytes: a row-wise read takes one chunk of 16 rows at a time, a transpose read four chunks of
-  // four rows (from a multiple of 4), a float32 transposed read 128 bytes of rows r and r + 4. The row's bits are dealt to
-  // the chunk's so that each of these covers the banks once. (Dealt for 32 banks the transpose reads took twice as long.)
+  // four rows (from a multiple of 4), a float32 transposed read 128 bytes of rows r and r + 4. The row's bits are dealt
+  // to the chunk's so that each of these covers the banks once. (Dealt for 32 banks the transpose reads took twice as
+  // long.)
   __device__ static inline int swz(int r) {
     if constexpr (kCPR == 4) return (r >> 2) & 3;
     else if constexpr (kCPR == 8) return ((r >> 1) & 1) << 2 | ((r >> 2) & 3);
@@ -325,9 +326,9 @@ template <typename T, int NDB> __device__ inline void store_row(T* row, const f3
 // longest workgroup has as many steps as each of the 512 places gets in all, took 313 us with the sequences one after
 // another and 275 so.
 //
-// More sequences than a wave has lanes for: sequence b's tiles start at unit start(b) / M + b, which leaves room for each
-// of them (a range of n rows spans at least ceil(n / M) of these numbers), so that no running total is needed; the lanes
-// look at 64 sequences at a time.
+// More sequences than a wave has lanes for: sequence b's tiles start at unit start(b) / M + b, which leaves room for
+// each of them (a range of n rows spans at least ceil(n / M) of these numbers), so that no running total is needed; the
+// lanes look at 64 sequences at a time.
 struct Unit {
   SeqRange s;
   int tile;  // tile of the sequence; may lie behind its end
@@ -443,13 +444,14 @@ __device__ inline float finish_lse(float used, float sum, bool any) {
 
 // Forward: a workgroup has 128 rows of one sequence and head, a wave 32 of them; the keys stream through LDS stages of
 // KT keys, shared by the four waves. Two workgroups a CU (registers), so that a SIMD has a wave of each: one's softmax
-// beside the other's products. 4 sequences of up to 8,192 rows, 8 heads over 2 of 128, bf16: 260 us, about 990 TFLOP/s of the
-// seen pairs; the matrix unit is busy 48% of the cycles and vector instructions issue in 41%, so a wave's chain of
-// scores, softmax and product bounds it, and the tail of the longest sequences. 128 sequences of up to 200 rows, 2
+// beside the other's products. 4 sequences of up to 8,192 rows, 8 heads over 2 of 128, bf16: 260 us, about 990 TFLOP/s
+// of the seen pairs; the matrix unit is busy 48% of the cycles and vector instructions issue in 41%, so a wave's chain
+// of scores, softmax and product bounds it, and the tail of the longest sequences. 128 sequences of up to 200 rows, 2
 // heads of 64: 11 us, latency (search, first tiles, up to four steps).
 //
-// SPLIT: `parts` workgroups for each tile of rows and head, with a share of its steps each (row_parts); they leave their
-// sums and, for each row, the maximum and sum of its exponentials (-1 for a row that sees no key) for k_attn_fwd_join.
+// SPLIT: `parts` workgroups for each tile of rows and head, with a share of its steps each (row_parts); they leave
+// their sums and, for each row, the maximum and sum of its exponentials (-1 for a row that sees no key) for
+// k_attn_fwd_join.
 template <typename T, int DH, bool SPLIT>
 __global__ __launch_bounds__(256, 2) void k_attn_fwd(Attn a, int parts, T* __restrict__ out, float* __restrict__ lse,
                                                      float* __restrict__ sums, float2* __restrict__ stats) {
@@ -563,10 +565,11 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(Attn a, int parts, T* __res
   }
 }
 
-// Few tiles of rows leave CUs idle: the keys that a tile sees are then dealt to several workgroups, no more than two a CU
-// in all, where a part gets 512 keys or more (256 in float32, whose products take longer). One sequence of 4,096 rows, 1
-// head of 128, bf16, in 8 parts with the join: forward 74 -> 25 us, dq 98 -> 33; of 2,048, float32: 270 -> 49 and 406 ->
-// 71. Two parts of 512 bf16 keys gain nothing over one workgroup (1,024 rows, 2 heads of 64: 18 us): the join takes 4.
+// Few tiles of rows leave CUs idle: the keys that a tile sees are then dealt to several workgroups, no more than two a
+// CU in all, where a part gets 512 keys or more (256 in float32, whose products take longer). One sequence of 4,096
+// rows, 1 head of 128, bf16, in 8 parts with the join: forward 74 -> 25 us, dq 98 -> 33; of 2,048, float32: 270 -> 49
+// and 406 -> 71. Two parts of 512 bf16 keys gain nothing over one workgroup (1,024 rows, 2 heads of 64: 18 us): the
+// join takes 4.
 int row_parts(const Attn& a) {
   const int64_t wgs = (a.q_rows / kRows + a.seqs + 1) * a.hq, most = a.k_pitch / (a.dtype == 1 ? 512 : 256);
   int64_t p = 512 / wgs;
@@ -605,11 +608,12 @@ __global__ __launch_bounds__(256) void k_attn_fwd_join(int parts, int64_t rows, 
 
 // dq, and the rows' (lse in base 2, delta) for dk and dv: the forward's layout and loop. At the forward's sizes 365 us
 // (matrix unit busy 53%, vector issue 41%) and 16 us. delta is needed from the first key on. dO . out with the rounded
-// out is off by out's rounding, which few keys leave as large as dS itself (bf16: dq off by 0.33% of its norm at 4 keys,
-// 0.28% at 16, 0.25% from 256 on; 0.23% is the rounding of dS and dq). So where a workgroup's keys fit into the LDS stages
-// all at once (256 keys, 128 at head_dim over 64), a first pass over them there sums P dP in float32 instead: dq off by
-// 0.23%, 14 -> 16 us at 128 sequences of up to 200. The workgroups with more keys take dO . out (their rows then add
-// little: 0.24% at any length); what it is off by is the sum of a row's dS in float32, and dk gets it added.
+// out is off by out's rounding, which few keys leave as large as dS itself (bf16: dq off by 0.33% of its norm at 4
+// keys, 0.28% at 16, 0.25% from 256 on; 0.23% is the rounding of dS and dq). So where a workgroup's keys fit into the
+// LDS stages all at once (256 keys, 128 at head_dim over 64), a first pass over them there sums P dP in float32
+// instead: dq off by 0.23%, 14 -> 16 us at 128 sequences of up to 200. The workgroups with more keys take dO . out
+// (their rows then add little: 0.24% at any length); what it is off by is the sum of a row's dS in float32, and dk gets
+// it added.
 //
 // SPLIT: `parts` workgroups for each tile of rows and head, as in the forward; they leave their sums (of dS in off) for
 // k_attn_dq_join. The first one takes all of the keys where they fit into LDS.
@@ -849,10 +853,11 @@ template <bool PACK> __device__ inline float get_p(const u32x4* p, int e) {
 // head_dim 128, one wave per SIMD, and half of them in accumulation registers that vector instructions cannot reach:
 // 1.33 ms at 4 x 8192). So a pair of waves shares 32 keys: the first has k and dv (scores, P, P^T dO), the second v
 // and dk (dP, dS, dS^T Q) one tile behind, with P handed over in LDS. Two waves per SIMD, one of each kind, hide each
-// other's latencies: 600 us (matrix unit busy 38%; the chain of a turn, scores to P to product, is covered only in part by
-// the other wave), 16 us at 128 sequences of up to 200. Where four stages leave too little room for two P's of each pair in float32, its upper 24 bits
-// are handed over: an error of 2^-16, under a hundredth of dS's rounding to bf16. (One P, with a second barrier before
-// it is overwritten, was slower; float16 loses what is under 2^-38 of a row's sum.)
+// other's latencies: 620 us (matrix unit busy 38%; the chain of a turn, scores to P to product, is covered only in part
+// by the other wave), 16 us at 128 sequences of up to 200. Where four stages leave too little room for two P's of each
+// pair in float32, its upper 24 bits are handed over: an error of 2^-16, under a hundredth of dS's rounding to bf16.
+// (One P, with a second barrier before it is overwritten, was slower; float16 loses what is under 2^-38 of a row's
+// sum.)
 //
 // SPLIT: `parts` workgroups for each key tile and head, with a share of its steps each (dkv_parts).
 template <typename T, int DH, bool SPLIT>
@@ -938,7 +943,8 @@ __global__ __launch_bounds__((Dkv<T, DH>::kThreads), 2) void k_attn_dkv(Attn a, 
   if (steps > 0) {
     using Op = Ahead<T, DH>;
     Op op;
-    // beside the first product: the second one's operands, and the loads of tile i + 2; beside the second: the next rows
+    // beside the first product: the second one's operands, and the loads of tile i + 2; beside the second: the next
+    // rows
     auto beside = [&](int k, uint32_t at) {
       spread(k, Op::NT, Op::S, [&](int e) { op.col(e, at); });
       spread(k, Op::NT, kPieces, piece);
@@ -1032,10 +1038,10 @@ __global__ __launch_bounds__((Dkv<T, DH>::kThreads), 2) void k_attn_dkv(Attn a, 
   }
 }
 
-// Few key tiles leave CUs idle: the rows (and heads) that a tile meets are then dealt to several workgroups, which leave
-// their sums in the workspace for k_attn_dkv_join. At least 256 rows each (fewer are mostly start-up), and no more
-// workgroups than two a CU in all. One sequence of 4,096 rows, 8 heads over 1 of 128, bf16: 491 us whole, 111
-// in 7 parts with the join; of 2,048, 1 head of 128, float32: 293 and 59; of 600, 2 heads over 1 of 64, bf16: 31 and 18.
+// Few key tiles leave CUs idle: the rows (and heads) that a tile meets are then dealt to several workgroups, which
+// leave their sums in the workspace for k_attn_dkv_join. At least 256 rows each (fewer are mostly start-up), and no
+// more workgroups than two a CU in all. One sequence of 4,096 rows, 8 heads over 1 of 128, bf16: 491 us whole, 111 in 7
+// parts with the join; of 2,048, 1 head of 128, float32: 293 and 59; of 600, 2 heads over 1 of 64, bf16: 31 and 18.
 int dkv_parts(const Attn& a) {
   const int64_t wgs = (a.k_rows / 64 + a.seqs + 1) * a.hk, most = a.q_pitch * a.group / 256;
   int64_t p = 512 / wgs;
@@ -1065,16 +1071,16 @@ __global__ __launch_bounds__(256) void k_attn_dkv_join(int parts, int64_t n, con
 // waves take 32-key blocks in turn, each through an LDS ring of its own (no barriers), and join their results in
 // LDS. With more than one part, the parts leave (out, max, sum) in the workspace and k_attn_join joins them in order.
 //
-// Bound by the cache's bytes: 16 ranges of up to 32,768 keys, 16 heads over 2 of 128, bf16 (403 MB): 80 us, 5.0 TB/s, and
-// 4.7 for the join. A workgroup has as many waves as let two of them share a CU's LDS: two of two waves took 81 us there,
-// one of four 86. 128 ranges of up to 200 keys, 2 heads of 64: 7.2 us (lengths, first tiles, two blocks a wave, the
-// waves' join).
+// Bound by the cache's bytes: 16 ranges of up to 32,768 keys, 16 heads over 2 of 128, bf16 (403 MB): 80 us, 5.0 TB/s,
+// and 4.7 for the join. A workgroup has as many waves as let two of them share a CU's LDS: two of two waves took 81 us
+// there, one of four 86. 128 ranges of up to 200 keys, 2 heads of 64: 7.2 us (lengths, first tiles, two blocks a wave,
+// the waves' join).
 //
 // bf16 rings have two stages of 32 keys, K and V each. A float32 block keeps the matrix unit busy for about as long as
 // its bytes take (32 columns, however few are used), so more waves matter more than more loads in flight: one stage,
 // where K of the next block is loaded from the end of the scores on and V from the end of the second product on. 16
-// ranges of up to 16,384 keys, 16 heads over 2 of 128 (403 MB): 157 us with two stages and one wave, 105 with one and two
-// (3.8 TB/s); 4 heads over 2 of 64: 76 and 53; 100 ranges of up to 200, 2 heads of 128: 37 and 25.
+// ranges of up to 16,384 keys, 16 heads over 2 of 128 (403 MB): 157 us with two stages and one wave, 105 with one and
+// two (3.8 TB/s); 4 heads over 2 of 64: 76 and 53; 100 ranges of up to 200, 2 heads of 128: 37 and 25.
 
 constexpr int kCols = 32;
 

@@ -96,8 +96,8 @@ __global__ __launch_bounds__(256) void k_embed(int64_t n, int V, int D, int lpr,
 // The gradient's table is cleared by the sorting kernels, whose own work fills few CUs and is all latency: the
 // workgroups behind the sorting ones clear a share of it each. At 876,000 x 128 bf16 (224 MB) and 25,600 ids the
 // six launches take 49 us; with the table cleared before them it was 28 us more. At 262,144 x 512 float32 (537 MB) and
-// 12,289 ids they take 94 us, 5.7 TB/s. The stores go past the caches: at 262,144 x 512 float32 (537 MB) the lookup and the row
-// sums around them then still find their rows there (13 -> 8 us each).
+// 12,289 ids they take 94 us, 5.7 TB/s. The stores go past the caches: at 262,144 x 512 float32 (537 MB) the lookup and
+// the row sums around them then still find their rows there (13 -> 8 us each).
 struct Fill {
   char* p;          // of this launch's share
   int64_t bytes;    // 0: nothing to clear
@@ -275,8 +275,8 @@ template <int N> __device__ inline void store_sums(float* row, int c, int D, con
 // One lane group per chunk of kChunk sorted pairs (and per lpr * N columns: blockIdx.y). An item whose pairs are all
 // in the chunk is written; the sum of the first item, where it began earlier, goes to part[chunk][0], that of the
 // last, where it began here and goes on, to part[chunk][1]. The chunk's rows are loaded together before they are
-// added: with one row after another the kernel took 39 us at 25,600 x 128 bf16, so 7.1 (6.6 MB read: latency; at 12,289 x
-// 512 float32, 25 MB, 7.8).
+// added: with one row after another the kernel took 39 us at 25,600 x 128 bf16, so 7.1 (6.6 MB read: latency; at 12,289
+// x 512 float32, 25 MB, 7.8).
 template <typename T>
 __global__ __launch_bounds__(256) void k_embed_grad(int64_t n, int V, int D, int lpr, const int* __restrict__ keys,
                                                     const int* __restrict__ pos, const T* __restrict__ dout,

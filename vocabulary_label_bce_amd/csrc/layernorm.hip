@@ -63,9 +63,10 @@ __device__ inline void group_sum(float& a, float& b, int G, float (*sh)[2]) {
   }
 }
 
-// Forward. C chunks of N elements a lane: chunk k of lane s covers the columns (k * G + s) * N .. + N - 1. 65,536 x 2048
-// bf16 (64 lanes of 32): 122 us, 4.4 TB/s read and written (a large copy 4.9); lanes of 16 elements, two waves a row, 157.
-// 25,600 x 128: 7.1 us, 1.8 TB/s, start-up and two rounds of exchanges. 32 x 64: 2.4 us (an empty kernel 1.4).
+// Forward. C chunks of N elements a lane: chunk k of lane s covers the columns (k * G + s) * N .. + N - 1. 65,536 x
+// 2048 bf16 (64 lanes of 32): 122 us, 4.4 TB/s read and written (a large copy 4.9); lanes of 16 elements, two waves a
+// row, 157. 25,600 x 128: 7.1 us, 1.8 TB/s, start-up and two rounds of exchanges. 32 x 64: 2.4 us (an empty kernel
+// 1.4).
 template <typename T, typename P, int C>
 __global__ __launch_bounds__(kThreads) void k_norm(int64_t rows, int D, int G, const T* __restrict__ x, int64_t xs,
                                                    const P* __restrict__ w, const P* __restrict__ b, float eps,
@@ -116,9 +117,9 @@ __global__ __launch_bounds__(kThreads) void k_norm(int64_t rows, int D, int G, c
 
 // One pass over a workgroup's rows: dx, and its share of dw and db. PARAMS: part is wanted. 65,536 x 2048 bf16: 177 us,
 // 4.6 TB/s; 25,600 x 128: 11.6 us and 4,097 x 1000 float32: 18.5 us (2.7 TB/s), where a group's two rows come one
-// after another, a latency each, with the sums over the groups behind them (workgroups of fewer rows leave more partials
-// to join: k_norm_join reads 2 D floats of each, 10 us at 1,536 x 2 x 2048, 4 us at the smaller sizes). Loading a row
-// ahead of its turn: 18.9 us and, for the registers, 258 instead of 174 at 65,536 x 2048.
+// after another, a latency each, with the sums over the groups behind them (workgroups of fewer rows leave more
+// partials to join: k_norm_join reads 2 D floats of each, 10 us at 1,536 x 2 x 2048, 4 us at the smaller sizes).
+// Loading a row ahead of its turn: 18.9 us and, for the registers, 258 instead of 174 at 65,536 x 2048.
 template <typename T, typename P, int C, bool PARAMS>
 __global__ __launch_bounds__(kThreads) void k_norm_grad(int64_t rows, int D, int G, const T* __restrict__ dy,
                                                         int64_t dys, const T* __restrict__ x, int64_t xs,
@@ -207,8 +208,8 @@ __global__ __launch_bounds__(kThreads) void k_norm_grad(int64_t rows, int D, int
   for (int c = threadIdx.x; c < 2 * D; c += kThreads) p[c] = acc[c];
 }
 
-// Rows of any width, a workgroup each, read three times, the second and third from the caches (a row of 8,193 float32 is
-// 33 KB, and a workgroup reads its own row only).
+// Rows of any width, a workgroup each, read three times, the second and third from the caches (a row of 8,193 float32
+// is 33 KB, and a workgroup reads its own row only).
 template <typename T, typename P>
 __global__ __launch_bounds__(kThreads) void k_norm_wide(int D, const T* __restrict__ x, int64_t xs,
                                                         const P* __restrict__ w, const P* __restrict__ b, float eps,
