@@ -1,0 +1,54 @@
+"""What autograd is told about the sequence encoder's operators. Only the launches are replaced here (they leave their
+outputs as they are), so this runs without a GPU: it is about which calls are refused, not about values."""
+import pytest
+import torch
+from torch.autograd import forward_ad
+
+from vocabulary_label_bce_amd import binding as B
+from vocabulary_label_bce_amd import encoder as E
+from vocabulary_label_bce_amd import ops
+
+
+@pytest.fixture(autouse=True)
+def _no_launches(monkeypatch):
+    monkeypatch.setattr(E, "_on_gpu", lambda what, *tensors: 0)
+    monkeypatch.setattr(B, "raw_stream", lambda device: 0)
+    for name in ("embedding_forward", "embedding_backward", "layer_norm_forward", "layer_norm_backward",
+                 "attention_forward", "attention_backward"):
+        monkeypatch.setattr(B, name, lambda *a: None)
+
+
+IDS = torch.tensor([1, 0, 3], dtype=torch.int32)
+CU = torch.tensor([0, 4], dtype=torch.int32)
+
+# name: (the inputs that a derivative may be taken of, the call)
+CALLS = {
+    "embedding": ([(5, 8)], lambda table: ops.embedding(IDS, table, 2.0)),
+    "layer_norm": ([(4, 8), (8,), (8,)], ops.layer_norm),
+    "packed_attention": ([(4, 2, 8), (4, 1, 8), (4, 1, 8)], lambda q, k, v: ops.packed_attention(q, k, v, CU)),
+}
+EACH = [(name, i) for name, (shapes, _) in CALLS.items() for i in range(len(shapes))]
+
+
+@pytest.mark.parametrize("name,i", EACH)
+@pytest.mark.parametrize("grad", [True, False])
+def test_forward_mode_is_refused(name, i, grad):
+    """There is no forward-mode derivative: a dual input raises, instead of giving an output without a tangent."""
+    shapes, call = CALLS[name]
+    x = [torch.ones(s) for s in shapes]
+    with forward_ad.dual_level(), torch.set_grad_enabled(grad):
+        call(*x)  # without a tangent there is nothing to refuse
+        x[i] = forward_ad.make_dual(x[i], torch.ones_like(x[i]))
+        with pytest.raises(NotImplementedError, match="jvp"):
+            call(*x)
+
+
+@pytest.mark.parametrize("i", [0, 1, 2])
+def test_forward_mode_is_refused_where_there_is_no_gradient_at_all(i):
+    x = [torch.ones(2, 2, 8), torch.ones(2, 6, 1, 8), torch.ones(2, 6, 1, 8)]
+    lens = torch.tensor([6, 3], dtype=torch.int32)
+    with forward_ad.dual_level():
+        ops.cached_attention(*x, lens)
+        x[i] = forward_ad.make_dual(x[i], torch.ones_like(x[i]))
+        with pytest.raises(ValueError, match="no gradient"):
+            ops.cached_attention(*x, lens)

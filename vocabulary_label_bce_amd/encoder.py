@@ -1,7 +1,8 @@
 """PyTorch front end of the sequence encoder's operators: what turns item ids into the hidden states that ``cut_bce``
-takes. Each is differentiable (``embedding``, ``layer_norm``, ``packed_attention``) and also has explicit forward and
-backward calls for callers that keep their own tape; ``cached_attention`` serves single tokens against a key/value
-cache. The arithmetic is libcutbce.so's; PyTorch allocates outputs and workspaces and supplies the stream.
+takes. Each is differentiable in reverse mode (``embedding``, ``layer_norm``, ``packed_attention``; forward-mode
+tangents are refused) and also has explicit forward and backward calls for callers that keep their own tape;
+``cached_attention`` serves single tokens against a key/value cache. The arithmetic is libcutbce.so's; PyTorch
+allocates outputs and workspaces and supplies the stream.
 
 All tensors live on the current GPU, float32 or bfloat16. Lengths and offsets stay on the device: no call
 synchronises with the host.
@@ -11,6 +12,7 @@ from __future__ import annotations
 import math
 
 import torch
+from torch.autograd import forward_ad
 
 from . import binding as B
 
@@ -35,6 +37,18 @@ def _on_gpu(what, first, *others):
         else:
             return dev
     raise ValueError(f"{what} runs on the GPU only: its tensors must be on the current device")
+
+
+def _derived(*tensors):
+    """Whether a derivative is taken of any of these: the call then goes through its autograd function, which refuses
+    the forward mode (a direct call would return an output without a tangent)."""
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                return True
+    if forward_ad._current_level >= 0:
+        return any(t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors)
+    return False
 
 
 # ---- embedding lookup -----------------------------------------------------------------------------------------
@@ -100,7 +114,7 @@ class _Embedding(torch.autograd.Function):
 def embedding(ids, table, scale: float = 1.0):
     """Rows of an item table: scale * table[ids] (ids int32 or int64 of any shape; an id outside [0, V) gives zeros
     and no gradient). table [V, D] float32 or bfloat16; the gradient flows to the table as a dense [V, D]."""
-    if torch.is_grad_enabled() and table.requires_grad:
+    if _derived(table):
         return _Embedding.apply(ids, table, scale)
     return embedding_forward(ids, table, scale)
 
@@ -198,7 +212,7 @@ class _LayerNorm(torch.autograd.Function):
 def layer_norm(x, weight=None, bias=None, eps: float = 1e-5):
     """Layer norm over the last dimension of x [..., D]: (x - mean) / sqrt(var + eps) * weight + bias, statistics in
     float32. weight and bias [D] (float32 or bfloat16, one dtype for both) may be None. Gradients flow to all three."""
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, weight, bias)):
+    if _derived(x, weight, bias):
         return _LayerNorm.apply(x, weight, bias, eps)
     return layer_norm_forward(x, weight, bias, eps, stats=False)[0]
 
@@ -327,7 +341,7 @@ def packed_attention(q, k, v, cu_q, cu_k=None, k_lens=None, causal: bool = True,
     n sees the keys j <= t + m - n of m, so that the last row sees all of them; a row that sees none gives zeros.
     scale: 1 / sqrt(head_dim) by default. cu_q, cu_k and k_lens are int32 on the device. Gradients flow to q, k, v.
     Non-finite values in k, v or the cotangent may reach every row of their own sequence and head, and no other."""
-    if torch.is_grad_enabled() and any(t.requires_grad for t in (q, k, v)):
+    if _derived(q, k, v):
         return _PackedAttention.apply(q, k, v, cu_q, cu_k, k_lens, causal, scale)
     return packed_attention_forward(q, k, v, cu_q, cu_k, k_lens, causal, scale, want_lse=False)[0]
 
@@ -340,7 +354,7 @@ def cached_attention(q, k_cache, v_cache, lens, causal: bool = True, scale=None)
     capacity, head_dim] as well); lens [sequences] on the device: the first lens[b] rows are filled, the newest tokens'
     own keys included, and the rest is never used. Returns q's shape."""
     dev = _on_gpu("cached_attention", q, k_cache, v_cache, lens)
-    if torch.is_grad_enabled() and (q.requires_grad or k_cache.requires_grad or v_cache.requires_grad):
+    if _derived(q, k_cache, v_cache):
         raise ValueError("cached_attention has no gradient: use packed_attention, or torch.no_grad()")
     q = q.contiguous()
     seqs = k_cache.shape[0]
