@@ -52,3 +52,19 @@ def test_forward_mode_is_refused_where_there_is_no_gradient_at_all(i):
         x[i] = forward_ad.make_dual(x[i], torch.ones_like(x[i]))
         with pytest.raises(ValueError, match="no gradient"):
             ops.cached_attention(*x, lens)
+
+
+@pytest.mark.parametrize("plain", [True, False])
+@pytest.mark.parametrize("name,i", EACH)
+def test_second_derivatives_are_refused(name, i, plain):
+    """The gradients are kernels' outputs: differentiating them raises, also in a sum with a term that has a graph (a
+    gradient penalty beside a loss), instead of leaving their part out."""
+    shapes, call = CALLS[name]
+    x = [torch.ones(s) for s in shapes]
+    x[i].requires_grad_()
+    y = call(*x)
+    # a cotangent without a graph, and one with
+    (grad,) = torch.autograd.grad(y.sum() if plain else y.square().sum(), x[i], create_graph=True)
+    loss = grad.square().sum() + x[i].square().sum()
+    with pytest.raises(RuntimeError, match="first derivatives only"):
+        loss.backward()

@@ -1,14 +1,15 @@
 """PyTorch front end of the sequence encoder's operators: what turns item ids into the hidden states that ``cut_bce``
 takes. Each is differentiable in reverse mode (``embedding``, ``layer_norm``, ``packed_attention``; forward-mode
-tangents are refused) and also has explicit forward and backward calls for callers that keep their own tape;
-``cached_attention`` serves single tokens against a key/value cache. The arithmetic is libcutbce.so's; PyTorch
-allocates outputs and workspaces and supplies the stream.
+tangents and second derivatives are refused) and also has explicit forward and backward calls for callers that keep
+their own tape; ``cached_attention`` serves single tokens against a key/value cache. The arithmetic is libcutbce.so's;
+PyTorch allocates outputs and workspaces and supplies the stream.
 
 All tensors live on the current GPU, float32 or bfloat16. Lengths and offsets stay on the device: no call
 synchronises with the host.
 """
 from __future__ import annotations
 
+import functools
 import math
 
 import torch
@@ -49,6 +50,37 @@ def _derived(*tensors):
     if forward_ad._current_level >= 0:
         return any(t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors)
     return False
+
+
+class _NoSecond(torch.autograd.Function):
+    """Gradients as they are; differentiating them raises."""
+
+    @staticmethod
+    def forward(ctx, anchor, *grads):
+        return tuple(g.view_as(g) for g in grads)
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("this operator has first derivatives only: its gradients cannot be differentiated")
+
+
+def _first_order(backward):
+    """Backward of an operator without second derivatives. The kernels' outputs have no graph, so under create_graph
+    they get one that raises: without it a term that is made of them would be left out of a sum. (once_differentiable
+    does so only where the cotangent has a graph itself, which that of a plain sum has not.)"""
+
+    @functools.wraps(backward)
+    def wrapped(ctx, *cotangents):
+        graph = torch.is_grad_enabled()
+        with torch.no_grad():
+            grads = list(backward(ctx, *cotangents))
+        if graph:
+            at = [i for i, g in enumerate(grads) if g is not None]
+            for i, g in zip(at, _NoSecond.apply(torch.empty(0, requires_grad=True), *[grads[i] for i in at])):
+                grads[i] = g
+        return tuple(grads)
+
+    return wrapped
 
 
 # ---- embedding lookup -----------------------------------------------------------------------------------------
@@ -106,6 +138,7 @@ class _Embedding(torch.autograd.Function):
         return embedding_forward(ids, table, scale)
 
     @staticmethod
+    @_first_order
     def backward(ctx, dout):
         (ids,) = ctx.saved_tensors
         return None, embedding_backward(dout, ids, ctx.vocab, ctx.scale), None
@@ -202,6 +235,7 @@ class _LayerNorm(torch.autograd.Function):
         return y
 
     @staticmethod
+    @_first_order
     def backward(ctx, dy):
         x, weight, mean, rstd = ctx.saved_tensors
         need = ctx.needs_input_grad
@@ -326,6 +360,7 @@ class _PackedAttention(torch.autograd.Function):
         return out
 
     @staticmethod
+    @_first_order
     def backward(ctx, dout):
         q, k, v, out, lse, cu_q, cu_k, k_lens = ctx.saved_tensors
         return packed_attention_backward(dout, q, k, v, out, lse, cu_q, cu_k, k_lens, *ctx.how) + (None,) * 5
