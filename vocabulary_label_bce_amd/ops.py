@@ -10,6 +10,7 @@ from __future__ import annotations
 import torch
 
 from . import binding as B
+from .encoder import _first_order
 from .encoder import (cached_attention, embedding, embedding_backward, embedding_forward,  # noqa: F401
                       layer_norm, layer_norm_backward, layer_norm_forward, packed_attention,
                       packed_attention_backward, packed_attention_forward)
@@ -61,6 +62,7 @@ class _CutBCE(torch.autograd.Function):
         return loss[0]
 
     @staticmethod
+    @_first_order
     def backward(ctx, g):
         H, E, row_offsets, item_ids, row_mask, dh_saved, row_weight = ctx.saved_tensors
         p = ctx.p
