@@ -34,3 +34,14 @@ def test_second_derivatives_are_refused(launches, i, plain):
     total = grad.square().sum() + x.square().sum()
     with pytest.raises(RuntimeError, match="first derivatives only"):
         total.backward()
+
+
+def test_a_second_backward_is_computed_too(launches):
+    """The forward's workspace serves the first backward through a graph that is kept; the next one prepares its own
+    (cutbce_backward_reuse has to follow the forward)."""
+    H, E, loss = _loss()
+    for first in (True, False):
+        torch.autograd.grad(loss, (H, E), retain_graph=True)
+        kind, ws, reuse = launches[-1]
+        assert kind == "backward" and reuse == first and (ws is launches[0][1]) == first
+    assert [k for k, *_ in launches] == ["forward", "backward", "backward"]

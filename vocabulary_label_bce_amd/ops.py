@@ -70,9 +70,10 @@ class _CutBCE(torch.autograd.Function):
         dH = torch.empty_like(H) if ctx.needs_input_grad[0] else None
         dE = torch.empty_like(E) if ctx.needs_input_grad[1] else None
         ws, ctx.ws = ctx.ws, None
-        if (dH is not None or dE is not None) and ws is not None:
-            B.backward(p, H, E, row_offsets, item_ids, row_mask, g, dh_saved, dH, dE, ws, row_weight=row_weight,
-                       reuse=True)
+        if dH is not None or dE is not None:
+            reuse = ws is not None  # else the graph was kept and this is not its first backward
+            B.backward(p, H, E, row_offsets, item_ids, row_mask, g, dh_saved, dH, dE,
+                       ws if reuse else B.alloc_workspace(p, H.device), row_weight=row_weight, reuse=reuse)
         return dH, dE, None, None, None, None
 
 
