@@ -68,3 +68,14 @@ def test_second_derivatives_are_refused(name, i, plain):
     loss = grad.square().sum() + x[i].square().sum()
     with pytest.raises(RuntimeError, match="first derivatives only"):
         loss.backward()
+
+
+@pytest.mark.parametrize("bias", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("rows", [torch.float32, torch.bfloat16])
+def test_a_bias_alone_gets_its_gradient_in_its_own_type(monkeypatch, rows, bias):
+    """The library writes dbias in the bias's type at once: no rounding to the rows' type in between."""
+    asked = []
+    monkeypatch.setattr(B, "layer_norm_backward", lambda dy, x, w, mean, rstd, dx, dw, db, *a: asked.append((dw, db)))
+    b = torch.zeros(8, dtype=bias, requires_grad=True)
+    ops.layer_norm(torch.ones(4, 8, dtype=rows), None, b).sum().backward()
+    assert [(dw, db.dtype) for dw, db in asked] == [(None, bias)] and b.grad.dtype == bias

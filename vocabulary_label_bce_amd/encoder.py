@@ -200,9 +200,9 @@ def layer_norm_forward(x, weight=None, bias=None, eps: float = 1e-5, stats: bool
 
 
 def layer_norm_backward(dy, x, weight, mean, rstd, want_dx: bool = True, want_dweight: bool = True,
-                        want_dbias: bool = True):
+                        want_dbias: bool = True, param_dtype=None):
     """(dx, dweight, dbias) from the cotangent dy, the forward's x, weight (or None) and its mean and rstd; dweight
-    and dbias in weight's dtype (x's without a weight). What is not wanted is None."""
+    and dbias in weight's dtype (without a weight in param_dtype, x's by default). What is not wanted is None."""
     dev = _on_gpu("layer_norm_backward", dy, x, weight, mean, rstd)
     if dy.shape != x.shape or dy.dtype != x.dtype or x.dtype not in _FLOATS:
         raise ValueError("dy must have x's shape and dtype")
@@ -213,7 +213,9 @@ def layer_norm_backward(dy, x, weight, mean, rstd, want_dx: bool = True, want_dw
     if not (mean.shape == n and rstd.shape == n and mean.dtype == rstd.dtype == torch.float32 and
             mean.is_contiguous() and rstd.is_contiguous()):
         raise ValueError("mean and rstd must be the forward's float32 [rows]")
-    pd = x.dtype if weight is None else weight.dtype
+    pd = weight.dtype if weight is not None else x.dtype if param_dtype is None else param_dtype
+    if pd not in _FLOATS or param_dtype not in (None, pd):
+        raise ValueError("param_dtype must be float32 or bfloat16, and weight's where there is one")
     dx = x.new_empty(x.shape) if want_dx else None
     dw = x.new_empty(D, dtype=pd) if want_dweight else None
     db = None
@@ -239,8 +241,7 @@ class _LayerNorm(torch.autograd.Function):
     def backward(ctx, dy):
         x, weight, mean, rstd = ctx.saved_tensors
         need = ctx.needs_input_grad
-        dx, dw, db = layer_norm_backward(dy, x, weight, mean, rstd, need[0], need[1], need[2])
-        return dx, dw, None if db is None else db.to(ctx.bias_dtype), None
+        return layer_norm_backward(dy, x, weight, mean, rstd, need[0], need[1], need[2], ctx.bias_dtype) + (None,)
 
 
 def layer_norm(x, weight=None, bias=None, eps: float = 1e-5):
