@@ -249,8 +249,10 @@ cutbce_status cutbce_layer_norm_backward(int64_t rows, int32_t dim, int32_t dtyp
  * Strides are in elements: row r, head h of q starts at q + r * q_row_stride + h * q_head_stride (k and v alike);
  * the head_dim elements of one row and head are contiguous. Arrays may be parts of a wider one (a fused
  * projection). q, k, v and their strides in bytes are multiples of 16 (strides may be 0; row strides and q_heads *
- * head_dim are at most 2^22), and (max(q_rows, k_rows) / 64 + seqs + 1) * q_heads is under 2^23. Outputs (out, dq, dk, dv) are dense
- * [rows][heads][head_dim].
+ * head_dim are at most 2^22). Outputs (out, dq, dk, dv) are dense [rows][heads][head_dim].
+ * Sizes: k_rows <= 2^31 - 1024. The forward takes (q_rows / 128 + seqs + 1) * q_heads under 2^23, or, without cu_q and
+ * cu_k where q_rows / seqs rows of q_heads / kv_heads heads are at most 32 (single tokens over a cache), seqs * kv_heads
+ * under 2^23, however long the caches are; the backward (max(q_rows, k_rows) / 64 + seqs + 1) * q_heads under 2^23.
  * Sequences, query side: sequence b has the rows cu_q[b] .. cu_q[b+1] - 1 (int32 [seqs + 1] on the device,
  * cu_q[0] = 0, non-decreasing, cu_q[seqs] <= q_rows), or, with cu_q NULL, the q_rows / seqs rows from
  * b * (q_rows / seqs) on. Key side: cu_k in the same way; with cu_k NULL, k_rows / seqs rows each when cu_q is NULL

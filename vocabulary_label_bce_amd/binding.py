@@ -266,14 +266,15 @@ def layer_norm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, ws, strea
 
 @functools.lru_cache(maxsize=256)
 def attention_problem(*fields):
-    """(Attention, bytes of the forward's workspace, bytes of the backward's): fields as in Attention, in order."""
+    """(Attention, bytes of the forward's workspace, bytes of the backward's): fields as in Attention, in order. None
+    where one of the two refuses the sizes (its call then does)."""
     a = Attention(*fields)
-    sizes = []
-    for backward in (0, 1):
-        b = ctypes.c_size_t(0)
-        _check(lib().cutbce_attention_workspace_size(ctypes.byref(a), backward, ctypes.byref(b)))
-        sizes.append(int(b.value))
-    return a, sizes[0], sizes[1]
+    b, c = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    forward = lib().cutbce_attention_workspace_size(ctypes.byref(a), 0, ctypes.byref(b))
+    backward = lib().cutbce_attention_workspace_size(ctypes.byref(a), 1, ctypes.byref(c))
+    if forward and backward:
+        _check(forward)
+    return a, None if forward else int(b.value), None if backward else int(c.value)
 
 
 def attention_forward(a: Attention, q, k, v, cu_q, cu_k, k_lens, out, lse, ws, stream=None):

@@ -1415,6 +1415,17 @@ hipError_t backward_t(const Attn& a, const void* dout, const void* out, const fl
 
 }  // namespace
 
+// A forward launches a workgroup for each tile of rows and head, or (few rows) for each part of a cache and key/value
+// head, at most 1,024 more than caches and heads: how many keys there are does not count. The backward is held
+// to a tile of 64 rows or keys for each query head, which covers both of its kernels.
+bool attention_fits(const Attn& a, bool backward) {
+  const int64_t rows = backward && a.k_rows > a.q_rows ? a.k_rows : a.q_rows;
+  const int64_t wgs = backward      ? units_of(rows, a.seqs, 64) * a.hq
+                      : few_rows(a) ? (int64_t)a.seqs * a.hk
+                                    : units_of(rows, a.seqs) * a.hq;
+  return wgs < kMaxGrid;
+}
+
 // (whether a forward is one of few rows depends on its arrays too: the size covers both)
 size_t attention_bytes(const Attn& a, bool backward) {
   const size_t rows = (size_t)a.q_rows * a.hq, keys = (size_t)a.k_rows * a.hk;

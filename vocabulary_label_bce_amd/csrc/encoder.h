@@ -136,6 +136,7 @@ size_t layer_norm_backward_bytes(int64_t rows, int D);
 hipError_t launch_layer_norm_backward(int64_t rows, int D, int dtype, int pdtype, const void* dy, int64_t dys,
                                       const void* x, int64_t xs, const void* w, const float* mean, const float* rstd,
                                       void* dx, void* dw, void* db, char* ws, hipStream_t st);
+bool attention_fits(const Attn& a, bool backward);  // whether one launch of each kernel takes these sizes
 size_t attention_bytes(const Attn& a, bool backward);
 hipError_t launch_attention_forward(const Attn& a, void* out, float* lse, char* ws, hipStream_t st);
 hipError_t launch_attention_backward(const Attn& a, const void* dout, const void* out, const float* lse, void* dq,

@@ -7,6 +7,7 @@ using namespace cutbce;
 namespace {
 
 constexpr int64_t kMaxRows = 0x7fffffff;
+constexpr int64_t kMaxKeys = kMaxRows - 1023;  // keys are counted in 32 bits, up to some tiles past the last
 constexpr int64_t kMaxVocab = (int64_t)0x7fffffff - 1024;
 constexpr int kMaxDim = 65536;
 constexpr int64_t kMaxSorted = (int64_t)1 << 28;  // a workgroup for 32 sorted positions or more, in one launch
@@ -33,7 +34,7 @@ cutbce_status make_attn(const cutbce_attention* p, const int32_t* cu_q, const in
                         Attn* a) {
   if (!p) return CUTBCE_ERR_NULL;
   if (!known(p->dtype)) return CUTBCE_ERR_DTYPE;
-  if (p->q_rows < 0 || p->k_rows < 0 || p->q_rows > kMaxRows || p->k_rows > kMaxRows || p->seqs < 1 ||
+  if (p->q_rows < 0 || p->k_rows < 0 || p->q_rows > kMaxRows || p->k_rows > kMaxKeys || p->seqs < 1 ||
       p->seqs > (1 << 24) || p->q_heads < 1 || p->kv_heads < 1 || p->q_heads > 65535 ||
       p->q_heads % p->kv_heads != 0)
     return CUTBCE_ERR_SHAPE;
@@ -49,9 +50,6 @@ cutbce_status make_attn(const cutbce_attention* p, const int32_t* cu_q, const in
   const int64_t row_max = (int64_t)1 << 22;
   if (st[0] > row_max || st[2] > row_max || st[4] > row_max || (int64_t)p->q_heads * p->head_dim > row_max)
     return CUTBCE_ERR_SHAPE;
-  // one workgroup, of at most 512 threads, per tile of 64 rows or more and head, in one launch
-  const int64_t rows = p->q_rows > p->k_rows ? p->q_rows : p->k_rows;
-  if ((rows / 64 + p->seqs + 1) * p->q_heads >= kMaxGrid) return CUTBCE_ERR_SHAPE;
   a->q_rs = st[0], a->q_hs = st[1], a->k_rs = st[2], a->k_hs = st[3], a->v_rs = st[4], a->v_hs = st[5];
   a->k_ss = st[6], a->v_ss = st[7];
   a->q_rows = p->q_rows, a->k_rows = p->k_rows;
@@ -153,9 +151,10 @@ cutbce_status cutbce_layer_norm_backward(int64_t rows, int32_t dim, int32_t dtyp
 
 cutbce_status cutbce_attention_workspace_size(const cutbce_attention* p, int32_t backward, size_t* bytes) {
   Attn a = {};
-  // the ranges' arrays do not change the size
+  // (without the ranges' arrays the sizes may be those of single tokens over a cache, which take the most)
   cutbce_status s = make_attn(p, nullptr, nullptr, nullptr, &a);
   if (s != CUTBCE_OK) return s;
+  if (!attention_fits(a, backward != 0)) return CUTBCE_ERR_SHAPE;
   if (!bytes) return CUTBCE_ERR_NULL;
   *bytes = attention_bytes(a, backward != 0);
   return CUTBCE_OK;
@@ -167,6 +166,7 @@ cutbce_status cutbce_attention_forward(const cutbce_attention* p, const void* q,
   Attn a = {};
   cutbce_status s = make_attn(p, cu_q, cu_k, k_lens, &a);
   if (s != CUTBCE_OK) return s;
+  if (!attention_fits(a, false)) return CUTBCE_ERR_SHAPE;
   if (a.q_rows == 0) return CUTBCE_OK;
   const size_t need = attention_bytes(a, false);
   if (!q || !out || (a.k_rows > 0 && (!k || !v)) || (need && !workspace)) return CUTBCE_ERR_NULL;
@@ -185,6 +185,7 @@ cutbce_status cutbce_attention_backward(const cutbce_attention* p, const void* d
   Attn a = {};
   cutbce_status s = make_attn(p, cu_q, cu_k, k_lens, &a);
   if (s != CUTBCE_OK) return s;
+  if (!attention_fits(a, true)) return CUTBCE_ERR_SHAPE;
   if (a.q_rows == 0 && a.k_rows == 0) return CUTBCE_OK;
   const size_t need = attention_bytes(a, true);
   if ((a.q_rows > 0 && (!dout || !q || !out || !lse || !dq)) || (a.k_rows > 0 && (!k || !v || !dk || !dv)) ||
