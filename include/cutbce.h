@@ -285,7 +285,9 @@ cutbce_status cutbce_attention_forward(const cutbce_attention *a, const void *q,
 
 /* Gradients from the cotangent dout (dense, like out) and the forward's out and lse. dq [q_rows][q_heads][head_dim],
  * dk, dv [k_rows][kv_heads][head_dim] (summed over the query heads that share a key/value head), all overwritten.
- * The probabilities are recomputed from q, k and lse. */
+ * The probabilities are recomputed from q, k and lse, and are off by the rounding of lse, 2^-24 |lse| of themselves:
+ * with scores in the millions a row keeps little but which of them is the largest (never more than probability 1
+ * each). The forward has no such limit: any finite scores, scale * q . k, up to float32's largest value. */
 cutbce_status cutbce_attention_backward(const cutbce_attention *a, const void *dout, const void *q, const void *k,
                                         const void *v, const void *out, const float *lse, const int32_t *cu_q,
                                         const int32_t *cu_k, const int32_t *k_lens, void *dq, void *dk, void *dv,

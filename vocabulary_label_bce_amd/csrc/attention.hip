@@ -406,29 +406,68 @@ template <typename T, int DH> constexpr int key_tile() { return sizeof(T) == 4 &
 // their way at once.
 template <typename T, int DH> constexpr int key_stages() { return key_tile<T, DH>() * Tile<T, DH>::kRowB > 8192 ? 2 : 4; }
 
-// Running softmax of one row per lane: `used` is the maximum that the exponents are taken against.
+// Exponents are scale * log2 e * (q . k) less a row's reference R. In one fused step, x * c - R, they are off by R's
+// own rounding, alike for the whole row: that cancels in the softmax, but it passes 128 from R = 2^31 on. So where a
+// row's reference is beyond kBig the product is rounded first, as R was, and the largest exponent is 0 (up to there
+// R's rounding is under 2^-11; ordinary scores are in the tens). And references are kept as R / 2 (c / 2 times the
+// scores; a factor of 2 is exact): scale * (q . k) up to float32's largest value is 1.44 times that in base 2.
+constexpr float kBig = 4096.f;  // of R / 2
+__device__ inline float rounded_less(float x, float c, float r) {
+#pragma clang fp contract(off)
+  const float p = x * c;
+  return p - r;
+}
+__device__ inline float rounded_product(float x, float c) {
+#pragma clang fp contract(off)
+  return x * c;
+}
+
+// Running softmax of one row per lane: `half` is R / 2, from the largest score so far or one not far below it.
 struct Online {
-  float used = -INFINITY, sum = 0.f;
+  float half = -INFINITY, sum = 0.f;
 };
 
-// P from scores of NS 32-key blocks (row-wise, c = scale * log2 e > 0); rescales the output when a row's maximum has
-// grown by more than a factor of 2^kLazy since it was last used (the exponentials stay below 2^kLazy until then).
-template <int NS, int NDB> __device__ inline void softmax_step(f32x16* s, float c, Online& st, f32x16* o) {
+// What the forward multiplies: q, negated for a negative scale and 0 for a scale of 0 (or one too small for c / 2), so
+// that c / 2 = |scale| log2 e / 2 is above 0 and a masked score of -inf stays so.
+template <typename T, int NT> __device__ inline float half_scale(float scale, u32x4* own) {
+  const float ch = fabsf(scale) * (0.5f * kLog2e);
+  if (scale < 0.f) {
+#pragma unroll
+    for (int i = 0; i < NT; ++i) own[i] = Mma<T>::negate(own[i]);
+  }
+  if (ch > 0.f) return ch;
+#pragma unroll
+  for (int i = 0; i < NT; ++i) own[i] = u32x4{0, 0, 0, 0};
+  return 1.f;
+}
+
+// P from scores of NS 32-key blocks (row-wise, ch = scale * log2 e / 2 > 0); rescales the output when a row's maximum
+// has grown by more than a factor of 2^kLazy since it was last used (the exponentials stay below 2^kLazy until then).
+template <int NS, int NDB> __device__ inline void softmax_step(f32x16* s, float ch, Online& st, f32x16* o) {
   float mx = s[0][0];
 #pragma unroll
   for (int b = 0; b < NS; ++b)
 #pragma unroll
     for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[b][i]);
   mx = fmaxf(mx, other_half(mx));
-  if (__any(mx * c > st.used + kLazy)) {
-    const float nw = fmaxf(st.used, mx * c);
-    const float f = st.used == -INFINITY ? 0.f : exp2_of(st.used - nw);
-    st.used = nw;
+  mx = rounded_product(mx, ch);
+  if (__any(mx > st.half + 0.5f * kLazy)) {
+    const float nw = fmaxf(st.half, mx);
+    const float f = st.half == -INFINITY ? 0.f : exp2_of(2.f * (st.half - nw));
+    st.half = nw;
     st.sum *= f;
 #pragma unroll
     for (int d = 0; d < NDB; ++d) o[d] *= f;
   }
-  const float base = st.used == -INFINITY ? 0.f : st.used;
+  const float half = st.half == -INFINITY ? 0.f : st.half;
+  float c = 2.f * ch, base = 2.f * half;
+  if (__builtin_expect(__any(fabsf(half) > kBig), 0)) {
+#pragma unroll
+    for (int b = 0; b < NS; ++b)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[b][i] = rounded_less(s[b][i], ch, half);
+    c = 2.f, base = 0.f;
+  }
 #pragma unroll
   for (int b = 0; b < NS; ++b)
 #pragma unroll
@@ -438,8 +477,20 @@ template <int NS, int NDB> __device__ inline void softmax_step(f32x16* s, float 
     }
 }
 
-__device__ inline float finish_lse(float used, float sum, bool any) {
-  return any ? (used + __builtin_amdgcn_logf(sum)) * kLn2 : -INFINITY;
+// (beyond kBig as the backward forms it again from a score, see big_exponent)
+__device__ inline float finish_lse(float half, float sum, bool any) {
+  if (!any) return -INFINITY;
+  const float l = __builtin_amdgcn_logf(sum);
+  return fabsf(half) > kBig ? rounded_product(half, 2.f * kLn2) + l * kLn2 : (2.f * half + l) * kLn2;
+}
+
+// The backward's exponent from lse where that is beyond kBigLse: rounded as the forward rounded it, so that a row's
+// largest score gives log2 of what its sum left in lse, and never more than 0. (P is then off by 2^-24 |lse| of itself,
+// lse's own rounding; from 2^27 on the sum is lost altogether: P = 1 at a row's largest score.)
+constexpr float kBigLse = kBig * 2.f * kLn2;
+__device__ inline float big_exponent(float x, float ch, float lse) {
+  const float y = rounded_less(rounded_product(x, ch), 2.f * kLn2, lse) * kLog2e;
+  return y > 0.f ? 0.f : y;
 }
 
 // Forward: a workgroup has 128 rows of one sequence and head, a wave 32 of them; the keys stream through LDS stages of
@@ -450,7 +501,7 @@ __device__ inline float finish_lse(float used, float sum, bool any) {
 // heads of 64: 11 us, latency (search, first tiles, up to four steps).
 //
 // SPLIT: `parts` workgroups for each tile of rows and head, with a share of its steps each (row_parts); they leave
-// their sums and, for each row, the maximum and sum of its exponentials (-1 for a row that sees no key) for
+// their sums and, for each row, its reference and the sum of its exponentials (-1 for a row that sees no key) for
 // k_attn_fwd_join.
 template <typename T, int DH, bool SPLIT>
 __global__ __launch_bounds__(256, 2) void k_attn_fwd(Attn a, int parts, T* __restrict__ out, float* __restrict__ lse,
@@ -472,12 +523,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(Attn a, int parts, T* __res
   const T* q = (const T*)a.q + (s.q0 + t) * a.q_rs + h * a.q_hs;
   u32x4 qo[Ti::kNT];
   load_own<T, DH>(qo, q, live, a.dh, lane);
-  // c > 0: a negative scale negates q, and a scale of 0 becomes one so small that every finite score is 0
-  const float c = fmaxf(fabsf(a.scale) * kLog2e, 1e-38f);
-  if (a.scale < 0.f) {
-#pragma unroll
-    for (int i = 0; i < Ti::kNT; ++i) qo[i] = Mma<T>::negate(qo[i]);
-  }
+  const float ch = half_scale<T, Ti::kNT>(a.scale, qo);
   const T* k = (const T*)a.k + s.kb + (h / a.group) * a.k_hs;
   const T* v = (const T*)a.v + s.vb + (h / a.group) * a.v_hs;
   const int mine = seen_by(a, s, t);                                     // keys of the lane's row
@@ -543,7 +589,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(Attn a, int parts, T* __res
         for (int e = 0; e < 16; ++e)
           if (j0 + b * 32 + acc_row(e, lane / 32) >= mine) x[b][e] = -INFINITY;
     }
-    softmax_step<NS, Ti::kNDB>(x, c, st, o);
+    softmax_step<NS, Ti::kNDB>(x, ch, st, o);
 #pragma unroll
     for (int b = 0; b < NS; ++b)
       op.product_t(o, Mma<T>::pack(x[b]), [&](int e) {
@@ -557,10 +603,10 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(Attn a, int parts, T* __res
     if constexpr (SPLIT) {
       const int64_t to = part * (a.q_rows * a.hq) + at;
       store_row<float, Ti::kNDB>(sums + to * a.dh, o, 1.f, a.dh, lane);
-      if (lane < 32) stats[to] = make_float2(st.used, mine > 0 ? sum : -1.f);
+      if (lane < 32) stats[to] = make_float2(st.half, mine > 0 ? sum : -1.f);
     } else {
       store_row<T, Ti::kNDB>(out + at * a.dh, o, mine > 0 ? 1.f / sum : 0.f, a.dh, lane);
-      if (lse && lane < 32) lse[at] = finish_lse(st.used, sum, mine > 0);
+      if (lse && lane < 32) lse[at] = finish_lse(st.half, sum, mine > 0);
     }
   }
 }
@@ -593,7 +639,7 @@ __global__ __launch_bounds__(256) void k_attn_fwd_join(int parts, int64_t rows, 
 #pragma unroll 4
   for (int p = 0; p < parts; ++p) {
     const float2 t = stats[p * rows + r];
-    const float f = t.x == -INFINITY ? 0.f : exp2_of(t.x - mx);
+    const float f = t.x == -INFINITY ? 0.f : exp2_of(2.f * (t.x - mx));
     sum += f * t.y;
     x += f * *(const f32x4*)(sums + (p * rows + r) * dh + d);
   }
@@ -641,9 +687,18 @@ __global__ __launch_bounds__(256, sizeof(T) == 4 && DH > 64 ? 1 : 2) void k_attn
   load_own<T, DH>(go, dout + at * a.dh, live, a.dh, lane);
   const int mine = live ? seen_by(a, s, t) : 0;
   // a row that sees no key has lse = -inf; +inf makes its probabilities 0
-  const float L = mine > 0 ? lse[at] * kLog2e : INFINITY;
+  const float ln = mine > 0 ? lse[at] : INFINITY;
+  const bool big = fabsf(ln) > kBigLse && fabsf(ln) < INFINITY, any_big = __any(big);
+  const float L0 = big ? ln : ln * kLog2e;
   float off_by = 0.f;  // sum dS
-  const float c = a.scale * kLog2e;
+  const float c0 = a.scale * kLog2e, ch = a.scale * (0.5f * kLog2e);
+  const float c = any_big ? 1.f : c0, L = any_big ? 0.f : L0;
+  auto look = [&](f32x16& x) {  // scores that are to be c x - L from here on
+    if (__builtin_expect(any_big, 0)) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) x[e] = big ? big_exponent(x[e], ch, L0) : __builtin_fmaf(x[e], c0, -L0);
+    }
+  };
   const T* k = (const T*)a.k + s.kb + (h / a.group) * a.k_hs;
   const T* v = (const T*)a.v + s.vb + (h / a.group) * a.v_hs;
   const int wave_lo = seen_by(a, s, r0 + wave * 32);
@@ -694,6 +749,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 4 && DH > 64 ? 1 : 2) void k_attn
         for (int b = 0; b < NS; ++b) {
           f32x16 x = product<T, DH>(kt + b * 32 * Ti::kRowB, qo, lane);
           const f32x16 g = product<T, DH>(kt + Ld::kBytes + b * 32 * Ti::kRowB, go, lane);
+          look(x);
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             x[e] = exp2_of(__builtin_fmaf(x[e], c, -L)) * g[e];
@@ -740,6 +796,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 4 && DH > 64 ? 1 : 2) void k_attn
       const f32x16 g = op.product(go, [&](int n) {
         spread(n, Op::NT, Op::S / 2, [&](int e) { op.col(e, kc); });
       });
+      look(x);
 #pragma unroll
       for (int e = 0; e < 16; ++e) x[e] = exp2_of(__builtin_fmaf(x[e], c, -L)) * (g[e] - delta);
       if (edge) {
@@ -760,16 +817,17 @@ __global__ __launch_bounds__(256, sizeof(T) == 4 && DH > 64 ? 1 : 2) void k_attn
   off_by += other_half(off_by);
   if (live) {
     const int64_t st = (int64_t)h * a.q_rows + s.q0 + t;
+    const float of_row = sizeof(T) == 4 ? ln : (big ? -INFINITY : L0);  // (dk and dv look up what is big)
     if constexpr (SPLIT) {
       const int64_t n = a.q_rows * a.hq;
       store_row<float, Ti::kNDB>(sums + (part * n + at) * a.dh, acc, a.scale, a.dh, lane);
       if (lane < 32) {
         off[part * n + st] = off_by;
-        if (part == 0) stat[st] = make_float2(L, delta);
+        if (part == 0) stat[st] = make_float2(of_row, delta);
       }
     } else {
       store_row<T, Ti::kNDB>(dq + at * a.dh, acc, a.scale, a.dh, lane);
-      if (lane < 32) stat[st] = make_float2(L, delta + off_by);
+      if (lane < 32) stat[st] = make_float2(of_row, delta + off_by);
     }
   }
 }
@@ -863,6 +921,7 @@ template <bool PACK> __device__ inline float get_p(const u32x4* p, int e) {
 template <typename T, int DH, bool SPLIT>
 __global__ __launch_bounds__((Dkv<T, DH>::kThreads), 2) void k_attn_dkv(Attn a, int parts,
                                                                         const T* __restrict__ dout,
+                                                                        const float* __restrict__ lse,
                                                                         const float2* __restrict__ stat,
                                                                         T* __restrict__ dk, T* __restrict__ dv,
                                                                         float* __restrict__ sums) {
@@ -870,6 +929,7 @@ __global__ __launch_bounds__((Dkv<T, DH>::kThreads), 2) void k_attn_dkv(Attn a, 
   using K = Dkv<T, DH>;
   using Ld = typename K::Ld;
   constexpr int QT = K::kQT;
+  constexpr bool kLn = sizeof(T) == 4;  // stat has lse itself
   extern __shared__ __align__(1024) char lds[];
   const uint32_t lds0 = uni((uint32_t)(size_t)(CUTBCE_LDS char*)lds);
   const int tid = threadIdx.x, wave = uni(tid / 64), lane = tid % 64, half = lane / 32;
@@ -886,7 +946,7 @@ __global__ __launch_bounds__((Dkv<T, DH>::kThreads), 2) void k_attn_dkv(Attn a, 
   u32x4 own[Ti::kNT];
   load_own<T, DH>(own, first ? (const T*)a.k + s.kb + j * a.k_rs + hk * a.k_hs
                              : (const T*)a.v + s.vb + j * a.v_rs + hk * a.v_hs, key, a.dh, lane);
-  const float c = a.scale * kLog2e;
+  const float c = a.scale * kLog2e, ch = a.scale * (0.5f * kLog2e);
   // the first row that sees key x: row t sees it if t >= x - (m - n)
   auto first_row = [&](int64_t x) { return a.causal ? (int)clamp64(x - ((int64_t)s.m - s.n), 0, s.n) : 0; };
   const int mine = first_row(j), wave_hi = first_row(j0 + kw * 32 + 31);
@@ -955,20 +1015,39 @@ __global__ __launch_bounds__((Dkv<T, DH>::kThreads), 2) void k_attn_dkv(Attn a, 
     wait_and_sync<>();
     if (first) {
       op.rows(Op::rows_at(rows, lane));
-      int ch = h0, ct = t0;
+      int cur = h0, ct = t0;
       for (int i = 0; i < steps; ++i) {
         wait_and_sync<>();
         prepare();
         const uint32_t at = stage(i);
-        const int t1 = ct * QT + rw * 32;
-        if (++ch == a.group) ch = 0, --ct;
+        const int t1 = ct * QT + rw * 32, at_head = cur;
+        if (++cur == a.group) cur = 0, --ct;
         f32x4 ld[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) ld[e] = __builtin_bit_cast(f32x4, lds16(words + at + e * 32));
+        // one of the 32 rows' words a lane: whether an lse has to be looked up
+        const float mark = *(CUTBCE_LDS const float*)(size_t)(words + at - half * 16 + (lane % 32) * 4);
         const uint32_t gc = Op::cols_at(rows + at + Ld::kBytes, lane), nr = Op::rows_at(rows + stage(i + 1), lane);
-        f32x16 x = op.product(own, [&](int k) { beside(k, gc); });
+        bool any_big = false;
+        f32x16 x = op.product(own, [&](int k) {
+          beside(k, gc);
+          if (!kLn && k + 1 == Op::NT) any_big = __any(mark == -INFINITY);
+        });
+        float f = c;
+        if (__builtin_expect(any_big, 0)) {
+          const int t = t1 + lane % 32;
+          const float l = t < s.n ? lse[(s.q0 + t) * a.hq + hk * a.group + (at_head + turn) % a.group] : 0.f;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] = exp2_of(__builtin_fmaf(x[e], c, -ld[e / 4][e % 4]));
+          for (int e = 0; e < 16; ++e) {
+            const float L = ld[e / 4][e % 4], big = __shfl(l, acc_row(e, half), 64);
+            x[e] = L == -INFINITY ? big_exponent(x[e], ch, big) : __builtin_fmaf(x[e], c, -L);
+            ld[e / 4][e % 4] = 0.f;
+          }
+          f = 1.f;
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          x[e] = exp2_of(kLn ? big_exponent(x[e], ch, ld[e / 4][e % 4]) : __builtin_fmaf(x[e], f, -ld[e / 4][e % 4]));
         if (t1 < wave_hi || t1 + 32 > s.n) {
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
@@ -1118,11 +1197,7 @@ __global__ __launch_bounds__((few_waves<T, DH>() * 64), 1) void k_attn_few(Attn 
   const bool live = col < cols;
   u32x4 qo[Ti::kNT];
   load_own<T, DH>(qo, (const T*)a.q + (s.q0 + t) * a.q_rs + head * a.q_hs, live, a.dh, lane);
-  const float c = fmaxf(fabsf(a.scale) * kLog2e, 1e-38f);
-  if (a.scale < 0.f) {
-#pragma unroll
-    for (int i = 0; i < Ti::kNT; ++i) qo[i] = Mma<T>::negate(qo[i]);
-  }
+  const float ch = half_scale<T, Ti::kNT>(a.scale, qo);
   const int mine = live ? seen_by(a, s, t) : 0, least = seen_by(a, s, 0);
   // this part's 32-key blocks, and the wave's
   const int blocks = (s.m + 31) / 32;
@@ -1181,7 +1256,7 @@ __global__ __launch_bounds__((few_waves<T, DH>() * 64), 1) void k_attn_few(Attn 
       for (int e = 0; e < 16; ++e)
         if (b * 32 + acc_row(e, lane / 32) >= mine) x[e] = -INFINITY;
     }
-    softmax_step<1, NDB>(&x, c, st, o);
+    softmax_step<1, NDB>(&x, ch, st, o);
     if (ST == 1) {
       if (more) arrived(integral_constant<int, 1>());
       else arrived(integral_constant<int, 0>());
@@ -1198,7 +1273,7 @@ __global__ __launch_bounds__((few_waves<T, DH>() * 64), 1) void k_attn_few(Attn 
   float* ms = (float*)lds;                  // [NW][2][32]
   float* ot = (float*)(lds + NW * 256);     // [NW][DH][32], one column per row's lane
   if (lane < 32) {
-    ms[wave * 64 + lane] = st.used;
+    ms[wave * 64 + lane] = st.half;
     ms[wave * 64 + 32 + lane] = st.sum;
   }
   __syncthreads();
@@ -1207,8 +1282,8 @@ __global__ __launch_bounds__((few_waves<T, DH>() * 64), 1) void k_attn_few(Attn 
   for (int w = 0; w < NW; ++w) mx = fmaxf(mx, ms[w * 64 + col]);
 #pragma unroll
   for (int w = 0; w < NW; ++w)
-    sum += ms[w * 64 + col] == -INFINITY ? 0.f * ms[w * 64 + 32 + col] : exp2_of(ms[w * 64 + col] - mx) * ms[w * 64 + 32 + col];
-  const float f = st.used == -INFINITY ? 0.f : exp2_of(st.used - mx);
+    sum += (ms[w * 64 + col] == -INFINITY ? 0.f : exp2_of(2.f * (ms[w * 64 + col] - mx))) * ms[w * 64 + 32 + col];
+  const float f = st.half == -INFINITY ? 0.f : exp2_of(2.f * (st.half - mx));
 #pragma unroll
   for (int db = 0; db < NDB; ++db)
 #pragma unroll
@@ -1266,7 +1341,7 @@ __global__ __launch_bounds__(256) void k_attn_join(Attn a, int parts, int cols, 
   if (tid % 64 == 0) red[wave][0] = mx;
   __syncthreads();
   mx = fmaxf(fmaxf(red[0][0], red[1][0]), fmaxf(red[2][0], red[3][0]));
-  const float f = m == -INFINITY ? 0.f : exp2_of(m - mx);
+  const float f = m == -INFINITY ? 0.f : exp2_of(2.f * (m - mx));
   f_of[tid] = f;
   float sum = f * l;
 #pragma unroll
@@ -1387,14 +1462,14 @@ hipError_t backward_t(const Attn& a, const void* dout, const void* out, const fl
     if (parts == 1) {
       const hipError_t e = allow_lds<k_attn_dkv<T, DH, false>>(bytes);
       if (e != hipSuccess) return e;
-      k_attn_dkv<T, DH, false><<<dim3(units), dim3(K::kThreads), bytes, st>>>(a, 1, (const T*)dout, stat, (T*)dk, (T*)dv,
-                                                                             nullptr);
+      k_attn_dkv<T, DH, false><<<dim3(units), dim3(K::kThreads), bytes, st>>>(a, 1, (const T*)dout, lse, stat, (T*)dk,
+                                                                             (T*)dv, nullptr);
     } else {
       const hipError_t e = allow_lds<k_attn_dkv<T, DH, true>>(bytes);
       if (e != hipSuccess) return e;
       const int64_t n = a.k_rows * a.hk * a.dh;
       float* sums = (float*)(ws + stat_bytes(a));
-      k_attn_dkv<T, DH, true><<<dim3(units * parts), dim3(K::kThreads), bytes, st>>>(a, parts, (const T*)dout, stat,
+      k_attn_dkv<T, DH, true><<<dim3(units * parts), dim3(K::kThreads), bytes, st>>>(a, parts, (const T*)dout, lse, stat,
                                                                                     (T*)dk, (T*)dv, sums);
       k_attn_dkv_join<T><<<dim3((unsigned)cdiv(n, 1024), 2), dim3(256), 0, st>>>(parts, n, sums, (T*)dk, (T*)dv);
     }
