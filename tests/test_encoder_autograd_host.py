@@ -79,3 +79,16 @@ def test_a_bias_alone_gets_its_gradient_in_its_own_type(monkeypatch, rows, bias)
     b = torch.zeros(8, dtype=bias, requires_grad=True)
     ops.layer_norm(torch.ones(4, 8, dtype=rows), None, b).sum().backward()
     assert [(dw, db.dtype) for dw, db in asked] == [(None, bias)] and b.grad.dtype == bias
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bool, torch.int16, torch.uint8])
+def test_offsets_and_lengths_of_other_types_are_refused(dtype):
+    """Like ids, they are int32 or int64: nothing is cut to a whole number in passing."""
+    q = torch.ones(4, 2, 8)
+    for kw in (dict(cu_q=CU.to(dtype)), dict(cu_q=CU, cu_k=CU.to(dtype)),
+               dict(cu_q=CU, k_lens=torch.ones(1, dtype=dtype))):
+        with pytest.raises(ValueError, match="int32 or int64"):
+            ops.packed_attention(q, q, q, **kw)
+    with pytest.raises(ValueError, match="int32 or int64"):
+        ops.cached_attention(q[:1], q[None], q[None], torch.ones(1, dtype=dtype))
+    ops.packed_attention(q, q, q, CU.long(), k_lens=torch.tensor([3]))

@@ -277,6 +277,8 @@ def _offsets(cu, n, name):
         return None
     if cu.shape != (n,):
         raise ValueError(f"{name} must have {n} entries on the device")
+    if cu.dtype != torch.int32 and cu.dtype != torch.int64:
+        raise ValueError(f"{name} must be int32 or int64")
     return cu if cu.dtype == torch.int32 and cu.is_contiguous() else cu.to(torch.int32).contiguous()
 
 
@@ -375,7 +377,7 @@ def packed_attention(q, k, v, cu_q, cu_k=None, k_lens=None, causal: bool = True,
     column ranges of one projection: rows and heads may be strided. Sequence b has the rows cu_q[b]:cu_q[b+1] and the
     keys cu_k[b]:cu_k[b+1] (cu_k None: cu_q); with k_lens only the first k_lens[b] of them are keys. causal: row t of
     n sees the keys j <= t + m - n of m, so that the last row sees all of them; a row that sees none gives zeros.
-    scale: 1 / sqrt(head_dim) by default. cu_q, cu_k and k_lens are int32 on the device. Gradients flow to q, k, v.
+    scale: 1 / sqrt(head_dim) by default. cu_q, cu_k and k_lens are int32 (int64 is converted) on the device. Gradients flow to q, k, v.
     Non-finite values in k, v or the cotangent may reach every row of their own sequence and head, and no other."""
     if _derived(q, k, v):
         return _PackedAttention.apply(q, k, v, cu_q, cu_k, k_lens, causal, scale)
