@@ -92,3 +92,12 @@ def test_offsets_and_lengths_of_other_types_are_refused(dtype):
     with pytest.raises(ValueError, match="int32 or int64"):
         ops.cached_attention(q[:1], q[None], q[None], torch.ones(1, dtype=dtype))
     ops.packed_attention(q, q, q, CU.long(), k_lens=torch.tensor([3]))
+
+
+def test_adding_to_a_table_gradient_is_seen_by_autograd():
+    """embedding_backward writes into dtable: where autograd has kept it for a backward, that one raises."""
+    dtable, w = torch.ones(5, 8), torch.ones(5, 8, requires_grad=True)
+    y = (w * dtable).sum()
+    assert ops.embedding_backward(torch.ones(3, 8), IDS, 5, dtable=dtable) is dtable
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()

@@ -127,6 +127,8 @@ def embedding_backward(dout, ids, vocab: int, scale: float = 1.0, dtable=None):
         dtable = dout.new_empty((vocab, D))
     ws = dout.new_empty(B.embedding_backward_workspace_size(ids.numel(), vocab, D, dout.dtype), dtype=torch.uint8)
     B.embedding_backward(ids, dout, scale, accumulate, dtable, ws, B.raw_stream(dev))
+    if accumulate:
+        torch.autograd.graph.increment_version(dtable)
     return dtable
 
 
