@@ -101,3 +101,5 @@ def test_adding_to_a_table_gradient_is_seen_by_autograd():
     assert ops.embedding_backward(torch.ones(3, 8), IDS, 5, dtable=dtable) is dtable
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         y.backward()
+    with torch.inference_mode():  # (without versions)
+        ops.embedding_backward(torch.ones(3, 8), IDS, 5, dtable=torch.ones(5, 8))

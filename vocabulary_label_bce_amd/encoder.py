@@ -127,7 +127,7 @@ def embedding_backward(dout, ids, vocab: int, scale: float = 1.0, dtable=None):
         dtable = dout.new_empty((vocab, D))
     ws = dout.new_empty(B.embedding_backward_workspace_size(ids.numel(), vocab, D, dout.dtype), dtype=torch.uint8)
     B.embedding_backward(ids, dout, scale, accumulate, dtable, ws, B.raw_stream(dev))
-    if accumulate:
+    if accumulate and not dtable.is_inference():
         torch.autograd.graph.increment_version(dtable)
     return dtable
 
@@ -379,8 +379,9 @@ def packed_attention(q, k, v, cu_q, cu_k=None, k_lens=None, causal: bool = True,
     column ranges of one projection: rows and heads may be strided. Sequence b has the rows cu_q[b]:cu_q[b+1] and the
     keys cu_k[b]:cu_k[b+1] (cu_k None: cu_q); with k_lens only the first k_lens[b] of them are keys. causal: row t of
     n sees the keys j <= t + m - n of m, so that the last row sees all of them; a row that sees none gives zeros.
-    scale: 1 / sqrt(head_dim) by default. cu_q, cu_k and k_lens are int32 (int64 is converted) on the device. Gradients flow to q, k, v.
-    Non-finite values in k, v or the cotangent may reach every row of their own sequence and head, and no other."""
+    scale: 1 / sqrt(head_dim) by default. cu_q, cu_k and k_lens are int32 (int64 is converted) on the device.
+    Gradients flow to q, k, v. Non-finite values in k, v or the cotangent may reach every row of their own sequence and
+    head, and no other."""
     if _derived(q, k, v):
         return _PackedAttention.apply(q, k, v, cu_q, cu_k, k_lens, causal, scale)
     return packed_attention_forward(q, k, v, cu_q, cu_k, k_lens, causal, scale, want_lse=False)[0]
