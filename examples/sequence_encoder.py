@@ -26,6 +26,14 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 from vocabulary_label_bce_amd import ops  # noqa: E402
 
 
+class Cache:
+    """Keys and values [users, capacity, kv heads, head_dim] and how many rows each user has filled (on the device);
+    `tokens` is the same count on the host, one more for every call, so that a full cache is known without asking."""
+
+    def __init__(self, keys, values, lens):
+        self.keys, self.values, self.lens, self.tokens = keys, values, lens, 0
+
+
 class Encoder:
     """Parameters and the block. dim = heads * head_dim; kv_heads <= heads share keys and values."""
 
@@ -91,14 +99,17 @@ class Encoder:
     # ---- serving ----
     def new_cache(self, users, capacity):
         shape = (users, capacity, self.kv_heads, self.head_dim)
-        return (torch.zeros(shape, dtype=self.items.dtype, device=self.items.device),
-                torch.zeros(shape, dtype=self.items.dtype, device=self.items.device),
-                torch.zeros(users, dtype=torch.int32, device=self.items.device))
+        return Cache(torch.zeros(shape, dtype=self.items.dtype, device=self.items.device),
+                     torch.zeros(shape, dtype=self.items.dtype, device=self.items.device),
+                     torch.zeros(users, dtype=torch.int32, device=self.items.device))
 
     @torch.no_grad()
     def serve(self, ids, cache, k=8):
         """Appends one item a user to the cache; returns (hidden [users, dim], the k best next items)."""
-        keys, values, lens = cache
+        keys, values, lens = cache.keys, cache.values, cache.lens
+        if cache.tokens >= min(keys.shape[1], self.p["positions"].shape[0]):
+            raise ValueError("the cache is full")
+        cache.tokens += 1
         x = ops.embedding(ids, self.items, self.scale) + ops.embedding(lens, self.p["positions"])
         q, kn, vn = self._qkv(x)
         user = torch.arange(ids.numel(), device=ids.device)
