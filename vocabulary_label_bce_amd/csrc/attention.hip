@@ -221,6 +221,27 @@ __device__ inline void product_t(f32x16* acc, const typename Mma<T>::P& p, uint3
     Mma<T>::template slot_t<NDB>(acc, k, Mma<T>::template load_t<DH>(k, base), p);
 }
 
+// acc += X^T P with what the rounding of P to 16 bits leaves over, as a second part: twice the matrix instructions, each
+// pair with one operand of X.
+template <typename T, int DH> __device__ inline void product_t_exact(f32x16* acc, f32x16 x, uint32_t at, int lane) {
+  if constexpr (sizeof(T) == 4) {
+    product_t<T, DH>(acc, Mma<T>::pack(x), at, lane);
+  } else {
+    constexpr int NDB = Tile<T, DH>::kNDB;
+    const typename Mma<T>::P p = Mma<T>::pack(x);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] -= to_f32(p.g[i / 8][i % 8]);
+    const typename Mma<T>::P rest = Mma<T>::pack(x);
+    const uint32_t base = Mma<T>::template base_t<DH>(at, lane);
+#pragma unroll
+    for (int k = 0; k < Mma<T>::kSlotsPerBlock * NDB; ++k) {
+      const typename Mma<T>::A t = Mma<T>::template load_t<DH>(k, base);
+      Mma<T>::template slot_t<NDB>(acc, k, t, p);
+      Mma<T>::template slot_t<NDB>(acc, k, t, rest);
+    }
+  }
+}
+
 // The tile's operand of k-step t: the 32 rows from `at`, through the lane's base as above.
 template <typename T, int DH> __device__ inline uint32_t base_row(uint32_t at, int lane) {
   using Ti = Tile<T, DH>;
@@ -1155,6 +1176,10 @@ __global__ __launch_bounds__(256) void k_attn_dkv_join(int parts, int64_t n, con
 // there, one of four 86. 128 ranges of up to 200 keys, 2 heads of 64: 7.2 us (lengths, first tiles, two blocks a wave,
 // the waves' join).
 //
+// The probabilities go into the second product as two bf16 parts: the kernel waits for memory, and the added matrix
+// instructions cost 1 to 3% (80.0 -> 80.7 us and 6.8 -> 7.0 at the sizes above) where one part's rounding was as large an
+// error as that of out itself.
+//
 // bf16 rings have two stages of 32 keys, K and V each. A float32 block keeps the matrix unit busy for about as long as
 // its bytes take (32 columns, however few are used), so more waves matter more than more loads in flight: one stage,
 // where K of the next block is loaded from the end of the scores on and V from the end of the second product on. 16
@@ -1261,7 +1286,7 @@ __global__ __launch_bounds__((few_waves<T, DH>() * 64), 1) void k_attn_few(Attn 
       if (more) arrived(integral_constant<int, 1>());
       else arrived(integral_constant<int, 0>());
     }
-    product_t<T, DH>(o, Mma<T>::pack(x), kt + Ld::kBytes, lane);
+    product_t_exact<T, DH>(o, x, kt + Ld::kBytes, lane);
     if (ST == 1 && more) {
       read();
       fetch_v(b + NW, 0);
