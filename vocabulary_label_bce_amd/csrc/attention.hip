@@ -221,8 +221,8 @@ __device__ inline void product_t(f32x16* acc, const typename Mma<T>::P& p, uint3
     Mma<T>::template slot_t<NDB>(acc, k, Mma<T>::template load_t<DH>(k, base), p);
 }
 
-// acc += X^T P with what the rounding of P to 16 bits leaves over, as a second part: twice the matrix instructions, each
-// pair with one operand of X.
+// acc += X^T P with what the rounding of P to 16 bits leaves over, as a second part: twice the matrix instructions,
+// each pair with one operand of X.
 template <typename T, int DH> __device__ inline void product_t_exact(f32x16* acc, f32x16 x, uint32_t at, int lane) {
   if constexpr (sizeof(T) == 4) {
     product_t<T, DH>(acc, Mma<T>::pack(x), at, lane);
@@ -516,10 +516,16 @@ __device__ inline float big_exponent(float x, float ch, float lse) {
 
 // Forward: a workgroup has 128 rows of one sequence and head, a wave 32 of them; the keys stream through LDS stages of
 // KT keys, shared by the four waves. Two workgroups a CU (registers), so that a SIMD has a wave of each: one's softmax
-// beside the other's products. 4 sequences of up to 8,192 rows, 8 heads over 2 of 128, bf16: 260 us, about 990 TFLOP/s
-// of the seen pairs; the matrix unit is busy 48% of the cycles and vector instructions issue in 41%, so a wave's chain
-// of scores, softmax and product bounds it, and the tail of the longest sequences. 128 sequences of up to 200 rows, 2
-// heads of 64: 11 us, latency (search, first tiles, up to four steps).
+// beside the other's products. 4 sequences of up to 8,192 rows, 8 heads over 2 of 128, bf16: 265 to 277 us (by the
+// card), 930 to 970 TFLOP/s of the seen pairs; the matrix unit is busy 48% of the cycles and vector instructions issue
+// in 41%, so a wave's chain of scores, softmax and product bounds it, and the tail of the longest sequences. 128
+// sequences of up to 200 rows, 2 heads of 64: 11 us, latency (search, first tiles, up to four steps). In float32 one
+// sequence of 2,048, 8 heads over 2 of 64, in 3 parts: 71 us and 5 for the join; its matrix instructions alone are 28.
+//
+// In bf16 the probabilities are rounded to bf16 for the product with the values: as an operand they have the precision
+// that v has, each errs by at most 2^-8 of itself, with either sign, and out's error is 0.14 to 0.21% of its norm
+// (0.17% is the rounding of out alone). A second part for what is left over, as in k_attn_few, would be half as many
+// matrix instructions again as the forward has.
 //
 // SPLIT: `parts` workgroups for each tile of rows and head, with a share of its steps each (row_parts); they leave
 // their sums and, for each row, its reference and the sum of its exponentials (-1 for a row that sees no key) for
@@ -633,10 +639,13 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(Attn a, int parts, T* __res
 }
 
 // Few tiles of rows leave CUs idle: the keys that a tile sees are then dealt to several workgroups, no more than two a
-// CU in all, where a part gets 512 keys or more (256 in float32, whose products take longer). One sequence of 4,096
-// rows, 1 head of 128, bf16, in 8 parts with the join: forward 74 -> 25 us, dq 98 -> 33; of 2,048, float32: 270 -> 49
-// and 406 -> 71. Two parts of 512 bf16 keys gain nothing over one workgroup (1,024 rows, 2 heads of 64: 18 us): the
-// join takes 4.
+// CU in all, where a part gets 512 keys or more (256 in float32, whose products take longer) and there are three parts
+// or more. One sequence of 4,096 rows, 1 head of 128, bf16, in 8 parts with the join: forward 74 -> 25 us, dq 98 ->
+// 35; of 2,048, float32: 270 -> 47 and 406 -> 69. Two parts of 512 bf16 keys gain nothing over one workgroup (1,024
+// rows, 2 heads of 64: 18 us): the join takes 4. Parts of half as many keys, forward and dq with their joins: bf16,
+// 1,024 rows, 2 heads of 64 18.7 -> 14.5 and 23.9 -> 20.7 us, 2 x 1,500, 4 heads of 128 33.4 -> 25.8 and 43.6 -> 35.3,
+// but 4 x 1,024, 4 heads of 64 (148 workgroups, 3 parts) 19.9 -> 20.0 and 25.1 -> 28.5; float32, 700 rows, 2 heads of
+// 64 52 -> 24 and 74 -> 31, 4 x 500, 4 heads of 128 75 -> 41 and 111 -> 59. So these bounds are on the safe side.
 int row_parts(const Attn& a) {
   const int64_t wgs = (a.q_rows / kRows + a.seqs + 1) * a.hq, most = a.k_pitch / (a.dtype == 1 ? 512 : 256);
   int64_t p = 512 / wgs;
@@ -673,14 +682,14 @@ __global__ __launch_bounds__(256) void k_attn_fwd_join(int parts, int64_t rows, 
 }
 
 
-// dq, and the rows' (lse in base 2, delta) for dk and dv: the forward's layout and loop. At the forward's sizes 365 us
-// (matrix unit busy 53%, vector issue 41%) and 16 us. delta is needed from the first key on. dO . out with the rounded
-// out is off by out's rounding, which few keys leave as large as dS itself (bf16: dq off by 0.33% of its norm at 4
-// keys, 0.28% at 16, 0.25% from 256 on; 0.23% is the rounding of dS and dq). So where a workgroup's keys fit into the
-// LDS stages all at once (256 keys, 128 at head_dim over 64), a first pass over them there sums P dP in float32
-// instead: dq off by 0.23%, 14 -> 16 us at 128 sequences of up to 200. The workgroups with more keys take dO . out
-// (their rows then add little: 0.24% at any length); what it is off by is the sum of a row's dS in float32, and dk gets
-// it added.
+// dq, and the rows' (lse in base 2, delta) for dk and dv: the forward's layout and loop. At the forward's sizes 367 to
+// 383 us (matrix unit busy 53%, vector issue 42%), 17 us, and in float32 103 us and 5 for the join. delta is needed
+// from the first key on. dO . out with the rounded out is off by out's rounding, which few keys leave as large as dS
+// itself (bf16: dq off by 0.33% of its norm at 4 keys, 0.28% at 16, 0.25% from 256 on; 0.23% is the rounding of dS and
+// dq). So where a workgroup's keys fit into the LDS stages all at once (256 keys, 128 at head_dim over 64), a first
+// pass over them there sums P dP in float32 instead: dq off by 0.23%, 14 -> 16 us at 128 sequences of up to 200. The
+// workgroups with more keys take dO . out (their rows then add little: 0.24% at any length); what it is off by is the
+// sum of a row's dS in float32, and dk gets it added.
 //
 // SPLIT: `parts` workgroups for each tile of rows and head, as in the forward; they leave their sums (of dS in off) for
 // k_attn_dq_join. The first one takes all of the keys where they fit into LDS.
@@ -932,11 +941,13 @@ template <bool PACK> __device__ inline float get_p(const u32x4* p, int e) {
 // head_dim 128, one wave per SIMD, and half of them in accumulation registers that vector instructions cannot reach:
 // 1.33 ms at 4 x 8192). So a pair of waves shares 32 keys: the first has k and dv (scores, P, P^T dO), the second v
 // and dk (dP, dS, dS^T Q) one tile behind, with P handed over in LDS. Two waves per SIMD, one of each kind, hide each
-// other's latencies: 620 us (matrix unit busy 38%; the chain of a turn, scores to P to product, is covered only in part
-// by the other wave), 16 us at 128 sequences of up to 200. Where four stages leave too little room for two P's of each
-// pair in float32, its upper 24 bits are handed over: an error of 2^-16, under a hundredth of dS's rounding to bf16.
-// (One P, with a second barrier before it is overwritten, was slower; float16 loses what is under 2^-38 of a row's
-// sum.)
+// other's latencies: 640 to 664 us (matrix unit busy 36%; the chain of a turn, scores to P to product, is covered only
+// in part by the other wave), 16 us at 128 sequences of up to 200; float32, one sequence of 2,048, 8 heads over 2 of
+// 64, in parts: 111 us and 5 for the join. P and dS are rounded to bf16 as operands of the second products, like P in
+// the forward: dv off by 0.21 to 0.24% of its norm, dk by 0.23 to 0.24%. Where four stages leave too little room for
+// two P's of each pair in float32, its upper 24 bits are handed over: an error of 2^-16, under a hundredth of dS's
+// rounding to bf16. (One P, with a second barrier before it is overwritten, was slower; float16 loses what is under
+// 2^-38 of a row's sum.)
 //
 // SPLIT: `parts` workgroups for each key tile and head, with a share of its steps each (dkv_parts).
 template <typename T, int DH, bool SPLIT>
@@ -1171,14 +1182,14 @@ __global__ __launch_bounds__(256) void k_attn_dkv_join(int parts, int64_t n, con
 // waves take 32-key blocks in turn, each through an LDS ring of its own (no barriers), and join their results in
 // LDS. With more than one part, the parts leave (out, max, sum) in the workspace and k_attn_join joins them in order.
 //
-// Bound by the cache's bytes: 16 ranges of up to 32,768 keys, 16 heads over 2 of 128, bf16 (403 MB): 80 us, 5.0 TB/s,
-// and 4.7 for the join. A workgroup has as many waves as let two of them share a CU's LDS: two of two waves took 81 us
-// there, one of four 86. 128 ranges of up to 200 keys, 2 heads of 64: 7.2 us (lengths, first tiles, two blocks a wave,
-// the waves' join).
+// Bound by the cache's bytes: 16 ranges of up to 32,768 keys, 16 heads over 2 of 128, bf16 (403 MB): 80 to 83 us, 4.9
+// to 5.0 TB/s, and 4.7 for the join. A workgroup has as many waves as let two of them share a CU's LDS: two of two
+// waves took 81 us there, one of four 86. 128 ranges of up to 200 keys, 2 heads of 64: 7.0 us (lengths, first tiles,
+// two blocks a wave, the waves' join).
 //
 // The probabilities go into the second product as two bf16 parts: the kernel waits for memory, and the added matrix
-// instructions cost 1 to 3% (80.0 -> 80.7 us and 6.8 -> 7.0 at the sizes above) where one part's rounding was as large an
-// error as that of out itself.
+// instructions cost 1 to 3% (80.0 -> 80.7 us and 6.8 -> 7.0 at the sizes above) where one part's rounding was as large
+// an error as that of out itself.
 //
 // bf16 rings have two stages of 32 keys, K and V each. A float32 block keeps the matrix unit busy for about as long as
 // its bytes take (32 columns, however few are used), so more waves matter more than more loads in flight: one stage,

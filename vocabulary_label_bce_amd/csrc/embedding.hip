@@ -94,10 +94,11 @@ __global__ __launch_bounds__(256) void k_embed(int64_t n, int V, int D, int lpr,
 }
 
 // The gradient's table is cleared by the sorting kernels, whose own work fills few CUs and is all latency: the
-// workgroups behind the sorting ones clear a share of it each. At 876,000 x 128 bf16 (224 MB) and 25,600 ids the
-// six launches take 49 us; with the table cleared before them it was 28 us more. At 262,144 x 512 float32 (537 MB) and
-// 12,289 ids they take 94 us, 5.7 TB/s. The stores go past the caches: at 262,144 x 512 float32 (537 MB) the lookup and
-// the row sums around them then still find their rows there (13 -> 8 us each).
+// workgroups behind the sorting ones clear a share of it each. At 876,000 x 128 bf16 (224 MB) and 25,600 ids the six
+// launches take 50 us; with the table cleared before them it was 28 us more, and without a table to clear (sums added
+// to it) they take 27. At 262,144 x 512 float32 (537 MB) and 12,289 ids they take 94 us, 5.7 TB/s, or 28. The stores
+// go past the caches: at 262,144 x 512 float32 (537 MB) the lookup and the row sums around them then still find their
+// rows there (13 -> 8 us each).
 struct Fill {
   char* p;          // of this launch's share
   int64_t bytes;    // 0: nothing to clear
@@ -332,7 +333,9 @@ __global__ __launch_bounds__(256) void k_embed_grad(int64_t n, int V, int D, int
 // Joins the partial sums of the items that span chunks. A wave looks at one chunk: if an item begins there and goes
 // on, it counts the chunks that the item reaches into (64 probes at a time: the keys are sorted). Then the workgroup
 // adds the partials of each such item: group g those of the chunks g, g + groups, ... in order, and the groups' sums
-// in order of g. 25,600 x 128 bf16: 6.7 us, the chain of probes, partials and sums of the hottest item.
+// in order of g. 25,600 x 128 bf16: 6.3 us, the chain of probes, partials and sums of the hottest item. An item's
+// partials are one workgroup's: 262,144 positions of 1,000 items (1 / rank: the hottest has 3,300 partials) x 512
+// float32 take 328 us here, beside 125 for the chunks (537 MB, 4.3 TB/s).
 template <typename T>
 __global__ __launch_bounds__(256) void k_embed_join(int64_t n, int64_t chunks, int V, int D, int lpr,
                                                     const int* __restrict__ keys, float scale, bool accumulate,
