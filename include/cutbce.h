@@ -293,6 +293,60 @@ cutbce_status cutbce_attention_backward(const cutbce_attention *a, const void *d
                                         const int32_t *cu_k, const int32_t *k_lens, void *dq, void *dk, void *dv,
                                         void *workspace, size_t workspace_bytes, void *stream);
 
+/* ---------------------------------------------------------------------------------------------------------
+ * A training step's other operators: the norm of all gradients and the AdamW step. They take lists of tensors (host
+ * arrays of `count` entries, read before the call returns); the conventions above hold otherwise. Tensors are dense
+ * and aligned to an element.
+ * --------------------------------------------------------------------------------------------------------- */
+
+/* Bytes of workspace of cutbce_grad_norm for tensors of n[i] elements (256-byte aligned). */
+cutbce_status cutbce_grad_norm_workspace_size(int32_t count, const int64_t *n, size_t *bytes);
+
+/* norm[0] (device float) = sqrt(sum over tensors and elements of grads[i][j]^2), summed in float64 in an order that
+ * depends on the sizes alone.
+ *   grads   (host) the tensors' device pointers; n (host) their elements; dtypes (host) a cutbce_dtype each.
+ * 0 <= count <= 2^20, n[i] >= 0; sum of n[i] / 16384 + count under 2^31. Errors: SHAPE, DTYPE, NULL, ALIGN, WORKSPACE. */
+cutbce_status cutbce_grad_norm(int32_t count, const void *const *grads, const int64_t *n, const int32_t *dtypes,
+                               float *norm, void *workspace, size_t workspace_bytes, void *stream);
+
+/* The tensors of an AdamW step (host struct of host arrays, `count` entries each; all pointers in them device). params,
+ * states, scales and masters are updated in place; no two of a call's arrays may overlap (not checked here). */
+typedef struct {
+    int32_t count;
+    int32_t reserved;              /* 0 */
+    void *const *param;            /* [n] in param_dtype */
+    const void *const *grad;       /* [n] in grad_dtype */
+    void *const *exp_avg;          /* m: float [n], or e4m3 bytes [n] */
+    void *const *exp_avg_sq;       /* v: float [n], or sqrt(v) as e4m3 bytes [n] */
+    void *const *exp_avg_scale;    /* states of 8 bits: float [ceil(n / 256)], a scale for each 256 elements; else NULL */
+    void *const *exp_avg_sq_scale; /* the same */
+    void *const *master;           /* float [n], the value that param is the rounding of, or a NULL entry; or NULL */
+    const int64_t *n;
+    const int32_t *param_dtype, *grad_dtype;
+    const float *weight_decay;
+} cutbce_adamw_tensors;
+
+/* What is the same for all tensors (host struct). */
+typedef struct {
+    int32_t *step;      /* (device) [1]: steps taken before this one; one more when the call is done */
+    const float *lr_at; /* (device) [1]: the learning rate, or NULL: lr */
+    const float *norm;  /* (device) [1]: the gradients' norm, or NULL: no clipping */
+    double max_norm;    /* with norm: gradients are multiplied by min(1, max_norm / (norm + 1e-6)) */
+    double lr, eps;
+    double beta1, beta2; /* in [0, 1) */
+    int32_t state_bits;  /* 32 or 8 */
+    uint32_t seed;       /* states of 8 bits: of the random rounding */
+} cutbce_adamw;
+
+/* AdamW with decoupled weight decay: with t = step + 1 and g the (clipped) gradient, in float32,
+ *   m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2,
+ *   p = p (1 - lr weight_decay) - lr (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps),
+ * param rounded to its type once. States of 8 bits hold m and sqrt(v): element j stands for e4m3 code * scale of block
+ * j / 256, the scale being the block's largest magnitude / 448; the new ones are rounded up or down at random with the
+ * probabilities that make the mean right (a positive sqrt(v) never to 0), by numbers that follow from seed, t, the
+ * tensor's place in the list and j. Steps are counted on the device: a captured step that is replayed advances. */
+cutbce_status cutbce_adamw_step(const cutbce_adamw_tensors *tensors, const cutbce_adamw *how, void *stream);
+
 /* Opt-in kernel timing for benchmarks (host calls). While enabled, every launch of the logit-tile sweeps
  * (kind 0: forward rows sweep, kind 1: backward dE sweep, kind 2: the scoring sweep of cutbce_topk) is
  * bracketed by HIP events recorded on the launch stream. cutbce_profile_read waits for those events and
@@ -324,7 +378,8 @@ cutbce_status cutbce_mfma_ceiling_random(int blocks, int waves_per_block, int it
 const char *cutbce_status_string(cutbce_status s);
 
 /* Library version as major*10000 + minor*100 + patch (host). 0.2.0 added row_weight to cutbce_forward and
- * cutbce_backward; 0.3.0 added the sequence encoder's operators. */
+ * cutbce_backward; 0.3.0 added the sequence encoder's operators; 0.4.0 the softmax cross entropy, the gradients' norm
+ * and the AdamW step. */
 int cutbce_version(void);
 
 #ifdef __cplusplus

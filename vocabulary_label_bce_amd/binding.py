@@ -6,6 +6,7 @@ library has not been built, the first call raises (there is no fallback path).
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import functools
 import os
@@ -39,12 +40,26 @@ class Attention(ctypes.Structure):
                [("scale", ctypes.c_float)]
 
 
+class AdamWTensors(ctypes.Structure):
+    _fields_ = [("count", ctypes.c_int32), ("reserved", ctypes.c_int32)] + \
+               [(n, ctypes.c_void_p) for n in ("param", "grad", "exp_avg", "exp_avg_sq", "exp_avg_scale",
+                                               "exp_avg_sq_scale", "master", "n", "param_dtype", "grad_dtype",
+                                               "weight_decay")]
+
+
+class AdamW(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("step", "lr_at", "norm")] + \
+               [(n, ctypes.c_double) for n in ("max_norm", "lr", "eps", "beta1", "beta2")] + \
+               [("state_bits", ctypes.c_int32), ("seed", ctypes.c_uint32)]
+
+
 EXPORTS = ["cutbce_workspace_size", "cutbce_forward", "cutbce_forward_noalloc", "cutbce_backward",
            "cutbce_backward_reuse", "cutbce_validate_targets",
            "cutbce_targets_to_csr", "cutbce_topk",
            "cutbce_embedding_forward", "cutbce_embedding_backward_workspace_size", "cutbce_embedding_backward",
            "cutbce_layer_norm_forward", "cutbce_layer_norm_backward_workspace_size", "cutbce_layer_norm_backward",
            "cutbce_attention_workspace_size", "cutbce_attention_forward", "cutbce_attention_backward",
+           "cutbce_grad_norm_workspace_size", "cutbce_grad_norm", "cutbce_adamw_step",
            "cutbce_profile_enable", "cutbce_profile_read", "cutbce_mfma_ceiling",
            "cutbce_mfma_ceiling_random", "cutbce_status_string",
            "cutbce_version"]
@@ -82,6 +97,9 @@ def lib():
         L.cutbce_attention_workspace_size.argtypes = [AP, i32, ctypes.POINTER(sz)]
         L.cutbce_attention_forward.argtypes = [AP, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
         L.cutbce_attention_backward.argtypes = [AP, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.cutbce_grad_norm_workspace_size.argtypes = [i32, vp, ctypes.POINTER(sz)]
+        L.cutbce_grad_norm.argtypes = [i32, vp, vp, vp, vp, vp, sz, vp]
+        L.cutbce_adamw_step.argtypes = [ctypes.POINTER(AdamWTensors), ctypes.POINTER(AdamW), vp]
         L.cutbce_profile_enable.argtypes = [i32]
         L.cutbce_profile_read.argtypes = [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_int64), i32]
         L.cutbce_profile_enable.restype = i32
@@ -99,7 +117,8 @@ def lib():
                   "cutbce_embedding_backward_workspace_size", "cutbce_embedding_backward",
                   "cutbce_layer_norm_forward", "cutbce_layer_norm_backward_workspace_size",
                   "cutbce_layer_norm_backward", "cutbce_attention_workspace_size", "cutbce_attention_forward",
-                  "cutbce_attention_backward"):
+                  "cutbce_attention_backward", "cutbce_grad_norm_workspace_size", "cutbce_grad_norm",
+                  "cutbce_adamw_step"):
             getattr(L, f).restype = i32
         _lib = L
         return L
@@ -289,6 +308,35 @@ def attention_backward(a: Attention, dout, q, k, v, out, lse, cu_q, cu_k, k_lens
     _check(lib().cutbce_attention_backward(a, _at(dout), _at(q), _at(k), _at(v), _at(out), _at(lse), _at(cu_q),
                                            _at(cu_k), _at(k_lens), _at(dq), _at(dk), _at(dv), _at(ws),
                                            ws.numel() if ws is not None else 0, _raw_stream(stream)))
+
+
+# ---- the training step's operators ------------------------------------------------------------------------------
+
+
+@functools.lru_cache(maxsize=256)
+def grad_norm_workspace_size(sizes: tuple) -> int:
+    n = array.array("q", sizes)
+    b = ctypes.c_size_t(0)
+    _check(lib().cutbce_grad_norm_workspace_size(len(n), n.buffer_info()[0], ctypes.byref(b)))
+    return int(b.value)
+
+
+def grad_norm(pointers, sizes: tuple, dtypes, norm, ws, stream=None):
+    """cutbce_grad_norm: the tensors' addresses, elements and dtypes; norm float32 [1]."""
+    at = array.array("Q", pointers)
+    n = array.array("q", sizes)
+    types = array.array("i", dtypes)
+    _check(lib().cutbce_grad_norm(len(n), at.buffer_info()[0], n.buffer_info()[0], types.buffer_info()[0], _at(norm),
+                                  _at(ws), ws.numel(), _raw_stream(stream)))
+
+
+def adamw_step(n, pointers, types, decay, how: AdamW, stream=None):
+    """cutbce_adamw_step: pointers the seven lists of addresses (param, grad, exp_avg, exp_avg_sq, their scales, master;
+    None for a list that is not there), types the parameters' and gradients' dtypes."""
+    arrays = [None if p is None else array.array("Q", p) for p in pointers]
+    arrays += [array.array("q", n), array.array("i", types[0]), array.array("i", types[1]), array.array("f", decay)]
+    x = AdamWTensors(len(n), 0, *[None if a is None else a.buffer_info()[0] for a in arrays])
+    _check(lib().cutbce_adamw_step(ctypes.byref(x), ctypes.byref(how), _raw_stream(stream)))
 
 
 SWEEP_KINDS = ("rows_sweep", "items_sweep", "topk_sweep")

@@ -14,6 +14,7 @@ from .encoder import _first_order
 from .encoder import (cached_attention, embedding, embedding_backward, embedding_forward,  # noqa: F401
                       layer_norm, layer_norm_backward, layer_norm_forward, packed_attention,
                       packed_attention_backward, packed_attention_forward)
+from .optimizer import AdamW, adamw_step, grad_norm  # noqa: F401
 
 
 def _weights(row_weight, H):
