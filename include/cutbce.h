@@ -294,6 +294,46 @@ cutbce_status cutbce_attention_backward(const cutbce_attention *a, const void *d
                                         void *workspace, size_t workspace_bytes, void *stream);
 
 /* ---------------------------------------------------------------------------------------------------------
+ * Softmax cross entropy over the whole vocabulary, the logits never written to memory in whole. The conventions above
+ * hold (deterministic, launches only, checks before anything is enqueued).
+ *   z = scale * H E^T,  l_r = log(sum_v exp z_rv) - z_rt for the rows whose target t is in [0, vocab); the others are
+ *   left out. With row weights w_r (1 when row_weight is NULL) and W their sum over the counted rows:
+ *   loss = sum w_r l_r / W;  dz_rv = w_r / W * (softmax(z_r)_v - [v = t]);  dH = g scale dz E;  dE = g scale dz^T H.
+ *   W = 0 gives loss 0 and zero gradients.
+ * H [rows][dim], E [vocab][dim], dH, dE: dense, 16-byte aligned, of one dtype. 0 <= rows <= 2^20,
+ * 1 <= vocab <= 2^31 - 1025, dim a multiple of 8 up to 16384. Logits up to float32's largest value are taken; the
+ * probabilities are off by 2^-24 |lse| of themselves. A non-finite value in a row of H makes that row's loss, the
+ * loss and all of dE non-finite.
+ * bf16: products of bf16 values in float32; the logits' gradients are rounded to bf16 as operands of the gradients'
+ * products, all sums are float32 and every output is rounded once.
+ * --------------------------------------------------------------------------------------------------------- */
+
+/* Bytes of `saved`, which the forward leaves for the backward (256-byte aligned): the counted rows' H, statistics and,
+ * for dtype bf16 and dim <= 256, their dH. */
+cutbce_status cutbce_cross_entropy_saved_size(int64_t rows, int64_t vocab, int32_t dim, int32_t dtype, size_t *bytes);
+
+/* Bytes of workspace: which = 0 the forward without `saved`, 1 with it, 2 the backward. Bounded in vocab: the gradients
+ * are formed in pieces of the vocabulary where they need more than sums. */
+cutbce_status cutbce_cross_entropy_workspace_size(int64_t rows, int64_t vocab, int32_t dim, int32_t dtype,
+                                                  int32_t which, size_t *bytes);
+
+/* Forward.
+ *   targets    (device) [rows] int32 (id_bytes = 4) or int64 (id_bytes = 8); outside [0, vocab): the row is left out.
+ *   row_weight (device) float [rows], finite and >= 0 (read for counted rows only), or NULL.
+ *   loss       (device) float [1]; row_loss (device) float [rows], l_r or 0 for rows left out, or NULL.
+ *   saved      (device) for the backward, or NULL: the loss alone. scale is finite. */
+cutbce_status cutbce_cross_entropy_forward(int64_t rows, int64_t vocab, int32_t dim, int32_t dtype, int32_t id_bytes,
+                                           const void *H, const void *E, const void *targets, const float *row_weight,
+                                           float scale, float *loss, float *row_loss, void *saved, void *workspace,
+                                           size_t workspace_bytes, void *stream);
+
+/* Backward, with the forward's sizes, E, scale and `saved` (which is only read: any number of backwards may follow one
+ * forward). grad_loss (device) float [1]: the cotangent g. dH, dE: overwritten, each may be NULL to skip it. */
+cutbce_status cutbce_cross_entropy_backward(int64_t rows, int64_t vocab, int32_t dim, int32_t dtype, const void *E,
+                                            float scale, const float *grad_loss, const void *saved, void *dH, void *dE,
+                                            void *workspace, size_t workspace_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------------------------------------
  * A training step's other operators: the norm of all gradients and the AdamW step. They take lists of tensors (host
  * arrays of `count` entries, read before the call returns); the conventions above hold otherwise. Tensors are dense
  * and aligned to an element.

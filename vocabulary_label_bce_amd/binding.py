@@ -59,6 +59,8 @@ EXPORTS = ["cutbce_workspace_size", "cutbce_forward", "cutbce_forward_noalloc", 
            "cutbce_embedding_forward", "cutbce_embedding_backward_workspace_size", "cutbce_embedding_backward",
            "cutbce_layer_norm_forward", "cutbce_layer_norm_backward_workspace_size", "cutbce_layer_norm_backward",
            "cutbce_attention_workspace_size", "cutbce_attention_forward", "cutbce_attention_backward",
+           "cutbce_cross_entropy_saved_size", "cutbce_cross_entropy_workspace_size", "cutbce_cross_entropy_forward",
+           "cutbce_cross_entropy_backward",
            "cutbce_grad_norm_workspace_size", "cutbce_grad_norm", "cutbce_adamw_step",
            "cutbce_profile_enable", "cutbce_profile_read", "cutbce_mfma_ceiling",
            "cutbce_mfma_ceiling_random", "cutbce_status_string",
@@ -97,6 +99,10 @@ def lib():
         L.cutbce_attention_workspace_size.argtypes = [AP, i32, ctypes.POINTER(sz)]
         L.cutbce_attention_forward.argtypes = [AP, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
         L.cutbce_attention_backward.argtypes = [AP, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.cutbce_cross_entropy_saved_size.argtypes = [i64, i64, i32, i32, ctypes.POINTER(sz)]
+        L.cutbce_cross_entropy_workspace_size.argtypes = [i64, i64, i32, i32, i32, ctypes.POINTER(sz)]
+        L.cutbce_cross_entropy_forward.argtypes = [i64, i64, i32, i32, i32, vp, vp, vp, vp, f32, vp, vp, vp, vp, sz, vp]
+        L.cutbce_cross_entropy_backward.argtypes = [i64, i64, i32, i32, vp, f32, vp, vp, vp, vp, vp, sz, vp]
         L.cutbce_grad_norm_workspace_size.argtypes = [i32, vp, ctypes.POINTER(sz)]
         L.cutbce_grad_norm.argtypes = [i32, vp, vp, vp, vp, vp, sz, vp]
         L.cutbce_adamw_step.argtypes = [ctypes.POINTER(AdamWTensors), ctypes.POINTER(AdamW), vp]
@@ -117,7 +123,9 @@ def lib():
                   "cutbce_embedding_backward_workspace_size", "cutbce_embedding_backward",
                   "cutbce_layer_norm_forward", "cutbce_layer_norm_backward_workspace_size",
                   "cutbce_layer_norm_backward", "cutbce_attention_workspace_size", "cutbce_attention_forward",
-                  "cutbce_attention_backward", "cutbce_grad_norm_workspace_size", "cutbce_grad_norm",
+                  "cutbce_attention_backward", "cutbce_cross_entropy_saved_size",
+                  "cutbce_cross_entropy_workspace_size", "cutbce_cross_entropy_forward",
+                  "cutbce_cross_entropy_backward", "cutbce_grad_norm_workspace_size", "cutbce_grad_norm",
                   "cutbce_adamw_step"):
             getattr(L, f).restype = i32
         _lib = L
@@ -311,6 +319,33 @@ def attention_backward(a: Attention, dout, q, k, v, out, lse, cu_q, cu_k, k_lens
 
 
 # ---- the training step's operators ------------------------------------------------------------------------------
+
+
+@functools.lru_cache(maxsize=256)
+def cross_entropy_sizes(rows: int, vocab: int, dim: int, dtype):
+    """Bytes of `saved`, and of the workspaces: of the forward without it, the forward with it, and the backward."""
+    b, found = ctypes.c_size_t(0), []
+    _check(lib().cutbce_cross_entropy_saved_size(rows, vocab, dim, _dtype(dtype), ctypes.byref(b)))
+    found.append(int(b.value))
+    for which in range(3):
+        _check(lib().cutbce_cross_entropy_workspace_size(rows, vocab, dim, _dtype(dtype), which, ctypes.byref(b)))
+        found.append(int(b.value))
+    return tuple(found)
+
+
+def cross_entropy_forward(H, E, targets, row_weight, scale: float, loss, row_loss, saved, ws, stream=None):
+    """cutbce_cross_entropy_forward: row_weight, row_loss and saved may be None."""
+    _check(lib().cutbce_cross_entropy_forward(H.shape[0], E.shape[0], E.shape[1], _dtype(E.dtype),
+                                              targets.element_size(), _at(H), _at(E), _at(targets), _at(row_weight),
+                                              scale, _at(loss), _at(row_loss), _at(saved), _at(ws), ws.numel(),
+                                              _raw_stream(stream)))
+
+
+def cross_entropy_backward(rows: int, E, scale: float, grad, saved, dH, dE, ws, stream=None):
+    """cutbce_cross_entropy_backward: dH, dE overwritten, either may be None."""
+    _check(lib().cutbce_cross_entropy_backward(rows, E.shape[0], E.shape[1], _dtype(E.dtype), _at(E), scale, _at(grad),
+                                               _at(saved), _at(dH), _at(dE), _at(ws), ws.numel(),
+                                               _raw_stream(stream)))
 
 
 @functools.lru_cache(maxsize=256)

@@ -14,7 +14,6 @@
 // Tiles go from memory to LDS by direct buffer loads. A tile's rows past the sequence's end and columns past
 // head_dim lie outside the buffer's range and arrive as zeros. The 16-byte chunks of a row are permuted by the
 // row (swz) so that both the row-wise and the transposed reads spread over the LDS banks.
-#include <atomic>
 #include <type_traits>
 
 #include "encoder.h"
@@ -218,11 +217,6 @@ int64_t units_of(int64_t rows, int seqs, int m = kRows) { return rows / m + seqs
 // Keys that row t of the sequence sees.
 __device__ inline int seen_by(const Attn& a, const SeqRange& s, int64_t t) {
   return a.causal ? (int)clamp64(t + s.m - s.n + 1, 0, s.m) : s.m;
-}
-
-// Waits until at most N of the wave's loads are in flight and its LDS accesses are done, then for the workgroup.
-template <int N = 0> __device__ inline void wait_and_sync() {
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
 template <typename T, int DH> constexpr int key_tile() { return sizeof(T) == 4 && DH > 64 ? 32 : 64; }
@@ -1216,20 +1210,6 @@ bool few_rows(const Attn& a) { return !a.cu_q && !a.cu_k && a.q_rows % a.seqs ==
 size_t few_bytes(const Attn& a) {
   const int parts = few_parts(a);
   return parts > 1 ? (size_t)a.seqs * a.hk * parts * a.q_pitch * a.group * (128 + 2) * 4 : 0;
-}
-
-// Lets kernel F use `bytes` of LDS (the same for every launch of F): set once per device.
-template <auto F> hipError_t allow_lds(int bytes) {
-  static std::atomic<uint64_t> done{0};
-  if (bytes <= 65536) return hipSuccess;
-  int dev = 0;
-  hipError_t e = hipGetDevice(&dev);
-  if (e != hipSuccess) return e;
-  const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
-  if (done.load(std::memory_order_relaxed) & bit) return hipSuccess;
-  e = hipFuncSetAttribute((const void*)F, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == hipSuccess) done.fetch_or(bit, std::memory_order_relaxed);
-  return e;
 }
 
 template <typename T, int DH> hipError_t forward_t(const Attn& a, void* out, float* lse, char* ws, hipStream_t st) {

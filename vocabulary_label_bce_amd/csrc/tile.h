@@ -1,6 +1,8 @@
 // Building blocks of the kernels that multiply tiles with 32x32 matrix instructions: tiles of rows in LDS, the direct
 // loads that fill them, and the operands that the instructions read from them, row by row or transposed.
 #pragma once
+#include <atomic>
+
 #include "encoder.h"
 
 namespace cutbce {
@@ -19,7 +21,7 @@ typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+__host__ __device__ constexpr inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 __host__ __device__ constexpr inline int acc_row(int i, int h) { return (i / 4) * 8 + h * 4 + (i % 4); }
 
@@ -198,6 +200,11 @@ __device__ inline void product_t(f32x16* acc, const typename Mma<T>::P& p, uint3
     Mma<T>::template slot_t<NDB>(acc, k, Mma<T>::template load_t<DH>(k, base), p);
 }
 
+// Waits until at most N of the wave's loads are in flight and its LDS accesses are done, then for the workgroup.
+template <int N = 0> __device__ inline void wait_and_sync() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
 // The tile's operand of k-step t: the 32 rows from `at`, through the lane's base as above.
 template <typename T, int DH> __device__ inline uint32_t base_row(uint32_t at, int lane) {
   using Ti = Tile<T, DH>;
@@ -205,6 +212,20 @@ template <typename T, int DH> __device__ inline uint32_t base_row(uint32_t at, i
   return at + r * Ti::kRowB + ((lane / 32) ^ Ti::swz(r)) * 16;
 }
 __device__ inline u32x4 load_row(uint32_t base, int t) { return lds16(base ^ (2 * t * 16)); }
+
+// Lets kernel F use `bytes` of LDS (the same for every launch of F): set once per device.
+template <auto F> hipError_t allow_lds(int bytes) {
+  static std::atomic<uint64_t> done{0};
+  if (bytes <= 65536) return hipSuccess;
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return hipSuccess;
+  e = hipFuncSetAttribute((const void*)F, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == hipSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 
 }  // namespace
 

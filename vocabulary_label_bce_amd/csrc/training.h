@@ -51,4 +51,36 @@ static_assert(sizeof(NormArgs) <= 4096, "kernel arguments");
 hipError_t launch_norm(const NormArgs& a, unsigned blocks, hipStream_t st);
 hipError_t launch_norm_join(const double* partials, int64_t n, float* norm, hipStream_t st);
 
+// ---------------------------------------------------------------------------------------------------------
+// Softmax cross entropy: z = scale H E^T, rows with a target in [0, V) counted ("compact") 0 .. n - 1 in their order.
+// ---------------------------------------------------------------------------------------------------------
+constexpr int64_t kCeMaxRows = (int64_t)1 << 20;
+constexpr int kCeMaxDim = 16384;
+
+struct CeHead {
+  int32_t n;     // rows that have a target
+  float weight;  // sum of their weights
+};
+
+// What the forward leaves for the backward, as byte offsets into `saved`; arrays of R entries unless said.
+struct CeSaved {
+  size_t head, rows, place, target, lse, rest, coef, hc, dh, bytes;
+};
+struct Ce {
+  int64_t R, V;
+  int D, dtype;
+  float scale;
+  const void* E;
+  CeSaved at;
+  char* saved;
+  char* ws;
+};
+bool ce_swept(int D, int dtype);  // whether the sweeps of the narrow path take this problem
+CeSaved ce_saved(int64_t R, int64_t V, int D, int dtype);
+size_t ce_forward_bytes(int64_t R, int64_t V, int D, int dtype, bool want_grad);
+size_t ce_backward_bytes(int64_t R, int64_t V, int D, int dtype);
+hipError_t launch_ce_forward(const Ce& c, int id_bytes, const void* H, const void* targets, const float* weight,
+                             bool want_grad, float* loss, float* row_loss, hipStream_t st);
+hipError_t launch_ce_backward(const Ce& c, const float* grad, void* dH, void* dE, hipStream_t st);
+
 }  // namespace cutbce

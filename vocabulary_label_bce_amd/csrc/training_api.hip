@@ -27,9 +27,70 @@ int64_t chunks_of(int32_t count, const int64_t* n, int64_t chunk) {
   return sum;
 }
 
+constexpr int64_t kMaxVocab = (int64_t)0x7fffffff - 1024;
+
+cutbce_status check_ce(int64_t rows, int64_t vocab, int32_t dim, int32_t dtype) {
+  if (!known(dtype)) return CUTBCE_ERR_DTYPE;
+  if (rows < 0 || rows > kCeMaxRows || vocab < 1 || vocab > kMaxVocab) return CUTBCE_ERR_SHAPE;
+  if (dim < 8 || dim > kCeMaxDim || dim % 8 != 0) return CUTBCE_ERR_UNSUPPORTED;
+  return CUTBCE_OK;
+}
+
 }  // namespace
 
 extern "C" {
+
+cutbce_status cutbce_cross_entropy_saved_size(int64_t rows, int64_t vocab, int32_t dim, int32_t dtype, size_t* bytes) {
+  if (!bytes) return CUTBCE_ERR_NULL;
+  const cutbce_status s = check_ce(rows, vocab, dim, dtype);
+  if (s == CUTBCE_OK) *bytes = ce_saved(rows, vocab, dim, dtype).bytes;
+  return s;
+}
+
+cutbce_status cutbce_cross_entropy_workspace_size(int64_t rows, int64_t vocab, int32_t dim, int32_t dtype,
+                                                  int32_t which, size_t* bytes) {
+  if (!bytes) return CUTBCE_ERR_NULL;
+  const cutbce_status s = check_ce(rows, vocab, dim, dtype);
+  if (s != CUTBCE_OK) return s;
+  if (which < 0 || which > 2) return CUTBCE_ERR_SHAPE;
+  *bytes = which == 2 ? ce_backward_bytes(rows, vocab, dim, dtype) : ce_forward_bytes(rows, vocab, dim, dtype, which == 1);
+  return CUTBCE_OK;
+}
+
+cutbce_status cutbce_cross_entropy_forward(int64_t rows, int64_t vocab, int32_t dim, int32_t dtype, int32_t id_bytes,
+                                           const void* H, const void* E, const void* targets, const float* row_weight,
+                                           float scale, float* loss, float* row_loss, void* saved, void* workspace,
+                                           size_t workspace_bytes, void* stream) {
+  const cutbce_status s = check_ce(rows, vocab, dim, dtype);
+  if (s != CUTBCE_OK) return s;
+  if (id_bytes != 4 && id_bytes != 8) return CUTBCE_ERR_DTYPE;
+  if (!(fabsf(scale) < INFINITY)) return CUTBCE_ERR_SHAPE;
+  if (!E || !loss || !workspace || (rows > 0 && (!H || !targets))) return CUTBCE_ERR_NULL;
+  if (bad_align(H, 16) || bad_align(E, 16) || bad_align(targets, id_bytes) || bad_align(row_weight, 4) ||
+      bad_align(loss, 4) || bad_align(row_loss, 4) || bad_align(saved, 256) || bad_align(workspace, 256))
+    return CUTBCE_ERR_ALIGN;
+  if (workspace_bytes < ce_forward_bytes(rows, vocab, dim, dtype, saved != nullptr)) return CUTBCE_ERR_WORKSPACE;
+  Ce c = {rows, vocab, dim, dtype, scale, E, ce_saved(rows, vocab, dim, dtype), (char*)saved, (char*)workspace};
+  if (!saved) c.saved = c.ws + ce_forward_bytes(rows, vocab, dim, dtype, true);
+  return of_hip(launch_ce_forward(c, id_bytes, H, targets, row_weight, saved != nullptr, loss, row_loss,
+                                  (hipStream_t)stream));
+}
+
+cutbce_status cutbce_cross_entropy_backward(int64_t rows, int64_t vocab, int32_t dim, int32_t dtype, const void* E,
+                                            float scale, const float* grad_loss, const void* saved, void* dH, void* dE,
+                                            void* workspace, size_t workspace_bytes, void* stream) {
+  const cutbce_status s = check_ce(rows, vocab, dim, dtype);
+  if (s != CUTBCE_OK) return s;
+  if (!(fabsf(scale) < INFINITY)) return CUTBCE_ERR_SHAPE;
+  if (!E || !grad_loss || !saved || !workspace) return CUTBCE_ERR_NULL;
+  if (bad_align(E, 16) || bad_align(grad_loss, 4) || bad_align(saved, 256) || bad_align(dH, 16) || bad_align(dE, 16) ||
+      bad_align(workspace, 256))
+    return CUTBCE_ERR_ALIGN;
+  if (workspace_bytes < ce_backward_bytes(rows, vocab, dim, dtype)) return CUTBCE_ERR_WORKSPACE;
+  if (!dH && !dE) return CUTBCE_OK;
+  const Ce c = {rows, vocab, dim, dtype, scale, E, ce_saved(rows, vocab, dim, dtype), (char*)saved, (char*)workspace};
+  return of_hip(launch_ce_backward(c, grad_loss, dH, dE, (hipStream_t)stream));
+}
 
 cutbce_status cutbce_grad_norm_workspace_size(int32_t count, const int64_t* n, size_t* bytes) {
   if (!bytes || (count > 0 && !n)) return CUTBCE_ERR_NULL;

@@ -10,6 +10,7 @@ from __future__ import annotations
 import torch
 
 from . import binding as B
+from .cross_entropy import cross_entropy_backward, cross_entropy_forward, cut_cross_entropy  # noqa: F401
 from .encoder import _first_order
 from .encoder import (cached_attention, embedding, embedding_backward, embedding_forward,  # noqa: F401
                       layer_norm, layer_norm_backward, layer_norm_forward, packed_attention,
