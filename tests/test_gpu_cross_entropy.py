@@ -11,6 +11,8 @@ are relative to), for row r A_r = max_v A_rv:
            the products: |dz_rv| is off by q = (U + ep) w/W p_rv, the target's by (U + ep + 4 u) of itself
   dH     : |scale| sum_v q_rv |E_v| + (sums over V) (V / 64 + 128) u |scale| sum_v |dz_rv E_v|, + U of itself
   dE     : the same with rows
+  both   : float32's exponentials below its smallest normal number, 2^-126, are 0, and so are bf16 operands: each |dz_rv|
+           is off by at most 2^-126 on top, the gradients by |scale| 2^-126 sum_v |E_v| (the rows' H for dE)
 Sums over V (or rows) are split between lanes, tiles and parts; V / 64 + 128 covers the longest chain of additions.
 """
 import math
@@ -81,7 +83,7 @@ def _want(H, E, t, w, scale):
         full, off = torch.zeros_like(H if k is not None else E), torch.zeros_like(H if k is not None else E)
         sl = k if k is not None else slice(None)
         full[sl] = scale * x @ y
-        off[sl] = s * (e @ y.abs() + length * (x.abs() @ y.abs()))
+        off[sl] = s * (e @ y.abs() + length * (x.abs() @ y.abs()) + 2.0 ** -126 * y.abs().sum(0))
         res[n], bound[n] = full, off + U * (full.abs() + off)
     return res, bound
 

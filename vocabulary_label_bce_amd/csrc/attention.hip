@@ -109,37 +109,6 @@ template <typename T, int DH> struct Ahead {
   }
 };
 
-// The own operand: lane l has the chunks 2t + l / 32 of one row (zeros past head_dim, or where !live).
-template <typename T, int DH> __device__ inline void load_own(u32x4* own, const T* row, bool live, int dh, int lane) {
-  using Ti = Tile<T, DH>;
-  const int h = lane / 32;
-#pragma unroll
-  for (int t = 0; t < Ti::kNT; ++t) {
-    const int c = 2 * t + h;
-    u32x4 x = {0, 0, 0, 0};
-    if (live && c * 16 < dh * Ti::kEsz) x = *(const u32x4*)((const char*)row + c * 16);
-    own[t] = x;
-  }
-}
-
-// A transposed result (lane: one row, the features 32 db + acc_row) times f, to a row of dh elements.
-template <typename T, int NDB> __device__ inline void store_row(T* row, const f32x16* acc, float f, int dh, int lane) {
-  const int h = lane / 32;
-#pragma unroll
-  for (int db = 0; db < NDB; ++db)
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int d = db * 32 + 8 * k + 4 * h;
-      if (d < dh) {
-        typedef T V4 __attribute__((ext_vector_type(4)));
-        V4 v;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = (T)(acc[db][4 * k + j] * f);
-        *(V4*)(row + d) = v;
-      }
-    }
-}
-
 // Work units: tiles of M rows, units_of(rows, seqs, M) numbers for them.
 //
 // Up to 63 sequences: the units are numbered by the tiles left from them to one end of their sequence, most first

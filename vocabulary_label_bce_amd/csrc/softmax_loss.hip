@@ -11,15 +11,11 @@
 // The path of this file, for every size: the sums by one product kernel whose tiles are reduced where they are formed
 // (k_ce_sums); the gradients in pieces of the vocabulary, for each of which dz is formed again, kept in 16 (32) bits and
 // multiplied with E and with H (k_ce_dz, k_ce_dh, k_ce_de).
-#include "tile.h"
-#include "training.h"
+#include "softmax.h"
 
 namespace cutbce {
 
 namespace {
-
-__host__ __device__ constexpr inline int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
-template <typename T> __device__ inline T* at(char* base, size_t off) { return (T*)(base + off); }
 
 // ---------------------------------------------------------------------------------------------------------
 // Rows: which have a target, their weights' sum, and their H together.
@@ -72,12 +68,6 @@ __global__ __launch_bounds__(1024) void k_ce_rows(Ce c, const I* __restrict__ ta
     if (r < r1) place[r] = in ? i : -1;
     from += __popcll(m);
   }
-}
-
-// c, and the sign that H takes: a scale of 0 (or one too small) makes H 0.
-__device__ inline float base2(float scale) {
-  const float c = fabsf(scale) * kLog2e;
-  return c > 0.f ? c : 1.f;
 }
 
 // A wave has a row: its copy, and c times its product with its target's item.
@@ -603,11 +593,17 @@ template <typename T> Plan plan_of(int64_t R, int64_t V, int D) {
 struct ForwardPlan {
   size_t zt, each, part, bytes;
 };
-template <typename P> ForwardPlan forward_plan(int64_t R) {
+template <typename T> ForwardPlan forward_plan(int64_t R, int D, bool grad) {
+  using P = typename Sizes<T>::Sums;
   ForwardPlan f;
   size_t b = 0;
   f.zt = b, b += up(R * 4, 256);
   f.each = b, b += up(R * 4, 256);
+  if (ce_swept(D, sizeof(T) == 2)) {
+    f.part = b, b += ce_rows_bytes(R, D, grad);
+    f.bytes = b;
+    return f;
+  }
   // shares x tiles of rows are at most the grid, or one share each
   const int64_t tiles = cdiv(R, P::BN);
   f.part = b, b += up((tiles > kCeGrid ? tiles : kCeGrid) * P::BN * P::WM * 8, 256);
@@ -616,19 +612,24 @@ template <typename P> ForwardPlan forward_plan(int64_t R) {
 }
 
 template <typename T>
-hipError_t forward_t(const Ce& c, int id_bytes, const T* H, const void* targets, const float* weight, float* loss,
-                     float* row_loss, hipStream_t st) {
+hipError_t forward_t(const Ce& c, int id_bytes, const T* H, const void* targets, const float* weight, bool grad,
+                     float* loss, float* row_loss, hipStream_t st) {
   using P = typename Sizes<T>::Sums;
-  const ForwardPlan f = forward_plan<P>(c.R);
+  const ForwardPlan f = forward_plan<T>(c.R, c.D, grad);
   float *zt = (float*)(c.ws + f.zt), *each = (float*)(c.ws + f.each);
   float2* part = (float2*)(c.ws + f.part);
   if (id_bytes == 4) k_ce_rows<int32_t><<<1, 1024, 0, st>>>(c, (const int32_t*)targets, weight);
   else k_ce_rows<int64_t><<<1, 1024, 0, st>>>(c, (const int64_t*)targets, weight);
   if (c.R) k_ce_gather<T><<<(unsigned)cdiv(c.R, 4), 256, 0, st>>>(c, H, zt);
-  hipError_t e = allow_lds<k_ce_sums<P>>(P::kLds);
-  if (e != hipSuccess) return e;
-  if (c.R) k_ce_sums<P><<<kCeGrid, P::NL, P::kLds, st>>>(c, part);
-  if (c.R) k_ce_join<<<(unsigned)cdiv(c.R, 4), 256, 0, st>>>(c, JoinHow{P::BM, P::BN, kCeGrid, P::WM}, part, zt, row_loss, each);
+  if (ce_swept(c.D, c.dtype)) {
+    const hipError_t e = c.R ? launch_ce_rows(c, c.ws + f.part, grad, zt, row_loss, each, st) : hipSuccess;
+    if (e != hipSuccess) return e;
+  } else if (c.R) {
+    const hipError_t e = allow_lds<k_ce_sums<P>>(P::kLds);
+    if (e != hipSuccess) return e;
+    k_ce_sums<P><<<kCeGrid, P::NL, P::kLds, st>>>(c, part);
+    k_ce_join<<<(unsigned)cdiv(c.R, 4), 256, 0, st>>>(c, JoinHow{P::BM, P::BN, kCeGrid, P::WM}, part, zt, row_loss, each);
+  }
   k_ce_loss<<<1, 1024, 0, st>>>(c, each, loss);
   return hipGetLastError();
 }
@@ -673,25 +674,27 @@ CeSaved ce_saved(int64_t R, int64_t V, int D, int dtype) {
   size_t* each[] = {&s.rows, &s.place, &s.target, &s.lse, &s.rest, &s.coef};
   for (size_t* x : each) *x = b, b += up(R * 4, 256);
   s.hc = b, b += up(R * D * (dtype ? 2 : 4), 256);
-  s.dh = b;
+  s.dh = b, b += ce_swept(D, dtype) ? up(R * D * 4, 256) : 0;
   s.bytes = b;
   return s;
 }
 
 size_t ce_forward_bytes(int64_t R, int64_t V, int D, int dtype, bool want_grad) {
-  const size_t own = dtype ? forward_plan<Sizes<__bf16>::Sums>(R).bytes : forward_plan<Sizes<float>::Sums>(R).bytes;
+  const size_t own = dtype ? forward_plan<__bf16>(R, D, want_grad).bytes : forward_plan<float>(R, D, want_grad).bytes;
   return own + (want_grad ? 0 : ce_saved(R, V, D, dtype).bytes);
 }
 size_t ce_backward_bytes(int64_t R, int64_t V, int D, int dtype) {
+  if (ce_swept(D, dtype)) return ce_items_bytes(R, V, D);
   return dtype ? plan_of<__bf16>(R, V, D).bytes : plan_of<float>(R, V, D).bytes;
 }
 
 hipError_t launch_ce_forward(const Ce& c, int id_bytes, const void* H, const void* targets, const float* weight,
                              bool want_grad, float* loss, float* row_loss, hipStream_t st) {
-  return c.dtype ? forward_t<__bf16>(c, id_bytes, (const __bf16*)H, targets, weight, loss, row_loss, st)
-                 : forward_t<float>(c, id_bytes, (const float*)H, targets, weight, loss, row_loss, st);
+  return c.dtype ? forward_t<__bf16>(c, id_bytes, (const __bf16*)H, targets, weight, want_grad, loss, row_loss, st)
+                 : forward_t<float>(c, id_bytes, (const float*)H, targets, weight, want_grad, loss, row_loss, st);
 }
 hipError_t launch_ce_backward(const Ce& c, const float* grad, void* dH, void* dE, hipStream_t st) {
+  if (ce_swept(c.D, c.dtype)) return launch_ce_items(c, c.ws, grad, dH, dE, st);
   return c.dtype ? backward_t<__bf16>(c, grad, (__bf16*)dH, (__bf16*)dE, st)
                  : backward_t<float>(c, grad, (float*)dH, (float*)dE, st);
 }

@@ -1,0 +1,763 @@
+// Softmax cross entropy in two sweeps, for bfloat16 rows of up to 128 features: neither the logits nor their gradients
+// leave the registers.
+//
+// Forward: a wave owns 64 rows (as two blocks of 32) and sweeps a share of the vocabulary, 32 items a step:
+//   Z^T = E_step H^T,  P = exp2(c Z - ref),  sums += P,  dH^T += E_step^T P     (ref a row's reference)
+// Backward: a wave owns 64 items and sweeps all rows:
+//   Z = H_step E^T,  P = w/W exp2(c Z - lse),  dE^T += H_step^T P
+// A step's results have the owned rows (or items) as columns, so that a lane has values of one of them, and P is the
+// second product's operand as it stands; the step's own tile, read row by row and transposed, is the other operand of both.
+//
+// Two blocks a wave halve what is read from LDS for a product: with one, LDS delivers 128 bytes a cycle at the matrix
+// units' full rate, all that it can. They take about 400 registers, so a SIMD has one wave, and the products hide the
+// vector instructions of the same wave: in one turn of the loop the products Z of the next step and the gradient's of
+// the step before run while the exponentials of this step are formed, none depending on another. The order is pinned, a
+// share of the vector work behind each matrix instruction.
+#include "softmax.h"
+
+namespace cutbce {
+
+namespace {
+
+#define INLINED __attribute__((always_inline))
+
+constexpr int kNB = 2;                        // blocks of 32 that a wave owns
+constexpr int kStages = 5, kAhead = 3;        // of the ring in LDS; a stage's loads are issued this many stages early
+constexpr int kItemsGrid = 256;                // workgroups of the backward: one a CU
+constexpr float kMost = 0x1p80f;              // sums of exponentials beyond which a row takes a new reference
+
+__device__ inline uint32_t pack2(float a, float b) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)a, (__bf16)b});
+}
+
+// The ring of one workgroup and a wave's operands.
+// Waves a SIMD has: two where the registers allow it.
+template <int DP, bool ITEMS> constexpr int kWaves = DP <= 64 && !ITEMS ? 2 : 1;
+
+template <int DP, bool AUX, bool GRAD> struct Sweep {
+  using Ti = Tile<__bf16, DP>;
+  using Ld = Dma<__bf16, DP, kSweepStage, 256>;
+  using M = Mma<__bf16>;
+  static constexpr int NT = Ti::kNT, NDB = Ti::kNDB;            // steps of Z's product; blocks of features
+  static constexpr int kRow = Ti::kRowB, kTile = Ld::kBytes;    // bytes
+  static constexpr int kAux = AUX ? 1024 : 0;                   // three arrays of 64 values, and room for a fourth
+  static constexpr int kStage = kTile + kAux, kLds = kStages * kStage;
+  static constexpr int kLoads = Ld::kRounds + (AUX ? 1 : 0);    // of a wave for a stage
+  static constexpr bool kAlone = kWaves<DP, AUX> == 1 && GRAD, kHeld = kWaves<DP, AUX> == 1;
+  static_assert(NT == 2 * NDB, "");
+
+  Ld ld;
+  uint32_t lds0;
+  int wave, lane, h;
+  const __bf16* X;       // the streamed rows
+  int64_t rows, from;    // how many there are; the first of this share
+  int D;
+  u32x4 own[kNB][NT];    // the owned rows
+  u32x4 x[NT];           // a step's rows
+  bf16x8 t[NT];          // a step's rows, transposed
+  f32x16 z[2][kNB];      // of the steps in turn
+  uint32_t p[2][kNB][8];
+  f32x16 acc[NDB][kNB];
+  uint32_t row_off, col_off;
+  uint32_t ra[NT], ca[NT];
+
+  __device__ inline void init(char* lds, const __bf16* X_, int64_t rows_, int D_) {
+    lds0 = uni((uint32_t)(size_t)(CUTBCE_LDS char*)lds);
+    wave = uni(threadIdx.x / 64), lane = threadIdx.x % 64, h = lane / 32;
+    X = X_, rows = rows_, D = D_;
+    ld.init(threadIdx.x, D);
+    row_off = base_row<__bf16, DP>(0, lane), col_off = M::template base_t<DP>(0, lane);
+  }
+  __device__ inline uint32_t slot(int s) const { return lds0 + (uint32_t)(s % kStages) * kStage; }
+  __device__ static inline uint32_t step_of(int s) {  // from stage s's place in the ring to that of the next
+    return s % kStages == kStages - 1 ? (uint32_t)-((kStages - 1) * kStage) : (uint32_t)kStage;
+  }
+  // The wave's loads of a stage from `range` to LDS byte `dst`, as load_lds16 does them one by one.
+  __device__ inline void load_stage(u32x4 range, uint32_t dst) const {
+    static_assert(Ld::kRounds == 2 || Ld::kRounds == 4, "");
+    if constexpr (Ld::kRounds == 4) {
+      asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %5, 0 offen lds\n\t"
+                   "s_add_u32 m0, m0, 0x1000\n\ts_nop 1\n\tbuffer_load_dwordx4 %2, %5, 0 offen lds\n\t"
+                   "s_add_u32 m0, m0, 0x1000\n\ts_nop 1\n\tbuffer_load_dwordx4 %3, %5, 0 offen lds\n\t"
+                   "s_add_u32 m0, m0, 0x1000\n\ts_nop 1\n\tbuffer_load_dwordx4 %4, %5, 0 offen lds"
+                   :: "s"(uni(dst)), "v"(ld.offset(0, D)), "v"(ld.offset(1, D)), "v"(ld.offset(2, D)),
+                      "v"(ld.offset(3, D)), "s"(range) : "m0", "scc");
+    } else {
+      asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %3, 0 offen lds\n\t"
+                   "s_add_u32 m0, m0, 0x1000\n\ts_nop 1\n\tbuffer_load_dwordx4 %2, %3, 0 offen lds"
+                   :: "s"(uni(dst)), "v"(ld.offset(0, D)), "v"(ld.offset(1, D)), "s"(range) : "m0", "scc");
+    }
+  }
+  __device__ inline void load_owned(const __bf16* base, int64_t first, int64_t n) {
+#pragma unroll
+    for (int b = 0; b < kNB; ++b) {
+      const int64_t i = first + b * 32 + lane % 32;
+      load_own<__bf16, DP>(own[b], base + i * D, i < n, D, lane);
+    }
+  }
+  __device__ inline void clear() {
+#pragma unroll
+    for (int b = 0; b < kNB; ++b) {
+#pragma unroll
+      for (int d = 0; d < NDB; ++d) acc[d][b] = f32x16{};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) p[1][b][i] = 0;
+    }
+#pragma unroll
+    for (int k = 0; k < NT; ++k) t[k] = bf16x8{};
+  }
+  // Z's product of a step (x is then free): into z[to]
+  __device__ inline void first(int to) {
+#pragma unroll
+    for (int b = 0; b < kNB; ++b) z[to][b] = f32x16{};
+#pragma unroll
+    for (int k = 0; k < NT; ++k)
+#pragma unroll
+      for (int b = 0; b < kNB; ++b) z[to][b] = M::mma(x[k], own[b][k], z[to][b]);
+  }
+  __device__ inline void read_rows(uint32_t at) {
+#pragma unroll
+    for (int k = 0; k < NT; ++k) x[k] = load_row(at + row_off, k);
+  }
+  __device__ inline bf16x8 operand(int q, int b, int g) const {
+    return __builtin_bit_cast(bf16x8, u32x4{p[q][b][4 * g], p[q][b][4 * g + 1], p[q][b][4 * g + 2], p[q][b][4 * g + 3]});
+  }
+  __device__ inline void gradient(int q, int k, int b) {  // the k-th of NT parts of the product with p[q]
+    if constexpr (GRAD)
+      acc[k % NDB][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(t[k], operand(q, b, k / NDB), acc[k % NDB][b], 0, 0, 0);
+  }
+  // Where a SIMD has one wave, the products' sums stay in accumulation registers (left alone, the compiler moves all of
+  // them to the others and back in every turn, for the rare branch that rescales them), and results are read from there
+  // one by one, each in its place.
+  __device__ inline void settle() {
+    if constexpr (GRAD && kAlone) {
+#pragma unroll
+      for (int d = 0; d < NDB; ++d)
+#pragma unroll
+        for (int b = 0; b < kNB; ++b) asm volatile("" : "+a"(acc[d][b]));
+    }
+  }
+  __device__ inline float result(int q, int b, int e) {
+    if constexpr (kAlone) asm volatile("" : "+a"(z[q][b]));
+    return z[q][b][e];
+  }
+  // LDS addresses of the reads ahead: of the rows from stage `next` on, of the transposed rows from stage `here` on. They
+  // are moved on from stage to stage, an addition each.
+  __device__ inline void aim(uint32_t next, uint32_t here) {
+    if constexpr (!kHeld) {
+      ra[0] = next + row_off, ca[0] = here + col_off;
+      return;
+    }
+#pragma unroll
+    for (int k = 0; k < NT; ++k) {
+      ra[k] = (next + row_off) ^ (2 * k * 16);
+      const int db = k % NDB, e = k / NDB;
+      ca[k] = (here + col_off) ^ (((db * 4) ^ Ti::swz(8 * e)) * 16);
+    }
+  }
+  __device__ inline void move_on(uint32_t by_next, uint32_t by_here) {
+#pragma unroll
+    for (int k = 0; k < (kHeld ? NT : 1); ++k) ra[k] += by_next, ca[k] += by_here;
+  }
+  __device__ inline uint32_t row_at(int k) const { return kHeld ? ra[k] : ra[0] ^ (2 * k * 16); }
+  __device__ inline uint32_t col_at(int db, int e) const {
+    return kHeld ? ca[e * NDB + db] : ca[0] ^ (((db * 4) ^ Ti::swz(8 * e)) * 16);
+  }
+  template <int Q> __device__ inline void read_row(int k) { x[k] = lds16(row_at(k) + Q * 32 * kRow); }
+  template <int Q> __device__ inline void read_col(int k) {
+    const int db = k % NDB, g = k / NDB;
+    s16x4 y[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      y[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+          (CUTBCE_LDS s16x4*)(size_t)(col_at(db, e) + (Q * 32 + 16 * g + 8 * e) * kRow));
+    t[k] = __builtin_bit_cast(bf16x8, (s16x8)__builtin_shufflevector(y[0], y[1], 0, 1, 2, 3, 4, 5, 6, 7));
+  }
+  // One turn: Z of the next step, the gradient's product of the step before, and work(0 .. kSlots - 1) in between, a share
+  // of the vector instructions behind each matrix instruction: they run beside it, and the next one waits for them.
+  // Reads ahead: the rows of the step after the next, the transposed rows of this step.
+  static constexpr int kSlots = (GRAD ? 2 : 1) * NT * kNB;
+  template <int Q, typename F> __device__ inline void turn(F work) {
+    settle();
+#pragma unroll
+    for (int b = 0; b < kNB; ++b) z[1 - Q][b] = f32x16{};
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int k = 0; k < NT; ++k) {
+#pragma unroll
+      for (int b = 0; b < kNB; ++b) {
+        z[1 - Q][b] = M::mma(x[k], own[b][k], z[1 - Q][b]);
+        if (b == kNB - 1) read_row<Q>(k);
+        work((k * kNB + b) * (GRAD ? 2 : 1));
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (GRAD) {
+          gradient(1 - Q, k, b);
+          if (b == kNB - 1) read_col<Q>(k);
+          work((k * kNB + b) * 2 + 1);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+    }
+  }
+  // The exponentials of step Q's results, element e = i / kNB of block b = i % kNB in turn: one is begun in its slot, and
+  // added and packed in later ones, when it is there. argument(b, e, z) gives the exponent.
+  template <int Q, typename A> __device__ inline void element(int i, float* y, A argument) {
+    y[i & 3] = exp2_of(argument(i % kNB, i / kNB, result(Q, i % kNB, i / kNB)));
+  }
+  template <int Q> __device__ inline void finished(int i, const float* y) {
+    const int b = i % kNB, e = i / kNB;
+    if (e & 1) {
+      p[Q][b][e / 2] = pack2(y[(i - kNB) & 3], y[i & 3]);
+      asm volatile("" : "+v"(p[Q][b][e / 2]));  // (here: the compiler would move what is not needed before the next turn)
+    }
+  }
+  // The last step's part of the gradient.
+  __device__ inline void last(int q) {
+#pragma unroll
+    for (int k = 0; k < NT; ++k)
+#pragma unroll
+      for (int b = 0; b < kNB; ++b) gradient(q, k, b);
+  }
+};
+
+template <int N> __device__ inline void landed_and_sync() {
+  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+// ---------------------------------------------------------------------------------------------------------
+// Forward. part[row * shares + share]: the row's reference and the sum of its exponentials, its target left out;
+// sums[share][row]: those of the products.
+// ---------------------------------------------------------------------------------------------------------
+//
+// A row's reference is the largest of its first step. It holds unless logits rise by 55 above that, or none of those
+// items counts, or something is not finite: the unit is then marked in `off`, and a second launch (CAREFUL) goes through
+// the marked ones again, one product after the other, a row whose exponentials have grown taking its largest as reference.
+// The unit's other rows go through the same numbers again: what a row gets does not depend on the others.
+template <int DP, bool GRAD, bool CAREFUL>
+__global__ __launch_bounds__(256, (kWaves<DP, false>)) void k_ce_sweep_rows(Ce c, float2* __restrict__ part,
+                                                                   float* __restrict__ sums, int* __restrict__ off) {
+  using S = Sweep<DP, false, GRAD>;
+  extern __shared__ __align__(1024) char lds[];
+  const int n = at<CeHead>(c.saved, c.at.head)->n;
+  const int tiles = (n + kSweepRows - 1) / kSweepRows;
+  const int64_t stages = cdiv(c.V, kSweepStage);
+  const int shares = sweep_shares(tiles, stages, sweep_grid(c.D)), total = tiles * shares, per = (total + 7) / 8;
+  const float cc = base2(c.scale);
+  const int32_t* targets = at<int32_t>(c.saved, c.at.target);
+  S s;
+  s.init(lds, (const __bf16*)c.E, c.V, c.D);
+  for (int unit = blockIdx.x / 8; unit < per; unit += gridDim.x / 8) {
+    const int u = (blockIdx.x % 8) * per + unit;  // neighbours, on one XCD, read the same items
+    if (u >= total) break;
+    if (CAREFUL && !off[u]) continue;
+    const int tile = u % tiles, share = u / tiles;
+    const int64_t s0 = stages * share / shares;
+    const int count = (int)(stages * (share + 1) / shares - s0);
+    const int64_t own0 = (int64_t)tile * kSweepRows + s.wave * (kNB * 32);
+    s.load_owned(at<__bf16>(c.saved, c.at.hc), own0, n);
+    int target[kNB];
+    float ref[kNB], sum[kNB];
+#pragma unroll
+    for (int b = 0; b < kNB; ++b) {
+      const int64_t i = own0 + b * 32 + s.lane % 32;
+      target[b] = i < n ? targets[i] : -1;
+    }
+    auto fetch = [&](int k) INLINED {
+      const int64_t row = (s0 + k) * kSweepStage;
+      const u32x4 r = s.ld.range(s.X + row * c.D, k < count ? c.V - row : 0, c.D, c.D);
+      s.load_stage(r, s.slot(k) + s.wave * 1024);
+    };
+    auto start = [&]() INLINED {
+      wait_and_sync<>();  // (the ring's last readers are done, and stores, which the waits below would count)
+      s.clear();
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) fetch(k);
+      landed_and_sync<(kAhead - 1) * S::kLoads>();
+      s.read_rows(s.slot(0));
+      s.first(0);
+    };
+    // leaves out of step Q of stage k what is a row's target or past the vocabulary's end
+    auto leave_out = [&](auto half, int k) INLINED {
+      constexpr int Q = decltype(half)::value;
+      const int item0 = (int)((s0 + k) * kSweepStage) + Q * 32;
+      bool rare = item0 + 32 > c.V;
+#pragma unroll
+      for (int b = 0; b < kNB; ++b) rare |= (unsigned)(target[b] - item0) < 32u;
+      if (__builtin_expect(__any(rare), 0)) {
+#pragma unroll
+        for (int b = 0; b < kNB; ++b)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int item = item0 + acc_row(e, s.h);
+            if (item == target[b] || item >= c.V) s.z[Q][b][e] = -INFINITY;
+          }
+      }
+    };
+    using Even = std::integral_constant<int, 0>;
+    using Odd = std::integral_constant<int, 1>;
+    // the first step's largest
+    auto begin = [&]() INLINED {
+      leave_out(Even{}, 0);
+#pragma unroll
+      for (int b = 0; b < kNB; ++b) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) top = fmaxf(top, s.z[0][b][e]);
+        top = fmaxf(top, other_half(top)) * cc;
+        ref[b] = top > -INFINITY ? top : 0.f;
+        sum[b] = 0.f;
+      }
+    };
+    start();
+    begin();
+    if constexpr (!CAREFUL) {
+      s.read_rows(s.slot(0) + 32 * S::kRow);
+      s.aim(s.slot(1), s.slot(0));
+      auto step = [&](auto half, int k) INLINED {
+        constexpr int Q = decltype(half)::value;
+        leave_out(half, k);
+        float add[kNB][2] = {};
+        float y[4];
+        constexpr int ALL = kNB * 16, EACH = ALL / S::kSlots;
+        auto end = [&](int i) {
+          float& a = add[i % kNB][i / kNB & 1];
+          a += y[i & 3];
+          asm volatile("" : "+v"(a));
+          if (GRAD) s.template finished<Q>(i, y);
+        };
+        s.template turn<Q>([&](int w) {
+          if (Q == 0 && w == 1) fetch(k + kAhead);
+  #pragma unroll
+          for (int i = EACH * w; i < EACH * (w + 1); ++i) {
+            s.template element<Q>(i, y, [&](int b, int, float z) { return __builtin_fmaf(z, cc, -ref[b]); });
+            if (i) end(i - 1);
+          }
+        });
+        end(ALL - 1);
+  #pragma unroll
+        for (int b = 0; b < kNB; ++b) sum[b] += add[b][0] + add[b][1];
+      };
+      s.settle();
+      for (int k = 0; k < count; ++k) {
+        landed_and_sync<(kAhead - 2) * S::kLoads>();  // stage k + 1 is there
+        step(Even{}, k);
+        step(Odd{}, k);
+        s.move_on(S::step_of(k + 1), S::step_of(k));
+        s.settle();
+      }
+      s.last(1);
+      bool bad = false;
+#pragma unroll
+      for (int b = 0; b < kNB; ++b) bad |= !(sum[b] <= kMost) || !(sum[b] + other_half(sum[b]) >= 0.5f);
+      bad = __syncthreads_or(bad);
+      if (threadIdx.x == 0) off[u] = bad;
+    } else {
+      auto careful = [&](auto half, int k) INLINED {
+        constexpr int Q = decltype(half)::value;
+        if (Q == 1 || k > 0) {
+          s.read_rows(s.slot(k) + Q * 32 * S::kRow);
+          s.first(Q);
+          leave_out(half, k);
+        }
+#pragma unroll
+        for (int b = 0; b < kNB; ++b) {
+          for (int again = 0; again < 2; ++again) {
+            float add[2] = {};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              float y[2];
+#pragma unroll
+              for (int j = 0; j < 2; ++j) add[j] += y[j] = exp2_of(__builtin_fmaf(s.z[Q][b][2 * i + j], cc, -ref[b]));
+              s.p[Q][b][i] = pack2(y[0], y[1]);
+            }
+            const uint64_t over = __ballot(!(add[0] + add[1] <= kMost) || !(sum[b] <= kMost));
+            if (again || !over) {
+              sum[b] += add[0] + add[1];
+              break;
+            }
+            if (!((over >> s.lane | over >> (s.lane ^ 32)) & 1)) continue;
+            float top = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) top = fmaxf(top, s.z[Q][b][e]);
+            top = fmaxf(top, other_half(top)) * cc;
+            const float next = fmaxf(ref[b], top), f = exp2_of(ref[b] - next);
+            ref[b] = next;
+            sum[b] *= f;
+            if constexpr (GRAD) {
+#pragma unroll
+              for (int d = 0; d < S::NDB; ++d) s.acc[d][b] *= f;
+            }
+          }
+        }
+        if constexpr (GRAD) {
+          s.aim(s.slot(k), s.slot(k));
+#pragma unroll
+          for (int n = 0; n < S::NT; ++n) s.template read_col<Q>(n);
+          s.last(Q);
+        }
+      };
+      for (int k = 0; k < count; ++k) {
+        if (k) landed_and_sync<(kAhead - 1) * S::kLoads>();
+        careful(Even{}, k);
+        careful(Odd{}, k);
+        wait_and_sync<(kAhead - 1) * S::kLoads>();  // (the stage's place is read out)
+        fetch(k + kAhead);
+      }
+    }
+    wait_and_sync<>();  // no load may reach LDS after the unit's end
+#pragma unroll
+    for (int b = 0; b < kNB; ++b) {
+      const int64_t i = own0 + b * 32 + s.lane % 32;
+      const float whole = sum[b] + other_half(sum[b]);
+      if (i >= n) continue;
+      if (s.lane < 32) part[i * shares + share] = make_float2(ref[b], whole);
+      if constexpr (GRAD) {
+        f32x16 o[S::NDB];
+#pragma unroll
+        for (int d = 0; d < S::NDB; ++d) o[d] = s.acc[d][b];
+        store_row<float, S::NDB>(sums + ((int64_t)share * n + i) * c.D, o, 1.f, c.D, s.lane);
+      }
+    }
+  }
+}
+
+// A workgroup has a row of the batch: joins its shares' sums (and products, into saved's dH: without the cotangent and
+// scale).
+template <bool GRAD>
+__global__ __launch_bounds__(256) void k_ce_sweep_join(Ce c, const float2* __restrict__ part,
+                                                       const float* __restrict__ sums, const float* __restrict__ zt,
+                                                       float* __restrict__ row_loss, float* __restrict__ each) {
+  __shared__ float factor[kSweepUnits];
+  __shared__ float4 rest[GRAD ? 256 : 1];
+  const int64_t r = blockIdx.x;
+  const int tid = threadIdx.x, lane = tid % 64;
+  const int i = at<int32_t>(c.saved, c.at.place)[r];
+  if (i < 0) {
+    if (tid == 0 && row_loss) row_loss[r] = 0.f;
+    return;
+  }
+  const int n = at<CeHead>(c.saved, c.at.head)->n;
+  const int shares = sweep_shares((n + kSweepRows - 1) / kSweepRows, cdiv(c.V, kSweepStage), sweep_grid(c.D));
+  const float z = zt[i];
+  const float2* mine_part = part + (int64_t)i * shares;
+  float m = z;
+  for (int k = lane; k < shares; k += 64) m = fmaxf(m, mine_part[k].x);
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
+  float others = 0.f;
+  for (int k = lane; k < shares; k += 64) {
+    const float2 x = mine_part[k];
+    const float f = x.x == -INFINITY ? 0.f : exp2_of(x.x - m);
+    others += x.y * f;
+    if (GRAD && tid < 64) factor[k] = f;
+  }
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) others += __shfl_xor(others, o, 64);
+  const float mine = exp2_of(z - m), sum = others + mine;
+  if (tid == 0) {
+    const float l = mine == 1.f ? log1pf(others) : (m - z) * kLn2 + logf(sum);
+    at<float>(c.saved, c.at.lse)[i] = m + log2f(sum);
+    at<float>(c.saved, c.at.rest)[i] = others / sum;
+    each[i] = l;
+    if (row_loss) row_loss[r] = l;
+  }
+  if constexpr (GRAD) {
+    // a group of DL lanes has the row's features, four each; the groups share the shares
+    const int DL = c.D / 4, groups = 256 / DL, g = tid / DL, d = tid % DL * 4;
+    __syncthreads();
+    f32x4 s = {0.f, 0.f, 0.f, 0.f};
+    if (g < groups) {
+#pragma unroll 4
+      for (int k = g; k < shares; k += groups) s += *(const f32x4*)(sums + ((int64_t)k * n + i) * c.D + d) * factor[k];
+    }
+    rest[tid] = make_float4(s[0], s[1], s[2], s[3]);
+    __syncthreads();
+    if (g == 0) {
+      for (int k = 1; k < groups; ++k) {
+        const float4 x = rest[k * DL + tid];
+        s += f32x4{x.x, x.y, x.z, x.w};
+      }
+      const float coef = at<float>(c.saved, c.at.coef)[i];
+      const __bf16* item = (const __bf16*)c.E + (int64_t)at<int32_t>(c.saved, c.at.target)[i] * c.D + d;
+      float* to = at<float>(c.saved, c.at.dh) + (int64_t)i * c.D + d;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) to[j] = coef * ((s[j] - others * (float)item[j]) / sum);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------------------------------------
+// Backward.
+// ---------------------------------------------------------------------------------------------------------
+
+// What a row brings to its column of P: exp2(c z - shift), or at its target `own` instead.
+__global__ __launch_bounds__(256) void k_ce_shift(Ce c, float* __restrict__ shift, float* __restrict__ own) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= at<CeHead>(c.saved, c.at.head)->n) return;
+  const float coef = at<float>(c.saved, c.at.coef)[i];
+  shift[i] = at<float>(c.saved, c.at.lse)[i] - log2f(coef);
+  own[i] = -coef * at<float>(c.saved, c.at.rest)[i];
+}
+
+// The work, tiles of items (in steps of `spread`) x stages of rows, is one line that is cut into as many equal parts as there are workgroups
+// (each at least kLeast stages, where there is that much): a workgroup goes through whole tiles, and the ends of its part
+// are pieces of tiles that it shares with its neighbours. A piece's sums go to place 0 of its workgroup's two if it
+// begins where the part does, else to 1, and are joined by k_ce_pieces_join. (With whole tiles alone 100,000 items of 64
+// features, 391 tiles on 256 CUs, take 235 us.)
+constexpr int kLeast = 4;
+struct Line {
+  int64_t stages, total;  // of a tile, and of all
+  int parts;
+  __device__ inline Line(int n, int64_t V) {
+    stages = n > 0 ? cdiv(n, kSweepStage) : 1;
+    total = cdiv(V, kSweepRows) * stages;
+    parts = (int)(total / kLeast < kItemsGrid ? (total < kLeast ? 1 : total / kLeast) : kItemsGrid);
+  }
+  __device__ inline int64_t begin(int part) const { return total * part / parts; }
+};
+
+template <int DP>
+__global__ __launch_bounds__(256, (kWaves<DP, true>)) void k_ce_sweep_items(Ce c, const float* __restrict__ shift,
+                                                                            const float* __restrict__ own,
+                                                                            const float* __restrict__ grad,
+                                                                            int64_t spread, __bf16* __restrict__ dE,
+                                                                            float* __restrict__ sums) {
+  using S = Sweep<DP, true, true>;
+  extern __shared__ __align__(1024) char lds[];
+  const int n = at<CeHead>(c.saved, c.at.head)->n;
+  const float cc = base2(c.scale);
+  const Line line(n, c.V);
+  if ((int)blockIdx.x >= line.parts) return;
+  const int64_t from = line.begin(blockIdx.x), to = line.begin(blockIdx.x + 1), tiles = cdiv(c.V, kSweepRows);
+  S s;
+  s.init(lds, at<__bf16>(c.saved, c.at.hc), n, c.D);
+  const int32_t* targets = at<int32_t>(c.saved, c.at.target);
+  const void* aux = s.wave == 1 ? (const void*)targets : (s.wave == 2 ? (const void*)own : (const void*)shift);
+  for (int64_t x = from; x < to;) {
+    const int64_t at_tile = x / line.stages, tile = at_tile * spread % tiles;
+    const int s0 = (int)(x - at_tile * line.stages);
+    const int count = (int)(line.stages - s0 < to - x ? line.stages - s0 : to - x);
+    const bool whole = count == line.stages;
+    const int place = x == from ? 0 : 1;
+    x += count;
+    const int64_t own0 = tile * kSweepRows + s.wave * (kNB * 32);
+    s.load_owned((const __bf16*)c.E, own0, c.V);
+    s.clear();
+    auto fetch = [&](int k) INLINED {
+      const int64_t row = (int64_t)(s0 + k) * kSweepStage;
+      const int64_t left = k < count ? n - row : 0;
+      const u32x4 r = s.ld.range(s.X + row * c.D, left, c.D, c.D);
+      s.load_stage(r, s.slot(k) + s.wave * 1024);
+      load_lds4(buffer_of((const char*)aux + row * 4, (int)clamp64(left, 0, kSweepStage) * 4), s.lane * 4,
+                s.slot(k) + S::kTile + s.wave * 256);
+    };
+    wait_and_sync<>();  // (the ring's last readers are done, and stores, which the waits below would count)
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) fetch(k);
+    landed_and_sync<(kAhead - 1) * S::kLoads>();
+    s.read_rows(s.slot(0));
+    s.first(0);
+    s.read_rows(s.slot(0) + 32 * S::kRow);
+    f32x4 sh[4];
+    // the shifts of a step (four at a time, as the ones before are done with) and, a row a lane, its targets
+    auto shifts_at = [&](uint32_t at) INLINED {
+      at += 16 * s.h;
+      asm volatile("" : "+v"(at));
+      return at;
+    };
+    auto read_shift = [&](int k, uint32_t at) INLINED { sh[k] = *(CUTBCE_LDS const f32x4*)(size_t)(at + 32 * k); };
+    auto read_target = [&](uint32_t at) { return *(CUTBCE_LDS const int*)(size_t)(at + 256 + (s.lane % 32) * 4); };
+#pragma unroll
+    for (int k = 0; k < 4; ++k) read_shift(k, shifts_at(s.slot(0) + S::kTile));
+    int t_next = read_target(s.slot(0) + S::kTile);
+    s.aim(s.slot(1), s.slot(0));
+    auto step = [&](auto half, int k) INLINED {
+      constexpr int Q = decltype(half)::value;
+      const uint32_t ax = s.slot(k) + S::kTile + Q * 128, after = Q == 0 ? ax + 128 : s.slot(k + 1) + S::kTile;
+      const uint32_t shifts = shifts_at(after);
+      const int t = t_next;
+      float y[4];
+      constexpr int ALL = kNB * 16, EACH = ALL / S::kSlots;
+      s.template turn<Q>([&](int w) {
+        if (Q == 0 && w == 1) fetch(k + kAhead);
+        if (w == 2) t_next = read_target(after);
+#pragma unroll
+        for (int i = EACH * w; i < EACH * (w + 1); ++i) {
+          s.template element<Q>(i, y, [&](int, int e, float z) { return __builtin_fmaf(z, cc, -sh[e / 4][e % 4]); });
+          if (i % (4 * kNB) == 4 * kNB - 1) read_shift(i / (4 * kNB), shifts);
+          if (i) s.template finished<Q>(i - 1, y);
+        }
+      });
+      s.template finished<Q>(ALL - 1, y);
+      // a row whose target is among the wave's items (behind the last row all that is loaded is 0: a row of zeros, whose
+      // product is 0 whatever P is)
+      if (__builtin_expect(__any((unsigned)(t - (int)own0) < (unsigned)(kNB * 32)), 0)) {
+        uint32_t at = ax + 16 * s.h;
+        asm volatile("" : "+v"(at));  // (one address and constants, not an address each)
+        typedef int s32x4 __attribute__((ext_vector_type(4)));
+        const int item = (int)own0 + s.lane % 32;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const s32x4 tr = *(CUTBCE_LDS const s32x4*)(size_t)(at + 256 + 32 * k);
+          const f32x4 mine = *(CUTBCE_LDS const f32x4*)(size_t)(at + 512 + 32 * k);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint32_t both = pack2(mine[2 * j], mine[2 * j + 1]);
+#pragma unroll
+            for (int b = 0; b < kNB; ++b) {
+              uint32_t& p = s.p[Q][b][2 * k + j];
+              p = tr[2 * j] == item + b * 32 ? (p & 0xffff0000u) | (both & 0xffffu) : p;
+              p = tr[2 * j + 1] == item + b * 32 ? (p & 0xffffu) | (both & 0xffff0000u) : p;
+            }
+          }
+        }
+      }
+    };
+    s.settle();
+    for (int k = 0; k < count; ++k) {
+      landed_and_sync<(kAhead - 2) * S::kLoads>();
+      step(std::integral_constant<int, 0>{}, k);
+      step(std::integral_constant<int, 1>{}, k);
+      s.move_on(S::step_of(k + 1), S::step_of(k));
+      s.settle();
+    }
+    s.last(1);
+    wait_and_sync<>();
+    const float f = whole ? *grad * fabsf(c.scale) : 1.f;
+#pragma unroll
+    for (int b = 0; b < kNB; ++b) {
+      const int at = s.wave * (kNB * 32) + b * 32 + s.lane % 32;
+      const int64_t v = tile * kSweepRows + at;
+      if (v >= c.V) continue;
+      f32x16 o[S::NDB];
+#pragma unroll
+      for (int d = 0; d < S::NDB; ++d) o[d] = s.acc[d][b];
+      if (whole) store_row<__bf16, S::NDB>(dE + v * c.D, o, f, c.D, s.lane);
+      else store_row<float, S::NDB>(sums + ((int64_t)(blockIdx.x * 2 + place) * kSweepRows + at) * c.D, o, f, c.D, s.lane);
+    }
+  }
+}
+
+// The tiles that were shared: block.x - 1 is the first workgroup of one, the others follow it. Four features a lane.
+__global__ __launch_bounds__(256) void k_ce_pieces_join(Ce c, const float* __restrict__ sums, int64_t spread,
+                                                        const float* __restrict__ grad, __bf16* __restrict__ dE) {
+  const Line line(at<CeHead>(c.saved, c.at.head)->n, c.V);
+  const int part = blockIdx.x + 1;  // of the tile's second piece
+  if (part >= line.parts) return;
+  const int64_t cut = line.begin(part), at_tile = cut / line.stages, x0 = at_tile * line.stages;
+  const int64_t tile = at_tile * spread % cdiv(c.V, kSweepRows);
+  const int64_t before = line.begin(part - 1);
+  if (cut == x0 || before > x0) return;  // cut at a tile's end, or not the tile's first cut
+  const int64_t v0 = tile * kSweepRows, rows = c.V - v0 < kSweepRows ? c.V - v0 : kSweepRows;
+  const int64_t x = ((int64_t)blockIdx.y * 256 + threadIdx.x) * 4;
+  if (x >= rows * c.D) return;
+  const int64_t piece = (int64_t)kSweepRows * c.D;
+  f32x4 s = *(const f32x4*)(sums + ((int64_t)(part - 1) * 2 + (before == x0 ? 0 : 1)) * piece + x);
+  for (int p = part; p < line.parts && line.begin(p) < x0 + line.stages; ++p)
+    s += *(const f32x4*)(sums + (int64_t)p * 2 * piece + x);
+  const float f = *grad * fabsf(c.scale);
+  typedef __bf16 V4 __attribute__((ext_vector_type(4)));
+  V4 y;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) y[j] = (__bf16)(s[j] * f);
+  *(V4*)(dE + v0 * c.D + x) = y;
+}
+
+// dH of all rows from saved's, zeros for those left out: four features a lane.
+__global__ __launch_bounds__(256) void k_ce_dh_out(Ce c, const float* __restrict__ grad, __bf16* __restrict__ dH) {
+  const int64_t x = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (x >= c.R * c.D) return;
+  const int64_t r = x / c.D;
+  const int i = at<int32_t>(c.saved, c.at.place)[r];
+  f32x4 s = {0.f, 0.f, 0.f, 0.f};
+  if (i >= 0) s = *(const f32x4*)(at<float>(c.saved, c.at.dh) + (int64_t)i * c.D + (x - r * c.D)) * (*grad * c.scale);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) dH[x + j] = (__bf16)s[j];
+}
+
+// The line's tiles are taken in steps of this many, a golden section of them with no common factor: neighbouring items,
+// often those that are targets most, go to different workgroups. (One with the first 13 of 3,422 tiles of items by
+// popularity took 30% longer than the others.)
+int64_t spread_of(int64_t tiles) {
+  int64_t m = tiles * 618 / 1000;
+  if (m < 1) return 1;
+  for (;; ++m) {
+    int64_t a = m, b = tiles;
+    while (b) {
+      const int64_t t = a % b;
+      a = b, b = t;
+    }
+    if (a == 1) return m;
+  }
+}
+
+struct RowsPlan {
+  size_t part, sums, off, bytes;
+};
+RowsPlan rows_plan(int64_t R, int D, bool grad) {
+  // shares x rows are at most the units of all turns, or a share of each row
+  const int64_t some = (int64_t)kSweepUnits * (R < kSweepRows ? R : kSweepRows);
+  const int64_t slots = some > R ? some : R;
+  RowsPlan p;
+  size_t b = 0;
+  p.part = b, b += up(slots * 8, 256);
+  p.sums = b, b += grad ? up(slots * D * 4, 256) : 0;
+  const int64_t tiles = cdiv(R, kSweepRows);
+  p.off = b, b += up((tiles > kSweepUnits ? tiles : kSweepUnits) * 4, 256);
+  p.bytes = b;
+  return p;
+}
+
+template <int DP, bool GRAD> hipError_t rows_t(const Ce& c, char* ws, const float* zt, float* row_loss, float* each,
+                                               hipStream_t st) {
+  using S = Sweep<DP, false, GRAD>;
+  const RowsPlan p = rows_plan(c.R, c.D, GRAD);
+  hipError_t e = allow_lds<k_ce_sweep_rows<DP, GRAD, false>>(S::kLds);
+  if (e == hipSuccess) e = allow_lds<k_ce_sweep_rows<DP, GRAD, true>>(S::kLds);
+  if (e != hipSuccess) return e;
+  k_ce_sweep_rows<DP, GRAD, false><<<sweep_grid(c.D), 256, S::kLds, st>>>(c, (float2*)(ws + p.part), (float*)(ws + p.sums),
+                                                                    (int*)(ws + p.off));
+  k_ce_sweep_rows<DP, GRAD, true><<<sweep_grid(c.D), 256, S::kLds, st>>>(c, (float2*)(ws + p.part), (float*)(ws + p.sums),
+                                                                   (int*)(ws + p.off));
+  k_ce_sweep_join<GRAD><<<(unsigned)c.R, 256, 0, st>>>(c, (const float2*)(ws + p.part), (const float*)(ws + p.sums), zt,
+                                                       row_loss, each);
+  return hipGetLastError();
+}
+
+template <int DP> hipError_t items_t(const Ce& c, char* ws, const float* grad, __bf16* dE, hipStream_t st) {
+  using S = Sweep<DP, true, true>;
+  float *shift = (float*)ws, *own = (float*)(ws + up(c.R * 4, 256)), *sums = (float*)(ws + 2 * up(c.R * 4, 256));
+  const hipError_t e = allow_lds<k_ce_sweep_items<DP>>(S::kLds);
+  if (e != hipSuccess) return e;
+  if (c.R) k_ce_shift<<<(unsigned)cdiv(c.R, 256), 256, 0, st>>>(c, shift, own);
+  const int64_t far = spread_of(cdiv(c.V, kSweepRows));
+  k_ce_sweep_items<DP><<<kItemsGrid, 256, S::kLds, st>>>(c, shift, own, grad, far, dE, sums);
+  k_ce_pieces_join<<<dim3(kItemsGrid - 1, (unsigned)cdiv((int64_t)kSweepRows * c.D, 1024)), 256, 0, st>>>(c, sums, far,
+                                                                                                      grad, dE);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+bool ce_swept(int D, int dtype) { return dtype == 1 && D <= 128; }
+
+size_t ce_rows_bytes(int64_t R, int D, bool grad) { return rows_plan(R, D, grad).bytes; }
+hipError_t launch_ce_rows(const Ce& c, char* ws, bool grad, const float* zt, float* row_loss, float* each,
+                          hipStream_t st) {
+  if (c.D <= 64) return grad ? rows_t<64, true>(c, ws, zt, row_loss, each, st) : rows_t<64, false>(c, ws, zt, row_loss, each, st);
+  return grad ? rows_t<128, true>(c, ws, zt, row_loss, each, st) : rows_t<128, false>(c, ws, zt, row_loss, each, st);
+}
+size_t ce_items_bytes(int64_t R, int64_t V, int D) {
+  return 2 * up(R * 4, 256) + (size_t)kItemsGrid * 2 * kSweepRows * D * 4;
+}
+hipError_t launch_ce_items(const Ce& c, char* ws, const float* grad, void* dH, void* dE, hipStream_t st) {
+  if (dH && c.R) k_ce_dh_out<<<(unsigned)cdiv(c.R * c.D, 1024), 256, 0, st>>>(c, grad, (__bf16*)dH);
+  if (dE) {
+    const hipError_t e = c.D <= 64 ? items_t<64>(c, ws, grad, (__bf16*)dE, st) : items_t<128>(c, ws, grad, (__bf16*)dE, st);
+    if (e != hipSuccess) return e;
+  }
+  return hipGetLastError();
+}
+
+}  // namespace cutbce

@@ -75,7 +75,14 @@ struct Ce {
   char* saved;
   char* ws;
 };
-bool ce_swept(int D, int dtype);  // whether the sweeps of the narrow path take this problem
+// The sweeps of narrow rows (softmax_sweep.hip): the sums of all rows, with their dH in `saved` where grad, and the
+// backward.
+bool ce_swept(int D, int dtype);  // whether they take this problem
+size_t ce_rows_bytes(int64_t R, int D, bool grad);
+hipError_t launch_ce_rows(const Ce& c, char* ws, bool grad, const float* zt, float* row_loss, float* each,
+                          hipStream_t st);
+size_t ce_items_bytes(int64_t R, int64_t V, int D);
+hipError_t launch_ce_items(const Ce& c, char* ws, const float* grad, void* dH, void* dE, hipStream_t st);
 CeSaved ce_saved(int64_t R, int64_t V, int D, int dtype);
 size_t ce_forward_bytes(int64_t R, int64_t V, int D, int dtype, bool want_grad);
 size_t ce_backward_bytes(int64_t R, int64_t V, int D, int dtype);

@@ -65,13 +65,14 @@ cutbce_status cutbce_cross_entropy_forward(int64_t rows, int64_t vocab, int32_t 
   if (s != CUTBCE_OK) return s;
   if (id_bytes != 4 && id_bytes != 8) return CUTBCE_ERR_DTYPE;
   if (!(fabsf(scale) < INFINITY)) return CUTBCE_ERR_SHAPE;
-  if (!E || !loss || !workspace || (rows > 0 && (!H || !targets))) return CUTBCE_ERR_NULL;
+  const size_t need = ce_forward_bytes(rows, vocab, dim, dtype, saved != nullptr);
+  if (!E || !loss || (need && !workspace) || (rows > 0 && (!H || !targets))) return CUTBCE_ERR_NULL;
   if (bad_align(H, 16) || bad_align(E, 16) || bad_align(targets, id_bytes) || bad_align(row_weight, 4) ||
       bad_align(loss, 4) || bad_align(row_loss, 4) || bad_align(saved, 256) || bad_align(workspace, 256))
     return CUTBCE_ERR_ALIGN;
-  if (workspace_bytes < ce_forward_bytes(rows, vocab, dim, dtype, saved != nullptr)) return CUTBCE_ERR_WORKSPACE;
+  if (workspace_bytes < need) return CUTBCE_ERR_WORKSPACE;
   Ce c = {rows, vocab, dim, dtype, scale, E, ce_saved(rows, vocab, dim, dtype), (char*)saved, (char*)workspace};
-  if (!saved) c.saved = c.ws + ce_forward_bytes(rows, vocab, dim, dtype, true);
+  if (!saved) c.saved = c.ws + need - c.at.bytes;
   return of_hip(launch_ce_forward(c, id_bytes, H, targets, row_weight, saved != nullptr, loss, row_loss,
                                   (hipStream_t)stream));
 }
@@ -82,11 +83,12 @@ cutbce_status cutbce_cross_entropy_backward(int64_t rows, int64_t vocab, int32_t
   const cutbce_status s = check_ce(rows, vocab, dim, dtype);
   if (s != CUTBCE_OK) return s;
   if (!(fabsf(scale) < INFINITY)) return CUTBCE_ERR_SHAPE;
-  if (!E || !grad_loss || !saved || !workspace) return CUTBCE_ERR_NULL;
+  const size_t need = ce_backward_bytes(rows, vocab, dim, dtype);
+  if (!E || !grad_loss || !saved || (need && !workspace)) return CUTBCE_ERR_NULL;
   if (bad_align(E, 16) || bad_align(grad_loss, 4) || bad_align(saved, 256) || bad_align(dH, 16) || bad_align(dE, 16) ||
       bad_align(workspace, 256))
     return CUTBCE_ERR_ALIGN;
-  if (workspace_bytes < ce_backward_bytes(rows, vocab, dim, dtype)) return CUTBCE_ERR_WORKSPACE;
+  if (workspace_bytes < need) return CUTBCE_ERR_WORKSPACE;
   if (!dH && !dE) return CUTBCE_OK;
   const Ce c = {rows, vocab, dim, dtype, scale, E, ce_saved(rows, vocab, dim, dtype), (char*)saved, (char*)workspace};
   return of_hip(launch_ce_backward(c, grad_loss, dH, dE, (hipStream_t)stream));
