@@ -16,10 +16,11 @@ __device__ inline float base2(float scale) {
   return c > 0.f ? c : 1.f;
 }
 
-// Units of work of the sweep over the vocabulary: tiles of kSweepRows rows x shares of its stages of kSweepStage items. The
+// Units of work of the sweep over the vocabulary: tiles of sweep_rows(D) rows x shares of its stages of kSweepStage items. The
 // resident workgroups (one a CU, two of narrow rows) take units in turn, kSweepUnits at most: of the numbers of shares
 // that make one unit each, two, ... the first is taken that leaves at most 4% of them idle in the last turn, or the best.
-constexpr int kSweepRows = 256, kSweepStage = 64, kSweepUnits = 1024;
+constexpr int kSweepStage = 64, kSweepUnits = 1024;
+__host__ __device__ constexpr inline int sweep_rows(int D) { return D <= 128 ? 256 : 128; }
 __host__ __device__ constexpr inline int sweep_grid(int D) { return D <= 64 ? 512 : 256; }
 __host__ __device__ inline int sweep_shares(int64_t tiles, int64_t stages, int grid) {
   const int64_t most = stages / 4 < 1 ? 1 : stages / 4;

@@ -98,46 +98,98 @@ __global__ __launch_bounds__(256) void k_ce_gather(Ce c, const T* __restrict__ H
 }
 
 // ---------------------------------------------------------------------------------------------------------
-// Products. A workgroup forms a tile of BM x BN results from stages of kStageK features (128 bytes) of both sides in
-// LDS, two stages in turn: the loads of one are on their way while the other is multiplied.
+// Products. A workgroup forms a tile of BM x BN results from stages of KB bytes of features (K of them) of both sides, in
+// a ring of kRing stages in LDS. Turn s multiplies stage s; stage s + 1 has landed by then, so that its first operands are
+// read while the last products of stage s run, and stages s + 2 and s + 3 are on their way. Two waves a SIMD; the order of
+// matrix instructions and reads is pinned, a step's operands being read behind the products of the step before.
 // A side is read by rows (the features next to each other) or transposed (the results' index next to each other).
 // ---------------------------------------------------------------------------------------------------------
-template <typename T> constexpr int kStageK = 128 / sizeof(T);
+// 2 or 4 loads of 16 bytes a lane, as load_lds16 does them one by one: from bytes voff[] of the buffer to LDS bytes dst,
+// dst + STEP, ... (+ lane * 16). A stage's loads are what its turn waits for and its scalar work: one block with one wait
+// for its operands (as load_lds16 has), and what does not change from stage to stage formed before (the products of 4,096
+// rows with 32,768 items of 2,048 features took a third longer with the ranges formed for each stage).
+template <int N, int STEP> __device__ inline void load_lds16s(u32x4 buffer, const int* voff, uint32_t dst) {
+  static_assert(N == 2 || N == 4, "");
+  if constexpr (N == 2) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %3, 0 offen lds\n\t"
+                 "s_add_u32 m0, m0, %4\n\ts_nop 1\n\tbuffer_load_dwordx4 %2, %3, 0 offen lds"
+                 :: "s"(uni(dst)), "v"(voff[0]), "v"(voff[1]), "s"(buffer), "n"(STEP) : "m0", "scc");
+  } else {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %5, 0 offen lds\n\t"
+                 "s_add_u32 m0, m0, %6\n\ts_nop 1\n\tbuffer_load_dwordx4 %2, %5, 0 offen lds\n\t"
+                 "s_add_u32 m0, m0, %6\n\ts_nop 1\n\tbuffer_load_dwordx4 %3, %5, 0 offen lds\n\t"
+                 "s_add_u32 m0, m0, %6\n\ts_nop 1\n\tbuffer_load_dwordx4 %4, %5, 0 offen lds"
+                 :: "s"(uni(dst)), "v"(voff[0]), "v"(voff[1]), "v"(voff[2]), "v"(voff[3]), "s"(buffer), "n"(STEP)
+                 : "m0", "scc");
+  }
+}
 
-template <typename T, int ROWS, bool TRANS, int NL> struct Side;
+template <typename T, int ROWS, bool TRANS, int NL, int KB> struct Side;
 
-template <typename T, int ROWS, int NL> struct Side<T, ROWS, false, NL> {
-  static constexpr int K = kStageK<T>, kBytes = ROWS * 128;
+template <typename T, int ROWS, int NL, int KB> struct Side<T, ROWS, false, NL, KB> {
+  static constexpr int K = KB / sizeof(T), kBytes = ROWS * KB;
   using Ld = Dma<T, K, ROWS, NL>;
+  static_assert(Tile<T, K>::kRowB == KB && Ld::kLanes == NL, "");
+  static constexpr int kLoads = Ld::kRounds;
   Ld ld;
   int64_t stride;
-  __device__ inline void init(int64_t s) { stride = s, ld.init(threadIdx.x, s); }
-  // rows from `row` of `rows`, features from `k` of `left`
-  __device__ inline void load(const T* base, int64_t row, int64_t rows, int64_t k, int64_t left, uint32_t dst) const {
-    const int dh = (int)clamp64(left - k, 0, K);
-    const u32x4 r = ld.range(base + row * stride + k, dh > 0 ? rows - row : 0, stride, dh);
+  const T* from;  // of the next stage
+  int whole, left;  // bytes of a whole stage's range; features left
+  int voff[kLoads];
+  __device__ inline void init(int64_t s) {
+    stride = s, ld.init(threadIdx.x, s);
 #pragma unroll
-    for (int q = 0; q < Ld::kRounds; ++q) ld.round(q, r, dh, dst);
+    for (int q = 0; q < kLoads; ++q) voff[q] = ld.offset(q, K);
+  }
+  // stages from row `row` of `rows`, feature k of `end`, on
+  __device__ inline void start(const T* base, int64_t row, int64_t rows, int64_t k, int64_t end) {
+    const int64_t r = clamp64(rows - row, 0, ROWS);
+    from = base + row * stride + k;
+    whole = r > 0 ? (int)(((r - 1) * stride + K) * sizeof(T)) : 0;
+    left = r > 0 && end > k ? (int)(end - k) : 0;
+  }
+  // loads the next stage: zeros past the last feature, nothing (but as many loads) behind the last stage
+  __device__ inline void load(uint32_t dst) {
+    if (__builtin_expect(left >= K, 1)) {
+      load_lds16s<kLoads, NL * 16>(buffer_of(from, whole), voff, dst);
+    } else {
+      int v[kLoads];
+#pragma unroll
+      for (int q = 0; q < kLoads; ++q) v[q] = ld.offset(q, left);
+      load_lds16s<kLoads, NL * 16>(buffer_of(from, left > 0 ? whole - (K - left) * (int)sizeof(T) : 0), v, dst);
+    }
+    from += K, left -= left > 0 ? (left < K ? left : K) : 0;
   }
   __device__ static inline u32x4 op(uint32_t at, int block, int t, int lane) {
-    return load_row(base_row<T, K>(at, lane) + block * 32 * 128, t);
+    return load_row(base_row<T, K>(at, lane) + block * 32 * KB, t);
   }
 };
 
-template <typename T, int ROWS, int NL> struct Side<T, ROWS, true, NL> {
-  static constexpr int K = kStageK<T>, kSub = K * Tile<T, 128>::kRowB, kBytes = ROWS / 128 * kSub;
+template <typename T, int ROWS, int NL, int KB> struct Side<T, ROWS, true, NL, KB> {
+  static constexpr int K = KB / sizeof(T), kSub = K * Tile<T, 128>::kRowB, kBytes = ROWS / 128 * kSub;
   using Ld = Dma<T, 128, K, NL>;
+  static_assert(Ld::kLanes == NL && kSub == Ld::kRounds * NL * 16, "");
+  static constexpr int kLoads = ROWS / 128 * Ld::kRounds;
   Ld ld;
   int64_t stride;
+  const T* from;
+  int cols, left;  // of the tile's results; features left
+  int voff[kLoads];
   __device__ inline void init(int64_t s) { stride = s, ld.init(threadIdx.x, s); }
-  __device__ inline void load(const T* base, int64_t row, int64_t rows, int64_t k, int64_t left, uint32_t dst) const {
+  __device__ inline void start(const T* base, int64_t row, int64_t rows, int64_t k, int64_t end) {
+    from = base + k * stride + row;
+    cols = (int)clamp64(rows - row, 0, ROWS);
+    left = cols > 0 && end > k ? (int)(end - k) : 0;
 #pragma unroll
-    for (int b = 0; b < ROWS / 128; ++b) {
-      const int dh = (int)clamp64(rows - row - b * 128, 0, 128);
-      const u32x4 r = ld.range(base + k * stride + row + b * 128, dh > 0 ? left - k : 0, stride, dh);
-#pragma unroll
-      for (int q = 0; q < Ld::kRounds; ++q) ld.round(q, r, dh, dst + b * kSub);
+    for (int q = 0; q < kLoads; ++q) {
+      const int b = q / Ld::kRounds;
+      voff[q] = ld.offset(q % Ld::kRounds, (int)clamp64(cols - b * 128, 0, 128)) + b * 128 * (int)sizeof(T);
     }
+  }
+  __device__ inline void load(uint32_t dst) {
+    const int n = left < K ? left : K;
+    load_lds16s<kLoads, NL * 16>(buffer_of(from, n > 0 ? ((n - 1) * (int)stride + cols) * (int)sizeof(T) : 0), voff, dst);
+    from += K * stride, left -= n;
   }
   __device__ static inline u32x4 op(uint32_t at, int block, int t, int lane) {
     const uint32_t base = Mma<T>::template base_t<128>(at + block / 4 * kSub, lane);
@@ -152,25 +204,28 @@ template <typename T, int ROWS, int NL> struct Side<T, ROWS, true, NL> {
   }
 };
 
-template <typename T_, int WM_, int WN_, int TM_, int TN_, bool TA, bool TB> struct Product {
+template <typename T_, int WM_, int WN_, int TM_, int TN_, int KB_, bool TA, bool TB> struct Product {
   using T = T_;
-  static constexpr int WM = WM_, WN = WN_, TM = TM_, TN = TN_;
-  static constexpr int NL = 64 * WM * WN, BM = WM * TM * 32, BN = WN * TN * 32, K = kStageK<T>;
-  using A = Side<T, BM, TA, NL>;
-  using B = Side<T, BN, TB, NL>;
-  static constexpr int kStage = A::kBytes + B::kBytes, kLds = 2 * kStage;
+  static constexpr int WM = WM_, WN = WN_, TM = TM_, TN = TN_, KB = KB_;
+  static constexpr int NL = 64 * WM * WN, BM = WM * TM * 32, BN = WN * TN * 32, K = KB / sizeof(T);
+  using A = Side<T, BM, TA, NL, KB>;
+  using B = Side<T, BN, TB, NL, KB>;
+  static constexpr int kRing = 4, kStage = A::kBytes + B::kBytes, kLds = kRing * kStage;
+  static constexpr int NT = KB / 32;  // steps of a stage
+  static constexpr int kWaves = TM * TN > 8 ? 1 : 2;  // that a SIMD has
+  static_assert(kLds <= 160 * 1024, "");
   A a;
   B b;
   uint32_t lds0;
   int wave, lane, wm, wn;
   f32x16 acc[TM][TN];
+  u32x4 x[2][TM], y[2][TN];
 
   __device__ inline void init(char* lds, int64_t sa, int64_t sb) {
     lds0 = uni((uint32_t)(size_t)(CUTBCE_LDS char*)lds);
     wave = uni(threadIdx.x / 64), lane = threadIdx.x % 64;
     wm = wave % WM, wn = wave / WM;
     a.init(sa), b.init(sb);
-    clear();
   }
   __device__ inline void clear() {
 #pragma unroll
@@ -178,32 +233,74 @@ template <typename T_, int WM_, int WN_, int TM_, int TN_, bool TA, bool TB> str
 #pragma unroll
       for (int j = 0; j < TN; ++j) acc[i][j] = f32x16{};
   }
-  __device__ inline uint32_t stage(int s) const { return lds0 + (s & 1) * kStage; }
-  __device__ inline uint32_t wave_dst(int s) const { return stage(s) + wave * 1024; }
-  // (the first load's wave kilobyte; every round of a side covers NL * 16 bytes)
-  __device__ inline void multiply(int s) {
-    const uint32_t pa = stage(s), pb = pa + A::kBytes;
+  __device__ inline uint32_t stage(int s) const { return lds0 + (uint32_t)(s & (kRing - 1)) * kStage; }
+  // operand n of a step, in the order in which the products need them: TN of side b, then TM of side a
+  __device__ inline void read(int q, int n, uint32_t at, int t) {
+    if (n < TN) y[q][n] = B::op(at + A::kBytes, wn * TN + n, t, lane);
+    else x[q][n - TN] = A::op(at, wm * TM + n - TN, t, lane);
+  }
+  __device__ inline void fetch(int s) {
+    a.load(stage(s) + wave * 1024);
+    b.load(stage(s) + A::kBytes + wave * 1024);
+  }
+  // The products of `turns` stages, which a and b have been started for; before(s) is called before stage s is loaded,
+  // done(s) behind its products.
+  template <typename F, typename D> __device__ inline void run(int turns, F before, D done) {
+    constexpr int kLoads = A::kLoads + B::kLoads, OPS = TM + TN, MMAS = TM * TN;
+    static_assert(OPS <= MMAS, "");
+    clear();
+    wait_and_sync<>();  // (the ring's last readers are done, and what the waits below would count)
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      u32x4 x[TM], y[TN];
+    for (int s = 0; s < 3; ++s) before(s), fetch(s);
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(2 * kLoads) : "memory");
 #pragma unroll
-      for (int i = 0; i < TM; ++i) x[i] = A::op(pa, wm * TM + i, t, lane);
+    for (int n = 0; n < OPS; ++n) read(0, n, stage(0), 0);
+    for (int s = 0; s < turns; ++s) {
+      asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kLoads) : "memory");
 #pragma unroll
-      for (int j = 0; j < TN; ++j) y[j] = B::op(pb, wn * TN + j, t, lane);
+      for (int t = 0; t < NT; ++t) {
+        const uint32_t at = t + 1 < NT ? stage(s) : stage(s + 1);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int i = 0; i < TM; ++i)
-#pragma unroll
-        for (int j = 0; j < TN; ++j) acc[i][j] = Mma<T>::mma(x[i], y[j], acc[i][j]);
+        for (int m = 0; m < MMAS; ++m) {
+          acc[m / TN][m % TN] = Mma<T>::mma(x[t & 1][m / TN], y[t & 1][m % TN], acc[m / TN][m % TN]);
+          if (m < OPS) read((t + 1) & 1, m, at, (t + 1) % NT);
+          if (t == 0 && m == 1) before(s + 3), fetch(s + 3);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+      done(s);
     }
+    wait_and_sync<>();  // no load may reach LDS after the workgroup's end
   }
 };
 
-// The sums: results are items x rows, so that a lane has one row's.
-template <typename T> struct Sizes {
-  using Sums = Product<T, 2, 2, 2, 2, false, false>;
-  using Dh = Product<T, 2, 2, 2, 2, false, true>;
-  using De = Product<T, 2, 2, 2, 2, true, true>;
+template <typename T, bool BIG> struct Sizes {
+  static constexpr int KB = sizeof(T) == 2 ? 64 : 128;
+  using Sums = Product<T, 2, 2, 2, 2, KB, false, false>;
+  using Dh = Product<T, 2, 2, 2, 2, KB, false, true>;
+  using De = Product<T, 2, 2, 2, 2, KB, true, true>;
 };
+template <> struct Sizes<__bf16, true> {
+  using Sums = Product<__bf16, 2, 4, 4, 2, 64, false, false>;
+  using Dh = Product<__bf16, 2, 4, 4, 2, 64, false, true>;
+  using De = Product<__bf16, 2, 4, 4, 2, 64, true, true>;
+};
+bool big(int64_t R, int D, int dtype) { return dtype == 1 && R >= 512; }
+
+// Tile (i, j) of ni x nj for a workgroup: every eighth workgroup, those of one XCD, has tiles next to each other, in
+// blocks eight tiles wide, so that they read the same rows of both sides at about the same time. j is out of range for
+// workgroups beyond the last tile.
+struct TileAt {
+  int i, j;
+};
+__device__ inline TileAt tile_at(int bid, int ni, int nj) {
+  const int total = ni * nj, per = total / 8, more = total % 8, xcd = bid % 8;
+  if (bid / 8 >= per + (xcd < more ? 1 : 0)) return {0, 0x7fffffff};  // (a grid for more rows than there are)
+  const int u = xcd * per + (xcd < more ? xcd : more) + bid / 8;
+  const int group = u / (8 * nj), wide = ni - group * 8 < 8 ? ni - group * 8 : 8, in = u - group * 8 * nj;
+  return {group * 8 + in % wide, in / wide};
+}
 
 // Units of work: tiles of rows x shares of the vocabulary, the shares' number from that of the tiles. Neighbouring
 // units, which read the same items, go to workgroups of one XCD (every eighth).
@@ -219,10 +316,10 @@ __device__ inline Units units_of(int n, int64_t V, int bm, int bn, int grid) {
   u.shares = s < 1 ? 1 : (int)s;
   return u;
 }
-constexpr int kCeGrid = 512;  // workgroups of the sums: two a CU
+template <typename P> constexpr int kCeGrid = P::kLds > 80 * 1024 ? 256 : 512;  // workgroups of the sums: what is resident
 
 template <typename P>
-__global__ __launch_bounds__(P::NL, 2) void k_ce_sums(Ce c, float2* __restrict__ part) {
+__global__ __launch_bounds__(P::NL, P::kWaves) void k_ce_sums(Ce c, float2* __restrict__ part) {
   using T = typename P::T;
   extern __shared__ __align__(1024) char lds[];
   const int n = at<CeHead>(c.saved, c.at.head)->n;
@@ -242,55 +339,60 @@ __global__ __launch_bounds__(P::NL, 2) void k_ce_sums(Ce c, float2* __restrict__
     const int64_t v0 = steps * share / units.shares, v1 = steps * (share + 1) / units.shares;
     const int64_t row0 = (int64_t)tile * P::BN;
     float m[P::TN], s[P::TN];
-    int64_t target[P::TN];
+    int target[P::TN];
 #pragma unroll
     for (int j = 0; j < P::TN; ++j) {
       const int64_t i = row0 + (p.wn * P::TN + j) * 32 + p.lane % 32;
       m[j] = -INFINITY, s[j] = 0.f;
       target[j] = i < n ? targets[i] : -1;
     }
-    const int64_t all = (v1 - v0) * nk;
-    auto fetch = [&](int64_t x) {
-      if (x >= all) return;
-      const int64_t v = (v0 + x / nk) * P::BM, kk = x % nk * P::K;
-      const uint32_t dst = p.wave_dst((int)(x & 1));
-      p.a.load(E, v, c.V, kk, c.D, dst);
-      p.b.load(H, row0, n, kk, c.D, dst + P::A::kBytes);
-    };
-    wait_and_sync<>();  // (the unit before is done with both stages)
-    fetch(0);
-    for (int64_t x = 0; x < all; ++x) {
-      wait_and_sync<>();
-      fetch(x + 1);
-      p.multiply((int)(x & 1));
-      if (x % nk != nk - 1) continue;
-      const int64_t v = (v0 + x / nk) * P::BM + p.wm * P::TM * 32;
+    int64_t fv = v0 * P::BM;  // the items whose stages are being loaded, and how many of those are left
+    int fk = nk, left = nk;   // (left: of the tile that is being multiplied)
+    int v = (int)(v0 * P::BM) + p.wm * P::TM * 32;
+    p.a.start(E, fv, c.V, 0, c.D);
+    p.b.start(H, row0, n, 0, c.D);
+    p.run(
+        (int)(v1 - v0) * nk,
+        [&](int) {
+          if (fk == 0) {
+            fk = nk, fv += P::BM;
+            p.a.start(E, fv, fv < v1 * P::BM ? c.V : 0, 0, c.D);
+            p.b.start(H, row0, n, 0, c.D);
+          }
+          --fk;
+        },
+        [&](int) {
+          if (--left) return;
+          left = nk;
 #pragma unroll
-      for (int j = 0; j < P::TN; ++j) {
-        if (__any((target[j] >= v && target[j] < v + P::TM * 32) || v + P::TM * 32 > c.V)) {
+          for (int j = 0; j < P::TN; ++j) {
+            if (__any((unsigned)(target[j] - v) < (unsigned)(P::TM * 32)) || (int64_t)v + P::TM * 32 > c.V) {
 #pragma unroll
-          for (int i = 0; i < P::TM; ++i)
+              for (int i = 0; i < P::TM; ++i)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const int64_t item = v + i * 32 + acc_row(e, h);
-              if (item == target[j] || item >= c.V) p.acc[i][j][e] = -INFINITY;
+                for (int e = 0; e < 16; ++e) {
+                  const int item = i * 32 + acc_row(e, h);
+                  if (item == target[j] - v || (int64_t)v + item >= c.V) p.acc[i][j][e] = -INFINITY;
+                }
             }
-        }
-        float top = -INFINITY;
+            float top = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < P::TM; ++i)
+            for (int i = 0; i < P::TM; ++i)
 #pragma unroll
-          for (int e = 0; e < 16; ++e) top = fmaxf(top, p.acc[i][j][e]);
-        const float next = fmaxf(m[j], top * cc), base = next == -INFINITY ? 0.f : next;
-        s[j] *= exp2_of(m[j] - base);
-        m[j] = next;
+              for (int e = 0; e < 16; ++e) top = fmaxf(top, p.acc[i][j][e]);
+            const float next = fmaxf(m[j], top * cc), base = next == -INFINITY ? 0.f : next;
+            s[j] *= exp2_of(m[j] - base);
+            m[j] = next;
+            float add[2] = {};
 #pragma unroll
-        for (int i = 0; i < P::TM; ++i)
+            for (int i = 0; i < P::TM; ++i)
 #pragma unroll
-          for (int e = 0; e < 16; ++e) s[j] += exp2_of(__builtin_fmaf(p.acc[i][j][e], cc, -base));
-      }
-      p.clear();
-    }
+              for (int e = 0; e < 16; ++e) add[e & 1] += exp2_of(__builtin_fmaf(p.acc[i][j][e], cc, -base));
+            s[j] += add[0] + add[1];
+          }
+          p.clear();
+          v += P::BM;
+        });
     const int slots = units.shares * P::WM, slot = share * P::WM + p.wm;
 #pragma unroll
     for (int j = 0; j < P::TN; ++j) {
@@ -370,34 +472,26 @@ __host__ __device__ constexpr inline int item_at(int place) {  // of 16 bits
   return (place & ~12) | (place & 4) << 1 | (place & 8) >> 1;
 }
 template <typename P>
-__global__ __launch_bounds__(P::NL, 2) void k_ce_dz(Ce c, int64_t v0, int64_t width, typename P::T* __restrict__ dz) {
+__global__ __launch_bounds__(P::NL, P::kWaves) void k_ce_dz(Ce c, int64_t v0, int64_t width, typename P::T* __restrict__ dz) {
   using T = typename P::T;
   extern __shared__ __align__(1024) char lds[];
   const int n = at<CeHead>(c.saved, c.at.head)->n;
-  const int tiles = (int)(width / P::BM);  // of items; neighbours read the same rows
-  const int64_t row0 = (int64_t)(blockIdx.x / tiles) * P::BN, v = v0 + (int64_t)(blockIdx.x % tiles) * P::BM;
-  if (row0 >= n) return;
+  const TileAt tile = tile_at(blockIdx.x, (int)cdiv(n, P::BN), (int)(width / P::BM));
+  const int64_t row0 = (int64_t)tile.i * P::BN, v = v0 + (int64_t)tile.j * P::BM;
+  if (row0 >= n || tile.j >= width / P::BM) return;
   P p;
   p.init(lds, c.D, c.D);
   const T *E = (const T*)c.E, *H = at<T>(c.saved, c.at.hc);
   const int nk = (c.D + P::K - 1) / P::K, h = p.lane / 32;
-  auto fetch = [&](int x) {
-    if (x >= nk) return;
-    p.a.load(E, v, c.V, x * P::K, c.D, p.wave_dst(x));
-    p.b.load(H, row0, n, x * P::K, c.D, p.wave_dst(x) + P::A::kBytes);
-  };
-  fetch(0);
-  for (int x = 0; x < nk; ++x) {
-    wait_and_sync<>();
-    fetch(x + 1);
-    p.multiply(x);
-  }
+  p.a.start(E, v, c.V, 0, c.D);
+  p.b.start(H, row0, n, 0, c.D);
+  p.run(nk, [](int) {}, [](int) {});
   const float cc = base2(c.scale);
 #pragma unroll
   for (int j = 0; j < P::TN; ++j) {
     const int64_t i = row0 + (p.wn * P::TN + j) * 32 + p.lane % 32;
     if (i >= n) continue;
-    const float lse = at<float>(c.saved, c.at.lse)[i], coef = at<float>(c.saved, c.at.coef)[i];
+    const float coef = at<float>(c.saved, c.at.coef)[i], shift = at<float>(c.saved, c.at.lse)[i] - log2f(coef);
     const float mine = -coef * at<float>(c.saved, c.at.rest)[i];
     const int64_t target = at<int32_t>(c.saved, c.at.target)[i];
 #pragma unroll
@@ -405,10 +499,13 @@ __global__ __launch_bounds__(P::NL, 2) void k_ce_dz(Ce c, int64_t v0, int64_t wi
       const int64_t first = v + (p.wm * P::TM + b) * 32;
       float x[16];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const int64_t item = first + acc_row(e, h);
-        x[e] = coef * exp2_of(__builtin_fmaf(p.acc[b][j][e], cc, -lse));
-        x[e] = item == target ? mine : (item < c.V ? x[e] : 0.f);
+      for (int e = 0; e < 16; ++e) x[e] = exp2_of(__builtin_fmaf(p.acc[b][j][e], cc, -shift));
+      if (__any((uint64_t)(target - first) < 32u) || first + 32 > c.V) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int64_t item = first + acc_row(e, h);
+          x[e] = item == target ? mine : (item < c.V ? x[e] : 0.f);
+        }
       }
       T* to = dz + i * width + (first - v0);
       if constexpr (sizeof(T) == 2) {
@@ -424,32 +521,24 @@ __global__ __launch_bounds__(P::NL, 2) void k_ce_dz(Ce c, int64_t v0, int64_t wi
 
 // sums[part] (+)= dz E over the part's items: rows x features.
 template <typename P>
-__global__ __launch_bounds__(P::NL, 2) void k_ce_dh(Ce c, int64_t v0, int64_t width, int parts, int first,
+__global__ __launch_bounds__(P::NL, P::kWaves) void k_ce_dh(Ce c, int64_t v0, int64_t width, int parts, int first,
                                                     const typename P::T* __restrict__ dz, float* __restrict__ sums) {
   using T = typename P::T;
   extern __shared__ __align__(1024) char lds[];
   const int n = at<CeHead>(c.saved, c.at.head)->n;
-  const int cols = (c.D + P::BN - 1) / P::BN;
-  const int part = blockIdx.x % parts, tile = blockIdx.x / parts;
-  const int64_t row0 = (int64_t)(tile / cols) * P::BM, d0 = (int64_t)(tile % cols) * P::BN;
-  if (row0 >= n) return;
+  const int cols = (c.D + P::BN - 1) / P::BN, rows = (int)cdiv(n, P::BM);
+  const TileAt tile = tile_at(blockIdx.x, cols, rows * parts);  // (of one part of the items: neighbours read the same)
+  if (!rows || tile.j >= rows * parts) return;
+  const int part = tile.j / rows;
+  const int64_t row0 = (int64_t)(tile.j % rows) * P::BM, d0 = (int64_t)tile.i * P::BN;
   P p;
   p.init(lds, width, c.D);
   const int64_t left = c.V - v0 < width ? c.V - v0 : width, steps = (left + P::K - 1) / P::K;
   const int64_t x0 = steps * part / parts, x1 = steps * (part + 1) / parts;
   const T* E = (const T*)c.E + v0 * c.D;
-  auto fetch = [&](int64_t x) {
-    if (x >= x1) return;
-    const uint32_t dst = p.wave_dst((int)(x & 1));
-    p.a.load(dz, row0, n, x * P::K, width, dst);
-    p.b.load(E, d0, c.D, x * P::K, left, dst + P::A::kBytes);
-  };
-  fetch(x0);
-  for (int64_t x = x0; x < x1; ++x) {
-    wait_and_sync<>();
-    fetch(x + 1);
-    p.multiply((int)(x & 1));
-  }
+  p.a.start(dz, row0, n, x0 * P::K, x1 * P::K < width ? x1 * P::K : width);
+  p.b.start(E, d0, c.D, x0 * P::K, x1 * P::K < left ? x1 * P::K : left);
+  p.run((int)(x1 - x0), [](int) {}, [](int) {});
   float* to = sums + (int64_t)part * c.R * c.D;
   const int h = p.lane / 32;
 #pragma unroll
@@ -470,33 +559,27 @@ __global__ __launch_bounds__(P::NL, 2) void k_ce_dh(Ce c, int64_t v0, int64_t wi
 
 // dE of the piece: items x features, over all rows; or a part of the rows, to be joined.
 template <typename P, bool PART>
-__global__ __launch_bounds__(P::NL, 2) void k_ce_de(Ce c, int64_t v0, int64_t width, int parts,
+__global__ __launch_bounds__(P::NL, P::kWaves) void k_ce_de(Ce c, int64_t v0, int64_t width, int parts,
                                                     const typename P::T* __restrict__ dz, const float* __restrict__ grad,
                                                     typename P::T* __restrict__ dE, float* __restrict__ sums) {
   using T = typename P::T;
   extern __shared__ __align__(1024) char lds[];
   const int n = at<CeHead>(c.saved, c.at.head)->n;
   const int cols = (c.D + P::BN - 1) / P::BN;
-  const int part = PART ? blockIdx.x % parts : 0, tile = PART ? blockIdx.x / parts : blockIdx.x;
-  const int64_t u0 = (int64_t)(tile / cols) * P::BM, d0 = (int64_t)(tile % cols) * P::BN;
-  if (v0 + u0 >= c.V) return;
+  const int64_t left = c.V - v0 < width ? c.V - v0 : width;
+  const int items = (int)cdiv(left, P::BM);
+  const TileAt tile = tile_at(blockIdx.x, cols, items * (PART ? parts : 1));
+  if (tile.j >= items * (PART ? parts : 1)) return;
+  const int part = PART ? tile.j / items : 0;
+  const int64_t u0 = (int64_t)(PART ? tile.j % items : tile.j) * P::BM, d0 = (int64_t)tile.i * P::BN;
   P p;
   p.init(lds, width, c.D);
   const T* H = at<T>(c.saved, c.at.hc);
   const int64_t steps = (n + P::K - 1) / P::K;
   const int64_t x0 = PART ? steps * part / parts : 0, x1 = PART ? steps * (part + 1) / parts : steps;
-  auto fetch = [&](int64_t x) {
-    if (x >= x1) return;
-    const uint32_t dst = p.wave_dst((int)(x & 1));
-    p.a.load(dz, u0, width, x * P::K, n, dst);
-    p.b.load(H, d0, c.D, x * P::K, n, dst + P::A::kBytes);
-  };
-  fetch(x0);
-  for (int64_t x = x0; x < x1; ++x) {
-    wait_and_sync<>();
-    fetch(x + 1);
-    p.multiply((int)(x & 1));
-  }
+  p.a.start(dz, u0, width, x0 * P::K, x1 * P::K < n ? x1 * P::K : n);
+  p.b.start(H, d0, c.D, x0 * P::K, x1 * P::K < n ? x1 * P::K : n);
+  p.run((int)(x1 - x0), [](int) {}, [](int) {});
   const float f = PART ? 1.f : *grad * fabsf(c.scale);
   const int h = p.lane / 32;
 #pragma unroll
@@ -563,14 +646,14 @@ struct Plan {
   int dh_parts, de_parts;
   size_t dz, dh, de, bytes;  // offsets in the workspace
 };
-int64_t clamp_parts(int64_t tiles, int64_t steps, int64_t most) {
-  int64_t parts = tiles < 512 ? 512 / (tiles ? tiles : 1) : 1;  // two workgroups a CU
+int64_t clamp_parts(int64_t tiles, int64_t steps, int64_t most, int grid) {
+  int64_t parts = tiles < grid ? grid / (tiles ? tiles : 1) : 1;  // as many workgroups as are resident
   if (parts > steps / 4) parts = steps / 4;                     // each at least four stages
   if (parts > most) parts = most;
   return parts < 1 ? 1 : parts;
 }
-template <typename T> Plan plan_of(int64_t R, int64_t V, int D) {
-  using S = Sizes<T>;
+template <typename T, bool BIG> Plan plan_of(int64_t R, int64_t V, int D) {
+  using S = Sizes<T, BIG>;
   if (R < 1) R = 1;
   Plan p;
   // a piece's dz takes up to 256 MB, the size of the memory-side cache
@@ -579,9 +662,9 @@ template <typename T> Plan plan_of(int64_t R, int64_t V, int D) {
   if (width > up(V, 256)) width = up(V, 256);
   if (width > (int64_t)1 << 22) width = (int64_t)1 << 22;  // (offsets inside a stage are 32-bit)
   p.width = width;
-  p.dh_parts = (int)clamp_parts(cdiv(R, S::Dh::BM) * cdiv(D, S::Dh::BN), width / kStageK<T>,
-                                ((int64_t)256 << 20) / (R * D * 4) + 1);
-  p.de_parts = (int)clamp_parts(width / S::De::BM * cdiv(D, S::De::BN), cdiv(R, kStageK<T>), 64);
+  p.dh_parts = (int)clamp_parts(cdiv(R, S::Dh::BM) * cdiv(D, S::Dh::BN), width / S::Dh::K,
+                                ((int64_t)256 << 20) / (R * D * 4) + 1, kCeGrid<typename S::Dh>);
+  p.de_parts = (int)clamp_parts(width / S::De::BM * cdiv(D, S::De::BN), cdiv(R, S::De::K), 64, kCeGrid<typename S::De>);
   size_t b = 0;
   p.dz = b, b += up(R * width * (int64_t)sizeof(T), 256);
   p.dh = b, b += up((int64_t)p.dh_parts * R * D * 4, 256);
@@ -593,8 +676,8 @@ template <typename T> Plan plan_of(int64_t R, int64_t V, int D) {
 struct ForwardPlan {
   size_t zt, each, part, bytes;
 };
-template <typename T> ForwardPlan forward_plan(int64_t R, int D, bool grad) {
-  using P = typename Sizes<T>::Sums;
+template <typename T, bool BIG> ForwardPlan forward_plan(int64_t R, int D, bool grad) {
+  using P = typename Sizes<T, BIG>::Sums;
   ForwardPlan f;
   size_t b = 0;
   f.zt = b, b += up(R * 4, 256);
@@ -606,16 +689,16 @@ template <typename T> ForwardPlan forward_plan(int64_t R, int D, bool grad) {
   }
   // shares x tiles of rows are at most the grid, or one share each
   const int64_t tiles = cdiv(R, P::BN);
-  f.part = b, b += up((tiles > kCeGrid ? tiles : kCeGrid) * P::BN * P::WM * 8, 256);
+  f.part = b, b += up((tiles > kCeGrid<P> ? tiles : kCeGrid<P>) * P::BN * P::WM * 8, 256);
   f.bytes = b;
   return f;
 }
 
-template <typename T>
+template <typename T, bool BIG>
 hipError_t forward_t(const Ce& c, int id_bytes, const T* H, const void* targets, const float* weight, bool grad,
                      float* loss, float* row_loss, hipStream_t st) {
-  using P = typename Sizes<T>::Sums;
-  const ForwardPlan f = forward_plan<T>(c.R, c.D, grad);
+  using P = typename Sizes<T, BIG>::Sums;
+  const ForwardPlan f = forward_plan<T, BIG>(c.R, c.D, grad);
   float *zt = (float*)(c.ws + f.zt), *each = (float*)(c.ws + f.each);
   float2* part = (float2*)(c.ws + f.part);
   if (id_bytes == 4) k_ce_rows<int32_t><<<1, 1024, 0, st>>>(c, (const int32_t*)targets, weight);
@@ -627,16 +710,17 @@ hipError_t forward_t(const Ce& c, int id_bytes, const T* H, const void* targets,
   } else if (c.R) {
     const hipError_t e = allow_lds<k_ce_sums<P>>(P::kLds);
     if (e != hipSuccess) return e;
-    k_ce_sums<P><<<kCeGrid, P::NL, P::kLds, st>>>(c, part);
-    k_ce_join<<<(unsigned)cdiv(c.R, 4), 256, 0, st>>>(c, JoinHow{P::BM, P::BN, kCeGrid, P::WM}, part, zt, row_loss, each);
+    k_ce_sums<P><<<kCeGrid<P>, P::NL, P::kLds, st>>>(c, part);
+    k_ce_join<<<(unsigned)cdiv(c.R, 4), 256, 0, st>>>(c, JoinHow{P::BM, P::BN, kCeGrid<P>, P::WM}, part, zt, row_loss, each);
   }
   k_ce_loss<<<1, 1024, 0, st>>>(c, each, loss);
   return hipGetLastError();
 }
 
-template <typename T> hipError_t backward_t(const Ce& c, const float* grad, T* dH, T* dE, hipStream_t st) {
-  using S = Sizes<T>;
-  const Plan p = plan_of<T>(c.R, c.V, c.D);
+template <typename T, bool BIG>
+hipError_t backward_t(const Ce& c, const float* grad, T* dH, T* dE, hipStream_t st) {
+  using S = Sizes<T, BIG>;
+  const Plan p = plan_of<T, BIG>(c.R, c.V, c.D);
   T* dz = (T*)(c.ws + p.dz);
   float *dh = (float*)(c.ws + p.dh), *de = (float*)(c.ws + p.de);
   hipError_t e = allow_lds<k_ce_dz<typename S::Sums>>(S::Sums::kLds);
@@ -680,23 +764,30 @@ CeSaved ce_saved(int64_t R, int64_t V, int D, int dtype) {
 }
 
 size_t ce_forward_bytes(int64_t R, int64_t V, int D, int dtype, bool want_grad) {
-  const size_t own = dtype ? forward_plan<__bf16>(R, D, want_grad).bytes : forward_plan<float>(R, D, want_grad).bytes;
+  const size_t own = !dtype            ? forward_plan<float, false>(R, D, want_grad).bytes
+                     : big(R, D, dtype) ? forward_plan<__bf16, true>(R, D, want_grad).bytes
+                                        : forward_plan<__bf16, false>(R, D, want_grad).bytes;
   return own + (want_grad ? 0 : ce_saved(R, V, D, dtype).bytes);
 }
 size_t ce_backward_bytes(int64_t R, int64_t V, int D, int dtype) {
   if (ce_swept(D, dtype)) return ce_items_bytes(R, V, D);
-  return dtype ? plan_of<__bf16>(R, V, D).bytes : plan_of<float>(R, V, D).bytes;
+  return !dtype             ? plan_of<float, false>(R, V, D).bytes
+         : big(R, D, dtype) ? plan_of<__bf16, true>(R, V, D).bytes
+                            : plan_of<__bf16, false>(R, V, D).bytes;
 }
 
 hipError_t launch_ce_forward(const Ce& c, int id_bytes, const void* H, const void* targets, const float* weight,
                              bool want_grad, float* loss, float* row_loss, hipStream_t st) {
-  return c.dtype ? forward_t<__bf16>(c, id_bytes, (const __bf16*)H, targets, weight, want_grad, loss, row_loss, st)
-                 : forward_t<float>(c, id_bytes, (const float*)H, targets, weight, want_grad, loss, row_loss, st);
+  if (!c.dtype) return forward_t<float, false>(c, id_bytes, (const float*)H, targets, weight, want_grad, loss, row_loss, st);
+  return big(c.R, c.D, 1)
+             ? forward_t<__bf16, true>(c, id_bytes, (const __bf16*)H, targets, weight, want_grad, loss, row_loss, st)
+             : forward_t<__bf16, false>(c, id_bytes, (const __bf16*)H, targets, weight, want_grad, loss, row_loss, st);
 }
 hipError_t launch_ce_backward(const Ce& c, const float* grad, void* dH, void* dE, hipStream_t st) {
   if (ce_swept(c.D, c.dtype)) return launch_ce_items(c, c.ws, grad, dH, dE, st);
-  return c.dtype ? backward_t<__bf16>(c, grad, (__bf16*)dH, (__bf16*)dE, st)
-                 : backward_t<float>(c, grad, (float*)dH, (float*)dE, st);
+  if (!c.dtype) return backward_t<float, false>(c, grad, (float*)dH, (float*)dE, st);
+  return big(c.R, c.D, 1) ? backward_t<__bf16, true>(c, grad, (__bf16*)dH, (__bf16*)dE, st)
+                          : backward_t<__bf16, false>(c, grad, (__bf16*)dH, (__bf16*)dE, st);
 }
 
 }  // namespace cutbce

@@ -1,9 +1,9 @@
-// Softmax cross entropy in two sweeps, for bfloat16 rows of up to 128 features: neither the logits nor their gradients
+// Softmax cross entropy in two sweeps, for bfloat16 rows of up to 256 features: neither the logits nor their gradients
 // leave the registers.
 //
-// Forward: a wave owns 64 rows (as two blocks of 32) and sweeps a share of the vocabulary, 32 items a step:
+// Forward: a wave owns 64 rows (as two blocks of 32; beyond 128 features one block) and sweeps a share of the vocabulary, 32 items a step:
 //   Z^T = E_step H^T,  P = exp2(c Z - ref),  sums += P,  dH^T += E_step^T P     (ref a row's reference)
-// Backward: a wave owns 64 items and sweeps all rows:
+// Backward: a wave owns as many items and sweeps all rows:
 //   Z = H_step E^T,  P = w/W exp2(c Z - lse),  dE^T += H_step^T P
 // A step's results have the owned rows (or items) as columns, so that a lane has values of one of them, and P is the
 // second product's operand as it stands; the step's own tile, read row by row and transposed, is the other operand of both.
@@ -21,8 +21,10 @@ namespace {
 
 #define INLINED __attribute__((always_inline))
 
-constexpr int kNB = 2;                        // blocks of 32 that a wave owns
-constexpr int kStages = 5, kAhead = 3;        // of the ring in LDS; a stage's loads are issued this many stages early
+// Blocks of 32 that a wave owns; the ring's stages in LDS; and how many stages early a stage's loads are issued.
+template <int DP> constexpr int kBlocks = DP > 128 ? 1 : 2;
+template <int DP> constexpr int kStages = DP > 128 ? 4 : 5;
+template <int DP> constexpr int kAhead = kStages<DP> - 2;
 constexpr int kItemsGrid = 256;                // workgroups of the backward: one a CU
 constexpr float kMost = 0x1p80f;              // sums of exponentials beyond which a row takes a new reference
 
@@ -40,6 +42,8 @@ template <int DP, bool AUX, bool GRAD> struct Sweep {
   using Ld = Dma<__bf16, DP, kSweepStage, 256>;
   using M = Mma<__bf16>;
   static constexpr int NT = Ti::kNT, NDB = Ti::kNDB;            // steps of Z's product; blocks of features
+  static constexpr int kNB = kBlocks<DP>, kOwned = 4 * kNB * 32;  // a wave's blocks; what a workgroup owns
+  static constexpr int kStages = cutbce::kStages<DP>, kAhead = cutbce::kAhead<DP>;
   static constexpr int kRow = Ti::kRowB, kTile = Ld::kBytes;    // bytes
   static constexpr int kAux = AUX ? 1024 : 0;                   // three arrays of 64 values, and room for a fourth
   static constexpr int kStage = kTile + kAux, kLds = kStages * kStage;
@@ -75,19 +79,25 @@ template <int DP, bool AUX, bool GRAD> struct Sweep {
   }
   // The wave's loads of a stage from `range` to LDS byte `dst`, as load_lds16 does them one by one.
   __device__ inline void load_stage(u32x4 range, uint32_t dst) const {
-    static_assert(Ld::kRounds == 2 || Ld::kRounds == 4, "");
-    if constexpr (Ld::kRounds == 4) {
-      asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %5, 0 offen lds\n\t"
-                   "s_add_u32 m0, m0, 0x1000\n\ts_nop 1\n\tbuffer_load_dwordx4 %2, %5, 0 offen lds\n\t"
-                   "s_add_u32 m0, m0, 0x1000\n\ts_nop 1\n\tbuffer_load_dwordx4 %3, %5, 0 offen lds\n\t"
-                   "s_add_u32 m0, m0, 0x1000\n\ts_nop 1\n\tbuffer_load_dwordx4 %4, %5, 0 offen lds"
-                   :: "s"(uni(dst)), "v"(ld.offset(0, D)), "v"(ld.offset(1, D)), "v"(ld.offset(2, D)),
-                      "v"(ld.offset(3, D)), "s"(range) : "m0", "scc");
+    static_assert(Ld::kRounds == 2 || Ld::kRounds == 4 || Ld::kRounds == 8, "");
+    if constexpr (Ld::kRounds == 8) {
+      load_four(range, dst, 0);
+      load_four(range, dst + 0x4000, 4);
+    } else if constexpr (Ld::kRounds == 4) {
+      load_four(range, dst, 0);
     } else {
       asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %3, 0 offen lds\n\t"
                    "s_add_u32 m0, m0, 0x1000\n\ts_nop 1\n\tbuffer_load_dwordx4 %2, %3, 0 offen lds"
                    :: "s"(uni(dst)), "v"(ld.offset(0, D)), "v"(ld.offset(1, D)), "s"(range) : "m0", "scc");
     }
+  }
+  __device__ inline void load_four(u32x4 range, uint32_t dst, int q) const {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %5, 0 offen lds\n\t"
+                 "s_add_u32 m0, m0, 0x1000\n\ts_nop 1\n\tbuffer_load_dwordx4 %2, %5, 0 offen lds\n\t"
+                 "s_add_u32 m0, m0, 0x1000\n\ts_nop 1\n\tbuffer_load_dwordx4 %3, %5, 0 offen lds\n\t"
+                 "s_add_u32 m0, m0, 0x1000\n\ts_nop 1\n\tbuffer_load_dwordx4 %4, %5, 0 offen lds"
+                 :: "s"(uni(dst)), "v"(ld.offset(q, D)), "v"(ld.offset(q + 1, D)), "v"(ld.offset(q + 2, D)),
+                    "v"(ld.offset(q + 3, D)), "s"(range) : "m0", "scc");
   }
   __device__ inline void load_owned(const __bf16* base, int64_t first, int64_t n) {
 #pragma unroll
@@ -240,7 +250,7 @@ __global__ __launch_bounds__(256, (kWaves<DP, false>)) void k_ce_sweep_rows(Ce c
   using S = Sweep<DP, false, GRAD>;
   extern __shared__ __align__(1024) char lds[];
   const int n = at<CeHead>(c.saved, c.at.head)->n;
-  const int tiles = (n + kSweepRows - 1) / kSweepRows;
+  const int tiles = (n + S::kOwned - 1) / S::kOwned;
   const int64_t stages = cdiv(c.V, kSweepStage);
   const int shares = sweep_shares(tiles, stages, sweep_grid(c.D)), total = tiles * shares, per = (total + 7) / 8;
   const float cc = base2(c.scale);
@@ -254,12 +264,12 @@ __global__ __launch_bounds__(256, (kWaves<DP, false>)) void k_ce_sweep_rows(Ce c
     const int tile = u % tiles, share = u / tiles;
     const int64_t s0 = stages * share / shares;
     const int count = (int)(stages * (share + 1) / shares - s0);
-    const int64_t own0 = (int64_t)tile * kSweepRows + s.wave * (kNB * 32);
+    const int64_t own0 = (int64_t)tile * S::kOwned + s.wave * (S::kNB * 32);
     s.load_owned(at<__bf16>(c.saved, c.at.hc), own0, n);
-    int target[kNB];
-    float ref[kNB], sum[kNB];
+    int target[S::kNB];
+    float ref[S::kNB], sum[S::kNB];
 #pragma unroll
-    for (int b = 0; b < kNB; ++b) {
+    for (int b = 0; b < S::kNB; ++b) {
       const int64_t i = own0 + b * 32 + s.lane % 32;
       target[b] = i < n ? targets[i] : -1;
     }
@@ -272,8 +282,8 @@ __global__ __launch_bounds__(256, (kWaves<DP, false>)) void k_ce_sweep_rows(Ce c
       wait_and_sync<>();  // (the ring's last readers are done, and stores, which the waits below would count)
       s.clear();
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) fetch(k);
-      landed_and_sync<(kAhead - 1) * S::kLoads>();
+      for (int k = 0; k < S::kAhead; ++k) fetch(k);
+      landed_and_sync<(S::kAhead - 1) * S::kLoads>();
       s.read_rows(s.slot(0));
       s.first(0);
     };
@@ -283,10 +293,10 @@ __global__ __launch_bounds__(256, (kWaves<DP, false>)) void k_ce_sweep_rows(Ce c
       const int item0 = (int)((s0 + k) * kSweepStage) + Q * 32;
       bool rare = item0 + 32 > c.V;
 #pragma unroll
-      for (int b = 0; b < kNB; ++b) rare |= (unsigned)(target[b] - item0) < 32u;
+      for (int b = 0; b < S::kNB; ++b) rare |= (unsigned)(target[b] - item0) < 32u;
       if (__builtin_expect(__any(rare), 0)) {
 #pragma unroll
-        for (int b = 0; b < kNB; ++b)
+        for (int b = 0; b < S::kNB; ++b)
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const int item = item0 + acc_row(e, s.h);
@@ -300,7 +310,7 @@ __global__ __launch_bounds__(256, (kWaves<DP, false>)) void k_ce_sweep_rows(Ce c
     auto begin = [&]() INLINED {
       leave_out(Even{}, 0);
 #pragma unroll
-      for (int b = 0; b < kNB; ++b) {
+      for (int b = 0; b < S::kNB; ++b) {
         float top = -INFINITY;
 #pragma unroll
         for (int e = 0; e < 16; ++e) top = fmaxf(top, s.z[0][b][e]);
@@ -317,30 +327,30 @@ __global__ __launch_bounds__(256, (kWaves<DP, false>)) void k_ce_sweep_rows(Ce c
       auto step = [&](auto half, int k) INLINED {
         constexpr int Q = decltype(half)::value;
         leave_out(half, k);
-        float add[kNB][2] = {};
+        float add[S::kNB][2] = {};
         float y[4];
-        constexpr int ALL = kNB * 16, EACH = ALL / S::kSlots;
+        constexpr int ALL = S::kNB * 16;
         auto end = [&](int i) {
-          float& a = add[i % kNB][i / kNB & 1];
+          float& a = add[i % S::kNB][i / S::kNB & 1];
           a += y[i & 3];
           asm volatile("" : "+v"(a));
           if (GRAD) s.template finished<Q>(i, y);
         };
         s.template turn<Q>([&](int w) {
-          if (Q == 0 && w == 1) fetch(k + kAhead);
+          if (Q == 0 && w == 1) fetch(k + S::kAhead);
   #pragma unroll
-          for (int i = EACH * w; i < EACH * (w + 1); ++i) {
+          for (int i = ALL * w / S::kSlots; i < ALL * (w + 1) / S::kSlots; ++i) {
             s.template element<Q>(i, y, [&](int b, int, float z) { return __builtin_fmaf(z, cc, -ref[b]); });
             if (i) end(i - 1);
           }
         });
         end(ALL - 1);
   #pragma unroll
-        for (int b = 0; b < kNB; ++b) sum[b] += add[b][0] + add[b][1];
+        for (int b = 0; b < S::kNB; ++b) sum[b] += add[b][0] + add[b][1];
       };
       s.settle();
       for (int k = 0; k < count; ++k) {
-        landed_and_sync<(kAhead - 2) * S::kLoads>();  // stage k + 1 is there
+        landed_and_sync<(S::kAhead - 2) * S::kLoads>();  // stage k + 1 is there
         step(Even{}, k);
         step(Odd{}, k);
         s.move_on(S::step_of(k + 1), S::step_of(k));
@@ -349,7 +359,7 @@ __global__ __launch_bounds__(256, (kWaves<DP, false>)) void k_ce_sweep_rows(Ce c
       s.last(1);
       bool bad = false;
 #pragma unroll
-      for (int b = 0; b < kNB; ++b) bad |= !(sum[b] <= kMost) || !(sum[b] + other_half(sum[b]) >= 0.5f);
+      for (int b = 0; b < S::kNB; ++b) bad |= !(sum[b] <= kMost) || !(sum[b] + other_half(sum[b]) >= 0.5f);
       bad = __syncthreads_or(bad);
       if (threadIdx.x == 0) off[u] = bad;
     } else {
@@ -361,7 +371,7 @@ __global__ __launch_bounds__(256, (kWaves<DP, false>)) void k_ce_sweep_rows(Ce c
           leave_out(half, k);
         }
 #pragma unroll
-        for (int b = 0; b < kNB; ++b) {
+        for (int b = 0; b < S::kNB; ++b) {
           for (int again = 0; again < 2; ++again) {
             float add[2] = {};
 #pragma unroll
@@ -398,16 +408,16 @@ __global__ __launch_bounds__(256, (kWaves<DP, false>)) void k_ce_sweep_rows(Ce c
         }
       };
       for (int k = 0; k < count; ++k) {
-        if (k) landed_and_sync<(kAhead - 1) * S::kLoads>();
+        if (k) landed_and_sync<(S::kAhead - 1) * S::kLoads>();
         careful(Even{}, k);
         careful(Odd{}, k);
-        wait_and_sync<(kAhead - 1) * S::kLoads>();  // (the stage's place is read out)
-        fetch(k + kAhead);
+        wait_and_sync<(S::kAhead - 1) * S::kLoads>();  // (the stage's place is read out)
+        fetch(k + S::kAhead);
       }
     }
     wait_and_sync<>();  // no load may reach LDS after the unit's end
 #pragma unroll
-    for (int b = 0; b < kNB; ++b) {
+    for (int b = 0; b < S::kNB; ++b) {
       const int64_t i = own0 + b * 32 + s.lane % 32;
       const float whole = sum[b] + other_half(sum[b]);
       if (i >= n) continue;
@@ -438,7 +448,7 @@ __global__ __launch_bounds__(256) void k_ce_sweep_join(Ce c, const float2* __res
     return;
   }
   const int n = at<CeHead>(c.saved, c.at.head)->n;
-  const int shares = sweep_shares((n + kSweepRows - 1) / kSweepRows, cdiv(c.V, kSweepStage), sweep_grid(c.D));
+  const int shares = sweep_shares(cdiv(n, sweep_rows(c.D)), cdiv(c.V, kSweepStage), sweep_grid(c.D));
   const float z = zt[i];
   const float2* mine_part = part + (int64_t)i * shares;
   float m = z;
@@ -509,9 +519,9 @@ constexpr int kLeast = 4;
 struct Line {
   int64_t stages, total;  // of a tile, and of all
   int parts;
-  __device__ inline Line(int n, int64_t V) {
+  __device__ inline Line(int n, int64_t V, int D) {
     stages = n > 0 ? cdiv(n, kSweepStage) : 1;
-    total = cdiv(V, kSweepRows) * stages;
+    total = cdiv(V, sweep_rows(D)) * stages;
     parts = (int)(total / kLeast < kItemsGrid ? (total < kLeast ? 1 : total / kLeast) : kItemsGrid);
   }
   __device__ inline int64_t begin(int part) const { return total * part / parts; }
@@ -527,9 +537,9 @@ __global__ __launch_bounds__(256, (kWaves<DP, true>)) void k_ce_sweep_items(Ce c
   extern __shared__ __align__(1024) char lds[];
   const int n = at<CeHead>(c.saved, c.at.head)->n;
   const float cc = base2(c.scale);
-  const Line line(n, c.V);
+  const Line line(n, c.V, c.D);
   if ((int)blockIdx.x >= line.parts) return;
-  const int64_t from = line.begin(blockIdx.x), to = line.begin(blockIdx.x + 1), tiles = cdiv(c.V, kSweepRows);
+  const int64_t from = line.begin(blockIdx.x), to = line.begin(blockIdx.x + 1), tiles = cdiv(c.V, S::kOwned);
   S s;
   s.init(lds, at<__bf16>(c.saved, c.at.hc), n, c.D);
   const int32_t* targets = at<int32_t>(c.saved, c.at.target);
@@ -541,7 +551,7 @@ __global__ __launch_bounds__(256, (kWaves<DP, true>)) void k_ce_sweep_items(Ce c
     const bool whole = count == line.stages;
     const int place = x == from ? 0 : 1;
     x += count;
-    const int64_t own0 = tile * kSweepRows + s.wave * (kNB * 32);
+    const int64_t own0 = tile * S::kOwned + s.wave * (S::kNB * 32);
     s.load_owned((const __bf16*)c.E, own0, c.V);
     s.clear();
     auto fetch = [&](int k) INLINED {
@@ -554,8 +564,8 @@ __global__ __launch_bounds__(256, (kWaves<DP, true>)) void k_ce_sweep_items(Ce c
     };
     wait_and_sync<>();  // (the ring's last readers are done, and stores, which the waits below would count)
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) fetch(k);
-    landed_and_sync<(kAhead - 1) * S::kLoads>();
+    for (int k = 0; k < S::kAhead; ++k) fetch(k);
+    landed_and_sync<(S::kAhead - 1) * S::kLoads>();
     s.read_rows(s.slot(0));
     s.first(0);
     s.read_rows(s.slot(0) + 32 * S::kRow);
@@ -578,21 +588,21 @@ __global__ __launch_bounds__(256, (kWaves<DP, true>)) void k_ce_sweep_items(Ce c
       const uint32_t shifts = shifts_at(after);
       const int t = t_next;
       float y[4];
-      constexpr int ALL = kNB * 16, EACH = ALL / S::kSlots;
+      constexpr int ALL = S::kNB * 16;
       s.template turn<Q>([&](int w) {
-        if (Q == 0 && w == 1) fetch(k + kAhead);
+        if (Q == 0 && w == 1) fetch(k + S::kAhead);
         if (w == 2) t_next = read_target(after);
 #pragma unroll
-        for (int i = EACH * w; i < EACH * (w + 1); ++i) {
+        for (int i = ALL * w / S::kSlots; i < ALL * (w + 1) / S::kSlots; ++i) {
           s.template element<Q>(i, y, [&](int, int e, float z) { return __builtin_fmaf(z, cc, -sh[e / 4][e % 4]); });
-          if (i % (4 * kNB) == 4 * kNB - 1) read_shift(i / (4 * kNB), shifts);
+          if (i % (4 * S::kNB) == 4 * S::kNB - 1) read_shift(i / (4 * S::kNB), shifts);
           if (i) s.template finished<Q>(i - 1, y);
         }
       });
       s.template finished<Q>(ALL - 1, y);
       // a row whose target is among the wave's items (behind the last row all that is loaded is 0: a row of zeros, whose
       // product is 0 whatever P is)
-      if (__builtin_expect(__any((unsigned)(t - (int)own0) < (unsigned)(kNB * 32)), 0)) {
+      if (__builtin_expect(__any((unsigned)(t - (int)own0) < (unsigned)(S::kNB * 32)), 0)) {
         uint32_t at = ax + 16 * s.h;
         asm volatile("" : "+v"(at));  // (one address and constants, not an address each)
         typedef int s32x4 __attribute__((ext_vector_type(4)));
@@ -605,7 +615,7 @@ __global__ __launch_bounds__(256, (kWaves<DP, true>)) void k_ce_sweep_items(Ce c
           for (int j = 0; j < 2; ++j) {
             const uint32_t both = pack2(mine[2 * j], mine[2 * j + 1]);
 #pragma unroll
-            for (int b = 0; b < kNB; ++b) {
+            for (int b = 0; b < S::kNB; ++b) {
               uint32_t& p = s.p[Q][b][2 * k + j];
               p = tr[2 * j] == item + b * 32 ? (p & 0xffff0000u) | (both & 0xffffu) : p;
               p = tr[2 * j + 1] == item + b * 32 ? (p & 0xffffu) | (both & 0xffff0000u) : p;
@@ -616,7 +626,7 @@ __global__ __launch_bounds__(256, (kWaves<DP, true>)) void k_ce_sweep_items(Ce c
     };
     s.settle();
     for (int k = 0; k < count; ++k) {
-      landed_and_sync<(kAhead - 2) * S::kLoads>();
+      landed_and_sync<(S::kAhead - 2) * S::kLoads>();
       step(std::integral_constant<int, 0>{}, k);
       step(std::integral_constant<int, 1>{}, k);
       s.move_on(S::step_of(k + 1), S::step_of(k));
@@ -626,15 +636,15 @@ __global__ __launch_bounds__(256, (kWaves<DP, true>)) void k_ce_sweep_items(Ce c
     wait_and_sync<>();
     const float f = whole ? *grad * fabsf(c.scale) : 1.f;
 #pragma unroll
-    for (int b = 0; b < kNB; ++b) {
-      const int at = s.wave * (kNB * 32) + b * 32 + s.lane % 32;
-      const int64_t v = tile * kSweepRows + at;
+    for (int b = 0; b < S::kNB; ++b) {
+      const int at = s.wave * (S::kNB * 32) + b * 32 + s.lane % 32;
+      const int64_t v = tile * S::kOwned + at;
       if (v >= c.V) continue;
       f32x16 o[S::NDB];
 #pragma unroll
       for (int d = 0; d < S::NDB; ++d) o[d] = s.acc[d][b];
       if (whole) store_row<__bf16, S::NDB>(dE + v * c.D, o, f, c.D, s.lane);
-      else store_row<float, S::NDB>(sums + ((int64_t)(blockIdx.x * 2 + place) * kSweepRows + at) * c.D, o, f, c.D, s.lane);
+      else store_row<float, S::NDB>(sums + ((int64_t)(blockIdx.x * 2 + place) * S::kOwned + at) * c.D, o, f, c.D, s.lane);
     }
   }
 }
@@ -642,17 +652,18 @@ __global__ __launch_bounds__(256, (kWaves<DP, true>)) void k_ce_sweep_items(Ce c
 // The tiles that were shared: block.x - 1 is the first workgroup of one, the others follow it. Four features a lane.
 __global__ __launch_bounds__(256) void k_ce_pieces_join(Ce c, const float* __restrict__ sums, int64_t spread,
                                                         const float* __restrict__ grad, __bf16* __restrict__ dE) {
-  const Line line(at<CeHead>(c.saved, c.at.head)->n, c.V);
+  const Line line(at<CeHead>(c.saved, c.at.head)->n, c.V, c.D);
   const int part = blockIdx.x + 1;  // of the tile's second piece
   if (part >= line.parts) return;
   const int64_t cut = line.begin(part), at_tile = cut / line.stages, x0 = at_tile * line.stages;
-  const int64_t tile = at_tile * spread % cdiv(c.V, kSweepRows);
+  const int owned = sweep_rows(c.D);
+  const int64_t tile = at_tile * spread % cdiv(c.V, owned);
   const int64_t before = line.begin(part - 1);
   if (cut == x0 || before > x0) return;  // cut at a tile's end, or not the tile's first cut
-  const int64_t v0 = tile * kSweepRows, rows = c.V - v0 < kSweepRows ? c.V - v0 : kSweepRows;
+  const int64_t v0 = tile * owned, rows = c.V - v0 < owned ? c.V - v0 : owned;
   const int64_t x = ((int64_t)blockIdx.y * 256 + threadIdx.x) * 4;
   if (x >= rows * c.D) return;
-  const int64_t piece = (int64_t)kSweepRows * c.D;
+  const int64_t piece = (int64_t)owned * c.D;
   f32x4 s = *(const f32x4*)(sums + ((int64_t)(part - 1) * 2 + (before == x0 ? 0 : 1)) * piece + x);
   for (int p = part; p < line.parts && line.begin(p) < x0 + line.stages; ++p)
     s += *(const f32x4*)(sums + (int64_t)p * 2 * piece + x);
@@ -697,13 +708,13 @@ struct RowsPlan {
 };
 RowsPlan rows_plan(int64_t R, int D, bool grad) {
   // shares x rows are at most the units of all turns, or a share of each row
-  const int64_t some = (int64_t)kSweepUnits * (R < kSweepRows ? R : kSweepRows);
+  const int64_t some = (int64_t)kSweepUnits * (R < sweep_rows(D) ? R : sweep_rows(D));
   const int64_t slots = some > R ? some : R;
   RowsPlan p;
   size_t b = 0;
   p.part = b, b += up(slots * 8, 256);
   p.sums = b, b += grad ? up(slots * D * 4, 256) : 0;
-  const int64_t tiles = cdiv(R, kSweepRows);
+  const int64_t tiles = cdiv(R, sweep_rows(D));
   p.off = b, b += up((tiles > kSweepUnits ? tiles : kSweepUnits) * 4, 256);
   p.bytes = b;
   return p;
@@ -731,30 +742,37 @@ template <int DP> hipError_t items_t(const Ce& c, char* ws, const float* grad, _
   const hipError_t e = allow_lds<k_ce_sweep_items<DP>>(S::kLds);
   if (e != hipSuccess) return e;
   if (c.R) k_ce_shift<<<(unsigned)cdiv(c.R, 256), 256, 0, st>>>(c, shift, own);
-  const int64_t far = spread_of(cdiv(c.V, kSweepRows));
+  const int64_t far = spread_of(cdiv(c.V, S::kOwned));
   k_ce_sweep_items<DP><<<kItemsGrid, 256, S::kLds, st>>>(c, shift, own, grad, far, dE, sums);
-  k_ce_pieces_join<<<dim3(kItemsGrid - 1, (unsigned)cdiv((int64_t)kSweepRows * c.D, 1024)), 256, 0, st>>>(c, sums, far,
+  k_ce_pieces_join<<<dim3(kItemsGrid - 1, (unsigned)cdiv((int64_t)S::kOwned * c.D, 1024)), 256, 0, st>>>(c, sums, far,
                                                                                                       grad, dE);
   return hipGetLastError();
 }
 
 }  // namespace
 
-bool ce_swept(int D, int dtype) { return dtype == 1 && D <= 128; }
+bool ce_swept(int D, int dtype) { return dtype == 1 && D <= 256; }
 
 size_t ce_rows_bytes(int64_t R, int D, bool grad) { return rows_plan(R, D, grad).bytes; }
 hipError_t launch_ce_rows(const Ce& c, char* ws, bool grad, const float* zt, float* row_loss, float* each,
                           hipStream_t st) {
-  if (c.D <= 64) return grad ? rows_t<64, true>(c, ws, zt, row_loss, each, st) : rows_t<64, false>(c, ws, zt, row_loss, each, st);
-  return grad ? rows_t<128, true>(c, ws, zt, row_loss, each, st) : rows_t<128, false>(c, ws, zt, row_loss, each, st);
+  auto by = [&](auto width) {
+    constexpr int DP = decltype(width)::value;
+    return grad ? rows_t<DP, true>(c, ws, zt, row_loss, each, st) : rows_t<DP, false>(c, ws, zt, row_loss, each, st);
+  };
+  return c.D <= 64    ? by(std::integral_constant<int, 64>{})
+         : c.D <= 128 ? by(std::integral_constant<int, 128>{})
+                      : by(std::integral_constant<int, 256>{});
 }
 size_t ce_items_bytes(int64_t R, int64_t V, int D) {
-  return 2 * up(R * 4, 256) + (size_t)kItemsGrid * 2 * kSweepRows * D * 4;
+  return 2 * up(R * 4, 256) + (size_t)kItemsGrid * 2 * sweep_rows(D) * D * 4;
 }
 hipError_t launch_ce_items(const Ce& c, char* ws, const float* grad, void* dH, void* dE, hipStream_t st) {
   if (dH && c.R) k_ce_dh_out<<<(unsigned)cdiv(c.R * c.D, 1024), 256, 0, st>>>(c, grad, (__bf16*)dH);
   if (dE) {
-    const hipError_t e = c.D <= 64 ? items_t<64>(c, ws, grad, (__bf16*)dE, st) : items_t<128>(c, ws, grad, (__bf16*)dE, st);
+    const hipError_t e = c.D <= 64    ? items_t<64>(c, ws, grad, (__bf16*)dE, st)
+                         : c.D <= 128 ? items_t<128>(c, ws, grad, (__bf16*)dE, st)
+                                      : items_t<256>(c, ws, grad, (__bf16*)dE, st);
     if (e != hipSuccess) return e;
   }
   return hipGetLastError();
