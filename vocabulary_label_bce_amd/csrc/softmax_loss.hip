@@ -276,7 +276,7 @@ template <typename T_, int WM_, int WN_, int TM_, int TN_, int KB_, bool TA, boo
 };
 
 template <typename T, bool BIG> struct Sizes {
-  static constexpr int KB = sizeof(T) == 2 ? 64 : 128;
+  static constexpr int KB = 64;
   using Sums = Product<T, 2, 2, 2, 2, KB, false, false>;
   using Dh = Product<T, 2, 2, 2, 2, KB, false, true>;
   using De = Product<T, 2, 2, 2, 2, KB, true, true>;
