@@ -52,31 +52,66 @@ __device__ inline void store4(int type, void* base, int64_t at, int n, const flo
   else store4<float>(base, at, n, x);
 }
 
-// Four e4m3 bytes as one word, and back to what they stand for.
-__device__ inline uint32_t load_codes(const void* base, int64_t at, int n) {
-  const uint8_t* p = (const uint8_t*)base + at;
-  typedef uint32_t U __attribute__((aligned(1)));
-  if (n == 4) return *(const U*)p;
-  uint32_t x = 0;
+// Sixteen consecutive elements, n of them there, the others 0; aligned to one element.
+template <typename T> __device__ inline void load16(const void* base, int64_t at, int n, float* x) {
+  const T* p = (const T*)base + at;
+  constexpr int N = Vec<T>::N;
+  if (n == 16) {
 #pragma unroll
-  for (int i = 0; i < 3; ++i)
-    if (i < n) x |= (uint32_t)p[i] << (8 * i);
-  return x;
-}
-__device__ inline void store_codes(void* base, int64_t at, int n, uint32_t x) {
-  uint8_t* p = (uint8_t*)base + at;
-  typedef uint32_t U __attribute__((aligned(1)));
-  if (n == 4) {
-    *(U*)p = x;
+    for (int i = 0; i < 16; i += N) load_vec(p + i, x + i);
   } else {
 #pragma unroll
-    for (int i = 0; i < 3; ++i)
-      if (i < n) p[i] = (uint8_t)(x >> (8 * i));
+    for (int i = 0; i < 16; ++i) x[i] = i < n ? to_f32(p[i]) : 0.f;
   }
 }
-__device__ inline void decode(uint32_t codes, float scale, float* x) {
-  const f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)codes, false), hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)codes, true);
-  x[0] = lo[0] * scale, x[1] = lo[1] * scale, x[2] = hi[0] * scale, x[3] = hi[1] * scale;
+template <typename T> __device__ inline void store16(void* base, int64_t at, int n, const float* x) {
+  T* p = (T*)base + at;
+  constexpr int N = Vec<T>::N;
+  if (n == 16) {
+#pragma unroll
+    for (int i = 0; i < 16; i += N) store_vec(p + i, x + i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (i < n) p[i] = from_f32<T>(x[i]);
+  }
+}
+// Sixteen e4m3 bytes.
+struct Codes {
+  uint32_t w[4];
+};
+__device__ inline Codes load_codes(const void* base, int64_t at, int n) {
+  const uint8_t* p = (const uint8_t*)base + at;
+  typedef uint32_t U __attribute__((ext_vector_type(4), aligned(1)));
+  Codes c = {};
+  if (n == 16) {
+    const U v = *(const U*)p;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c.w[i] = v[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 15; ++i)
+      if (i < n) c.w[i / 4] |= (uint32_t)p[i] << (8 * (i % 4));
+  }
+  return c;
+}
+__device__ inline void store_codes(void* base, int64_t at, int n, const Codes& c) {
+  uint8_t* p = (uint8_t*)base + at;
+  typedef uint32_t U __attribute__((ext_vector_type(4), aligned(1)));
+  if (n == 16) {
+    *(U*)p = U{c.w[0], c.w[1], c.w[2], c.w[3]};
+  } else {
+#pragma unroll
+    for (int i = 0; i < 15; ++i)
+      if (i < n) p[i] = (uint8_t)(c.w[i / 4] >> (8 * (i % 4)));
+  }
+}
+__device__ inline void decode(const Codes& c, float scale, float* x) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.w[i], false), hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.w[i], true);
+    x[4 * i] = lo[0] * scale, x[4 * i + 1] = lo[1] * scale, x[4 * i + 2] = hi[0] * scale, x[4 * i + 3] = hi[1] * scale;
+  }
 }
 
 // 32 bits that look random from a number: multiplications and shifts, each of which can be undone.
@@ -99,32 +134,33 @@ __device__ inline uint32_t encode(float y, uint32_t random, uint32_t least) {
   return c | ((bits >> 31) << 7);
 }
 
-// The largest magnitude of the wave's values; NaN passes through as the largest.
-__device__ inline float wave_top(float a) {
-  uint32_t x = __float_as_uint(a);  // (of a magnitude: ordered like the whole number, NaN above infinity)
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) {
-    const uint32_t y = (uint32_t)__shfl_xor((int)x, o, 64);
-    x = y > x ? y : x;
+// The largest of 16 lanes' numbers.
+__device__ inline uint32_t row_top(uint32_t x) {
+#define CUTBCE_TURN(ctrl)                                                                    \
+  {                                                                                          \
+    const uint32_t y = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, ctrl, 0xf, 0xf, true); \
+    x = y > x ? y : x;                                                                       \
   }
-  return __uint_as_float(x);
+  CUTBCE_TURN(0x128) CUTBCE_TURN(0x124) CUTBCE_TURN(0x122) CUTBCE_TURN(0x121)  // (turned by 8, 4, 2 and 1 lanes)
+#undef CUTBCE_TURN
+  return x;
 }
-// The wave's values in e4m3 and their scale.
-__device__ inline uint32_t hold(const float* x, const uint32_t* random, int shift, uint32_t least, float* scale) {
-  float top = 0.f;
+// A block's values, sixteen a lane, in e4m3 and their scale. NaN counts as the largest (magnitudes are ordered like the
+// whole numbers of their bits).
+__device__ inline Codes hold(const float* x, const uint32_t* random, int shift, uint32_t least, float* scale) {
   uint32_t t = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 16; ++i) {
     const uint32_t a = __float_as_uint(x[i]) & 0x7fffffffu;
     t = a > t ? a : t;
   }
-  top = wave_top(__uint_as_float(t));
+  const float top = __uint_as_float(row_top(t));
   *scale = top * (1.f / 448.f);
   const float f = top > 1e-35f ? 1.f / top * 448.f : (top <= 1e-35f ? 0.f : top);  // (what is smaller is held as 0; NaN stays)
-  uint32_t codes = 0;
+  Codes c = {};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) codes |= encode(x[i] * f, (random[i] >> shift) & 0xffffu, least) << (8 * i);
-  return codes;
+  for (int i = 0; i < 16; ++i) c.w[i / 4] |= encode(x[i] * f, (random[i] >> shift) & 0xffffu, least) << (8 * (i % 4));
+  return c;
 }
 
 // The states' step, each operation rounded by itself: the random rounding of states of 8 bits turns a difference in the
@@ -135,73 +171,98 @@ __device__ inline void advance(const AdamHow& h, float x, bool root, float& m, f
   v = (root ? v * v : v) * h.beta2 + x * x * h.rest2;
 }
 
-// A workgroup has kChunk elements of one tensor, a lane four consecutive ones at a time.
-template <bool B8> __global__ __launch_bounds__(256) void k_adamw(AdamArgs a) {
-  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+// What a workgroup needs of the step: its tensor and place in it, and the factors of this step.
+struct Place {
+  int id;
+  int64_t from;
+  float clip, keep, rate, c2;
+  int32_t t;
+};
+__device__ inline Place place_of(const AdamArgs& a) {
+  Place p;
+  const int lane = threadIdx.x % 64;
   const bool here = lane < kListed && a.start[lane < kListed ? lane : 0] <= blockIdx.x;
-  const int id = __builtin_amdgcn_readfirstlane(__popcll(__ballot(here)) - 1);
-  const AdamEntry& e = a.e[id];
-  const int64_t from = (int64_t)(blockIdx.x - a.start[id]) * kChunk;
+  p.id = __builtin_amdgcn_readfirstlane(__popcll(__ballot(here)) - 1);
+  p.from = (int64_t)(blockIdx.x - a.start[p.id]) * kChunk;
   const AdamHow& h = a.how;
-  const int32_t t = *h.step + 1;
-  const float c1 = -1.f / expm1f((float)t * h.log_beta1), c2 = sqrtf(-1.f / expm1f((float)t * h.log_beta2));
+  p.t = *h.step + 1;
+  const float c1 = -1.f / expm1f((float)p.t * h.log_beta1);
+  p.c2 = sqrtf(-1.f / expm1f((float)p.t * h.log_beta2));
   const float lr = h.lr_at ? *h.lr_at : h.lr;
-  float clip = 1.f;
+  p.clip = 1.f;
   if (h.norm) {
     const float x = h.max_norm / (*h.norm + 1e-6f);
-    clip = x >= 1.f ? 1.f : x;  // (NaN stays)
+    p.clip = x >= 1.f ? 1.f : x;  // (NaN stays)
   }
-  const float keep = 1.f - lr * e.decay, rate = lr * c1;
-  const uint32_t key = B8 ? hash32(hash32(h.seed ^ hash32((uint32_t)t)) + a.first + id) : 0;
+  p.keep = 1.f - lr * a.e[p.id].decay, p.rate = lr * c1;
+  return p;
+}
+
+// A workgroup has kChunk elements of one tensor, a lane four consecutive ones at a time. Memory bounds it: 112 million
+// bf16 parameters with float32 states, 22 bytes each, take 453 us, 5.45 TB/s.
+__global__ __launch_bounds__(256) void k_adamw(AdamArgs a) {
+  const Place w = place_of(a);
+  const AdamEntry& e = a.e[w.id];
+  const AdamHow& h = a.how;
 #pragma unroll
   for (int u = 0; u < kChunk / 1024; ++u) {
-    const int64_t at = from + u * 1024 + wave * 256 + lane * 4;
+    const int64_t at = w.from + u * 1024 + threadIdx.x * 4;
     const int64_t left = e.n - at;
-    const int n = left >= 4 ? 4 : (left > 0 ? (int)left : 0);
-    if (B8 ? at - lane * 4 >= e.n : n == 0) break;
-    float p[4] = {}, g[4] = {}, m[4] = {}, v[4] = {}, r[4];
-    if (n) {
-      load4(e.g_type, e.g, at, n, g);
-      if (e.master) load4<float>(e.master, at, n, p);
-      else load4(e.p_type, e.p, at, n, p);
-    }
-    const int64_t block = (at - lane * 4) / kBlock8;
-    if constexpr (B8) {
-      decode(n ? load_codes(e.m, at, n) : 0, e.ms[block], m);
-      decode(n ? load_codes(e.v, at, n) : 0, e.vs[block], v);
-    } else {
-      load4<float>(e.m, at, n, m);
-      load4<float>(e.v, at, n, v);
-    }
+    if (left <= 0) break;
+    const int n = left >= 4 ? 4 : (int)left;
+    float p[4], g[4], m[4], v[4];
+    load4(e.g_type, e.g, at, n, g);
+    if (e.master) load4<float>(e.master, at, n, p);
+    else load4(e.p_type, e.p, at, n, p);
+    load4<float>(e.m, at, n, m);
+    load4<float>(e.v, at, n, v);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      advance(h, g[i] * clip, B8, m[i], v[i]);
-      r[i] = sqrtf(v[i]);
-      p[i] = p[i] * keep - rate * m[i] / (r[i] * c2 + h.eps);
+      advance(h, g[i] * w.clip, false, m[i], v[i]);
+      p[i] = p[i] * w.keep - w.rate * m[i] / (sqrtf(v[i]) * w.c2 + h.eps);
     }
-    if constexpr (B8) {
-      uint32_t random[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        random[i] = hash32(key + (uint32_t)(at + i));
-        if (i >= n) m[i] = r[i] = 0.f;
-      }
-      float ms, vs;
-      const uint32_t cm = hold(m, random, 0, 0, &ms), cv = hold(r, random, 16, 1, &vs);
-      if (n) {
-        store_codes(e.m, at, n, cm);
-        store_codes(e.v, at, n, cv);
-      }
-      if (lane == 0) e.ms[block] = ms, e.vs[block] = vs;
-    } else {
-      store4<float>(e.m, at, n, m);
-      store4<float>(e.v, at, n, v);
-    }
-    if (n) {
-      if (e.master) store4<float>(e.master, at, n, p);
-      store4(e.p_type, e.p, at, n, p);
-    }
+    store4<float>(e.m, at, n, m);
+    store4<float>(e.v, at, n, v);
+    if (e.master) store4<float>(e.master, at, n, p);
+    store4(e.p_type, e.p, at, n, p);
   }
+}
+
+// The same with states of 8 bits: a lane has sixteen consecutive elements and 16 lanes a block, so that what a block
+// costs, the largest of its lanes and two quotients, is shared by many elements.
+__global__ __launch_bounds__(256, 4) void k_adamw8(AdamArgs a) {
+  const Place w = place_of(a);
+  const AdamEntry& e = a.e[w.id];
+  const AdamHow& h = a.how;
+  const uint32_t key = hash32(hash32(h.seed ^ hash32((uint32_t)w.t)) + a.first + w.id);
+  const int64_t at = w.from + threadIdx.x * 16, left = e.n - at, block = at / kBlock8;
+  if (block * kBlock8 >= e.n) return;  // (all of the block's lanes)
+  const int n = left >= 16 ? 16 : (left > 0 ? (int)left : 0);
+  float p[16], g[16], m[16], r[16];
+  if (e.g_type) load16<__bf16>(e.g, at, n, g);
+  else load16<float>(e.g, at, n, g);
+  if (e.master || !e.p_type) load16<float>(e.master ? (const void*)e.master : e.p, at, n, p);
+  else load16<__bf16>(e.p, at, n, p);
+  decode(load_codes(e.m, at, n), e.ms[block], m);
+  decode(load_codes(e.v, at, n), e.vs[block], r);
+  uint32_t random[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    advance(h, g[i] * w.clip, true, m[i], r[i]);
+    r[i] = sqrtf(r[i]);
+    // (the quotient to one unit in its last place: it only moves p)
+    p[i] = p[i] * w.keep - w.rate * m[i] * __builtin_amdgcn_rcpf(r[i] * w.c2 + h.eps);
+    random[i] = hash32(key + (uint32_t)(at + i));
+    if (i >= n) m[i] = r[i] = 0.f;
+  }
+  float ms, vs;
+  const Codes cm = hold(m, random, 0, 0, &ms), cv = hold(r, random, 16, 1, &vs);
+  store_codes(e.m, at, n, cm);
+  store_codes(e.v, at, n, cv);
+  if (threadIdx.x % 16 == 0) e.ms[block] = ms, e.vs[block] = vs;
+  if (e.master) store16<float>(e.master, at, n, p);
+  if (e.p_type) store16<__bf16>(e.p, at, n, p);
+  else store16<float>(e.p, at, n, p);
 }
 
 __global__ void k_step(int32_t* step) { *step += 1; }
@@ -260,8 +321,8 @@ __global__ __launch_bounds__(1024) void k_norm_join(const double* partials, int6
 }  // namespace
 
 hipError_t launch_adamw(const AdamArgs& a, unsigned blocks, bool bits8, hipStream_t st) {
-  if (bits8) k_adamw<true><<<blocks, 256, 0, st>>>(a);
-  else k_adamw<false><<<blocks, 256, 0, st>>>(a);
+  if (bits8) k_adamw8<<<blocks, 256, 0, st>>>(a);
+  else k_adamw<<<blocks, 256, 0, st>>>(a);
   return hipGetLastError();
 }
 hipError_t launch_step(int32_t* step, hipStream_t st) {

@@ -9,7 +9,7 @@ namespace cutbce {
 // ---------------------------------------------------------------------------------------------------------
 constexpr int kListed = 48;
 constexpr int kChunk = 4096;  // elements of a workgroup
-constexpr int kBlock8 = 256;  // elements that share a scale in states of 8 bits: a wave's four each
+constexpr int kBlock8 = 256;  // elements that share a scale in states of 8 bits: 16 lanes' sixteen each
 
 struct AdamEntry {
   void *p, *m, *v;
