@@ -7,10 +7,12 @@ the item table shared between the lookup and the full-vocabulary loss:
   training   ids of all users packed one after another (no padding) -> embedding (scaled rows of the item table, and
              of a position table) -> layer_norm -> packed_attention -> layer_norm -> two-layer perceptron ->
              layer_norm -> cut_bce's forward and backward -> the encoder's backward; the lookup's gradient is added
-             to the rows of the loss's dE that it touches (embedding_backward with dtable)
+             to the rows of the loss's dE that it touches (embedding_backward with dtable). Or, with --loss softmax:
+             cross_entropy_forward and cross_entropy_backward of each row's next item, then the norm of all gradients
+             (grad_norm) and a step of AdamW that is clipped by it
   serving    one new item a user: its key and value go into the cache, cached_attention reads it, topk ranks the items
 
-Run on a GPU:  python examples/sequence_encoder.py [--users 64 --items 20000 --steps 20]
+Run on a GPU:  python examples/sequence_encoder.py [--users 64 --items 20000 --steps 20 --loss softmax --state-bits 8]
 """
 from __future__ import annotations
 
@@ -96,6 +98,33 @@ class Encoder:
                 t.grad = None
         return loss
 
+    def optimizer(self, lr=1e-3, **options):
+        """AdamW over the item table and the block: vectors and tables of positions do not decay."""
+        kept = {"positions"} | {n for n, t in self.p.items() if t.dim() == 1}
+        decay = options.pop("weight_decay", 0.01)
+        return ops.AdamW([self.items, *self.p.values()], lr=lr, **options,
+                         weight_decay=[decay] + [0.0 if n in kept else decay for n in self.p])
+
+    def softmax_step(self, ids, places, cu, next_ids, optimizer, max_norm=1.0):
+        """One step of `optimizer` on the softmax cross entropy of each row's next item (a row whose next_ids is -1 has
+        none), with all gradients scaled down to a norm of max_norm; returns (loss, norm). Nothing waits for the GPU,
+        so that a step can be captured into a graph."""
+        x = ops.embedding_forward(ids, self.items, self.scale).requires_grad_()
+        hidden = self.hidden(x, places, cu)
+        with torch.no_grad():
+            H = hidden.detach()
+            loss, _, saved = ops.cross_entropy_forward(H, self.items, next_ids)
+            dH, dE = ops.cross_entropy_backward(torch.ones_like(loss), H, self.items, saved)
+        hidden.backward(dH)
+        with torch.no_grad():
+            ops.embedding_backward(x.grad, ids, self.items.shape[0], self.scale, dtable=dE)
+            grads = [dE] + [t.grad for t in self.p.values()]
+            norm = ops.grad_norm(grads)
+            optimizer.step(grads, norm=norm, max_norm=max_norm)
+            for t in self.p.values():
+                t.grad = None
+        return loss, norm
+
     # ---- serving ----
     def new_cache(self, users, capacity):
         shape = (users, capacity, self.kv_heads, self.head_dim)
@@ -141,11 +170,15 @@ def main():
     ap.add_argument("--users", type=int, default=64)
     ap.add_argument("--items", type=int, default=20_000)
     ap.add_argument("--steps", type=int, default=20)
+    ap.add_argument("--loss", choices=("bce", "softmax"), default="bce")
+    ap.add_argument("--state-bits", type=int, choices=(32, 8), default=32, help="of the optimizer that softmax has")
     a = ap.parse_args()
     model = Encoder(a.items)
     batch, lens = histories(a.users, a.items, 20, 200, seed=1)
+    ids, places, cu, _, next_ids = batch
+    optimizer = model.optimizer(state_bits=a.state_bits, master=True) if a.loss == "softmax" else None
     for i in range(a.steps):
-        loss = model.train_step(*batch)
+        loss = model.softmax_step(ids, places, cu, next_ids, optimizer)[0] if optimizer else model.train_step(*batch)
         if i % 5 == 0 or i == a.steps - 1:
             print(f"step {i}: loss {loss.item():.6f}", flush=True)
     cache = model.new_cache(a.users, 200)

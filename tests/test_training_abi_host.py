@@ -4,6 +4,7 @@ import ctypes
 import math
 
 import pytest
+import torch
 
 from vocabulary_label_bce_amd import binding as B
 
@@ -83,3 +84,69 @@ def test_adamw_structs_are_checked():
     assert B.lib().cutbce_adamw_step(ctypes.byref(B.AdamWTensors()), None, None) == NULL
     assert _adamw(dict(state_bits=8), ms=256, vs=256, missing="vs") == NULL
     assert _adamw(dict(state_bits=8), ms=258, vs=256) == ALIGN
+
+
+CE = dict(R=64, V=1000, D=64, dt=BF16, idb=4, H=256, E=256, t=256, w=None, scale=1.0, loss=256, row=None, saved=256, ws=256,
+          size=1 << 40)
+BACK = dict(R=64, V=1000, D=64, dt=BF16, E=256, scale=1.0, g=256, saved=256, dH=256, dE=256, ws=256, size=1 << 40)
+
+
+def _forward(**over):
+    return B.lib().cutbce_cross_entropy_forward(*dict(CE, **over).values(), None)
+
+
+def _backward(**over):
+    return B.lib().cutbce_cross_entropy_backward(*dict(BACK, **over).values(), None)
+
+
+SIZES = [(dict(R=-1), SHAPE), (dict(R=(1 << 20) + 1), None), (dict(V=0), SHAPE), (dict(V=1 << 40), None),
+         (dict(D=0), UNSUPPORTED), (dict(D=12), None), (dict(D=16392), None), (dict(dt=2), DTYPE), (dict(dt=-1), DTYPE)]
+
+
+@pytest.mark.parametrize("over,status", SIZES)
+def test_cross_entropy_sizes_are_checked(over, status):
+    """One answer from every entry point; sizes beyond the operator's are SHAPE or UNSUPPORTED."""
+    n = ctypes.c_size_t(0)
+    x = dict(CE, **over)
+    size = x["R"], x["V"], x["D"], x["dt"]
+    got = [_forward(**over), _backward(**over), B.lib().cutbce_cross_entropy_saved_size(*size, ctypes.byref(n))]
+    got += [B.lib().cutbce_cross_entropy_workspace_size(*size, k, ctypes.byref(n)) for k in range(3)]
+    assert len(set(got)) == 1 and (got[0] == status or (status is None and got[0] in (SHAPE, UNSUPPORTED)))
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(idb=2), DTYPE), (dict(scale=math.inf), SHAPE), (dict(scale=math.nan), SHAPE), (dict(E=None), NULL),
+    (dict(H=None), NULL), (dict(t=None), NULL), (dict(loss=None), NULL), (dict(ws=None), NULL), (dict(H=264), ALIGN),
+    (dict(E=264), ALIGN), (dict(t=258), ALIGN), (dict(t=260, idb=8), ALIGN), (dict(w=258), ALIGN), (dict(loss=258), ALIGN),
+    (dict(row=258), ALIGN), (dict(saved=128), ALIGN), (dict(ws=128), ALIGN), (dict(size=0), WORKSPACE),
+])
+def test_cross_entropy_forward_arguments_are_checked(over, status):
+    assert _forward(**over) == status
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(scale=math.inf), SHAPE), (dict(E=None), NULL), (dict(g=None), NULL), (dict(saved=None), NULL), (dict(ws=None), NULL),
+    (dict(E=264), ALIGN), (dict(g=258), ALIGN), (dict(saved=128), ALIGN), (dict(dH=264), ALIGN), (dict(dE=264), ALIGN),
+    (dict(ws=128), ALIGN), (dict(size=0), WORKSPACE), (dict(dH=None, dE=None), OK),
+])
+def test_cross_entropy_backward_arguments_are_checked(over, status):
+    assert _backward(**over) == status
+
+
+def test_cross_entropy_queries():
+    n = ctypes.c_size_t(0)
+    ok = 64, 1000, 64, BF16
+    assert B.lib().cutbce_cross_entropy_saved_size(*ok, None) == NULL
+    assert B.lib().cutbce_cross_entropy_workspace_size(*ok, 0, None) == NULL
+    for which in (-1, 3):
+        assert B.lib().cutbce_cross_entropy_workspace_size(*ok, which, ctypes.byref(n)) == SHAPE
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("R,D", [(1, 8), (4096, 64), (4096, 512), (25_600, 128), (1 << 20, 256), (4096, 16384)])
+def test_cross_entropy_memory_is_bounded_in_the_vocabulary(R, D, dt):
+    """Ten times the items: nothing that is saved grows, and no workspace by more than a share of a row or an item each."""
+    small, large = (B.cross_entropy_sizes(R, V, D, {BF16: torch.bfloat16, F32: torch.float32}[dt]) for V in (10 ** 6, 10 ** 7))
+    assert small[0] == large[0]
+    for a, b in zip(small[1:], large[1:]):
+        assert b <= a + 16 * 10 ** 7 + R * 16
