@@ -367,12 +367,14 @@ __global__ __launch_bounds__(P::NL, P::kWaves) void k_ce_sums(Ce c, float2* __re
 #pragma unroll
           for (int j = 0; j < P::TN; ++j) {
             if (__any((unsigned)(target[j] - v) < (unsigned)(P::TM * 32)) || (int64_t)v + P::TM * 32 > c.V) {
+              // (compared with constants: a lane's items held as numbers would not fit the registers)
+              const int hit = target[j] - v - 4 * h, end = (int)clamp64(c.V - v, 0, P::TM * 32) - 4 * h;
 #pragma unroll
               for (int i = 0; i < P::TM; ++i)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
-                  const int item = i * 32 + acc_row(e, h);
-                  if (item == target[j] - v || (int64_t)v + item >= c.V) p.acc[i][j][e] = -INFINITY;
+                  const int item = i * 32 + acc_row(e, 0);
+                  if (item == hit || item >= end) p.acc[i][j][e] = -INFINITY;
                 }
             }
             float top = -INFINITY;
