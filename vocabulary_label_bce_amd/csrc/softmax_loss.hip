@@ -132,19 +132,20 @@ template <typename T, int ROWS, int NL, int KB> struct Side<T, ROWS, false, NL, 
   static_assert(Tile<T, K>::kRowB == KB && Ld::kLanes == NL, "");
   static constexpr int kLoads = Ld::kRounds;
   Ld ld;
-  int64_t stride;
+  int64_t stride, step;  // of rows, and of stages
   const T* from;  // of the next stage
   int whole, left;  // bytes of a whole stage's range; features left
   int voff[kLoads];
   __device__ inline void init(int64_t s) {
-    stride = s, ld.init(threadIdx.x, s);
+    stride = s, step = K, ld.init(threadIdx.x, s);
 #pragma unroll
     for (int q = 0; q < kLoads; ++q) voff[q] = ld.offset(q, K);
   }
+  __device__ inline void init_blocked(int64_t rows) { init(K), step = rows * K; }
   // stages from row `row` of `rows`, feature k of `end`, on
   __device__ inline void start(const T* base, int64_t row, int64_t rows, int64_t k, int64_t end) {
     const int64_t r = clamp64(rows - row, 0, ROWS);
-    from = base + row * stride + k;
+    from = base + row * stride + k / K * step + k % K;
     whole = r > 0 ? (int)(((r - 1) * stride + K) * sizeof(T)) : 0;
     left = r > 0 && end > k ? (int)(end - k) : 0;
   }
@@ -158,7 +159,7 @@ template <typename T, int ROWS, int NL, int KB> struct Side<T, ROWS, false, NL, 
       for (int q = 0; q < kLoads; ++q) v[q] = ld.offset(q, left);
       load_lds16s<kLoads, NL * 16>(buffer_of(from, left > 0 ? whole - (K - left) * (int)sizeof(T) : 0), v, dst);
     }
-    from += K, left -= left > 0 ? (left < K ? left : K) : 0;
+    from += step, left -= left > 0 ? (left < K ? left : K) : 0;
   }
   __device__ static inline u32x4 op(uint32_t at, int block, int t, int lane) {
     return load_row(base_row<T, K>(at, lane) + block * 32 * KB, t);
@@ -174,8 +175,25 @@ template <typename T, int ROWS, int NL, int KB> struct Side<T, ROWS, true, NL, K
   int64_t stride;
   const T* from;
   int cols, left;  // of the tile's results; features left
+  int whole;       // blocked: bytes of a stage's range
   int voff[kLoads];
-  __device__ inline void init(int64_t s) { stride = s, ld.init(threadIdx.x, s); }
+  __device__ inline void init(int64_t s) { stride = s, whole = 0, ld.init(threadIdx.x, s); }
+  // Blocked: all results and features of a stage are there.
+  __device__ inline void init_blocked(int64_t rows) {
+    constexpr int C = KB / sizeof(T);  // of a block
+    init(C);
+    whole = (int)(((ROWS / C - 1) * rows + K) * KB);
+#pragma unroll
+    for (int q = 0; q < kLoads; ++q) {
+      const int round = q % Ld::kRounds, row = threadIdx.x / Ld::Ti::kCPR + round * Ld::kStep;
+      const int x = (ld.chunk ^ Ld::Ti::swz(round * Ld::kStep)) * 16 + q / Ld::kRounds * 128 * (int)sizeof(T);
+      voff[q] = x / KB * (int)(rows * KB) + row * KB + x % KB;
+    }
+  }
+  __device__ inline void start_blocked(const T* base, int64_t block, int64_t rows, int64_t k, int64_t end) {
+    from = base + (block * rows + k) * stride;
+    left = end > k ? (int)(end - k) : 0;
+  }
   __device__ inline void start(const T* base, int64_t row, int64_t rows, int64_t k, int64_t end) {
     from = base + k * stride + row;
     cols = (int)clamp64(rows - row, 0, ROWS);
@@ -188,7 +206,8 @@ template <typename T, int ROWS, int NL, int KB> struct Side<T, ROWS, true, NL, K
   }
   __device__ inline void load(uint32_t dst) {
     const int n = left < K ? left : K;
-    load_lds16s<kLoads, NL * 16>(buffer_of(from, n > 0 ? ((n - 1) * (int)stride + cols) * (int)sizeof(T) : 0), voff, dst);
+    const int range = whole ? whole : ((n - 1) * (int)stride + cols) * (int)sizeof(T);
+    load_lds16s<kLoads, NL * 16>(buffer_of(from, n > 0 ? range : 0), voff, dst);
     from += K * stride, left -= n;
   }
   __device__ static inline u32x4 op(uint32_t at, int block, int t, int lane) {
@@ -300,6 +319,13 @@ __device__ inline TileAt tile_at(int bid, int ni, int nj) {
   const int u = xcd * per + (xcd < more ? xcd : more) + bid / 8;
   const int group = u / (8 * nj), wide = ni - group * 8 < 8 ? ni - group * 8 : 8, in = u - group * 8 * nj;
   return {group * 8 + in % wide, in / wide};
+}
+
+// How many of them a workgroup has that takes bid, bid + the grid, ... in turn (a grid that is a multiple of 8).
+__device__ inline int tiles_at(int ni, int nj) {
+  const int total = ni * nj, mine = total / 8 + ((int)blockIdx.x % 8 < total % 8 ? 1 : 0), first = blockIdx.x / 8;
+  const int step = gridDim.x / 8;
+  return mine > first ? (mine - first + step - 1) / step : 0;
 }
 
 // Units of work: tiles of rows x shares of the vocabulary, the shares' number from that of the tiles. Neighbouring
@@ -467,9 +493,12 @@ __global__ __launch_bounds__(1024) void k_ce_loss(Ce c, const float* __restrict_
 // Gradients, a piece of the vocabulary at a time: items v0 .. v0 + width - 1 (width a multiple of 256).
 // ---------------------------------------------------------------------------------------------------------
 
-// dz of the piece, [n][width] (zeros for items behind the vocabulary's end). In 16 bits the items of each 16 stand in the
-// order 0-3, 8-11, 4-7, 12-15: a lane's eight results are next to each other, and are the operand of the product with E
-// in the order in which the transposed reads of E give their items.
+// dz of the piece in blocks of 64 bytes of items: [width / block][rows][block], rows = R rounded up to 32; zeros for items
+// behind the vocabulary's end and for the rows from n to the next multiple of 32. A stage of the product with E is then one
+// range of memory, and what a wave stores whole lines. In 16 bits the items of each 16 stand in the order 0-3, 8-11, 4-7,
+// 12-15: a lane's eight results are next to each other, and are the operand of the product with E in the order in which
+// the transposed reads of E give their items.
+template <typename T> constexpr int kBlock = 64 / sizeof(T);
 __host__ __device__ constexpr inline int item_at(int place) {  // of 16 bits
   return (place & ~12) | (place & 4) << 1 | (place & 8) >> 1;
 }
@@ -478,47 +507,71 @@ __global__ __launch_bounds__(P::NL, P::kWaves) void k_ce_dz(Ce c, int64_t v0, in
   using T = typename P::T;
   extern __shared__ __align__(1024) char lds[];
   const int n = at<CeHead>(c.saved, c.at.head)->n;
-  const TileAt tile = tile_at(blockIdx.x, (int)cdiv(n, P::BN), (int)(width / P::BM));
-  const int64_t row0 = (int64_t)tile.i * P::BN, v = v0 + (int64_t)tile.j * P::BM;
-  if (row0 >= n || tile.j >= width / P::BM) return;
+  const int ni = (int)cdiv(n, P::BN), nj = (int)(width / P::BM), mine = tiles_at(ni, nj);
   P p;
   p.init(lds, c.D, c.D);
   const T *E = (const T*)c.E, *H = at<T>(c.saved, c.at.hc);
   const int nk = (c.D + P::K - 1) / P::K, h = p.lane / 32;
-  p.a.start(E, v, c.V, 0, c.D);
-  p.b.start(H, row0, n, 0, c.D);
-  p.run(nk, [](int) {}, [](int) {});
   const float cc = base2(c.scale);
-#pragma unroll
-  for (int j = 0; j < P::TN; ++j) {
-    const int64_t i = row0 + (p.wn * P::TN + j) * 32 + p.lane % 32;
-    if (i >= n) continue;
-    const float coef = at<float>(c.saved, c.at.coef)[i], shift = at<float>(c.saved, c.at.lse)[i] - log2f(coef);
-    const float mine = -coef * at<float>(c.saved, c.at.rest)[i];
-    const int64_t target = at<int32_t>(c.saved, c.at.target)[i];
-#pragma unroll
-    for (int b = 0; b < P::TM; ++b) {
-      const int64_t first = v + (p.wm * P::TM + b) * 32;
-      float x[16];
-#pragma unroll
-      for (int e = 0; e < 16; ++e) x[e] = exp2_of(__builtin_fmaf(p.acc[b][j][e], cc, -shift));
-      if (__any((uint64_t)(target - first) < 32u) || first + 32 > c.V) {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int64_t item = first + acc_row(e, h);
-          x[e] = item == target ? mine : (item < c.V ? x[e] : 0.f);
+  const int64_t rows = up(c.R, 32);
+  int next = 0, fk = 0;          // the tile whose stages are loaded next, and how many of the one before are left
+  int here = 0, left = nk;       // the tile that is being multiplied, and how many of its stages are left
+  p.run(
+      mine * nk,
+      [&](int) {
+        if (fk == 0) {
+          const TileAt t = tile_at(blockIdx.x + next * gridDim.x, ni, nj);
+          const bool any = next < mine;
+          p.a.start(E, any ? v0 + (int64_t)t.j * P::BM : 0, any ? c.V : 0, 0, c.D);
+          p.b.start(H, any ? (int64_t)t.i * P::BN : 0, any ? n : 0, 0, c.D);
+          fk = nk, ++next;
         }
-      }
-      T* to = dz + i * width + (first - v0);
-      if constexpr (sizeof(T) == 2) {
-        store_vec(to + 8 * h, x);
-        store_vec(to + 16 + 8 * h, x + 8);
-      } else {
+        --fk;
+      },
+      [&](int) {
+        if (--left) return;
+        left = nk;
+        const TileAt t = tile_at(blockIdx.x + here * gridDim.x, ni, nj);
+        ++here;
+        const int64_t row0 = (int64_t)t.i * P::BN, v = v0 + (int64_t)t.j * P::BM;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) store_vec(to + 8 * k + 4 * h, x + 4 * k);
-      }
-    }
-  }
+        for (int j = 0; j < P::TN; ++j) {
+          const int64_t i = row0 + (p.wn * P::TN + j) * 32 + p.lane % 32;
+          if (i >= up(n, 32)) continue;
+          float shift = INFINITY, own = 0.f;
+          int64_t target = -1;
+          if (i < n) {
+            const float coef = at<float>(c.saved, c.at.coef)[i];
+            shift = at<float>(c.saved, c.at.lse)[i] - log2f(coef);
+            own = -coef * at<float>(c.saved, c.at.rest)[i];
+            target = at<int32_t>(c.saved, c.at.target)[i];
+          }
+#pragma unroll
+          for (int b = 0; b < P::TM; ++b) {
+            const int64_t first = v + (p.wm * P::TM + b) * 32;
+            float x[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[e] = exp2_of(__builtin_fmaf(p.acc[b][j][e], cc, -shift));
+            if (__any((uint64_t)(target - first) < 32u) || first + 32 > c.V) {
+              const int hit = (int)clamp64(target - first, -1, 32) - 4 * h, end = (int)clamp64(c.V - first, 0, 32) - 4 * h;
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const int item = acc_row(e, 0);
+                x[e] = item >= end ? 0.f : (item == hit ? own : x[e]);
+              }
+            }
+            T* to = dz + ((first - v0) / kBlock<T> * rows + i) * kBlock<T>;
+            if constexpr (sizeof(T) == 2) {
+              store_vec(to + 8 * h, x);
+              store_vec(to + 16 + 8 * h, x + 8);
+            } else {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) store_vec(to + k / 2 * rows * kBlock<T> + k % 2 * 8 + 4 * h, x + 4 * k);
+            }
+          }
+        }
+        p.clear();
+      });
 }
 
 // sums[part] (+)= dz E over the part's items: rows x features.
@@ -534,7 +587,8 @@ __global__ __launch_bounds__(P::NL, P::kWaves) void k_ce_dh(Ce c, int64_t v0, in
   const int part = tile.j / rows;
   const int64_t row0 = (int64_t)(tile.j % rows) * P::BM, d0 = (int64_t)tile.i * P::BN;
   P p;
-  p.init(lds, width, c.D);
+  p.init(lds, 0, c.D);
+  p.a.init_blocked(up(c.R, 32));
   const int64_t left = c.V - v0 < width ? c.V - v0 : width, steps = (left + P::K - 1) / P::K;
   const int64_t x0 = steps * part / parts, x1 = steps * (part + 1) / parts;
   const T* E = (const T*)c.E + v0 * c.D;
@@ -575,11 +629,12 @@ __global__ __launch_bounds__(P::NL, P::kWaves) void k_ce_de(Ce c, int64_t v0, in
   const int part = PART ? tile.j / items : 0;
   const int64_t u0 = (int64_t)(PART ? tile.j % items : tile.j) * P::BM, d0 = (int64_t)tile.i * P::BN;
   P p;
-  p.init(lds, width, c.D);
+  p.init(lds, 0, c.D);
+  p.a.init_blocked(up(c.R, 32));
   const T* H = at<T>(c.saved, c.at.hc);
   const int64_t steps = (n + P::K - 1) / P::K;
   const int64_t x0 = PART ? steps * part / parts : 0, x1 = PART ? steps * (part + 1) / parts : steps;
-  p.a.start(dz, u0, width, x0 * P::K, x1 * P::K < n ? x1 * P::K : n);
+  p.a.start_blocked(dz, u0 / kBlock<T>, up(c.R, 32), x0 * P::K, x1 * P::K < n ? x1 * P::K : n);
   p.b.start(H, d0, c.D, x0 * P::K, x1 * P::K < n ? x1 * P::K : n);
   p.run((int)(x1 - x0), [](int) {}, [](int) {});
   const float f = PART ? 1.f : *grad * fabsf(c.scale);
@@ -623,7 +678,7 @@ __global__ __launch_bounds__(256) void k_ce_de_join(Ce c, int64_t v0, int64_t wi
 template <typename T>
 __global__ __launch_bounds__(256) void k_ce_dh_join(Ce c, int parts, const float* __restrict__ sums,
                                                     const float* __restrict__ grad, T* __restrict__ dH) {
-  const int64_t x = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  const int64_t x = ((int64_t)(blockIdx.y * gridDim.x + blockIdx.x) * 256 + threadIdx.x) * 4;
   if (x >= c.R * c.D) return;
   const int64_t r = x / c.D;
   const int i = at<int32_t>(c.saved, c.at.place)[r];
@@ -659,16 +714,16 @@ template <typename T, bool BIG> Plan plan_of(int64_t R, int64_t V, int D) {
   if (R < 1) R = 1;
   Plan p;
   // a piece's dz takes up to 256 MB, the size of the memory-side cache
-  int64_t width = ((int64_t)256 << 20) / (R * (int64_t)sizeof(T)) / 256 * 256;
+  const int64_t rows = up(R, 32);
+  int64_t width = ((int64_t)256 << 20) / (rows * (int64_t)sizeof(T)) / 256 * 256;
   if (width < 256) width = 256;
   if (width > up(V, 256)) width = up(V, 256);
-  if (width > (int64_t)1 << 22) width = (int64_t)1 << 22;  // (offsets inside a stage are 32-bit)
   p.width = width;
   p.dh_parts = (int)clamp_parts(cdiv(R, S::Dh::BM) * cdiv(D, S::Dh::BN), width / S::Dh::K,
                                 ((int64_t)256 << 20) / (R * D * 4) + 1, kCeGrid<typename S::Dh>);
   p.de_parts = (int)clamp_parts(width / S::De::BM * cdiv(D, S::De::BN), cdiv(R, S::De::K), 64, kCeGrid<typename S::De>);
   size_t b = 0;
-  p.dz = b, b += up(R * width * (int64_t)sizeof(T), 256);
+  p.dz = b, b += up(rows * width * (int64_t)sizeof(T), 256);
   p.dh = b, b += up((int64_t)p.dh_parts * R * D * 4, 256);
   p.de = b, b += p.de_parts > 1 ? up((int64_t)p.de_parts * width * D * 4, 256) : 0;
   p.bytes = b;
@@ -731,8 +786,9 @@ hipError_t backward_t(const Ce& c, const float* grad, T* dH, T* dE, hipStream_t 
   if (e == hipSuccess) e = allow_lds<k_ce_de<typename S::De, true>>(S::De::kLds);
   if (e != hipSuccess) return e;
   for (int64_t v = 0; v < c.V; v += p.width) {
-    if (c.R) k_ce_dz<typename S::Sums><<<(unsigned)(cdiv(c.R, S::Sums::BN) * (p.width / S::Sums::BM)), S::Sums::NL, S::Sums::kLds,
-                                st>>>(c, v, p.width, dz);
+    const int64_t tiles = up(cdiv(c.R, S::Sums::BN) * (p.width / S::Sums::BM), 8);
+    if (c.R) k_ce_dz<typename S::Sums><<<(unsigned)(tiles < kCeGrid<typename S::Sums> ? tiles : kCeGrid<typename S::Sums>),
+                                         S::Sums::NL, S::Sums::kLds, st>>>(c, v, p.width, dz);
     if (dH && c.R)
       k_ce_dh<typename S::Dh><<<(unsigned)(cdiv(c.R, S::Dh::BM) * cdiv(c.D, S::Dh::BN) * p.dh_parts), S::Dh::NL,
                                 S::Dh::kLds, st>>>(c, v, p.width, p.dh_parts, v == 0, dz, dh);
@@ -747,7 +803,8 @@ hipError_t backward_t(const Ce& c, const float* grad, T* dH, T* dE, hipStream_t 
       }
     }
   }
-  if (dH && c.R) k_ce_dh_join<T><<<(unsigned)cdiv(c.R * c.D, 1024), 256, 0, st>>>(c, p.dh_parts, dh, grad, dH);
+  const int64_t blocks = cdiv(c.R * c.D, 1024), turns = cdiv(blocks, kMaxGrid);
+  if (dH && c.R) k_ce_dh_join<T><<<dim3((unsigned)cdiv(blocks, turns), (unsigned)turns), 256, 0, st>>>(c, p.dh_parts, dh, grad, dH);
   return hipGetLastError();
 }
 
