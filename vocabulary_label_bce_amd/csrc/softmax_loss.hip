@@ -3,7 +3,7 @@
 //   z = scale H E^T,  lse_r = log sum_v exp z_rv,  l_r = lse_r - z_rt,  loss = sum w_r l_r / W
 //   dz_rv = w_r / W (p_rv - [v = t_r]),  p = exp(z - lse),  dH = scale dz E,  dE = scale dz^T H
 //
-// Rows without a target are left out first (k_ce_rows), the others' H is copied together (k_ce_gather). Exponents are in
+// Rows without a target are left out first, the others' H is copied together (k_ce_rows). Exponents are in
 // base 2, c = |scale| log2 e times the products; a negative scale turns H's signs. A row's target is left out of the
 // sums and products and joined in at the end: 1 - p_t is the others' share of the sum, and is exact to rounding where
 // p_t is near 1, as a row's loss log(1 + others / e_t) is.
@@ -21,80 +21,80 @@ namespace {
 // Rows: which have a target, their weights' sum, and their H together.
 // ---------------------------------------------------------------------------------------------------------
 
-// One workgroup; a wave has a range of rows and goes through it twice, counting first.
-template <typename I>
-__global__ __launch_bounds__(1024) void k_ce_rows(Ce c, const I* __restrict__ targets,
-                                                  const float* __restrict__ weight) {
-  __shared__ int count[16];
+// A workgroup has a range of rows, each wave one at a time: its place among the counted ones, its copy, and c times its
+// product with its target's item. All of them count all targets first, which is what one of them would have to do before
+// the others could start.
+template <typename T, typename I>
+__global__ __launch_bounds__(1024) void k_ce_rows(Ce c, const T* __restrict__ H, const I* __restrict__ targets,
+                                                  const float* __restrict__ weight, float* __restrict__ zt) {
+  __shared__ int count[16], early[16], list[1024], aims[1024];
   __shared__ double sum[16];
   const int wave = uni(threadIdx.x / 64), lane = threadIdx.x % 64;
-  const int64_t share = up(cdiv(c.R, 16), 64), r0 = wave * share, r1 = r0 + share < c.R ? r0 + share : c.R;
-  int n = 0;
+  const int64_t share = cdiv(c.R, gridDim.x), r0 = blockIdx.x * share, r1 = r0 + share < c.R ? r0 + share : c.R;
+  int n = 0, before = 0;
   double w = 0;
 #pragma unroll 4
-  for (int64_t r = r0 + lane; r < r1; r += 64) {
+  for (int64_t r = threadIdx.x; r < c.R; r += 1024) {
     const int64_t t = targets[r];
     const bool in = t >= 0 && t < c.V;
     n += in;
+    before += in && r < r0;
     w += in ? (weight ? (double)weight[r] : 1.0) : 0.0;
   }
 #pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) n += __shfl_xor(n, o, 64), w += __shfl_xor(w, o, 64);
-  if (lane == 0) count[wave] = n, sum[wave] = w;
+  for (int o = 32; o >= 1; o >>= 1) n += __shfl_xor(n, o, 64), before += __shfl_xor(before, o, 64), w += __shfl_xor(w, o, 64);
+  if (lane == 0) count[wave] = n, early[wave] = before, sum[wave] = w;
   __syncthreads();
   int from = 0, total = 0;
   double W = 0;
-  for (int i = 0; i < 16; ++i) {
-    if (i < wave) from += count[i];
-    total += count[i];
-    W += sum[i];
-  }
-  if (threadIdx.x == 0) *at<CeHead>(c.saved, c.at.head) = {total, (float)W};
+  for (int i = 0; i < 16; ++i) from += early[i], total += count[i], W += sum[i];
+  if (blockIdx.x == 0 && threadIdx.x == 0) *at<CeHead>(c.saved, c.at.head) = {total, (float)W};
   const double f = W > 0 ? 1.0 / W : (W == 0 ? 0.0 : W);  // (NaN stays)
+  const bool none = !(fabsf(c.scale) * kLog2e > 0.f);
   int32_t *rows = at<int32_t>(c.saved, c.at.rows), *place = at<int32_t>(c.saved, c.at.place),
           *target = at<int32_t>(c.saved, c.at.target);
   float* coef = at<float>(c.saved, c.at.coef);
-  for (int64_t b = r0; b < r1; b += 64) {
-    const int64_t r = b + lane;
+  for (int64_t b = r0; b < r1; b += 1024) {
+    const int64_t r = b + threadIdx.x;
     const int64_t t = r < r1 ? (int64_t)targets[r] : -1;
     const bool in = t >= 0 && t < c.V;
     const uint64_t m = __ballot(in);
-    const int i = from + __popcll(m & (((uint64_t)1 << lane) - 1));
+    __syncthreads();  // (the last turn's lists are read, and the counts)
+    if (lane == 0) count[wave] = __popcll(m);
+    __syncthreads();
+    int k = __popcll(m & (((uint64_t)1 << lane) - 1)), here = 0;
+    for (int i = 0; i < 16; ++i) k += i < wave ? count[i] : 0, here += count[i];
     if (in) {
-      rows[i] = (int32_t)r;
-      target[i] = (int32_t)t;
-      coef[i] = (float)((weight ? (double)weight[r] : 1.0) * f);
+      rows[from + k] = (int32_t)r;
+      target[from + k] = (int32_t)t;
+      coef[from + k] = (float)((weight ? (double)weight[r] : 1.0) * f);
+      list[k] = (int)(r - b), aims[k] = (int)t;
     }
-    if (r < r1) place[r] = in ? i : -1;
-    from += __popcll(m);
-  }
-}
-
-// A wave has a row: its copy, and c times its product with its target's item.
-template <typename T>
-__global__ __launch_bounds__(256) void k_ce_gather(Ce c, const T* __restrict__ H, float* __restrict__ zt) {
-  const int i = blockIdx.x * 4 + threadIdx.x / 64, lane = threadIdx.x % 64;
-  if (i >= at<CeHead>(c.saved, c.at.head)->n) return;
-  const T* from = H + (int64_t)at<int32_t>(c.saved, c.at.rows)[i] * c.D;
-  const T* item = (const T*)c.E + (int64_t)at<int32_t>(c.saved, c.at.target)[i] * c.D;
-  T* to = at<T>(c.saved, c.at.hc) + (int64_t)i * c.D;
-  const bool none = !(fabsf(c.scale) * kLog2e > 0.f);
-  float s = 0.f;
-  constexpr int N = Vec<T>::N;
-  for (int d = lane * N; d < c.D; d += 64 * N) {
-    float x[N], y[N];
-    load_vec(from + d, x);
-    load_vec(item + d, y);
+    if (r < r1) place[r] = in ? from + k : -1;
+    __syncthreads();
+    for (int j = wave; j < here; j += 16) {
+      const T* x_at = H + (b + list[j]) * c.D;
+      const T* item = (const T*)c.E + (int64_t)aims[j] * c.D;
+      T* to = at<T>(c.saved, c.at.hc) + (int64_t)(from + j) * c.D;
+      float s = 0.f;
+      constexpr int N = Vec<T>::N;
+      for (int d = lane * N; d < c.D; d += 64 * N) {
+        float x[N], y[N];
+        load_vec(x_at + d, x);
+        load_vec(item + d, y);
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-      x[j] = none ? 0.f : (c.scale < 0.f ? -x[j] : x[j]);
-      s += x[j] * y[j];
+        for (int q = 0; q < N; ++q) {
+          x[q] = none ? 0.f : (c.scale < 0.f ? -x[q] : x[q]);
+          s += x[q] * y[q];
+        }
+        store_vec(to + d, x);
+      }
+#pragma unroll
+      for (int o = 32; o >= 1; o >>= 1) s += __shfl_xor(s, o, 64);
+      if (lane == 0) zt[from + j] = s * base2(c.scale);
     }
-    store_vec(to + d, x);
+    from += here;
   }
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) s += __shfl_xor(s, o, 64);
-  if (lane == 0) zt[i] = s * base2(c.scale);
 }
 
 // ---------------------------------------------------------------------------------------------------------
@@ -336,13 +336,12 @@ struct Units {
 __device__ inline Units units_of(int n, int64_t V, int bm, int bn, int grid) {
   Units u;
   u.tiles = (n + bn - 1) / bn;
-  const int64_t steps = (V + bm - 1) / bm;
-  int64_t s = u.tiles ? grid / u.tiles : 1;
-  s = s > steps ? steps : s;
-  u.shares = s < 1 ? 1 : (int)s;
+  const int steps = (int)(((uint32_t)V + bm - 1) / bm);
+  const int s = u.tiles ? grid / u.tiles : 1;
+  u.shares = s < 1 ? 1 : (s > steps ? steps : s);
   return u;
 }
-template <typename P> constexpr int kCeGrid = P::kLds > 80 * 1024 ? 256 : 512;  // workgroups of the sums: what is resident
+template <typename P> constexpr int kCeGrid = P::kLds > 80 * 1024 ? 256 : 512;  // workgroups that are resident
 
 template <typename P>
 __global__ __launch_bounds__(P::NL, P::kWaves) void k_ce_sums(Ce c, float2* __restrict__ part) {
@@ -356,13 +355,14 @@ __global__ __launch_bounds__(P::NL, P::kWaves) void k_ce_sums(Ce c, float2* __re
   const T *E = (const T*)c.E, *H = at<T>(c.saved, c.at.hc);
   const float cc = base2(c.scale);
   const int32_t* targets = at<int32_t>(c.saved, c.at.target);
-  const int64_t steps = (c.V + P::BM - 1) / P::BM;
+  const int steps = (int)(((uint32_t)c.V + P::BM - 1) / P::BM);
   const int nk = (c.D + P::K - 1) / P::K, h = p.lane / 32;
   for (int k = blockIdx.x / 8; k < per; k += gridDim.x / 8) {
     const int u = (blockIdx.x % 8) * per + k;
     if (u >= total) break;
     const int tile = u % units.tiles, share = u / units.tiles;
-    const int64_t v0 = steps * share / units.shares, v1 = steps * (share + 1) / units.shares;
+    const Share part_of = share_at(steps, units.shares, share);
+    const int64_t v0 = part_of.first, v1 = v0 + part_of.count;
     const int64_t row0 = (int64_t)tile * P::BN;
     float m[P::TN], s[P::TN];
     int target[P::TN];
@@ -433,10 +433,16 @@ __global__ __launch_bounds__(P::NL, P::kWaves) void k_ce_sums(Ce c, float2* __re
   }
 }
 
-// A wave has a row of the batch: joins its shares' sums.
+// What a row's shares are, in the kernel that left their sums: k_ce_sums (slots for each share), or the sweep.
 struct JoinHow {
-  int bm, bn, grid, slots;  // of the kernel that left the sums; slots for each share
+  int bm, bn, grid, slots;
+  __device__ inline int of(int n, int64_t V) const {
+    if (!bm) return sweep_shares((n + bn - 1) / bn, sweep_stages(V), grid);
+    return units_of(n, V, bm, bn, grid).shares * slots;
+  }
 };
+
+// A wave has a row of the batch: joins its shares' sums.
 __global__ __launch_bounds__(256) void k_ce_join(Ce c, JoinHow how, const float2* __restrict__ part,
                                                  const float* __restrict__ zt, float* __restrict__ row_loss,
                                                  float* __restrict__ each) {
@@ -448,27 +454,20 @@ __global__ __launch_bounds__(256) void k_ce_join(Ce c, JoinHow how, const float2
     if (lane == 0 && row_loss) row_loss[r] = 0.f;
     return;
   }
-  const Units u = units_of(at<CeHead>(c.saved, c.at.head)->n, c.V, how.bm, how.bn, how.grid);
-  const int slots = u.shares * how.slots;
+  const int slots = how.of(at<CeHead>(c.saved, c.at.head)->n, c.V);
+  const float2* mine = part + (int64_t)i * slots;
   const float z = zt[i];
   float m = z;
-  for (int k = lane; k < slots; k += 64) m = fmaxf(m, part[(int64_t)i * slots + k].x);
+#pragma unroll 4
+  for (int k = lane; k < slots; k += 64) m = top_of(m, mine[k]);
 #pragma unroll
   for (int o = 32; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
   float others = 0.f;
-  for (int k = lane; k < slots; k += 64) {
-    const float2 x = part[(int64_t)i * slots + k];
-    others += x.y == 0.f ? 0.f : x.y * exp2_of(x.x - m);
-  }
+#pragma unroll 4
+  for (int k = lane; k < slots; k += 64) others += mine[k].y * share_of(mine[k], m);
 #pragma unroll
   for (int o = 32; o >= 1; o >>= 1) others += __shfl_xor(others, o, 64);
-  if (lane) return;
-  const float mine = exp2_of(z - m), sum = others + mine;
-  const float l = mine == 1.f ? log1pf(others) : (m - z) * kLn2 + logf(sum);
-  at<float>(c.saved, c.at.lse)[i] = m + log2f(sum);
-  at<float>(c.saved, c.at.rest)[i] = others / sum;
-  each[i] = l;
-  if (row_loss) row_loss[r] = l;
+  if (lane == 0) finish_row(c, i, r, z, m, others, row_loss, each);
 }
 
 __global__ __launch_bounds__(1024) void k_ce_loss(Ce c, const float* __restrict__ each, float* __restrict__ loss) {
@@ -758,17 +757,21 @@ hipError_t forward_t(const Ce& c, int id_bytes, const T* H, const void* targets,
   const ForwardPlan f = forward_plan<T, BIG>(c.R, c.D, grad);
   float *zt = (float*)(c.ws + f.zt), *each = (float*)(c.ws + f.each);
   float2* part = (float2*)(c.ws + f.part);
-  if (id_bytes == 4) k_ce_rows<int32_t><<<1, 1024, 0, st>>>(c, (const int32_t*)targets, weight);
-  else k_ce_rows<int64_t><<<1, 1024, 0, st>>>(c, (const int64_t*)targets, weight);
-  if (c.R) k_ce_gather<T><<<(unsigned)cdiv(c.R, 4), 256, 0, st>>>(c, H, zt);
-  if (ce_swept(c.D, c.dtype)) {
-    const hipError_t e = c.R ? launch_ce_rows(c, c.ws + f.part, grad, zt, row_loss, each, st) : hipSuccess;
+  const unsigned groups = (unsigned)(c.R < 16 ? 1 : c.R > 8192 ? 512 : cdiv(c.R, 16));
+  if (id_bytes == 4) k_ce_rows<T, int32_t><<<groups, 1024, 0, st>>>(c, H, (const int32_t*)targets, weight, zt);
+  else k_ce_rows<T, int64_t><<<groups, 1024, 0, st>>>(c, H, (const int64_t*)targets, weight, zt);
+  const bool swept = ce_swept(c.D, c.dtype);
+  if (swept && c.R) {
+    const hipError_t e = launch_ce_rows(c, c.ws + f.part, grad, zt, row_loss, each, st);
     if (e != hipSuccess) return e;
   } else if (c.R) {
     const hipError_t e = allow_lds<k_ce_sums<P>>(P::kLds);
     if (e != hipSuccess) return e;
     k_ce_sums<P><<<kCeGrid<P>, P::NL, P::kLds, st>>>(c, part);
-    k_ce_join<<<(unsigned)cdiv(c.R, 4), 256, 0, st>>>(c, JoinHow{P::BM, P::BN, kCeGrid<P>, P::WM}, part, zt, row_loss, each);
+  }
+  if (c.R && !(swept && grad)) {
+    const JoinHow how = swept ? JoinHow{0, sweep_rows(c.D), sweep_grid(c.D), 1} : JoinHow{P::BM, P::BN, kCeGrid<P>, P::WM};
+    k_ce_join<<<(unsigned)cdiv(c.R, 4), 256, 0, st>>>(c, how, part, zt, row_loss, each);
   }
   k_ce_loss<<<1, 1024, 0, st>>>(c, each, loss);
   return hipGetLastError();

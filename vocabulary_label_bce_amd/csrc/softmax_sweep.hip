@@ -251,7 +251,7 @@ __global__ __launch_bounds__(256, (kWaves<DP, false>)) void k_ce_sweep_rows(Ce c
   extern __shared__ __align__(1024) char lds[];
   const int n = at<CeHead>(c.saved, c.at.head)->n;
   const int tiles = (n + S::kOwned - 1) / S::kOwned;
-  const int64_t stages = cdiv(c.V, kSweepStage);
+  const int stages = sweep_stages(c.V);
   const int shares = sweep_shares(tiles, stages, sweep_grid(c.D)), total = tiles * shares, per = (total + 7) / 8;
   const float cc = base2(c.scale);
   const int32_t* targets = at<int32_t>(c.saved, c.at.target);
@@ -262,9 +262,11 @@ __global__ __launch_bounds__(256, (kWaves<DP, false>)) void k_ce_sweep_rows(Ce c
     if (u >= total) break;
     if (CAREFUL && !off[u]) continue;
     const int tile = u % tiles, share = u / tiles;
-    const int64_t s0 = stages * share / shares;
-    const int count = (int)(stages * (share + 1) / shares - s0);
+    const Share part_of = share_at(stages, shares, share);
+    const int64_t s0 = part_of.first;
+    const int count = part_of.count;
     const int64_t own0 = (int64_t)tile * S::kOwned + s.wave * (S::kNB * 32);
+    wait_and_sync<>();  // (the ring's last readers are done, and stores, which the waits below would count)
     s.load_owned(at<__bf16>(c.saved, c.at.hc), own0, n);
     int target[S::kNB];
     float ref[S::kNB], sum[S::kNB];
@@ -279,7 +281,6 @@ __global__ __launch_bounds__(256, (kWaves<DP, false>)) void k_ce_sweep_rows(Ce c
       s.load_stage(r, s.slot(k) + s.wave * 1024);
     };
     auto start = [&]() INLINED {
-      wait_and_sync<>();  // (the ring's last readers are done, and stores, which the waits below would count)
       s.clear();
 #pragma unroll
       for (int k = 0; k < S::kAhead; ++k) fetch(k);
@@ -432,14 +433,13 @@ __global__ __launch_bounds__(256, (kWaves<DP, false>)) void k_ce_sweep_rows(Ce c
   }
 }
 
-// A workgroup has a row of the batch: joins its shares' sums (and products, into saved's dH: without the cotangent and
-// scale).
-template <bool GRAD>
+// A workgroup has a row of the batch: joins its shares' sums, and products into saved's dH (without the cotangent and
+// scale). Without products k_ce_join does it.
 __global__ __launch_bounds__(256) void k_ce_sweep_join(Ce c, const float2* __restrict__ part,
                                                        const float* __restrict__ sums, const float* __restrict__ zt,
                                                        float* __restrict__ row_loss, float* __restrict__ each) {
   __shared__ float factor[kSweepUnits];
-  __shared__ float4 rest[GRAD ? 256 : 1];
+  __shared__ float4 rest[256];
   const int64_t r = blockIdx.x;
   const int tid = threadIdx.x, lane = tid % 64;
   const int i = at<int32_t>(c.saved, c.at.place)[r];
@@ -448,52 +448,43 @@ __global__ __launch_bounds__(256) void k_ce_sweep_join(Ce c, const float2* __res
     return;
   }
   const int n = at<CeHead>(c.saved, c.at.head)->n;
-  const int shares = sweep_shares(cdiv(n, sweep_rows(c.D)), cdiv(c.V, kSweepStage), sweep_grid(c.D));
+  const int shares = sweep_shares((n + sweep_rows(c.D) - 1) / sweep_rows(c.D), sweep_stages(c.V), sweep_grid(c.D));
   const float z = zt[i];
   const float2* mine_part = part + (int64_t)i * shares;
   float m = z;
-  for (int k = lane; k < shares; k += 64) m = fmaxf(m, mine_part[k].x);
+  for (int k = lane; k < shares; k += 64) m = top_of(m, mine_part[k]);
 #pragma unroll
   for (int o = 32; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
   float others = 0.f;
   for (int k = lane; k < shares; k += 64) {
-    const float2 x = mine_part[k];
-    const float f = x.x == -INFINITY ? 0.f : exp2_of(x.x - m);
-    others += x.y * f;
-    if (GRAD && tid < 64) factor[k] = f;
+    const float f = share_of(mine_part[k], m);
+    others += mine_part[k].y * f;
+    if (tid < 64) factor[k] = f;
   }
 #pragma unroll
   for (int o = 32; o >= 1; o >>= 1) others += __shfl_xor(others, o, 64);
-  const float mine = exp2_of(z - m), sum = others + mine;
-  if (tid == 0) {
-    const float l = mine == 1.f ? log1pf(others) : (m - z) * kLn2 + logf(sum);
-    at<float>(c.saved, c.at.lse)[i] = m + log2f(sum);
-    at<float>(c.saved, c.at.rest)[i] = others / sum;
-    each[i] = l;
-    if (row_loss) row_loss[r] = l;
-  }
-  if constexpr (GRAD) {
-    // a group of DL lanes has the row's features, four each; the groups share the shares
-    const int DL = c.D / 4, groups = 256 / DL, g = tid / DL, d = tid % DL * 4;
-    __syncthreads();
-    f32x4 s = {0.f, 0.f, 0.f, 0.f};
-    if (g < groups) {
+  const float sum = others + exp2_of(z - m);
+  if (tid == 0) finish_row(c, i, r, z, m, others, row_loss, each);
+  // a group of DL lanes has the row's features, four each; the groups share the shares
+  const int DL = c.D / 4, groups = 256 / DL, g = tid / DL, d = tid % DL * 4;
+  __syncthreads();
+  f32x4 s = {0.f, 0.f, 0.f, 0.f};
+  if (g < groups) {
 #pragma unroll 4
-      for (int k = g; k < shares; k += groups) s += *(const f32x4*)(sums + ((int64_t)k * n + i) * c.D + d) * factor[k];
+    for (int k = g; k < shares; k += groups) s += *(const f32x4*)(sums + ((int64_t)k * n + i) * c.D + d) * factor[k];
+  }
+  rest[tid] = make_float4(s[0], s[1], s[2], s[3]);
+  __syncthreads();
+  if (g == 0) {
+    for (int k = 1; k < groups; ++k) {
+      const float4 x = rest[k * DL + tid];
+      s += f32x4{x.x, x.y, x.z, x.w};
     }
-    rest[tid] = make_float4(s[0], s[1], s[2], s[3]);
-    __syncthreads();
-    if (g == 0) {
-      for (int k = 1; k < groups; ++k) {
-        const float4 x = rest[k * DL + tid];
-        s += f32x4{x.x, x.y, x.z, x.w};
-      }
-      const float coef = at<float>(c.saved, c.at.coef)[i];
-      const __bf16* item = (const __bf16*)c.E + (int64_t)at<int32_t>(c.saved, c.at.target)[i] * c.D + d;
-      float* to = at<float>(c.saved, c.at.dh) + (int64_t)i * c.D + d;
+    const float coef = at<float>(c.saved, c.at.coef)[i];
+    const __bf16* item = (const __bf16*)c.E + (int64_t)at<int32_t>(c.saved, c.at.target)[i] * c.D + d;
+    float* to = at<float>(c.saved, c.at.dh) + (int64_t)i * c.D + d;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) to[j] = coef * ((s[j] - others * (float)item[j]) / sum);
-    }
+    for (int j = 0; j < 4; ++j) to[j] = coef * ((s[j] - others * (float)item[j]) / sum);
   }
 }
 
@@ -552,6 +543,7 @@ __global__ __launch_bounds__(256, (kWaves<DP, true>)) void k_ce_sweep_items(Ce c
     const int place = x == from ? 0 : 1;
     x += count;
     const int64_t own0 = tile * S::kOwned + s.wave * (S::kNB * 32);
+    wait_and_sync<>();  // (the ring's last readers are done, and stores, which the waits below would count)
     s.load_owned((const __bf16*)c.E, own0, c.V);
     s.clear();
     auto fetch = [&](int k) INLINED {
@@ -562,7 +554,6 @@ __global__ __launch_bounds__(256, (kWaves<DP, true>)) void k_ce_sweep_items(Ce c
       load_lds4(buffer_of((const char*)aux + row * 4, (int)clamp64(left, 0, kSweepStage) * 4), s.lane * 4,
                 s.slot(k) + S::kTile + s.wave * 256);
     };
-    wait_and_sync<>();  // (the ring's last readers are done, and stores, which the waits below would count)
 #pragma unroll
     for (int k = 0; k < S::kAhead; ++k) fetch(k);
     landed_and_sync<(S::kAhead - 1) * S::kLoads>();
@@ -731,8 +722,9 @@ template <int DP, bool GRAD> hipError_t rows_t(const Ce& c, char* ws, const floa
                                                                     (int*)(ws + p.off));
   k_ce_sweep_rows<DP, GRAD, true><<<sweep_grid(c.D), 256, S::kLds, st>>>(c, (float2*)(ws + p.part), (float*)(ws + p.sums),
                                                                    (int*)(ws + p.off));
-  k_ce_sweep_join<GRAD><<<(unsigned)c.R, 256, 0, st>>>(c, (const float2*)(ws + p.part), (const float*)(ws + p.sums), zt,
-                                                       row_loss, each);
+  if (GRAD)
+    k_ce_sweep_join<<<(unsigned)c.R, 256, 0, st>>>(c, (const float2*)(ws + p.part), (const float*)(ws + p.sums), zt,
+                                                   row_loss, each);
   return hipGetLastError();
 }
 
