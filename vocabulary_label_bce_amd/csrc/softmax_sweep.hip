@@ -25,7 +25,7 @@ namespace {
 template <int DP> constexpr int kBlocks = DP > 128 ? 1 : 2;
 template <int DP> constexpr int kStages = DP > 128 ? 4 : 5;
 template <int DP> constexpr int kAhead = kStages<DP> - 2;
-constexpr int kItemsGrid = 256;                // workgroups of the backward: one a CU
+__host__ __device__ constexpr inline int items_grid(int D) { return D <= 64 ? 512 : 256; }  // workgroups of the backward
 constexpr float kMost = 0x1p80f;              // sums of exponentials beyond which a row takes a new reference
 
 __device__ inline uint32_t pack2(float a, float b) {
@@ -35,7 +35,7 @@ __device__ inline uint32_t pack2(float a, float b) {
 
 // The ring of one workgroup and a wave's operands.
 // Waves a SIMD has: two where the registers allow it.
-template <int DP, bool ITEMS> constexpr int kWaves = DP <= 64 && !ITEMS ? 2 : 1;
+template <int DP, bool ITEMS> constexpr int kWaves = DP <= 64 ? 2 : 1;
 
 template <int DP, bool AUX, bool GRAD> struct Sweep {
   using Ti = Tile<__bf16, DP>;
@@ -49,6 +49,7 @@ template <int DP, bool AUX, bool GRAD> struct Sweep {
   static constexpr int kStage = kTile + kAux, kLds = kStages * kStage;
   static constexpr int kLoads = Ld::kRounds + (AUX ? 1 : 0);    // of a wave for a stage
   static constexpr bool kAlone = kWaves<DP, AUX> == 1 && GRAD, kHeld = kWaves<DP, AUX> == 1;
+  static constexpr bool kPlain = !kHeld;
   static_assert(NT == 2 * NDB, "");
 
   Ld ld;
@@ -323,14 +324,35 @@ __global__ __launch_bounds__(256, (kWaves<DP, false>)) void k_ce_sweep_rows(Ce c
     start();
     begin();
     if constexpr (!CAREFUL) {
-      s.read_rows(s.slot(0) + 32 * S::kRow);
+      s.read_rows(s.slot(0) + (S::kPlain ? 0 : 32 * S::kRow));
       s.aim(s.slot(1), s.slot(0));
       auto step = [&](auto half, int k) INLINED {
         constexpr int Q = decltype(half)::value;
-        leave_out(half, k);
         float add[S::kNB][2] = {};
+        if constexpr (S::kPlain) {
+          s.first(Q);
+          if (Q == 0) fetch(k + S::kAhead);
+          s.read_rows(Q == 0 ? s.slot(k) + 32 * S::kRow : s.slot(k + 1));
+          if constexpr (GRAD) {
+#pragma unroll
+            for (int n = 0; n < S::NT; ++n) s.template read_col<Q>(n);
+          }
+        }
+        leave_out(half, k);
         float y[4];
         constexpr int ALL = S::kNB * 16;
+        if constexpr (S::kPlain) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int b = 0; b < S::kNB; ++b) {
+              float v[2];
+#pragma unroll
+              for (int j = 0; j < 2; ++j) add[b][j] += v[j] = exp2_of(__builtin_fmaf(s.z[Q][b][2 * i + j], cc, -ref[b]));
+              if constexpr (GRAD) s.p[Q][b][i] = pack2(v[0], v[1]);
+            }
+          if constexpr (GRAD) s.last(Q);
+        } else {
         auto end = [&](int i) {
           float& a = add[i % S::kNB][i / S::kNB & 1];
           a += y[i & 3];
@@ -346,6 +368,7 @@ __global__ __launch_bounds__(256, (kWaves<DP, false>)) void k_ce_sweep_rows(Ce c
           }
         });
         end(ALL - 1);
+        }
   #pragma unroll
         for (int b = 0; b < S::kNB; ++b) sum[b] += add[b][0] + add[b][1];
       };
@@ -357,7 +380,7 @@ __global__ __launch_bounds__(256, (kWaves<DP, false>)) void k_ce_sweep_rows(Ce c
         s.move_on(S::step_of(k + 1), S::step_of(k));
         s.settle();
       }
-      s.last(1);
+      if constexpr (!S::kPlain) s.last(1);
       bool bad = false;
 #pragma unroll
       for (int b = 0; b < S::kNB; ++b) bad |= !(sum[b] <= kMost) || !(sum[b] + other_half(sum[b]) >= 0.5f);
@@ -513,7 +536,8 @@ struct Line {
   __device__ inline Line(int n, int64_t V, int D) {
     stages = n > 0 ? cdiv(n, kSweepStage) : 1;
     total = cdiv(V, sweep_rows(D)) * stages;
-    parts = (int)(total / kLeast < kItemsGrid ? (total < kLeast ? 1 : total / kLeast) : kItemsGrid);
+    const int grid = items_grid(D);
+    parts = (int)(total / kLeast < grid ? (total < kLeast ? 1 : total / kLeast) : grid);
   }
   __device__ inline int64_t begin(int part) const { return total * part / parts; }
 };
@@ -558,8 +582,10 @@ __global__ __launch_bounds__(256, (kWaves<DP, true>)) void k_ce_sweep_items(Ce c
     for (int k = 0; k < S::kAhead; ++k) fetch(k);
     landed_and_sync<(S::kAhead - 1) * S::kLoads>();
     s.read_rows(s.slot(0));
-    s.first(0);
-    s.read_rows(s.slot(0) + 32 * S::kRow);
+    if constexpr (!S::kPlain) {
+      s.first(0);
+      s.read_rows(s.slot(0) + 32 * S::kRow);
+    }
     f32x4 sh[4];
     // the shifts of a step (four at a time, as the ones before are done with) and, a row a lane, its targets
     auto shifts_at = [&](uint32_t at) INLINED {
@@ -580,6 +606,26 @@ __global__ __launch_bounds__(256, (kWaves<DP, true>)) void k_ce_sweep_items(Ce c
       const int t = t_next;
       float y[4];
       constexpr int ALL = S::kNB * 16;
+      if constexpr (S::kPlain) {
+        s.first(Q);
+        if (Q == 0) fetch(k + S::kAhead);
+        s.read_rows(Q == 0 ? s.slot(k) + 32 * S::kRow : s.slot(k + 1));
+        t_next = read_target(after);
+#pragma unroll
+        for (int n = 0; n < S::NT; ++n) s.template read_col<Q>(n);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+#pragma unroll
+          for (int b = 0; b < S::kNB; ++b) {
+            float v[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              v[j] = exp2_of(__builtin_fmaf(s.z[Q][b][2 * i + j], cc, -sh[i / 2][2 * i % 4 + j]));
+            s.p[Q][b][i] = pack2(v[0], v[1]);
+          }
+          if (i % 2) read_shift(i / 2, shifts);
+        }
+      } else {
       s.template turn<Q>([&](int w) {
         if (Q == 0 && w == 1) fetch(k + S::kAhead);
         if (w == 2) t_next = read_target(after);
@@ -591,6 +637,7 @@ __global__ __launch_bounds__(256, (kWaves<DP, true>)) void k_ce_sweep_items(Ce c
         }
       });
       s.template finished<Q>(ALL - 1, y);
+      }
       // a row whose target is among the wave's items (behind the last row all that is loaded is 0: a row of zeros, whose
       // product is 0 whatever P is)
       if (__builtin_expect(__any((unsigned)(t - (int)own0) < (unsigned)(S::kNB * 32)), 0)) {
@@ -614,6 +661,7 @@ __global__ __launch_bounds__(256, (kWaves<DP, true>)) void k_ce_sweep_items(Ce c
           }
         }
       }
+      if constexpr (S::kPlain) s.last(Q);
     };
     s.settle();
     for (int k = 0; k < count; ++k) {
@@ -623,7 +671,7 @@ __global__ __launch_bounds__(256, (kWaves<DP, true>)) void k_ce_sweep_items(Ce c
       s.move_on(S::step_of(k + 1), S::step_of(k));
       s.settle();
     }
-    s.last(1);
+    if constexpr (!S::kPlain) s.last(1);
     wait_and_sync<>();
     const float f = whole ? *grad * fabsf(c.scale) : 1.f;
 #pragma unroll
@@ -735,8 +783,8 @@ template <int DP> hipError_t items_t(const Ce& c, char* ws, const float* grad, _
   if (e != hipSuccess) return e;
   if (c.R) k_ce_shift<<<(unsigned)cdiv(c.R, 256), 256, 0, st>>>(c, shift, own);
   const int64_t far = spread_of(cdiv(c.V, S::kOwned));
-  k_ce_sweep_items<DP><<<kItemsGrid, 256, S::kLds, st>>>(c, shift, own, grad, far, dE, sums);
-  k_ce_pieces_join<<<dim3(kItemsGrid - 1, (unsigned)cdiv((int64_t)S::kOwned * c.D, 1024)), 256, 0, st>>>(c, sums, far,
+  k_ce_sweep_items<DP><<<items_grid(c.D), 256, S::kLds, st>>>(c, shift, own, grad, far, dE, sums);
+  k_ce_pieces_join<<<dim3(items_grid(c.D) - 1, (unsigned)cdiv((int64_t)S::kOwned * c.D, 1024)), 256, 0, st>>>(c, sums, far,
                                                                                                       grad, dE);
   return hipGetLastError();
 }
@@ -757,7 +805,7 @@ hipError_t launch_ce_rows(const Ce& c, char* ws, bool grad, const float* zt, flo
                       : by(std::integral_constant<int, 256>{});
 }
 size_t ce_items_bytes(int64_t R, int64_t V, int D) {
-  return 2 * up(R * 4, 256) + (size_t)kItemsGrid * 2 * sweep_rows(D) * D * 4;
+  return 2 * up(R * 4, 256) + (size_t)items_grid(D) * 2 * sweep_rows(D) * D * 4;
 }
 hipError_t launch_ce_items(const Ce& c, char* ws, const float* grad, void* dH, void* dE, hipStream_t st) {
   if (dH && c.R) k_ce_dh_out<<<(unsigned)cdiv(c.R * c.D, 1024), 256, 0, st>>>(c, grad, (__bf16*)dH);
