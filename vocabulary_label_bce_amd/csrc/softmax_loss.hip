@@ -8,9 +8,12 @@
 // sums and products and joined in at the end: 1 - p_t is the others' share of the sum, and is exact to rounding where
 // p_t is near 1, as a row's loss log(1 + others / e_t) is.
 //
-// The path of this file, for every size: the sums by one product kernel whose tiles are reduced where they are formed
-// (k_ce_sums); the gradients in pieces of the vocabulary, for each of which dz is formed again, kept in 16 (32) bits and
-// multiplied with E and with H (k_ce_dz, k_ce_dh, k_ce_de).
+// The path of this file, for float32 and for bf16 rows of more than 256 features: the sums by one product kernel whose tiles
+// are reduced where they are formed (k_ce_sums); the gradients in pieces of the vocabulary, for each of which dz is formed
+// again, kept in 16 (32) bits and multiplied with E and with H (k_ce_dz, k_ce_dh, k_ce_de). The matrix units bound it:
+// 4,096 rows, 131,072 items of 2,048 features, bf16, 0.97 to 1.07 PFLOP/s in each of the four products (a large product of
+// the library: 1.30); 738 x 65,537 x 256 in float32 84 to 104 TFLOP/s (154), where a tile has 16 stages for its beginning
+// and end to hide behind, and 513 x 2 tiles of dE come to two rounds of the chip and two tiles.
 #include "softmax.h"
 
 namespace cutbce {
@@ -23,7 +26,8 @@ namespace {
 
 // A workgroup has a range of rows, each wave one at a time: its place among the counted ones, its copy, and c times its
 // product with its target's item. All of them count all targets first, which is what one of them would have to do before
-// the others could start.
+// the others could start. Latency bounds it: 5.4 us for 32 rows of 64 (two launches: 6.6), 28 for 25,600 of 128 (25), most
+// of it the count.
 template <typename T, typename I>
 __global__ __launch_bounds__(1024) void k_ce_rows(Ce c, const T* __restrict__ H, const I* __restrict__ targets,
                                                   const float* __restrict__ weight, float* __restrict__ zt) {
@@ -305,7 +309,10 @@ template <> struct Sizes<__bf16, true> {
   using Dh = Product<__bf16, 2, 4, 4, 2, 64, false, true>;
   using De = Product<__bf16, 2, 4, 4, 2, 64, true, true>;
 };
-bool big(int64_t R, int D, int dtype) { return dtype == 1 && R >= 512; }
+// Tiles of 256 x 256 are read by half as many workgroups, but leave CUs idle where there are few rows. 65,536 items of
+// 1,024 features, all four products: 200 rows 224 us in large tiles and 212 in small ones, 512 rows 366 and 410; 4,096
+// rows, 131,072 items of 2,048: 8.5 ms and 10.7.
+bool big(int64_t R, int dtype) { return dtype == 1 && R >= 512; }
 
 // Tile (i, j) of ni x nj for a workgroup: every eighth workgroup, those of one XCD, has tiles next to each other, in
 // blocks eight tiles wide, so that they read the same rows of both sides at about the same time. j is out of range for
@@ -343,6 +350,10 @@ __device__ inline Units units_of(int n, int64_t V, int bm, int bn, int grid) {
 }
 template <typename P> constexpr int kCeGrid = P::kLds > 80 * 1024 ? 256 : 512;  // workgroups that are resident
 
+// A unit's tiles follow one another without a pause in the loads. A lane has results of TN rows and keeps their running
+// maximum (of z in base 2) and sum of exponentials; both halves of a wave join at the unit's end. The exponentials are not
+// hidden: 128 a lane and tile, a third of the time at 512 features (4,096 rows x 262,144 x 512: 1,230 to 1,390 us, 0.79 to
+// 0.89 PFLOP/s), a tenth at 2,048.
 template <typename P>
 __global__ __launch_bounds__(P::NL, P::kWaves) void k_ce_sums(Ce c, float2* __restrict__ part) {
   using T = typename P::T;
@@ -497,6 +508,9 @@ __global__ __launch_bounds__(1024) void k_ce_loss(Ce c, const float* __restrict_
 // range of memory, and what a wave stores whole lines. In 16 bits the items of each 16 stand in the order 0-3, 8-11, 4-7,
 // 12-15: a lane's eight results are next to each other, and are the operand of the product with E in the order in which
 // the transposed reads of E give their items.
+// (Rows of the piece's width instead, 64 KB apart: dH of 4,096 x 262,144 x 512 1,740 us, so 1,490.) A workgroup goes
+// through its tiles without a pause in the loads (each tile a workgroup: dz 1,660 us, so 1,490). Storing the values in
+// 16 bits rounds them by at most 2^-8 of themselves, as the product's operands are in any case.
 template <typename T> constexpr int kBlock = 64 / sizeof(T);
 __host__ __device__ constexpr inline int item_at(int place) {  // of 16 bits
   return (place & ~12) | (place & 4) << 1 | (place & 8) >> 1;
@@ -573,7 +587,8 @@ __global__ __launch_bounds__(P::NL, P::kWaves) void k_ce_dz(Ce c, int64_t v0, in
       });
 }
 
-// sums[part] (+)= dz E over the part's items: rows x features.
+// sums[part] (+)= dz E over the part's items: rows x features, the first piece of the vocabulary writes. Parts are as many
+// as fill the chip (clamp_parts), each at least four stages.
 template <typename P>
 __global__ __launch_bounds__(P::NL, P::kWaves) void k_ce_dh(Ce c, int64_t v0, int64_t width, int parts, int first,
                                                     const typename P::T* __restrict__ dz, float* __restrict__ sums) {
@@ -712,9 +727,11 @@ template <typename T, bool BIG> Plan plan_of(int64_t R, int64_t V, int D) {
   using S = Sizes<T, BIG>;
   if (R < 1) R = 1;
   Plan p;
-  // a piece's dz takes up to 256 MB, the size of the memory-side cache
+  // A piece's dz takes up to 512 MB. For each piece dH's partial sums are read and written again, and the launches have
+  // their tails; what is beyond the 256 MB of the memory-side cache comes from memory. Measured, dz + dH + dE of 4,096 x
+  // 262,144 x 512 in pieces of 64 MB, 256 MB, 1 GB: 5.6, 4.2, 3.8 ms; of 131,072 x 2,048: 6.7, 6.2, 6.0.
   const int64_t rows = up(R, 32);
-  int64_t width = ((int64_t)256 << 20) / (rows * (int64_t)sizeof(T)) / 256 * 256;
+  int64_t width = ((int64_t)512 << 20) / (rows * (int64_t)sizeof(T)) / 256 * 256;
   if (width < 256) width = 256;
   if (width > up(V, 256)) width = up(V, 256);
   p.width = width;
@@ -827,28 +844,28 @@ CeSaved ce_saved(int64_t R, int64_t V, int D, int dtype) {
 
 size_t ce_forward_bytes(int64_t R, int64_t V, int D, int dtype, bool want_grad) {
   const size_t own = !dtype            ? forward_plan<float, false>(R, D, want_grad).bytes
-                     : big(R, D, dtype) ? forward_plan<__bf16, true>(R, D, want_grad).bytes
+                     : big(R, dtype) ? forward_plan<__bf16, true>(R, D, want_grad).bytes
                                         : forward_plan<__bf16, false>(R, D, want_grad).bytes;
   return own + (want_grad ? 0 : ce_saved(R, V, D, dtype).bytes);
 }
 size_t ce_backward_bytes(int64_t R, int64_t V, int D, int dtype) {
   if (ce_swept(D, dtype)) return ce_items_bytes(R, V, D);
   return !dtype             ? plan_of<float, false>(R, V, D).bytes
-         : big(R, D, dtype) ? plan_of<__bf16, true>(R, V, D).bytes
+         : big(R, dtype) ? plan_of<__bf16, true>(R, V, D).bytes
                             : plan_of<__bf16, false>(R, V, D).bytes;
 }
 
 hipError_t launch_ce_forward(const Ce& c, int id_bytes, const void* H, const void* targets, const float* weight,
                              bool want_grad, float* loss, float* row_loss, hipStream_t st) {
   if (!c.dtype) return forward_t<float, false>(c, id_bytes, (const float*)H, targets, weight, want_grad, loss, row_loss, st);
-  return big(c.R, c.D, 1)
+  return big(c.R, 1)
              ? forward_t<__bf16, true>(c, id_bytes, (const __bf16*)H, targets, weight, want_grad, loss, row_loss, st)
              : forward_t<__bf16, false>(c, id_bytes, (const __bf16*)H, targets, weight, want_grad, loss, row_loss, st);
 }
 hipError_t launch_ce_backward(const Ce& c, const float* grad, void* dH, void* dE, hipStream_t st) {
   if (ce_swept(c.D, c.dtype)) return launch_ce_items(c, c.ws, grad, dH, dE, st);
   if (!c.dtype) return backward_t<float, false>(c, grad, (float*)dH, (float*)dE, st);
-  return big(c.R, c.D, 1) ? backward_t<__bf16, true>(c, grad, (__bf16*)dH, (__bf16*)dE, st)
+  return big(c.R, 1) ? backward_t<__bf16, true>(c, grad, (__bf16*)dH, (__bf16*)dE, st)
                           : backward_t<__bf16, false>(c, grad, (__bf16*)dH, (__bf16*)dE, st);
 }
 

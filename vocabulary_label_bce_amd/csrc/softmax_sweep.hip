@@ -9,10 +9,17 @@
 // second product's operand as it stands; the step's own tile, read row by row and transposed, is the other operand of both.
 //
 // Two blocks a wave halve what is read from LDS for a product: with one, LDS delivers 128 bytes a cycle at the matrix
-// units' full rate, all that it can. They take about 400 registers, so a SIMD has one wave, and the products hide the
-// vector instructions of the same wave: in one turn of the loop the products Z of the next step and the gradient's of
-// the step before run while the exponentials of this step are formed, none depending on another. The order is pinned, a
-// share of the vector work behind each matrix instruction.
+// units' full rate, all that it can. Beyond 64 features they take all of a SIMD's registers for one wave, so the products
+// have to hide the vector instructions of the same wave: in one turn of the loop the products Z of the next step and the
+// gradient's of the step before run while the exponentials of this step are formed, none depending on another. The order
+// is pinned, a share of the vector work behind each matrix instruction. Up to 64 features two workgroups fit a CU, and
+// their waves hide each other (kPlain): a step's products, exponentials and products follow one another, which needs
+// fewer registers (the backward's sweep of 5,120 rows and 100,000 items of 64 in turns as above, one wave a SIMD: 236 us,
+// so 157; the forward's 168 either way).
+//
+// What bounds them: the matrix units' power. 14,336 rows x 876,000 x 128: 5.1 to 5.6 ms a sweep, 1.15 to 1.26 PFLOP/s at
+// 1.5 to 1.8 GHz, a large product of the library having 1.30 on the same card. At 64 features an exponential costs as much
+// as its products (770 to 840 TFLOP/s), at 256 a wave has one block (4,096 rows x 131,072: 1.05 ms for both, 1.05 PFLOP/s).
 #include "softmax.h"
 
 namespace cutbce {
@@ -33,10 +40,10 @@ __device__ inline uint32_t pack2(float a, float b) {
   return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)a, (__bf16)b});
 }
 
-// The ring of one workgroup and a wave's operands.
 // Waves a SIMD has: two where the registers allow it.
 template <int DP, bool ITEMS> constexpr int kWaves = DP <= 64 ? 2 : 1;
 
+// The ring of one workgroup and a wave's operands.
 template <int DP, bool AUX, bool GRAD> struct Sweep {
   using Ti = Tile<__bf16, DP>;
   using Ld = Dma<__bf16, DP, kSweepStage, 256>;
@@ -49,7 +56,7 @@ template <int DP, bool AUX, bool GRAD> struct Sweep {
   static constexpr int kStage = kTile + kAux, kLds = kStages * kStage;
   static constexpr int kLoads = Ld::kRounds + (AUX ? 1 : 0);    // of a wave for a stage
   static constexpr bool kAlone = kWaves<DP, AUX> == 1 && GRAD, kHeld = kWaves<DP, AUX> == 1;
-  static constexpr bool kPlain = !kHeld;
+  static constexpr bool kPlain = !kHeld;  // one product after the other
   static_assert(NT == 2 * NDB, "");
 
   Ld ld;
@@ -353,23 +360,23 @@ __global__ __launch_bounds__(256, (kWaves<DP, false>)) void k_ce_sweep_rows(Ce c
             }
           if constexpr (GRAD) s.last(Q);
         } else {
-        auto end = [&](int i) {
-          float& a = add[i % S::kNB][i / S::kNB & 1];
-          a += y[i & 3];
-          asm volatile("" : "+v"(a));
-          if (GRAD) s.template finished<Q>(i, y);
-        };
-        s.template turn<Q>([&](int w) {
-          if (Q == 0 && w == 1) fetch(k + S::kAhead);
-  #pragma unroll
-          for (int i = ALL * w / S::kSlots; i < ALL * (w + 1) / S::kSlots; ++i) {
-            s.template element<Q>(i, y, [&](int b, int, float z) { return __builtin_fmaf(z, cc, -ref[b]); });
-            if (i) end(i - 1);
-          }
-        });
-        end(ALL - 1);
+          auto end = [&](int i) {
+            float& a = add[i % S::kNB][i / S::kNB & 1];
+            a += y[i & 3];
+            asm volatile("" : "+v"(a));
+            if (GRAD) s.template finished<Q>(i, y);
+          };
+          s.template turn<Q>([&](int w) {
+            if (Q == 0 && w == 1) fetch(k + S::kAhead);
+#pragma unroll
+            for (int i = ALL * w / S::kSlots; i < ALL * (w + 1) / S::kSlots; ++i) {
+              s.template element<Q>(i, y, [&](int b, int, float z) { return __builtin_fmaf(z, cc, -ref[b]); });
+              if (i) end(i - 1);
+            }
+          });
+          end(ALL - 1);
         }
-  #pragma unroll
+#pragma unroll
         for (int b = 0; b < S::kNB; ++b) sum[b] += add[b][0] + add[b][1];
       };
       s.settle();
@@ -527,8 +534,8 @@ __global__ __launch_bounds__(256) void k_ce_shift(Ce c, float* __restrict__ shif
 // The work, tiles of items (in steps of `spread`) x stages of rows, is one line that is cut into as many equal parts as there are workgroups
 // (each at least kLeast stages, where there is that much): a workgroup goes through whole tiles, and the ends of its part
 // are pieces of tiles that it shares with its neighbours. A piece's sums go to place 0 of its workgroup's two if it
-// begins where the part does, else to 1, and are joined by k_ce_pieces_join. (With whole tiles alone 100,000 items of 64
-// features, 391 tiles on 256 CUs, take 235 us.)
+// begins where the part does, else to 1, and are joined by k_ce_pieces_join. (With whole tiles alone 391 tiles of 100,000
+// items on 256 CUs would take the time of 512.)
 constexpr int kLeast = 4;
 struct Line {
   int64_t stages, total;  // of a tile, and of all
@@ -626,17 +633,17 @@ __global__ __launch_bounds__(256, (kWaves<DP, true>)) void k_ce_sweep_items(Ce c
           if (i % 2) read_shift(i / 2, shifts);
         }
       } else {
-      s.template turn<Q>([&](int w) {
-        if (Q == 0 && w == 1) fetch(k + S::kAhead);
-        if (w == 2) t_next = read_target(after);
+        s.template turn<Q>([&](int w) {
+          if (Q == 0 && w == 1) fetch(k + S::kAhead);
+          if (w == 2) t_next = read_target(after);
 #pragma unroll
-        for (int i = ALL * w / S::kSlots; i < ALL * (w + 1) / S::kSlots; ++i) {
-          s.template element<Q>(i, y, [&](int, int e, float z) { return __builtin_fmaf(z, cc, -sh[e / 4][e % 4]); });
-          if (i % (4 * S::kNB) == 4 * S::kNB - 1) read_shift(i / (4 * S::kNB), shifts);
-          if (i) s.template finished<Q>(i - 1, y);
-        }
-      });
-      s.template finished<Q>(ALL - 1, y);
+          for (int i = ALL * w / S::kSlots; i < ALL * (w + 1) / S::kSlots; ++i) {
+            s.template element<Q>(i, y, [&](int, int e, float z) { return __builtin_fmaf(z, cc, -sh[e / 4][e % 4]); });
+            if (i % (4 * S::kNB) == 4 * S::kNB - 1) read_shift(i / (4 * S::kNB), shifts);
+            if (i) s.template finished<Q>(i - 1, y);
+          }
+        });
+        s.template finished<Q>(ALL - 1, y);
       }
       // a row whose target is among the wave's items (behind the last row all that is loaded is 0: a row of zeros, whose
       // product is 0 whatever P is)
