@@ -587,15 +587,26 @@ __global__ __launch_bounds__(P::NL, P::kWaves) void k_ce_dz(Ce c, int64_t v0, in
       });
 }
 
-// sums[part] (+)= dz E over the part's items: rows x features, the first piece of the vocabulary writes. Parts are as many
-// as fill the chip (clamp_parts), each at least four stages.
+// Parts of a long axis, of `steps` stages, for so many tiles: as many workgroups as are resident, each at least four stages.
+__host__ __device__ inline int parts_of(int64_t tiles, int64_t steps, int grid) {
+  int64_t parts = tiles < grid ? grid / (tiles ? (int)tiles : 1) : 1;
+  if (parts > steps / 4) parts = steps / 4;
+  return parts < 1 ? 1 : (int)parts;
+}
+// Of dH: by the rows that are counted, which only the device knows (777 rows, 739 of them counted, 65,537 x 256, float32:
+// 275 us by all rows, 432 workgroups on 512 places; so 241).
+template <typename P> __host__ __device__ inline int dh_parts(int64_t n, int D, int64_t width) {
+  return parts_of(cdiv(n, P::BM) * cdiv(D, P::BN), width / P::K, kCeGrid<P>);
+}
+
+// sums[part][n][D] (+)= dz E over the part's items: rows x features, the first piece of the vocabulary writes.
 template <typename P>
-__global__ __launch_bounds__(P::NL, P::kWaves) void k_ce_dh(Ce c, int64_t v0, int64_t width, int parts, int first,
+__global__ __launch_bounds__(P::NL, P::kWaves) void k_ce_dh(Ce c, int64_t v0, int64_t width, int first,
                                                     const typename P::T* __restrict__ dz, float* __restrict__ sums) {
   using T = typename P::T;
   extern __shared__ __align__(1024) char lds[];
   const int n = at<CeHead>(c.saved, c.at.head)->n;
-  const int cols = (c.D + P::BN - 1) / P::BN, rows = (int)cdiv(n, P::BM);
+  const int cols = (c.D + P::BN - 1) / P::BN, rows = (int)cdiv(n, P::BM), parts = dh_parts<P>(n, c.D, width);
   const TileAt tile = tile_at(blockIdx.x, cols, rows * parts);  // (of one part of the items: neighbours read the same)
   if (!rows || tile.j >= rows * parts) return;
   const int part = tile.j / rows;
@@ -609,7 +620,7 @@ __global__ __launch_bounds__(P::NL, P::kWaves) void k_ce_dh(Ce c, int64_t v0, in
   p.a.start(dz, row0, n, x0 * P::K, x1 * P::K < width ? x1 * P::K : width);
   p.b.start(E, d0, c.D, x0 * P::K, x1 * P::K < left ? x1 * P::K : left);
   p.run((int)(x1 - x0), [](int) {}, [](int) {});
-  float* to = sums + (int64_t)part * c.R * c.D;
+  float* to = sums + (int64_t)part * n * c.D;
   const int h = p.lane / 32;
 #pragma unroll
   for (int i = 0; i < P::TM; ++i)
@@ -689,9 +700,10 @@ __global__ __launch_bounds__(256) void k_ce_de_join(Ce c, int64_t v0, int64_t wi
 }
 
 // dH of all rows, zeros for those without a target: four features a lane, the sum of the parts'.
-template <typename T>
-__global__ __launch_bounds__(256) void k_ce_dh_join(Ce c, int parts, const float* __restrict__ sums,
-                                                    const float* __restrict__ grad, T* __restrict__ dH) {
+template <typename P>
+__global__ __launch_bounds__(256) void k_ce_dh_join(Ce c, int64_t width, const float* __restrict__ sums,
+                                                    const float* __restrict__ grad, typename P::T* __restrict__ dH) {
+  using T = typename P::T;
   const int64_t x = ((int64_t)(blockIdx.y * gridDim.x + blockIdx.x) * 256 + threadIdx.x) * 4;
   if (x >= c.R * c.D) return;
   const int64_t r = x / c.D;
@@ -699,7 +711,8 @@ __global__ __launch_bounds__(256) void k_ce_dh_join(Ce c, int parts, const float
   f32x4 s = {0.f, 0.f, 0.f, 0.f};
   if (i >= 0) {
     const int64_t from = (int64_t)i * c.D + (x - r * c.D);
-    for (int k = 0; k < parts; ++k) s += *(const f32x4*)(sums + (int64_t)k * c.R * c.D + from);
+    const int n = at<CeHead>(c.saved, c.at.head)->n, parts = dh_parts<P>(n, c.D, width);
+    for (int k = 0; k < parts; ++k) s += *(const f32x4*)(sums + (int64_t)k * n * c.D + from);
     s *= *grad * c.scale;
   }
   typedef T V4 __attribute__((ext_vector_type(4)));
@@ -714,15 +727,9 @@ __global__ __launch_bounds__(256) void k_ce_dh_join(Ce c, int parts, const float
 // ---------------------------------------------------------------------------------------------------------
 struct Plan {
   int64_t width;           // items of a piece
-  int dh_parts, de_parts;
+  int de_parts;
   size_t dz, dh, de, bytes;  // offsets in the workspace
 };
-int64_t clamp_parts(int64_t tiles, int64_t steps, int64_t most, int grid) {
-  int64_t parts = tiles < grid ? grid / (tiles ? tiles : 1) : 1;  // as many workgroups as are resident
-  if (parts > steps / 4) parts = steps / 4;                     // each at least four stages
-  if (parts > most) parts = most;
-  return parts < 1 ? 1 : parts;
-}
 template <typename T, bool BIG> Plan plan_of(int64_t R, int64_t V, int D) {
   using S = Sizes<T, BIG>;
   if (R < 1) R = 1;
@@ -735,12 +742,12 @@ template <typename T, bool BIG> Plan plan_of(int64_t R, int64_t V, int D) {
   if (width < 256) width = 256;
   if (width > up(V, 256)) width = up(V, 256);
   p.width = width;
-  p.dh_parts = (int)clamp_parts(cdiv(R, S::Dh::BM) * cdiv(D, S::Dh::BN), width / S::Dh::K,
-                                ((int64_t)256 << 20) / (R * D * 4) + 1, kCeGrid<typename S::Dh>);
-  p.de_parts = (int)clamp_parts(width / S::De::BM * cdiv(D, S::De::BN), cdiv(R, S::De::K), 64, kCeGrid<typename S::De>);
+  p.de_parts = parts_of(width / S::De::BM * cdiv(D, S::De::BN), cdiv(R, S::De::K), kCeGrid<typename S::De>);
   size_t b = 0;
   p.dz = b, b += up(rows * width * (int64_t)sizeof(T), 256);
-  p.dh = b, b += up((int64_t)p.dh_parts * R * D * 4, 256);
+  // dH's parts: one of all rows, or as many tiles as are resident
+  const int64_t few = (int64_t)kCeGrid<typename S::Dh> * S::Dh::BM * (S::Dh::BN < D ? S::Dh::BN : D);
+  p.dh = b, b += up((few > R * D ? few : R * D) * 4, 256);
   p.de = b, b += p.de_parts > 1 ? up((int64_t)p.de_parts * width * D * 4, 256) : 0;
   p.bytes = b;
   return p;
@@ -809,9 +816,11 @@ hipError_t backward_t(const Ce& c, const float* grad, T* dH, T* dE, hipStream_t 
     const int64_t tiles = up(cdiv(c.R, S::Sums::BN) * (p.width / S::Sums::BM), 8);
     if (c.R) k_ce_dz<typename S::Sums><<<(unsigned)(tiles < kCeGrid<typename S::Sums> ? tiles : kCeGrid<typename S::Sums>),
                                          S::Sums::NL, S::Sums::kLds, st>>>(c, v, p.width, dz);
-    if (dH && c.R)
-      k_ce_dh<typename S::Dh><<<(unsigned)(cdiv(c.R, S::Dh::BM) * cdiv(c.D, S::Dh::BN) * p.dh_parts), S::Dh::NL,
-                                S::Dh::kLds, st>>>(c, v, p.width, p.dh_parts, v == 0, dz, dh);
+    if (dH && c.R) {
+      const int64_t most = up(cdiv(c.R, S::Dh::BM) * cdiv(c.D, S::Dh::BN), 8);
+      k_ce_dh<typename S::Dh><<<(unsigned)(most > kCeGrid<typename S::Dh> ? most : kCeGrid<typename S::Dh>), S::Dh::NL,
+                                S::Dh::kLds, st>>>(c, v, p.width, v == 0, dz, dh);
+    }
     if (dE) {
       const unsigned tiles = (unsigned)(p.width / S::De::BM * cdiv(c.D, S::De::BN));
       if (p.de_parts > 1) {
@@ -824,7 +833,7 @@ hipError_t backward_t(const Ce& c, const float* grad, T* dH, T* dE, hipStream_t 
     }
   }
   const int64_t blocks = cdiv(c.R * c.D, 1024), turns = cdiv(blocks, kMaxGrid);
-  if (dH && c.R) k_ce_dh_join<T><<<dim3((unsigned)cdiv(blocks, turns), (unsigned)turns), 256, 0, st>>>(c, p.dh_parts, dh, grad, dH);
+  if (dH && c.R) k_ce_dh_join<typename S::Dh><<<dim3((unsigned)cdiv(blocks, turns), (unsigned)turns), 256, 0, st>>>(c, p.width, dh, grad, dH);
   return hipGetLastError();
 }
 
