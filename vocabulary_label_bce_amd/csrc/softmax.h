@@ -53,8 +53,9 @@ __device__ inline void finish_row(const Ce& c, int i, int64_t r, float z, float 
                                   float* each) {
   const float mine = exp2_of(z - m), sum = others + mine;
   const float l = mine == 1.f ? log1pf(others) : (m - z) * kLn2 + logf(sum);
-  at<float>(c.saved, c.at.lse)[i] = m + log2f(sum);
-  at<float>(c.saved, c.at.rest)[i] = others / sum;
+  const float coef = at<float>(c.saved, c.at.coef)[i];
+  at<float>(c.saved, c.at.shift)[i] = m + log2f(sum) - log2f(coef);
+  at<float>(c.saved, c.at.own)[i] = -coef * (others / sum);
   each[i] = l;
   if (row_loss) row_loss[r] = l;
 }

@@ -554,9 +554,8 @@ __global__ __launch_bounds__(P::NL, P::kWaves) void k_ce_dz(Ce c, int64_t v0, in
           float shift = INFINITY, own = 0.f;
           int64_t target = -1;
           if (i < n) {
-            const float coef = at<float>(c.saved, c.at.coef)[i];
-            shift = at<float>(c.saved, c.at.lse)[i] - log2f(coef);
-            own = -coef * at<float>(c.saved, c.at.rest)[i];
+            shift = at<float>(c.saved, c.at.shift)[i];
+            own = at<float>(c.saved, c.at.own)[i];
             target = at<int32_t>(c.saved, c.at.target)[i];
           }
 #pragma unroll
@@ -843,7 +842,7 @@ CeSaved ce_saved(int64_t R, int64_t V, int D, int dtype) {
   CeSaved s;
   size_t b = 0;
   s.head = b, b += 256;
-  size_t* each[] = {&s.rows, &s.place, &s.target, &s.lse, &s.rest, &s.coef};
+  size_t* each[] = {&s.rows, &s.place, &s.target, &s.shift, &s.own, &s.coef};
   for (size_t* x : each) *x = b, b += up(R * 4, 256);
   s.hc = b, b += up(R * D * (dtype ? 2 : 4), 256);
   s.dh = b, b += ce_swept(D, dtype) ? up(R * D * 4, 256) : 0;
@@ -858,7 +857,7 @@ size_t ce_forward_bytes(int64_t R, int64_t V, int D, int dtype, bool want_grad) 
   return own + (want_grad ? 0 : ce_saved(R, V, D, dtype).bytes);
 }
 size_t ce_backward_bytes(int64_t R, int64_t V, int D, int dtype) {
-  if (ce_swept(D, dtype)) return ce_items_bytes(R, V, D);
+  if (ce_swept(D, dtype)) return ce_items_bytes(D);
   return !dtype             ? plan_of<float, false>(R, V, D).bytes
          : big(R, dtype) ? plan_of<__bf16, true>(R, V, D).bytes
                             : plan_of<__bf16, false>(R, V, D).bytes;

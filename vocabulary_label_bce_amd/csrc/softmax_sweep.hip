@@ -522,19 +522,10 @@ __global__ __launch_bounds__(256) void k_ce_sweep_join(Ce c, const float2* __res
 // Backward.
 // ---------------------------------------------------------------------------------------------------------
 
-// What a row brings to its column of P: exp2(c z - shift), or at its target `own` instead.
-__global__ __launch_bounds__(256) void k_ce_shift(Ce c, float* __restrict__ shift, float* __restrict__ own) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= at<CeHead>(c.saved, c.at.head)->n) return;
-  const float coef = at<float>(c.saved, c.at.coef)[i];
-  shift[i] = at<float>(c.saved, c.at.lse)[i] - log2f(coef);
-  own[i] = -coef * at<float>(c.saved, c.at.rest)[i];
-}
-
 // The work, tiles of items (in steps of `spread`) x stages of rows, is one line that is cut into as many equal parts as there are workgroups
 // (each at least kLeast stages, where there is that much): a workgroup goes through whole tiles, and the ends of its part
 // are pieces of tiles that it shares with its neighbours. A piece's sums go to place 0 of its workgroup's two if it
-// begins where the part does, else to 1, and are joined by k_ce_pieces_join. (With whole tiles alone 391 tiles of 100,000
+// begins where the part does, else to 1, and are joined by k_ce_finish. (With whole tiles alone 391 tiles of 100,000
 // items on 256 CUs would take the time of 512.)
 constexpr int kLeast = 4;
 struct Line {
@@ -550,9 +541,7 @@ struct Line {
 };
 
 template <int DP>
-__global__ __launch_bounds__(256, (kWaves<DP, true>)) void k_ce_sweep_items(Ce c, const float* __restrict__ shift,
-                                                                            const float* __restrict__ own,
-                                                                            const float* __restrict__ grad,
+__global__ __launch_bounds__(256, (kWaves<DP, true>)) void k_ce_sweep_items(Ce c, const float* __restrict__ grad,
                                                                             int64_t spread, __bf16* __restrict__ dE,
                                                                             float* __restrict__ sums) {
   using S = Sweep<DP, true, true>;
@@ -565,7 +554,7 @@ __global__ __launch_bounds__(256, (kWaves<DP, true>)) void k_ce_sweep_items(Ce c
   S s;
   s.init(lds, at<__bf16>(c.saved, c.at.hc), n, c.D);
   const int32_t* targets = at<int32_t>(c.saved, c.at.target);
-  const void* aux = s.wave == 1 ? (const void*)targets : (s.wave == 2 ? (const void*)own : (const void*)shift);
+  const void* aux = s.wave == 1 ? (const void*)targets : c.saved + (s.wave == 2 ? c.at.own : c.at.shift);
   for (int64_t x = from; x < to;) {
     const int64_t at_tile = x / line.stages, tile = at_tile * spread % tiles;
     const int s0 = (int)(x - at_tile * line.stages);
@@ -695,42 +684,46 @@ __global__ __launch_bounds__(256, (kWaves<DP, true>)) void k_ce_sweep_items(Ce c
   }
 }
 
-// The tiles that were shared: block.x - 1 is the first workgroup of one, the others follow it. Four features a lane.
-__global__ __launch_bounds__(256) void k_ce_pieces_join(Ce c, const float* __restrict__ sums, int64_t spread,
-                                                        const float* __restrict__ grad, __bf16* __restrict__ dE) {
-  const Line line(at<CeHead>(c.saved, c.at.head)->n, c.V, c.D);
-  const int part = blockIdx.x + 1;  // of the tile's second piece
-  if (part >= line.parts) return;
-  const int64_t cut = line.begin(part), at_tile = cut / line.stages, x0 = at_tile * line.stages;
-  const int owned = sweep_rows(c.D);
-  const int64_t tile = at_tile * spread % cdiv(c.V, owned);
-  const int64_t before = line.begin(part - 1);
-  if (cut == x0 || before > x0) return;  // cut at a tile's end, or not the tile's first cut
-  const int64_t v0 = tile * owned, rows = c.V - v0 < owned ? c.V - v0 : owned;
-  const int64_t x = ((int64_t)blockIdx.y * 256 + threadIdx.x) * 4;
-  if (x >= rows * c.D) return;
-  const int64_t piece = (int64_t)owned * c.D;
-  f32x4 s = *(const f32x4*)(sums + ((int64_t)(part - 1) * 2 + (before == x0 ? 0 : 1)) * piece + x);
-  for (int p = part; p < line.parts && line.begin(p) < x0 + line.stages; ++p)
-    s += *(const f32x4*)(sums + (int64_t)p * 2 * piece + x);
-  const float f = *grad * fabsf(c.scale);
+// What is left when the sweep is done, four features a lane. The first `pieces` workgroups: the tiles that were shared, each
+// by the first workgroup of its parts but one. The others: dH of all rows from saved's, zeros for those left out.
+__global__ __launch_bounds__(256) void k_ce_finish(Ce c, const float* __restrict__ sums, int64_t spread, int pieces,
+                                                   const float* __restrict__ grad, __bf16* __restrict__ dH,
+                                                   __bf16* __restrict__ dE) {
   typedef __bf16 V4 __attribute__((ext_vector_type(4)));
+  f32x4 s = {0.f, 0.f, 0.f, 0.f};
+  V4* to;
+  float f;
+  if ((int)blockIdx.x >= pieces) {
+    const int64_t x = ((int64_t)(blockIdx.x - pieces) * 256 + threadIdx.x) * 4;
+    if (x >= c.R * c.D) return;
+    const int64_t r = x / c.D;
+    const int i = at<int32_t>(c.saved, c.at.place)[r];
+    if (i >= 0) s = *(const f32x4*)(at<float>(c.saved, c.at.dh) + (int64_t)i * c.D + (x - r * c.D));
+    f = *grad * c.scale, to = (V4*)(dH + x);
+    if (i < 0) f = 0.f;
+  } else {
+    const Line line(at<CeHead>(c.saved, c.at.head)->n, c.V, c.D);
+    const int parts = items_grid(c.D) - 1;
+    const int part = blockIdx.x % parts + 1;  // of the tile's second piece
+    if (part >= line.parts) return;
+    const int64_t cut = line.begin(part), at_tile = cut / line.stages, x0 = at_tile * line.stages;
+    const int owned = sweep_rows(c.D);
+    const int64_t tile = at_tile * spread % cdiv(c.V, owned);
+    const int64_t before = line.begin(part - 1);
+    if (cut == x0 || before > x0) return;  // cut at a tile's end, or not the tile's first cut
+    const int64_t v0 = tile * owned, rows = c.V - v0 < owned ? c.V - v0 : owned;
+    const int64_t x = ((int64_t)(blockIdx.x / parts) * 256 + threadIdx.x) * 4;
+    if (x >= rows * c.D) return;
+    const int64_t piece = (int64_t)owned * c.D;
+    s = *(const f32x4*)(sums + ((int64_t)(part - 1) * 2 + (before == x0 ? 0 : 1)) * piece + x);
+    for (int p = part; p < line.parts && line.begin(p) < x0 + line.stages; ++p)
+      s += *(const f32x4*)(sums + (int64_t)p * 2 * piece + x);
+    f = *grad * fabsf(c.scale), to = (V4*)(dE + v0 * c.D + x);
+  }
   V4 y;
 #pragma unroll
   for (int j = 0; j < 4; ++j) y[j] = (__bf16)(s[j] * f);
-  *(V4*)(dE + v0 * c.D + x) = y;
-}
-
-// dH of all rows from saved's, zeros for those left out: four features a lane.
-__global__ __launch_bounds__(256) void k_ce_dh_out(Ce c, const float* __restrict__ grad, __bf16* __restrict__ dH) {
-  const int64_t x = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
-  if (x >= c.R * c.D) return;
-  const int64_t r = x / c.D;
-  const int i = at<int32_t>(c.saved, c.at.place)[r];
-  f32x4 s = {0.f, 0.f, 0.f, 0.f};
-  if (i >= 0) s = *(const f32x4*)(at<float>(c.saved, c.at.dh) + (int64_t)i * c.D + (x - r * c.D)) * (*grad * c.scale);
-#pragma unroll
-  for (int j = 0; j < 4; ++j) dH[x + j] = (__bf16)s[j];
+  *to = y;
 }
 
 // The line's tiles are taken in steps of this many, a golden section of them with no common factor: neighbouring items,
@@ -783,16 +776,11 @@ template <int DP, bool GRAD> hipError_t rows_t(const Ce& c, char* ws, const floa
   return hipGetLastError();
 }
 
-template <int DP> hipError_t items_t(const Ce& c, char* ws, const float* grad, __bf16* dE, hipStream_t st) {
+template <int DP> hipError_t items_t(const Ce& c, float* sums, const float* grad, int64_t far, __bf16* dE, hipStream_t st) {
   using S = Sweep<DP, true, true>;
-  float *shift = (float*)ws, *own = (float*)(ws + up(c.R * 4, 256)), *sums = (float*)(ws + 2 * up(c.R * 4, 256));
   const hipError_t e = allow_lds<k_ce_sweep_items<DP>>(S::kLds);
   if (e != hipSuccess) return e;
-  if (c.R) k_ce_shift<<<(unsigned)cdiv(c.R, 256), 256, 0, st>>>(c, shift, own);
-  const int64_t far = spread_of(cdiv(c.V, S::kOwned));
-  k_ce_sweep_items<DP><<<items_grid(c.D), 256, S::kLds, st>>>(c, shift, own, grad, far, dE, sums);
-  k_ce_pieces_join<<<dim3(items_grid(c.D) - 1, (unsigned)cdiv((int64_t)S::kOwned * c.D, 1024)), 256, 0, st>>>(c, sums, far,
-                                                                                                      grad, dE);
+  k_ce_sweep_items<DP><<<items_grid(c.D), 256, S::kLds, st>>>(c, grad, far, dE, sums);
   return hipGetLastError();
 }
 
@@ -811,17 +799,19 @@ hipError_t launch_ce_rows(const Ce& c, char* ws, bool grad, const float* zt, flo
          : c.D <= 128 ? by(std::integral_constant<int, 128>{})
                       : by(std::integral_constant<int, 256>{});
 }
-size_t ce_items_bytes(int64_t R, int64_t V, int D) {
-  return 2 * up(R * 4, 256) + (size_t)items_grid(D) * 2 * sweep_rows(D) * D * 4;
-}
+size_t ce_items_bytes(int D) { return (size_t)items_grid(D) * 2 * sweep_rows(D) * D * 4; }
 hipError_t launch_ce_items(const Ce& c, char* ws, const float* grad, void* dH, void* dE, hipStream_t st) {
-  if (dH && c.R) k_ce_dh_out<<<(unsigned)cdiv(c.R * c.D, 1024), 256, 0, st>>>(c, grad, (__bf16*)dH);
+  const int64_t far = spread_of(cdiv(c.V, sweep_rows(c.D)));
+  float* sums = (float*)ws;
   if (dE) {
-    const hipError_t e = c.D <= 64    ? items_t<64>(c, ws, grad, (__bf16*)dE, st)
-                         : c.D <= 128 ? items_t<128>(c, ws, grad, (__bf16*)dE, st)
-                                      : items_t<256>(c, ws, grad, (__bf16*)dE, st);
+    const hipError_t e = c.D <= 64    ? items_t<64>(c, sums, grad, far, (__bf16*)dE, st)
+                         : c.D <= 128 ? items_t<128>(c, sums, grad, far, (__bf16*)dE, st)
+                                      : items_t<256>(c, sums, grad, far, (__bf16*)dE, st);
     if (e != hipSuccess) return e;
   }
+  const int pieces = dE ? (items_grid(c.D) - 1) * (int)cdiv((int64_t)sweep_rows(c.D) * c.D, 1024) : 0;
+  const int64_t blocks = pieces + (dH ? cdiv(c.R * c.D, 1024) : 0);
+  if (blocks) k_ce_finish<<<(unsigned)blocks, 256, 0, st>>>(c, sums, far, pieces, grad, (__bf16*)dH, (__bf16*)dE);
   return hipGetLastError();
 }
 

@@ -62,9 +62,10 @@ struct CeHead {
   float weight;  // sum of their weights
 };
 
-// What the forward leaves for the backward, as byte offsets into `saved`; arrays of R entries unless said.
+// What the forward leaves for the backward, as byte offsets into `saved`; arrays of R entries unless said. What a row brings
+// to dz: exp2(c z - shift), or at its target `own` instead; coef = w / W.
 struct CeSaved {
-  size_t head, rows, place, target, lse, rest, coef, hc, dh, bytes;
+  size_t head, rows, place, target, shift, own, coef, hc, dh, bytes;
 };
 struct Ce {
   int64_t R, V;
@@ -81,7 +82,7 @@ bool ce_swept(int D, int dtype);  // whether they take this problem
 size_t ce_rows_bytes(int64_t R, int D, bool grad);
 hipError_t launch_ce_rows(const Ce& c, char* ws, bool grad, const float* zt, float* row_loss, float* each,
                           hipStream_t st);
-size_t ce_items_bytes(int64_t R, int64_t V, int D);
+size_t ce_items_bytes(int D);
 hipError_t launch_ce_items(const Ce& c, char* ws, const float* grad, void* dH, void* dE, hipStream_t st);
 CeSaved ce_saved(int64_t R, int64_t V, int D, int dtype);
 size_t ce_forward_bytes(int64_t R, int64_t V, int D, int dtype, bool want_grad);
