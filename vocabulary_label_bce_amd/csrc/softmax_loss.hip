@@ -733,7 +733,7 @@ template <typename T, bool BIG> Plan plan_of(int64_t R, int64_t V, int D) {
   using S = Sizes<T, BIG>;
   if (R < 1) R = 1;
   Plan p;
-  // A piece's dz takes up to 512 MB. For each piece dH's partial sums are read and written again, and the launches have
+  // A piece's dz takes up to 512 MB, or that of 256 items. For each piece dH's partial sums are read and written again, and the launches have
   // their tails; what is beyond the 256 MB of the memory-side cache comes from memory. Measured, dz + dH + dE of 4,096 x
   // 262,144 x 512 in pieces of 64 MB, 256 MB, 1 GB: 5.6, 4.2, 3.8 ms; of 131,072 x 2,048: 6.7, 6.2, 6.0.
   const int64_t rows = up(R, 32);
