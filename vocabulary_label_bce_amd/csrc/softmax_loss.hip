@@ -104,7 +104,7 @@ __global__ __launch_bounds__(1024) void k_ce_rows(Ce c, const T* __restrict__ H,
 // ---------------------------------------------------------------------------------------------------------
 // Products. A workgroup forms a tile of BM x BN results from stages of KB bytes of features (K of them) of both sides, in
 // a ring of kRing stages in LDS. Turn s multiplies stage s; stage s + 1 has landed by then, so that its first operands are
-// read while the last products of stage s run, and stages s + 2 and s + 3 are on their way. Two waves a SIMD; the order of
+// read while the last products of stage s run, and the stages behind it are on their way. Two waves a SIMD; the order of
 // matrix instructions and reads is pinned, a step's operands being read behind the products of the step before.
 // A side is read by rows (the features next to each other) or transposed (the results' index next to each other).
 // ---------------------------------------------------------------------------------------------------------
@@ -270,16 +270,16 @@ template <typename T_, int WM_, int WN_, int TM_, int TN_, int KB_, bool TA, boo
   // done(s) behind its products.
   template <typename F, typename D> __device__ inline void run(int turns, F before, D done) {
     constexpr int kLoads = A::kLoads + B::kLoads, OPS = TM + TN, MMAS = TM * TN;
-    static_assert(OPS <= MMAS, "");
+    static_assert(OPS <= MMAS && (kRing - 2) * kLoads < 64, "");
     clear();
     wait_and_sync<>();  // (the ring's last readers are done, and what the waits below would count)
 #pragma unroll
-    for (int s = 0; s < 3; ++s) before(s), fetch(s);
-    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(2 * kLoads) : "memory");
+    for (int s = 0; s < kRing - 1; ++s) before(s), fetch(s);
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((kRing - 2) * kLoads) : "memory");
 #pragma unroll
     for (int n = 0; n < OPS; ++n) read(0, n, stage(0), 0);
     for (int s = 0; s < turns; ++s) {
-      asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kLoads) : "memory");
+      asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((kRing - 3) * kLoads) : "memory");
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         const uint32_t at = t + 1 < NT ? stage(s) : stage(s + 1);
@@ -288,7 +288,7 @@ template <typename T_, int WM_, int WN_, int TM_, int TN_, int KB_, bool TA, boo
         for (int m = 0; m < MMAS; ++m) {
           acc[m / TN][m % TN] = Mma<T>::mma(x[t & 1][m / TN], y[t & 1][m % TN], acc[m / TN][m % TN]);
           if (m < OPS) read((t + 1) & 1, m, at, (t + 1) % NT);
-          if (t == 0 && m == 1) before(s + 3), fetch(s + 3);
+          if (t == 0 && m == 1) before(s + kRing - 1), fetch(s + kRing - 1);
           __builtin_amdgcn_sched_barrier(0);
         }
       }
@@ -298,7 +298,7 @@ template <typename T_, int WM_, int WN_, int TM_, int TN_, int KB_, bool TA, boo
   }
 };
 
-template <typename T, bool BIG> struct Sizes {
+template <typename T, bool LARGE> struct Sizes {
   static constexpr int KB = 64;
   using Sums = Product<T, 2, 2, 2, 2, KB, false, false>;
   using Dh = Product<T, 2, 2, 2, 2, KB, false, true>;
@@ -309,10 +309,12 @@ template <> struct Sizes<__bf16, true> {
   using Dh = Product<__bf16, 2, 4, 4, 2, 64, false, true>;
   using De = Product<__bf16, 2, 4, 4, 2, 64, true, true>;
 };
-// Tiles of 256 x 256 are read by half as many workgroups, but leave CUs idle where there are few rows. 65,536 items of
+// Tiles of 256 x 256 are read by half as many workgroups, but leave CUs idle where there are few of them. 65,536 items of
 // 1,024 features, all four products: 200 rows 224 us in large tiles and 212 in small ones, 512 rows 366 and 410; 4,096
-// rows, 131,072 items of 2,048: 8.5 ms and 10.7.
-bool big(int64_t R, int dtype) { return dtype == 1 && R >= 512; }
+// rows, 131,072 items of 2,048: 8.5 ms and 10.7. 4,149 rows, 392 items of 1,000, 34 large tiles: logits 37 us, so 20.
+inline bool large(int64_t R, int64_t V, int dtype) {
+  return dtype == 1 && R >= 512 && cdiv(R, 256) * cdiv(V, 256) >= 256;
+}
 
 // Tile (i, j) of ni x nj for a workgroup: every eighth workgroup, those of one XCD, has tiles next to each other, in
 // blocks eight tiles wide, so that they read the same rows of both sides at about the same time. j is out of range for
@@ -593,9 +595,31 @@ __host__ __device__ inline int parts_of(int64_t tiles, int64_t steps, int grid) 
   return parts < 1 ? 1 : (int)parts;
 }
 // Of dH: by the rows that are counted, which only the device knows (777 rows, 739 of them counted, 65,537 x 256, float32:
-// 275 us by all rows, 432 workgroups on 512 places; so 241).
+// 275 us by all rows, 432 workgroups on 512 places; so 241). Of the numbers of parts that fill one turn of the resident
+// workgroups, two, ... the first is taken that leaves at most 10% of them idle, or the best (296 tiles on 512 places, 4,697
+// rows, 202,265 x 1,000, float32: 25.8 ms in one part, 15.9 in five).
+constexpr int kTurns = 4;
+template <typename P> __host__ __device__ inline int64_t dh_tiles(int64_t n, int D) {
+  return cdiv(n, P::BM) * cdiv(D, P::BN);
+}
+template <typename P> __host__ __device__ inline int64_t dh_most(int64_t width) {  // parts of at least four stages
+  return width / P::K / 4 < 1 ? 1 : width / P::K / 4;
+}
 template <typename P> __host__ __device__ inline int dh_parts(int64_t n, int D, int64_t width) {
-  return parts_of(cdiv(n, P::BM) * cdiv(D, P::BN), width / P::K, kCeGrid<P>);
+  const int grid = kCeGrid<P>;
+  const int64_t all = dh_tiles<P>(n, D), most = dh_most<P>(width);
+  if (all < 1 || all >= kTurns * grid) return 1;
+  const int tiles = (int)all;
+  int best = 1;
+  float good = 0.f;
+  for (int k = 1; k <= kTurns; ++k) {
+    int p = k * grid / tiles;
+    p = p < 1 ? 1 : (p > most ? (int)most : p);
+    const float e = (float)(p * tiles) / (float)((p * tiles + grid - 1) / grid * grid);
+    if (e > good) good = e, best = p;
+    if (e >= 0.9f) break;
+  }
+  return best;
 }
 
 // sums[part][n][D] (+)= dz E over the part's items: rows x features, the first piece of the vocabulary writes.
@@ -729,8 +753,8 @@ struct Plan {
   int de_parts;
   size_t dz, dh, de, bytes;  // offsets in the workspace
 };
-template <typename T, bool BIG> Plan plan_of(int64_t R, int64_t V, int D) {
-  using S = Sizes<T, BIG>;
+template <typename T, bool LARGE> Plan plan_of(int64_t R, int64_t V, int D) {
+  using S = Sizes<T, LARGE>;
   if (R < 1) R = 1;
   Plan p;
   // A piece's dz takes up to 512 MB, or that of 256 items. For each piece dH's partial sums are read and written again, and the launches have
@@ -744,8 +768,9 @@ template <typename T, bool BIG> Plan plan_of(int64_t R, int64_t V, int D) {
   p.de_parts = parts_of(width / S::De::BM * cdiv(D, S::De::BN), cdiv(R, S::De::K), kCeGrid<typename S::De>);
   size_t b = 0;
   p.dz = b, b += up(rows * width * (int64_t)sizeof(T), 256);
-  // dH's parts: one of all rows, or as many tiles as are resident
-  const int64_t few = (int64_t)kCeGrid<typename S::Dh> * S::Dh::BM * (S::Dh::BN < D ? S::Dh::BN : D);
+  // dH's parts: one of all rows, or as many tiles as kTurns turns have
+  int64_t few = (int64_t)kTurns * kCeGrid<typename S::Dh> * S::Dh::BM * (S::Dh::BN < D ? S::Dh::BN : D);
+  if (few > dh_most<typename S::Dh>(width) * R * D) few = dh_most<typename S::Dh>(width) * R * D;
   p.dh = b, b += up((few > R * D ? few : R * D) * 4, 256);
   p.de = b, b += p.de_parts > 1 ? up((int64_t)p.de_parts * width * D * 4, 256) : 0;
   p.bytes = b;
@@ -755,8 +780,8 @@ template <typename T, bool BIG> Plan plan_of(int64_t R, int64_t V, int D) {
 struct ForwardPlan {
   size_t zt, each, part, bytes;
 };
-template <typename T, bool BIG> ForwardPlan forward_plan(int64_t R, int D, bool grad) {
-  using P = typename Sizes<T, BIG>::Sums;
+template <typename T, bool LARGE> ForwardPlan forward_plan(int64_t R, int D, bool grad) {
+  using P = typename Sizes<T, LARGE>::Sums;
   ForwardPlan f;
   size_t b = 0;
   f.zt = b, b += up(R * 4, 256);
@@ -773,11 +798,11 @@ template <typename T, bool BIG> ForwardPlan forward_plan(int64_t R, int D, bool 
   return f;
 }
 
-template <typename T, bool BIG>
+template <typename T, bool LARGE>
 hipError_t forward_t(const Ce& c, int id_bytes, const T* H, const void* targets, const float* weight, bool grad,
                      float* loss, float* row_loss, hipStream_t st) {
-  using P = typename Sizes<T, BIG>::Sums;
-  const ForwardPlan f = forward_plan<T, BIG>(c.R, c.D, grad);
+  using P = typename Sizes<T, LARGE>::Sums;
+  const ForwardPlan f = forward_plan<T, LARGE>(c.R, c.D, grad);
   float *zt = (float*)(c.ws + f.zt), *each = (float*)(c.ws + f.each);
   float2* part = (float2*)(c.ws + f.part);
   const unsigned groups = (unsigned)(c.R < 16 ? 1 : c.R > 8192 ? 512 : cdiv(c.R, 16));
@@ -800,10 +825,10 @@ hipError_t forward_t(const Ce& c, int id_bytes, const T* H, const void* targets,
   return hipGetLastError();
 }
 
-template <typename T, bool BIG>
+template <typename T, bool LARGE>
 hipError_t backward_t(const Ce& c, const float* grad, T* dH, T* dE, hipStream_t st) {
-  using S = Sizes<T, BIG>;
-  const Plan p = plan_of<T, BIG>(c.R, c.V, c.D);
+  using S = Sizes<T, LARGE>;
+  const Plan p = plan_of<T, LARGE>(c.R, c.V, c.D);
   T* dz = (T*)(c.ws + p.dz);
   float *dh = (float*)(c.ws + p.dh), *de = (float*)(c.ws + p.de);
   hipError_t e = allow_lds<k_ce_dz<typename S::Sums>>(S::Sums::kLds);
@@ -816,9 +841,10 @@ hipError_t backward_t(const Ce& c, const float* grad, T* dH, T* dE, hipStream_t 
     if (c.R) k_ce_dz<typename S::Sums><<<(unsigned)(tiles < kCeGrid<typename S::Sums> ? tiles : kCeGrid<typename S::Sums>),
                                          S::Sums::NL, S::Sums::kLds, st>>>(c, v, p.width, dz);
     if (dH && c.R) {
-      const int64_t most = up(cdiv(c.R, S::Dh::BM) * cdiv(c.D, S::Dh::BN), 8);
-      k_ce_dh<typename S::Dh><<<(unsigned)(most > kCeGrid<typename S::Dh> ? most : kCeGrid<typename S::Dh>), S::Dh::NL,
-                                S::Dh::kLds, st>>>(c, v, p.width, v == 0, dz, dh);
+      const int64_t one = dh_tiles<typename S::Dh>(c.R, c.D), turns = kTurns * kCeGrid<typename S::Dh>;
+      int64_t most = one * dh_most<typename S::Dh>(p.width);  // workgroups, for any number of counted rows
+      most = most > turns ? (one > turns ? one : turns) : most;
+      k_ce_dh<typename S::Dh><<<(unsigned)up(most, 8), S::Dh::NL, S::Dh::kLds, st>>>(c, v, p.width, v == 0, dz, dh);
     }
     if (dE) {
       const unsigned tiles = (unsigned)(p.width / S::De::BM * cdiv(c.D, S::De::BN));
@@ -850,31 +876,38 @@ CeSaved ce_saved(int64_t R, int64_t V, int D, int dtype) {
   return s;
 }
 
+// f with the type and the tiles' size of a problem
+template <typename F> auto by_sizes(int64_t R, int64_t V, int dtype, F f) {
+  if (!dtype) return f(0.f, std::false_type{});
+  return large(R, V, dtype) ? f((__bf16)0.f, std::true_type{}) : f((__bf16)0.f, std::false_type{});
+}
+
 size_t ce_forward_bytes(int64_t R, int64_t V, int D, int dtype, bool want_grad) {
-  const size_t own = !dtype            ? forward_plan<float, false>(R, D, want_grad).bytes
-                     : big(R, dtype) ? forward_plan<__bf16, true>(R, D, want_grad).bytes
-                                        : forward_plan<__bf16, false>(R, D, want_grad).bytes;
+  const size_t own = by_sizes(R, V, dtype, [&](auto x, auto wide) {
+    return forward_plan<decltype(x), decltype(wide)::value>(R, D, want_grad).bytes;
+  });
   return own + (want_grad ? 0 : ce_saved(R, V, D, dtype).bytes);
 }
 size_t ce_backward_bytes(int64_t R, int64_t V, int D, int dtype) {
   if (ce_swept(D, dtype)) return ce_items_bytes(D);
-  return !dtype             ? plan_of<float, false>(R, V, D).bytes
-         : big(R, dtype) ? plan_of<__bf16, true>(R, V, D).bytes
-                            : plan_of<__bf16, false>(R, V, D).bytes;
+  return by_sizes(R, V, dtype, [&](auto x, auto wide) {
+    return plan_of<decltype(x), decltype(wide)::value>(R, V, D).bytes;
+  });
 }
 
 hipError_t launch_ce_forward(const Ce& c, int id_bytes, const void* H, const void* targets, const float* weight,
                              bool want_grad, float* loss, float* row_loss, hipStream_t st) {
-  if (!c.dtype) return forward_t<float, false>(c, id_bytes, (const float*)H, targets, weight, want_grad, loss, row_loss, st);
-  return big(c.R, 1)
-             ? forward_t<__bf16, true>(c, id_bytes, (const __bf16*)H, targets, weight, want_grad, loss, row_loss, st)
-             : forward_t<__bf16, false>(c, id_bytes, (const __bf16*)H, targets, weight, want_grad, loss, row_loss, st);
+  return by_sizes(c.R, c.V, c.dtype, [&](auto x, auto wide) {
+    using T = decltype(x);
+    return forward_t<T, decltype(wide)::value>(c, id_bytes, (const T*)H, targets, weight, want_grad, loss, row_loss, st);
+  });
 }
 hipError_t launch_ce_backward(const Ce& c, const float* grad, void* dH, void* dE, hipStream_t st) {
   if (ce_swept(c.D, c.dtype)) return launch_ce_items(c, c.ws, grad, dH, dE, st);
-  if (!c.dtype) return backward_t<float, false>(c, grad, (float*)dH, (float*)dE, st);
-  return big(c.R, 1) ? backward_t<__bf16, true>(c, grad, (__bf16*)dH, (__bf16*)dE, st)
-                          : backward_t<__bf16, false>(c, grad, (__bf16*)dH, (__bf16*)dE, st);
+  return by_sizes(c.R, c.V, c.dtype, [&](auto x, auto wide) {
+    using T = decltype(x);
+    return backward_t<T, decltype(wide)::value>(c, grad, (T*)dH, (T*)dE, st);
+  });
 }
 
 }  // namespace cutbce
