@@ -108,13 +108,15 @@ __global__ __launch_bounds__(1024) void k_ce_rows(Ce c, const T* __restrict__ H,
 // matrix instructions and reads is pinned, a step's operands being read behind the products of the step before.
 // A side is read by rows (the features next to each other) or transposed (the results' index next to each other).
 // ---------------------------------------------------------------------------------------------------------
-// 2 or 4 loads of 16 bytes a lane, as load_lds16 does them one by one: from bytes voff[] of the buffer to LDS bytes dst,
+// 1, 2 or 4 loads of 16 bytes a lane, as load_lds16 does them one by one: from bytes voff[] of the buffer to LDS bytes dst,
 // dst + STEP, ... (+ lane * 16). A stage's loads are what its turn waits for and its scalar work: one block with one wait
 // for its operands (as load_lds16 has), and what does not change from stage to stage formed before (the products of 4,096
 // rows with 32,768 items of 2,048 features took a third longer with the ranges formed for each stage).
 template <int N, int STEP> __device__ inline void load_lds16s(u32x4 buffer, const int* voff, uint32_t dst) {
-  static_assert(N == 2 || N == 4, "");
-  if constexpr (N == 2) {
+  static_assert(N == 1 || N == 2 || N == 4, "");
+  if constexpr (N == 1) {
+    load_lds16(buffer, voff[0], dst);
+  } else if constexpr (N == 2) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %3, 0 offen lds\n\t"
                  "s_add_u32 m0, m0, %4\n\ts_nop 1\n\tbuffer_load_dwordx4 %2, %3, 0 offen lds"
                  :: "s"(uni(dst)), "v"(voff[0]), "v"(voff[1]), "s"(buffer), "n"(STEP) : "m0", "scc");
@@ -235,7 +237,7 @@ template <typename T_, int WM_, int WN_, int TM_, int TN_, int KB_, bool TA, boo
   using B = Side<T, BN, TB, NL, KB>;
   static constexpr int kRing = 4, kStage = A::kBytes + B::kBytes, kLds = kRing * kStage;
   static constexpr int NT = KB / 32;  // steps of a stage
-  static constexpr int kWaves = TM * TN > 8 ? 1 : 2;  // that a SIMD has
+  static constexpr int kWaves = 2;      // that a SIMD has
   static_assert(kLds <= 160 * 1024, "");
   A a;
   B b;
@@ -270,7 +272,7 @@ template <typename T_, int WM_, int WN_, int TM_, int TN_, int KB_, bool TA, boo
   // done(s) behind its products.
   template <typename F, typename D> __device__ inline void run(int turns, F before, D done) {
     constexpr int kLoads = A::kLoads + B::kLoads, OPS = TM + TN, MMAS = TM * TN;
-    static_assert(OPS <= MMAS && (kRing - 2) * kLoads < 64, "");
+    static_assert(OPS <= 2 * MMAS && (kRing - 2) * kLoads < 64, "");
     clear();
     wait_and_sync<>();  // (the ring's last readers are done, and what the waits below would count)
 #pragma unroll
@@ -287,7 +289,8 @@ template <typename T_, int WM_, int WN_, int TM_, int TN_, int KB_, bool TA, boo
 #pragma unroll
         for (int m = 0; m < MMAS; ++m) {
           acc[m / TN][m % TN] = Mma<T>::mma(x[t & 1][m / TN], y[t & 1][m % TN], acc[m / TN][m % TN]);
-          if (m < OPS) read((t + 1) & 1, m, at, (t + 1) % NT);
+#pragma unroll
+          for (int n = m; n < OPS; n += MMAS) read((t + 1) & 1, n, at, (t + 1) % NT);
           if (t == 0 && m == 1) before(s + kRing - 1), fetch(s + kRing - 1);
           __builtin_amdgcn_sched_barrier(0);
         }
@@ -298,22 +301,30 @@ template <typename T_, int WM_, int WN_, int TM_, int TN_, int KB_, bool TA, boo
   }
 };
 
-template <typename T, bool LARGE> struct Sizes {
+enum Tiling { kSmall, kLarge, kNarrow };
+template <typename T, int TILING> struct Sizes {
   static constexpr int KB = 64;
   using Sums = Product<T, 2, 2, 2, 2, KB, false, false>;
   using Dh = Product<T, 2, 2, 2, 2, KB, false, true>;
   using De = Product<T, 2, 2, 2, 2, KB, true, true>;
 };
-template <> struct Sizes<__bf16, true> {
+template <> struct Sizes<__bf16, kLarge> {
   using Sums = Product<__bf16, 2, 4, 4, 2, 64, false, false>;
   using Dh = Product<__bf16, 2, 4, 4, 2, 64, false, true>;
   using De = Product<__bf16, 2, 4, 4, 2, 64, true, true>;
 };
+template <typename T> struct Sizes<T, kNarrow> : Sizes<T, kSmall> {
+  using Sums = Product<T, 4, 1, 1, 2, 64, false, false>;
+  using Dh = Product<T, 1, 4, 2, 1, 64, false, true>;
+};
 // Tiles of 256 x 256 are read by half as many workgroups, but leave CUs idle where there are few of them. 65,536 items of
 // 1,024 features, all four products: 200 rows 224 us in large tiles and 212 in small ones, 512 rows 366 and 410; 4,096
 // rows, 131,072 items of 2,048: 8.5 ms and 10.7. 4,149 rows, 392 items of 1,000, 34 large tiles: logits 37 us, so 20.
-inline bool large(int64_t R, int64_t V, int dtype) {
-  return dtype == 1 && R >= 512 && cdiv(R, 256) * cdiv(V, 256) >= 256;
+// Up to 64 rows tiles are 64 rows wide, where half a small one would be empty (float32, 64 rows,
+// 100,000 x 512: logits 143 us in small tiles and 83, dH 119 and 68; bf16 of 40,000 x 512: 15 and 13, 15 and 12).
+inline Tiling tiling_of(int64_t R, int64_t V, int dtype) {
+  if (R <= 64) return kNarrow;
+  return dtype == 1 && R >= 512 && cdiv(R, 256) * cdiv(V, 256) >= 256 ? kLarge : kSmall;
 }
 
 // Tile (i, j) of ni x nj for a workgroup: every eighth workgroup, those of one XCD, has tiles next to each other, in
@@ -722,22 +733,34 @@ __global__ __launch_bounds__(256) void k_ce_de_join(Ce c, int64_t v0, int64_t wi
   *(V4*)(dE + v0 * c.D + x) = y;
 }
 
-// dH of all rows, zeros for those without a target: four features a lane, the sum of the parts'.
-template <typename P>
+// dH of all rows, zeros for those without a target: four features a lane, the sum of the parts', G lanes each.
+template <typename P, int G>
 __global__ __launch_bounds__(256) void k_ce_dh_join(Ce c, int64_t width, const float* __restrict__ sums,
                                                     const float* __restrict__ grad, typename P::T* __restrict__ dH) {
   using T = typename P::T;
-  const int64_t x = ((int64_t)(blockIdx.y * gridDim.x + blockIdx.x) * 256 + threadIdx.x) * 4;
-  if (x >= c.R * c.D) return;
-  const int64_t r = x / c.D;
-  const int i = at<int32_t>(c.saved, c.at.place)[r];
+  __shared__ f32x4 rest[G > 1 ? 256 : 1];
+  constexpr int N = 256 / G;
+  const int g = threadIdx.x / N;
+  const int64_t x = ((int64_t)(blockIdx.y * gridDim.x + blockIdx.x) * N + threadIdx.x % N) * 4;
+  const bool there = x < c.R * c.D;
+  const int64_t r = there ? x / c.D : 0;
+  const int i = there ? at<int32_t>(c.saved, c.at.place)[r] : -1;
   f32x4 s = {0.f, 0.f, 0.f, 0.f};
   if (i >= 0) {
     const int64_t from = (int64_t)i * c.D + (x - r * c.D);
     const int n = at<CeHead>(c.saved, c.at.head)->n, parts = dh_parts<P>(n, c.D, width);
-    for (int k = 0; k < parts; ++k) s += *(const f32x4*)(sums + (int64_t)k * n * c.D + from);
-    s *= *grad * c.scale;
+#pragma unroll 4
+    for (int k = g; k < parts; k += G) s += *(const f32x4*)(sums + (int64_t)k * n * c.D + from);
   }
+  if constexpr (G > 1) {
+    rest[threadIdx.x] = s;
+    __syncthreads();
+    if (g) return;
+#pragma unroll
+    for (int k = 1; k < G; ++k) s += rest[k * N + threadIdx.x];
+  }
+  if (!there) return;
+  if (i >= 0) s *= *grad * c.scale;
   typedef T V4 __attribute__((ext_vector_type(4)));
   V4 y;
 #pragma unroll
@@ -753,8 +776,8 @@ struct Plan {
   int de_parts;
   size_t dz, dh, de, bytes;  // offsets in the workspace
 };
-template <typename T, bool LARGE> Plan plan_of(int64_t R, int64_t V, int D) {
-  using S = Sizes<T, LARGE>;
+template <typename T, int TILING> Plan plan_of(int64_t R, int64_t V, int D) {
+  using S = Sizes<T, TILING>;
   if (R < 1) R = 1;
   Plan p;
   // A piece's dz takes up to 512 MB, or that of 256 items. For each piece dH's partial sums are read and written again, and the launches have
@@ -780,8 +803,8 @@ template <typename T, bool LARGE> Plan plan_of(int64_t R, int64_t V, int D) {
 struct ForwardPlan {
   size_t zt, each, part, bytes;
 };
-template <typename T, bool LARGE> ForwardPlan forward_plan(int64_t R, int D, bool grad) {
-  using P = typename Sizes<T, LARGE>::Sums;
+template <typename T, int TILING> ForwardPlan forward_plan(int64_t R, int D, bool grad) {
+  using P = typename Sizes<T, TILING>::Sums;
   ForwardPlan f;
   size_t b = 0;
   f.zt = b, b += up(R * 4, 256);
@@ -798,11 +821,11 @@ template <typename T, bool LARGE> ForwardPlan forward_plan(int64_t R, int D, boo
   return f;
 }
 
-template <typename T, bool LARGE>
+template <typename T, int TILING>
 hipError_t forward_t(const Ce& c, int id_bytes, const T* H, const void* targets, const float* weight, bool grad,
                      float* loss, float* row_loss, hipStream_t st) {
-  using P = typename Sizes<T, LARGE>::Sums;
-  const ForwardPlan f = forward_plan<T, LARGE>(c.R, c.D, grad);
+  using P = typename Sizes<T, TILING>::Sums;
+  const ForwardPlan f = forward_plan<T, TILING>(c.R, c.D, grad);
   float *zt = (float*)(c.ws + f.zt), *each = (float*)(c.ws + f.each);
   float2* part = (float2*)(c.ws + f.part);
   const unsigned groups = (unsigned)(c.R < 16 ? 1 : c.R > 8192 ? 512 : cdiv(c.R, 16));
@@ -825,10 +848,10 @@ hipError_t forward_t(const Ce& c, int id_bytes, const T* H, const void* targets,
   return hipGetLastError();
 }
 
-template <typename T, bool LARGE>
+template <typename T, int TILING>
 hipError_t backward_t(const Ce& c, const float* grad, T* dH, T* dE, hipStream_t st) {
-  using S = Sizes<T, LARGE>;
-  const Plan p = plan_of<T, LARGE>(c.R, c.V, c.D);
+  using S = Sizes<T, TILING>;
+  const Plan p = plan_of<T, TILING>(c.R, c.V, c.D);
   T* dz = (T*)(c.ws + p.dz);
   float *dh = (float*)(c.ws + p.dh), *de = (float*)(c.ws + p.de);
   hipError_t e = allow_lds<k_ce_dz<typename S::Sums>>(S::Sums::kLds);
@@ -857,8 +880,15 @@ hipError_t backward_t(const Ce& c, const float* grad, T* dH, T* dE, hipStream_t 
       }
     }
   }
-  const int64_t blocks = cdiv(c.R * c.D, 1024), turns = cdiv(blocks, kMaxGrid);
-  if (dH && c.R) k_ce_dh_join<typename S::Dh><<<dim3((unsigned)cdiv(blocks, turns), (unsigned)turns), 256, 0, st>>>(c, p.width, dh, grad, dH);
+  if (dH && c.R) {
+    // many parts are joined by 16 lanes for each four features (32 rows, 100,000 x 128, float32, 512 parts: 126 us by one
+    // lane, so 6)
+    const bool many = dh_parts<typename S::Dh>(c.R, c.D, p.width) >= 16;
+    const int64_t blocks = cdiv(c.R * c.D, many ? 64 : 1024), turns = cdiv(blocks, kMaxGrid);
+    const dim3 grid((unsigned)cdiv(blocks, turns), (unsigned)turns);
+    if (many) k_ce_dh_join<typename S::Dh, 16><<<grid, 256, 0, st>>>(c, p.width, dh, grad, dH);
+    else k_ce_dh_join<typename S::Dh, 1><<<grid, 256, 0, st>>>(c, p.width, dh, grad, dH);
+  }
   return hipGetLastError();
 }
 
@@ -876,37 +906,41 @@ CeSaved ce_saved(int64_t R, int64_t V, int D, int dtype) {
   return s;
 }
 
-// f with the type and the tiles' size of a problem
+// f with the type and the tiling of a problem
 template <typename F> auto by_sizes(int64_t R, int64_t V, int dtype, F f) {
-  if (!dtype) return f(0.f, std::false_type{});
-  return large(R, V, dtype) ? f((__bf16)0.f, std::true_type{}) : f((__bf16)0.f, std::false_type{});
+  using std::integral_constant;
+  const Tiling tiling = tiling_of(R, V, dtype);
+  if (!dtype) return tiling == kNarrow ? f(0.f, integral_constant<int, kNarrow>{}) : f(0.f, integral_constant<int, kSmall>{});
+  return tiling == kNarrow  ? f((__bf16)0.f, integral_constant<int, kNarrow>{})
+         : tiling == kLarge ? f((__bf16)0.f, integral_constant<int, kLarge>{})
+                            : f((__bf16)0.f, integral_constant<int, kSmall>{});
 }
 
 size_t ce_forward_bytes(int64_t R, int64_t V, int D, int dtype, bool want_grad) {
-  const size_t own = by_sizes(R, V, dtype, [&](auto x, auto wide) {
-    return forward_plan<decltype(x), decltype(wide)::value>(R, D, want_grad).bytes;
+  const size_t own = by_sizes(R, V, dtype, [&](auto x, auto tiling) {
+    return forward_plan<decltype(x), decltype(tiling)::value>(R, D, want_grad).bytes;
   });
   return own + (want_grad ? 0 : ce_saved(R, V, D, dtype).bytes);
 }
 size_t ce_backward_bytes(int64_t R, int64_t V, int D, int dtype) {
   if (ce_swept(D, dtype)) return ce_items_bytes(D);
-  return by_sizes(R, V, dtype, [&](auto x, auto wide) {
-    return plan_of<decltype(x), decltype(wide)::value>(R, V, D).bytes;
+  return by_sizes(R, V, dtype, [&](auto x, auto tiling) {
+    return plan_of<decltype(x), decltype(tiling)::value>(R, V, D).bytes;
   });
 }
 
 hipError_t launch_ce_forward(const Ce& c, int id_bytes, const void* H, const void* targets, const float* weight,
                              bool want_grad, float* loss, float* row_loss, hipStream_t st) {
-  return by_sizes(c.R, c.V, c.dtype, [&](auto x, auto wide) {
+  return by_sizes(c.R, c.V, c.dtype, [&](auto x, auto tiling) {
     using T = decltype(x);
-    return forward_t<T, decltype(wide)::value>(c, id_bytes, (const T*)H, targets, weight, want_grad, loss, row_loss, st);
+    return forward_t<T, decltype(tiling)::value>(c, id_bytes, (const T*)H, targets, weight, want_grad, loss, row_loss, st);
   });
 }
 hipError_t launch_ce_backward(const Ce& c, const float* grad, void* dH, void* dE, hipStream_t st) {
   if (ce_swept(c.D, c.dtype)) return launch_ce_items(c, c.ws, grad, dH, dE, st);
-  return by_sizes(c.R, c.V, c.dtype, [&](auto x, auto wide) {
+  return by_sizes(c.R, c.V, c.dtype, [&](auto x, auto tiling) {
     using T = decltype(x);
-    return backward_t<T, decltype(wide)::value>(c, grad, (T*)dH, (T*)dE, st);
+    return backward_t<T, decltype(tiling)::value>(c, grad, (T*)dH, (T*)dE, st);
   });
 }
 
