@@ -121,3 +121,13 @@ def test_offsets_past_32_bits(V, D):
     want = p @ e
     off = (p.abs() * (UNIT[BF] + chain)) @ e.abs() + 2.0 ** -126 * e.abs().sum(0)
     _close("dH", dH, want, off + UNIT[BF] * (want.abs() + off))
+
+
+@pytest.mark.parametrize("left_out", [0.0, 0.2])
+@pytest.mark.parametrize("R,V,D,dt", [(600, 500, 8192, F), (600, 500, 8192, BF), (2100, 7500, 2000, BF), (700, 70_000, 264, BF),
+                                      (64, 30_000, 272, F), (64, 30_000, 520, BF)])
+def test_long_axes_in_parts(R, V, D, dt, left_out):
+    """Tiles of dH that do not fill whole turns of the chip, or few of them with many parts; how many depends on the rows
+    that are counted."""
+    H, E, t, w = _case(R, V, D, dt, seed=R + D, left_out=left_out)
+    _check(H, E, t, w)
