@@ -305,7 +305,8 @@ cutbce_status cutbce_attention_backward(const cutbce_attention *a, const void *d
  * probabilities are off by 2^-24 |lse| of themselves. A non-finite value in a row of H makes that row's loss, the
  * loss and all of dE non-finite.
  * bf16: products of bf16 values in float32; the logits' gradients are rounded to bf16 as operands of the gradients'
- * products, all sums are float32 and every output is rounded once.
+ * products, a row's own (that of its target) to twice as many bits, all sums are float32 and every output is rounded
+ * once.
  * --------------------------------------------------------------------------------------------------------- */
 
 /* Bytes of `saved`, which the forward leaves for the backward (256-byte aligned): the counted rows' H, statistics and,

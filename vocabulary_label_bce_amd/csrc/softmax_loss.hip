@@ -523,7 +523,8 @@ __global__ __launch_bounds__(1024) void k_ce_loss(Ce c, const float* __restrict_
 // the transposed reads of E give their items.
 // (Rows of the piece's width instead, 64 KB apart: dH of 4,096 x 262,144 x 512 1,740 us, so 1,490.) A workgroup goes
 // through its tiles without a pause in the loads (each tile a workgroup: dz 1,660 us, so 1,490). Storing the values in
-// 16 bits rounds them by at most 2^-8 of themselves, as the product's operands are in any case.
+// 16 bits rounds them by at most 2^-8 of themselves, as the product's operands are in any case; what that cuts off the
+// targets' is added to both products (multiply_rests, k_ce_dh_join).
 template <typename T> constexpr int kBlock = 64 / sizeof(T);
 __host__ __device__ constexpr inline int item_at(int place) {  // of 16 bits
   return (place & ~12) | (place & 4) << 1 | (place & 8) >> 1;
@@ -696,6 +697,27 @@ __global__ __launch_bounds__(P::NL, P::kWaves) void k_ce_de(Ce c, int64_t v0, in
   p.a.start_blocked(dz, u0 / kBlock<T>, up(c.R, 32), x0 * P::K, x1 * P::K < n ? x1 * P::K : n);
   p.b.start(H, d0, c.D, x0 * P::K, x1 * P::K < n ? x1 * P::K : n);
   p.run((int)(x1 - x0), [](int) {}, [](int) {});
+  if constexpr (sizeof(T) == 2) {
+    // what bf16 cut off the dz of this wave's items' own rows
+    constexpr int kWide = P::TN * 32, kEach = kRests<kWide> + kRestList * 4;
+    static_assert(P::WM * P::WN * kEach <= P::kLds && kEach % 256 == 0, "");
+    const int64_t d = d0 + p.wn * kWide, last = x1 * P::K < n ? x1 * P::K : n;
+    const uint32_t own = p.lds0 + p.wave * kEach, list = own + kRests<kWide>;
+    for (int64_t next = d < c.D ? x0 * P::K : last; next < last;) {
+      const int rests = list_rests(c, next, last, list, p.lane, [&](int t) {
+        const int64_t place = t - (v0 + u0 + p.wm * P::TM * 32);
+        return place >= 0 && place < P::TM * 32 ? (int)place : -1;
+      });
+      if (rests)
+        multiply_rests<kWide, P::TM, 1>(
+            c, H + d, (int)clamp64(c.D - d, 0, kWide), list, rests, item_at(p.lane % 32), own, p.lane,
+            [&](int j, bf16x8 features, const u32x4* items) {
+#pragma unroll
+              for (int i = 0; i < P::TM; ++i)
+                p.acc[i][j] = Mma<T>::mma(items[i], __builtin_bit_cast(u32x4, features), p.acc[i][j]);
+            });
+    }
+  }
   const float f = PART ? 1.f : *grad * fabsf(c.scale);
   const int h = p.lane / 32;
 #pragma unroll
@@ -751,6 +773,15 @@ __global__ __launch_bounds__(256) void k_ce_dh_join(Ce c, int64_t width, const f
     const int n = at<CeHead>(c.saved, c.at.head)->n, parts = dh_parts<P>(n, c.D, width);
 #pragma unroll 4
     for (int k = g; k < parts; k += G) s += *(const f32x4*)(sums + (int64_t)k * n * c.D + from);
+    if constexpr (sizeof(T) == 2) {
+      if (g == 0) {  // what bf16 cut off the target's dz (multiply_rests has it for dE)
+        const float own = at<float>(c.saved, c.at.own)[i], rest = own - (float)(__bf16)own;
+        const int64_t target = at<int32_t>(c.saved, c.at.target)[i];
+        const bf16x4 item = *(const bf16x4*)((const __bf16*)c.E + target * c.D + (x - r * c.D));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[j] += rest * (float)item[j];
+      }
+    }
   }
   if constexpr (G > 1) {
     rest[threadIdx.x] = s;

@@ -107,10 +107,10 @@ template <int DP, bool AUX, bool GRAD> struct Sweep {
                  :: "s"(uni(dst)), "v"(ld.offset(q, D)), "v"(ld.offset(q + 1, D)), "v"(ld.offset(q + 2, D)),
                     "v"(ld.offset(q + 3, D)), "s"(range) : "m0", "scc");
   }
-  __device__ inline void load_owned(const __bf16* base, int64_t first, int64_t n) {
+  template <int STEP> __device__ inline void load_owned(const __bf16* base, int64_t first, int64_t n) {
 #pragma unroll
     for (int b = 0; b < kNB; ++b) {
-      const int64_t i = first + b * 32 + lane % 32;
+      const int64_t i = first + (b * 32 + lane % 32) * STEP;
       load_own<__bf16, DP>(own[b], base + i * D, i < n, D, lane);
     }
   }
@@ -275,7 +275,7 @@ __global__ __launch_bounds__(256, (kWaves<DP, false>)) void k_ce_sweep_rows(Ce c
     const int count = part_of.count;
     const int64_t own0 = (int64_t)tile * S::kOwned + s.wave * (S::kNB * 32);
     wait_and_sync<>();  // (the ring's last readers are done, and stores, which the waits below would count)
-    s.load_owned(at<__bf16>(c.saved, c.at.hc), own0, n);
+    s.template load_owned<1>(at<__bf16>(c.saved, c.at.hc), own0, n);
     int target[S::kNB];
     float ref[S::kNB], sum[S::kNB];
 #pragma unroll
@@ -532,7 +532,7 @@ __global__ __launch_bounds__(256) void k_ce_sweep_join(Ce c, const float2* __res
 // are pieces of tiles that it shares with its neighbours. A piece's sums go to place 0 of its workgroup's two if it
 // begins where the part does, else to 1, and are joined by k_ce_finish. (With whole tiles alone 391 tiles of 100,000
 // items on 256 CUs would take the time of 512.)
-constexpr int kLeast = 4;
+constexpr int kLeast = 4, kListBytes = 16 + kRestList * 4;
 struct Line {
   int64_t stages, total;  // of a tile, and of all
   int parts;
@@ -567,9 +567,12 @@ __global__ __launch_bounds__(256, (kWaves<DP, true>)) void k_ce_sweep_items(Ce c
     const bool whole = count == line.stages;
     const int place = x == from ? 0 : 1;
     x += count;
-    const int64_t own0 = tile * S::kOwned + s.wave * (S::kNB * 32);
+    // The tile's items are dealt to the four waves one by one: neighbours, often targets together, go to different ones
+    // (5,120 rows, 100,000 x 64, targets by popularity: 64 neighbours a wave 200 us, so 178).
+    const int64_t own0 = tile * S::kOwned + s.wave;
+    constexpr int kPlaces = (S::kOwned / 4 - 1) * 4;  // bits of an item that say which one of a wave's it is
     wait_and_sync<>();  // (the ring's last readers are done, and stores, which the waits below would count)
-    s.load_owned((const __bf16*)c.E, own0, c.V);
+    s.template load_owned<4>((const __bf16*)c.E, own0, c.V);
     s.clear();
     auto fetch = [&](int k) INLINED {
       const int64_t row = (int64_t)(s0 + k) * kSweepStage;
@@ -587,6 +590,10 @@ __global__ __launch_bounds__(256, (kWaves<DP, true>)) void k_ce_sweep_items(Ce c
       s.first(0);
       s.read_rows(s.slot(0) + 32 * S::kRow);
     }
+    // The wave's list of rows whose target it has: the row from which on it was full, the entries; and their number,
+    // with 2 kRestList added when it is full.
+    const uint32_t list = s.lds0 + S::kLds + s.wave * kListBytes;
+    int listed = 0;
     f32x4 sh[4];
     // the shifts of a step (four at a time, as the ones before are done with) and, a row a lane, its targets
     auto shifts_at = [&](uint32_t at) INLINED {
@@ -641,11 +648,21 @@ __global__ __launch_bounds__(256, (kWaves<DP, true>)) void k_ce_sweep_items(Ce c
       }
       // a row whose target is among the wave's items (behind the last row all that is loaded is 0: a row of zeros, whose
       // product is 0 whatever P is)
-      if (__builtin_expect(__any((unsigned)(t - (int)own0) < (unsigned)(S::kNB * 32)), 0)) {
+      if (__builtin_expect(__any((t & ~kPlaces) == (int)own0), 0)) {
         uint32_t at = ax + 16 * s.h;
         asm volatile("" : "+v"(at));  // (one address and constants, not an address each)
         typedef int s32x4 __attribute__((ext_vector_type(4)));
-        const int item = (int)own0 + s.lane % 32;
+        const int item = (int)own0 + s.lane % 32 * 4, row = (s0 + k) * kSweepStage + Q * 32 + s.lane;
+        const uint32_t hits = (uint32_t)__ballot(row < n && (t & ~kPlaces) == (int)own0);  // (both halves' are alike)
+        if (listed <= kRestList - 32) {
+          if (s.lane < 32 && (hits >> s.lane & 1))
+            *(CUTBCE_LDS uint32_t*)(size_t)(list + 16 + __builtin_amdgcn_mbcnt_lo(hits, listed) * 4) =
+                (uint32_t)row * 128 + (uint32_t)(t & kPlaces) / 4;
+          listed = uni(listed + __popc(hits));
+        } else if (listed <= kRestList) {
+          *(CUTBCE_LDS int*)(size_t)list = row - s.lane;
+          listed = uni(listed + 2 * kRestList);
+        }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const s32x4 tr = *(CUTBCE_LDS const s32x4*)(size_t)(at + 256 + 32 * k);
@@ -656,8 +673,8 @@ __global__ __launch_bounds__(256, (kWaves<DP, true>)) void k_ce_sweep_items(Ce c
 #pragma unroll
             for (int b = 0; b < S::kNB; ++b) {
               uint32_t& p = s.p[Q][b][2 * k + j];
-              p = tr[2 * j] == item + b * 32 ? (p & 0xffff0000u) | (both & 0xffffu) : p;
-              p = tr[2 * j + 1] == item + b * 32 ? (p & 0xffffu) | (both & 0xffff0000u) : p;
+              p = tr[2 * j] == item + b * 128 ? (p & 0xffff0000u) | (both & 0xffffu) : p;
+              p = tr[2 * j + 1] == item + b * 128 ? (p & 0xffffu) | (both & 0xffff0000u) : p;
             }
           }
         }
@@ -674,10 +691,32 @@ __global__ __launch_bounds__(256, (kWaves<DP, true>)) void k_ce_sweep_items(Ce c
     }
     if constexpr (!S::kPlain) s.last(1);
     wait_and_sync<>();
+    {
+      static_assert(4 * kRests<DP> <= S::kLds, "");
+      int lane = s.lane;
+      asm volatile("" : "+v"(lane));  // (addresses are formed here, not kept through the loops above)
+      int64_t last = (int64_t)(s0 + count) * kSweepStage, next;
+      last = last < n ? last : n;
+      next = listed > kRestList ? uni(*(CUTBCE_LDS const int*)(size_t)list) : last;
+      for (int rests = listed > kRestList ? listed - 2 * kRestList : listed;;) {
+        if (rests)
+          multiply_rests<DP, S::kNB, DP <= 128 ? 2 : 1>(
+              c, s.X, c.D, list + 16, rests, lane % 32, s.lds0 + s.wave * kRests<DP>, lane,
+              [&](int d, bf16x8 features, const u32x4* items) INLINED {
+                s.settle();
+#pragma unroll
+                for (int b = 0; b < S::kNB; ++b)
+                  s.acc[d][b] = S::M::mma(__builtin_bit_cast(u32x4, features), items[b], s.acc[d][b]);
+              });
+        if (next >= last) break;
+        rests = list_rests(c, next, last, list + 16, lane,
+                           [&](int t) { return (t & ~kPlaces) == (int)own0 ? (t & kPlaces) / 4 : -1; });
+      }
+    }
     const float f = whole ? *grad * fabsf(c.scale) : 1.f;
 #pragma unroll
     for (int b = 0; b < S::kNB; ++b) {
-      const int at = s.wave * (S::kNB * 32) + b * 32 + s.lane % 32;
+      const int at = (b * 32 + s.lane % 32) * 4 + s.wave;
       const int64_t v = tile * S::kOwned + at;
       if (v >= c.V) continue;
       f32x16 o[S::NDB];
@@ -789,10 +828,11 @@ template <int DP, bool GRAD> hipError_t rows_t(const Ce& c, char* ws, const floa
 }
 
 template <int DP> hipError_t items_t(const Ce& c, float* sums, const float* grad, int64_t far, __bf16* dE, hipStream_t st) {
-  using S = Sweep<DP, true, true>;
-  const hipError_t e = allow_lds<k_ce_sweep_items<DP>>(S::kLds);
+  constexpr int kLds = Sweep<DP, true, true>::kLds + 4 * kListBytes;
+  static_assert(kLds * kWaves<DP, true> <= 160 * 1024, "");
+  const hipError_t e = allow_lds<k_ce_sweep_items<DP>>(kLds);
   if (e != hipSuccess) return e;
-  k_ce_sweep_items<DP><<<items_grid(c.D), 256, S::kLds, st>>>(c, grad, far, dE, sums);
+  k_ce_sweep_items<DP><<<items_grid(c.D), 256, kLds, st>>>(c, grad, far, dE, sums);
   return hipGetLastError();
 }
 
