@@ -301,9 +301,10 @@ cutbce_status cutbce_attention_backward(const cutbce_attention *a, const void *d
  *   loss = sum w_r l_r / W;  dz_rv = w_r / W * (softmax(z_r)_v - [v = t]);  dH = g scale dz E;  dE = g scale dz^T H.
  *   W = 0 gives loss 0 and zero gradients.
  * H [rows][dim], E [vocab][dim], dH, dE: dense, 16-byte aligned, of one dtype. 0 <= rows <= 2^20,
- * 1 <= vocab <= 2^31 - 1025, dim a multiple of 8 up to 16384. Logits up to float32's largest value are taken; the
- * probabilities are off by 2^-24 |lse| of themselves. A non-finite value in a row of H makes that row's loss, the
- * loss and all of dE non-finite.
+ * 1 <= vocab <= 2^31 - 1025, dim a multiple of 8 up to 16384. Logits up to 1e9 are taken: beyond, a row's loss is right
+ * or not finite. The probabilities are off by 2^-24 |lse / log 2| of themselves; where that would be all of them (lse from
+ * 1.1e7 on, a row of weight 0 excepted) dE is not a number, nor is the row's dH unless it comes with the sums (bf16, dim
+ * <= 256). A non-finite value in a row of H makes that row's loss, the loss and all of dE non-finite.
  * bf16: products of bf16 values in float32; the logits' gradients are rounded to bf16 as operands of the gradients'
  * products, a row's own (that of its target) to twice as many bits, all sums are float32 and every output is rounded
  * once.

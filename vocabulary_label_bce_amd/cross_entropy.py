@@ -99,7 +99,10 @@ def cut_cross_entropy(H, E, targets, row_weight=None, scale: float = 1.0):
     H [R, D] and E [V, D] (float32 or bfloat16, D a multiple of 8 up to 16384), targets [R] int32 or int64: a row whose
     target is outside [0, V) (padding, e.g. -1) is left out of the loss and gets no gradient. row_weight [R] (finite,
     >= 0): the loss becomes the average weighted by it. scale: 1 / temperature. Returns a 0-d float32; gradients flow to
-    H and E (not to the weights). No tensor of R x V elements is kept: memory is bounded in V."""
+    H and E (not to the weights). No tensor of R x V elements is kept: memory is bounded in V.
+
+    Logits up to 1e9 are taken; a row with one beyond has the right loss or one that is not finite. The probabilities that
+    gradients are made of are off by 2^-24 |logsumexp / log 2|, and not a number where that is 1 (from 1.1e7 on)."""
     if row_weight is not None and row_weight.requires_grad and torch.is_grad_enabled():
         raise ValueError("row_weight gets no gradient: detach it")
     if _derived(H, E):

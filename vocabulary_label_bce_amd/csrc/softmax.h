@@ -45,16 +45,25 @@ __device__ inline Share share_at(int steps, int shares, int share) {
   return {share * each + (share < more ? share : more), each + (share < more ? 1 : 0)};
 }
 
-// Joining a row's shares, (reference, sum of exponentials): the largest reference of a share in which something counts
-// (one in which nothing does has the sum 0, whatever its reference), a share's factor, and what is kept of a row.
+// Joining a row's shares, (reference, sum of exponentials): the largest reference of a share in which something counts,
+// a share's factor, and what is kept of a row. A share in which nothing counts has the sum 0 and the reference 0 or
+// -inf. Another one has lost its largest exponential, which is 1 but for the reference's rounding: exponents are formed
+// by one multiply-add, so that a reference from 2^31 on may be off by 64 and more, and beyond float32 it is infinite.
+// Such a share, left out, would leave a loss that looks like one; it makes its row not a number.
+__device__ inline bool lost(float2 share) { return share.y == 0.f && share.x != 0.f && share.x != -INFINITY; }
 __device__ inline float top_of(float m, float2 share) { return share.y == 0.f ? m : fmaxf(m, share.x); }
-__device__ inline float share_of(float2 share, float m) { return share.y == 0.f ? 0.f : exp2_of(share.x - m); }
+__device__ inline float share_of(float2 share, float m) {
+  return lost(share) ? NAN : share.y == 0.f ? 0.f : exp2_of(share.x - m);
+}
+// Probabilities are exponents less `shift`, off by 2^-24 of it: from 2^24 on they would have lost their last bit, and are
+// not a number (a row of weight 0 has the shift inf, which makes them 0).
 __device__ inline void finish_row(const Ce& c, int i, int64_t r, float z, float m, float others, float* row_loss,
                                   float* each) {
   const float mine = exp2_of(z - m), sum = others + mine;
   const float l = mine == 1.f ? log1pf(others) : (m - z) * kLn2 + logf(sum);
   const float coef = at<float>(c.saved, c.at.coef)[i];
-  at<float>(c.saved, c.at.shift)[i] = m + log2f(sum) - log2f(coef);
+  const float shift = m + log2f(sum) - log2f(coef);
+  at<float>(c.saved, c.at.shift)[i] = coef > 0.f && !(fabsf(shift) < 0x1p24f) ? NAN : shift;
   at<float>(c.saved, c.at.own)[i] = -coef * (others / sum);
   each[i] = l;
   if (row_loss) row_loss[r] = l;
