@@ -190,18 +190,22 @@ class AdamW:
                                               "exp_avg_sq_scales", "masters")}
 
     def load_state_dict(self, state):
-        """Copies a state_dict's values into this optimizer's tensors."""
-        with torch.no_grad():
-            for n, mine in self.state_dict().items():
-                given = state[n]
-                _need((mine is None) == (given is None), f"{n}: one state has it and the other has not")
-                if mine is None:
+        """Copies a state_dict's values into this optimizer's tensors. A state that is refused changes none of them."""
+        copies = []
+        for n, mine in self.state_dict().items():
+            given = state[n]
+            _need((mine is None) == (given is None), f"{n}: one state has it and the other has not")
+            if mine is None:
+                continue
+            if isinstance(mine, torch.Tensor):
+                mine, given = [mine], [given]
+            _need(len(mine) == len(given), f"{n}: another number of tensors")
+            for a, b in zip(mine, given):
+                if a is None and b is None:
                     continue
-                pairs = [(mine, given)] if isinstance(mine, torch.Tensor) else list(zip(mine, given))
-                _need(isinstance(mine, torch.Tensor) or len(mine) == len(given), f"{n}: another number of tensors")
-                for a, b in pairs:
-                    if a is None and b is None:
-                        continue
-                    _need(a is not None and b is not None and a.shape == b.shape and a.dtype == b.dtype,
-                          f"{n}: another shape or type")
-                    a.copy_(b)
+                _need(a is not None and b is not None and a.shape == b.shape and a.dtype == b.dtype,
+                      f"{n}: another shape or type")
+                copies.append((a, b))
+        with torch.no_grad():
+            for a, b in copies:
+                a.copy_(b)
