@@ -103,8 +103,8 @@ def cut_cross_entropy(H, E, targets, row_weight=None, scale: float = 1.0):
 
     Logits up to 1e9 are taken; a row with one beyond has the right loss or one that is not finite. The probabilities that
     gradients are made of are off by 2^-24 |logsumexp / log 2|, and not a number where that is 1 (from 1.1e7 on)."""
-    if row_weight is not None and row_weight.requires_grad and torch.is_grad_enabled():
-        raise ValueError("row_weight gets no gradient: detach it")
+    if _derived(row_weight):
+        raise ValueError("row_weight gets no gradient and no tangent: detach it")
     if _derived(H, E):
         return _CutCrossEntropy.apply(H, E, targets, row_weight, scale)
     return cross_entropy_forward(H, E, targets, row_weight, scale, want_grad=False)[0]
