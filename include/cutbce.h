@@ -301,17 +301,17 @@ cutbce_status cutbce_attention_backward(const cutbce_attention *a, const void *d
  *   loss = sum w_r l_r / W;  dz_rv = w_r / W * (softmax(z_r)_v - [v = t]);  dH = g scale dz E;  dE = g scale dz^T H.
  *   W = 0 gives loss 0 and zero gradients.
  * H [rows][dim], E [vocab][dim], dH, dE: dense, 16-byte aligned, of one dtype. 0 <= rows <= 2^20,
- * 1 <= vocab <= 2^31 - 1025, dim a multiple of 8 up to 16384. Logits up to 1e9 are taken: beyond, a row's loss is right
- * or not finite. The probabilities are off by 2^-24 |lse / log 2| of themselves; where that would be all of them (lse from
- * 1.1e7 on, a row of weight 0 excepted) dE is not a number, nor is the row's dH unless it comes with the sums (bf16, dim
- * <= 256). A non-finite value in a row of H makes that row's loss, the loss and all of dE non-finite.
+ * 1 <= vocab <= 2^31 - 1025, dim a multiple of 8 up to 16384. Logits up to 1e9 are taken: beyond, a row's loss is
+ * right or not finite. The probabilities are off by 2^-24 |lse / log 2| of themselves; where that would be all of them
+ * (lse from 1.1e7 on, a row of weight 0 excepted) dE is not a number, nor is the row's dH unless it comes with the sums
+ * (bf16, dim <= 256). A non-finite value in a row of H makes that row's loss, the loss and all of dE non-finite.
  * bf16: products of bf16 values in float32; the logits' gradients are rounded to bf16 as operands of the gradients'
  * products, a row's own (that of its target) to twice as many bits, all sums are float32 and every output is rounded
  * once.
  * --------------------------------------------------------------------------------------------------------- */
 
 /* Bytes of `saved`, which the forward leaves for the backward (256-byte aligned): the counted rows' H, statistics and,
- * for dtype bf16 and dim <= 256, their dH. */
+ * for dtype bf16 and dim <= 256, their dH, which is formed with the sums whatever the backward will be asked for. */
 cutbce_status cutbce_cross_entropy_saved_size(int64_t rows, int64_t vocab, int32_t dim, int32_t dtype, size_t *bytes);
 
 /* Bytes of workspace: which = 0 the forward without `saved`, 1 with it, 2 the backward. Bounded in vocab: the gradients
@@ -386,7 +386,8 @@ typedef struct {
  * param rounded to its type once. States of 8 bits hold m and sqrt(v): element j stands for e4m3 code * scale of block
  * j / 256, the scale being the block's largest magnitude / 448; the new ones are rounded up or down at random with the
  * probabilities that make the mean right (a positive sqrt(v) never to 0), by numbers that follow from seed, t, the
- * tensor's place in the list and j. Steps are counted on the device: a captured step that is replayed advances. */
+ * tensor's place in the list and j; a value that is not finite makes its block's states so. Steps are counted on the
+ * device: a captured step that is replayed advances. */
 cutbce_status cutbce_adamw_step(const cutbce_adamw_tensors *tensors, const cutbce_adamw *how, void *stream);
 
 /* Opt-in kernel timing for benchmarks (host calls). While enabled, every launch of the logit-tile sweeps

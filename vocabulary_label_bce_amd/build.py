@@ -15,7 +15,8 @@ CSRC = os.path.join(PKG, "csrc")
 OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libcutbce.so")
 SOURCES = ["prep.hip", "sweep.hip", "finish.hip", "api.hip", "ceiling.hip", "embedding.hip", "layernorm.hip",
-           "attention.hip", "encoder_api.hip", "softmax_loss.hip", "softmax_sweep.hip", "optimizer.hip", "training_api.hip"]
+           "attention.hip", "encoder_api.hip", "softmax_loss.hip", "softmax_sweep.hip", "optimizer.hip",
+           "training_api.hip"]
 ARCH = os.environ.get("CUTBCE_ARCH", "gfx950")
 
 # Packed-fp32 VALU instructions are disabled for all device code (plain float code is used instead).

@@ -1,7 +1,7 @@
 """PyTorch front end of the softmax cross entropy over a whole vocabulary: ``cut_cross_entropy`` is differentiable in
-reverse mode; ``cross_entropy_forward`` and ``cross_entropy_backward`` serve callers that keep their own tape. The logits
-are never kept. The arithmetic is libcutbce.so's; all tensors live on the current GPU and nothing synchronises with the
-host.
+reverse mode; ``cross_entropy_forward`` and ``cross_entropy_backward`` serve callers that keep their own tape. The
+logits are never kept. The arithmetic is libcutbce.so's; all tensors live on the current GPU and nothing synchronises
+with the host.
 """
 from __future__ import annotations
 
@@ -44,8 +44,9 @@ def _checked(H, E, targets, row_weight, scale):
 
 
 def cross_entropy_forward(H, E, targets, row_weight=None, scale: float = 1.0, want_grad: bool = True):
-    """(loss, row_loss, saved) of cut_cross_entropy: loss float32 0-d; row_loss float32 [R], each row's own loss, 0 where
-    it is left out; saved for cross_entropy_backward, None with want_grad=False."""
+    """(loss, row_loss, saved) of cut_cross_entropy: loss float32 0-d; row_loss float32 [R], each row's own loss, 0
+    where it is left out; saved for cross_entropy_backward, None with want_grad=False. For bfloat16 and D up to 256
+    saved has dH (R * D float32, half of the forward's products), also where the backward will be asked for dE alone."""
     dev, H, E, targets, row_weight = _checked(H, E, targets, row_weight, scale)
     R, (V, D) = H.shape[0], E.shape
     saved_bytes, alone, beside, _ = B.cross_entropy_sizes(R, V, D, H.dtype)
@@ -58,8 +59,8 @@ def cross_entropy_forward(H, E, targets, row_weight=None, scale: float = 1.0, wa
 
 
 def cross_entropy_backward(grad, H, E, saved, want_dH: bool = True, want_dE: bool = True):
-    """(dH, dE) from the cotangent of the loss (one element on the device), the forward's H and E and what it saved (of H
-    the shape alone is looked at: its counted rows are in saved). What is not wanted is None."""
+    """(dH, dE) from the cotangent of the loss (one element on the device), the forward's H and E and what it saved (of
+    H the shape and type alone are looked at: its counted rows are in saved). What is not wanted is None."""
     dev = _on_gpu("cross_entropy_backward", E, H, grad, saved.buffer)
     R, V, D, dt = saved.rows, saved.vocab, saved.dim, saved.dtype
     if H.shape != (R, D) or E.shape != (V, D) or H.dtype != dt or E.dtype != dt:
@@ -101,8 +102,9 @@ def cut_cross_entropy(H, E, targets, row_weight=None, scale: float = 1.0):
     >= 0): the loss becomes the average weighted by it. scale: 1 / temperature. Returns a 0-d float32; gradients flow to
     H and E (not to the weights). No tensor of R x V elements is kept: memory is bounded in V.
 
-    Logits up to 1e9 are taken; a row with one beyond has the right loss or one that is not finite. The probabilities that
-    gradients are made of are off by 2^-24 |logsumexp / log 2|, and not a number where that is 1 (from 1.1e7 on)."""
+    Logits up to 1e9 are taken; a row with one beyond has the right loss or one that is not finite. The probabilities
+    that gradients are made of are off by 2^-24 |logsumexp / log 2|, and not a number where that is 1 (from 1.1e7 on).
+    """
     if _derived(row_weight):
         raise ValueError("row_weight gets no gradient and no tangent: detach it")
     if _derived(H, E):

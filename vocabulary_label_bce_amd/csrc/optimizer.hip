@@ -109,12 +109,14 @@ __device__ inline void store_codes(void* base, int64_t at, int n, const Codes& c
 __device__ inline void decode(const Codes& c, float scale, float* x) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.w[i], false), hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.w[i], true);
+    const f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.w[i], false);
+    const f32x2 hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.w[i], true);
     x[4 * i] = lo[0] * scale, x[4 * i + 1] = lo[1] * scale, x[4 * i + 2] = hi[0] * scale, x[4 * i + 3] = hi[1] * scale;
   }
 }
 
-// 32 bits that look random from a number: multiplications and shifts, each of which can be undone.
+// 32 bits that look random from a number: the published finalizer of the hash MurmurHash3, two multiplications and
+// three shifts, each of which can be undone.
 __device__ inline uint32_t hash32(uint32_t x) {
   x = (x ^ (x >> 16)) * 0x85EBCA6Bu;
   x = (x ^ (x >> 13)) * 0xC2B2AE35u;
@@ -125,7 +127,8 @@ __device__ inline uint32_t hash32(uint32_t x) {
 // stays NaN. `least`: the smallest code of a y that is not 0.
 __device__ inline uint32_t encode(float y, uint32_t random, uint32_t least) {
   const uint32_t bits = __float_as_uint(y), a = bits & 0x7fffffffu;
-  const uint32_t small = (uint32_t)(__uint_as_float(a) * 512.f + (float)random * 0x1p-16f);  // below 2^-6: steps of 2^-9
+  // (below 2^-6: steps of 2^-9)
+  const uint32_t small = (uint32_t)(__uint_as_float(a) * 512.f + (float)random * 0x1p-16f);
   const uint32_t large = ((a + (random << 4)) >> 20) - (120u << 3);
   uint32_t c = a < 0x3c800000u ? small : large;
   c = c > 0x7eu ? 0x7eu : c;
@@ -156,7 +159,8 @@ __device__ inline Codes hold(const float* x, const uint32_t* random, int shift, 
   }
   const float top = __uint_as_float(row_top(t));
   *scale = top * (1.f / 448.f);
-  const float f = top > 1e-35f ? 1.f / top * 448.f : (top <= 1e-35f ? 0.f : top);  // (what is smaller is held as 0; NaN stays)
+  // (what is smaller is held as 0; NaN stays)
+  const float f = top > 1e-35f ? 1.f / top * 448.f : (top <= 1e-35f ? 0.f : top);
   Codes c = {};
 #pragma unroll
   for (int i = 0; i < 16; ++i) c.w[i / 4] |= encode(x[i] * f, (random[i] >> shift) & 0xffffu, least) << (8 * (i % 4));

@@ -16,11 +16,14 @@ __device__ inline float base2(float scale) {
   return c > 0.f ? c : 1.f;
 }
 
-// Units of work of the sweep over the vocabulary: tiles of sweep_rows(D) rows x shares of its stages of kSweepStage items. The
-// resident workgroups (one a CU, two of narrow rows) take units in turn, kSweepUnits at most: of the numbers of shares
-// that make one unit each, two, ... the first is taken that leaves at most 4% of them idle in the last turn, or the best.
+// Units of work of the sweep over the vocabulary: tiles of sweep_rows(D) rows x shares of its stages of kSweepStage
+// items. The resident workgroups (one a CU, two of narrow rows) take units in turn, kSweepUnits at most: of the
+// numbers of shares that make one unit each, two, ... the first is taken that leaves at most 4% of them idle in the
+// last turn, or the best.
 constexpr int kSweepStage = 64, kSweepUnits = 1024;
-__host__ __device__ constexpr inline int sweep_stages(int64_t V) { return (int)(((uint32_t)V + kSweepStage - 1) / kSweepStage); }
+__host__ __device__ constexpr inline int sweep_stages(int64_t V) {
+  return (int)(((uint32_t)V + kSweepStage - 1) / kSweepStage);
+}
 __host__ __device__ constexpr inline int sweep_rows(int D) { return D <= 128 ? 256 : 128; }
 __host__ __device__ constexpr inline int sweep_grid(int D) { return D <= 64 ? 512 : 256; }
 __host__ __device__ inline int sweep_shares(int tiles, int stages, int grid) {  // (32 bits: these are quotients)
@@ -55,8 +58,8 @@ __device__ inline float top_of(float m, float2 share) { return share.y == 0.f ? 
 __device__ inline float share_of(float2 share, float m) {
   return lost(share) ? NAN : share.y == 0.f ? 0.f : exp2_of(share.x - m);
 }
-// Probabilities are exponents less `shift`, off by 2^-24 of it: from 2^24 on they would have lost their last bit, and are
-// not a number (a row of weight 0 has the shift inf, which makes them 0).
+// Probabilities are exponents less `shift`, off by 2^-24 of it: from 2^24 on they would have lost their last bit, and
+// are not a number (a row of weight 0 has the shift inf, which makes them 0).
 __device__ inline void finish_row(const Ce& c, int i, int64_t r, float z, float m, float others, float* row_loss,
                                   float* each) {
   const float mine = exp2_of(z - m), sum = others + mine;
@@ -70,11 +73,12 @@ __device__ inline void finish_row(const Ce& c, int i, int64_t r, float z, float 
 }
 
 // What bf16 cuts off a row's own dz, that of its target and by far its largest: the products take the value rounded,
-// and the rest is multiplied afterwards, so that dE of the targets is off by its own rounding and little else (gradients
-// of 4,096 rows, 128,000 x 2,048: off by 0.24% of their norm without, 0.17% with, as with a dz in float32). A wave has
-// the sums of NI blocks of 32 items and a list in LDS of the rows whose target is one of them: row * 128 + the place of
-// the item. What it costs where targets follow their popularity, and few waves have many rows: the sweep of 5,120 rows, 100,000 x
-// 64 163 -> 183 us, of 14,336, 876,000 x 128 5,192 -> 5,243; dE of 64,000 x 2,048 942 -> 994.
+// and the rest is multiplied afterwards, so that dE of the targets is off by its own rounding and little else
+// (gradients of 4,096 rows, 128,000 x 2,048: off by 0.24% of their norm without, 0.17% with, as with a dz in
+// float32). A wave has the sums of NI blocks of 32 items and a list in LDS of the rows whose target is one of them:
+// row * 128 + the place of the item. What it costs where targets follow their popularity, and few waves have many
+// rows: the sweep of 5,120 rows, 100,000 x 64 163 -> 183 us, of 14,336, 876,000 x 128 5,192 -> 5,243; dE of 64,000 x
+// 2,048 942 -> 994.
 constexpr int kRestList = 1536;
 template <int DP> constexpr int kRestRows = DP <= 128 ? 64 : 32;  // that are multiplied at a time
 template <int DP> constexpr int kRests = kRestRows<DP> * Tile<__bf16, DP>::kRowB + 512;  // bytes of LDS that takes

@@ -8,12 +8,13 @@
 // sums and products and joined in at the end: 1 - p_t is the others' share of the sum, and is exact to rounding where
 // p_t is near 1, as a row's loss log(1 + others / e_t) is.
 //
-// The path of this file, for float32 and for bf16 rows of more than 256 features: the sums by one product kernel whose tiles
-// are reduced where they are formed (k_ce_sums); the gradients in pieces of the vocabulary, for each of which dz is formed
-// again, kept in 16 (32) bits and multiplied with E and with H (k_ce_dz, k_ce_dh, k_ce_de). The matrix units bound it:
-// 4,096 rows, 131,072 items of 2,048 features, bf16, 0.97 to 1.07 PFLOP/s in each of the four products (a large product of
-// the library: 1.30); 738 x 65,537 x 256 in float32 84 to 104 TFLOP/s (154), where a tile has 16 stages for its beginning
-// and end to hide behind, and 513 x 2 tiles of dE come to two rounds of the chip and two tiles.
+// The path of this file, for float32 and for bf16 rows of more than 256 features: the sums by one product kernel
+// whose tiles are reduced where they are formed (k_ce_sums); the gradients in pieces of the vocabulary, for each of
+// which dz is formed again, kept in 16 (32) bits and multiplied with E and with H (k_ce_dz, k_ce_dh, k_ce_de). The
+// matrix units bound it: 4,096 rows, 128,000 items of 2,048 features, bf16, 0.95 to 1.25 PFLOP/s in the four
+// products, dH the most (a large product of the library: 1.30); 768 x 65,536 x 256 in float32 112 to 118 TFLOP/s
+// (154) in each. 739 rows of 65,537 items take as long as 768 (six tiles), and the one item more a seventh turn of a
+// few tiles: 3% in the sums, 5% in dz; in dE a third round of the chip for two tiles (231 us, so 276).
 #include "softmax.h"
 
 namespace cutbce {
@@ -25,9 +26,9 @@ namespace {
 // ---------------------------------------------------------------------------------------------------------
 
 // A workgroup has a range of rows, each wave one at a time: its place among the counted ones, its copy, and c times its
-// product with its target's item. All of them count all targets first, which is what one of them would have to do before
-// the others could start. Latency bounds it: 5.4 us for 32 rows of 64 (two launches: 6.6), 28 for 25,600 of 128 (25), most
-// of it the count.
+// product with its target's item. All of them count all targets first, which is what one of them would have to do
+// before the others could start. Latency bounds it: 5.4 us for 32 rows of 64 (two launches: 6.6), 28 for 25,600 of
+// 128 (25), most of it the count.
 template <typename T, typename I>
 __global__ __launch_bounds__(1024) void k_ce_rows(Ce c, const T* __restrict__ H, const I* __restrict__ targets,
                                                   const float* __restrict__ weight, float* __restrict__ zt) {
@@ -46,7 +47,8 @@ __global__ __launch_bounds__(1024) void k_ce_rows(Ce c, const T* __restrict__ H,
     w += in ? (weight ? (double)weight[r] : 1.0) : 0.0;
   }
 #pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) n += __shfl_xor(n, o, 64), before += __shfl_xor(before, o, 64), w += __shfl_xor(w, o, 64);
+  for (int o = 32; o >= 1; o >>= 1)
+    n += __shfl_xor(n, o, 64), before += __shfl_xor(before, o, 64), w += __shfl_xor(w, o, 64);
   if (lane == 0) count[wave] = n, early[wave] = before, sum[wave] = w;
   __syncthreads();
   int from = 0, total = 0;
@@ -102,16 +104,17 @@ __global__ __launch_bounds__(1024) void k_ce_rows(Ce c, const T* __restrict__ H,
 }
 
 // ---------------------------------------------------------------------------------------------------------
-// Products. A workgroup forms a tile of BM x BN results from stages of KB bytes of features (K of them) of both sides, in
-// a ring of kRing stages in LDS. Turn s multiplies stage s; stage s + 1 has landed by then, so that its first operands are
-// read while the last products of stage s run, and the stages behind it are on their way. Two waves a SIMD; the order of
-// matrix instructions and reads is pinned, a step's operands being read behind the products of the step before.
-// A side is read by rows (the features next to each other) or transposed (the results' index next to each other).
-// ---------------------------------------------------------------------------------------------------------
-// 1, 2 or 4 loads of 16 bytes a lane, as load_lds16 does them one by one: from bytes voff[] of the buffer to LDS bytes dst,
-// dst + STEP, ... (+ lane * 16). A stage's loads are what its turn waits for and its scalar work: one block with one wait
-// for its operands (as load_lds16 has), and what does not change from stage to stage formed before (the products of 4,096
-// rows with 32,768 items of 2,048 features took a third longer with the ranges formed for each stage).
+// Products. A workgroup forms a tile of BM x BN results from stages of KB bytes of features (K of them) of both
+// sides, in a ring of kRing stages in LDS. Turn s multiplies stage s; stage s + 1 has landed by then, so that its
+// first operands are read while the last products of stage s run, and the stages behind it are on their way. Two
+// waves a SIMD; the order of matrix instructions and reads is pinned, a step's operands being read behind the
+// products of the step before. A side is read by rows (the features next to each other) or transposed (the results'
+// index next to each other).
+// --------------------------------------------------------------------------------------------------------- 1, 2 or 4
+// loads of 16 bytes a lane, as load_lds16 does them one by one: from bytes voff[] of the buffer to LDS bytes dst, dst
+// + STEP, ... (+ lane * 16). A stage's loads are what its turn waits for and its scalar work: one block with one wait
+// for its operands (as load_lds16 has), and what does not change from stage to stage formed before (the products of
+// 4,096 rows with 32,768 items of 2,048 features took a third longer with the ranges formed for each stage).
 template <int N, int STEP> __device__ inline void load_lds16s(u32x4 buffer, const int* voff, uint32_t dst) {
   static_assert(N == 1 || N == 2 || N == 4, "");
   if constexpr (N == 1) {
@@ -317,11 +320,13 @@ template <typename T> struct Sizes<T, kNarrow> : Sizes<T, kSmall> {
   using Sums = Product<T, 4, 1, 1, 2, 64, false, false>;
   using Dh = Product<T, 1, 4, 2, 1, 64, false, true>;
 };
-// Tiles of 256 x 256 are read by half as many workgroups, but leave CUs idle where there are few of them. 65,536 items of
-// 1,024 features, all four products: 200 rows 224 us in large tiles and 212 in small ones, 512 rows 366 and 410; 4,096
-// rows, 131,072 items of 2,048: 8.5 ms and 10.7. 4,149 rows, 392 items of 1,000, 34 large tiles: logits 37 us, so 20.
-// Up to 64 rows tiles are 64 rows wide, where half a small one would be empty (float32, 64 rows,
-// 100,000 x 512: logits 143 us in small tiles and 83, dH 119 and 68; bf16 of 40,000 x 512: 15 and 13, 15 and 12).
+// Tiles of 256 x 256 are read by half as many workgroups, but leave CUs idle where there are few of them. 65,536
+// items of 1,024 features, all four products: 200 rows 224 us in large tiles and 212 in small ones, 512 rows 366 and
+// 410; 4,096 rows, 131,072 items of 2,048: 8.5 ms and 10.7. 4,149 rows, 392 items of 1,000, 34 large tiles: logits 37
+// us, so 20. Up to 64 rows tiles are 64 rows wide, where half a small one would be empty (float32, 64 rows, 100,000 x
+// 512: logits 143 us in small tiles and 83, dH 119 and 68; bf16 of 40,000 x 512: 15 and 13, 15 and 12). From 65 rows
+// on two of them take what one small tile does (65 to 96 rows, all four products, small and narrow: float32 533 and
+// 506 us, bf16 78 and 82).
 inline Tiling tiling_of(int64_t R, int64_t V, int dtype) {
   if (R <= 64) return kNarrow;
   return dtype == 1 && R >= 512 && cdiv(R, 256) * cdiv(V, 256) >= 256 ? kLarge : kSmall;
@@ -364,9 +369,9 @@ __device__ inline Units units_of(int n, int64_t V, int bm, int bn, int grid) {
 template <typename P> constexpr int kCeGrid = P::kLds > 80 * 1024 ? 256 : 512;  // workgroups that are resident
 
 // A unit's tiles follow one another without a pause in the loads. A lane has results of TN rows and keeps their running
-// maximum (of z in base 2) and sum of exponentials; both halves of a wave join at the unit's end. The exponentials are not
-// hidden: 128 a lane and tile, a third of the time at 512 features (4,096 rows x 262,144 x 512: 1,230 to 1,390 us, 0.79 to
-// 0.89 PFLOP/s), a tenth at 2,048.
+// maximum (of z in base 2) and sum of exponentials; both halves of a wave join at the unit's end. The exponentials
+// are not hidden: 128 a lane and tile, a third of the time at 512 features (4,096 rows x 262,144 x 512: 1,230 to
+// 1,390 us, 0.79 to 0.89 PFLOP/s), a tenth at 2,048.
 template <typename P>
 __global__ __launch_bounds__(P::NL, P::kWaves) void k_ce_sums(Ce c, float2* __restrict__ part) {
   using T = typename P::T;
@@ -516,21 +521,22 @@ __global__ __launch_bounds__(1024) void k_ce_loss(Ce c, const float* __restrict_
 // Gradients, a piece of the vocabulary at a time: items v0 .. v0 + width - 1 (width a multiple of 256).
 // ---------------------------------------------------------------------------------------------------------
 
-// dz of the piece in blocks of 64 bytes of items: [width / block][rows][block], rows = R rounded up to 32; zeros for items
-// behind the vocabulary's end and for the rows from n to the next multiple of 32. A stage of the product with E is then one
-// range of memory, and what a wave stores whole lines. In 16 bits the items of each 16 stand in the order 0-3, 8-11, 4-7,
-// 12-15: a lane's eight results are next to each other, and are the operand of the product with E in the order in which
-// the transposed reads of E give their items.
-// (Rows of the piece's width instead, 64 KB apart: dH of 4,096 x 262,144 x 512 1,740 us, so 1,490.) A workgroup goes
-// through its tiles without a pause in the loads (each tile a workgroup: dz 1,660 us, so 1,490). Storing the values in
-// 16 bits rounds them by at most 2^-8 of themselves, as the product's operands are in any case; what that cuts off the
-// targets' is added to both products (multiply_rests, k_ce_dh_join).
+// dz of the piece in blocks of 64 bytes of items: [width / block][rows][block], rows = R rounded up to 32; zeros for
+// items behind the vocabulary's end and for the rows from n to the next multiple of 32. A stage of the product with E
+// is then one range of memory, and what a wave stores whole lines. In 16 bits the items of each 16 stand in the order
+// 0-3, 8-11, 4-7, 12-15: a lane's eight results are next to each other, and are the operand of the product with E in
+// the order in which the transposed reads of E give their items. (Rows of the piece's width instead, 64 KB apart: dH
+// of 4,096 x 262,144 x 512 1,740 us, so 1,490.) A workgroup goes through its tiles without a pause in the loads (each
+// tile a workgroup: dz 1,660 us, so 1,490). Storing the values in 16 bits rounds them by at most 2^-8 of themselves,
+// as the product's operands are in any case; what that cuts off the targets' is added to both products
+// (multiply_rests, k_ce_dh_join).
 template <typename T> constexpr int kBlock = 64 / sizeof(T);
 __host__ __device__ constexpr inline int item_at(int place) {  // of 16 bits
   return (place & ~12) | (place & 4) << 1 | (place & 8) >> 1;
 }
 template <typename P>
-__global__ __launch_bounds__(P::NL, P::kWaves) void k_ce_dz(Ce c, int64_t v0, int64_t width, typename P::T* __restrict__ dz) {
+__global__ __launch_bounds__(P::NL, P::kWaves) void k_ce_dz(Ce c, int64_t v0, int64_t width,
+                                                            typename P::T* __restrict__ dz) {
   using T = typename P::T;
   extern __shared__ __align__(1024) char lds[];
   const int n = at<CeHead>(c.saved, c.at.head)->n;
@@ -579,7 +585,8 @@ __global__ __launch_bounds__(P::NL, P::kWaves) void k_ce_dz(Ce c, int64_t v0, in
 #pragma unroll
             for (int e = 0; e < 16; ++e) x[e] = exp2_of(__builtin_fmaf(p.acc[b][j][e], cc, -shift));
             if (__any((uint64_t)(target - first) < 32u) || first + 32 > c.V) {
-              const int hit = (int)clamp64(target - first, -1, 32) - 4 * h, end = (int)clamp64(c.V - first, 0, 32) - 4 * h;
+              const int hit = (int)clamp64(target - first, -1, 32) - 4 * h;
+              const int end = (int)clamp64(c.V - first, 0, 32) - 4 * h;
 #pragma unroll
               for (int e = 0; e < 16; ++e) {
                 const int item = acc_row(e, 0);
@@ -600,16 +607,17 @@ __global__ __launch_bounds__(P::NL, P::kWaves) void k_ce_dz(Ce c, int64_t v0, in
       });
 }
 
-// Parts of a long axis, of `steps` stages, for so many tiles: as many workgroups as are resident, each at least four stages.
+// Parts of a long axis, of `steps` stages, for so many tiles: as many workgroups as are resident, each at least four
+// stages.
 __host__ __device__ inline int parts_of(int64_t tiles, int64_t steps, int grid) {
   int64_t parts = tiles < grid ? grid / (tiles ? (int)tiles : 1) : 1;
   if (parts > steps / 4) parts = steps / 4;
   return parts < 1 ? 1 : (int)parts;
 }
-// Of dH: by the rows that are counted, which only the device knows (777 rows, 739 of them counted, 65,537 x 256, float32:
-// 275 us by all rows, 432 workgroups on 512 places; so 241). Of the numbers of parts that fill one turn of the resident
-// workgroups, two, ... the first is taken that leaves at most 10% of them idle, or the best (296 tiles on 512 places, 4,697
-// rows, 202,265 x 1,000, float32: 25.8 ms in one part, 15.9 in five).
+// Of dH: by the rows that are counted, which only the device knows (777 rows, 739 of them counted, 65,537 x 256,
+// float32: 275 us by all rows, 432 workgroups on 512 places; so 241). Of the numbers of parts that fill one turn of
+// the resident workgroups, two, ... the first is taken that leaves at most 10% of them idle, or the best (296 tiles
+// on 512 places, 4,697 rows, 202,265 x 1,000, float32: 25.8 ms in one part, 15.9 in five).
 constexpr int kTurns = 4;
 template <typename P> __host__ __device__ inline int64_t dh_tiles(int64_t n, int D) {
   return cdiv(n, P::BM) * cdiv(D, P::BN);
@@ -676,8 +684,9 @@ __global__ __launch_bounds__(P::NL, P::kWaves) void k_ce_dh(Ce c, int64_t v0, in
 // dE of the piece: items x features, over all rows; or a part of the rows, to be joined.
 template <typename P, bool PART>
 __global__ __launch_bounds__(P::NL, P::kWaves) void k_ce_de(Ce c, int64_t v0, int64_t width, int parts,
-                                                    const typename P::T* __restrict__ dz, const float* __restrict__ grad,
-                                                    typename P::T* __restrict__ dE, float* __restrict__ sums) {
+                                                            const typename P::T* __restrict__ dz,
+                                                            const float* __restrict__ grad,
+                                                            typename P::T* __restrict__ dE, float* __restrict__ sums) {
   using T = typename P::T;
   extern __shared__ __align__(1024) char lds[];
   const int n = at<CeHead>(c.saved, c.at.head)->n;
@@ -811,9 +820,10 @@ template <typename T, int TILING> Plan plan_of(int64_t R, int64_t V, int D) {
   using S = Sizes<T, TILING>;
   if (R < 1) R = 1;
   Plan p;
-  // A piece's dz takes up to 512 MB, or that of 256 items. For each piece dH's partial sums are read and written again, and the launches have
-  // their tails; what is beyond the 256 MB of the memory-side cache comes from memory. Measured, dz + dH + dE of 4,096 x
-  // 262,144 x 512 in pieces of 64 MB, 256 MB, 1 GB: 5.6, 4.2, 3.8 ms; of 131,072 x 2,048: 6.7, 6.2, 6.0.
+  // A piece's dz takes up to 512 MB, or that of 256 items. For each piece dH's partial sums are read and written
+  // again, and the launches have their tails; what is beyond the 256 MB of the memory-side cache comes from memory.
+  // Measured, dz + dH + dE of 4,096 x 262,144 x 512 in pieces of 64 MB, 256 MB, 1 GB: 5.6, 4.2, 3.8 ms; of 131,072 x
+  // 2,048: 6.7, 6.2, 6.0.
   const int64_t rows = up(R, 32);
   int64_t width = ((int64_t)512 << 20) / (rows * (int64_t)sizeof(T)) / 256 * 256;
   if (width < 256) width = 256;
@@ -872,7 +882,8 @@ hipError_t forward_t(const Ce& c, int id_bytes, const T* H, const void* targets,
     k_ce_sums<P><<<kCeGrid<P>, P::NL, P::kLds, st>>>(c, part);
   }
   if (c.R && !(swept && grad)) {
-    const JoinHow how = swept ? JoinHow{0, sweep_rows(c.D), sweep_grid(c.D), 1} : JoinHow{P::BM, P::BN, kCeGrid<P>, P::WM};
+    const JoinHow how =
+        swept ? JoinHow{0, sweep_rows(c.D), sweep_grid(c.D), 1} : JoinHow{P::BM, P::BN, kCeGrid<P>, P::WM};
     k_ce_join<<<(unsigned)cdiv(c.R, 4), 256, 0, st>>>(c, how, part, zt, row_loss, each);
   }
   k_ce_loss<<<1, 1024, 0, st>>>(c, each, loss);
@@ -892,8 +903,8 @@ hipError_t backward_t(const Ce& c, const float* grad, T* dH, T* dE, hipStream_t 
   if (e != hipSuccess) return e;
   for (int64_t v = 0; v < c.V; v += p.width) {
     const int64_t tiles = up(cdiv(c.R, S::Sums::BN) * (p.width / S::Sums::BM), 8);
-    if (c.R) k_ce_dz<typename S::Sums><<<(unsigned)(tiles < kCeGrid<typename S::Sums> ? tiles : kCeGrid<typename S::Sums>),
-                                         S::Sums::NL, S::Sums::kLds, st>>>(c, v, p.width, dz);
+    const unsigned grid = (unsigned)(tiles < kCeGrid<typename S::Sums> ? tiles : kCeGrid<typename S::Sums>);
+    if (c.R) k_ce_dz<typename S::Sums><<<grid, S::Sums::NL, S::Sums::kLds, st>>>(c, v, p.width, dz);
     if (dH && c.R) {
       const int64_t one = dh_tiles<typename S::Dh>(c.R, c.D), turns = kTurns * kCeGrid<typename S::Dh>;
       int64_t most = one * dh_most<typename S::Dh>(p.width);  // workgroups, for any number of counted rows
@@ -912,8 +923,8 @@ hipError_t backward_t(const Ce& c, const float* grad, T* dH, T* dE, hipStream_t 
     }
   }
   if (dH && c.R) {
-    // many parts are joined by 16 lanes for each four features (32 rows, 100,000 x 128, float32, 512 parts: 126 us by one
-    // lane, so 6)
+    // many parts are joined by 16 lanes for each four features (32 rows, 100,000 x 128, float32, 512 parts: 126 us by
+    // one lane, so 6)
     const bool many = dh_parts<typename S::Dh>(c.R, c.D, p.width) >= 16;
     const int64_t blocks = cdiv(c.R * c.D, many ? 64 : 1024), turns = cdiv(blocks, kMaxGrid);
     const dim3 grid((unsigned)cdiv(blocks, turns), (unsigned)turns);
@@ -941,7 +952,8 @@ CeSaved ce_saved(int64_t R, int64_t V, int D, int dtype) {
 template <typename F> auto by_sizes(int64_t R, int64_t V, int dtype, F f) {
   using std::integral_constant;
   const Tiling tiling = tiling_of(R, V, dtype);
-  if (!dtype) return tiling == kNarrow ? f(0.f, integral_constant<int, kNarrow>{}) : f(0.f, integral_constant<int, kSmall>{});
+  if (!dtype)
+    return tiling == kNarrow ? f(0.f, integral_constant<int, kNarrow>{}) : f(0.f, integral_constant<int, kSmall>{});
   return tiling == kNarrow  ? f((__bf16)0.f, integral_constant<int, kNarrow>{})
          : tiling == kLarge ? f((__bf16)0.f, integral_constant<int, kLarge>{})
                             : f((__bf16)0.f, integral_constant<int, kSmall>{});
@@ -964,7 +976,8 @@ hipError_t launch_ce_forward(const Ce& c, int id_bytes, const void* H, const voi
                              bool want_grad, float* loss, float* row_loss, hipStream_t st) {
   return by_sizes(c.R, c.V, c.dtype, [&](auto x, auto tiling) {
     using T = decltype(x);
-    return forward_t<T, decltype(tiling)::value>(c, id_bytes, (const T*)H, targets, weight, want_grad, loss, row_loss, st);
+    return forward_t<T, decltype(tiling)::value>(c, id_bytes, (const T*)H, targets, weight, want_grad, loss, row_loss,
+                                                 st);
   });
 }
 hipError_t launch_ce_backward(const Ce& c, const float* grad, void* dH, void* dE, hipStream_t st) {

@@ -1,25 +1,29 @@
 // Softmax cross entropy in two sweeps, for bfloat16 rows of up to 256 features: neither the logits nor their gradients
 // leave the registers.
 //
-// Forward: a wave owns 64 rows (as two blocks of 32; beyond 128 features one block) and sweeps a share of the vocabulary, 32 items a step:
+// Forward: a wave owns 64 rows (as two blocks of 32; beyond 128 features one block) and sweeps a share of the
+// vocabulary, 32 items a step:
 //   Z^T = E_step H^T,  P = exp2(c Z - ref),  sums += P,  dH^T += E_step^T P     (ref a row's reference)
 // Backward: a wave owns as many items and sweeps all rows:
 //   Z = H_step E^T,  P = w/W exp2(c Z - lse),  dE^T += H_step^T P
 // A step's results have the owned rows (or items) as columns, so that a lane has values of one of them, and P is the
-// second product's operand as it stands; the step's own tile, read row by row and transposed, is the other operand of both.
+// second product's operand as it stands; the step's own tile, read row by row and transposed, is the other operand of
+// both.
 //
 // Two blocks a wave halve what is read from LDS for a product: with one, LDS delivers 128 bytes a cycle at the matrix
-// units' full rate, all that it can. Beyond 64 features they take all of a SIMD's registers for one wave, so the products
-// have to hide the vector instructions of the same wave: in one turn of the loop the products Z of the next step and the
-// gradient's of the step before run while the exponentials of this step are formed, none depending on another. The order
-// is pinned, a share of the vector work behind each matrix instruction. Up to 64 features two workgroups fit a CU, and
-// their waves hide each other (kPlain): a step's products, exponentials and products follow one another, which needs
-// fewer registers (the backward's sweep of 5,120 rows and 100,000 items of 64 in turns as above, one wave a SIMD: 236 us,
-// so 157; the forward's 168 either way).
+// units' full rate, all that it can. Beyond 64 features they take all of a SIMD's registers for one wave, so the
+// products have to hide the vector instructions of the same wave: in one turn of the loop the products Z of the next
+// step and the gradient's of the step before run while the exponentials of this step are formed, none depending on
+// another. The order is pinned, a share of the vector work behind each matrix instruction. Up to 64 features two
+// workgroups fit a CU, and their waves hide each other (kPlain): a step's products, exponentials and products follow
+// one another, which needs fewer registers (the backward's sweep of 5,120 rows and 100,000 items of 64 in turns as
+// above, one wave a SIMD: 236 us, so 157, which with the rests of the targets are 160 to 180; the forward's 168
+// either way).
 //
-// What bounds them: the matrix units' power. 14,336 rows x 876,000 x 128: 5.1 to 5.6 ms a sweep, 1.15 to 1.26 PFLOP/s at
-// 1.5 to 1.8 GHz, a large product of the library having 1.30 on the same card. At 64 features an exponential costs as much
-// as its products (770 to 840 TFLOP/s), at 256 a wave has one block (4,096 rows x 131,072: 1.05 ms for both, 1.05 PFLOP/s).
+// What bounds them: the matrix units' power. 14,336 rows x 876,000 x 128: 5.0 to 5.8 ms a sweep, 1.1 to 1.28 PFLOP/s at
+// 1.5 to 1.8 GHz, a large product of the library having 1.30 on the same card. At 64 features an exponential costs as
+// much as its products (770 to 840 TFLOP/s), at 256 a wave has one block (4,096 rows x 131,072: 1.05 ms for both,
+// 1.05 PFLOP/s).
 #include "softmax.h"
 
 namespace cutbce {
@@ -32,7 +36,7 @@ namespace {
 template <int DP> constexpr int kBlocks = DP > 128 ? 1 : 2;
 template <int DP> constexpr int kStages = DP > 128 ? 4 : 5;
 template <int DP> constexpr int kAhead = kStages<DP> - 2;
-__host__ __device__ constexpr inline int items_grid(int D) { return D <= 64 ? 512 : 256; }  // workgroups of the backward
+__host__ __device__ constexpr inline int items_grid(int D) { return D <= 64 ? 512 : 256; }  // of the backward
 constexpr float kMost = 0x1p80f;              // sums of exponentials beyond which a row takes a new reference
 
 __device__ inline uint32_t pack2(float a, float b) {
@@ -139,7 +143,8 @@ template <int DP, bool AUX, bool GRAD> struct Sweep {
     for (int k = 0; k < NT; ++k) x[k] = load_row(at + row_off, k);
   }
   __device__ inline bf16x8 operand(int q, int b, int g) const {
-    return __builtin_bit_cast(bf16x8, u32x4{p[q][b][4 * g], p[q][b][4 * g + 1], p[q][b][4 * g + 2], p[q][b][4 * g + 3]});
+    const uint32_t* x = p[q][b] + 4 * g;
+    return __builtin_bit_cast(bf16x8, u32x4{x[0], x[1], x[2], x[3]});
   }
   __device__ inline void gradient(int q, int k, int b) {  // the k-th of NT parts of the product with p[q]
     if constexpr (GRAD)
@@ -160,8 +165,8 @@ template <int DP, bool AUX, bool GRAD> struct Sweep {
     if constexpr (kAlone) asm volatile("" : "+a"(z[q][b]));
     return z[q][b][e];
   }
-  // LDS addresses of the reads ahead: of the rows from stage `next` on, of the transposed rows from stage `here` on. They
-  // are moved on from stage to stage, an addition each.
+  // LDS addresses of the reads ahead: of the rows from stage `next` on, of the transposed rows from stage `here` on.
+  // They are moved on from stage to stage, an addition each.
   __device__ inline void aim(uint32_t next, uint32_t here) {
     if constexpr (!kHeld) {
       ra[0] = next + row_off, ca[0] = here + col_off;
@@ -192,9 +197,9 @@ template <int DP, bool AUX, bool GRAD> struct Sweep {
           (CUTBCE_LDS s16x4*)(size_t)(col_at(db, e) + (Q * 32 + 16 * g + 8 * e) * kRow));
     t[k] = __builtin_bit_cast(bf16x8, (s16x8)__builtin_shufflevector(y[0], y[1], 0, 1, 2, 3, 4, 5, 6, 7));
   }
-  // One turn: Z of the next step, the gradient's product of the step before, and work(0 .. kSlots - 1) in between, a share
-  // of the vector instructions behind each matrix instruction: they run beside it, and the next one waits for them.
-  // Reads ahead: the rows of the step after the next, the transposed rows of this step.
+  // One turn: Z of the next step, the gradient's product of the step before, and work(0 .. kSlots - 1) in between, a
+  // share of the vector instructions behind each matrix instruction: they run beside it, and the next one waits for
+  // them. Reads ahead: the rows of the step after the next, the transposed rows of this step.
   static constexpr int kSlots = (GRAD ? 2 : 1) * NT * kNB;
   template <int Q, typename F> __device__ inline void turn(F work) {
     settle();
@@ -218,8 +223,8 @@ template <int DP, bool AUX, bool GRAD> struct Sweep {
       }
     }
   }
-  // The exponentials of step Q's results, element e = i / kNB of block b = i % kNB in turn: one is begun in its slot, and
-  // added and packed in later ones, when it is there. argument(b, e, z) gives the exponent.
+  // The exponentials of step Q's results, element e = i / kNB of block b = i % kNB in turn: one is begun in its slot,
+  // and added and packed in later ones, when it is there. argument(b, e, z) gives the exponent.
   template <int Q, typename A> __device__ inline void element(int i, float* y, A argument) {
     y[i & 3] = exp2_of(argument(i % kNB, i / kNB, result(Q, i % kNB, i / kNB)));
   }
@@ -227,7 +232,8 @@ template <int DP, bool AUX, bool GRAD> struct Sweep {
     const int b = i % kNB, e = i / kNB;
     if (e & 1) {
       p[Q][b][e / 2] = pack2(y[(i - kNB) & 3], y[i & 3]);
-      asm volatile("" : "+v"(p[Q][b][e / 2]));  // (here: the compiler would move what is not needed before the next turn)
+      // (here: the compiler would move what is not needed before the next turn)
+      asm volatile("" : "+v"(p[Q][b][e / 2]));
     }
   }
   // The last step's part of the gradient.
@@ -249,9 +255,10 @@ template <int N> __device__ inline void landed_and_sync() {
 // ---------------------------------------------------------------------------------------------------------
 //
 // A row's reference is the largest of its first step. It holds unless logits rise by 55 above that, or none of those
-// items counts, or something is not finite: the unit is then marked in `off`, and a second launch (CAREFUL) goes through
-// the marked ones again, one product after the other, a row whose exponentials have grown taking its largest as reference.
-// The unit's other rows go through the same numbers again: what a row gets does not depend on the others.
+// items counts, or something is not finite: the unit is then marked in `off`, and a second launch (CAREFUL) goes
+// through the marked ones again, one product after the other, a row whose exponentials have grown taking its largest
+// as reference. The unit's other rows go through the same numbers again: what a row gets does not depend on the
+// others.
 template <int DP, bool GRAD, bool CAREFUL>
 __global__ __launch_bounds__(256, (kWaves<DP, false>)) void k_ce_sweep_rows(Ce c, float2* __restrict__ part,
                                                                    float* __restrict__ sums, int* __restrict__ off) {
@@ -355,7 +362,8 @@ __global__ __launch_bounds__(256, (kWaves<DP, false>)) void k_ce_sweep_rows(Ce c
             for (int b = 0; b < S::kNB; ++b) {
               float v[2];
 #pragma unroll
-              for (int j = 0; j < 2; ++j) add[b][j] += v[j] = exp2_of(__builtin_fmaf(s.z[Q][b][2 * i + j], cc, -ref[b]));
+              for (int j = 0; j < 2; ++j)
+                add[b][j] += v[j] = exp2_of(__builtin_fmaf(s.z[Q][b][2 * i + j], cc, -ref[b]));
               if constexpr (GRAD) s.p[Q][b][i] = pack2(v[0], v[1]);
             }
           if constexpr (GRAD) s.last(Q);
@@ -527,11 +535,11 @@ __global__ __launch_bounds__(256) void k_ce_sweep_join(Ce c, const float2* __res
 // Backward.
 // ---------------------------------------------------------------------------------------------------------
 
-// The work, tiles of items (in steps of `spread`) x stages of rows, is one line that is cut into as many equal parts as there are workgroups
-// (each at least kLeast stages, where there is that much): a workgroup goes through whole tiles, and the ends of its part
-// are pieces of tiles that it shares with its neighbours. A piece's sums go to place 0 of its workgroup's two if it
-// begins where the part does, else to 1, and are joined by k_ce_finish. (With whole tiles alone 391 tiles of 100,000
-// items on 256 CUs would take the time of 512.)
+// The work, tiles of items (in steps of `spread`) x stages of rows, is one line that is cut into as many equal parts
+// as there are workgroups (each at least kLeast stages, where there is that much): a workgroup goes through whole
+// tiles, and the ends of its part are pieces of tiles that it shares with its neighbours. A piece's sums go to place
+// 0 of its workgroup's two if it begins where the part does, else to 1, and are joined by k_ce_finish. (With whole
+// tiles alone 391 tiles of 100,000 items on 256 CUs would take the time of 512.)
 constexpr int kLeast = 4, kListBytes = 16 + kRestList * 4;
 struct Line {
   int64_t stages, total;  // of a tile, and of all
@@ -646,8 +654,8 @@ __global__ __launch_bounds__(256, (kWaves<DP, true>)) void k_ce_sweep_items(Ce c
         });
         s.template finished<Q>(ALL - 1, y);
       }
-      // a row whose target is among the wave's items (behind the last row all that is loaded is 0: a row of zeros, whose
-      // product is 0 whatever P is)
+      // a row whose target is among the wave's items (behind the last row all that is loaded is 0: a row of zeros,
+      // whose product is 0 whatever P is)
       if (__builtin_expect(__any((t & ~kPlaces) == (int)own0), 0)) {
         uint32_t at = ax + 16 * s.h;
         asm volatile("" : "+v"(at));  // (one address and constants, not an address each)
@@ -722,14 +730,16 @@ __global__ __launch_bounds__(256, (kWaves<DP, true>)) void k_ce_sweep_items(Ce c
       f32x16 o[S::NDB];
 #pragma unroll
       for (int d = 0; d < S::NDB; ++d) o[d] = s.acc[d][b];
+      const int64_t piece = blockIdx.x * 2 + place;
       if (whole) store_row<__bf16, S::NDB>(dE + v * c.D, o, f, c.D, s.lane);
-      else store_row<float, S::NDB>(sums + ((int64_t)(blockIdx.x * 2 + place) * S::kOwned + at) * c.D, o, f, c.D, s.lane);
+      else store_row<float, S::NDB>(sums + (piece * S::kOwned + at) * c.D, o, f, c.D, s.lane);
     }
   }
 }
 
-// What is left when the sweep is done, four features a lane. The first `pieces` workgroups: the tiles that were shared, each
-// by the first workgroup of its parts but one. The others: dH of all rows from saved's, zeros for those left out.
+// What is left when the sweep is done, four features a lane. The first `pieces` workgroups: the tiles that were
+// shared, each by the first workgroup of its parts but one. The others: dH of all rows from saved's, zeros for those
+// left out.
 __global__ __launch_bounds__(256) void k_ce_finish(Ce c, const float* __restrict__ sums, int64_t spread, int pieces,
                                                    const float* __restrict__ grad, __bf16* __restrict__ dH,
                                                    __bf16* __restrict__ dE) {
@@ -803,8 +813,8 @@ RowsPlan rows_plan(int64_t R, int D, bool grad) {
   return p;
 }
 
-// Rows from which on they are joined a wave each (by a workgroup and by a wave: 2,048 rows, 100,000 x 64 9.6 and 9.5 us, 5,120
-// 15.7 and 10.0, 15,503 rows, 1,613 x 200 42 and 17).
+// Rows from which on they are joined a wave each (by a workgroup and by a wave: 2,048 rows, 100,000 x 64 9.6 and 9.5
+// us, 5,120 15.7 and 10.0, 15,503 rows, 1,613 x 200 42 and 17).
 constexpr int64_t kManyRows = 2048;
 
 template <int DP, bool GRAD> hipError_t rows_t(const Ce& c, char* ws, const float* zt, float* row_loss, float* each,
@@ -814,20 +824,21 @@ template <int DP, bool GRAD> hipError_t rows_t(const Ce& c, char* ws, const floa
   hipError_t e = allow_lds<k_ce_sweep_rows<DP, GRAD, false>>(S::kLds);
   if (e == hipSuccess) e = allow_lds<k_ce_sweep_rows<DP, GRAD, true>>(S::kLds);
   if (e != hipSuccess) return e;
-  k_ce_sweep_rows<DP, GRAD, false><<<sweep_grid(c.D), 256, S::kLds, st>>>(c, (float2*)(ws + p.part), (float*)(ws + p.sums),
-                                                                    (int*)(ws + p.off));
-  k_ce_sweep_rows<DP, GRAD, true><<<sweep_grid(c.D), 256, S::kLds, st>>>(c, (float2*)(ws + p.part), (float*)(ws + p.sums),
-                                                                   (int*)(ws + p.off));
+  float2* part = (float2*)(ws + p.part);
+  float* sums = (float*)(ws + p.sums);
+  int* off = (int*)(ws + p.off);
+  k_ce_sweep_rows<DP, GRAD, false><<<sweep_grid(c.D), 256, S::kLds, st>>>(c, part, sums, off);
+  k_ce_sweep_rows<DP, GRAD, true><<<sweep_grid(c.D), 256, S::kLds, st>>>(c, part, sums, off);
   if (GRAD) {
-    const float2* part = (const float2*)(ws + p.part);
-    const float* sums = (const float*)(ws + p.sums);
-    if (c.R >= kManyRows) k_ce_sweep_join<true><<<(unsigned)cdiv(c.R, 4), 256, 0, st>>>(c, part, sums, zt, row_loss, each);
+    const unsigned waves = (unsigned)cdiv(c.R, 4);
+    if (c.R >= kManyRows) k_ce_sweep_join<true><<<waves, 256, 0, st>>>(c, part, sums, zt, row_loss, each);
     else k_ce_sweep_join<false><<<(unsigned)c.R, 256, 0, st>>>(c, part, sums, zt, row_loss, each);
   }
   return hipGetLastError();
 }
 
-template <int DP> hipError_t items_t(const Ce& c, float* sums, const float* grad, int64_t far, __bf16* dE, hipStream_t st) {
+template <int DP>
+hipError_t items_t(const Ce& c, float* sums, const float* grad, int64_t far, __bf16* dE, hipStream_t st) {
   constexpr int kLds = Sweep<DP, true, true>::kLds + 4 * kListBytes;
   static_assert(kLds * kWaves<DP, true> <= 160 * 1024, "");
   const hipError_t e = allow_lds<k_ce_sweep_items<DP>>(kLds);

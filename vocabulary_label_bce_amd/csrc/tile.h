@@ -40,7 +40,8 @@ __device__ inline float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
 // c ^ swz(r).
 template <typename T, int DH> struct Tile {
   static constexpr int kEsz = sizeof(T);
-  static constexpr int kRowB = (DH <= 16 && kEsz == 4 ? 16 : DH <= 32 ? 32 : DH <= 64 ? 64 : DH <= 128 ? 128 : 256) * kEsz;
+  static constexpr int kRowB =
+      (DH <= 16 && kEsz == 4 ? 16 : DH <= 32 ? 32 : DH <= 64 ? 64 : DH <= 128 ? 128 : 256) * kEsz;
   static constexpr int kCPR = kRowB / 16;
   static constexpr int kNT = DH * kEsz / 32;  // pairs of chunks: k-steps of a product over the features
   static constexpr int kNDB = DH / 32;        // 32-wide blocks of features

@@ -5,8 +5,8 @@
 namespace cutbce {
 
 // ---------------------------------------------------------------------------------------------------------
-// Lists of tensors. A launch takes kListed of them by value, as kernel arguments: nothing is copied to the device first.
-// ---------------------------------------------------------------------------------------------------------
+// Lists of tensors. A launch takes kListed of them by value, as kernel arguments: nothing is copied to the device
+// first. ---------------------------------------------------------------------------------------------------------
 constexpr int kListed = 48;
 constexpr int kChunk = 4096;  // elements of a workgroup
 constexpr int kBlock8 = 256;  // elements that share a scale in states of 8 bits: 16 lanes' sixteen each
@@ -62,8 +62,8 @@ struct CeHead {
   float weight;  // sum of their weights
 };
 
-// What the forward leaves for the backward, as byte offsets into `saved`; arrays of R entries unless said. What a row brings
-// to dz: exp2(c z - shift), or at its target `own` instead; coef = w / W.
+// What the forward leaves for the backward, as byte offsets into `saved`; arrays of R entries unless said. What a row
+// brings to dz: exp2(c z - shift), or at its target `own` instead; coef = w / W.
 struct CeSaved {
   size_t head, rows, place, target, shift, own, coef, hc, dh, bytes;
 };

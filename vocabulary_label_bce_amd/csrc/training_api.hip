@@ -53,7 +53,8 @@ cutbce_status cutbce_cross_entropy_workspace_size(int64_t rows, int64_t vocab, i
   const cutbce_status s = check_ce(rows, vocab, dim, dtype);
   if (s != CUTBCE_OK) return s;
   if (which < 0 || which > 2) return CUTBCE_ERR_SHAPE;
-  *bytes = which == 2 ? ce_backward_bytes(rows, vocab, dim, dtype) : ce_forward_bytes(rows, vocab, dim, dtype, which == 1);
+  *bytes = which == 2 ? ce_backward_bytes(rows, vocab, dim, dtype)
+                      : ce_forward_bytes(rows, vocab, dim, dtype, which == 1);
   return CUTBCE_OK;
 }
 

@@ -71,15 +71,16 @@ def adamw_step(params, grads, exp_avgs, exp_avg_sqs, step, lr, betas=(0.9, 0.999
       m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2,  t = step + 1,
       p = p (1 - lr weight_decay) - lr (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps).
 
-    params (contiguous), grads: tensors of equal sizes in pairs, float32 or bfloat16 each. step: int32 [1] on the device,
-    one more after the call. lr: a number, or a float32 of one element on the device. weight_decay: a number, or one for
-    each tensor. norm (of grad_norm) with max_norm: gradients are multiplied by min(1, max_norm / (norm + 1e-6)).
-    masters: for each tensor the float32 values that the parameter is the rounding of, or None.
+    params (contiguous), grads: tensors of equal sizes in pairs, float32 or bfloat16 each. step: int32 [1] on the
+    device, one more after the call. lr: a number, or a float32 of one element on the device. weight_decay: a number, or
+    one for each tensor. norm (of grad_norm) with max_norm: gradients are multiplied by
+    min(1, max_norm / (norm + 1e-6)). masters: for each tensor the float32 values that the parameter is the rounding of,
+    or None. Tensors that are changed may not overlap any other (only the same address twice is seen and refused).
 
     exp_avgs, exp_avg_sqs: float32 states m and v; or, with exp_avg_scales and exp_avg_sq_scales (float32, one for each
     256 elements), float8_e4m3fn states of m and sqrt(v): an element stands for its value times its block's scale. Those
     are rounded at random, without bias, by numbers that follow from seed, t, the tensor's place in the list and the
-    element's; a positive sqrt(v) is never rounded to zero."""
+    element's; a positive sqrt(v) is never rounded to zero. A value that is not finite spoils its block's states."""
     n = len(params)
     bits8 = exp_avg_scales is not None or exp_avg_sq_scales is not None
     if len(grads) != n or len(exp_avgs) != n or len(exp_avg_sqs) != n or (masters is not None and len(masters) != n):
